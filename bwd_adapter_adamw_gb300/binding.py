@@ -26,6 +26,14 @@ LORA_ERR_TIMEOUT = 7
 LORA_F32 = 0
 LORA_BF16 = 1
 LORA_BF16_FP8 = 2
+LORA_NORM_LAYER = 0
+LORA_NORM_RMS = 1
+LORA_NORM_MAX_DIM = 16384
+LORA_KIND_A = 0
+LORA_KIND_B = 1
+LORA_MUON_ADJUST_ASPECT = 0
+LORA_MUON_ADJUST_RMS = 1
+LORA_SCALE_BLOCK = 128
 LORA_SCHED_CONSTANT = 0
 LORA_SCHED_WARMUP_COSINE = 1
 LORA_MAX_RANK = 64
@@ -72,6 +80,22 @@ class lora_adamw_hp(C.Structure):
                 ("weight_decay", C.c_double), ("plus_ratio", C.c_double)]
 
 
+class lora_norm_desc(C.Structure):
+    _fields_ = [("dim", C.c_int64), ("kind", C.c_int32), ("dtype", C.c_int32),
+                ("eps", C.c_float)]
+
+
+class lora_mat(C.Structure):
+    _fields_ = [("offset", C.c_int64), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("group", C.c_int32), ("kind", C.c_int32)]
+
+
+class lora_muon_hp(C.Structure):
+    _fields_ = [("momentum", C.c_double), ("weight_decay", C.c_double),
+                ("plus_ratio", C.c_double), ("coef", C.c_double * 3), ("steps", C.c_int32),
+                ("nesterov", C.c_int32), ("adjust", C.c_int32)]
+
+
 def _load() -> C.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -115,6 +139,18 @@ def _load() -> C.CDLL:
                                                  C.POINTER(lora_slot), P, P, P, SZ, P]),
         "multi_lora_backward_planned": (C.c_int, [DP, CP, I64, I32, P, P, P, I32,
                                                   C.POINTER(lora_slot), P, P, P, P, SZ, P]),
+        "lora_block_product_workspace_size": (SZ, [I64, I64, I64, I32]),
+        "lora_block_product": (C.c_int, [I64, I64, I64, P, P, P, P, I32, P, SZ, P]),
+        "lora_block_quantize_weight": (C.c_int, [P, I64, I64, P, P, P]),
+        "lora_block_quantize": (C.c_int, [P, I64, I64, P, P, P]),
+        "lora_norm_forward": (C.c_int, [C.POINTER(lora_norm_desc), I64, P, P, P, P, P, P]),
+        "lora_norm_backward_workspace_size": (SZ, [C.POINTER(lora_norm_desc), I64]),
+        "lora_norm_backward": (C.c_int, [C.POINTER(lora_norm_desc), I64, P, P, P, P, P, P, P, P,
+                                         P, SZ, P]),
+        "lora_muon_workspace_size": (SZ, [I32, C.POINTER(lora_mat)]),
+        "lora_muon_step": (C.c_int, [P, P, P, I32, C.POINTER(lora_group), I32,
+                                     C.POINTER(lora_mat), C.POINTER(lora_muon_hp), P, P, I32, P,
+                                     SZ, P]),
         "lora_dropout_mask": (C.c_int, [DP, CP, I64, P, P]),
         "lora_quantize_e4m3": (C.c_int, [P, I64, I64, P, P, P]),
         "multi_lora_token_slots": (C.c_int, [I64, I32, P, P, I32, P, P]),
@@ -143,6 +179,10 @@ EXPORTED = ("lora_status_string", "lora_scale", "lora_lr_at", "lora_workspace_si
             "multi_lora_plan_size", "multi_lora_plan_build", "multi_lora_forward_planned",
             "multi_lora_backward_planned",
             "lora_fused_workspace_size", "lora_fused_forward", "lora_fused_backward",
+            "lora_block_product_workspace_size", "lora_block_product",
+            "lora_block_quantize_weight", "lora_block_quantize", "lora_norm_forward",
+            "lora_norm_backward_workspace_size", "lora_norm_backward",
+            "lora_muon_workspace_size", "lora_muon_step",
             "lora_dropout_mask", "lora_quantize_e4m3", "multi_lora_token_slots", "lora_profile_arm",
             "lora_profile_used", "lora_launch_counter", "lora_last_cuda_error",
             "lora_device_error", "lora_device_check", "lora_set_wait_limit")
@@ -416,6 +456,90 @@ def multi_lora_backward_planned(d, c, T, n_seg, plan, X, W_prep, slots, dY, H_sa
                                           slots, _ptr(dY), _ptr(H_save), _ptr(dX), _ptr(ws),
                                           nbytes, _stream(stream))
     return _check(st, "multi_lora_backward_planned") if check else st
+
+
+def _nbytes(ws, ws_bytes: Optional[int]) -> int:
+    if ws_bytes is not None:
+        return ws_bytes
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def lora_block_product_workspace_size(T: int, out_dim: int, in_dim: int, transposed=False) -> int:
+    return _lib.lora_block_product_workspace_size(T, out_dim, in_dim, 1 if transposed else 0)
+
+
+def lora_block_product(T: int, out_dim: int, in_dim: int, X, W8, sw, Y, transposed, ws,
+                       ws_bytes: Optional[int] = None, stream=None, check=True):
+    """Y = X W~^T (or X W~ when transposed) over E4M3 codes with 128 x 128 block scales."""
+    st = _lib.lora_block_product(T, out_dim, in_dim, _ptr(X), _ptr(W8), _ptr(sw), _ptr(Y),
+                                 1 if transposed else 0, _ptr(ws), _nbytes(ws, ws_bytes),
+                                 _stream(stream))
+    return _check(st, "lora_block_product") if check else st
+
+
+def lora_block_quantize_weight(W, out_dim: int, in_dim: int, W8, sw, stream=None, check=True):
+    """E4M3 codes and 128 x 128 block scales of a bf16 W [out_dim, in_dim]."""
+    st = _lib.lora_block_quantize_weight(_ptr(W), out_dim, in_dim, _ptr(W8), _ptr(sw),
+                                         _stream(stream))
+    return _check(st, "lora_block_quantize_weight") if check else st
+
+
+def lora_block_quantize(src, rows: int, K: int, codes, scales, stream=None, check=True):
+    """E4M3 codes and 1 x 128 block scales of a bf16 [rows, K] matrix."""
+    st = _lib.lora_block_quantize(_ptr(src), rows, K, _ptr(codes), _ptr(scales), _stream(stream))
+    return _check(st, "lora_block_quantize") if check else st
+
+
+def make_norm_desc(dim, kind=LORA_NORM_LAYER, dtype=LORA_BF16, eps=1e-5) -> lora_norm_desc:
+    return lora_norm_desc(dim, kind, dtype, eps)
+
+
+def lora_norm_forward(d: lora_norm_desc, T: int, X, gamma, beta, Y, stats, stream=None,
+                      check=True):
+    st = _lib.lora_norm_forward(C.byref(d), T, _ptr(X), _ptr(gamma), _ptr(beta), _ptr(Y),
+                                _ptr(stats), _stream(stream))
+    return _check(st, "lora_norm_forward") if check else st
+
+
+def lora_norm_backward_workspace_size(d: lora_norm_desc, T: int) -> int:
+    return _lib.lora_norm_backward_workspace_size(C.byref(d), T)
+
+
+def lora_norm_backward(d: lora_norm_desc, T: int, X, gamma, dY, stats, dX_add, dX, dgamma, dbeta,
+                       ws, ws_bytes: Optional[int] = None, stream=None, check=True):
+    """dX (plus dX_add), dgamma += and dbeta += from the forward's statistics."""
+    st = _lib.lora_norm_backward(C.byref(d), T, _ptr(X), _ptr(gamma), _ptr(dY), _ptr(stats),
+                                 _ptr(dX_add), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws),
+                                 _nbytes(ws, ws_bytes), _stream(stream))
+    return _check(st, "lora_norm_backward") if check else st
+
+
+def make_mats(mats: Sequence[dict]):
+    arr = (lora_mat * len(mats))()
+    for i, m in enumerate(mats):
+        arr[i] = lora_mat(m["offset"], m["rows"], m["cols"], m.get("group", 0), m["kind"])
+    return arr
+
+
+def make_muon_hp(momentum=0.95, weight_decay=0.01, plus_ratio=1.0,
+                 coef=(3.4445, -4.7750, 2.0315), steps=5, nesterov=True,
+                 adjust=LORA_MUON_ADJUST_ASPECT) -> lora_muon_hp:
+    return lora_muon_hp(momentum, weight_decay, plus_ratio, (C.c_double * 3)(*coef), steps,
+                        1 if nesterov else 0, adjust)
+
+
+def lora_muon_workspace_size(mats) -> int:
+    return _lib.lora_muon_workspace_size(len(mats), mats)
+
+
+def lora_muon_step(params, grads, m, groups, mats, hp: lora_muon_hp, d_scale_norm, d_status,
+                   zero_grads, ws, ws_bytes: Optional[int] = None, stream=None, check=True):
+    """Momentum and orthogonalised (Newton-Schulz) update of the adapter matrices `mats`."""
+    st = _lib.lora_muon_step(_ptr(params), _ptr(grads), _ptr(m), len(groups), groups, len(mats),
+                             mats, C.byref(hp), _ptr(d_scale_norm), _ptr(d_status),
+                             1 if zero_grads else 0, _ptr(ws), _nbytes(ws, ws_bytes),
+                             _stream(stream))
+    return _check(st, "lora_muon_step") if check else st
 
 
 def lora_dropout_mask(d: lora_desc, c: Optional[lora_ctx], T: int, mask, stream=None, check=True):

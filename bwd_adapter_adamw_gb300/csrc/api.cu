@@ -4,46 +4,21 @@
 #include <cmath>
 #include <cstring>
 
-#include "lora_kernels.h"
+#include "api_util.h"
 
 using namespace lora;
 
 namespace {
-
-constexpr size_t kWsAlign = 256;
-
-struct Carve {
-  char* base;
-  size_t off = 0;
-  explicit Carve(void* b) : base(static_cast<char*>(b)) {}
-  template <typename T>
-  T* take(size_t count) {
-    off = (off + kWsAlign - 1) / kWsAlign * kWsAlign;
-    T* p = base ? reinterpret_cast<T*>(base + off) : nullptr;
-    off += count * sizeof(T);
-    return p;
-  }
-};
-
-inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 thread_local cudaError_t t_last_error = cudaSuccess;
+}  // namespace
 
-// Errors left behind by other code in this thread (cudaGetLastError reports the most recent
-// error of any runtime call) are cleared before our launches, so that a LORA_ERR_CUDA is ours.
-inline void clear_stale() { (void)cudaGetLastError(); }
-
-inline int cuda_status(cudaError_t e) {
+int lora::cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return LORA_OK;
   t_last_error = e;
   return LORA_ERR_CUDA;
 }
 
-#define LORA_TRY(expr)                                 \
-  do {                                                 \
-    cudaError_t _e = (expr);                           \
-    if (_e != cudaSuccess) return cuda_status(_e);     \
-  } while (0)
+namespace {
 
 int64_t max_gemm_items(int64_t T, int32_t n_seg) {
   if (n_seg < 1) n_seg = 1;
@@ -1509,8 +1484,8 @@ size_t lora_grad_prepare_workspace_size(int32_t n_groups, const lora_group* grou
 
 }  // extern "C"
 
-namespace {
-int build_groups(int32_t n_groups, const lora_group* groups, GroupTab& g, const lora_adamw_hp* hp) {
+int lora::build_groups(int32_t n_groups, const lora_group* groups, GroupTab& g,
+                       const lora_adamw_hp* hp) {
   if (!groups || n_groups < 1) return LORA_ERR_INVALID;
   if (n_groups > LORA_MAX_GROUPS) return LORA_ERR_UNSUPPORTED;
   std::memset(&g, 0, sizeof(g));
@@ -1542,7 +1517,6 @@ int build_groups(int32_t n_groups, const lora_group* groups, GroupTab& g, const 
     }
   return LORA_OK;
 }
-}  // namespace
 
 extern "C" {
 

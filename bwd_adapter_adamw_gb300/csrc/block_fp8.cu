@@ -1,0 +1,215 @@
+// E4M3 operands with one scale per block of 128: quantisation of activations (1 x 128 blocks) and
+// of a frozen weight (128 x 128 blocks), and the frozen product over them.
+//
+// A block x (fp32, each operation rounded): amax = max |x|, r = 448 (1 / amax), codes = e4m3(x r)
+// rounded to nearest even with saturation, scale = amax (1 / 448); r = scale = 1 when amax is 0 or
+// r is not finite. The factors are products with a reciprocal, not quotients: x / amax of two
+// bf16 numbers often lies on a tie between two codes, so the last bit of r decides codes.
+#include <cuda_fp8.h>
+
+#include "lora_kernels.h"
+
+namespace lora {
+
+namespace {
+
+constexpr int kBlk = LORA_SCALE_BLOCK;
+
+__device__ __forceinline__ void block_scales(float amax, float& rcp, float& scale) {
+  rcp = __fmul_rn(__fdiv_rn(1.f, amax), 448.f);
+  if (amax > 0.f && isfinite(rcp)) {
+    scale = __fmul_rn(amax, 1.f / 448.f);
+  } else {
+    rcp = 1.f;
+    scale = 1.f;
+  }
+}
+
+// E4M3 codes of 8 bf16 values (one 16-byte vector) times rcp
+__device__ __forceinline__ uint2 encode8(const uint4& v, float rcp) {
+  const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = make_float2(__fmul_rn(__uint_as_float(h[e] << 16), rcp),
+                                 __fmul_rn(__uint_as_float(h[e] & 0xFFFF0000u), rcp));
+    w[e] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+__device__ __forceinline__ float amax8(const uint4& v) {
+  const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(h[e] << 16)),
+                       fabsf(__uint_as_float(h[e] & 0xFFFF0000u))));
+  return m;
+}
+
+// One 1 x 128 block per 16 lanes: a 16-byte load, the maximum over the lanes, an 8-byte store.
+// A thread takes kQuantBatch blocks whose loads are in flight together.
+constexpr int kQuantBatch = 4;
+__global__ void __launch_bounds__(256) k_block_quant(const __nv_bfloat16* __restrict__ src,
+                                                     int64_t rows, int64_t K, int64_t nkb,
+                                                     uint8_t* __restrict__ codes,
+                                                     float* __restrict__ scales) {
+  grid_dep_sync();
+  const int sub = threadIdx.x & 15;
+  const int64_t blocks = rows * nkb;
+  const int64_t per_pass = (int64_t)gridDim.x * 16;
+  for (int64_t b0 = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); b0 < blocks;
+       b0 += per_pass * kQuantBatch) {
+    uint4 v[kQuantBatch];
+    int64_t row[kQuantBatch], col[kQuantBatch];
+#pragma unroll
+    for (int u = 0; u < kQuantBatch; ++u) {
+      const int64_t b = b0 + u * per_pass;
+      row[u] = b / nkb;
+      col[u] = (b - row[u] * nkb) * kBlk + sub * 8;
+      v[u] = b < blocks && col[u] < K
+                 ? __ldg(reinterpret_cast<const uint4*>(src + row[u] * K + col[u]))
+                 : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kQuantBatch; ++u) {
+      const int64_t b = b0 + u * per_pass;
+      float m = amax8(v[u]);
+      // the 16 lanes of a block are one half of a warp, and all take the same branches
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFu << (threadIdx.x & 16), m, o));
+      if (b >= blocks) break;
+      float rcp, sc;
+      block_scales(m, rcp, sc);
+      if (sub == 0) scales[b] = sc;
+      if (col[u] < K) *reinterpret_cast<uint2*>(codes + row[u] * K + col[u]) = encode8(v[u], rcp);
+    }
+  }
+}
+
+// One 128 x 128 block of W per CTA.
+__global__ void __launch_bounds__(256) k_block_quant_weight(const __nv_bfloat16* __restrict__ W,
+                                                            int64_t rows, int64_t cols,
+                                                            uint8_t* __restrict__ codes,
+                                                            float* __restrict__ scales) {
+  grid_dep_sync();
+  __shared__ float sh[8];
+  const int64_t r0 = (int64_t)blockIdx.y * kBlk, c = (int64_t)blockIdx.x * kBlk + (threadIdx.x & 15) * 8;
+  uint4 v[8];
+  float m = 0.f;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int64_t r = r0 + (threadIdx.x >> 4) + u * 16;
+    v[u] = r < rows && c < cols ? __ldg(reinterpret_cast<const uint4*>(W + r * cols + c))
+                                : make_uint4(0, 0, 0, 0);
+    m = fmaxf(m, amax8(v[u]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = sh[0];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) m = fmaxf(m, sh[w]);
+  float rcp, sc;
+  block_scales(m, rcp, sc);
+  if (threadIdx.x == 0) scales[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = sc;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int64_t r = r0 + (threadIdx.x >> 4) + u * 16;
+    if (r < rows && c < cols) *reinterpret_cast<uint2*>(codes + r * cols + c) = encode8(v[u], rcp);
+  }
+}
+
+__device__ __forceinline__ float e4m3_to_f(uint8_t c) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+}
+
+// 64 x 64 outputs per CTA on CUDA cores: each block of 128 summed over its unscaled codes, then
+// added with its two scales.
+__global__ void __launch_bounds__(256) k_block_product(const uint8_t* __restrict__ A,
+                                                       const float* __restrict__ sa,
+                                                       const uint8_t* __restrict__ W,
+                                                       const float* __restrict__ sw, int64_t T,
+                                                       int64_t N, int64_t K, int64_t ldw,
+                                                       int64_t ld_sw, int transposed,
+                                                       __nv_bfloat16* __restrict__ Y) {
+  grid_dep_sync();
+  __shared__ float a[32][65], w[32][65];
+  const int64_t t0 = (int64_t)blockIdx.x * 64, n0 = (int64_t)blockIdx.y * 64;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int64_t nkb = (K + kBlk - 1) / kBlk;
+  float acc[4][4] = {};
+  for (int64_t kb = 0; kb < nkb; ++kb) {
+    float d[4][4] = {};
+    for (int64_t k0 = kb * kBlk; k0 < kb * kBlk + kBlk; k0 += 32) {
+      for (int e = threadIdx.x; e < 32 * 64; e += 256) {
+        int kk = e & 31, r = e >> 5;
+        a[kk][r] = t0 + r < T && k0 + kk < K ? e4m3_to_f(A[(t0 + r) * K + k0 + kk]) : 0.f;
+        if (transposed) { kk = e >> 6; r = e & 63; }
+        const int64_t at = transposed ? (k0 + kk) * ldw + n0 + r : (n0 + r) * ldw + k0 + kk;
+        w[kk][r] = n0 + r < N && k0 + kk < K ? e4m3_to_f(W[at]) : 0.f;
+      }
+      __syncthreads();
+#pragma unroll 8
+      for (int kk = 0; kk < 32; ++kk)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[i][j] = fmaf(a[kk][ty + 16 * i], w[kk][tx + 16 * j], d[i][j]);
+      __syncthreads();
+    }
+    const int64_t nb = n0 / kBlk;
+    const float s = transposed ? sw[kb * ld_sw + nb] : sw[nb * ld_sw + kb];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + ty + 16 * i;
+      const float f = t < T ? sa[t * nkb + kb] * s : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(f, d[i][j], acc[i][j]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t t = t0 + ty + 16 * i, n = n0 + tx + 16 * j;
+      if (t < T && n < N) Y[t * N + n] = __float2bfloat16(acc[i][j]);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_block_quant(const void* src, int64_t rows, int64_t K, uint8_t* codes,
+                               float* scales, cudaStream_t st) {
+  if (rows <= 0) return cudaSuccess;
+  const int64_t nkb = (K + kBlk - 1) / kBlk;
+  int64_t g = (rows * nkb + 16 * kQuantBatch - 1) / (16 * kQuantBatch);
+  if (g > 8 * 152) g = 8 * 152;
+  prof_begin(0, st);
+  return launch_kernel(k_block_quant, (unsigned)g, 256, 0, st,
+                       static_cast<const __nv_bfloat16*>(src), rows, K, nkb, codes, scales);
+}
+
+cudaError_t launch_block_quant_weight(const void* W, int64_t rows, int64_t cols, uint8_t* codes,
+                                      float* scales, cudaStream_t st) {
+  prof_begin(0, st);
+  return launch_kernel(k_block_quant_weight,
+                       dim3((unsigned)((cols + kBlk - 1) / kBlk), (unsigned)((rows + kBlk - 1) / kBlk)),
+                       256, 0, st, static_cast<const __nv_bfloat16*>(W), rows, cols, codes, scales);
+}
+
+cudaError_t launch_block_product(const BlockProductArgs& a, cudaStream_t st) {
+  const int64_t K = a.transposed ? a.out_dim : a.in_dim, N = a.transposed ? a.in_dim : a.out_dim;
+  cudaError_t e = launch_block_quant(a.X, a.T, K, a.codes, a.scales, st);
+  if (e != cudaSuccess) return e;
+  prof_begin(0, st);
+  return launch_kernel(k_block_product,
+                       dim3((unsigned)((a.T + 63) / 64), (unsigned)((N + 63) / 64)), 256, 0, st,
+                       (const uint8_t*)a.codes, (const float*)a.scales, a.W8, a.sw, a.T, N, K,
+                       a.in_dim, (a.in_dim + kBlk - 1) / kBlk, a.transposed,
+                       static_cast<__nv_bfloat16*>(a.Y));
+}
+
+}  // namespace lora

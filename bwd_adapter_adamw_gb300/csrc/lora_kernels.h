@@ -381,4 +381,66 @@ cudaError_t launch_adamw(float* p, float* g, float* m, float* v, const GroupTab&
                          const AdamK& hp, const double* d_scale_norm, const int32_t* d_status,
                          int zero_grads, cudaStream_t st);
 
+// ---- block_fp8.cu: frozen product over E4M3 codes with 128-blocks ----
+struct BlockProductArgs {
+  const void* X;             // [T, K] bf16; K = in_dim, or out_dim when transposed
+  int64_t T, out_dim, in_dim;
+  const uint8_t* W8;         // [out_dim, in_dim] E4M3 codes
+  const float* sw;           // [ceil(out_dim / 128), ceil(in_dim / 128)]
+  int32_t transposed;
+  void* Y;                   // [T, N] bf16; N = out_dim, or in_dim when transposed
+  uint8_t* codes;            // workspace: [T, K] codes of X and their [T, ceil(K / 128)] scales
+  float* scales;
+};
+cudaError_t launch_block_quant(const void* src, int64_t rows, int64_t K, uint8_t* codes,
+                               float* scales, cudaStream_t st);
+cudaError_t launch_block_quant_weight(const void* W, int64_t rows, int64_t cols, uint8_t* codes,
+                                      float* scales, cudaStream_t st);
+cudaError_t launch_block_product(const BlockProductArgs& a, cudaStream_t st);
+
+// ---- norm.cu ----
+struct NormArgs {
+  int64_t T, dim;
+  int dtype, rms;
+  float eps;
+  const void* X;
+  const float* gamma;
+  const float* beta;         // nullable
+  void* Y;
+  float* stats;              // [T, 2]: written by the forward, read by the backward
+  const void* dY;
+  const void* dX_add;        // nullable
+  void* dX;                  // nullable
+  float* dgamma;             // nullable
+  float* dbeta;              // nullable
+  float* part;               // [norm_bwd_parts][2][dim]
+};
+int norm_bwd_parts(int64_t dim, int dtype, int64_t T);
+cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t st);
+
+// ---- muon.cu ----
+struct MuonMat {             // s x n over the smaller and the longer side
+  int64_t offset;
+  int64_t n;
+  int32_t s;
+  int32_t tall;              // 1: the rows are the longer side (element (i, j) at j s + i)
+  int32_t group;
+  float lr;                  // decay: lr * decay
+  float step;                // lr * ratio * adjustment
+  float decay;
+};
+constexpr int kMuonMatsPerLaunch = 512;
+struct MuonTab {
+  MuonMat m[kMuonMatsPerLaunch];
+  int32_t n;
+};
+struct MuonK {
+  float mu, a, b, c;
+  int32_t steps, nesterov;
+};
+cudaError_t launch_muon(float* p, float* g, float* m, const MuonTab& tab, const MuonK& hp,
+                        const double* scale_norm, const int32_t* status, int zero_grads,
+                        cudaStream_t st);
+
 }  // namespace lora

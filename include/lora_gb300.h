@@ -257,6 +257,107 @@ int lora_adamw_step(float* params, float* grads, float* m, float* v, int32_t n_g
                     const lora_group* groups, const lora_adamw_hp* hp, const double* d_scale_norm,
                     const int32_t* d_status, int32_t zero_grads, void* stream);
 
+/* ---- frozen product over a block-scaled E4M3 base --------------------------------------------*/
+/* A frozen weight kept as E4M3 codes W8 [out_dim, in_dim] (uint8, row-major) with one fp32 scale
+ * for each 128 x 128 block, sw [ceil(out_dim / 128), ceil(in_dim / 128)] (blocks at the far edges
+ * are partial): W~[o, i] = sw[o / 128, i / 128] * W8[o, i] ("LoRA Training and Serving", Quantized
+ * rollout: an FP8 base under a bf16-trained adapter). The activations, bf16, are quantised inside
+ * each call in blocks of 1 x 128 along the contraction: x8 = e4m3(x * r), r = 448 * (1 / amax),
+ * sx = amax * (1 / 448) (codes to nearest even and saturated; fp32, each operation rounded;
+ * r = sx = 1 where amax is 0 or r is not finite). Then
+ *   forward     (transposed = 0)  Y [T, out_dim] = X W~^T,  X [T, in_dim]
+ *   input grad. (transposed != 0) Y [T, in_dim]  = X W~,    X [T, out_dim]
+ *   Y[t, n] = bf16( sum over blocks kb of sx[t, kb] sw[block of (n, kb)] sum_{k in kb} x8 w8 )
+ * with each block's sum in fp32 on the tensor cores and the sum over blocks in fp32 registers.
+ * Both directions read the same codes, so the gradient is that of the forward's weight, and one
+ * copy of the weight serves both. A row of X holding a NaN or an infinity gives a NaN row of Y
+ * and touches no other row. T from 1 (one decoded token) up; in_dim and out_dim multiples of 16
+ * (LORA_ERR_ALIGN), T below 2^31 - 256 and dimensions at most 2^20 (LORA_ERR_UNSUPPORTED). */
+#define LORA_SCALE_BLOCK 128
+size_t lora_block_product_workspace_size(int64_t T, int64_t out_dim, int64_t in_dim,
+                                         int32_t transposed);
+int lora_block_product(int64_t T, int64_t out_dim, int64_t in_dim, const void* X,
+                       const uint8_t* W8, const float* sw, void* Y, int32_t transposed, void* ws,
+                       size_t ws_bytes, void* stream);
+/* Codes and block scales of a bf16 W [out_dim, in_dim] (once per frozen weight), by the rule above
+ * over 128 x 128 blocks. */
+int lora_block_quantize_weight(const void* W, int64_t out_dim, int64_t in_dim, uint8_t* W8,
+                               float* sw, void* stream);
+/* The activations' quantisation alone: codes [rows, K] and scales [rows, ceil(K / 128)] of a bf16
+ * [rows, K] matrix. K % 16 == 0. */
+int lora_block_quantize(const void* src, int64_t rows, int64_t K, uint8_t* codes, float* scales,
+                        void* stream);
+
+/* ---- layer norm in front of an adapted linear -------------------------------------------------*/
+/* Rows of X [T, dim], dtype LORA_F32 or LORA_BF16; gamma, beta and their gradients fp32 [dim] (they
+ * may live in an arena's magnitude range: no decay, plain learning rate).
+ *   LORA_NORM_LAYER: mean = sum x / dim, var = sum (x - mean)^2 / dim
+ *   LORA_NORM_RMS:   mean = 0,           var = sum x^2 / dim          (beta must be NULL)
+ *   rstd = 1 / sqrt(var + eps),  xhat = (x - mean) rstd
+ *   forward   Y = gamma xhat + beta;  stats [T, 2] fp32 = (mean, rstd), which the backward reads
+ *   backward  g = gamma dY;  dX = rstd (g - [LAYER: sum g / dim] - xhat (sum g xhat) / dim) + dX_add
+ *             dgamma += sum_t dY xhat;  dbeta += sum_t dY
+ * All arithmetic in fp32 from registers (the variance is of the centred values), outputs rounded
+ * once. beta may be NULL (no shift); dX_add [T, dim] (the residual branch's gradient) may be NULL
+ * and may be dX itself; dgamma, dbeta and dX may be NULL each (not all). The token sums are
+ * reduced in a fixed order: reruns are bitwise equal. dim a multiple of 8 (LORA_ERR_ALIGN) and at
+ * most LORA_NORM_MAX_DIM, T below 2^31 - 256 (LORA_ERR_UNSUPPORTED); T = 0 is a no-op. */
+#define LORA_NORM_LAYER 0
+#define LORA_NORM_RMS 1
+#define LORA_NORM_MAX_DIM 16384
+typedef struct lora_norm_desc {
+  int64_t dim;
+  int32_t kind;        /* LORA_NORM_LAYER | LORA_NORM_RMS */
+  int32_t dtype;       /* LORA_F32 | LORA_BF16 for X, Y, dY, dX */
+  float eps;           /* >= 0 */
+} lora_norm_desc;
+int lora_norm_forward(const lora_norm_desc* d, int64_t T, const void* X, const float* gamma,
+                      const float* beta, void* Y, float* stats, void* stream);
+size_t lora_norm_backward_workspace_size(const lora_norm_desc* d, int64_t T);
+int lora_norm_backward(const lora_norm_desc* d, int64_t T, const void* X, const float* gamma,
+                       const void* dY, const float* stats, const void* dX_add, void* dX,
+                       float* dgamma, float* dbeta, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- orthogonalised update (in place of lora_adamw_step for the adapter matrices) -------------*/
+/* One matrix of the flat arenas, [rows, cols] row-major from element `offset` (a multiple of 4).
+ * The smaller side is at most LORA_MAX_RANK and a multiple of 4. `group` indexes the call's groups
+ * and the matrix lies inside that group's range; its kind decides the decay and the LoRA+ ratio. */
+#define LORA_KIND_A 0
+#define LORA_KIND_B 1
+typedef struct lora_mat {
+  int64_t offset;
+  int64_t rows;
+  int64_t cols;
+  int32_t group;
+  int32_t kind;        /* LORA_KIND_A | LORA_KIND_B */
+} lora_mat;
+
+#define LORA_MUON_ADJUST_ASPECT 0   /* s = sqrt(max(1, rows / cols)) */
+#define LORA_MUON_ADJUST_RMS 1      /* s = 0.2 sqrt(max(rows, cols)): Adam's usual update RMS */
+typedef struct lora_muon_hp {
+  double momentum;      /* mu, 0.95 */
+  double weight_decay;  /* applied to kind A only */
+  double plus_ratio;    /* LoRA+: B's lr = lr * plus_ratio */
+  double coef[3];       /* a, b, c of the Newton-Schulz step (3.4445, -4.7750, 2.0315) */
+  int32_t steps;        /* Newton-Schulz steps, 1 .. 8 (5) */
+  int32_t nesterov;     /* 1: u = c g + mu m, 0: u = m */
+  int32_t adjust;       /* LORA_MUON_ADJUST_* */
+} lora_muon_hp;
+
+/* For every matrix whose group's device status is LORA_OK (others are left untouched):
+ *   m = mu m + c g  (c = d_scale_norm[2 * group], from lora_grad_prepare);  u as above
+ *   X = u / ||u||_F (0 where u is 0);  `steps` times: X <- (a I + b G + c G^2) X, G = X X^T over the
+ *   smaller side
+ *   A: p -= lr s X + lr wd p      B: p -= lr plus_ratio s X       (p before the update in the decay)
+ * lr is the group's; zero_grads != 0 clears the matrices' gradients after reading them. Elements
+ * of the arenas outside the matrices (DoRA magnitudes, norm weights) are not touched: give them
+ * to lora_adamw_step in a group of their own. Matrices must not overlap; any number of them. */
+size_t lora_muon_workspace_size(int32_t n_mats, const lora_mat* mats);
+int lora_muon_step(float* params, float* grads, float* m, int32_t n_groups,
+                   const lora_group* groups, int32_t n_mats, const lora_mat* mats,
+                   const lora_muon_hp* hp, const double* d_scale_norm, const int32_t* d_status,
+                   int32_t zero_grads, void* ws, size_t ws_bytes, void* stream);
+
 /* ---- fused projections ----------------------------------------------------------------------*/
 /* Projections that read one input (q/k/v, gate/up) run as one fused linear: one frozen product
  * over the stacked weight W_cat = [W_0; W_1; ...] ([sum out_k, in]) and one output
