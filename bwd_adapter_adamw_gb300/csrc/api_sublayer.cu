@@ -30,7 +30,7 @@ ProductWs product_carve(int64_t T, int64_t K, void* ws) {
   ProductWs w;
   Carve c(ws);
   w.codes = c.take<uint8_t>((size_t)T * K);
-  w.scales = c.take<float>((size_t)T * ((K + LORA_SCALE_BLOCK - 1) / LORA_SCALE_BLOCK));
+  w.scales = c.take<float>((size_t)block_scales_ld(T) * ((K + LORA_SCALE_BLOCK - 1) / LORA_SCALE_BLOCK));
   w.bytes = c.off + kWsAlign;
   return w;
 }
@@ -96,10 +96,14 @@ int lora_block_product(int64_t T, int64_t out_dim, int64_t in_dim, const void* X
   if (T == 0) return LORA_OK;
   clear_stale();
   BlockProductArgs a{};
-  a.X = X; a.T = T; a.out_dim = out_dim; a.in_dim = in_dim;
+  a.T = T; a.out_dim = out_dim; a.in_dim = in_dim;
   a.W8 = W8; a.sw = sw; a.transposed = transposed != 0; a.Y = Y;
-  a.codes = w.codes; a.scales = w.scales;
-  return cuda_status(launch_block_product(a, (cudaStream_t)stream));
+  a.codes = w.codes; a.scales = w.scales; a.ld_scales = block_scales_ld(T);
+  const cudaStream_t st = (cudaStream_t)stream;
+  LORA_TRY(launch_block_quant(X, T, transposed ? out_dim : in_dim, w.codes, w.scales, 1,
+                              a.ld_scales, st));
+  LORA_TRY(launch_block_gemm(a, st, 0));
+  return LORA_OK;
 }
 
 int lora_block_quantize_weight(const void* W, int64_t out_dim, int64_t in_dim, uint8_t* W8,
@@ -118,7 +122,9 @@ int lora_block_quantize(const void* src, int64_t rows, int64_t K, uint8_t* codes
   if (K % 16 || !al16(src) || !al16(codes) || !al16(scales)) return LORA_ERR_ALIGN;
   if (K > kMaxDim || rows >= kMaxTokens) return LORA_ERR_UNSUPPORTED;
   clear_stale();
-  return cuda_status(launch_block_quant(src, rows, K, codes, scales, (cudaStream_t)stream));
+  return cuda_status(launch_block_quant(src, rows, K, codes, scales,
+                                        (K + LORA_SCALE_BLOCK - 1) / LORA_SCALE_BLOCK, 1,
+                                        (cudaStream_t)stream));
 }
 
 int lora_norm_forward(const lora_norm_desc* d, int64_t T, const void* X, const float* gamma,

@@ -54,7 +54,8 @@ constexpr int kQuantBatch = 4;
 __global__ void __launch_bounds__(256) k_block_quant(const __nv_bfloat16* __restrict__ src,
                                                      int64_t rows, int64_t K, int64_t nkb,
                                                      uint8_t* __restrict__ codes,
-                                                     float* __restrict__ scales) {
+                                                     float* __restrict__ scales, int64_t ld_row,
+                                                     int64_t ld_kb) {
   grid_dep_sync();
   const int sub = threadIdx.x & 15;
   const int64_t blocks = rows * nkb;
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(256) k_block_quant(const __nv_bfloat16* __rest
       if (b >= blocks) break;
       float rcp, sc;
       block_scales(m, rcp, sc);
-      if (sub == 0) scales[b] = sc;
+      if (sub == 0) scales[row[u] * ld_row + (b - row[u] * nkb) * ld_kb] = sc;
       if (col[u] < K) *reinterpret_cast<uint2*>(codes + row[u] * K + col[u]) = encode8(v[u], rcp);
     }
   }
@@ -122,74 +123,18 @@ __global__ void __launch_bounds__(256) k_block_quant_weight(const __nv_bfloat16*
   }
 }
 
-__device__ __forceinline__ float e4m3_to_f(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-}
-
-// 64 x 64 outputs per CTA on CUDA cores: each block of 128 summed over its unscaled codes, then
-// added with its two scales.
-__global__ void __launch_bounds__(256) k_block_product(const uint8_t* __restrict__ A,
-                                                       const float* __restrict__ sa,
-                                                       const uint8_t* __restrict__ W,
-                                                       const float* __restrict__ sw, int64_t T,
-                                                       int64_t N, int64_t K, int64_t ldw,
-                                                       int64_t ld_sw, int transposed,
-                                                       __nv_bfloat16* __restrict__ Y) {
-  grid_dep_sync();
-  __shared__ float a[32][65], w[32][65];
-  const int64_t t0 = (int64_t)blockIdx.x * 64, n0 = (int64_t)blockIdx.y * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t nkb = (K + kBlk - 1) / kBlk;
-  float acc[4][4] = {};
-  for (int64_t kb = 0; kb < nkb; ++kb) {
-    float d[4][4] = {};
-    for (int64_t k0 = kb * kBlk; k0 < kb * kBlk + kBlk; k0 += 32) {
-      for (int e = threadIdx.x; e < 32 * 64; e += 256) {
-        int kk = e & 31, r = e >> 5;
-        a[kk][r] = t0 + r < T && k0 + kk < K ? e4m3_to_f(A[(t0 + r) * K + k0 + kk]) : 0.f;
-        if (transposed) { kk = e >> 6; r = e & 63; }
-        const int64_t at = transposed ? (k0 + kk) * ldw + n0 + r : (n0 + r) * ldw + k0 + kk;
-        w[kk][r] = n0 + r < N && k0 + kk < K ? e4m3_to_f(W[at]) : 0.f;
-      }
-      __syncthreads();
-#pragma unroll 8
-      for (int kk = 0; kk < 32; ++kk)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) d[i][j] = fmaf(a[kk][ty + 16 * i], w[kk][tx + 16 * j], d[i][j]);
-      __syncthreads();
-    }
-    const int64_t nb = n0 / kBlk;
-    const float s = transposed ? sw[kb * ld_sw + nb] : sw[nb * ld_sw + kb];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t t = t0 + ty + 16 * i;
-      const float f = t < T ? sa[t * nkb + kb] * s : 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(f, d[i][j], acc[i][j]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t t = t0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (t < T && n < N) Y[t * N + n] = __float2bfloat16(acc[i][j]);
-    }
-}
-
 }  // namespace
 
 cudaError_t launch_block_quant(const void* src, int64_t rows, int64_t K, uint8_t* codes,
-                               float* scales, cudaStream_t st) {
+                               float* scales, int64_t ld_row, int64_t ld_kb, cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
   const int64_t nkb = (K + kBlk - 1) / kBlk;
   int64_t g = (rows * nkb + 16 * kQuantBatch - 1) / (16 * kQuantBatch);
   if (g > 8 * 152) g = 8 * 152;
   prof_begin(0, st);
   return launch_kernel(k_block_quant, (unsigned)g, 256, 0, st,
-                       static_cast<const __nv_bfloat16*>(src), rows, K, nkb, codes, scales);
+                       static_cast<const __nv_bfloat16*>(src), rows, K, nkb, codes, scales, ld_row,
+                       ld_kb);
 }
 
 cudaError_t launch_block_quant_weight(const void* W, int64_t rows, int64_t cols, uint8_t* codes,
@@ -198,18 +143,6 @@ cudaError_t launch_block_quant_weight(const void* W, int64_t rows, int64_t cols,
   return launch_kernel(k_block_quant_weight,
                        dim3((unsigned)((cols + kBlk - 1) / kBlk), (unsigned)((rows + kBlk - 1) / kBlk)),
                        256, 0, st, static_cast<const __nv_bfloat16*>(W), rows, cols, codes, scales);
-}
-
-cudaError_t launch_block_product(const BlockProductArgs& a, cudaStream_t st) {
-  const int64_t K = a.transposed ? a.out_dim : a.in_dim, N = a.transposed ? a.in_dim : a.out_dim;
-  cudaError_t e = launch_block_quant(a.X, a.T, K, a.codes, a.scales, st);
-  if (e != cudaSuccess) return e;
-  prof_begin(0, st);
-  return launch_kernel(k_block_product,
-                       dim3((unsigned)((a.T + 63) / 64), (unsigned)((N + 63) / 64)), 256, 0, st,
-                       (const uint8_t*)a.codes, (const float*)a.scales, a.W8, a.sw, a.T, N, K,
-                       a.in_dim, (a.in_dim + kBlk - 1) / kBlk, a.transposed,
-                       static_cast<__nv_bfloat16*>(a.Y));
 }
 
 }  // namespace lora

@@ -1,0 +1,672 @@
+// Frozen product over E4M3 codes with one scale per block of 128, on sm_103a tensor cores:
+//
+//   Y[t, n] = sum_kb sx[t, kb] sw[n / 128, kb] D_kb[t, n] (+ mask (P Q^T)[t, n]),
+//   D_kb[t, n] = sum_{k in block kb} x8[t, k] w8[n, k]
+//
+// The scales change along the contraction, so one accumulator cannot run over it: every block of
+// 128 is summed on the tensor cores (kind::f8f6f4) into one of two TMEM buffers, and the epilogue
+// warps add it, scaled, to fp32 accumulators in their registers while the next block's MMAs run
+// into the other buffer. The LoRA term (kind::tf32) is one more such block with scale one.
+//
+// For the input gradient the weight's codes are read in place: the operand is [out, in] with the
+// contraction along the rows, an MN-major tile in the 128-byte swizzle.
+//
+// Two kernels. k_block_tile: 128 tokens x BN outputs, tokens as the M side. k_block_stream: 128
+// outputs x NT tokens, the weight as the M side and the contraction split over a cluster, for few
+// tokens, where the weight's bytes bound the product.
+#include <cstring>
+#include <mutex>
+
+#include "tc_ptx.cuh"
+
+namespace lora {
+
+namespace {
+using namespace tc;
+
+constexpr int kBlk = LORA_SCALE_BLOCK;
+constexpr int kTileBytes = 128 * 128;   // 128 rows of 128 bytes
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// (a0, a1) += (s0, s1) * (d0, d1): two FMAs in one instruction
+__device__ __forceinline__ void fma2(float& a0, float& a1, float s0, float s1, uint32_t d0,
+                                     uint32_t d1) {
+  uint64_t a, s, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(s) : "f"(s0), "f"(s1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(s), "l"(d));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+}
+
+// ---- 128 tokens x BN outputs ------------------------------------------------------------------
+// Warps: 0 TMA, 1 TMEM allocation and MMA (one thread), 2 and 3 idle; 4 .. 11 epilogue: warp w
+// takes TMEM lanes 32 (w % 4) .. and columns (w - 4) / 4 * BN / 2 .., so that a thread holds BN / 2
+// accumulators of one row and, BN / 2 dividing 128, one weight scale per block.
+constexpr int kTileThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kBox = 32 * 64;   // 32 rows x 32 bf16 columns, 64-byte swizzle
+
+template <int BN>
+struct TileCfg {
+  static_assert(BN == 256 || BN == 128, "columns of one warp lie in one block of 128");
+  static constexpr int kStageBytes = kTileBytes + BN * 128;
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kEpiBytes = kEpiWarps * 2 * kBox;
+  static constexpr int kSmem = kStages * kStageBytes + kEpiBytes + 512 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+struct TileParams {
+  CUtensorMap ta;     // codes [T, K], box {128, 128}
+  CUtensorMap tb;     // W8 [out, in], box {128, BN} (forward) or {128, 128} (transposed)
+  CUtensorMap to;     // Y [T, N] bf16, box {32, 32}
+  CUtensorMap tp;     // P [T, rank] fp32, box {32, 128}
+  CUtensorMap tq;     // Q [N, rank] fp32, box {32, BN}
+  const float* sx;
+  const float* sw;
+  int64_t ld_sx;
+  int64_t sw_n, sw_k;           // strides of sw over blocks of N and of K
+  int64_t T, N;
+  int32_t nk, n_lora;           // K-blocks; 32-wide LoRA blocks (0: none)
+  int32_t n_tiles, m_tiles, group_m, total;
+  uint32_t* err;
+  unsigned long long wait_limit;
+  DropParams drop;
+};
+
+__device__ __forceinline__ void tile_at(const TileParams& p, int t, int32_t& m0, int32_t& nt) {
+  const int per_group = p.group_m * p.n_tiles;
+  const int group = t / per_group, first = group * p.group_m;
+  const int gsize = min(p.group_m, p.m_tiles - first);
+  const int idx = t - group * per_group;
+  nt = idx / gsize;
+  m0 = (first + idx % gsize) * 128;
+}
+
+template <int BN, bool TR>
+__global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_constant__ TileParams p) {
+  using C = TileCfg<BN>;
+  constexpr int kStages = C::kStages;
+  constexpr int HC = BN / 2;   // columns of an epilogue warp
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* boxes = base + kStages * C::kStageBytes;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(boxes + C::kEpiBytes);
+  uint64_t* empty_bar = full_bar + kStages;
+  uint64_t* acc_full = empty_bar + kStages;   // [2]
+  uint64_t* acc_empty = acc_full + 2;         // [2]
+  uint64_t* mma_done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], kEpiWarps);
+    }
+    mbar_init(mma_done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_sync();
+
+  const int nblk = p.nk + (p.n_lora > 0 ? 1 : 0);   // accumulator uses per tile
+  if (warp < 4) {
+    // 384 threads start with 168 registers each; the epilogue takes what the other four warps
+    // leave: 56 + 2 x 224 = 3 x 168
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 && lane == 0) {
+      int g = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < p.total && ok; t += gridDim.x) {
+        int32_t m0, nt;
+        tile_at(p, t, m0, nt);
+        const int n0 = nt * BN;
+        for (int kb = 0; kb < p.nk + p.n_lora; ++kb, ++g) {
+          const int s = g % kStages;
+          const uint32_t ph = (uint32_t)(g / kStages) & 1u;
+          if (g >= kStages && !mbar_wait_for(&empty_bar[s], ph ^ 1u, 1u, p.err, p.wait_limit)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = base + s * C::kStageBytes;
+          uint8_t* sb = sa + kTileBytes;
+          mbar_expect_tx(&full_bar[s], C::kStageBytes);
+          if (kb < p.nk) {
+            tma_load_2d(sa, &p.ta, &full_bar[s], kb * kBlk, m0);
+            if constexpr (TR) {
+#pragma unroll
+              for (int c = 0; c < BN / 128; ++c)
+                tma_load_2d(sb + c * kTileBytes, &p.tb, &full_bar[s], n0 + c * 128, kb * kBlk);
+            } else {
+              tma_load_2d(sb, &p.tb, &full_bar[s], kb * kBlk, n0);
+            }
+          } else {
+            tma_load_2d(sa, &p.tp, &full_bar[s], (kb - p.nk) * 32, m0);
+            tma_load_2d(sb, &p.tq, &full_bar[s], (kb - p.nk) * 32, n0);
+          }
+        }
+      }
+      // every issued load has landed before the CTA may exit
+      for (int gg = (g > kStages ? g - kStages : 0); gg < g; ++gg)
+        if (!mbar_wait(&full_bar[gg % kStages], (uint32_t)(gg / kStages) & 1u, 1u, p.err)) break;
+    } else if (warp == 1 && lane == 0) {
+      constexpr uint32_t id8 = idesc(kFmtE4M3, 128, BN, false, TR);
+      constexpr uint32_t id32 = idesc(kFmtTF32, 128, BN);
+      int g = 0, j = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < p.total && ok; t += gridDim.x) {
+        for (int kb = 0; kb < nblk && ok; ++kb, ++j) {
+          const int b = j & 1, use = j >> 1;
+          if (use >= 1 && !mbar_wait_for(&acc_empty[b], (uint32_t)(use - 1) & 1u, 2u, p.err, p.wait_limit)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const uint32_t d = tmem + 256u * (uint32_t)b;
+          const int loads = kb < p.nk ? 1 : p.n_lora;
+          for (int l = 0; l < loads; ++l, ++g) {
+            const int s = g % kStages;
+            if (!mbar_wait_for(&full_bar[s], (uint32_t)(g / kStages) & 1u, 2u, p.err, p.wait_limit)) {
+              ok = false;
+              break;
+            }
+            fence_after();
+            const uint32_t sa = smem_u32(base + s * C::kStageBytes);
+            const uint64_t da = smem_desc_sw128(sa);
+            if (kb < p.nk) {
+              // K = 32 codes per instruction: 32 bytes along a K-major row, four 8-row groups
+              // of the MN-major tile
+              const uint64_t db = TR ? smem_desc_sw128_mn(sa + kTileBytes, kTileBytes)
+                                     : smem_desc_sw128(sa + kTileBytes);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_f8(d, da + 2 * k, db + (TR ? 256 : 2) * k, id8, k > 0 ? 1u : 0u);
+            } else {
+              const uint64_t db = smem_desc_sw128(sa + kTileBytes);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_tf32(d, da + 2 * k, db + 2 * k, id32, (l > 0 || k > 0) ? 1u : 0u);
+            }
+            umma_commit(&empty_bar[s]);
+          }
+          if (ok) umma_commit(&acc_full[b]);
+        }
+      }
+      umma_commit(mma_done);
+      mbar_wait(mma_done, 0u, 2u, p.err);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    uint8_t* box0 = boxes + (warp - 4) * 2 * kBox;
+    int nbox = 0, j = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < p.total && ok; t += gridDim.x) {
+      int32_t m0, nt;
+      tile_at(p, t, m0, nt);
+      const int64_t m = m0 + q * 32 + lane;
+      const int64_t n0 = (int64_t)nt * BN + h * HC;
+      const bool row_ok = m < p.T;
+      const float* sx = p.sx + m;   // the padded stride covers every row of the tile
+      const float* sw = p.sw + (n0 < p.N ? n0 / kBlk : 0) * p.sw_n;
+      float acc[HC];
+#pragma unroll
+      for (int c = 0; c < HC; ++c) acc[c] = 0.f;
+      float s_next = row_ok ? __ldg(sx) * __ldg(sw) : 0.f;
+      for (int kb = 0; kb < nblk; ++kb, ++j) {
+        const int b = j & 1;
+        const float s = s_next;
+        if (kb + 1 < p.nk)
+          s_next = row_ok ? __ldg(sx + (kb + 1) * p.ld_sx) * __ldg(sw + (kb + 1) * p.sw_k) : 0.f;
+        // warp-uniform: the TMEM loads below are .sync.aligned
+        if (!__all_sync(0xffffffffu, mbar_wait_for(&acc_full[b], (uint32_t)(j >> 1) & 1u, 4u, p.err,
+                                                   p.wait_limit))) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint32_t d = tmem + lanes + 256u * (uint32_t)b + (uint32_t)(h * HC);
+        if (kb < p.nk) {
+          uint32_t r0[32], r1[32];
+          tmem_ld32_nw(d, r0);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < HC / 32; c += 2) {
+            tmem_ld32_nw(d + (uint32_t)(c * 32 + 32), r1);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              fma2(acc[c * 32 + i], acc[c * 32 + i + 1], s, s, r0[i], r0[i + 1]);
+            tmem_wait_ld();
+            if (c + 2 < HC / 32) {
+              tmem_ld32_nw(d + (uint32_t)(c * 32 + 64), r0);
+            } else {   // this warp has read its part of the buffer
+              fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&acc_empty[b]);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              fma2(acc[c * 32 + 32 + i], acc[c * 32 + 33 + i], s, s, r1[i], r1[i + 1]);
+            if (c + 2 < HC / 32) tmem_wait_ld();
+          }
+        } else {   // the LoRA term, masked by dropout at (t, n)
+#pragma unroll
+          for (int c = 0; c < HC / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32_nw(d + (uint32_t)(c * 32), r);
+            tmem_wait_ld();
+            if (p.drop.enabled) {
+              const DropRow row = drop_row(p.drop, row_ok ? m : 0);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (drop_keep_at(row, p.drop.tau, n0 + c * 32 + i))
+                  acc[c * 32 + i] += __uint_as_float(r[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[c * 32 + i] += __uint_as_float(r[i]);
+            }
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[b]);
+        }
+      }
+      if (!ok) break;
+      // rows past T and columns past N are clipped by the bulk store
+      const int32_t wrow = m0 + q * 32;
+      if (wrow < p.T) {
+#pragma unroll
+        for (int c = 0; c < HC / 32; ++c) {
+          if (n0 + c * 32 >= p.N) break;
+          uint8_t* box = box0 + (nbox & 1) * kBox;
+          ++nbox;
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int gq = 0; gq < 4; ++gq)
+            store8(reinterpret_cast<__nv_bfloat16*>(box + lane * 64 + ((gq ^ ((lane >> 1) & 3)) << 4)),
+                   acc + c * 32 + gq * 8);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&p.to, box, (int32_t)(n0 + c * 32), wrow);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        }
+      }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+    fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int BN, bool TR>
+cudaError_t launch_tile(const BlockProductArgs& a, const TileParams& prm, cudaStream_t st) {
+  static bool attr = false;
+  if (!attr) {
+    cudaError_t e = cudaFuncSetAttribute(k_block_tile<BN, TR>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<BN>::kSmem);
+    if (e != cudaSuccess) return e;
+    attr = true;
+  }
+  const int sms = sm_count();
+  return launch_kernel(k_block_tile<BN, TR>, (unsigned)(prm.total < sms ? prm.total : sms),
+                       kTileThreads, TileCfg<BN>::kSmem, st, prm);
+}
+
+cudaError_t run_tile(const BlockProductArgs& a, cudaStream_t st, int prof_kind) {
+  static TileParams prm;   // large: filled per call on the host, copied into the launch
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);
+  std::memset(&prm, 0, sizeof(prm));
+  const int64_t K = a.transposed ? a.out_dim : a.in_dim, N = a.transposed ? a.in_dim : a.out_dim;
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int64_t mt = (a.T + 127) / 128;
+  // rounds of tiles times their width
+  const int64_t r256 = (mt * ((N + 255) / 256) + sms - 1) / sms * 2;
+  const int64_t r128 = (mt * ((N + 127) / 128) + sms - 1) / sms;
+  const int bn = r128 < r256 ? 128 : 256;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (!make_map_2d(&prm.ta, a.codes, u8, 1, K, a.T, K, 128, 128) ||
+      !make_map_2d(&prm.tb, a.W8, u8, 1, a.in_dim, a.out_dim, a.in_dim, 128, a.transposed ? 128 : bn) ||
+      !make_map_2d(&prm.to, a.Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, N, a.T, N, 32, 32))
+    return cudaErrorInvalidValue;
+  if (a.p) {
+    const CUtensorMapDataType f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    if (!make_map_2d(&prm.tp, a.p, f32, 4, a.rank, a.T, a.rank, 32, 128) ||
+        !make_map_2d(&prm.tq, a.q, f32, 4, a.rank, N, a.rank, 32, bn))
+      return cudaErrorInvalidValue;
+    prm.n_lora = (a.rank + 31) / 32;
+    prm.drop = a.drop;
+  }
+  const int64_t ib = (a.in_dim + kBlk - 1) / kBlk;
+  prm.sx = a.scales; prm.ld_sx = a.ld_scales;
+  prm.sw = a.sw;
+  prm.sw_n = a.transposed ? 1 : ib;
+  prm.sw_k = a.transposed ? ib : 1;
+  prm.T = a.T; prm.N = N;
+  prm.nk = (int32_t)((K + kBlk - 1) / kBlk);
+  prm.n_tiles = (int32_t)((N + bn - 1) / bn);
+  prm.m_tiles = (int32_t)mt;
+  prm.group_m = prm.n_tiles > 16 ? 32 : 1;
+  if ((int64_t)prm.n_tiles * mt > INT32_MAX) return cudaErrorInvalidValue;
+  prm.total = (int32_t)(prm.n_tiles * mt);
+  prm.err = error_word();
+  if (!prm.err) return cudaErrorInvalidDevice;
+  prm.wait_limit = tc_wait_limit();
+  prof_begin(prof_kind, st);
+  cudaError_t e;
+  if (bn == 256) e = a.transposed ? launch_tile<256, true>(a, prm, st) : launch_tile<256, false>(a, prm, st);
+  else e = a.transposed ? launch_tile<128, true>(a, prm, st) : launch_tile<128, false>(a, prm, st);
+  if (e != cudaSuccess) return e;
+  prof_end(prof_kind, st);
+  return cudaGetLastError();
+}
+
+// ---- 128 outputs x NT tokens, the contraction split over a cluster -----------------------------
+// Warps: 0 .. 3 epilogue (warp w drains TMEM lanes 32 w ..: a thread holds one output row and NT
+// accumulators), 4 TMA, 5 TMEM allocation and MMA. Split s of S takes an even share of the
+// K-blocks; the S partial tiles meet in distributed shared memory, each CTA adding an S-th of the
+// tile in split order, so that reruns are bitwise equal.
+constexpr int kStreamThreads = 192;
+
+template <int NT>
+struct StreamCfg {
+  static constexpr int kStageBytes = kTileBytes + NT * 128;
+  static constexpr int kScaleBytes = NT * 4;
+  static constexpr int kTileF32 = 128 * NT * 4;   // the partial tile, over the drained stages
+  static constexpr int kStages = (100 * 1024) / kStageBytes;
+  static constexpr int kSmem = kStages * (kStageBytes + kScaleBytes) + 512 + 1024;
+  static constexpr uint32_t kCols = 2 * NT < 32 ? 32 : 2 * NT;
+  static_assert(kTileF32 <= kStages * kStageBytes, "partial tile fits the stages");
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+struct StreamParams {
+  CUtensorMap tw;     // W8 [out, in], box {128, 128}
+  CUtensorMap tx;     // codes [T, K], box {128, NT}
+  const float* sx;
+  const float* sw;
+  int64_t ld_sx, sw_n, sw_k;
+  int64_t T, N;
+  int32_t nk, splits;
+  __nv_bfloat16* Y;
+  uint32_t* err;
+  unsigned long long wait_limit;
+};
+
+template <int NT, bool TR>
+__global__ void __launch_bounds__(kStreamThreads, 2) k_block_stream(const __grid_constant__ StreamParams p) {
+  using C = StreamCfg<NT>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* scales = reinterpret_cast<float*>(base + kStages * C::kStageBytes);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(scales + kStages * NT);
+  uint64_t* empty_bar = full_bar + kStages;   // MMA and epilogue have read the stage
+  uint64_t* acc_full = empty_bar + kStages;   // [2]
+  uint64_t* acc_empty = acc_full + 2;         // [2]
+  uint64_t* mma_done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = (int)blockIdx.x % p.splits, nt = (int)blockIdx.x / p.splits;
+  const int kb0 = (int)((int64_t)p.nk * split / p.splits);
+  const int kb1 = (int)((int64_t)p.nk * (split + 1) / p.splits);
+  const int nk = kb1 - kb0;
+  const int32_t t0 = (int32_t)blockIdx.y * NT, n0 = nt * 128;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1 + 4);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 4);
+    }
+    mbar_init(mma_done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 5) tmem_alloc(tmem_slot, C::kCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  float acc[NT];
+  if (warp == 4) {
+    if (lane == 0) {
+      // The weight does not depend on the kernel before this one (the quantisation of X, which
+      // itself waited for everything earlier), so the first stages' weight tiles are on their way
+      // before that kernel has finished.
+      auto load_w = [&](int i) {
+        const int s = i % kStages;
+        mbar_expect_tx(&full_bar[s], C::kStageBytes + C::kScaleBytes);
+        const int32_t k0 = (kb0 + i) * kBlk;
+        tma_load_2d(base + s * C::kStageBytes, &p.tw, &full_bar[s], TR ? n0 : k0, TR ? k0 : n0);
+      };
+      auto load_x = [&](int i) {
+        const int s = i % kStages;
+        tma_load_2d(base + s * C::kStageBytes + kTileBytes, &p.tx, &full_bar[s], (kb0 + i) * kBlk, t0);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                smem_u32(scales + s * NT)),
+            "l"(p.sx + (int64_t)(kb0 + i) * p.ld_sx + t0), "r"(C::kScaleBytes), "r"(smem_u32(&full_bar[s]))
+            : "memory");
+      };
+      const int ahead = nk < kStages ? nk : kStages;
+      for (int i = 0; i < ahead; ++i) load_w(i);
+      grid_dep_sync();
+      int i = 0;
+      for (; i < ahead; ++i) load_x(i);
+      for (; i < nk; ++i) {
+        if (!mbar_wait_for(&empty_bar[i % kStages], (uint32_t)(i / kStages - 1) & 1u, 1u, p.err, p.wait_limit))
+          break;
+        load_w(i);
+        load_x(i);
+      }
+      // every issued load has landed before the stages are written over or the CTA exits
+      for (int k = (i > kStages ? i - kStages : 0); k < i; ++k)
+        if (!mbar_wait(&full_bar[k % kStages], (uint32_t)(k / kStages) & 1u, 1u, p.err)) break;
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      constexpr uint32_t id8 = idesc(kFmtE4M3, 128, NT, TR, false);
+      for (int i = 0; i < nk; ++i) {
+        const int b = i & 1, s = i % kStages;
+        if (i >= 2 && !mbar_wait_for(&acc_empty[b], (uint32_t)((i >> 1) - 1) & 1u, 2u, p.err, p.wait_limit)) break;
+        if (!mbar_wait_for(&full_bar[s], (uint32_t)(i / kStages) & 1u, 2u, p.err, p.wait_limit)) break;
+        fence_after();
+        const uint32_t sw = smem_u32(base + s * C::kStageBytes);
+        const uint64_t da = TR ? smem_desc_sw128_mn(sw, kTileBytes) : smem_desc_sw128(sw);
+        const uint64_t db = smem_desc_sw128(sw + kTileBytes);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          umma_f8(tmem + (uint32_t)(b * NT), da + (TR ? 256 : 2) * k, db + 2 * k, id8, k > 0 ? 1u : 0u);
+        umma_commit(&empty_bar[s]);
+        umma_commit(&acc_full[b]);
+      }
+      umma_commit(mma_done);
+      mbar_wait(mma_done, 0u, 2u, p.err);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < NT; ++c) acc[c] = 0.f;
+    const float* sw = p.sw + (int64_t)nt * p.sw_n + (int64_t)kb0 * p.sw_k;
+    float w_next = nk > 0 ? __ldg(sw) : 0.f;
+    constexpr int CH = NT == 32 || NT == 64 ? 32 : 16;   // columns in flight beside the accumulators
+    for (int i = 0; i < nk; ++i) {
+      const int b = i & 1, s = i % kStages;
+      const float w = w_next;
+      if (i + 1 < nk) w_next = __ldg(sw + (int64_t)(i + 1) * p.sw_k);
+      // the stage's scales (its full barrier) and the block's sums
+      const bool ready = mbar_wait_for(&full_bar[s], (uint32_t)(i / kStages) & 1u, 4u, p.err, p.wait_limit) &&
+                         mbar_wait_for(&acc_full[b], (uint32_t)(i >> 1) & 1u, 4u, p.err, p.wait_limit);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      fence_after();
+      const float4* sc = reinterpret_cast<const float4*>(scales + s * NT);
+#pragma unroll
+      for (int c = 0; c < NT / CH; ++c) {
+        uint32_t r[CH];
+        const uint32_t d = tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(b * NT + c * CH);
+        if constexpr (CH == 32) tmem_ld32_nw(d, r);
+        else tmem_ld16_nw(d, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int v = 0; v < CH; v += 4) {
+          const float4 f = sc[(c * CH + v) / 4];
+          fma2(acc[c * CH + v], acc[c * CH + v + 1], f.x * w, f.y * w, r[v], r[v + 1]);
+          fma2(acc[c * CH + v + 2], acc[c * CH + v + 3], f.z * w, f.w * w, r[v + 2], r[v + 3]);
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&acc_empty[b]);
+        mbar_arrive(&empty_bar[s]);
+      }
+    }
+  }
+  // all loads have landed and all MMAs are done: the stages become the partial tile [NT][128]
+  __syncthreads();
+  float* part = reinterpret_cast<float*>(base);
+  if (warp < 4) {
+#pragma unroll
+    for (int c = 0; c < NT; ++c) part[c * 128 + warp * 32 + lane] = acc[c];
+  }
+  __syncwarp();
+  if (p.splits > 1) cluster_sync_all();
+  else __syncthreads();
+  const int share = 128 * NT / p.splits;   // floats of the tile that this CTA adds up
+  for (int e = threadIdx.x * 4; e < share; e += kStreamThreads * 4) {
+    const int at = split * share + e;
+    const int64_t t = t0 + at / 128, n = n0 + at % 128;
+    if (t >= p.T || n >= p.N) continue;
+    float4 v;
+    if (p.splits > 1) {
+      v = dsmem_ld4(part + at, 0);
+      for (int s = 1; s < p.splits; ++s) {
+        const float4 o = dsmem_ld4(part + at, (uint32_t)s);
+        v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+      }
+    } else {
+      v = *reinterpret_cast<const float4*>(part + at);
+    }
+    store4(p.Y + t * p.N + n, &v.x);
+  }
+  __syncwarp();
+  if (p.splits > 1) cluster_sync_all();   // the peers have read this CTA's shared memory
+  else __syncthreads();
+  if (warp == 5) {
+    fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+template <int NT, bool TR>
+cudaError_t launch_stream(const BlockProductArgs& a, StreamParams& prm, cudaStream_t st) {
+  using C = StreamCfg<NT>;
+  static bool attr = false;
+  if (!attr) {
+    cudaError_t e = cudaFuncSetAttribute(k_block_stream<NT, TR>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k_block_stream<NT, TR>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    attr = true;
+  }
+  const int64_t K = a.transposed ? a.out_dim : a.in_dim;
+  if (!make_map_2d(&prm.tx, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, a.T, K, 128, NT))
+    return cudaErrorInvalidValue;
+  const int64_t nt = (prm.N + 127) / 128, tt = (a.T + NT - 1) / NT;
+  // as many splits as two CTAs per SM hold, at least two K-blocks each
+  int splits = 1;
+  while (splits < 16 && nt * tt * splits * 2 <= 2 * sm_count() && splits * 4 <= prm.nk) splits *= 2;
+  prm.splits = splits;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(nt * splits), (unsigned)tt);
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)splits;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = add_pdl_attr(at, 1);
+  return cudaLaunchKernelEx(&cfg, k_block_stream<NT, TR>, prm);
+}
+
+cudaError_t run_stream(const BlockProductArgs& a, cudaStream_t st, int prof_kind) {
+  StreamParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  if (!make_map_2d(&prm.tw, a.W8, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.in_dim, a.out_dim, a.in_dim, 128, 128))
+    return cudaErrorInvalidValue;
+  const int64_t K = a.transposed ? a.out_dim : a.in_dim;
+  const int64_t ib = (a.in_dim + kBlk - 1) / kBlk;
+  prm.sx = a.scales; prm.ld_sx = a.ld_scales; prm.sw = a.sw;
+  prm.sw_n = a.transposed ? 1 : ib;
+  prm.sw_k = a.transposed ? ib : 1;
+  prm.T = a.T;
+  prm.N = a.transposed ? a.in_dim : a.out_dim;
+  prm.nk = (int32_t)((K + kBlk - 1) / kBlk);
+  prm.Y = static_cast<__nv_bfloat16*>(a.Y);
+  prm.err = error_word();
+  if (!prm.err || sm_count() <= 0) return cudaErrorInvalidDevice;
+  prm.wait_limit = tc_wait_limit();
+  prof_begin(prof_kind, st);
+  cudaError_t e;
+  if (a.T <= 16) e = a.transposed ? launch_stream<16, true>(a, prm, st) : launch_stream<16, false>(a, prm, st);
+  else if (a.T <= 32) e = a.transposed ? launch_stream<32, true>(a, prm, st) : launch_stream<32, false>(a, prm, st);
+  else if (a.T <= 64) e = a.transposed ? launch_stream<64, true>(a, prm, st) : launch_stream<64, false>(a, prm, st);
+  else e = a.transposed ? launch_stream<128, true>(a, prm, st) : launch_stream<128, false>(a, prm, st);
+  if (e != cudaSuccess) return e;
+  prof_end(prof_kind, st);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_block_gemm(const BlockProductArgs& a, cudaStream_t st, int prof_kind) {
+  if (a.T <= 128 && !a.p) return run_stream(a, st, prof_kind);
+  return run_tile(a, st, prof_kind);
+}
+
+}  // namespace lora

@@ -546,6 +546,11 @@ std::atomic<unsigned long long> g_wait_limit{0};   // pipeline-wait bound in cyc
 
 void set_tc_wait_limit(unsigned long long cycles) { g_wait_limit.store(cycles); }
 
+unsigned long long tc_wait_limit() {
+  const unsigned long long lim = g_wait_limit.load();
+  return lim ? lim : tc::kWaitCycles;
+}
+
 cudaError_t launch_tc_gemm(const TcGemmArgs& a, cudaStream_t st, int prof_kind) {
   static TcParams prm;   // large: filled per call on the host, copied into the launch
   static std::mutex mu;
@@ -594,8 +599,7 @@ cudaError_t launch_tc_gemm(const TcGemmArgs& a, cudaStream_t st, int prof_kind) 
     return cudaErrorInvalidValue;
   prm.err = tc::error_word();
   if (!prm.err) return cudaErrorInvalidDevice;
-  const unsigned long long lim = g_wait_limit.load();
-  prm.wait_limit = lim ? lim : tc::kWaitCycles;
+  prm.wait_limit = tc_wait_limit();
   prm.nk_main = (int32_t)((a.K + kblk - 1) / kblk);
   prm.lora_separate = a.lora_separate;
   prm.n_colscale = a.n_colscale;

@@ -80,6 +80,7 @@ cudaError_t read_tc_error(uint32_t* out, bool reset);
 // the default. Their drain waits (copies in flight, MMAs before the tensor memory is freed) keep
 // the default bound.
 void set_tc_wait_limit(unsigned long long cycles);
+unsigned long long tc_wait_limit();   // the bound in force
 
 // out_slot[j, i] (+)= sum over items of `slot` of part[item][...]; see lowrank.cu
 struct ReduceTab {
@@ -381,22 +382,36 @@ cudaError_t launch_adamw(float* p, float* g, float* m, float* v, const GroupTab&
                          const AdamK& hp, const double* d_scale_norm, const int32_t* d_status,
                          int zero_grads, cudaStream_t st);
 
-// ---- block_fp8.cu: frozen product over E4M3 codes with 128-blocks ----
+// ---- block_fp8.cu: E4M3 operands with 128-blocks ----
+// codes [rows, K] and scales of a bf16 [rows, K] matrix, the scale of block (row, kb) at
+// scales[row * ld_row + kb * ld_kb]
+cudaError_t launch_block_quant(const void* src, int64_t rows, int64_t K, uint8_t* codes,
+                               float* scales, int64_t ld_row, int64_t ld_kb, cudaStream_t st);
+cudaError_t launch_block_quant_weight(const void* W, int64_t rows, int64_t cols, uint8_t* codes,
+                                      float* scales, cudaStream_t st);
+
+// ---- gemm_block.cu: frozen product over them ----
 struct BlockProductArgs {
-  const void* X;             // [T, K] bf16; K = in_dim, or out_dim when transposed
+  const uint8_t* codes;      // [T, K] E4M3 codes of the activations; K = in_dim, or out_dim when
+                             //   transposed
+  const float* scales;       // [ceil(K / 128), ld_scales], block (t, kb) at kb * ld_scales + t
+  int64_t ld_scales;         // block_scales_ld(T)
   int64_t T, out_dim, in_dim;
   const uint8_t* W8;         // [out_dim, in_dim] E4M3 codes
   const float* sw;           // [ceil(out_dim / 128), ceil(in_dim / 128)]
   int32_t transposed;
   void* Y;                   // [T, N] bf16; N = out_dim, or in_dim when transposed
-  uint8_t* codes;            // workspace: [T, K] codes of X and their [T, ceil(K / 128)] scales
-  float* scales;
+  // LoRA term added to Y (tiled kernel only): P [T, rank] Q [N, rank]^T, both fp32, times the
+  // dropout mask at (t, n) when drop.enabled
+  const float* p;
+  const float* q;
+  int32_t rank;
+  DropParams drop;
 };
-cudaError_t launch_block_quant(const void* src, int64_t rows, int64_t K, uint8_t* codes,
-                               float* scales, cudaStream_t st);
-cudaError_t launch_block_quant_weight(const void* W, int64_t rows, int64_t cols, uint8_t* codes,
-                                      float* scales, cudaStream_t st);
-cudaError_t launch_block_product(const BlockProductArgs& a, cudaStream_t st);
+// Token stride of the activation scales: whole 128-token tiles, so that a tile's scales are one
+// aligned run (the entries past T are never used).
+inline int64_t block_scales_ld(int64_t T) { return (T + 127) / 128 * 128; }
+cudaError_t launch_block_gemm(const BlockProductArgs& a, cudaStream_t st, int prof_kind);
 
 // ---- norm.cu ----
 struct NormArgs {
