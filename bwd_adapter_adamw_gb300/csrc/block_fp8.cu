@@ -49,43 +49,45 @@ __device__ __forceinline__ float amax8(const uint4& v) {
 }
 
 // One 1 x 128 block per 16 lanes: a 16-byte load, the maximum over the lanes, an 8-byte store.
-// A thread takes kQuantBatch blocks whose loads are in flight together.
+// A thread takes kQuantBatch blocks whose loads are in flight together. A CTA's blocks lie in a
+// slab of kQuantRows rows, so that a block's row comes from a 32-bit division (with 64-bit ones
+// the kernel was bound by its index arithmetic: 45 us for 4096 x 4096).
 constexpr int kQuantBatch = 4;
+constexpr int kQuantRows = 1024;
 __global__ void __launch_bounds__(256) k_block_quant(const __nv_bfloat16* __restrict__ src,
-                                                     int64_t rows, int64_t K, int64_t nkb,
+                                                     int64_t rows, int64_t K, uint32_t nkb,
                                                      uint8_t* __restrict__ codes,
                                                      float* __restrict__ scales, int64_t ld_row,
                                                      int64_t ld_kb) {
   grid_dep_sync();
   const int sub = threadIdx.x & 15;
-  const int64_t blocks = rows * nkb;
-  const int64_t per_pass = (int64_t)gridDim.x * 16;
-  for (int64_t b0 = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); b0 < blocks;
-       b0 += per_pass * kQuantBatch) {
-    uint4 v[kQuantBatch];
-    int64_t row[kQuantBatch], col[kQuantBatch];
+  const int64_t row0 = (int64_t)blockIdx.y * kQuantRows;
+  const uint32_t blocks = (uint32_t)(rows - row0 < kQuantRows ? rows - row0 : kQuantRows) * nkb;
+  const uint32_t first = blockIdx.x * (16 * kQuantBatch) + (threadIdx.x >> 4);
+  uint4 v[kQuantBatch];
+  int64_t row[kQuantBatch];
+  uint32_t kb[kQuantBatch];
 #pragma unroll
-    for (int u = 0; u < kQuantBatch; ++u) {
-      const int64_t b = b0 + u * per_pass;
-      row[u] = b / nkb;
-      col[u] = (b - row[u] * nkb) * kBlk + sub * 8;
-      v[u] = b < blocks && col[u] < K
-                 ? __ldg(reinterpret_cast<const uint4*>(src + row[u] * K + col[u]))
-                 : make_uint4(0, 0, 0, 0);
-    }
+  for (int u = 0; u < kQuantBatch; ++u) {
+    const uint32_t b = first + u * 16;
+    const uint32_t r = b / nkb;
+    row[u] = row0 + r;
+    kb[u] = b - r * nkb;
+    const int64_t col = (int64_t)kb[u] * kBlk + sub * 8;
+    v[u] = b < blocks && col < K ? __ldg(reinterpret_cast<const uint4*>(src + row[u] * K + col))
+                                 : make_uint4(0, 0, 0, 0);
+  }
 #pragma unroll
-    for (int u = 0; u < kQuantBatch; ++u) {
-      const int64_t b = b0 + u * per_pass;
-      float m = amax8(v[u]);
-      // the 16 lanes of a block are one half of a warp, and all take the same branches
+  for (int u = 0; u < kQuantBatch; ++u) {
+    float m = amax8(v[u]);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFu << (threadIdx.x & 16), m, o));
-      if (b >= blocks) break;
-      float rcp, sc;
-      block_scales(m, rcp, sc);
-      if (sub == 0) scales[row[u] * ld_row + (b - row[u] * nkb) * ld_kb] = sc;
-      if (col[u] < K) *reinterpret_cast<uint2*>(codes + row[u] * K + col[u]) = encode8(v[u], rcp);
-    }
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (first + u * 16 >= blocks) continue;
+    float rcp, sc;
+    block_scales(m, rcp, sc);
+    const int64_t col = (int64_t)kb[u] * kBlk + sub * 8;
+    if (sub == 0) scales[row[u] * ld_row + kb[u] * ld_kb] = sc;
+    if (col < K) *reinterpret_cast<uint2*>(codes + row[u] * K + col) = encode8(v[u], rcp);
   }
 }
 
@@ -129,12 +131,22 @@ cudaError_t launch_block_quant(const void* src, int64_t rows, int64_t K, uint8_t
                                float* scales, int64_t ld_row, int64_t ld_kb, cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
   const int64_t nkb = (K + kBlk - 1) / kBlk;
-  int64_t g = (rows * nkb + 16 * kQuantBatch - 1) / (16 * kQuantBatch);
-  if (g > 8 * 152) g = 8 * 152;
-  prof_begin(0, st);
-  return launch_kernel(k_block_quant, (unsigned)g, 256, 0, st,
-                       static_cast<const __nv_bfloat16*>(src), rows, K, nkb, codes, scales, ld_row,
-                       ld_kb);
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(src);
+  // 32768 slabs (2^25 rows) per launch
+  constexpr int64_t kMost = (int64_t)32768 * kQuantRows;
+  for (int64_t at = 0; at < rows; at += kMost) {
+    const int64_t n = rows - at < kMost ? rows - at : kMost;
+    const int64_t slab = n < kQuantRows ? n : kQuantRows;
+    prof_begin(0, st);
+    cudaError_t e = launch_kernel(
+        k_block_quant,
+        dim3((unsigned)((slab * nkb + 16 * kQuantBatch - 1) / (16 * kQuantBatch)),
+             (unsigned)((n + kQuantRows - 1) / kQuantRows)),
+        256, 0, st, x + at * K, n, K, (uint32_t)nkb, codes + at * K, scales + at * ld_row, ld_row,
+        ld_kb);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_block_quant_weight(const void* W, int64_t rows, int64_t cols, uint8_t* codes,
