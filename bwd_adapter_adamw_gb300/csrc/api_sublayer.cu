@@ -74,6 +74,40 @@ int check_mats(int32_t n_mats, const lora_mat* mats, const GroupTab* groups) {
   return LORA_OK;
 }
 
+// The matrices in the order of their launches: by kernel (smaller side at most 16, each of its own,
+// or above), cluster size, and falling length; a launch takes a run of equal keys.
+struct MuonOrder {
+  int32_t at;      // index into the caller's table
+  int32_t key;     // cluster size and smaller side (0: above 16)
+  MuonMat m;
+};
+
+std::vector<MuonOrder> muon_order(int32_t n_mats, const lora_mat* mats) {
+  std::vector<MuonOrder> v(n_mats);
+  for (int32_t i = 0; i < n_mats; ++i) {
+    const lora_mat& e = mats[i];
+    MuonMat& t = v[i].m;
+    t = MuonMat{};
+    t.offset = e.offset;
+    t.tall = e.rows > e.cols;
+    t.s = (int32_t)std::min(e.rows, e.cols);
+    t.n = std::max(e.rows, e.cols);
+    t.group = e.group;
+    v[i].at = i;
+    v[i].key = muon_cluster(t, n_mats) * 32 + (t.s <= 16 ? t.s : 0);
+  }
+  std::stable_sort(v.begin(), v.end(), [](const MuonOrder& a, const MuonOrder& b) {
+    return a.key != b.key ? a.key < b.key : a.m.n > b.m.n;
+  });
+  return v;
+}
+
+int32_t muon_run(const std::vector<MuonOrder>& v, int32_t at) {   // matrices of the launch at `at`
+  int32_t n = 1;
+  while (n < kMuonMatsPerLaunch && at + n < (int32_t)v.size() && v[at + n].key == v[at].key) ++n;
+  return n;
+}
+
 }  // namespace
 
 extern "C" {
@@ -170,7 +204,15 @@ int lora_norm_backward(const lora_norm_desc* d, int64_t T, const void* X, const 
 
 size_t lora_muon_workspace_size(int32_t n_mats, const lora_mat* mats) {
   if (check_mats(n_mats, mats, nullptr) != LORA_OK) return 0;
-  return kWsAlign;
+  // the launches run one after the other and share the room for tiles that do not fit on chip
+  const std::vector<MuonOrder> v = muon_order(n_mats, mats);
+  size_t most = 0;
+  for (int32_t at = 0; at < n_mats;) {
+    const int32_t n = muon_run(v, at);
+    most = std::max(most, muon_spill_bytes(v[at].m, v[at].key / 32, n));
+    at += n;
+  }
+  return most + kWsAlign;
 }
 
 int lora_muon_step(float* params, float* grads, float* m, int32_t n_groups,
@@ -200,16 +242,13 @@ int lora_muon_step(float* params, float* grads, float* m, int32_t n_groups,
   k.a = (float)hp->coef[0]; k.b = (float)hp->coef[1]; k.c = (float)hp->coef[2];
   k.steps = hp->steps; k.nesterov = hp->nesterov;
   MuonTab tab;
-  for (int32_t at = 0; at < n_mats; at += kMuonMatsPerLaunch) {
-    tab.n = std::min(n_mats - at, (int32_t)kMuonMatsPerLaunch);
+  const std::vector<MuonOrder> v = muon_order(n_mats, mats);
+  for (int32_t at = 0; at < n_mats;) {
+    tab.n = muon_run(v, at);
     for (int32_t i = 0; i < tab.n; ++i) {
-      const lora_mat& e = mats[at + i];
+      const lora_mat& e = mats[v[at + i].at];
       MuonMat& t = tab.m[i];
-      t.offset = e.offset;
-      t.tall = e.rows > e.cols;
-      t.s = (int32_t)std::min(e.rows, e.cols);
-      t.n = std::max(e.rows, e.cols);
-      t.group = e.group;
+      t = v[at + i].m;
       const double lr = g.lr[e.group];
       const double adj = hp->adjust == LORA_MUON_ADJUST_RMS
                              ? 0.2 * std::sqrt((double)t.n)
@@ -219,7 +258,8 @@ int lora_muon_step(float* params, float* grads, float* m, int32_t n_groups,
       t.step = (float)(lr * adj * (e.kind == LORA_KIND_B ? hp->plus_ratio : 1.0));
     }
     LORA_TRY(launch_muon(params, grads, m, tab, k, d_scale_norm, d_status, zero_grads != 0,
-                         (cudaStream_t)stream));
+                         v[at].key / 32, Carve(ws).take<char>(1), (cudaStream_t)stream));
+    at += tab.n;
   }
   return LORA_OK;
 }

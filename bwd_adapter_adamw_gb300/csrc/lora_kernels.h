@@ -454,8 +454,15 @@ struct MuonK {
   float mu, a, b, c;
   int32_t steps, nesterov;
 };
+constexpr int kMuonMaxCtas = 152;      // CTAs of a persistent launch of the tensor-core form
+// CTAs of the cluster that takes a matrix, with n_mats matrices in the call
+int muon_cluster(const MuonMat& m, int n_mats);
+// workspace of a launch over n such matrices (tiles that do not fit on chip)
+size_t muon_spill_bytes(const MuonMat& m, int C, int n);
+// One launch: the table's matrices share the cluster size C, and their smaller sides are all
+// above 16, or all equal and at most 16.
 cudaError_t launch_muon(float* p, float* g, float* m, const MuonTab& tab, const MuonK& hp,
-                        const double* scale_norm, const int32_t* status, int zero_grads,
-                        cudaStream_t st);
+                        const double* scale_norm, const int32_t* status, int zero_grads, int C,
+                        void* spill, cudaStream_t st);
 
 }  // namespace lora

@@ -1,185 +1,880 @@
 // Orthogonalised update of the adapter matrices: momentum, then a Newton-Schulz sequence
-// X <- (a I + b G + c G^2) X, G = X X^T over the smaller side (at most 64), from X = u / ||u||_F.
+// X <- (a I + b G + c G^2) X, G = X X^T over the smaller side s (at most 64), from X = u / ||u||_F.
 //
 // The smaller side is the adapter's rank, so the sequence acts on the small Gram matrix G alone:
 // with P = a I + b G + c G^2 (a polynomial in G, so they commute) one step maps G to P G P and
-// multiplies X by P. Several steps then cost one Gram matrix, small products and one product
+// multiplies X by P. Several steps then cost one Gram matrix, small products, and one product
 // Q X = P_m .. P_1 X on the long axis. A rounding of G, relative to its largest eigenvalue, is
-// amplified by about a^2 per step at the smallest ones, so after at most kStageSteps steps the
-// Gram matrix is formed again from Q X.
-#include "lora_kernels.h"
+// amplified by about a^2 per step at the smallest ones, so after at most kStageSteps steps (five
+// steps: two, then three) the Gram matrix is formed again from Q X, which brings the error down
+// to that of iterating on X itself (the CPU oracle's bound in the tests).
+//
+// One cluster of CTAs per matrix, its long axis spread over the CTAs, u held on chip: the arenas
+// are read and written once (20 bytes per element: p and m both ways, g in). The Gram matrices of
+// the CTAs are added through distributed shared memory in rank order (bitwise reproducible), and
+// every CTA repeats the small products.
+//
+// s <= 16: CUDA cores, u in fp32 (k_muon_simt). Larger s: the two long products on tensor cores
+// (k_muon_tc), u as a two-term bf16 split, all four products of the terms kept.
+#include <algorithm>
+#include <mutex>
+
+#include "tc_ptx.cuh"
 
 namespace lora {
 
 namespace {
+using namespace tc;
 
 constexpr int kMuonThreads = 256;
-constexpr int kS = LORA_MAX_RANK;   // largest smaller side
-constexpr int kLd = kS + 1;         // row stride of the small matrices
-constexpr int kTile = 32;           // long-axis elements per tile
 constexpr int kStageSteps = 3;
-constexpr int kMuonSmem = (5 * kS * kLd + 2 * kTile * kLd) * 4;
 
-__device__ __forceinline__ float block_max(float v, float* sh) {
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = sh[0];
-  for (int w = 1; w < kMuonThreads / 32; ++w) v = fmaxf(v, sh[w]);
   return v;
 }
 
-// C = alpha I + beta A + gamma A B for s x s matrices (B and A commute; C distinct from both)
-__device__ void small_mm(float* C, const float* A, const float* B, int s, float alpha, float beta,
-                         float gamma) {
-  for (int e = threadIdx.x; e < s * s; e += kMuonThreads) {
-    const int i = e / s, j = e % s;
-    float d = 0.f;
-    for (int k = 0; k < s; ++k) d = fmaf(A[i * kLd + k], B[k * kLd + j], d);
-    C[i * kLd + j] = gamma * d + beta * A[i * kLd + j] + (i == j ? alpha : 0.f);
+__device__ __forceinline__ float dsmem_ld(const float* local, uint32_t rank) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  cluster_sync_all();
+}
+
+// The power of two that brings the cluster's largest |u| to about one when its squares could
+// leave the fp32 range; one otherwise. `sh` holds 8 floats and the CTA's maximum.
+__device__ __forceinline__ float range_scale(float mx, float* sh, int C) {
+  mx = warp_max(mx);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = mx;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kMuonThreads / 32; ++w) mx = fmaxf(mx, sh[w]);
+    sh[8] = mx;
   }
+  if (C > 1) cluster_sync();
+  else __syncthreads();
+  mx = sh[8];
+  for (int r = 0; r < C; ++r) mx = C > 1 ? fmaxf(mx, dsmem_ld(sh + 8, (uint32_t)r)) : mx;
+  if (C > 1) cluster_sync();   // sh may be written again
+  if (!(mx > 0.f) || !isfinite(mx) || (mx > 0x1p-30f && mx < 0x1p30f)) return 1.f;
+  return exp2f((float)-min(max(ilogbf(mx), -126), 126));
+}
+
+// ---- s <= 16 on CUDA cores ----------------------------------------------------------------------
+// S = 4 S4. u [columns][SP] fp32 in shared memory (SP keeps 4-way bank conflicts at most for a
+// column-wise walk); columns past the cap are computed again from g and m in every pass.
+template <int S4>
+struct SimtCfg {
+  static constexpr int S = 4 * S4;
+  static constexpr int SP = S % 8 == 0 ? S + 4 : S;
+  static constexpr int kBlocks = S4 * S4;                      // 4 x 4 blocks of the Gram matrix
+  static constexpr int kLanes = kBlocks == 9 ? 16 : kBlocks;   // threads of one column group
+  static constexpr int kGroups = kMuonThreads / kLanes;
+  static constexpr int kSmallFloats = 8 * S * S + 5 * S * S + 16;
+  static constexpr int kCap = (200 * 1024 - kSmallFloats * 4) / (SP * 4) / 4 * 4;
+};
+
+template <int S4>
+__device__ __forceinline__ void simt_mm(float* C, const float* A, const float* B) {
+  constexpr int S = 4 * S4;
+  const int i = threadIdx.x / S, j = threadIdx.x % S;
+  float d = 0.f;
+  if (threadIdx.x < S * S) {
+#pragma unroll
+    for (int k = 0; k < S; ++k) d = fmaf(A[i * S + k], B[k * S + j], d);
+  }
+  __syncthreads();
+  if (threadIdx.x < S * S) C[threadIdx.x] = d;
   __syncthreads();
 }
 
-// One matrix per CTA.
-__global__ void __launch_bounds__(kMuonThreads) k_muon(float* __restrict__ P, float* __restrict__ G,
-                                                       float* __restrict__ M, const MuonTab tab,
-                                                       const MuonK hp,
-                                                       const double* __restrict__ scale_norm,
-                                                       const int32_t* __restrict__ status,
-                                                       int zero_grads) {
+template <int S4>
+__global__ void __launch_bounds__(kMuonThreads) k_muon_simt(float* __restrict__ P, float* __restrict__ G,
+                                                            float* __restrict__ M,
+                                                            const __grid_constant__ MuonTab tab,
+                                                            const MuonK hp,
+                                                            const double* __restrict__ scale_norm,
+                                                            const int32_t* __restrict__ status,
+                                                            int zero_grads, int C) {
   grid_dep_sync();
+  using F = SimtCfg<S4>;
+  constexpr int S = F::S, SP = F::SP;
   extern __shared__ float sm[];
-  float* g0 = sm;                    // Gram matrix
-  float* q = g0 + kS * kLd;          // product of the steps so far
-  float* t1 = q + kS * kLd;
-  float* t2 = t1 + kS * kLd;
-  float* t3 = t2 + kS * kLd;
-  float* u = t3 + kS * kLd;          // [kTile][kLd]
-  float* x = u + kTile * kLd;        // [kTile][kLd]
-  __shared__ float sh[kMuonThreads / 32];
-  const MuonMat mt = tab.m[blockIdx.x];
-  if (status[mt.group] != LORA_OK) return;
-  const float c = (float)scale_norm[2 * mt.group];
-  const int s = mt.s;
-  const int64_t n = mt.n;
-  const int64_t sj = mt.tall ? s : 1, si = mt.tall ? 1 : n;   // element (i, j): i * si + j * sj
-  float* p = P + mt.offset;
-  float* g = G + mt.offset;
-  float* m = M + mt.offset;
-  const float mu = hp.mu;
-  // momentum and the largest |u|
-  float mx = 0.f;
-  for (int64_t e = threadIdx.x; e < n * s; e += kMuonThreads) {
-    const float gh = c * g[e];
-    const float mn = fmaf(mu, m[e], gh);
-    m[e] = mn;
-    mx = fmaxf(mx, fabsf(hp.nesterov ? fmaf(mu, mn, gh) : mn));
-  }
-  mx = block_max(mx, sh);
-  // u scaled by a power of two to about one, so that its squares stay in range
-  const float pre = mx > 0.f && isfinite(mx) ? exp2f((float)-min(max(ilogbf(mx), -120), 120)) : 1.f;
-  for (int e = threadIdx.x; e < s * s; e += kMuonThreads) q[e / s * kLd + e % s] = e / s == e % s;
-  __syncthreads();
-  auto load_tile = [&](int64_t j0) {   // u of long-axis elements j0 .. j0 + kTile, zeros past n
-    for (int e = threadIdx.x; e < kTile * s; e += kMuonThreads) {
-      const int jj = mt.tall ? e / s : e % kTile, i = mt.tall ? e % s : e / kTile;
-      float v = 0.f;
-      if (j0 + jj < n) {
-        const int64_t at = i * si + (j0 + jj) * sj;
-        v = hp.nesterov ? fmaf(mu, m[at], c * g[at]) : m[at];
+  float* part = sm;               // [8][S S] warps' Gram matrices; then [0] the CTA's
+  float* g0 = part + 8 * S * S;   // Gram matrix
+  float* qs = g0 + S * S;         // product of this stage's steps
+  float* qt = qs + S * S;         // product of all steps (columns past the cap)
+  float* t1 = qt + S * S;
+  float* t2 = t1 + S * S;
+  float* sh = t2 + S * S;
+  float* u = sh + 16;             // [cap][SP]
+  const int rank = C > 1 ? (int)cluster_ctarank() : 0;
+  const int tid = threadIdx.x;
+  for (int mi = (int)blockIdx.x / C; mi < tab.n; mi += (int)gridDim.x / C) {
+    const MuonMat mt = tab.m[mi];
+    if (status[mt.group] != LORA_OK) continue;
+    const float c = (float)scale_norm[2 * mt.group], mu = hp.mu;
+    const int64_t n4 = mt.n / 4;   // columns are shared out by fours
+    const int64_t j0 = n4 * rank / C * 4, j1 = n4 * (rank + 1) / C * 4;
+    const int cols = (int)(j1 - j0), held = min(cols, F::kCap);
+    const int64_t sj = mt.tall ? S : 1, si = mt.tall ? 1 : mt.n;   // element (i, j): i si + j sj
+    float* p = P + mt.offset + j0 * sj;
+    float* g = G + mt.offset + j0 * sj;
+    float* m = M + mt.offset + j0 * sj;
+    auto make_u = [&](float gv, float mv) {   // mv: the new momentum
+      return hp.nesterov ? fmaf(mu, mv, c * gv) : mv;
+    };
+    // momentum, u and its largest magnitude
+    float mx = 0.f;
+    const int units = cols * S4;
+    for (int e0 = tid; e0 < units; e0 += 4 * kMuonThreads) {
+      float4 gv[4], mv[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int e = e0 + v * kMuonThreads;
+        if (e < units) {
+          // tall: four rows' entries of one column; wide: four columns' entries of one row
+          const int64_t at = mt.tall ? (int64_t)e * 4 : (int64_t)(e / (cols / 4)) * si + e % (cols / 4) * 4;
+          gv[v] = *reinterpret_cast<const float4*>(g + at);
+          mv[v] = *reinterpret_cast<const float4*>(m + at);
+        }
       }
-      u[jj * kLd + i] = v * pre;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int e = e0 + v * kMuonThreads;
+        if (e >= units) break;
+        const int i = mt.tall ? e % S4 * 4 : e / (cols / 4);
+        const int j = mt.tall ? e / S4 : e % (cols / 4) * 4;
+        const int64_t at = i * si + j * sj;
+        float* a = &gv[v].x;
+        float* b = &mv[v].x;
+        float w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          b[q] = fmaf(mu, b[q], c * a[q]);
+          w[q] = make_u(a[q], b[q]);
+          mx = fmaxf(mx, fabsf(w[q]));
+        }
+        *reinterpret_cast<float4*>(m + at) = mv[v];
+        if (mt.tall) {
+          if (j < held) *reinterpret_cast<float4*>(u + j * SP + i) = make_float4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (j + q < held) u[(j + q) * SP + i] = w[q];
+        }
+      }
     }
+    const float pre = range_scale(mx, sh, C);
+    if (tid < S * S) qt[tid] = tid / S == tid % S ? pre : 0.f;
+    if (pre != 1.f)
+      for (int e = tid; e < held * S; e += kMuonThreads) u[e / S * SP + e % S] *= pre;
     __syncthreads();
-    for (int e = threadIdx.x; e < kTile * s; e += kMuonThreads) {
-      const int jj = e / s, i = e % s;
+    for (int done = 0; done < hp.steps;) {
+      const int left = hp.steps - done;
+      const int now = left % kStageSteps ? left % kStageSteps : kStageSteps;
+      // Gram matrix: a thread adds a 4 x 4 block over its group's columns
+      {
+        float acc[4][4] = {};
+        const int b = tid % F::kLanes, grp = tid / F::kLanes;
+        const int bi = b / S4 * 4, bk = b % S4 * 4;
+        if (b < F::kBlocks) {
+          for (int j = grp; j < held; j += F::kGroups) {
+            const float4 a = *reinterpret_cast<const float4*>(u + j * SP + bi);
+            const float4 d = *reinterpret_cast<const float4*>(u + j * SP + bk);
+            const float av[4] = {a.x, a.y, a.z, a.w}, dv[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) acc[y][z] = fmaf(av[y], dv[z], acc[y][z]);
+          }
+          for (int j = held + grp; j < cols; j += F::kGroups) {
+            float av[4] = {}, dv[4] = {};
+            for (int k = 0; k < S; ++k) {
+              const int64_t at = k * si + j * sj;
+              const float w = make_u(g[at], m[at]);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                av[q] = fmaf(qt[(bi + q) * S + k], w, av[q]);
+                dv[q] = fmaf(qt[(bk + q) * S + k], w, dv[q]);
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) acc[y][z] = fmaf(av[y], dv[z], acc[y][z]);
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+#pragma unroll
+            for (int o = F::kLanes; o < 32; o *= 2) acc[y][z] += __shfl_xor_sync(0xffffffffu, acc[y][z], o);
+            if (b < F::kBlocks && (tid & 31) < F::kLanes)
+              part[(tid >> 5) * S * S + (bi + y) * S + bk + z] = acc[y][z];
+          }
+      }
+      __syncthreads();
       float d = 0.f;
-      for (int k = 0; k < s; ++k) d = fmaf(q[i * kLd + k], u[jj * kLd + k], d);
-      x[jj * kLd + i] = d;
-    }
-    __syncthreads();
-  };
-  for (int done = 0; done < hp.steps;) {
-    const int left = hp.steps - done;
-    const int now = left % kStageSteps ? left % kStageSteps : kStageSteps;
-    float acc[kS * kS / kMuonThreads] = {};
-    for (int64_t j0 = 0; j0 < n; j0 += kTile) {
-      load_tile(j0);
+      if (tid < S * S) {
 #pragma unroll
-      for (int v = 0; v < kS * kS / kMuonThreads; ++v) {
-        const int e = threadIdx.x + v * kMuonThreads;
-        if (e >= s * s) break;
-        const int i = e / s, k = e % s;
-        for (int jj = 0; jj < kTile; ++jj) acc[v] = fmaf(x[jj * kLd + i], x[jj * kLd + k], acc[v]);
+        for (int w = 0; w < kMuonThreads / 32; ++w) d += part[w * S * S + tid];
       }
+      if (C > 1) {
+        __syncthreads();
+        if (tid < S * S) part[tid] = d;
+        cluster_sync();
+        if (tid < S * S) {
+          d = 0.f;
+          for (int r = 0; r < C; ++r) d += dsmem_ld(part + tid, (uint32_t)r);
+        }
+        cluster_sync();   // the peers have read part
+      }
+      if (tid < S * S) g0[tid] = d;
       __syncthreads();
-    }
-    for (int v = 0, e = threadIdx.x; e < s * s; ++v, e += kMuonThreads) {
+      float inv = 1.f;
+      if (done == 0) {   // X = u / ||u||, ||u||^2 = trace G
+        float tr = 0.f;
 #pragma unroll
-      for (int w = 0; w < kS * kS / kMuonThreads; ++w)
-        if (w == v) g0[e / s * kLd + e % s] = acc[w];
-    }
-    __syncthreads();
-    if (done == 0) {   // X = u / ||u||, ||u||^2 = trace G
-      float tr = 0.f;
-      for (int i = 0; i < s; ++i) tr += g0[i * kLd + i];
-      __syncthreads();
-      const float inv = tr > 0.f ? 1.f / sqrtf(tr) : 0.f;
-      for (int e = threadIdx.x; e < s * s; e += kMuonThreads) {
-        g0[e / s * kLd + e % s] *= inv * inv;
-        q[e / s * kLd + e % s] *= inv;
-      }
-      __syncthreads();
-    }
-    for (int k = 0; k < now; ++k) {
-      small_mm(t1, g0, g0, s, 0.f, 0.f, 1.f);                 // G^2
-      for (int e = threadIdx.x; e < s * s; e += kMuonThreads) {   // P
-        const int i = e / s, j = e % s;
-        t1[i * kLd + j] = hp.c * t1[i * kLd + j] + hp.b * g0[i * kLd + j] + (i == j ? hp.a : 0.f);
-      }
-      __syncthreads();
-      small_mm(t2, t1, q, s, 0.f, 0.f, 1.f);                  // Q <- P Q
-      for (int e = threadIdx.x; e < s * s; e += kMuonThreads) q[e / s * kLd + e % s] = t2[e / s * kLd + e % s];
-      __syncthreads();
-      if (k + 1 < now) {                                      // G <- P (G P)
-        small_mm(t2, g0, t1, s, 0.f, 0.f, 1.f);
-        small_mm(t3, t1, t2, s, 0.f, 0.f, 1.f);
-        for (int e = threadIdx.x; e < s * s; e += kMuonThreads) g0[e / s * kLd + e % s] = t3[e / s * kLd + e % s];
+        for (int i = 0; i < S; ++i) tr += g0[i * S + i];
+        inv = tr > 0.f ? 1.f / sqrtf(tr) : 0.f;
+        __syncthreads();
+        if (tid < S * S) g0[tid] *= inv * inv;
         __syncthreads();
       }
+      if (tid < S * S) qs[tid] = tid / S == tid % S ? inv : 0.f;
+      for (int k = 0; k < now; ++k) {
+        simt_mm<S4>(t1, g0, g0);                                        // G^2
+        if (tid < S * S)
+          t1[tid] = hp.c * t1[tid] + hp.b * g0[tid] + (tid / S == tid % S ? hp.a : 0.f);   // P
+        __syncthreads();
+        simt_mm<S4>(qs, t1, qs);                                        // Q <- P Q
+        if (k + 1 < now) {                                              // G <- P (G P)
+          simt_mm<S4>(t2, g0, t1);
+          simt_mm<S4>(g0, t1, t2);
+        }
+      }
+      done += now;
+      if (cols > held) simt_mm<S4>(qt, qs, qt);
+      // X <- Q X on the held columns
+      for (int j = tid; j < held; j += kMuonThreads) {
+        float x[S], y[S];
+#pragma unroll
+        for (int i = 0; i < S; i += 4) *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(u + j * SP + i);
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          y[i] = 0.f;
+#pragma unroll
+          for (int k = 0; k < S; k += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(qs + i * S + k);
+            y[i] = fmaf(w.x, x[k], fmaf(w.y, x[k + 1], fmaf(w.z, x[k + 2], fmaf(w.w, x[k + 3], y[i]))));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < S; i += 4) *reinterpret_cast<float4*>(u + j * SP + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+      }
+      __syncthreads();
     }
-    done += now;
+    const float step = mt.step, dec = mt.lr * mt.decay;
+    const int hunits = held * S4;
+    for (int e = tid; e < hunits; e += kMuonThreads) {
+      const int i = mt.tall ? e % S4 * 4 : e / (held / 4);
+      const int j = mt.tall ? e / S4 : e % (held / 4) * 4;
+      const int64_t at = i * si + j * sj;
+      float4 pv = *reinterpret_cast<const float4*>(p + at);
+      float* a = &pv.x;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float x = mt.tall ? u[j * SP + i + q] : u[(j + q) * SP + i];
+        a[q] = a[q] - step * x - dec * a[q];
+      }
+      *reinterpret_cast<float4*>(p + at) = pv;
+      if (zero_grads) *reinterpret_cast<float4*>(g + at) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // the other columns: (all steps) u
+    for (int e = tid; e < (cols - held) * S4; e += kMuonThreads) {
+      const int j = held + e / S4, i = e % S4 * 4;
+      float x[4] = {};
+      for (int k = 0; k < S; ++k) {
+        const float w = make_u(g[k * si + j * sj], m[k * si + j * sj]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] = fmaf(qt[(i + q) * S + k], w, x[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t at = (i + q) * si + j * sj;
+        p[at] = p[at] - step * x[q] - dec * p[at];
+      }
+    }
+    if (zero_grads && cols > held) {   // read by every thread above
+      __syncthreads();
+      for (int e = tid; e < (cols - held) * S; e += kMuonThreads)
+        g[(e % S) * si + (held + e / S) * sj] = 0.f;
+    }
+    __syncthreads();   // u, part and sh are free for the next matrix
   }
-  const float lr = mt.lr, step = mt.step, wd = mt.decay;
-  for (int64_t j0 = 0; j0 < n; j0 += kTile) {
-    load_tile(j0);
-    for (int e = threadIdx.x; e < kTile * s; e += kMuonThreads) {
-      const int jj = mt.tall ? e / s : e % kTile, i = mt.tall ? e % s : e / kTile;
-      if (j0 + jj >= n) continue;
-      const int64_t at = i * si + (j0 + jj) * sj;
-      p[at] = p[at] - step * x[jj * kLd + i] - lr * wd * p[at];
-      if (zero_grads) g[at] = 0.f;
+}
+
+// ---- s <= 64 on tensor cores --------------------------------------------------------------------
+// A tile is 128 columns of u as two arrays of 128 rows x 64 bf16 (hi, lo; rows past s are zero),
+// 128-byte rows in the 128-byte swizzle. One layout serves both products:
+//   Gram   [hi; lo] [hi; lo]^T: M = N = 128 over the columns, MN-major operands whose second
+//          64-row block is the lo array: the four products of the split are the quadrants of D
+//   Q X    rows are K-major A operands, B = [Q_hi; Q_lo] (N = 128): hi and lo into one
+//          accumulator, the two halves of its columns added in the epilogue
+constexpr int kTcTiles = 5;                    // tiles held per CTA; others go through `spill`
+constexpr int kTcTileBytes = 32 * 1024;
+constexpr int kTcLdG = 68;
+constexpr int kTcSmem = (kTcTiles + 1) * kTcTileBytes + 16 * 1024 + 64 * kTcLdG * 4 + 256 + 1024;
+static_assert(kTcSmem <= 227 * 1024, "shared memory per CTA");
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight values as 16 bytes of hi and of lo at chunk c (8 values) of row `row` of a 64-wide split
+__device__ __forceinline__ void put_split8(uint8_t* hi, uint8_t* lo, int row, int c, const float* v) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    h[q] = pack_bf16(v[2 * q], v[2 * q + 1]);
+    l[q] = pack_bf16(v[2 * q] - __uint_as_float(h[q] << 16), v[2 * q + 1] - __uint_as_float(h[q] & 0xFFFF0000u));
+  }
+  const int at = row * 128 + ((c ^ (row & 7)) << 4);
+  *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+  *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+struct TcArgs {
+  float* P;
+  float* G;
+  float* M;
+  const double* scale_norm;
+  const int32_t* status;
+  uint8_t* spill;        // [CTA][spill_tiles][kTcTileBytes]
+  int32_t spill_tiles;
+  int32_t zero_grads, C;
+  uint32_t* err;
+  unsigned long long wait_limit;
+};
+
+// 4 x 4 block of the product of two commuting symmetric matrices, both read by rows
+__device__ __forceinline__ void mm4(float (&acc)[4][4], const float* A, int lda, const float* B, int ldb, int s) {
+  const int r = (threadIdx.x >> 4) * 4, c = (threadIdx.x & 15) * 4;
+#pragma unroll
+  for (int y = 0; y < 4; ++y)
+#pragma unroll
+    for (int z = 0; z < 4; ++z) acc[y][z] = 0.f;
+  if (r >= s || c >= s) return;
+#pragma unroll 4
+  for (int k = 0; k < s; ++k) {
+    const float4 a = *reinterpret_cast<const float4*>(A + k * lda + r);
+    const float4 b = *reinterpret_cast<const float4*>(B + k * ldb + c);
+    const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+      for (int z = 0; z < 4; ++z) acc[y][z] = fmaf(av[y], bv[z], acc[y][z]);
+  }
+}
+__device__ __forceinline__ void put4(float* C, int ld, const float (&acc)[4][4]) {
+  const int r = (threadIdx.x >> 4) * 4, c = (threadIdx.x & 15) * 4;
+#pragma unroll
+  for (int y = 0; y < 4; ++y) store4(C + (r + y) * ld + c, acc[y]);
+}
+
+__global__ void __launch_bounds__(kMuonThreads, 1) k_muon_tc(const __grid_constant__ MuonTab tab,
+                                                             const MuonK hp, const TcArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* scratch = tiles + kTcTiles * kTcTileBytes;   // a spilled tile, or two small matrices
+  uint8_t* qop = scratch + kTcTileBytes;                // [Q_hi; Q_lo] operand, or Q in fp32
+  float* g0 = reinterpret_cast<float*>(qop + 16 * 1024);   // Gram matrix [64][68]
+  float* sh = g0 + 64 * kTcLdG;                         // [16]
+  uint64_t* bar_apply = reinterpret_cast<uint64_t*>(sh + 16);   // [2]
+  uint64_t* bar_gram = bar_apply + 2;
+  uint64_t* bar_load = bar_gram + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_load + 1);
+  float* t1 = reinterpret_cast<float*>(scratch);        // [64][64]
+  float* t2 = t1 + 64 * 64;
+  float* qf = reinterpret_cast<float*>(qop);            // [64][64]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = a.C;
+  const int rank = C > 1 ? (int)cluster_ctarank() : 0;
+  if (tid == 0) {
+    mbar_init(&bar_apply[0], 1);
+    mbar_init(&bar_apply[1], 1);
+    mbar_init(bar_gram, 1);
+    mbar_init(bar_load, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  grid_dep_sync();
+  if (warp == 0) tmem_alloc(tmem_slot, 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tm_gram = tmem, tm_apply = tmem + 128;   // apply buffers at +128 and +256
+  uint8_t* spill = a.spill + (size_t)blockIdx.x * a.spill_tiles * kTcTileBytes;
+  constexpr uint32_t id_gram = idesc(kFmtBF16, 128, 128, true, true);
+  constexpr uint32_t id_apply = idesc(kFmtBF16, 128, 128);
+  uint32_t ph_apply[2] = {0, 0}, ph_gram = 0, ph_load = 0;   // the same in every thread
+  bool ok = true;                                            // no wait has run out of its bound
+  auto wait = [&](uint64_t* bar, uint32_t ph) {
+    ok = __all_sync(0xffffffffu, mbar_wait_for(bar, ph, 2u, a.err, ok ? a.wait_limit : 0ull)) && ok;
+    fence_after();
+  };
+  // every thread's writes to shared memory become visible to the tensor cores and bulk copies
+  auto publish = [&]() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    fence_before();
+    __syncthreads();
+    fence_after();
+  };
+
+  for (int mi = (int)blockIdx.x / C; mi < tab.n; mi += (int)gridDim.x / C) {
+    const MuonMat mt = tab.m[mi];
+    if (a.status[mt.group] != LORA_OK) continue;
+    const float c = (float)a.scale_norm[2 * mt.group], mu = hp.mu;
+    const int s = mt.s;
+    const int64_t all = (mt.n + 127) / 128;
+    const int64_t first = all * rank / C;
+    const int nt = (int)(all * (rank + 1) / C - first);
+    const int64_t sj = mt.tall ? s : 1, si = mt.tall ? 1 : mt.n;
+    float* p = a.P + mt.offset;
+    float* g = a.G + mt.offset;
+    float* m = a.M + mt.offset;
+    // Tile t of this CTA in shared memory: held, or brought back from the spill.
+    auto fetch = [&](int t) -> uint8_t* {
+      if (t < kTcTiles) return tiles + t * kTcTileBytes;
+      if (tid == 0) {
+        mbar_expect_tx(bar_load, kTcTileBytes);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                smem_u32(scratch)),
+            "l"(spill + (size_t)(t - kTcTiles) * kTcTileBytes), "r"(kTcTileBytes), "r"(smem_u32(bar_load))
+            : "memory");
+      }
+      wait(bar_load, ph_load);
+      ph_load ^= 1u;
+      return scratch;
+    };
+    // writes a spilled tile out (after publish) and waits until the copy is complete
+    auto flush = [&](int t) {
+      if (t < kTcTiles) return;
+      if (tid == 0) {
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                         spill + (size_t)(t - kTcTiles) * kTcTileBytes),
+                     "r"(smem_u32(scratch)), "r"(kTcTileBytes)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        asm volatile("fence.proxy.async;" ::: "memory");
+      }
+      __syncthreads();
+    };
+    auto gram_mma = [&](const uint8_t* tile, bool begin) {   // thread 0
+      const uint64_t d = smem_desc_sw128_mn(smem_u32(tile), 16 * 1024);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) umma_f16(tm_gram, d + 128 * k, d + 128 * k, id_gram, (begin && k == 0) ? 0u : 1u);
+    };
+    auto apply_mma = [&](const uint8_t* tile, int buf) {     // thread 0
+      const uint64_t dq = smem_desc_sw128(smem_u32(qop));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint64_t d = smem_desc_sw128(smem_u32(tile) + h * 16 * 1024);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          umma_f16(tm_apply + 128u * (uint32_t)buf, d + 2 * k, dq + 2 * k, id_apply, (h || k) ? 1u : 0u);
+      }
+      umma_commit(&bar_apply[buf]);
+    };
+
+    // ---- momentum, u and its largest magnitude
+    float mx = 0.f;
+    for (int t = 0; t < nt; ++t) {
+      uint8_t* hi = t < kTcTiles ? tiles + t * kTcTileBytes : scratch;
+      uint8_t* lo = hi + 16 * 1024;
+      const int64_t j0 = (first + t) * 128;
+      // unit: 8 rows of one column (tall) or of 32 columns, one per lane (wide)
+#pragma unroll 2
+      for (int un = 0; un < 4; ++un) {
+        int row, ch;
+        if (mt.tall) {
+          const int e = un * kMuonThreads + tid;
+          row = e >> 3;
+          ch = e & 7;
+        } else {
+          const int e = un * 8 + warp;   // 32 units of (chunk, 32 columns)
+          row = (e & 3) * 32 + lane;
+          ch = e >> 2;
+        }
+        float gv[8], mv[8], w[8];
+        const bool in = j0 + row < mt.n;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) gv[q] = mv[q] = w[q] = 0.f;
+        if (mt.tall) {
+          const int64_t at = (j0 + row) * sj + ch * 8;
+#pragma unroll
+          for (int q = 0; q < 8; q += 4)
+            if (in && ch * 8 + q < s) {
+              *reinterpret_cast<float4*>(gv + q) = __ldcs(reinterpret_cast<const float4*>(g + at + q));
+              *reinterpret_cast<float4*>(mv + q) = __ldcs(reinterpret_cast<const float4*>(m + at + q));
+            }
+        } else {
+          const int64_t at = (int64_t)(ch * 8) * si + j0 + row;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (in && ch * 8 + q < s) {
+              gv[q] = __ldcs(g + at + q * si);
+              mv[q] = __ldcs(m + at + q * si);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          mv[q] = fmaf(mu, mv[q], c * gv[q]);
+          w[q] = hp.nesterov ? fmaf(mu, mv[q], c * gv[q]) : mv[q];
+          mx = fmaxf(mx, fabsf(w[q]));
+        }
+        if (mt.tall) {
+          const int64_t at = (j0 + row) * sj + ch * 8;
+#pragma unroll
+          for (int q = 0; q < 8; q += 4)
+            if (in && ch * 8 + q < s) {
+              store4(m + at + q, mv + q);
+              if (a.zero_grads) *reinterpret_cast<float4*>(g + at + q) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        } else {
+          const int64_t at = (int64_t)(ch * 8) * si + j0 + row;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (in && ch * 8 + q < s) {
+              m[at + q * si] = mv[q];
+              if (a.zero_grads) g[at + q * si] = 0.f;
+            }
+        }
+        put_split8(hi, lo, row, ch, w);
+      }
+      if (t >= kTcTiles) {
+        publish();
+        flush(t);
+      }
+    }
+    const float pre = range_scale(mx, sh, C);
+    if (pre != 1.f) {
+      for (int t = 0; t < nt; ++t) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(fetch(t));
+        __syncthreads();
+        for (int e = tid; e < kTcTileBytes / 4; e += kMuonThreads)
+          w[e] = pack_bf16(__uint_as_float(w[e] << 16) * pre, __uint_as_float(w[e] & 0xFFFF0000u) * pre);
+        publish();
+        flush(t);
+      }
+    }
+    publish();
+
+    // ---- Gram matrix of u
+    for (int t = 0; t < nt; ++t) {
+      const uint8_t* tile = fetch(t);
+      if (tid == 0) gram_mma(tile, t == 0);
+      if (t >= kTcTiles || t + 1 == nt) {
+        if (tid == 0) umma_commit(bar_gram);
+        wait(bar_gram, ph_gram);
+        ph_gram ^= 1u;
+      }
+      if (t >= kTcTiles) __syncthreads();
+    }
+
+    for (int done = 0; done < hp.steps;) {
+      const int left = hp.steps - done;
+      const int now = left % kStageSteps ? left % kStageSteps : kStageSteps;
+      // ---- G = the sum of D's quadrants, then over the cluster
+      if (warp < 4) {
+        float v[64];
+        const uint32_t d = tm_gram + ((uint32_t)(warp * 32) << 16);
+        if (nt > 0) {
+          float x[32];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld32(d + (uint32_t)(h * 32), v + h * 32);
+            tmem_ld32(d + 64u + (uint32_t)(h * 32), x);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[h * 32 + q] += x[q];
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 64; ++q) v[q] = 0.f;
+        }
+        fence_before();
+        float* row = g0 + ((warp & 1) * 32 + lane) * kTcLdG;
+        if (warp < 2) {
+#pragma unroll
+          for (int q = 0; q < 64; q += 4) store4(row + q, v + q);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (warp >= 2) {
+#pragma unroll
+          for (int q = 0; q < 64; q += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(row + q);
+            *reinterpret_cast<float4*>(row + q) = make_float4(o.x + v[q], o.y + v[q + 1], o.z + v[q + 2], o.w + v[q + 3]);
+          }
+        }
+      }
+      __syncthreads();
+      if (C > 1) {
+        // CTA r adds an r-th of the matrix over the ranks, then every CTA gathers the parts
+        const int per = 1024 / C;
+        cluster_sync();
+        for (int e = tid; e < per; e += kMuonThreads) {
+          const int at = rank * per + e, i = at >> 4, k = (at & 15) * 4;
+          float4 v = dsmem_ld4(g0 + i * kTcLdG + k, 0);
+          for (int r = 1; r < C; ++r) {
+            const float4 o = dsmem_ld4(g0 + i * kTcLdG + k, (uint32_t)r);
+            v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+          }
+          *reinterpret_cast<float4*>(t1 + at * 4) = v;
+        }
+        cluster_sync();
+        for (int at = tid; at < 1024; at += kMuonThreads) {
+          const float4 v = dsmem_ld4(t1 + at * 4, (uint32_t)(at / per));
+          *reinterpret_cast<float4*>(g0 + (at >> 4) * kTcLdG + (at & 15) * 4) = v;
+        }
+        cluster_sync();   // the peers have read t1
+      }
+      float inv = 1.f;
+      if (done == 0) {   // X = u / ||u||, ||u||^2 = trace G
+        float tr = 0.f;
+        for (int i = 0; i < s; ++i) tr += g0[i * kTcLdG + i];
+        inv = tr > 0.f ? 1.f / sqrtf(tr) : 0.f;
+        __syncthreads();
+        for (int e = tid; e < 64 * 64; e += kMuonThreads) g0[(e >> 6) * kTcLdG + (e & 63)] *= inv * inv;
+        __syncthreads();
+      }
+      // ---- the stage's steps on G; Q, their product, in fp32 over the operand's place
+      const int r = (tid >> 4) * 4, cc = (tid & 15) * 4;
+      float acc[4][4];
+      for (int k = 0; k < now; ++k) {
+        mm4(acc, g0, kTcLdG, g0, kTcLdG, s);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            acc[y][z] = hp.c * acc[y][z] + hp.b * g0[(r + y) * kTcLdG + cc + z] +
+                        (r + y == cc + z && r + y < s ? hp.a : 0.f);
+        put4(t1, 64, acc);                                   // P
+        if (k == 0 && now > 1) put4(qf, 64, acc);
+        __syncthreads();
+        if (k + 1 < now) {
+          mm4(acc, t1, 64, t1, 64, s);                       // P^2
+          put4(t2, 64, acc);
+          if (k > 0) {
+            mm4(acc, t1, 64, qf, 64, s);                     // Q <- P Q
+            __syncthreads();
+            put4(qf, 64, acc);
+          }
+          __syncthreads();
+          mm4(acc, g0, kTcLdG, t2, 64, s);                   // G <- P^2 G
+          __syncthreads();
+          put4(g0, kTcLdG, acc);
+          __syncthreads();
+        } else if (k > 0) {
+          mm4(acc, t1, 64, qf, 64, s);
+          __syncthreads();
+        }
+      }
+      done += now;
+      // acc holds this thread's block of Q: [Q_hi; Q_lo] as the B operand
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        uint32_t h[2], l[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float v0 = acc[y][2 * q] * inv, v1 = acc[y][2 * q + 1] * inv;
+          h[q] = pack_bf16(v0, v1);
+          l[q] = pack_bf16(v0 - __uint_as_float(h[q] << 16), v1 - __uint_as_float(h[q] & 0xFFFF0000u));
+        }
+        const int row = r + y;
+        const int at = row * 128 + (((cc >> 3) ^ (row & 7)) << 4) + (cc & 4) * 2;
+        *reinterpret_cast<uint2*>(qop + at) = make_uint2(h[0], h[1]);
+        *reinterpret_cast<uint2*>(qop + 64 * 128 + at) = make_uint2(l[0], l[1]);
+      }
+      publish();
+      // ---- X <- Q X: into the tiles, with the next Gram matrix, or into the parameters
+      const bool last = done >= hp.steps;
+      const int quad = warp & 3, ih = warp >> 2;
+      const int jrow = quad * 32 + lane;
+      if (tid == 0 && nt > 0) apply_mma(tiles, 0);
+      for (int t = 0; t < nt; ++t) {
+        const int buf = t & 1;
+        uint8_t* tile = tiles + t * kTcTileBytes;
+        if (t >= kTcTiles) {
+          tile = fetch(t);
+          if (tid == 0) apply_mma(tile, buf);
+        }
+        if (t + 1 < nt && t + 1 < kTcTiles && tid == 0) apply_mma(tiles + (t + 1) * kTcTileBytes, buf ^ 1);
+        wait(&bar_apply[buf], ph_apply[buf]);
+        ph_apply[buf] ^= 1u;
+        float x[32];
+        {
+          float y[32];
+          const uint32_t d = tm_apply + 128u * (uint32_t)buf + ((uint32_t)(quad * 32) << 16) + (uint32_t)(ih * 32);
+          tmem_ld32(d, x);
+          tmem_ld32(d + 64u, y);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) x[q] += y[q];
+        }
+        if (!last) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) put_split8(tile, tile + 16 * 1024, jrow, ih * 4 + q, x + q * 8);
+          publish();
+          if (tid == 0) gram_mma(tile, t == 0);
+          if (t >= kTcTiles || t + 1 == nt) {
+            if (tid == 0) umma_commit(bar_gram);
+            wait(bar_gram, ph_gram);
+            ph_gram ^= 1u;
+            flush(t);
+          }
+        } else {
+          // X [128][64] fp32 over the tile, 16-byte chunks spread by the row
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            store4(reinterpret_cast<float*>(tile + jrow * 256 + (((ih * 8 + q) ^ (jrow & 15)) << 4)), x + q * 4);
+          fence_before();
+          __syncthreads();
+          fence_after();
+          const int64_t j0 = (first + t) * 128;
+          const float step = mt.step, dec = mt.lr * mt.decay;
+          if (mt.tall) {
+            for (int e = tid; e < 128 * (s / 4); e += kMuonThreads) {
+              const int j = e / (s / 4), q = e - j * (s / 4);
+              if (j0 + j >= mt.n || !ok) continue;
+              float* at = p + (j0 + j) * sj + q * 4;
+              float4 pv = *reinterpret_cast<const float4*>(at);
+              const float4 xv = *reinterpret_cast<const float4*>(tile + j * 256 + ((q ^ (j & 15)) << 4));
+              pv.x = pv.x - step * xv.x - dec * pv.x;
+              pv.y = pv.y - step * xv.y - dec * pv.y;
+              pv.z = pv.z - step * xv.z - dec * pv.z;
+              pv.w = pv.w - step * xv.w - dec * pv.w;
+              *reinterpret_cast<float4*>(at) = pv;
+            }
+          } else {
+            const int j = tid & 127;
+            if (j0 + j < mt.n && ok) {
+#pragma unroll 8
+              for (int i = tid >> 7; i < s; i += 2) {
+                float* at = p + i * si + j0 + j;
+                const float pv = *at;
+                const float xv = *reinterpret_cast<const float*>(tile + j * 256 + (((i >> 2) ^ (j & 15)) << 4) + (i & 3) * 4);
+                *at = pv - step * xv - dec * pv;
+              }
+            }
+          }
+          publish();   // a spilled tile's room is the next one's
+        }
+      }
     }
     __syncthreads();
   }
+  // every MMA's completion has been waited for; the peers are done with this CTA's memory
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// One launch of `kernel` over the table's matrices, a cluster of C CTAs each, persistent.
+template <typename K, typename... Args>
+cudaError_t launch_clusters(K kernel, int smem, int n, int C, int most, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kMuonThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)C;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = add_pdl_attr(at, 1);
+  const int clusters = std::max(1, std::min(n, most / C));
+  cfg.gridDim = dim3((unsigned)(clusters * C));
+  prof_begin(0, st);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename K>
+cudaError_t set_attrs(K kernel, int smem) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e;
+}
+
+template <int S4>
+cudaError_t run_simt(float* p, float* g, float* m, const MuonTab& tab, const MuonK& hp,
+                     const double* scale_norm, const int32_t* status, int zero_grads, int C,
+                     int held, cudaStream_t st) {
+  using F = SimtCfg<S4>;
+  static cudaError_t set = set_attrs(k_muon_simt<S4>, (F::kSmallFloats + F::kCap * F::SP) * 4);
+  if (set != cudaSuccess) return set;
+  const int smem = (F::kSmallFloats + std::min(held, F::kCap) * F::SP) * 4;
+  return launch_clusters(k_muon_simt<S4>, smem, tab.n, C, 1 << 20, st, p, g, m, tab, hp, scale_norm,
+                         status, zero_grads, C);
 }
 
 }  // namespace
 
+int muon_cluster(const MuonMat& m, int n_mats) {
+  const int64_t fit = m.s <= 16 ? 512 : 128 * kTcTiles;   // columns a CTA takes before the cluster grows
+  int C = 1;
+  while (C < 16 && (m.n > fit * C || (n_mats * C * 2 <= 152 && m.n > 128 * C))) C *= 2;
+  return C;
+}
+
+size_t muon_spill_bytes(const MuonMat& m, int C, int n) {
+  if (m.s <= 16) return 0;
+  const int64_t tiles = ((m.n + 127) / 128 + C - 1) / C;
+  if (tiles <= kTcTiles) return 0;
+  const int64_t ctas = (int64_t)std::max(1, std::min(n, kMuonMaxCtas / C)) * C;
+  return (size_t)ctas * (tiles - kTcTiles) * kTcTileBytes;
+}
+
 cudaError_t launch_muon(float* p, float* g, float* m, const MuonTab& tab, const MuonK& hp,
-                        const double* scale_norm, const int32_t* status, int zero_grads,
-                        cudaStream_t st) {
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(k_muon, cudaFuncAttributeMaxDynamicSharedMemorySize, kMuonSmem);
-    if (e != cudaSuccess) return e;
-    attr = true;
+                        const double* scale_norm, const int32_t* status, int zero_grads, int C,
+                        void* spill, cudaStream_t st) {
+  int64_t n = 0;
+  for (int i = 0; i < tab.n; ++i) n = std::max(n, tab.m[i].n);
+  if (tab.m[0].s <= 16) {
+    const int held = (int)std::min<int64_t>((n / 4 + C - 1) / C * 4, 1 << 20);
+    switch (tab.m[0].s / 4) {
+      case 1: return run_simt<1>(p, g, m, tab, hp, scale_norm, status, zero_grads, C, held, st);
+      case 2: return run_simt<2>(p, g, m, tab, hp, scale_norm, status, zero_grads, C, held, st);
+      case 3: return run_simt<3>(p, g, m, tab, hp, scale_norm, status, zero_grads, C, held, st);
+      default: return run_simt<4>(p, g, m, tab, hp, scale_norm, status, zero_grads, C, held, st);
+    }
   }
-  prof_begin(0, st);
-  return launch_kernel(k_muon, (unsigned)tab.n, kMuonThreads, kMuonSmem, st, p, g, m, tab, hp,
-                       scale_norm, status, zero_grads);
+  static cudaError_t set = set_attrs(k_muon_tc, kTcSmem);
+  if (set != cudaSuccess) return set;
+  TcArgs a{};
+  a.P = p; a.G = g; a.M = m;
+  a.scale_norm = scale_norm; a.status = status;
+  a.spill = static_cast<uint8_t*>(spill);
+  const int64_t tiles = ((n + 127) / 128 + C - 1) / C;
+  a.spill_tiles = (int32_t)std::max<int64_t>(0, tiles - kTcTiles);
+  a.zero_grads = zero_grads; a.C = C;
+  a.err = error_word();
+  if (!a.err) return cudaErrorInvalidDevice;
+  a.wait_limit = tc_wait_limit();
+  return launch_clusters(k_muon_tc, kTcSmem, tab.n, C, kMuonMaxCtas, st, tab, hp, a);
 }
 
 }  // namespace lora
