@@ -17,7 +17,7 @@
 // s <= 16: CUDA cores, u in fp32 (k_muon_simt). Larger s: the two long products on tensor cores
 // (k_muon_tc), u as a two-term bf16 split, all four products of the terms kept.
 #include <algorithm>
-#include <mutex>
+#include <atomic>
 
 #include "tc_ptx.cuh"
 
@@ -49,19 +49,20 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // The power of two that brings the cluster's largest |u| to about one when its squares could
-// leave the fp32 range; one otherwise. `sh` holds 8 floats and the CTA's maximum.
+// leave the fp32 range; one otherwise. `sh` holds a float per warp (16 at most) and the CTA's maximum.
+template <int Threads>
 __device__ __forceinline__ float range_scale(float mx, float* sh, int C) {
   mx = warp_max(mx);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = mx;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kMuonThreads / 32; ++w) mx = fmaxf(mx, sh[w]);
-    sh[8] = mx;
+    for (int w = 1; w < Threads / 32; ++w) mx = fmaxf(mx, sh[w]);
+    sh[16] = mx;
   }
   if (C > 1) cluster_sync();
   else __syncthreads();
-  mx = sh[8];
-  for (int r = 0; r < C; ++r) mx = C > 1 ? fmaxf(mx, dsmem_ld(sh + 8, (uint32_t)r)) : mx;
+  mx = sh[16];
+  for (int r = 0; r < C; ++r) mx = C > 1 ? fmaxf(mx, dsmem_ld(sh + 16, (uint32_t)r)) : mx;
   if (C > 1) cluster_sync();   // sh may be written again
   if (!(mx > 0.f) || !isfinite(mx) || (mx > 0x1p-30f && mx < 0x1p30f)) return 1.f;
   return exp2f((float)-min(max(ilogbf(mx), -126), 126));
@@ -77,7 +78,7 @@ struct SimtCfg {
   static constexpr int kBlocks = S4 * S4;                      // 4 x 4 blocks of the Gram matrix
   static constexpr int kLanes = kBlocks == 9 ? 16 : kBlocks;   // threads of one column group
   static constexpr int kGroups = kMuonThreads / kLanes;
-  static constexpr int kSmallFloats = 8 * S * S + 5 * S * S + 16;
+  static constexpr int kSmallFloats = 8 * S * S + 5 * S * S + 20;
   static constexpr int kCap = (200 * 1024 - kSmallFloats * 4) / (SP * 4) / 4 * 4;
 };
 
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kMuonThreads) k_muon_simt(float* __restrict__ 
   float* t1 = qt + S * S;
   float* t2 = t1 + S * S;
   float* sh = t2 + S * S;
-  float* u = sh + 16;             // [cap][SP]
+  float* u = sh + 20;             // [cap][SP]
   const int rank = C > 1 ? (int)cluster_ctarank() : 0;
   const int tid = threadIdx.x;
   for (int mi = (int)blockIdx.x / C; mi < tab.n; mi += (int)gridDim.x / C) {
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kMuonThreads) k_muon_simt(float* __restrict__ 
         }
       }
     }
-    const float pre = range_scale(mx, sh, C);
+    const float pre = range_scale<kMuonThreads>(mx, sh, C);
     if (tid < S * S) qt[tid] = tid / S == tid % S ? pre : 0.f;
     if (pre != 1.f)
       for (int e = tid; e < held * S; e += kMuonThreads) u[e / S * SP + e % S] *= pre;
@@ -330,10 +331,10 @@ __global__ void __launch_bounds__(kMuonThreads) k_muon_simt(float* __restrict__ 
 //          64-row block is the lo array: the four products of the split are the quadrants of D
 //   Q X    rows are K-major A operands, B = [Q_hi; Q_lo] (N = 128): hi and lo into one
 //          accumulator, the two halves of its columns added in the epilogue
-constexpr int kTcTiles = 5;                    // tiles held per CTA; others go through `spill`
+constexpr int kTcThreads = 512;
+constexpr int kTcTiles = 4;                    // tiles held per CTA; others go through `spill`
 constexpr int kTcTileBytes = 32 * 1024;
-constexpr int kTcLdG = 68;
-constexpr int kTcSmem = (kTcTiles + 1) * kTcTileBytes + 16 * 1024 + 64 * kTcLdG * 4 + 256 + 1024;
+constexpr int kTcSmem = (kTcTiles + 2) * kTcTileBytes + 2 * 16 * 1024 + 256 + 1024;
 static_assert(kTcSmem <= 227 * 1024, "shared memory per CTA");
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -367,46 +368,88 @@ struct TcArgs {
   unsigned long long wait_limit;
 };
 
-// 4 x 4 block of the product of two commuting symmetric matrices, both read by rows
-__device__ __forceinline__ void mm4(float (&acc)[4][4], const float* A, int lda, const float* B, int ldb, int s) {
-  const int r = (threadIdx.x >> 4) * 4, c = (threadIdx.x & 15) * 4;
-#pragma unroll
-  for (int y = 0; y < 4; ++y)
-#pragma unroll
-    for (int z = 0; z < 4; ++z) acc[y][z] = 0.f;
-  if (r >= s || c >= s) return;
-#pragma unroll 4
-  for (int k = 0; k < s; ++k) {
-    const float4 a = *reinterpret_cast<const float4*>(A + k * lda + r);
-    const float4 b = *reinterpret_cast<const float4*>(B + k * ldb + c);
-    const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int y = 0; y < 4; ++y)
-#pragma unroll
-      for (int z = 0; z < 4; ++z) acc[y][z] = fmaf(av[y], bv[z], acc[y][z]);
-  }
-}
-__device__ __forceinline__ void put4(float* C, int ld, const float (&acc)[4][4]) {
-  const int r = (threadIdx.x >> 4) * 4, c = (threadIdx.x & 15) * 4;
-#pragma unroll
-  for (int y = 0; y < 4; ++y) store4(C + (r + y) * ld + c, acc[y]);
+// The small matrices are [64][64] fp32 with the 16-byte chunks of a row spread by the row (no bank
+// conflicts for the fragment reads below): element (i, j) at mat_at(i, j).
+__device__ __forceinline__ int mat_at(int i, int j) { return i * 64 + (j ^ ((i & 7) << 2)); }
+
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const float (&a)[4], float b0, float b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
+        "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
 
-__global__ void __launch_bounds__(kMuonThreads, 1) k_muon_tc(const __grid_constant__ MuonTab tab,
+// D = gamma A B + beta E + alpha I (alpha on the first s of the diagonal) for commuting symmetric
+// matrices, D one of them or another, 16 warps: warp w the rows 16 (w % 4) .. and columns
+// 16 (w / 4) .., three tf32 products of a two-term split (about 2^-21). Thread-level tensor-core
+// instructions fit here: the operands are fp32 in shared memory already, and the product is bound
+// by latency (tcgen05 would need split operands written out and a trip through tensor memory each
+// time). Not inlined: one copy of its code serves the fourteen products of an update.
+__device__ __noinline__ void small_product(float* D, const float* A, const float* B, const float* E, int s,
+                                           float alpha, float beta, float gamma) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = (warp & 3) * 16 + (lane >> 2), n = (warp >> 2) * 16 + (lane >> 2), kq = lane & 3;
+  float acc[2][4] = {};
+  // every row a lane reads has the same spread, (lane >> 2) << 2, so eight offsets cover a row
+  const int spread = (lane >> 2) << 2;
+  const float* pa = A + r * 64;
+  const float* pb = B + n * 64;
+#pragma unroll
+  for (int k = 0; k < 64; k += 8) {
+    if (k >= s) break;
+    const int o0 = (k & 32) + (((k & 24) + kq) ^ spread), o1 = o0 ^ 4;
+    const float xa[4] = {pa[o0], pa[o0 + 8 * 64], pa[o1], pa[o1 + 8 * 64]};
+    const float xb[4] = {pb[o0], pb[o1], pb[o0 + 8 * 64], pb[o1 + 8 * 64]};
+    float ah[4], al[4], bh[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      ah[q] = tf32_hi(xa[q]);
+      al[q] = xa[q] - ah[q];
+      bh[q] = tf32_hi(xb[q]);
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      mma_tf32(acc[v], al, bh[2 * v], bh[2 * v + 1]);
+      mma_tf32(acc[v], ah, xb[2 * v] - bh[2 * v], xb[2 * v + 1] - bh[2 * v + 1]);
+      mma_tf32(acc[v], ah, bh[2 * v], bh[2 * v + 1]);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < 2; ++v)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = r + (q >> 1) * 8, j = (warp >> 2) * 16 + v * 8 + kq * 2 + (q & 1);
+      acc[v][q] = gamma * acc[v][q] + beta * E[mat_at(i, j)] + (i == j && i < s ? alpha : 0.f);
+    }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < 2; ++v)
+#pragma unroll
+    for (int q = 0; q < 4; q += 2)
+      *reinterpret_cast<float2*>(D + mat_at(r + (q >> 1) * 8, (warp >> 2) * 16 + v * 8 + kq * 2)) =
+          make_float2(acc[v][q], acc[v][q + 1]);
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant__ MuonTab tab,
                                                              const MuonK hp, const TcArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* scratch = tiles + kTcTiles * kTcTileBytes;   // a spilled tile, or two small matrices
-  uint8_t* qop = scratch + kTcTileBytes;                // [Q_hi; Q_lo] operand, or Q in fp32
-  float* g0 = reinterpret_cast<float*>(qop + 16 * 1024);   // Gram matrix [64][68]
-  float* sh = g0 + 64 * kTcLdG;                         // [16]
-  uint64_t* bar_apply = reinterpret_cast<uint64_t*>(sh + 16);   // [2]
+  uint8_t* scratch = tiles + kTcTiles * kTcTileBytes;   // two spilled tiles; the first also two
+                                                        //   small matrices
+  uint8_t* qop = scratch + 2 * kTcTileBytes;            // [Q_hi; Q_lo] operand, or Q in fp32
+  float* g0 = reinterpret_cast<float*>(qop + 16 * 1024);   // Gram matrix
+  float* sh = g0 + 64 * 64;                         // [20]
+  uint64_t* bar_apply = reinterpret_cast<uint64_t*>(sh + 20);   // [2]
   uint64_t* bar_gram = bar_apply + 2;
-  uint64_t* bar_load = bar_gram + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_load + 1);
-  float* t1 = reinterpret_cast<float*>(scratch);        // [64][64]
+  uint64_t* bar_load = bar_gram + 1;   // [2]: a spilled tile is back
+  uint64_t* bar_used = bar_load + 2;   // [2]: a spilled tile's Gram products are done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_used + 2);
+  float* t1 = reinterpret_cast<float*>(scratch);
   float* t2 = t1 + 64 * 64;
-  float* qf = reinterpret_cast<float*>(qop);            // [64][64]
+  float* qf = reinterpret_cast<float*>(qop);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = a.C;
   const int rank = C > 1 ? (int)cluster_ctarank() : 0;
@@ -414,7 +457,10 @@ __global__ void __launch_bounds__(kMuonThreads, 1) k_muon_tc(const __grid_consta
     mbar_init(&bar_apply[0], 1);
     mbar_init(&bar_apply[1], 1);
     mbar_init(bar_gram, 1);
-    mbar_init(bar_load, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bar_load[b], 1);
+      mbar_init(&bar_used[b], 1);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -428,7 +474,8 @@ __global__ void __launch_bounds__(kMuonThreads, 1) k_muon_tc(const __grid_consta
   uint8_t* spill = a.spill + (size_t)blockIdx.x * a.spill_tiles * kTcTileBytes;
   constexpr uint32_t id_gram = idesc(kFmtBF16, 128, 128, true, true);
   constexpr uint32_t id_apply = idesc(kFmtBF16, 128, 128);
-  uint32_t ph_apply[2] = {0, 0}, ph_gram = 0, ph_load = 0;   // the same in every thread
+  uint32_t ph_apply[2] = {0, 0}, ph_gram = 0;   // the same in every thread
+  uint32_t ph_load[2] = {0, 0}, ph_used[2] = {0, 0};   // of thread 0, which alone waits on them
   bool ok = true;                                            // no wait has run out of its bound
   auto wait = [&](uint64_t* bar, uint32_t ph) {
     ok = __all_sync(0xffffffffu, mbar_wait_for(bar, ph, 2u, a.err, ok ? a.wait_limit : 0ull)) && ok;
@@ -454,34 +501,47 @@ __global__ void __launch_bounds__(kMuonThreads, 1) k_muon_tc(const __grid_consta
     float* p = a.P + mt.offset;
     float* g = a.G + mt.offset;
     float* m = a.M + mt.offset;
-    // Tile t of this CTA in shared memory: held, or brought back from the spill.
-    auto fetch = [&](int t) -> uint8_t* {
-      if (t < kTcTiles) return tiles + t * kTcTileBytes;
-      if (tid == 0) {
-        mbar_expect_tx(bar_load, kTcTileBytes);
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                smem_u32(scratch)),
-            "l"(spill + (size_t)(t - kTcTiles) * kTcTileBytes), "r"(kTcTileBytes), "r"(smem_u32(bar_load))
-            : "memory");
-      }
-      wait(bar_load, ph_load);
-      ph_load ^= 1u;
-      return scratch;
+    // Tile t of this CTA: held, or, while it is in use, in one of the two scratch tiles. Spilled tiles
+    // move by bulk copies of thread 0.
+    auto place = [&](int t) {
+      return t < kTcTiles ? tiles + t * kTcTileBytes : scratch + ((t - kTcTiles) & 1) * kTcTileBytes;
     };
-    // writes a spilled tile out (after publish) and waits until the copy is complete
-    auto flush = [&](int t) {
-      if (t < kTcTiles) return;
-      if (tid == 0) {
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                         spill + (size_t)(t - kTcTiles) * kTcTileBytes),
-                     "r"(smem_u32(scratch)), "r"(kTcTileBytes)
-                     : "memory");
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        asm volatile("fence.proxy.async;" ::: "memory");
-      }
-      __syncthreads();
+    auto wait0 = [&](uint64_t* bar, uint32_t& ph) {   // thread 0
+      ok = mbar_wait_for(bar, ph, 2u, a.err, ok ? a.wait_limit : 0ull) && ok;
+      ph ^= 1u;
+      fence_after();
+    };
+    auto begin_fetch = [&](int t) {
+      uint64_t* bar = &bar_load[(t - kTcTiles) & 1];
+      mbar_expect_tx(bar, kTcTileBytes);
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+              smem_u32(place(t))),
+          "l"(spill + (size_t)(t - kTcTiles) * kTcTileBytes), "r"(kTcTileBytes), "r"(smem_u32(bar))
+          : "memory");
+    };
+    auto end_fetch = [&](int t) { wait0(&bar_load[(t - kTcTiles) & 1], ph_load[(t - kTcTiles) & 1]); };
+    auto begin_flush = [&](int t) {   // after publish
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                       spill + (size_t)(t - kTcTiles) * kTcTileBytes),
+                   "r"(smem_u32(place(t))), "r"(kTcTileBytes)
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    };
+    auto end_flushes = [&]() {   // the spilled tiles are in global memory
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      asm volatile("fence.proxy.async;" ::: "memory");
+    };
+    // the scratch tile of t is free: t - 2's copy out has read it and its Gram products are done
+    auto scratch_free = [&](int t) {
+      if (t - 2 < kTcTiles) return;
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      wait0(&bar_used[(t - kTcTiles) & 1], ph_used[(t - kTcTiles) & 1]);
+    };
+    // the last one or two uses of the scratch tiles, at the end of a pass
+    auto drain_used = [&]() {
+      for (int t = max(kTcTiles, nt - 2); t < nt; ++t)
+        wait0(&bar_used[(t - kTcTiles) & 1], ph_used[(t - kTcTiles) & 1]);
     };
     auto gram_mma = [&](const uint8_t* tile, bool begin) {   // thread 0
       const uint64_t d = smem_desc_sw128_mn(smem_u32(tile), 16 * 1024);
@@ -500,58 +560,77 @@ __global__ void __launch_bounds__(kMuonThreads, 1) k_muon_tc(const __grid_consta
       umma_commit(&bar_apply[buf]);
     };
 
-    // ---- momentum, u and its largest magnitude
-    float mx = 0.f;
-    for (int t = 0; t < nt; ++t) {
-      uint8_t* hi = t < kTcTiles ? tiles + t * kTcTileBytes : scratch;
-      uint8_t* lo = hi + 16 * 1024;
+    // ---- momentum and u; unit: 8 rows of one column (tall) or of 32 columns, one per lane (wide);
+    // a thread's two units are loaded together
+    float gv[2][8], mv[2][8];
+    auto unit = [&](int un, int& row, int& ch) {
+      if (mt.tall) {
+        const int e = un * kTcThreads + tid;
+        row = e >> 3;
+        ch = e & 7;
+      } else {
+        const int e = un * 16 + warp;   // 32 units of (chunk, 32 columns)
+        row = (e & 3) * 32 + lane;
+        ch = e >> 2;
+      }
+    };
+    auto load = [&](int t) {
       const int64_t j0 = (first + t) * 128;
-      // unit: 8 rows of one column (tall) or of 32 columns, one per lane (wide)
-#pragma unroll 2
-      for (int un = 0; un < 4; ++un) {
-        int row, ch;
-        if (mt.tall) {
-          const int e = un * kMuonThreads + tid;
-          row = e >> 3;
-          ch = e & 7;
-        } else {
-          const int e = un * 8 + warp;   // 32 units of (chunk, 32 columns)
-          row = (e & 3) * 32 + lane;
-          ch = e >> 2;
-        }
-        float gv[8], mv[8], w[8];
-        const bool in = j0 + row < mt.n;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) gv[q] = mv[q] = w[q] = 0.f;
+      for (int un = 0; un < 2; ++un) {
+        int row, ch;
+        unit(un, row, ch);
+        const bool in = t < nt && j0 + row < mt.n;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) gv[un][q] = mv[un][q] = 0.f;
         if (mt.tall) {
           const int64_t at = (j0 + row) * sj + ch * 8;
 #pragma unroll
           for (int q = 0; q < 8; q += 4)
             if (in && ch * 8 + q < s) {
-              *reinterpret_cast<float4*>(gv + q) = __ldcs(reinterpret_cast<const float4*>(g + at + q));
-              *reinterpret_cast<float4*>(mv + q) = __ldcs(reinterpret_cast<const float4*>(m + at + q));
+              *reinterpret_cast<float4*>(gv[un] + q) = __ldcs(reinterpret_cast<const float4*>(g + at + q));
+              *reinterpret_cast<float4*>(mv[un] + q) = __ldcs(reinterpret_cast<const float4*>(m + at + q));
             }
         } else {
           const int64_t at = (int64_t)(ch * 8) * si + j0 + row;
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             if (in && ch * 8 + q < s) {
-              gv[q] = __ldcs(g + at + q * si);
-              mv[q] = __ldcs(m + at + q * si);
+              gv[un][q] = __ldcs(g + at + q * si);
+              mv[un][q] = __ldcs(m + at + q * si);
             }
         }
+      }
+    };
+    load(0);
+    for (int t = 0; t < nt; ++t) {
+      uint8_t* hi = place(t);
+      uint8_t* lo = hi + 16 * 1024;
+      const int64_t j0 = (first + t) * 128;
+      if (t >= kTcTiles + 2) {
+        if (tid == 0) scratch_free(t);
+        __syncthreads();
+      }
+      float w[2][8];
+#pragma unroll
+      for (int un = 0; un < 2; ++un)
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          mv[q] = fmaf(mu, mv[q], c * gv[q]);
-          w[q] = hp.nesterov ? fmaf(mu, mv[q], c * gv[q]) : mv[q];
-          mx = fmaxf(mx, fabsf(w[q]));
+          const float gh = c * gv[un][q];
+          mv[un][q] = fmaf(mu, mv[un][q], gh);
+          w[un][q] = hp.nesterov ? fmaf(mu, mv[un][q], gh) : mv[un][q];
         }
+#pragma unroll
+      for (int un = 0; un < 2; ++un) {
+        int row, ch;
+        unit(un, row, ch);
+        const bool in = j0 + row < mt.n;
         if (mt.tall) {
           const int64_t at = (j0 + row) * sj + ch * 8;
 #pragma unroll
           for (int q = 0; q < 8; q += 4)
             if (in && ch * 8 + q < s) {
-              store4(m + at + q, mv + q);
+              store4(m + at + q, mv[un] + q);
               if (a.zero_grads) *reinterpret_cast<float4*>(g + at + q) = make_float4(0.f, 0.f, 0.f, 0.f);
             }
         } else {
@@ -559,224 +638,285 @@ __global__ void __launch_bounds__(kMuonThreads, 1) k_muon_tc(const __grid_consta
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             if (in && ch * 8 + q < s) {
-              m[at + q * si] = mv[q];
+              m[at + q * si] = mv[un][q];
               if (a.zero_grads) g[at + q * si] = 0.f;
             }
         }
-        put_split8(hi, lo, row, ch, w);
       }
-      if (t >= kTcTiles) {
-        publish();
-        flush(t);
+      load(t + 1);   // on its way while this tile is split and stored
+#pragma unroll
+      for (int un = 0; un < 2; ++un) {
+        int row, ch;
+        unit(un, row, ch);
+        put_split8(hi, lo, row, ch, w[un]);
+      }
+      publish();
+      if (tid == 0) {
+        gram_mma(hi, t == 0);
+        if (t >= kTcTiles) {
+          umma_commit(&bar_used[(t - kTcTiles) & 1]);
+          begin_flush(t);
+        }
+        if (t + 1 == nt) {
+          umma_commit(bar_gram);
+          end_flushes();
+          drain_used();
+        }
       }
     }
-    const float pre = range_scale(mx, sh, C);
-    if (pre != 1.f) {
-      for (int t = 0; t < nt; ++t) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(fetch(t));
-        __syncthreads();
-        for (int e = tid; e < kTcTileBytes / 4; e += kMuonThreads)
-          w[e] = pack_bf16(__uint_as_float(w[e] << 16) * pre, __uint_as_float(w[e] & 0xFFFF0000u) * pre);
-        publish();
-        flush(t);
-      }
-    }
-    publish();
 
-    // ---- Gram matrix of u
-    for (int t = 0; t < nt; ++t) {
-      const uint8_t* tile = fetch(t);
-      if (tid == 0) gram_mma(tile, t == 0);
-      if (t >= kTcTiles || t + 1 == nt) {
-        if (tid == 0) umma_commit(bar_gram);
+    // G of the tiles (the Gram products in D_gram), summed over the cluster, in g0
+    auto gram_all = [&]() {
+      if (nt > 0) {
         wait(bar_gram, ph_gram);
         ph_gram ^= 1u;
       }
-      if (t >= kTcTiles) __syncthreads();
-    }
-
-    for (int done = 0; done < hp.steps;) {
-      const int left = hp.steps - done;
-      const int now = left % kStageSteps ? left % kStageSteps : kStageSteps;
       // ---- G = the sum of D's quadrants, then over the cluster
       if (warp < 4) {
-        float v[64];
         const uint32_t d = tm_gram + ((uint32_t)(warp * 32) << 16);
-        if (nt > 0) {
-          float x[32];
+        const int grow = (warp & 1) * 32 + lane;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tmem_ld32(d + (uint32_t)(h * 32), v + h * 32);
-            tmem_ld32(d + 64u + (uint32_t)(h * 32), x);
+        for (int h = 0; h < 64; h += 32) {
+          float v[32];
+          if (nt > 0) {
+            float x[32];
+            tmem_ld32(d + (uint32_t)h, v);
+            tmem_ld32(d + 64u + (uint32_t)h, x);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) v[h * 32 + q] += x[q];
+            for (int q = 0; q < 32; ++q) v[q] += x[q];
+          } else {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] = 0.f;
           }
-        } else {
+          if (warp < 2) {
 #pragma unroll
-          for (int q = 0; q < 64; ++q) v[q] = 0.f;
+            for (int q = 0; q < 32; q += 4) store4(g0 + mat_at(grow, h + q), v + q);
+          }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (warp >= 2) {
+#pragma unroll
+            for (int q = 0; q < 32; q += 4) {
+              float4* at = reinterpret_cast<float4*>(g0 + mat_at(grow, h + q));
+              const float4 o = *at;
+              *at = make_float4(o.x + v[q], o.y + v[q + 1], o.z + v[q + 2], o.w + v[q + 3]);
+            }
+          }
         }
         fence_before();
-        float* row = g0 + ((warp & 1) * 32 + lane) * kTcLdG;
-        if (warp < 2) {
-#pragma unroll
-          for (int q = 0; q < 64; q += 4) store4(row + q, v + q);
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (warp >= 2) {
-#pragma unroll
-          for (int q = 0; q < 64; q += 4) {
-            const float4 o = *reinterpret_cast<const float4*>(row + q);
-            *reinterpret_cast<float4*>(row + q) = make_float4(o.x + v[q], o.y + v[q + 1], o.z + v[q + 2], o.w + v[q + 3]);
-          }
-        }
       }
       __syncthreads();
       if (C > 1) {
         // CTA r adds an r-th of the matrix over the ranks, then every CTA gathers the parts
         const int per = 1024 / C;
         cluster_sync();
-        for (int e = tid; e < per; e += kMuonThreads) {
-          const int at = rank * per + e, i = at >> 4, k = (at & 15) * 4;
-          float4 v = dsmem_ld4(g0 + i * kTcLdG + k, 0);
+        for (int e = tid; e < per; e += kTcThreads) {
+          const int at = rank * per + e;
+          float4 v = dsmem_ld4(g0 + at * 4, 0);
           for (int r = 1; r < C; ++r) {
-            const float4 o = dsmem_ld4(g0 + i * kTcLdG + k, (uint32_t)r);
+            const float4 o = dsmem_ld4(g0 + at * 4, (uint32_t)r);
             v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
           }
           *reinterpret_cast<float4*>(t1 + at * 4) = v;
         }
         cluster_sync();
-        for (int at = tid; at < 1024; at += kMuonThreads) {
+        for (int at = tid; at < 1024; at += kTcThreads) {
           const float4 v = dsmem_ld4(t1 + at * 4, (uint32_t)(at / per));
-          *reinterpret_cast<float4*>(g0 + (at >> 4) * kTcLdG + (at & 15) * 4) = v;
+          *reinterpret_cast<float4*>(g0 + at * 4) = v;
         }
         cluster_sync();   // the peers have read t1
       }
+    };
+
+    for (int done = 0; done < hp.steps;) {
+      const int left = hp.steps - done;
+      const int now = left % kStageSteps ? left % kStageSteps : kStageSteps;
+      gram_all();
       float inv = 1.f;
       if (done == 0) {   // X = u / ||u||, ||u||^2 = trace G
-        float tr = 0.f;
-        for (int i = 0; i < s; ++i) tr += g0[i * kTcLdG + i];
+        auto trace = [&]() {
+          float tr = 0.f;
+          for (int i = 0; i < s; ++i) tr += g0[mat_at(i, i)];
+          return tr;
+        };
+        float tr = trace();
+        if (!(tr > 1e-18f && tr < 1e30f)) {
+          // the squares may have left the fp32 range (or u is zero): scale u by a power of two that
+          // brings its largest magnitude to about one, and sum again
+          float mx = 0.f, pre = 1.f;
+          for (int pass = 0; pass < 2; ++pass) {
+            if (pass == 1 && pre == 1.f) break;
+            publish();
+            for (int t = 0; t < nt; ++t) {
+              uint32_t* w = reinterpret_cast<uint32_t*>(place(t));
+              if (tid == 0 && t >= kTcTiles) {
+                begin_fetch(t);
+                end_fetch(t);
+              }
+              __syncthreads();
+              if (pass == 0) {
+                for (int e = tid; e < kTcTileBytes / 8; e += kTcThreads)   // the hi terms
+                  mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+                publish();
+                continue;
+              }
+              for (int e = tid; e < kTcTileBytes / 4; e += kTcThreads)
+                w[e] = pack_bf16(__uint_as_float(w[e] << 16) * pre, __uint_as_float(w[e] & 0xFFFF0000u) * pre);
+              publish();
+              if (tid == 0) {
+                gram_mma(place(t), t == 0);
+                if (t >= kTcTiles) {
+                  umma_commit(&bar_used[(t - kTcTiles) & 1]);
+                  begin_flush(t);
+                  end_flushes();
+                  wait0(&bar_used[(t - kTcTiles) & 1], ph_used[(t - kTcTiles) & 1]);
+                }
+                if (t + 1 == nt) umma_commit(bar_gram);
+              }
+              __syncthreads();
+            }
+            if (pass == 0) pre = range_scale<kTcThreads>(mx, sh, C);
+          }
+          if (pre != 1.f) {
+            gram_all();
+            tr = trace();
+          }
+        }
         inv = tr > 0.f ? 1.f / sqrtf(tr) : 0.f;
         __syncthreads();
-        for (int e = tid; e < 64 * 64; e += kMuonThreads) g0[(e >> 6) * kTcLdG + (e & 63)] *= inv * inv;
+        for (int e = tid; e < 64 * 64; e += kTcThreads) g0[e] *= inv * inv;
         __syncthreads();
       }
-      // ---- the stage's steps on G; Q, their product, in fp32 over the operand's place
-      const int r = (tid >> 4) * 4, cc = (tid & 15) * 4;
-      float acc[4][4];
+      // ---- the stage's steps on G: P = a I + b G + c G^2, Q <- P Q, G <- P^2 G
+      float* q_now = t1;   // the first step's P is the product so far
       for (int k = 0; k < now; ++k) {
-        mm4(acc, g0, kTcLdG, g0, kTcLdG, s);
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-#pragma unroll
-          for (int z = 0; z < 4; ++z)
-            acc[y][z] = hp.c * acc[y][z] + hp.b * g0[(r + y) * kTcLdG + cc + z] +
-                        (r + y == cc + z && r + y < s ? hp.a : 0.f);
-        put4(t1, 64, acc);                                   // P
-        if (k == 0 && now > 1) put4(qf, 64, acc);
-        __syncthreads();
+        float* pk = k == 0 ? t1 : t2;
+        small_product(pk, g0, g0, g0, s, hp.a, hp.b, hp.c);
+        if (k > 0) {
+          small_product(qf, pk, q_now, g0, s, 0.f, 0.f, 1.f);
+          q_now = qf;
+        }
         if (k + 1 < now) {
-          mm4(acc, t1, 64, t1, 64, s);                       // P^2
-          put4(t2, 64, acc);
-          if (k > 0) {
-            mm4(acc, t1, 64, qf, 64, s);                     // Q <- P Q
-            __syncthreads();
-            put4(qf, 64, acc);
-          }
-          __syncthreads();
-          mm4(acc, g0, kTcLdG, t2, 64, s);                   // G <- P^2 G
-          __syncthreads();
-          put4(g0, kTcLdG, acc);
-          __syncthreads();
-        } else if (k > 0) {
-          mm4(acc, t1, 64, qf, 64, s);
-          __syncthreads();
+          // P^2 goes where neither P nor Q is: over the other small matrix
+          float* sq = k == 0 ? t2 : t1;
+          small_product(sq, pk, pk, g0, s, 0.f, 0.f, 1.f);
+          small_product(g0, g0, sq, g0, s, 0.f, 0.f, 1.f);
         }
       }
       done += now;
-      // acc holds this thread's block of Q: [Q_hi; Q_lo] as the B operand
+      // [Q_hi; Q_lo] as the B operand: 8 elements of a row per thread
+      {
+        const int row = tid >> 3, ch = tid & 7;
+        float v[8];
+        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(q_now + mat_at(row, ch * 8));
+        *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(q_now + mat_at(row, ch * 8 + 4));
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        uint32_t h[2], l[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float v0 = acc[y][2 * q] * inv, v1 = acc[y][2 * q + 1] * inv;
-          h[q] = pack_bf16(v0, v1);
-          l[q] = pack_bf16(v0 - __uint_as_float(h[q] << 16), v1 - __uint_as_float(h[q] & 0xFFFF0000u));
-        }
-        const int row = r + y;
-        const int at = row * 128 + (((cc >> 3) ^ (row & 7)) << 4) + (cc & 4) * 2;
-        *reinterpret_cast<uint2*>(qop + at) = make_uint2(h[0], h[1]);
-        *reinterpret_cast<uint2*>(qop + 64 * 128 + at) = make_uint2(l[0], l[1]);
+        for (int q = 0; q < 8; ++q) v[q] *= inv;
+        __syncthreads();   // Q may lie where the operand goes
+        put_split8(qop, qop + 64 * 128, row, ch, v);
       }
       publish();
       // ---- X <- Q X: into the tiles, with the next Gram matrix, or into the parameters
       const bool last = done >= hp.steps;
-      const int quad = warp & 3, ih = warp >> 2;
+      const int quad = warp & 3, ih = warp >> 2;   // TMEM lanes, 16 of the 64 rows of X
       const int jrow = quad * 32 + lane;
-      if (tid == 0 && nt > 0) apply_mma(tiles, 0);
+      if (tid == 0) {
+        if (nt > kTcTiles) begin_fetch(kTcTiles);
+        if (nt > 0) apply_mma(tiles, 0);
+      }
+      // the parameters of a tile are on their way while the tile before it is updated
+      float pn[16];
+      auto load_p = [&](int t) {
+        const int64_t j0 = (first + t) * 128;
+        if (mt.tall) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int e = v * kTcThreads + tid, j = e >> 4, q = e & 15;
+            if (t < nt && q * 4 < s && j0 + j < mt.n)
+              *reinterpret_cast<float4*>(pn + 4 * v) = __ldcs(reinterpret_cast<const float4*>(p + (j0 + j) * sj + q * 4));
+          }
+        } else {
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int i = v * 4 + (tid >> 7);
+            if (t < nt && i < s && j0 + (tid & 127) < mt.n) pn[v] = __ldcs(p + i * si + j0 + (tid & 127));
+          }
+        }
+      };
+      if (last) load_p(0);
       for (int t = 0; t < nt; ++t) {
         const int buf = t & 1;
-        uint8_t* tile = tiles + t * kTcTileBytes;
-        if (t >= kTcTiles) {
-          tile = fetch(t);
-          if (tid == 0) apply_mma(tile, buf);
+        uint8_t* tile = place(t);
+        if (tid == 0) {
+          if (t >= kTcTiles) {
+            end_fetch(t);
+            apply_mma(tile, buf);
+            if (t + 1 < nt) {   // the next spilled tile, over the one before this one
+              if (!last) scratch_free(t + 1);
+              begin_fetch(t + 1);
+            }
+          }
+          if (t + 1 < nt && t + 1 < kTcTiles) apply_mma(place(t + 1), buf ^ 1);
         }
-        if (t + 1 < nt && t + 1 < kTcTiles && tid == 0) apply_mma(tiles + (t + 1) * kTcTileBytes, buf ^ 1);
+        const int64_t j0 = (first + t) * 128;
         wait(&bar_apply[buf], ph_apply[buf]);
         ph_apply[buf] ^= 1u;
-        float x[32];
+        float x[16];
         {
-          float y[32];
-          const uint32_t d = tm_apply + 128u * (uint32_t)buf + ((uint32_t)(quad * 32) << 16) + (uint32_t)(ih * 32);
-          tmem_ld32(d, x);
-          tmem_ld32(d + 64u, y);
+          float y[16];
+          const uint32_t d = tm_apply + 128u * (uint32_t)buf + ((uint32_t)(quad * 32) << 16) + (uint32_t)(ih * 16);
+          tmem_ld16(d, x);
+          tmem_ld16(d + 64u, y);
 #pragma unroll
-          for (int q = 0; q < 32; ++q) x[q] += y[q];
+          for (int q = 0; q < 16; ++q) x[q] += y[q];
         }
         if (!last) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) put_split8(tile, tile + 16 * 1024, jrow, ih * 4 + q, x + q * 8);
+          for (int q = 0; q < 2; ++q) put_split8(tile, tile + 16 * 1024, jrow, ih * 2 + q, x + q * 8);
           publish();
-          if (tid == 0) gram_mma(tile, t == 0);
-          if (t >= kTcTiles || t + 1 == nt) {
-            if (tid == 0) umma_commit(bar_gram);
-            wait(bar_gram, ph_gram);
-            ph_gram ^= 1u;
-            flush(t);
+          if (tid == 0) {
+            gram_mma(tile, t == 0);
+            if (t >= kTcTiles) {
+              umma_commit(&bar_used[(t - kTcTiles) & 1]);
+              begin_flush(t);
+            }
+            if (t + 1 == nt) {
+              umma_commit(bar_gram);
+              end_flushes();
+              drain_used();
+            }
           }
         } else {
           // X [128][64] fp32 over the tile, 16-byte chunks spread by the row
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            store4(reinterpret_cast<float*>(tile + jrow * 256 + (((ih * 8 + q) ^ (jrow & 15)) << 4)), x + q * 4);
+          for (int q = 0; q < 4; ++q)
+            store4(reinterpret_cast<float*>(tile + jrow * 256 + (((ih * 4 + q) ^ (jrow & 15)) << 4)), x + q * 4);
           fence_before();
           __syncthreads();
           fence_after();
-          const int64_t j0 = (first + t) * 128;
           const float step = mt.step, dec = mt.lr * mt.decay;
+          float pc[16];
+#pragma unroll
+          for (int v = 0; v < 16; ++v) pc[v] = pn[v];
+          load_p(t + 1);
           if (mt.tall) {
-            for (int e = tid; e < 128 * (s / 4); e += kMuonThreads) {
-              const int j = e / (s / 4), q = e - j * (s / 4);
-              if (j0 + j >= mt.n || !ok) continue;
-              float* at = p + (j0 + j) * sj + q * 4;
-              float4 pv = *reinterpret_cast<const float4*>(at);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int e = v * kTcThreads + tid, j = e >> 4, q = e & 15;
+              if (q * 4 >= s || j0 + j >= mt.n || !ok) continue;
               const float4 xv = *reinterpret_cast<const float4*>(tile + j * 256 + ((q ^ (j & 15)) << 4));
-              pv.x = pv.x - step * xv.x - dec * pv.x;
-              pv.y = pv.y - step * xv.y - dec * pv.y;
-              pv.z = pv.z - step * xv.z - dec * pv.z;
-              pv.w = pv.w - step * xv.w - dec * pv.w;
-              *reinterpret_cast<float4*>(at) = pv;
+              const float xs[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+              for (int z = 0; z < 4; ++z) pc[4 * v + z] = pc[4 * v + z] - step * xs[z] - dec * pc[4 * v + z];
+              store4(p + (j0 + j) * sj + q * 4, pc + 4 * v);
             }
           } else {
             const int j = tid & 127;
-            if (j0 + j < mt.n && ok) {
-#pragma unroll 8
-              for (int i = tid >> 7; i < s; i += 2) {
-                float* at = p + i * si + j0 + j;
-                const float pv = *at;
-                const float xv = *reinterpret_cast<const float*>(tile + j * 256 + (((i >> 2) ^ (j & 15)) << 4) + (i & 3) * 4);
-                *at = pv - step * xv - dec * pv;
-              }
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+              const int i = v * 4 + (tid >> 7);
+              if (i >= s || j0 + j >= mt.n || !ok) continue;
+              const float xv = *reinterpret_cast<const float*>(tile + j * 256 + (((i >> 2) ^ (j & 15)) << 4) + (i & 3) * 4);
+              p[i * si + j0 + j] = pc[v] - step * xv - dec * pc[v];
             }
           }
           publish();   // a spilled tile's room is the next one's
@@ -794,9 +934,9 @@ __global__ void __launch_bounds__(kMuonThreads, 1) k_muon_tc(const __grid_consta
 
 // One launch of `kernel` over the table's matrices, a cluster of C CTAs each, persistent.
 template <typename K, typename... Args>
-cudaError_t launch_clusters(K kernel, int smem, int n, int C, int most, cudaStream_t st, const Args&... args) {
+cudaError_t launch_clusters(K kernel, int threads, int smem, int n, int C, int most, cudaStream_t st, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kMuonThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
@@ -806,8 +946,19 @@ cudaError_t launch_clusters(K kernel, int smem, int n, int C, int most, cudaStre
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = add_pdl_attr(at, 1);
-  const int clusters = std::max(1, std::min(n, most / C));
-  cfg.gridDim = dim3((unsigned)(clusters * C));
+  cfg.gridDim = dim3((unsigned)C);
+  if (most < (1 << 20)) {   // persistent: as many clusters as are resident at a time
+    static std::atomic<int> fits[17];   // by cluster size
+    int fit = fits[C].load();
+    if (fit == 0) {
+      cudaError_t e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      fit = std::max(fit, 1);
+      fits[C].store(fit);
+    }
+    most = std::min(most / C, fit);
+  }
+  cfg.gridDim = dim3((unsigned)(std::max(1, std::min(n, most)) * C));
   prof_begin(0, st);
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
@@ -827,16 +978,23 @@ cudaError_t run_simt(float* p, float* g, float* m, const MuonTab& tab, const Muo
   static cudaError_t set = set_attrs(k_muon_simt<S4>, (F::kSmallFloats + F::kCap * F::SP) * 4);
   if (set != cudaSuccess) return set;
   const int smem = (F::kSmallFloats + std::min(held, F::kCap) * F::SP) * 4;
-  return launch_clusters(k_muon_simt<S4>, smem, tab.n, C, 1 << 20, st, p, g, m, tab, hp, scale_norm,
+  return launch_clusters(k_muon_simt<S4>, kMuonThreads, smem, tab.n, C, 1 << 20, st, p, g, m, tab, hp, scale_norm,
                          status, zero_grads, C);
 }
 
 }  // namespace
 
+// CTAs of a matrix's cluster. CUDA cores: 512 columns a CTA. Tensor cores: small clusters, since
+// every CTA repeats the products of the small matrices and clusters of 16 leave SMs without a
+// place (32 matrices 64 x 14336: 571 us with 16 CTAs each, five or six clusters at a time); as
+// many as the call needs to use every SM, and at least a tile per CTA.
 int muon_cluster(const MuonMat& m, int n_mats) {
-  const int64_t fit = m.s <= 16 ? 512 : 128 * kTcTiles;   // columns a CTA takes before the cluster grows
   int C = 1;
-  while (C < 16 && (m.n > fit * C || (n_mats * C * 2 <= 152 && m.n > 128 * C))) C *= 2;
+  if (m.s <= 16) {
+    while (C < 16 && (m.n > 512 * (int64_t)C || (n_mats * C * 2 <= 152 && m.n > 128 * C))) C *= 2;
+  } else {
+    while (C < 16 && n_mats * C < 152 && m.n > 128 * (int64_t)C) C *= 2;
+  }
   return C;
 }
 
@@ -874,7 +1032,7 @@ cudaError_t launch_muon(float* p, float* g, float* m, const MuonTab& tab, const 
   a.err = error_word();
   if (!a.err) return cudaErrorInvalidDevice;
   a.wait_limit = tc_wait_limit();
-  return launch_clusters(k_muon_tc, kTcSmem, tab.n, C, kMuonMaxCtas, st, tab, hp, a);
+  return launch_clusters(k_muon_tc, kTcThreads, kTcSmem, tab.n, C, kMuonMaxCtas, st, tab, hp, a);
 }
 
 }  // namespace lora
