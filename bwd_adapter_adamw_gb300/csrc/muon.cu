@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(kMuonThreads) k_muon_simt(float* __restrict__ 
 constexpr int kTcThreads = 512;
 constexpr int kTcTiles = 4;                    // tiles held per CTA; others go through `spill`
 constexpr int kTcTileBytes = 32 * 1024;
+constexpr int kTcAhead = 4;                    // tiles prefetched to L2 ahead of the one in use
 constexpr int kTcSmem = (kTcTiles + 2) * kTcTileBytes + 2 * 16 * 1024 + 256 + 1024;
 static_assert(kTcSmem <= 227 * 1024, "shared memory per CTA");
 
@@ -477,8 +478,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
   uint32_t ph_apply[2] = {0, 0}, ph_gram = 0;   // the same in every thread
   uint32_t ph_load[2] = {0, 0}, ph_used[2] = {0, 0};   // of thread 0, which alone waits on them
   bool ok = true;                                            // no wait has run out of its bound
+  // One warp polls, the others wait at the barrier: polling by all of them took most of the issue
+  // slots.
   auto wait = [&](uint64_t* bar, uint32_t ph) {
-    ok = __all_sync(0xffffffffu, mbar_wait_for(bar, ph, 2u, a.err, ok ? a.wait_limit : 0ull)) && ok;
+    if (warp == 0) ok = mbar_wait_for(bar, ph, 2u, a.err, ok ? a.wait_limit : 0ull) && ok;
+    __syncthreads();
     fence_after();
   };
   // every thread's writes to shared memory become visible to the tensor cores and bulk copies
@@ -501,6 +505,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
     float* p = a.P + mt.offset;
     float* g = a.G + mt.offset;
     float* m = a.M + mt.offset;
+    const bool nesterov = hp.nesterov;
+    const float mu_u = nesterov ? mu : 1.f, c_u = nesterov ? c : 0.f;   // u = c_u g + mu_u m
     // Tile t of this CTA: held, or, while it is in use, in one of the two scratch tiles. Spilled tiles
     // move by bulk copies of thread 0.
     auto place = [&](int t) {
@@ -533,9 +539,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       asm volatile("fence.proxy.async;" ::: "memory");
     };
     // the scratch tile of t is free: t - 2's copy out has read it and its Gram products are done
-    auto scratch_free = [&](int t) {
+    // (t - 1's copy out, where it has begun, may go on)
+    auto scratch_free = [&](int t, bool newer) {
       if (t - 2 < kTcTiles) return;
-      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      if (newer) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       wait0(&bar_used[(t - kTcTiles) & 1], ph_used[(t - kTcTiles) & 1]);
     };
     // the last one or two uses of the scratch tiles, at the end of a pass
@@ -562,53 +570,69 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
 
     // ---- momentum and u; unit: 8 rows of one column (tall) or of 32 columns, one per lane (wide);
     // a thread's two units are loaded together
-    float gv[2][8], mv[2][8];
-    auto unit = [&](int un, int& row, int& ch) {
+    // (row, chunk) of this thread's units, and where they start in the first tile
+    int row[2], ch[2], live[2];   // live: how many of the 8 rows exist
+    int64_t at0[2];
+#pragma unroll
+    for (int un = 0; un < 2; ++un) {
       if (mt.tall) {
-        const int e = un * kTcThreads + tid;
-        row = e >> 3;
-        ch = e & 7;
+        row[un] = (un * kTcThreads + tid) >> 3;
+        ch[un] = tid & 7;
       } else {
         const int e = un * 16 + warp;   // 32 units of (chunk, 32 columns)
-        row = (e & 3) * 32 + lane;
-        ch = e >> 2;
+        row[un] = (e & 3) * 32 + lane;
+        ch[un] = e >> 2;
       }
-    };
+      live[un] = min(8, max(0, s - ch[un] * 8));
+      at0[un] = (first * 128 + row[un]) * sj + (int64_t)(ch[un] * 8) * si;
+    }
+    const int left0 = (int)(mt.n - first * 128);   // columns from the first tile to the end
+    float gv[2][8], mv[2][8];
     auto load = [&](int t) {
-      const int64_t j0 = (first + t) * 128;
 #pragma unroll
       for (int un = 0; un < 2; ++un) {
-        int row, ch;
-        unit(un, row, ch);
-        const bool in = t < nt && j0 + row < mt.n;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) gv[un][q] = mv[un][q] = 0.f;
+        const int k = t < nt && t * 128 + row[un] < left0 ? live[un] : 0;
+        const float* gp = g + at0[un] + (int64_t)t * 128 * sj;
+        const float* mp = m + at0[un] + (int64_t)t * 128 * sj;
         if (mt.tall) {
-          const int64_t at = (j0 + row) * sj + ch * 8;
+          const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int q = 0; q < 8; q += 4)
-            if (in && ch * 8 + q < s) {
-              *reinterpret_cast<float4*>(gv[un] + q) = __ldcs(reinterpret_cast<const float4*>(g + at + q));
-              *reinterpret_cast<float4*>(mv[un] + q) = __ldcs(reinterpret_cast<const float4*>(m + at + q));
-            }
+          for (int q = 0; q < 8; q += 4) {
+            *reinterpret_cast<float4*>(gv[un] + q) = q < k ? __ldcs(reinterpret_cast<const float4*>(gp + q)) : z;
+            *reinterpret_cast<float4*>(mv[un] + q) = q < k ? __ldcs(reinterpret_cast<const float4*>(mp + q)) : z;
+          }
         } else {
-          const int64_t at = (int64_t)(ch * 8) * si + j0 + row;
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (in && ch * 8 + q < s) {
-              gv[un][q] = __ldcs(g + at + q * si);
-              mv[un][q] = __ldcs(m + at + q * si);
-            }
+          for (int q = 0; q < 8; ++q, gp += si, mp += si) {
+            gv[un][q] = q < k ? __ldcs(gp) : 0.f;
+            mv[un][q] = q < k ? __ldcs(mp) : 0.f;
+          }
         }
       }
     };
+    // Lines of later tiles to L2, one per thread and array (a tile is at most 256 lines): registers
+    // hold one tile ahead, which covers L2's latency but not memory's.
+    auto prefetch = [&](const float* base, int t, int l) {
+      const int64_t j0 = (first + t) * 128;
+      if (t >= nt) return;
+      int64_t at;
+      if (mt.tall) {
+        at = j0 * s + (int64_t)l * 32;
+        if (l >= 4 * s || at >= mt.n * s) return;
+      } else {
+        at = (int64_t)(l >> 2) * si + j0 + (l & 3) * 32;
+        if ((l >> 2) >= s || j0 + (l & 3) * 32 >= mt.n) return;
+      }
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(base + at));
+    };
+    for (int t = 1; t < kTcAhead; ++t) prefetch(tid < 256 ? g : m, t, tid & 255);
     load(0);
     for (int t = 0; t < nt; ++t) {
+      prefetch(tid < 256 ? g : m, t + kTcAhead, tid & 255);
       uint8_t* hi = place(t);
       uint8_t* lo = hi + 16 * 1024;
-      const int64_t j0 = (first + t) * 128;
       if (t >= kTcTiles + 2) {
-        if (tid == 0) scratch_free(t);
+        if (tid == 0) scratch_free(t, true);
         __syncthreads();
       }
       float w[2][8];
@@ -616,40 +640,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       for (int un = 0; un < 2; ++un)
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const float gh = c * gv[un][q];
-          mv[un][q] = fmaf(mu, mv[un][q], gh);
-          w[un][q] = hp.nesterov ? fmaf(mu, mv[un][q], gh) : mv[un][q];
+          mv[un][q] = fmaf(mu, mv[un][q], c * gv[un][q]);
+          w[un][q] = fmaf(mu_u, mv[un][q], c_u * gv[un][q]);
         }
 #pragma unroll
       for (int un = 0; un < 2; ++un) {
-        int row, ch;
-        unit(un, row, ch);
-        const bool in = j0 + row < mt.n;
+        const int k = t * 128 + row[un] < left0 ? live[un] : 0;
+        float* gp = g + at0[un] + (int64_t)t * 128 * sj;
+        float* mp = m + at0[un] + (int64_t)t * 128 * sj;
         if (mt.tall) {
-          const int64_t at = (j0 + row) * sj + ch * 8;
 #pragma unroll
           for (int q = 0; q < 8; q += 4)
-            if (in && ch * 8 + q < s) {
-              store4(m + at + q, mv[un] + q);
-              if (a.zero_grads) *reinterpret_cast<float4*>(g + at + q) = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+            if (q < k) store4(mp + q, mv[un] + q);
         } else {
-          const int64_t at = (int64_t)(ch * 8) * si + j0 + row;
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (in && ch * 8 + q < s) {
-              m[at + q * si] = mv[un][q];
-              if (a.zero_grads) g[at + q * si] = 0.f;
-            }
+          for (int q = 0; q < 8; ++q, mp += si)
+            if (q < k) *mp = mv[un][q];
+        }
+        if (a.zero_grads) {
+          for (int q = 0; q < k; ++q, gp += si) *gp = 0.f;
         }
       }
       load(t + 1);   // on its way while this tile is split and stored
 #pragma unroll
-      for (int un = 0; un < 2; ++un) {
-        int row, ch;
-        unit(un, row, ch);
-        put_split8(hi, lo, row, ch, w[un]);
-      }
+      for (int un = 0; un < 2; ++un) put_split8(hi, lo, row[un], ch[un], w[un]);
       publish();
       if (tid == 0) {
         gram_mma(hi, t == 0);
@@ -823,27 +837,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
         if (nt > kTcTiles) begin_fetch(kTcTiles);
         if (nt > 0) apply_mma(tiles, 0);
       }
-      // the parameters of a tile are on their way while the tile before it is updated
+      // The parameters of a tile are on their way while the tile before it is updated. A thread's are
+      // four 16-byte vectors, 512 threads apart (tall), or 16 rows of a column, four apart (wide).
       float pn[16];
+      const int prow = mt.tall ? tid >> 4 : tid & 127, pq = mt.tall ? (tid & 15) * 4 : tid >> 7;
+      float* p0 = p + (first * 128 + prow) * sj + pq * si;
+      const bool pcol = pq < s;
       auto load_p = [&](int t) {
-        const int64_t j0 = (first + t) * 128;
+        const float* pp = p0 + (int64_t)t * 128 * sj;
         if (mt.tall) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int e = v * kTcThreads + tid, j = e >> 4, q = e & 15;
-            if (t < nt && q * 4 < s && j0 + j < mt.n)
-              *reinterpret_cast<float4*>(pn + 4 * v) = __ldcs(reinterpret_cast<const float4*>(p + (j0 + j) * sj + q * 4));
-          }
+          for (int v = 0; v < 4; ++v)
+            if (t < nt && pcol && t * 128 + prow + v * 32 < left0)
+              *reinterpret_cast<float4*>(pn + 4 * v) = __ldcs(reinterpret_cast<const float4*>(pp + v * 32 * sj));
         } else {
+          const int k = t < nt && t * 128 + prow < left0 ? s - pq : 0;
 #pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int i = v * 4 + (tid >> 7);
-            if (t < nt && i < s && j0 + (tid & 127) < mt.n) pn[v] = __ldcs(p + i * si + j0 + (tid & 127));
-          }
+          for (int v = 0; v < 16; ++v, pp += 4 * si)
+            if (4 * v < k) pn[v] = __ldcs(pp);
         }
       };
-      if (last) load_p(0);
+      if (last) {
+        load_p(0);
+        if (tid >= 256)
+          for (int t = 1; t < kTcAhead; ++t) prefetch(p, t, tid & 255);
+      }
       for (int t = 0; t < nt; ++t) {
+        if (last && tid >= 256) prefetch(p, t + kTcAhead, tid & 255);
         const int buf = t & 1;
         uint8_t* tile = place(t);
         if (tid == 0) {
@@ -851,13 +871,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
             end_fetch(t);
             apply_mma(tile, buf);
             if (t + 1 < nt) {   // the next spilled tile, over the one before this one
-              if (!last) scratch_free(t + 1);
+              if (!last) scratch_free(t + 1, false);
               begin_fetch(t + 1);
             }
           }
           if (t + 1 < nt && t + 1 < kTcTiles) apply_mma(place(t + 1), buf ^ 1);
         }
-        const int64_t j0 = (first + t) * 128;
         wait(&bar_apply[buf], ph_apply[buf]);
         ph_apply[buf] ^= 1u;
         float x[16];
@@ -893,30 +912,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
           fence_before();
           __syncthreads();
           fence_after();
-          const float step = mt.step, dec = mt.lr * mt.decay;
+          const float step = ok ? mt.step : 0.f, dec = ok ? mt.lr * mt.decay : 0.f;
           float pc[16];
 #pragma unroll
           for (int v = 0; v < 16; ++v) pc[v] = pn[v];
           load_p(t + 1);
+          float* pp = p0 + (int64_t)t * 128 * sj;
           if (mt.tall) {
+            if (pcol) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const int e = v * kTcThreads + tid, j = e >> 4, q = e & 15;
-              if (q * 4 >= s || j0 + j >= mt.n || !ok) continue;
-              const float4 xv = *reinterpret_cast<const float4*>(tile + j * 256 + ((q ^ (j & 15)) << 4));
-              const float xs[4] = {xv.x, xv.y, xv.z, xv.w};
+              for (int v = 0; v < 4; ++v) {
+                const int j = prow + v * 32;
+                if (t * 128 + j >= left0) continue;
+                const float4 xv = *reinterpret_cast<const float4*>(tile + j * 256 + (((pq >> 2) ^ (j & 15)) << 4));
+                const float xs[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-              for (int z = 0; z < 4; ++z) pc[4 * v + z] = pc[4 * v + z] - step * xs[z] - dec * pc[4 * v + z];
-              store4(p + (j0 + j) * sj + q * 4, pc + 4 * v);
+                for (int z = 0; z < 4; ++z) pc[4 * v + z] = pc[4 * v + z] - step * xs[z] - dec * pc[4 * v + z];
+                store4(pp + v * 32 * sj, pc + 4 * v);
+              }
             }
           } else {
-            const int j = tid & 127;
+            const int k = t * 128 + prow < left0 ? s - pq : 0;
+            const uint8_t* xrow = tile + prow * 256 + pq * 4;
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-              const int i = v * 4 + (tid >> 7);
-              if (i >= s || j0 + j >= mt.n || !ok) continue;
-              const float xv = *reinterpret_cast<const float*>(tile + j * 256 + (((i >> 2) ^ (j & 15)) << 4) + (i & 3) * 4);
-              p[i * si + j0 + j] = pc[v] - step * xv - dec * pc[v];
+            for (int v = 0; v < 16; ++v, pp += 4 * si) {
+              if (4 * v >= k) continue;
+              const float xv = *reinterpret_cast<const float*>(xrow + ((v ^ (prow & 15)) << 4));
+              *pp = pc[v] - step * xv - dec * pc[v];
             }
           }
           publish();   // a spilled tile's room is the next one's
