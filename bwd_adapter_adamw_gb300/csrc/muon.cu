@@ -472,6 +472,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
   fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_gram = tmem, tm_apply = tmem + 128;   // apply buffers at +128 and +256
+  // Spilled tiles should live in L2 (each CTA writes its own room again and again); the arenas pass
+  // through it once.
+  uint64_t keep;
+  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
   uint8_t* spill = a.spill + (size_t)blockIdx.x * a.spill_tiles * kTcTileBytes;
   constexpr uint32_t id_gram = idesc(kFmtBF16, 128, 128, true, true);
   constexpr uint32_t id_apply = idesc(kFmtBF16, 128, 128);
@@ -521,16 +525,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       uint64_t* bar = &bar_load[(t - kTcTiles) & 1];
       mbar_expect_tx(bar, kTcTileBytes);
       asm volatile(
-          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
               smem_u32(place(t))),
-          "l"(spill + (size_t)(t - kTcTiles) * kTcTileBytes), "r"(kTcTileBytes), "r"(smem_u32(bar))
+          "l"(spill + (size_t)(t - kTcTiles) * kTcTileBytes), "r"(kTcTileBytes), "r"(smem_u32(bar)), "l"(keep)
           : "memory");
     };
     auto end_fetch = [&](int t) { wait0(&bar_load[(t - kTcTiles) & 1], ph_load[(t - kTcTiles) & 1]); };
     auto begin_flush = [&](int t) {   // after publish
-      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;" ::"l"(
                        spill + (size_t)(t - kTcTiles) * kTcTileBytes),
-                   "r"(smem_u32(place(t))), "r"(kTcTileBytes)
+                   "r"(smem_u32(place(t))), "r"(kTcTileBytes), "l"(keep)
                    : "memory");
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     };
@@ -538,18 +542,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       asm volatile("fence.proxy.async;" ::: "memory");
     };
-    // the scratch tile of t is free: t - 2's copy out has read it and its Gram products are done
-    // (t - 1's copy out, where it has begun, may go on)
+    // The scratch tile of a pass's spilled tile is free: its user two spilled tiles earlier in the pass
+    // has been copied out and its Gram products are done. `newer`: the one between has begun its copy.
     auto scratch_free = [&](int t, bool newer) {
-      if (t - 2 < kTcTiles) return;
       if (newer) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
       else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       wait0(&bar_used[(t - kTcTiles) & 1], ph_used[(t - kTcTiles) & 1]);
     };
     // the last one or two uses of the scratch tiles, at the end of a pass
     auto drain_used = [&]() {
-      for (int t = max(kTcTiles, nt - 2); t < nt; ++t)
-        wait0(&bar_used[(t - kTcTiles) & 1], ph_used[(t - kTcTiles) & 1]);
+      const int n = nt - kTcTiles;   // spilled tiles
+      for (int k = 0; k < min(n, 2); ++k) wait0(&bar_used[k], ph_used[k]);
     };
     auto gram_mma = [&](const uint8_t* tile, bool begin) {   // thread 0
       const uint64_t d = smem_desc_sw128_mn(smem_u32(tile), 16 * 1024);
@@ -651,11 +654,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
         if (mt.tall) {
 #pragma unroll
           for (int q = 0; q < 8; q += 4)
-            if (q < k) store4(mp + q, mv[un] + q);
+            if (q < k) __stcs(reinterpret_cast<float4*>(mp + q), *reinterpret_cast<const float4*>(mv[un] + q));
         } else {
 #pragma unroll
           for (int q = 0; q < 8; ++q, mp += si)
-            if (q < k) *mp = mv[un][q];
+            if (q < k) __stcs(mp, mv[un][q]);
         }
         if (a.zero_grads) {
           for (int q = 0; q < k; ++q, gp += si) *gp = 0.f;
@@ -741,6 +744,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       }
     };
 
+    bool backwards = false;
     for (int done = 0; done < hp.steps;) {
       const int left = hp.steps - done;
       const int now = left % kStageSteps ? left % kStageSteps : kStageSteps;
@@ -833,9 +837,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       const bool last = done >= hp.steps;
       const int quad = warp & 3, ih = warp >> 2;   // TMEM lanes, 16 of the 64 rows of X
       const int jrow = quad * 32 + lane;
-      if (tid == 0) {
-        if (nt > kTcTiles) begin_fetch(kTcTiles);
-        if (nt > 0) apply_mma(tiles, 0);
+      // Passes go through the tiles in turn forwards (the first, over g and m) and backwards, so that
+      // a pass begins with the spilled tiles that were written last.
+      backwards = !backwards;
+      auto order = [&](int i) { return backwards ? nt - 1 - i : i; };
+      if (tid == 0 && nt > 0) {
+        if (nt > kTcTiles) begin_fetch(backwards ? nt - 1 : kTcTiles);
+        if (order(0) < kTcTiles) apply_mma(place(order(0)), 0);
       }
       // The parameters of a tile are on their way while the tile before it is updated. A thread's are
       // four 16-byte vectors, 512 threads apart (tall), or 16 rows of a column, four apart (wide).
@@ -857,25 +865,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
             if (4 * v < k) pn[v] = __ldcs(pp);
         }
       };
-      if (last) {
-        load_p(0);
+      if (last && nt > 0) {
+        load_p(order(0));
         if (tid >= 256)
-          for (int t = 1; t < kTcAhead; ++t) prefetch(p, t, tid & 255);
+          for (int i = 1; i < min(kTcAhead, nt); ++i) prefetch(p, order(i), tid & 255);
       }
-      for (int t = 0; t < nt; ++t) {
-        if (last && tid >= 256) prefetch(p, t + kTcAhead, tid & 255);
-        const int buf = t & 1;
+      for (int i = 0; i < nt; ++i) {
+        const int t = order(i), next = i + 1 < nt ? order(i + 1) : INT32_MAX;   // the latter: none
+        if (last && tid >= 256 && i + kTcAhead < nt) prefetch(p, order(i + kTcAhead), tid & 255);
+        const int buf = i & 1;
         uint8_t* tile = place(t);
         if (tid == 0) {
           if (t >= kTcTiles) {
             end_fetch(t);
             apply_mma(tile, buf);
-            if (t + 1 < nt) {   // the next spilled tile, over the one before this one
-              if (!last) scratch_free(t + 1, false);
-              begin_fetch(t + 1);
+            if (next < nt && next >= kTcTiles) {   // over the spilled tile before this one
+              if (!last && (backwards ? nt - 1 - t : t - kTcTiles) >= 1) scratch_free(next, false);
+              begin_fetch(next);
             }
           }
-          if (t + 1 < nt && t + 1 < kTcTiles) apply_mma(place(t + 1), buf ^ 1);
+          if (next < kTcTiles) apply_mma(place(next), buf ^ 1);
         }
         wait(&bar_apply[buf], ph_apply[buf]);
         ph_apply[buf] ^= 1u;
@@ -893,12 +902,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
           for (int q = 0; q < 2; ++q) put_split8(tile, tile + 16 * 1024, jrow, ih * 2 + q, x + q * 8);
           publish();
           if (tid == 0) {
-            gram_mma(tile, t == 0);
+            gram_mma(tile, i == 0);
             if (t >= kTcTiles) {
               umma_commit(&bar_used[(t - kTcTiles) & 1]);
               begin_flush(t);
             }
-            if (t + 1 == nt) {
+            if (i + 1 == nt) {
               umma_commit(bar_gram);
               end_flushes();
               drain_used();
@@ -916,7 +925,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
           float pc[16];
 #pragma unroll
           for (int v = 0; v < 16; ++v) pc[v] = pn[v];
-          load_p(t + 1);
+          load_p(next);
           float* pp = p0 + (int64_t)t * 128 * sj;
           if (mt.tall) {
             if (pcol) {
@@ -928,7 +937,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
                 const float xs[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
                 for (int z = 0; z < 4; ++z) pc[4 * v + z] = pc[4 * v + z] - step * xs[z] - dec * pc[4 * v + z];
-                store4(pp + v * 32 * sj, pc + 4 * v);
+                __stcs(reinterpret_cast<float4*>(pp + v * 32 * sj), *reinterpret_cast<const float4*>(pc + 4 * v));
               }
             }
           } else {
@@ -938,7 +947,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
             for (int v = 0; v < 16; ++v, pp += 4 * si) {
               if (4 * v >= k) continue;
               const float xv = *reinterpret_cast<const float*>(xrow + ((v ^ (prow & 15)) << 4));
-              *pp = pc[v] - step * xv - dec * pc[v];
+              __stcs(pp, pc[v] - step * xv - dec * pc[v]);
             }
           }
           publish();   // a spilled tile's room is the next one's
