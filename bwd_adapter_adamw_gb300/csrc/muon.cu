@@ -356,6 +356,19 @@ __device__ __forceinline__ void put_split8(uint8_t* hi, uint8_t* lo, int row, in
   *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// The same for the four values from column col of the split
+__device__ __forceinline__ void put_split4(uint8_t* hi, uint8_t* lo, int row, int col, const float* v) {
+  uint32_t h[2], l[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    h[q] = pack_bf16(v[2 * q], v[2 * q + 1]);
+    l[q] = pack_bf16(v[2 * q] - __uint_as_float(h[q] << 16), v[2 * q + 1] - __uint_as_float(h[q] & 0xFFFF0000u));
+  }
+  const int at = row * 128 + (((col >> 3) ^ (row & 7)) << 4) + (col & 4) * 2;
+  *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0], h[1]);
+  *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0], l[1]);
+}
+
 struct TcArgs {
   float* P;
   float* G;
@@ -543,10 +556,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       asm volatile("fence.proxy.async;" ::: "memory");
     };
     // The scratch tile of a pass's spilled tile is free: its user two spilled tiles earlier in the pass
-    // has been copied out and its Gram products are done. `newer`: the one between has begun its copy.
-    auto scratch_free = [&](int t, bool newer) {
-      if (newer) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-      else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    // has been copied out and its Gram products are done (the one between has not begun its copy).
+    auto scratch_free = [&](int t) {
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       wait0(&bar_used[(t - kTcTiles) & 1], ph_used[(t - kTcTiles) & 1]);
     };
     // the last one or two uses of the scratch tiles, at the end of a pass
@@ -571,44 +583,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       umma_commit(&bar_apply[buf]);
     };
 
-    // ---- momentum and u; unit: 8 rows of one column (tall) or of 32 columns, one per lane (wide);
-    // a thread's two units are loaded together
-    // (row, chunk) of this thread's units, and where they start in the first tile
-    int row[2], ch[2], live[2];   // live: how many of the 8 rows exist
-    int64_t at0[2];
+    // ---- momentum and u. A thread's part of a tile: four 16-byte vectors of the arena, 512 threads
+    // apart (tall: whole lines per request), or two units of 8 rows of a column, one column per lane
+    // (wide).
+    int row[2], ch[2], live[2];   // wide: column, chunk of 8 rows, how many of them exist
+    int64_t at0[2];               // wide: where the unit starts in the first tile
 #pragma unroll
     for (int un = 0; un < 2; ++un) {
-      if (mt.tall) {
-        row[un] = (un * kTcThreads + tid) >> 3;
-        ch[un] = tid & 7;
-      } else {
-        const int e = un * 16 + warp;   // 32 units of (chunk, 32 columns)
-        row[un] = (e & 3) * 32 + lane;
-        ch[un] = e >> 2;
-      }
+      const int e = un * 16 + warp;   // 32 units of (chunk, 32 columns)
+      row[un] = (e & 3) * 32 + lane;
+      ch[un] = e >> 2;
       live[un] = min(8, max(0, s - ch[un] * 8));
-      at0[un] = (first * 128 + row[un]) * sj + (int64_t)(ch[un] * 8) * si;
+      at0[un] = first * 128 + row[un] + (int64_t)(ch[un] * 8) * si;
     }
+    const int vrow = tid >> 4, vq = (tid & 15) * 4;   // tall: column vrow + 32 v, rows vq ..
+    const int64_t v0 = (first * 128 + vrow) * (int64_t)s + vq;
     const int left0 = (int)(mt.n - first * 128);   // columns from the first tile to the end
-    float gv[2][8], mv[2][8];
+    float gv[16], mv[16];
     auto load = [&](int t) {
+      if (mt.tall) {
+        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int un = 0; un < 2; ++un) {
-        const int k = t < nt && t * 128 + row[un] < left0 ? live[un] : 0;
-        const float* gp = g + at0[un] + (int64_t)t * 128 * sj;
-        const float* mp = m + at0[un] + (int64_t)t * 128 * sj;
-        if (mt.tall) {
-          const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int v = 0; v < 4; ++v) {
+          const bool in = t < nt && vq < s && t * 128 + vrow + 32 * v < left0;
+          const int64_t at = v0 + ((int64_t)t * 128 + 32 * v) * s;
+          *reinterpret_cast<float4*>(gv + 4 * v) = in ? __ldcs(reinterpret_cast<const float4*>(g + at)) : z;
+          *reinterpret_cast<float4*>(mv + 4 * v) = in ? __ldcs(reinterpret_cast<const float4*>(m + at)) : z;
+        }
+      } else {
 #pragma unroll
-          for (int q = 0; q < 8; q += 4) {
-            *reinterpret_cast<float4*>(gv[un] + q) = q < k ? __ldcs(reinterpret_cast<const float4*>(gp + q)) : z;
-            *reinterpret_cast<float4*>(mv[un] + q) = q < k ? __ldcs(reinterpret_cast<const float4*>(mp + q)) : z;
-          }
-        } else {
+        for (int un = 0; un < 2; ++un) {
+          const int k = t < nt && t * 128 + row[un] < left0 ? live[un] : 0;
+          const float* gp = g + at0[un] + (int64_t)t * 128;
+          const float* mp = m + at0[un] + (int64_t)t * 128;
 #pragma unroll
           for (int q = 0; q < 8; ++q, gp += si, mp += si) {
-            gv[un][q] = q < k ? __ldcs(gp) : 0.f;
-            mv[un][q] = q < k ? __ldcs(mp) : 0.f;
+            gv[un * 8 + q] = q < k ? __ldcs(gp) : 0.f;
+            mv[un * 8 + q] = q < k ? __ldcs(mp) : 0.f;
           }
         }
       }
@@ -634,39 +645,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       prefetch(tid < 256 ? g : m, t + kTcAhead, tid & 255);
       uint8_t* hi = place(t);
       uint8_t* lo = hi + 16 * 1024;
-      if (t >= kTcTiles + 2) {
-        if (tid == 0) scratch_free(t, true);
-        __syncthreads();
+      float w[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        mv[q] = fmaf(mu, mv[q], c * gv[q]);
+        w[q] = fmaf(mu_u, mv[q], c_u * gv[q]);
       }
-      float w[2][8];
+      if (mt.tall) {
 #pragma unroll
-      for (int un = 0; un < 2; ++un)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          mv[un][q] = fmaf(mu, mv[un][q], c * gv[un][q]);
-          w[un][q] = fmaf(mu_u, mv[un][q], c_u * gv[un][q]);
+        for (int v = 0; v < 4; ++v) {
+          if (vq >= s || t * 128 + vrow + 32 * v >= left0) continue;
+          const int64_t at = v0 + ((int64_t)t * 128 + 32 * v) * s;
+          __stcs(reinterpret_cast<float4*>(m + at), *reinterpret_cast<const float4*>(mv + 4 * v));
+          if (a.zero_grads) __stcs(reinterpret_cast<float4*>(g + at), make_float4(0.f, 0.f, 0.f, 0.f));
         }
+      } else {
 #pragma unroll
-      for (int un = 0; un < 2; ++un) {
-        const int k = t * 128 + row[un] < left0 ? live[un] : 0;
-        float* gp = g + at0[un] + (int64_t)t * 128 * sj;
-        float* mp = m + at0[un] + (int64_t)t * 128 * sj;
-        if (mt.tall) {
-#pragma unroll
-          for (int q = 0; q < 8; q += 4)
-            if (q < k) __stcs(reinterpret_cast<float4*>(mp + q), *reinterpret_cast<const float4*>(mv[un] + q));
-        } else {
+        for (int un = 0; un < 2; ++un) {
+          const int k = t * 128 + row[un] < left0 ? live[un] : 0;
+          float* mp = m + at0[un] + (int64_t)t * 128;
 #pragma unroll
           for (int q = 0; q < 8; ++q, mp += si)
-            if (q < k) __stcs(mp, mv[un][q]);
-        }
-        if (a.zero_grads) {
-          for (int q = 0; q < k; ++q, gp += si) *gp = 0.f;
+            if (q < k) __stcs(mp, mv[un * 8 + q]);
+          if (a.zero_grads) {
+            float* gp = g + at0[un] + (int64_t)t * 128;
+            for (int q = 0; q < k; ++q, gp += si) *gp = 0.f;
+          }
         }
       }
       load(t + 1);   // on its way while this tile is split and stored
+      if (mt.tall) {
 #pragma unroll
-      for (int un = 0; un < 2; ++un) put_split8(hi, lo, row[un], ch[un], w[un]);
+        for (int v = 0; v < 4; ++v) put_split4(hi, lo, vrow + 32 * v, vq, w + 4 * v);
+      } else {
+#pragma unroll
+        for (int un = 0; un < 2; ++un) put_split8(hi, lo, row[un], ch[un], w + 8 * un);
+      }
+      // the next tile's room, checked while this tile is finished; publish tells the other threads
+      if (tid == 0 && t + 1 < nt && t + 1 >= kTcTiles + 2) scratch_free(t + 1);
       publish();
       if (tid == 0) {
         gram_mma(hi, t == 0);
@@ -880,7 +896,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
             end_fetch(t);
             apply_mma(tile, buf);
             if (next < nt && next >= kTcTiles) {   // over the spilled tile before this one
-              if (!last && (backwards ? nt - 1 - t : t - kTcTiles) >= 1) scratch_free(next, false);
+              if (!last && (backwards ? nt - 1 - t : t - kTcTiles) >= 1) scratch_free(next);
               begin_fetch(next);
             }
           }
