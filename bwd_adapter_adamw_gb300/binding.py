@@ -212,10 +212,24 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_torch_C = None
+
+
+def _current_stream() -> int:
+    """Handle of torch's current stream on the current device. The raw getter costs 0.1 us a call,
+    torch.cuda.current_stream() 2.9 us, which the smallest calls would wait for."""
+    global _torch_C
+    if _torch_C is None:
+        import torch
+        if not torch.cuda.is_initialized() or not hasattr(torch._C, "_cuda_getCurrentRawStream"):
+            return torch.cuda.current_stream().cuda_stream
+        _torch_C = torch._C
+    return _torch_C._cuda_getCurrentRawStream(_torch_C._cuda_getDevice())
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

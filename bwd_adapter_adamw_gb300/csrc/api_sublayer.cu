@@ -75,7 +75,8 @@ int check_mats(int32_t n_mats, const lora_mat* mats, const GroupTab* groups) {
 }
 
 // The matrices in the order of their launches: by kernel (smaller side at most 16, each of its own,
-// or above), cluster size, and falling length; a launch takes a run of equal keys.
+// or above) and falling length. A launch takes a run of equal keys; the cluster size is the largest
+// that one of the kernel's matrices asks for, so that the matrices of a call share one launch.
 struct MuonOrder {
   int32_t at;      // index into the caller's table
   int32_t key;     // cluster size and smaller side (0: above 16)
@@ -84,6 +85,7 @@ struct MuonOrder {
 
 std::vector<MuonOrder> muon_order(int32_t n_mats, const lora_mat* mats) {
   std::vector<MuonOrder> v(n_mats);
+  int cluster[17] = {};
   for (int32_t i = 0; i < n_mats; ++i) {
     const lora_mat& e = mats[i];
     MuonMat& t = v[i].m;
@@ -94,8 +96,10 @@ std::vector<MuonOrder> muon_order(int32_t n_mats, const lora_mat* mats) {
     t.n = std::max(e.rows, e.cols);
     t.group = e.group;
     v[i].at = i;
-    v[i].key = muon_cluster(t, n_mats) * 32 + (t.s <= 16 ? t.s : 0);
+    v[i].key = t.s <= 16 ? t.s : 0;
+    cluster[v[i].key] = std::max(cluster[v[i].key], muon_cluster(t, n_mats));
   }
+  for (MuonOrder& e : v) e.key += 32 * cluster[e.key];
   std::stable_sort(v.begin(), v.end(), [](const MuonOrder& a, const MuonOrder& b) {
     return a.key != b.key ? a.key < b.key : a.m.n > b.m.n;
   });
@@ -133,11 +137,8 @@ int lora_block_product(int64_t T, int64_t out_dim, int64_t in_dim, const void* X
   a.T = T; a.out_dim = out_dim; a.in_dim = in_dim;
   a.W8 = W8; a.sw = sw; a.transposed = transposed != 0; a.Y = Y;
   a.codes = w.codes; a.scales = w.scales; a.ld_scales = block_scales_ld(T);
-  const cudaStream_t st = (cudaStream_t)stream;
-  LORA_TRY(launch_block_quant(X, T, transposed ? out_dim : in_dim, w.codes, w.scales, 1,
-                              a.ld_scales, st));
-  LORA_TRY(launch_block_gemm(a, st, 0));
-  return LORA_OK;
+  a.X = X;
+  return cuda_status(launch_block_product(a, (cudaStream_t)stream, 0));
 }
 
 int lora_block_quantize_weight(const void* W, int64_t out_dim, int64_t in_dim, uint8_t* W8,

@@ -17,6 +17,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "block_e4m3.cuh"
 #include "tc_ptx.cuh"
 
 namespace lora {
@@ -470,46 +471,61 @@ cudaError_t run_tile(const BlockProductArgs& a, cudaStream_t st, int prof_kind) 
 // accumulators), 4 TMA, 5 TMEM allocation and MMA. Split s of S takes an even share of the
 // K-blocks; the S partial tiles meet in distributed shared memory, each CTA adding an S-th of the
 // tile in split order, so that reruns are bitwise equal.
+//
+// The weight's bytes bound it, so it wants every SM to stream all the time: short shares (at least
+// two K-blocks) in several small CTAs per SM, all resident at once.
+//
+// FUSED (a few tokens): the epilogue warps quantise the CTA's share of X themselves while the
+// weight is on its way, and the call is one launch.
 constexpr int kStreamThreads = 192;
+constexpr int kFusedTokens = 8;    // tokens of the fused form
+constexpr int kFusedBlocks = 8;    // K-blocks of a CTA's share in it
 
-template <int NT>
+template <int NT, bool FUSED>
 struct StreamCfg {
-  static constexpr int kStageBytes = kTileBytes + NT * 128;
-  static constexpr int kScaleBytes = NT * 4;
+  static constexpr int kXTile = NT * 128;
+  static constexpr int kStageBytes = kTileBytes + (FUSED ? 0 : kXTile);
+  static constexpr int kScaleBytes = FUSED ? 0 : NT * 4;
+  static constexpr int kXBytes = FUSED ? kFusedBlocks * (kXTile + NT * 4) : 0;   // the share of X
   static constexpr int kTileF32 = 128 * NT * 4;   // the partial tile, over the drained stages
-  static constexpr int kStages = (100 * 1024) / kStageBytes;
-  static constexpr int kSmem = kStages * (kStageBytes + kScaleBytes) + 512 + 1024;
+  static constexpr int kPerSm = FUSED ? 3 : NT == 16 ? 4 : NT == 32 ? 3 : 2;
+  static constexpr int kStages = NT == 64 ? 4 : 3;
+  static constexpr int kSmem = kStages * (kStageBytes + kScaleBytes) + kXBytes + 512 + 1024;
   static constexpr uint32_t kCols = 2 * NT < 32 ? 32 : 2 * NT;
   static_assert(kTileF32 <= kStages * kStageBytes, "partial tile fits the stages");
-  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024 && kPerSm * kCols <= 512, "CTAs per SM");
 };
 
 struct StreamParams {
   CUtensorMap tw;     // W8 [out, in], box {128, 128}
   CUtensorMap tx;     // codes [T, K], box {128, NT}
+  const __nv_bfloat16* X;   // fused: [T, K]
   const float* sx;
   const float* sw;
   int64_t ld_sx, sw_n, sw_k;
-  int64_t T, N;
+  int64_t T, N, K;
   int32_t nk, splits;
   __nv_bfloat16* Y;
   uint32_t* err;
   unsigned long long wait_limit;
 };
 
-template <int NT, bool TR>
-__global__ void __launch_bounds__(kStreamThreads, 2) k_block_stream(const __grid_constant__ StreamParams p) {
-  using C = StreamCfg<NT>;
+template <int NT, bool TR, bool FUSED>
+__global__ void __launch_bounds__(kStreamThreads, StreamCfg<NT, FUSED>::kPerSm)
+    k_block_stream(const __grid_constant__ StreamParams p) {
+  using C = StreamCfg<NT, FUSED>;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* scales = reinterpret_cast<float*>(base + kStages * C::kStageBytes);
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(scales + kStages * NT);
+  uint8_t* xtiles = base + kStages * C::kStageBytes;                       // fused: [block][NT][128]
+  float* scales = reinterpret_cast<float*>(xtiles + (FUSED ? kFusedBlocks * C::kXTile : 0));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(scales + (FUSED ? kFusedBlocks : kStages) * NT);
   uint64_t* empty_bar = full_bar + kStages;   // MMA and epilogue have read the stage
   uint64_t* acc_full = empty_bar + kStages;   // [2]
   uint64_t* acc_empty = acc_full + 2;         // [2]
   uint64_t* mma_done = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint64_t* x_ready = mma_done + 1;           // fused: the share of X is quantised
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(x_ready + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = (int)blockIdx.x % p.splits, nt = (int)blockIdx.x / p.splits;
   const int kb0 = (int)((int64_t)p.nk * split / p.splits);
@@ -520,13 +536,14 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_block_stream(const __grid
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full_bar[s], 1);
-      mbar_init(&empty_bar[s], 1 + 4);
+      mbar_init(&empty_bar[s], FUSED ? 1 : 1 + 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 4);
     }
     mbar_init(mma_done, 1);
+    mbar_init(x_ready, 128);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -535,13 +552,14 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_block_stream(const __grid
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (FUSED) grid_dep_sync();   // X and the weight may come from the kernel before this one
 
   uint64_t acc[NT / 2];
   if (warp == 4) {
     if (lane == 0) {
-      // The weight does not depend on the kernel before this one (the quantisation of X, which
-      // itself waited for everything earlier), so the first stages' weight tiles are on their way
-      // before that kernel has finished.
+      // Not fused: the weight does not depend on the kernel before this one (the quantisation of X,
+      // which itself waited for everything earlier), so the first stages' weight tiles are on their
+      // way before that kernel has finished.
       auto load_w = [&](int i) {
         const int s = i % kStages;
         mbar_expect_tx(&full_bar[s], C::kStageBytes + C::kScaleBytes);
@@ -549,17 +567,19 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_block_stream(const __grid
         tma_load_2d(base + s * C::kStageBytes, &p.tw, &full_bar[s], TR ? n0 : k0, TR ? k0 : n0);
       };
       auto load_x = [&](int i) {
-        const int s = i % kStages;
-        tma_load_2d(base + s * C::kStageBytes + kTileBytes, &p.tx, &full_bar[s], (kb0 + i) * kBlk, t0);
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                smem_u32(scales + s * NT)),
-            "l"(p.sx + (int64_t)(kb0 + i) * p.ld_sx + t0), "r"(C::kScaleBytes), "r"(smem_u32(&full_bar[s]))
-            : "memory");
+        if constexpr (!FUSED) {
+          const int s = i % kStages;
+          tma_load_2d(base + s * C::kStageBytes + kTileBytes, &p.tx, &full_bar[s], (kb0 + i) * kBlk, t0);
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                  smem_u32(scales + s * NT)),
+              "l"(p.sx + (int64_t)(kb0 + i) * p.ld_sx + t0), "r"(C::kScaleBytes), "r"(smem_u32(&full_bar[s]))
+              : "memory");
+        }
       };
       const int ahead = nk < kStages ? nk : kStages;
       for (int i = 0; i < ahead; ++i) load_w(i);
-      grid_dep_sync();
+      if constexpr (!FUSED) grid_dep_sync();
       int i = 0;
       for (; i < ahead; ++i) load_x(i);
       for (; i < nk; ++i) {
@@ -575,14 +595,15 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_block_stream(const __grid
   } else if (warp == 5) {
     if (lane == 0) {
       constexpr uint32_t id8 = idesc(kFmtE4M3, 128, NT, TR, false);
-      for (int i = 0; i < nk; ++i) {
+      bool ok = !FUSED || mbar_wait_for(x_ready, 0u, 2u, p.err, p.wait_limit);
+      for (int i = 0; i < nk && ok; ++i) {
         const int b = i & 1, s = i % kStages;
         if (i >= 2 && !mbar_wait_for(&acc_empty[b], (uint32_t)((i >> 1) - 1) & 1u, 2u, p.err, p.wait_limit)) break;
         if (!mbar_wait_for(&full_bar[s], (uint32_t)(i / kStages) & 1u, 2u, p.err, p.wait_limit)) break;
         fence_after();
         const uint32_t sw = smem_u32(base + s * C::kStageBytes);
         const uint64_t da = TR ? smem_desc_sw128_mn(sw, kTileBytes) : smem_desc_sw128(sw);
-        const uint64_t db = smem_desc_sw128(sw + kTileBytes);
+        const uint64_t db = smem_desc_sw128(FUSED ? smem_u32(xtiles + i * C::kXTile) : sw + kTileBytes);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           umma_f8(tmem + (uint32_t)(b * NT), da + (TR ? 256 : 2) * k, db + 2 * k, id8, k > 0 ? 1u : 0u);
@@ -593,21 +614,56 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_block_stream(const __grid
       mbar_wait(mma_done, 0u, 2u, p.err);
     }
   } else {
+    if constexpr (FUSED) {
+      // Half-warp per (block, token), four in flight; rows past T keep what they hold (their outputs
+      // are not stored).
+      const int sub = threadIdx.x & 15, T = (int)p.T, units = nk * T;
+      for (int u0 = threadIdx.x >> 4; u0 < units; u0 += 32) {
+        uint4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int u = u0 + q * 8, i = u / T, t = u - i * T;
+          const int64_t col = (int64_t)(kb0 + i) * kBlk + sub * 8;
+          v[q] = u < units && col < p.K ? __ldg(reinterpret_cast<const uint4*>(p.X + t * p.K + col))
+                                        : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int u = u0 + q * 8, i = u / T, t = u - i * T;
+          float m = amax8(v[q]);
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFu << (threadIdx.x & 16), m, o));
+          if (u >= units) break;
+          float rcp, sc;
+          block_scales(m, rcp, sc);
+          if (sub == 0) scales[i * NT + t] = sc;
+          *reinterpret_cast<uint2*>(xtiles + i * C::kXTile + t * 128 + (((sub >> 1) ^ (t & 7)) << 4) + (sub & 1) * 8) =
+              encode8(v[q], rcp);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(x_ready);
+    }
 #pragma unroll
     for (int c = 0; c < NT / 2; ++c) acc[c] = 0;
     const float* sw = p.sw + (int64_t)nt * p.sw_n + (int64_t)kb0 * p.sw_k;
     float w_next = nk > 0 ? __ldg(sw) : 0.f;
-    constexpr int CH = NT == 32 || NT == 64 ? 32 : 16;   // columns in flight beside the accumulators
+    constexpr int CH = NT < 32 ? NT : 32;   // columns in flight beside the accumulators
     for (int i = 0; i < nk; ++i) {
       const int b = i & 1, s = i % kStages;
       const float w = w_next;
       if (i + 1 < nk) w_next = __ldg(sw + (int64_t)(i + 1) * p.sw_k);
-      // the stage's scales (its full barrier) and the block's sums
-      const bool ready = mbar_wait_for(&full_bar[s], (uint32_t)(i / kStages) & 1u, 4u, p.err, p.wait_limit) &&
-                         mbar_wait_for(&acc_full[b], (uint32_t)(i >> 1) & 1u, 4u, p.err, p.wait_limit);
+      // the block's scales (its stage's barrier, or the quantisation) and its sums
+      bool ready;
+      if constexpr (FUSED) {
+        ready = i > 0 || mbar_wait_for(x_ready, 0u, 4u, p.err, p.wait_limit);
+      } else {
+        ready = mbar_wait_for(&full_bar[s], (uint32_t)(i / kStages) & 1u, 4u, p.err, p.wait_limit);
+      }
+      ready = ready && mbar_wait_for(&acc_full[b], (uint32_t)(i >> 1) & 1u, 4u, p.err, p.wait_limit);
       if (!__all_sync(0xffffffffu, ready)) break;
       fence_after();
-      const float4* sc = reinterpret_cast<const float4*>(scales + s * NT);
+      const float4* sc = reinterpret_cast<const float4*>(scales + (FUSED ? i : s) * NT);
 #pragma unroll
       for (int c = 0; c < NT / CH; ++c) {
         uint32_t r[CH];
@@ -625,7 +681,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_block_stream(const __grid
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&acc_empty[b]);
-        mbar_arrive(&empty_bar[s]);
+        if constexpr (!FUSED) mbar_arrive(&empty_bar[s]);
       }
     }
   }
@@ -644,11 +700,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_block_stream(const __grid
   __syncwarp();
   if (p.splits > 1) cluster_sync_all();
   else __syncthreads();
-  const int share = 128 * NT / p.splits;   // floats of the tile that this CTA adds up
-  for (int e = threadIdx.x * 4; e < share; e += kStreamThreads * 4) {
-    const int at = split * share + e;
+  // vectors of four outputs of one token; this CTA adds an S-th of the tokens' ones
+  const int rows = (int)(p.T - t0 < NT ? p.T - t0 : NT), vecs = rows * 32;
+  for (int e = split * kStreamThreads + threadIdx.x; e < vecs; e += p.splits * kStreamThreads) {
+    const int at = e * 4;
     const int64_t t = t0 + at / 128, n = n0 + at % 128;
-    if (t >= p.T || n >= p.N) continue;
+    if (n >= p.N) continue;
     float4 v;
     if (p.splits > 1) {
       v = dsmem_ld4(part + at, 0);
@@ -670,64 +727,82 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_block_stream(const __grid
   }
 }
 
-template <int NT, bool TR>
+// Shares per output tile: as many as keep all CTAs resident at once, at least two K-blocks each and
+// at most ten (us with 2 / 5 / 8 / 10 / 16 shares: 37 tokens 9728 -> 2560 20.5 / 12.6 / 12.7 / 12.2 /
+// 17.6; 1 token 2560 -> 1024 7.5 / 5.5 / 5.4 / 4.8 / 4.8; 1 token 4096 -> 14336 14.0 / 13.2 / 16.5 /
+// 16.9 / 26.3, where more than five are not resident together).
+int stream_splits(int64_t tiles, int64_t nk, int per_sm) {
+  int64_t s = (int64_t)per_sm * sm_count() / tiles;
+  if (s > nk / 2) s = nk / 2;
+  if (s > 10) s = 10;
+  return s < 1 ? 1 : (int)s;
+}
+
+template <int NT, bool TR, bool FUSED>
 cudaError_t launch_stream(const BlockProductArgs& a, StreamParams& prm, cudaStream_t st) {
-  using C = StreamCfg<NT>;
+  using C = StreamCfg<NT, FUSED>;
   static bool attr = false;
   if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(k_block_stream<NT, TR>,
+    cudaError_t e = cudaFuncSetAttribute(k_block_stream<NT, TR, FUSED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_block_stream<NT, TR>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      e = cudaFuncSetAttribute(k_block_stream<NT, TR, FUSED>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     attr = true;
   }
-  const int64_t K = a.transposed ? a.out_dim : a.in_dim;
-  if (!make_map_2d(&prm.tx, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, a.T, K, 128, NT))
+  if (!FUSED && !make_map_2d(&prm.tx, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, prm.K, a.T, prm.K, 128, NT))
     return cudaErrorInvalidValue;
   const int64_t nt = (prm.N + 127) / 128, tt = (a.T + NT - 1) / NT;
-  // as many splits as two CTAs per SM hold, at least two K-blocks each
-  int splits = 1;
-  while (splits < 16 && nt * tt * splits * 2 <= 2 * sm_count() && splits * 4 <= prm.nk) splits *= 2;
-  prm.splits = splits;
+  prm.splits = stream_splits(nt * tt, prm.nk, C::kPerSm);
+  if (FUSED) {   // a share fits its room
+    const int least = (prm.nk + kFusedBlocks - 1) / kFusedBlocks;
+    if (prm.splits < least) prm.splits = least;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(nt * splits), (unsigned)tt);
+  cfg.gridDim = dim3((unsigned)(nt * prm.splits), (unsigned)tt);
   cfg.blockDim = dim3(kStreamThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)splits;
+  at[0].val.clusterDim.x = (unsigned)prm.splits;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = add_pdl_attr(at, 1);
-  return cudaLaunchKernelEx(&cfg, k_block_stream<NT, TR>, prm);
+  return cudaLaunchKernelEx(&cfg, k_block_stream<NT, TR, FUSED>, prm);
 }
 
-cudaError_t run_stream(const BlockProductArgs& a, cudaStream_t st, int prof_kind) {
+template <int NT, bool FUSED>
+cudaError_t launch_stream(const BlockProductArgs& a, StreamParams& prm, cudaStream_t st) {
+  return a.transposed ? launch_stream<NT, true, FUSED>(a, prm, st) : launch_stream<NT, false, FUSED>(a, prm, st);
+}
+
+cudaError_t run_stream(const BlockProductArgs& a, bool fused, cudaStream_t st, int prof_kind) {
   StreamParams prm;
   std::memset(&prm, 0, sizeof(prm));
   if (!make_map_2d(&prm.tw, a.W8, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.in_dim, a.out_dim, a.in_dim, 128, 128))
     return cudaErrorInvalidValue;
-  const int64_t K = a.transposed ? a.out_dim : a.in_dim;
   const int64_t ib = (a.in_dim + kBlk - 1) / kBlk;
+  prm.K = a.transposed ? a.out_dim : a.in_dim;
+  prm.X = static_cast<const __nv_bfloat16*>(a.X);
   prm.sx = a.scales; prm.ld_sx = a.ld_scales; prm.sw = a.sw;
   prm.sw_n = a.transposed ? 1 : ib;
   prm.sw_k = a.transposed ? ib : 1;
   prm.T = a.T;
   prm.N = a.transposed ? a.in_dim : a.out_dim;
-  prm.nk = (int32_t)((K + kBlk - 1) / kBlk);
+  prm.nk = (int32_t)((prm.K + kBlk - 1) / kBlk);
   prm.Y = static_cast<__nv_bfloat16*>(a.Y);
   prm.err = error_word();
   if (!prm.err || sm_count() <= 0) return cudaErrorInvalidDevice;
   prm.wait_limit = tc_wait_limit();
   prof_begin(prof_kind, st);
   cudaError_t e;
-  if (a.T <= 16) e = a.transposed ? launch_stream<16, true>(a, prm, st) : launch_stream<16, false>(a, prm, st);
-  else if (a.T <= 32) e = a.transposed ? launch_stream<32, true>(a, prm, st) : launch_stream<32, false>(a, prm, st);
-  else if (a.T <= 64) e = a.transposed ? launch_stream<64, true>(a, prm, st) : launch_stream<64, false>(a, prm, st);
-  else e = a.transposed ? launch_stream<128, true>(a, prm, st) : launch_stream<128, false>(a, prm, st);
+  if (fused) e = launch_stream<16, true>(a, prm, st);
+  else if (a.T <= 16) e = launch_stream<16, false>(a, prm, st);
+  else if (a.T <= 32) e = launch_stream<32, false>(a, prm, st);
+  else e = launch_stream<64, false>(a, prm, st);   // (two 64-token tiles beat one of 128, whose
+                                                   // accumulators do not fit the registers)
   if (e != cudaSuccess) return e;
   prof_end(prof_kind, st);
   return cudaGetLastError();
@@ -736,8 +811,19 @@ cudaError_t run_stream(const BlockProductArgs& a, cudaStream_t st, int prof_kind
 }  // namespace
 
 cudaError_t launch_block_gemm(const BlockProductArgs& a, cudaStream_t st, int prof_kind) {
-  if (a.T <= 128 && !a.p) return run_stream(a, st, prof_kind);
+  if (a.T <= 128 && !a.p) return run_stream(a, false, st, prof_kind);
   return run_tile(a, st, prof_kind);
+}
+
+cudaError_t launch_block_product(const BlockProductArgs& a, cudaStream_t st, int prof_kind) {
+  const int64_t K = a.transposed ? a.out_dim : a.in_dim;
+  // One launch for a few tokens and a weight that streams in a few microseconds (1 token: 2560 ->
+  // 1024 4.0 us against 4.8, 4096 -> 4096 6.5 against 7.8); a larger one gains more from its loads
+  // starting ahead of the quantisation (4096 -> 14336 15.5 against 13.2).
+  if (a.T <= kFusedTokens && !a.p && K <= 10 * kFusedBlocks * kBlk && a.in_dim * a.out_dim <= (32 << 20))
+    return run_stream(a, true, st, prof_kind);
+  cudaError_t e = launch_block_quant(a.X, a.T, K, a.codes, a.scales, 1, a.ld_scales, st);
+  return e != cudaSuccess ? e : launch_block_gemm(a, st, prof_kind);
 }
 
 }  // namespace lora

@@ -392,9 +392,10 @@ cudaError_t launch_block_quant_weight(const void* W, int64_t rows, int64_t cols,
 
 // ---- gemm_block.cu: frozen product over them ----
 struct BlockProductArgs {
-  const uint8_t* codes;      // [T, K] E4M3 codes of the activations; K = in_dim, or out_dim when
+  const void* X;             // [T, K] bf16 (launch_block_product)
+  uint8_t* codes;      // [T, K] E4M3 codes of the activations; K = in_dim, or out_dim when
                              //   transposed
-  const float* scales;       // [ceil(K / 128), ld_scales], block (t, kb) at kb * ld_scales + t
+  float* scales;             // [ceil(K / 128), ld_scales], block (t, kb) at kb * ld_scales + t
   int64_t ld_scales;         // block_scales_ld(T)
   int64_t T, out_dim, in_dim;
   const uint8_t* W8;         // [out_dim, in_dim] E4M3 codes
@@ -412,6 +413,9 @@ struct BlockProductArgs {
 // aligned run (the entries past T are never used).
 inline int64_t block_scales_ld(int64_t T) { return (T + 127) / 128 * 128; }
 cudaError_t launch_block_gemm(const BlockProductArgs& a, cudaStream_t st, int prof_kind);
+// the product from X itself: its quantisation (into codes and scales where the form needs them) and
+// the product
+cudaError_t launch_block_product(const BlockProductArgs& a, cudaStream_t st, int prof_kind);
 
 // ---- norm.cu ----
 struct NormArgs {

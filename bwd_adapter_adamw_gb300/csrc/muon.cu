@@ -132,8 +132,7 @@ __global__ void __launch_bounds__(kMuonThreads) k_muon_simt(float* __restrict__ 
     auto make_u = [&](float gv, float mv) {   // mv: the new momentum
       return hp.nesterov ? fmaf(mu, mv, c * gv) : mv;
     };
-    // momentum, u and its largest magnitude
-    float mx = 0.f;
+    // momentum and u
     const int units = cols * S4;
     for (int e0 = tid; e0 < units; e0 += 4 * kMuonThreads) {
       float4 gv[4], mv[4];
@@ -161,7 +160,6 @@ __global__ void __launch_bounds__(kMuonThreads) k_muon_simt(float* __restrict__ 
         for (int q = 0; q < 4; ++q) {
           b[q] = fmaf(mu, b[q], c * a[q]);
           w[q] = make_u(a[q], b[q]);
-          mx = fmaxf(mx, fabsf(w[q]));
         }
         *reinterpret_cast<float4*>(m + at) = mv[v];
         if (mt.tall) {
@@ -173,15 +171,11 @@ __global__ void __launch_bounds__(kMuonThreads) k_muon_simt(float* __restrict__ 
         }
       }
     }
-    const float pre = range_scale<kMuonThreads>(mx, sh, C);
-    if (tid < S * S) qt[tid] = tid / S == tid % S ? pre : 0.f;
-    if (pre != 1.f)
-      for (int e = tid; e < held * S; e += kMuonThreads) u[e / S * SP + e % S] *= pre;
+    if (tid < S * S) qt[tid] = tid / S == tid % S ? 1.f : 0.f;
     __syncthreads();
-    for (int done = 0; done < hp.steps;) {
-      const int left = hp.steps - done;
-      const int now = left % kStageSteps ? left % kStageSteps : kStageSteps;
-      // Gram matrix: a thread adds a 4 x 4 block over its group's columns
+    // G, summed over the cluster, in g0
+    auto gram = [&]() {
+      // a thread adds a 4 x 4 block over its group's columns
       {
         float acc[4][4] = {};
         const int b = tid % F::kLanes, grp = tid / F::kLanes;
@@ -241,11 +235,37 @@ __global__ void __launch_bounds__(kMuonThreads) k_muon_simt(float* __restrict__ 
       }
       if (tid < S * S) g0[tid] = d;
       __syncthreads();
+    };
+    for (int done = 0; done < hp.steps;) {
+      const int left = hp.steps - done;
+      const int now = left % kStageSteps ? left % kStageSteps : kStageSteps;
+      gram();
       float inv = 1.f;
       if (done == 0) {   // X = u / ||u||, ||u||^2 = trace G
-        float tr = 0.f;
+        auto trace = [&]() {
+          float tr = 0.f;
 #pragma unroll
-        for (int i = 0; i < S; ++i) tr += g0[i * S + i];
+          for (int i = 0; i < S; ++i) tr += g0[i * S + i];
+          return tr;
+        };
+        float tr = trace();
+        if (!(tr > 1e-18f && tr < 1e30f)) {
+          // the squares may have left the fp32 range (or u is zero): scale u by a power of two that
+          // brings its largest magnitude to about one, and sum again
+          float mx = 0.f;
+          for (int e = tid; e < cols * S; e += kMuonThreads) {
+            const int j = e / S, i = e % S;
+            mx = fmaxf(mx, fabsf(j < held ? u[j * SP + i] : make_u(g[i * si + j * sj], m[i * si + j * sj])));
+          }
+          const float pre = range_scale<kMuonThreads>(mx, sh, C);
+          if (pre != 1.f) {
+            for (int e = tid; e < held * S; e += kMuonThreads) u[e / S * SP + e % S] *= pre;
+            if (tid < S * S) qt[tid] *= pre;
+            __syncthreads();
+            gram();
+            tr = trace();
+          }
+        }
         inv = tr > 0.f ? 1.f / sqrtf(tr) : 0.f;
         __syncthreads();
         if (tid < S * S) g0[tid] *= inv * inv;
@@ -267,20 +287,23 @@ __global__ void __launch_bounds__(kMuonThreads) k_muon_simt(float* __restrict__ 
       if (cols > held) simt_mm<S4>(qt, qs, qt);
       // X <- Q X on the held columns
       for (int j = tid; j < held; j += kMuonThreads) {
-        float x[S], y[S];
+        float x[S];
 #pragma unroll
         for (int i = 0; i < S; i += 4) *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(u + j * SP + i);
+#pragma unroll 1   // (all of Q at once does not fit the registers)
+        for (int i = 0; i < S; i += 4) {
+          float y[4];
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-          y[i] = 0.f;
+          for (int q = 0; q < 4; ++q) {
+            y[q] = 0.f;
 #pragma unroll
-          for (int k = 0; k < S; k += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(qs + i * S + k);
-            y[i] = fmaf(w.x, x[k], fmaf(w.y, x[k + 1], fmaf(w.z, x[k + 2], fmaf(w.w, x[k + 3], y[i]))));
+            for (int k = 0; k < S; k += 4) {
+              const float4 w = *reinterpret_cast<const float4*>(qs + (i + q) * S + k);
+              y[q] = fmaf(w.x, x[k], fmaf(w.y, x[k + 1], fmaf(w.z, x[k + 2], fmaf(w.w, x[k + 3], y[q]))));
+            }
           }
+          *reinterpret_cast<float4*>(u + j * SP + i) = make_float4(y[0], y[1], y[2], y[3]);
         }
-#pragma unroll
-        for (int i = 0; i < S; i += 4) *reinterpret_cast<float4*>(u + j * SP + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
       }
       __syncthreads();
     }
