@@ -7,7 +7,7 @@
 //
 // Both passes are bound by memory: a row is read once, held in registers between its sums and its
 // outputs, and written once.
-#include "lora_kernels.h"
+#include "tc_ptx.cuh"
 
 namespace lora {
 
@@ -143,62 +143,109 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_fwd(const E* __restrict__
   }
 }
 
-constexpr int kBwdThreads = 512;
+constexpr int kBwdRing = 8;   // most groups of rows in flight
 
-// TPR threads per row, NV vectors per thread, kBwdThreads / TPR rows at a time; persistent over
-// the rows, so that a thread keeps its columns and sums their gradients in registers. The next
-// rows are loaded ahead of the current rows' sums. Partials go to part[CTA][2][dim], added up in
-// order by k_norm_reduce.
-template <typename E, int TPR, int NV>
-__global__ void __launch_bounds__(kBwdThreads, NV == 1 ? 2 : 1)
+// Groups of rows in flight per CTA: two CTAs of 256 threads per SM, or one of 512.
+int bwd_ring(int64_t group_bytes, int threads) {
+  const int64_t room = (threads == 256 ? 96 : 200) * 1024;
+  const int64_t n = room / (2 * group_bytes);
+  return (int)(n < 1 ? 1 : n > kBwdRing ? kBwdRing : n);
+}
+
+// TPR threads per row, NV vectors per thread, TH / TPR rows at a time; persistent over
+// the rows, so that a thread keeps its columns and sums their gradients in registers. Groups of
+// rows of X and dY arrive in a ring of shared-memory buffers by bulk copies issued `ring` groups
+// ahead: loading the next group into registers instead kept 32 KB in flight per SM and ran at
+// 2.8 TB/s (8192 x 4096 bf16, 72 us). The barrier of a row's sums also frees its buffer. Partials
+// go to part[CTA][2][dim], added up in order by k_norm_reduce.
+//
+// A thread takes 16 columns where the row allows: a row's fixed cost (the wait, the sums' shuffles
+// and barrier) was as large as its arithmetic with 8 (8192 x 4096 bf16: 51 us with 512 threads per
+// row, MEASURE with 256).
+template <typename E, int TH, int TPR, int NV>
+__global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
     k_norm_bwd(const E* __restrict__ X, const float* __restrict__ gamma, const E* __restrict__ dY,
                const float2* __restrict__ stats, const E* dX_add, E* dX, float* __restrict__ part,
-               int64_t T, int dim, float inv_dim, int rms, int want) {
+               int64_t T, int dim, float inv_dim, int rms, int want, int ring, uint32_t* err) {
   grid_dep_sync();
   constexpr int N = Pack<E>::N;
-  constexpr int RPB = kBwdThreads / TPR;
+  constexpr int RPB = TH / TPR;
   constexpr int WPR = TPR / 32;
-  __shared__ float2 sh[2][kBwdThreads / 32];
-  __shared__ float comb[RPB > 1 ? kBwdThreads * NV * N : 1];
+  extern __shared__ __align__(16) uint8_t bufs[];   // [ring][X | dY][RPB][dim]; then the column sums
+  __shared__ float2 sh[2][TH / 32];
+  __shared__ uint64_t full[kBwdRing];
   const int row = threadIdx.x / TPR, col = threadIdx.x % TPR;
   const int warp = threadIdx.x >> 5;
   const int nvec = dim / N;
-  float dg[NV * N], db[NV * N];
-#pragma unroll
-  for (int j = 0; j < NV * N; ++j) dg[j] = db[j] = 0.f;
-  uint4 xv[NV], yv[NV];
-  float2 st = make_float2(0.f, 0.f);
+  const int group = RPB * dim * (int)sizeof(E);
   const int64_t step = (int64_t)gridDim.x * RPB;
   const int64_t t_first = (int64_t)blockIdx.x * RPB;
-  auto load = [&](int64_t t) {
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int i = col + u * TPR;
-      const bool in = t < T && i < nvec;
-      xv[u] = in ? __ldcs(reinterpret_cast<const uint4*>(X + t * dim) + i) : make_uint4(0, 0, 0, 0);
-      yv[u] = in ? __ldcs(reinterpret_cast<const uint4*>(dY + t * dim) + i) : make_uint4(0, 0, 0, 0);
-    }
-    st = t < T ? __ldg(stats + t) : make_float2(0.f, 0.f);
+  auto fill = [&](int s, int64_t t0) {   // thread 0: rows t0 .. of the group, as far as they exist
+    if (t0 >= T) return;
+    const int64_t rows = T - t0 < RPB ? T - t0 : RPB;
+    const uint32_t bytes = (uint32_t)(rows * dim * (int64_t)sizeof(E));
+    tc::mbar_expect_tx(&full[s], 2 * bytes);
+    for (int k = 0; k < 2; ++k)
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+              tc::smem_u32(bufs + (size_t)(2 * s + k) * group)),
+          "l"((k ? dY : X) + t0 * dim), "r"(bytes), "r"(tc::smem_u32(&full[s]))
+          : "memory");
   };
-  load(t_first + row);
-  int buf = 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ring; ++s) tc::mbar_init(&full[s], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    for (int s = 0; s < ring; ++s) fill(s, t_first + s * step);
+  }
+  // with few columns per thread the weights, and a row's g and xhat, stay in registers
+  constexpr bool kKeep = NV * N <= 16;
+  float dg[NV * N], db[NV * N], gw[kKeep ? NV * N : 1];
+#pragma unroll
+  for (int j = 0; j < NV * N; ++j) dg[j] = db[j] = 0.f;
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int j = 0; j < NV * N; j += 4) {
+      const int i = col + j / N * TPR;
+      if (i < nvec) load16(gamma + i * N + j % N, gw + j);
+    }
+  }
+  auto weights = [&](int u, int i, float (&ga)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ga[j + q] = gw[u * N + j + q];
+      } else {
+        load16(gamma + i * N + j, ga + j);
+      }
+    }
+  };
+  __syncthreads();   // the barriers are set up
+  int buf = 0, s = 0;
+  uint32_t phase = 0;
+  bool ok = true;
   for (int64_t t0 = t_first; t0 < T; t0 += step, buf ^= 1) {
     const int64_t t = t0 + row;
+    const bool live = t < T;
+    const float2 sc = live ? __ldg(stats + t) : make_float2(0.f, 0.f);
+    ok = ok && tc::mbar_wait(&full[s], phase, 1u, err);
+    const uint4* px = reinterpret_cast<const uint4*>(bufs + (size_t)(2 * s) * group) + row * nvec;
+    const uint4* py = reinterpret_cast<const uint4*>(bufs + (size_t)(2 * s + 1) * group) + row * nvec;
     uint4 xc[NV], yc[NV];
-    const float2 sc = st;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) { xc[u] = xv[u]; yc[u] = yv[u]; }
-    if (t0 + step < T) load(t + step);
+    float hk[kKeep ? NV * N : 1], gk[kKeep ? NV * N : 1];
     float s1 = 0.f, s2 = 0.f;   // sum g, sum g xhat
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int i = col + u * TPR;
+      const bool in = live && i < nvec;
+      xc[u] = in ? px[i] : make_uint4(0, 0, 0, 0);
+      yc[u] = in ? py[i] : make_uint4(0, 0, 0, 0);
       if (i >= nvec) continue;
       float x[N], y[N], ga[N];
       Pack<E>::get(xc[u], x);
       Pack<E>::get(yc[u], y);
-#pragma unroll
-      for (int j = 0; j < N; j += 4) load16(gamma + i * N + j, ga + j);
+      weights(u, i, ga);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float h = (x[j] - sc.x) * sc.y;
@@ -207,63 +254,82 @@ __global__ void __launch_bounds__(kBwdThreads, NV == 1 ? 2 : 1)
         s2 = fmaf(g, h, s2);
         dg[u * N + j] = fmaf(y[j], h, dg[u * N + j]);
         db[u * N + j] += y[j];
+        if constexpr (kKeep) {
+          hk[u * N + j] = h;
+          gk[u * N + j] = g;
+        }
       }
     }
-    if (!(want & 1)) continue;   // no dX: the rows' sums are not needed
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if constexpr (WPR > 1) {
+    if (want & 1) {
+      s1 = warp_sum(s1);
+      s2 = warp_sum(s2);
       if ((threadIdx.x & 31) == 0) sh[buf][warp] = make_float2(s1, s2);
-      __syncthreads();
-      const int w0 = warp / WPR * WPR;
-      s1 = s2 = 0.f;
+    }
+    __syncthreads();   // the sums are in place, and every thread has read the buffer
+    if (threadIdx.x == 0) fill(s, t0 + ring * step);
+    if (++s == ring) {
+      s = 0;
+      phase ^= 1u;
+    }
+    if (!(want & 1)) continue;
+    if constexpr (WPR > 1) {   // lane w adds warp w's share, the lanes in a fixed tree
+      const float2 v = sh[buf][warp / WPR * WPR + (threadIdx.x & (WPR - 1))];
+      s1 = v.x;
+      s2 = v.y;
 #pragma unroll
-      for (int w = 0; w < WPR; ++w) {
-        s1 += sh[buf][w0 + w].x;
-        s2 += sh[buf][w0 + w].y;
+      for (int o = WPR / 2; o > 0; o >>= 1) {
+        s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+        s2 += __shfl_xor_sync(0xffffffffu, s2, o);
       }
     }
-    if (t >= T) continue;
-    s1 = rms ? 0.f : s1 * inv_dim;
-    s2 *= inv_dim;
+    if (!live) continue;
+    const float c1 = rms ? 0.f : s1 * inv_dim * sc.y, c2 = s2 * inv_dim * sc.y;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int i = col + u * TPR;
       if (i >= nvec) continue;
       float x[N], y[N], ga[N], add[N];
-      Pack<E>::get(xc[u], x);
-      Pack<E>::get(yc[u], y);
-#pragma unroll
-      for (int j = 0; j < N; j += 4) load16(gamma + i * N + j, ga + j);
+      if constexpr (!kKeep) {
+        Pack<E>::get(xc[u], x);
+        Pack<E>::get(yc[u], y);
+        weights(u, i, ga);
+      }
       if (dX_add) Pack<E>::get(*(reinterpret_cast<const uint4*>(dX_add + t * dim) + i), add);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float h = (x[j] - sc.x) * sc.y;
-        const float d = (y[j] * ga[j] - s1 - h * s2) * sc.y;
+        float h, g;
+        if constexpr (kKeep) {
+          h = hk[u * N + j];
+          g = gk[u * N + j];
+        } else {
+          h = (x[j] - sc.x) * sc.y;
+          g = y[j] * ga[j];
+        }
+        const float d = fmaf(g, sc.y, -c1) - h * c2;
         x[j] = dX_add ? d + add[j] : d;
       }
-      *(reinterpret_cast<uint4*>(dX + t * dim) + i) = Pack<E>::put(x);
+      __stcs(reinterpret_cast<uint4*>(dX + t * dim) + i, Pack<E>::put(x));
     }
   }
   if (!(want & 6)) return;
   float* out = part + (int64_t)blockIdx.x * 2 * dim;
+  float* comb = reinterpret_cast<float*>(bufs);   // every copy has landed and been read
+#pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (!(want & (2 << k))) continue;
-    const float* acc = k ? db : dg;
     if constexpr (RPB > 1) {
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < NV * N; ++j)
         comb[row * (TPR * NV * N) + (col + j / N * TPR) * N + j % N] = k ? db[j] : dg[j];
       __syncthreads();
-      for (int c = threadIdx.x; c < dim; c += kBwdThreads) {
-        float s = 0.f;
+      for (int c = threadIdx.x; c < dim; c += TH) {
+        float v = 0.f;
 #pragma unroll 4
-        for (int r = 0; r < RPB; ++r) s += comb[r * (TPR * NV * N) + c];
-        out[k * dim + c] = s;
+        for (int r = 0; r < RPB; ++r) v += comb[r * (TPR * NV * N) + c];
+        out[k * dim + c] = v;
       }
     } else {
-      (void)acc;
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
         const int i = col + u * TPR;
@@ -276,30 +342,33 @@ __global__ void __launch_bounds__(kBwdThreads, NV == 1 ? 2 : 1)
   }
 }
 
-// dst[c] += sum over the CTAs of part[CTA][k][c], in CTA order within each of 8 interleaved runs,
-// then the runs in order.
-__global__ void __launch_bounds__(256) k_norm_reduce(const float* __restrict__ part, int n, int dim,
-                                                     float* dgamma, float* dbeta) {
+// dst[c] += sum over the CTAs of part[CTA][k][c]: 32 interleaved runs in CTA order, then the runs in
+// a fixed tree. A thread's whole run is in flight at once.
+constexpr int kRedRuns = 32;
+constexpr int kRedMost = 2 * 152;   // most CTAs of k_norm_bwd
+__global__ void __launch_bounds__(32 * kRedRuns) k_norm_reduce(const float* __restrict__ part, int n, int dim,
+                                                               float* dgamma, float* dbeta) {
   grid_dep_sync();
-  __shared__ float sh[8][33];
+  __shared__ float sh[kRedRuns][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;
   float* dst = blockIdx.y ? dbeta : dgamma;
   if (!dst) return;
-  float s = 0.f;
-  if (c < dim) {
-    const float* p = part + (int64_t)blockIdx.y * dim + c;
-#pragma unroll 4
-    for (int i = ty; i < n; i += 8) s += __ldcg(p + (int64_t)i * 2 * dim);
+  const float* p = part + (int64_t)blockIdx.y * dim + c;
+  float v[(kRedMost + kRedRuns - 1) / kRedRuns];
+#pragma unroll
+  for (int k = 0; k < (kRedMost + kRedRuns - 1) / kRedRuns; ++k) {
+    const int i = ty + k * kRedRuns;
+    v[k] = c < dim && i < n ? __ldcg(p + (int64_t)i * 2 * dim) : 0.f;
   }
+  float s = 0.f;
+#pragma unroll
+  for (int k = 0; k < (kRedMost + kRedRuns - 1) / kRedRuns; ++k) s += v[k];
   sh[ty][tx] = s;
   __syncthreads();
-  if (ty == 0 && c < dim) {
-    s = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s += sh[k][tx];
-    dst[c] += s;
-  }
+  s = warp_sum(sh[tx][ty]);   // warp ty: column ty of the block
+  const int cc = blockIdx.x * 32 + ty;
+  if (tx == 0 && cc < dim) dst[cc] += s;
 }
 
 template <typename E, int WPR, int NV>
@@ -326,21 +395,37 @@ cudaError_t fwd_type(const NormArgs& a, cudaStream_t st) {
   if (nvec <= 512) return fwd_launch<E, 8, 2>(a, st);
   if (nvec <= 1024) return fwd_launch<E, 8, 4>(a, st);
   if (nvec <= 2048) return fwd_launch<E, 8, 8>(a, st);
-  return fwd_launch<E, 8, 16>(a, st);
+  if constexpr (sizeof(E) == 4) return fwd_launch<E, 8, 16>(a, st);
+  return cudaErrorInvalidValue;   // past LORA_NORM_MAX_DIM
 }
 
-template <typename E, int TPR, int NV>
+template <typename E, int TH, int TPR, int NV>
 cudaError_t bwd_launch(const NormArgs& a, int grid, cudaStream_t st) {
+  constexpr int RPB = TH / TPR;
+  static bool attr = false;
+  if (!attr) {
+    cudaError_t e = cudaFuncSetAttribute(k_norm_bwd<E, TH, TPR, NV>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (e != cudaSuccess) return e;
+    attr = true;
+  }
+  const int64_t group = RPB * a.dim * (int64_t)sizeof(E);
+  const int ring = bwd_ring(group, TH);
+  int64_t smem = 2 * ring * group;
+  const int64_t comb = RPB > 1 ? (int64_t)TH * NV * Pack<E>::N * 4 : 0;
+  if (smem < comb) smem = comb;
+  uint32_t* err = tc::error_word();
+  if (!err) return cudaErrorInvalidDevice;
   prof_begin(0, st);
   const int want = (a.dX ? 1 : 0) | (a.dgamma ? 2 : 0) | (a.dbeta ? 4 : 0);
   cudaError_t e = launch_kernel(
-      k_norm_bwd<E, TPR, NV>, (unsigned)grid, kBwdThreads, 0, st, static_cast<const E*>(a.X),
+      k_norm_bwd<E, TH, TPR, NV>, (unsigned)grid, TH, (size_t)smem, st, static_cast<const E*>(a.X),
       a.gamma, static_cast<const E*>(a.dY), reinterpret_cast<const float2*>(a.stats),
       static_cast<const E*>(a.dX_add), static_cast<E*>(a.dX), a.part, a.T, (int)a.dim,
-      1.f / (float)a.dim, a.rms, want);
+      1.f / (float)a.dim, a.rms, want, ring, err);
   if (e != cudaSuccess || !(want & 6)) return e;
   prof_begin(0, st);
-  return launch_kernel(k_norm_reduce, dim3((unsigned)((a.dim + 31) / 32), 2), 256, 0, st, a.part,
+  return launch_kernel(k_norm_reduce, dim3((unsigned)((a.dim + 31) / 32), 2), 32 * kRedRuns, 0, st, a.part,
                        grid, (int)a.dim, a.dgamma, a.dbeta);
 }
 
@@ -348,25 +433,31 @@ template <typename E>
 cudaError_t bwd_type(const NormArgs& a, cudaStream_t st) {
   const int64_t nvec = a.dim / Pack<E>::N;
   const int grid = norm_bwd_parts(a.dim, a.dtype, a.T);
-  if (nvec <= 32) return bwd_launch<E, 32, 1>(a, grid, st);
-  if (nvec <= 64) return bwd_launch<E, 64, 1>(a, grid, st);
-  if (nvec <= 128) return bwd_launch<E, 128, 1>(a, grid, st);
-  if (nvec <= 256) return bwd_launch<E, 256, 1>(a, grid, st);
-  if (nvec <= 512) return bwd_launch<E, 512, 1>(a, grid, st);
-  if (nvec <= 1024) return bwd_launch<E, 512, 2>(a, grid, st);
-  if (nvec <= 2048) return bwd_launch<E, 512, 4>(a, grid, st);
-  return bwd_launch<E, 512, 8>(a, grid, st);
+  if (nvec <= 32) return bwd_launch<E, 256, 32, 1>(a, grid, st);
+  if (nvec <= 64) return bwd_launch<E, 256, 32, 2>(a, grid, st);
+  if (nvec <= 128) return bwd_launch<E, 256, 64, 2>(a, grid, st);
+  if (nvec <= 256) return bwd_launch<E, 256, 128, 2>(a, grid, st);
+  if (nvec <= 512) return bwd_launch<E, 256, 256, 2>(a, grid, st);
+  if (nvec <= 1024) return bwd_launch<E, 512, 512, 2>(a, grid, st);
+  if (nvec <= 2048) return bwd_launch<E, 512, 512, 4>(a, grid, st);
+  if constexpr (sizeof(E) == 4) return bwd_launch<E, 512, 512, 8>(a, grid, st);
+  return cudaErrorInvalidValue;   // past LORA_NORM_MAX_DIM
 }
 
 }  // namespace
 
+// CTAs (and partials) of a backward pass: two per SM, one where a row takes 512
+// threads, and few enough that a CTA has four groups of rows (the partials are 8 bytes per column
+// and CTA, a row 6 or 12).
 int norm_bwd_parts(int64_t dim, int dtype, int64_t T) {
   const int64_t nvec = dim / (dtype == LORA_BF16 ? 8 : 4);
+  const int64_t th = nvec <= 512 ? 256 : 512;
   int64_t tpr = 32;
-  while (tpr < nvec && tpr < kBwdThreads) tpr *= 2;
-  const int64_t groups = (T * tpr + kBwdThreads - 1) / kBwdThreads;
-  const int64_t most = nvec <= kBwdThreads ? 2 * 152 : 152;
-  return (int)(groups < most ? groups : most);
+  while (2 * tpr < nvec && tpr < th) tpr *= 2;
+  const int64_t groups = (T * tpr + th - 1) / th;
+  const int64_t most = nvec <= 512 ? kRedMost : kRedMost / 2;
+  const int64_t want = (groups + 3) / 4;
+  return (int)(want < most ? want : most);
 }
 
 cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t st) {
