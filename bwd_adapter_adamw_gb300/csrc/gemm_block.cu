@@ -6,7 +6,8 @@
 // The scales change along the contraction, so one accumulator cannot run over it: every block of
 // 128 is summed on the tensor cores (kind::f8f6f4) into one of two TMEM buffers, and the epilogue
 // warps add it, scaled, to fp32 accumulators in their registers while the next block's MMAs run
-// into the other buffer. The LoRA term (kind::tf32) is one more such block with scale one.
+// into the other buffer. The LoRA term (kind::tf32) is one more such block per 32 of the rank, with
+// scale one.
 //
 // For the input gradient the weight's codes are read in place: the operand is [out, in] with the
 // contraction along the rows, an MN-major tile in the 128-byte swizzle.
@@ -124,8 +125,8 @@ __device__ __forceinline__ void tile_at(const TileParams& p, int t, int32_t& m0,
   m0 = (first + idx % gsize) * 128;
 }
 
-// MASK: the LoRA block is masked by dropout at (t, n); otherwise it is added like any other block,
-// with scale one.
+// MASK: the LoRA blocks are masked by dropout at (t, n); otherwise they are added like any other
+// block, with scale one.
 template <int BN, bool TR, bool MASK>
 __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_constant__ TileParams p) {
   using C = TileCfg<BN>;
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
   const uint32_t tmem = *tmem_slot;
   grid_dep_sync();
 
-  const int nblk = p.nk + (p.n_lora > 0 ? 1 : 0);   // accumulator uses per tile
+  const int nblk = p.nk + p.n_lora;   // blocks of a tile
   if (warp < 4) {
     // 384 threads start with 168 registers each; the epilogue takes what the other four warps leave:
     // 72 + 2 x 216 = 3 x 168
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
           int32_t m0, nt;
           tile_at(p, t, m0, nt);
           const int n0 = nt * BN;
-          for (int kb = 0; kb < p.nk + p.n_lora; ++kb, ++g) {
+          for (int kb = 0; kb < nblk; ++kb, ++g) {
             const int s = g % kStages;
             const uint32_t ph = (uint32_t)(g / kStages) & 1u;
             if (g >= kStages && !mbar_wait_for(&empty_bar[s], ph ^ 1u, 1u, p.err, p.wait_limit)) {
@@ -213,45 +214,42 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
       if (lane == 0) {
         constexpr uint32_t id8 = idesc(kFmtE4M3, 128, BN, false, TR);
         constexpr uint32_t id32 = idesc(kFmtTF32, 128, BN);
-        int g = 0, j = 0;
+        int j = 0;
         bool ok = true;
         for (int t = blockIdx.x; t < p.total && ok; t += gridDim.x) {
-          for (int kb = 0; kb < nblk && ok; ++kb, ++j) {
-            const int b = j % kSlots, use = j / kSlots;
-            const int loads = kb < p.nk ? 1 : p.n_lora;
-            if ((j & 1) != warp - 1) {   // the other MMA warp's block
-              g += loads;
-              continue;
+          for (int kb = 0; kb < nblk; ++kb, ++j) {
+            if ((j & 1) != warp - 1) continue;   // the other MMA warp's block
+            const int b = j % kSlots, use = j / kSlots, s = j % kStages;
+            // The accumulator first: once block j - kSlots has been read out, every load up to it
+            // has landed, the stage's last one (j - kStages) among them. Only then does the parity
+            // name this block's phase and not the one before it, which the other warp waited for.
+            static_assert(kStages >= kSlots && kSlots % 2 == 0, "phases of the stages");
+            if ((use >= 1 &&
+                 !mbar_wait_for(&acc_empty[b], (uint32_t)(use - 1) & 1u, 2u, p.err, p.wait_limit)) ||
+                !mbar_wait_for(&full_bar[s], (uint32_t)(j / kStages) & 1u, 2u, p.err, p.wait_limit)) {
+              ok = false;
+              break;
             }
+            fence_after();
             const uint32_t d = tmem + (uint32_t)(BN * b);
-            for (int l = 0; l < loads; ++l, ++g) {
-              const int s = g % kStages;
-              if (!mbar_wait_for(&full_bar[s], (uint32_t)(g / kStages) & 1u, 2u, p.err, p.wait_limit) ||
-                  (l == 0 && use >= 1 &&
-                   !mbar_wait_for(&acc_empty[b], (uint32_t)(use - 1) & 1u, 2u, p.err, p.wait_limit))) {
-                ok = false;
-                break;
-              }
-              fence_after();
-              const uint32_t sa = smem_u32(base + s * C::kStageBytes);
-              const uint64_t da = smem_desc_sw128(sa);
-              if (kb < p.nk) {
-                // K = 32 codes per instruction: 32 bytes along a K-major row, four 8-row groups
-                // of the MN-major tile
-                const uint64_t db = TR ? smem_desc_sw128_mn(sa + kTileBytes, kTileBytes)
-                                       : smem_desc_sw128(sa + kTileBytes);
+            const uint32_t sa = smem_u32(base + s * C::kStageBytes);
+            const uint64_t da = smem_desc_sw128(sa);
+            if (kb < p.nk) {
+              // K = 32 codes per instruction: 32 bytes along a K-major row, four 8-row groups
+              // of the MN-major tile
+              const uint64_t db = TR ? smem_desc_sw128_mn(sa + kTileBytes, kTileBytes)
+                                     : smem_desc_sw128(sa + kTileBytes);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  umma_f8(d, da + 2 * k, db + (TR ? 256 : 2) * k, id8, k > 0 ? 1u : 0u);
-              } else {
-                const uint64_t db = smem_desc_sw128(sa + kTileBytes);
+              for (int k = 0; k < 4; ++k)
+                umma_f8(d, da + 2 * k, db + (TR ? 256 : 2) * k, id8, k > 0 ? 1u : 0u);
+            } else {
+              const uint64_t db = smem_desc_sw128(sa + kTileBytes);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  umma_tf32(d, da + 2 * k, db + 2 * k, id32, (l > 0 || k > 0) ? 1u : 0u);
-              }
-              umma_commit(&empty_bar[s]);
+              for (int k = 0; k < 4; ++k)
+                umma_tf32(d, da + 2 * k, db + 2 * k, id32, k > 0 ? 1u : 0u);
             }
-            if (ok) umma_commit(&acc_full[b]);
+            umma_commit(&empty_bar[s]);
+            umma_commit(&acc_full[b]);
           }
         }
         umma_commit(&mma_done[warp - 1]);
@@ -337,26 +335,27 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
         }
       }
       if constexpr (MASK) {
-        epi_barrier();
-        fence_after();
-        const uint32_t d = tcol + (uint32_t)(BN * (j % kSlots));
         const int64_t m = m0 + q * 32 + lane;
         const DropRow drow = drop_row(p.drop, m < p.T ? m : 0);
+        for (int l = 0; l < p.n_lora; ++l, ++j) {
+          epi_barrier();
+          fence_after();
+          const uint32_t d = tcol + (uint32_t)(BN * (j % kSlots));
 #pragma unroll
-        for (int c = 0; c < HC / 16; ++c) {
-          uint32_t r[16];
-          tmem_ldc(d + (uint32_t)(c * 16), r);
-          tmem_wait_ld();
+          for (int c = 0; c < HC / 16; ++c) {
+            uint32_t r[16];
+            tmem_ldc(d + (uint32_t)(c * 16), r);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (!drop_keep_at(drow, p.drop.tau, n0 + c * 16 + i)) r[i] = 0u;
+            for (int i = 0; i < 16; ++i)
+              if (!drop_keep_at(drow, p.drop.tau, n0 + c * 16 + i)) r[i] = 0u;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], pack2(1.f, 1.f), r[2 * i], r[2 * i + 1]);
+            for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], pack2(1.f, 1.f), r[2 * i], r[2 * i + 1]);
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[j % kSlots]);
         }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[j % kSlots]);
-        ++j;
       }
       // rows past T and columns past N are clipped by the bulk store
       const int32_t wrow = m0 + q * 32;
