@@ -402,7 +402,6 @@ struct TcArgs {
   int32_t spill_tiles;
   int32_t zero_grads, C;
   uint32_t* err;
-  unsigned long long wait_limit;
 };
 
 // The small matrices are [64][64] fp32 with the 16-byte chunks of a row spread by the row (no bank
@@ -483,7 +482,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
   uint64_t* bar_gram = bar_apply + 2;
   uint64_t* bar_load = bar_gram + 1;   // [2]: a spilled tile is back
   uint64_t* bar_used = bar_load + 2;   // [2]: a spilled tile's Gram products are done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_used + 2);
+  uint64_t* bar_done = bar_used + 2;   // every MMA of this CTA is done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_done + 1);
+  volatile uint32_t* failed = tmem_slot + 1;
   float* t1 = reinterpret_cast<float*>(scratch);
   float* t2 = t1 + 64 * 64;
   float* qf = reinterpret_cast<float*>(qop);
@@ -493,7 +494,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
   if (tid == 0) {
     mbar_init(&bar_apply[0], 1);
     mbar_init(&bar_apply[1], 1);
+    *failed = 0u;
     mbar_init(bar_gram, 1);
+    mbar_init(bar_done, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bar_load[b], 1);
       mbar_init(&bar_used[b], 1);
@@ -517,12 +520,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
   constexpr uint32_t id_apply = idesc(kFmtBF16, 128, 128);
   uint32_t ph_apply[2] = {0, 0}, ph_gram = 0;   // the same in every thread
   uint32_t ph_load[2] = {0, 0}, ph_used[2] = {0, 0};   // of thread 0, which alone waits on them
-  bool ok = true;                                            // no wait has run out of its bound
+  bool ok = true;                                      // no wait has run out of its bound
   // One warp polls, the others wait at the barrier: polling by all of them took most of the issue
-  // slots.
+  // slots. A wait that runs out of its bound marks the launch as failed: its parameters are not
+  // written, and the waits that follow are short.
+  auto bound = [&]() { return ok ? kWaitCycles : 1ull << 22; };
   auto wait = [&](uint64_t* bar, uint32_t ph) {
-    if (warp == 0) ok = mbar_wait_for(bar, ph, 2u, a.err, ok ? a.wait_limit : 0ull) && ok;
+    if (warp == 0 && !mbar_wait_for(bar, ph, 2u, a.err, bound())) *failed = 1u;
     __syncthreads();
+    ok = *failed == 0u;
     fence_after();
   };
   // every thread's writes to shared memory become visible to the tensor cores and bulk copies
@@ -553,7 +559,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       return t < kTcTiles ? tiles + t * kTcTileBytes : scratch + ((t - kTcTiles) & 1) * kTcTileBytes;
     };
     auto wait0 = [&](uint64_t* bar, uint32_t& ph) {   // thread 0
-      ok = mbar_wait_for(bar, ph, 2u, a.err, ok ? a.wait_limit : 0ull) && ok;
+      if (!mbar_wait_for(bar, ph, 2u, a.err, bound())) *failed = 1u;
       ph ^= 1u;
       fence_after();
     };
@@ -995,7 +1001,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
     }
     __syncthreads();
   }
-  // every MMA's completion has been waited for; the peers are done with this CTA's memory
+  // every MMA is done before the tensor memory is freed (after a failed wait nothing else says so);
+  // the peers are done with this CTA's memory
+  if (tid == 0) {
+    umma_commit(bar_done);
+    mbar_wait(bar_done, 0u, 2u, a.err);
+  }
   fence_before();
   __syncthreads();
   fence_after();
@@ -1101,7 +1112,6 @@ cudaError_t launch_muon(float* p, float* g, float* m, const MuonTab& tab, const 
   a.zero_grads = zero_grads; a.C = C;
   a.err = error_word();
   if (!a.err) return cudaErrorInvalidDevice;
-  a.wait_limit = tc_wait_limit();
   return launch_clusters(k_muon_tc, kTcThreads, kTcSmem, tab.n, C, kMuonMaxCtas, st, tab, hp, a);
 }
 
