@@ -875,7 +875,7 @@ def run_ours(args):
             bound, punit = "tensor", "TFLOP/s"
             note = (f"split-bf16 effective: measured bf16 {kind} {bf16_peak:.0f} / 4 products "
                     f"({peak_src})")
-        elif cfg.dtype == "bf16fp8":
+        elif cfg.dtype in ("bf16fp8", "bf16blk8"):
             # E4M3 products: the measured bf16 rate x the nominal fp8 : bf16 ratio (4.5 : 2.25)
             peak = bf16_peak * 4.5 / 2.25
             bound, punit = "tensor", "TFLOP/s"

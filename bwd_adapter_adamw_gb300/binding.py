@@ -26,6 +26,7 @@ LORA_ERR_TIMEOUT = 7
 LORA_F32 = 0
 LORA_BF16 = 1
 LORA_BF16_FP8 = 2
+LORA_BF16_BLK8 = 3
 LORA_NORM_LAYER = 0
 LORA_NORM_RMS = 1
 LORA_NORM_MAX_DIM = 16384

@@ -33,7 +33,8 @@ int64_t max_red_items(int64_t T, int32_t n_seg) {
 int check_desc(const lora_desc* d, int64_t T, bool multi) {
   if (!d || T < 0) return LORA_ERR_INVALID;
   if (d->in_dim <= 0 || d->out_dim <= 0) return LORA_ERR_INVALID;
-  if (d->dtype != LORA_F32 && d->dtype != LORA_BF16 && d->dtype != LORA_BF16_FP8)
+  if (d->dtype != LORA_F32 && d->dtype != LORA_BF16 && d->dtype != LORA_BF16_FP8 &&
+      d->dtype != LORA_BF16_BLK8)
     return LORA_ERR_INVALID;
   if (d->rank <= 0) return LORA_ERR_INVALID;
   if (d->rank > LORA_MAX_RANK || (d->rank % 4) != 0) return LORA_ERR_UNSUPPORTED;
@@ -46,6 +47,10 @@ int check_desc(const lora_desc* d, int64_t T, bool multi) {
     // E4M3 rows are K bytes (16-byte TMA strides); a row is quantised from registers
     if ((d->in_dim % 16) != 0 || (d->out_dim % 16) != 0) return LORA_ERR_ALIGN;
     if (multi || d->dora || d->in_dim > 16384 || d->out_dim > 16384) return LORA_ERR_UNSUPPORTED;
+  }
+  if (d->dtype == LORA_BF16_BLK8) {
+    if ((d->in_dim % 16) != 0 || (d->out_dim % 16) != 0) return LORA_ERR_ALIGN;
+    if (multi || d->dora || d->in_dim > (1 << 20) || d->out_dim > (1 << 20)) return LORA_ERR_UNSUPPORTED;
   }
   if (!multi && !std::isfinite(d->scale)) return LORA_ERR_INVALID;
   if (T >= (int64_t(1) << 31) - kRedTileT) return LORA_ERR_UNSUPPORTED;
@@ -233,6 +238,13 @@ Fp8Prep fp8_prep(const void* Wp, int64_t out, int64_t in) {
   return f;
 }
 
+// Block-scaled prepared weight: [W8 (out x in) | sw]
+int64_t scale_blocks(int64_t n) { return (n + LORA_SCALE_BLOCK - 1) / LORA_SCALE_BLOCK; }
+uint8_t* blk8_codes(const void* Wp) { return static_cast<uint8_t*>(const_cast<void*>(Wp)); }
+float* blk8_scales(const void* Wp, const lora_desc* d) {
+  return reinterpret_cast<float*>(blk8_codes(Wp) + (size_t)d->out_dim * d->in_dim);
+}
+
 Layout carve(const lora_desc* d, int64_t T, int32_t n_seg, int n_slots, int64_t rank_sum,
              bool backward, void* ws) {
   Layout L{};
@@ -288,6 +300,11 @@ Layout carve(const lora_desc* d, int64_t T, int32_t n_seg, int n_slots, int64_t 
     L.sq = c.take<float>((size_t)T);
     L.Pq = c.take<float>((size_t)T * d->rank);
     L.Qq = c.take<float>((size_t)kmax * d->rank);
+  }
+  if (d->dtype == LORA_BF16_BLK8) {
+    const int64_t kmax = d->in_dim > d->out_dim ? d->in_dim : d->out_dim;
+    L.Aq = c.take<uint8_t>((size_t)T * kmax);
+    L.sq = c.take<float>((size_t)block_scales_ld(T) * scale_blocks(kmax));
   }
   if (!tc) {
     const int64_t kmax = d->in_dim > d->out_dim ? d->in_dim : d->out_dim;
@@ -433,6 +450,23 @@ void set_routed_gemm(TcGemmArgs& t, const Slots& s, const Layout& L, int64_t T, 
   }
 }
 
+// Frozen product over block-scaled codes with the LoRA term P Q^T: the activations `in` [T, K]
+// quantised first (LORA_BF16_BLK8).
+int blk8_product(const lora_desc* d, const DropParams& dp, int64_t T, const void* in, const void* Wp,
+                 const float* P, const float* Q, void* out, bool transposed, const Layout& L,
+                 cudaStream_t st) {
+  BlockProductArgs a{};
+  a.codes = L.Aq; a.scales = L.sq; a.ld_scales = block_scales_ld(T);
+  a.T = T; a.out_dim = d->out_dim; a.in_dim = d->in_dim;
+  a.W8 = blk8_codes(Wp); a.sw = blk8_scales(Wp, d);
+  a.transposed = transposed; a.Y = out;
+  a.p = P; a.q = Q; a.rank = d->rank;
+  if (transposed) a.drop = dp;   // only the input gradient's LoRA term is masked
+  LORA_TRY(launch_block_quant(in, T, transposed ? d->out_dim : d->in_dim, L.Aq, L.sq, 1, a.ld_scales, st));
+  LORA_TRY(launch_block_gemm(a, st, transposed ? LORA_PROF_FROZEN_DX : LORA_PROF_FROZEN_FWD));
+  return LORA_OK;
+}
+
 // forward, bf16 activations: shrink and frozen product on tensor cores
 int run_forward_tc(const lora_desc* d, const DropParams& dp, int64_t T, const void* X,
                    const void* W, const void* Wprep, int32_t n_seg, const int32_t* seg_start,
@@ -463,6 +497,8 @@ int run_forward_tc(const lora_desc* d, const DropParams& dp, int64_t T, const vo
   }
   int rc = tc_shrink(d, dp, T, X, n_seg, s, L, H, routed ? L.Px : nullptr, st);
   if (rc) return rc;
+  if (d->dtype == LORA_BF16_BLK8)
+    return blk8_product(d, dp, T, X, Wprep, H, s.B[0], Y, false, L, st);
   TcGemmArgs t{};
   t.a = X; t.T = T; t.b = W; t.n_rows = d->out_dim; t.K = d->in_dim;
   t.p = H; t.ldp = d->rank; t.n_slots = s.n;
@@ -576,7 +612,10 @@ int run_backward_tc(const lora_desc* d, const DropParams& dp, int64_t T, const v
     LORA_TRY(launch_tc_rows(r, st, LORA_PROF_G));
   }
   // dX = dY' W + (Gs A_k) * M
-  if (dX) {
+  if (dX && d->dtype == LORA_BF16_BLK8) {
+    const int rr = blk8_product(d, dp, T, dYp, Wt, L.Gs, At[0], dX, true, L, st);
+    if (rr) return rr;
+  } else if (dX) {
     TcGemmArgs t{};
     t.a = dYp; t.T = T; t.b = Wt; t.n_rows = d->in_dim; t.K = d->out_dim;
     t.p = L.Gs; t.ldp = d->rank; t.n_slots = s.n;
@@ -1256,6 +1295,8 @@ size_t lora_prepared_weight_size(const lora_desc* d) {
   if (check_desc(d, 0, false) != LORA_OK) return 0;
   const size_t n = (size_t)d->out_dim * (size_t)d->in_dim;
   if (d->dtype == LORA_BF16_FP8) return fp8_prep_bytes(d->out_dim, d->in_dim);
+  if (d->dtype == LORA_BF16_BLK8)
+    return n + (size_t)scale_blocks(d->out_dim) * scale_blocks(d->in_dim) * sizeof(float);
   return d->dtype == LORA_F32 ? 8 * n : 2 * n;
 }
 
@@ -1275,12 +1316,15 @@ int lora_prepare_weight(const lora_desc* d, const void* W, void* W_prep, void* s
                                  const_cast<float*>(f.swT), (cudaStream_t)stream);
     return cuda_status(e);
   }
+  if (d->dtype == LORA_BF16_BLK8)
+    return cuda_status(launch_block_quant_weight(W, d->out_dim, d->in_dim, blk8_codes(W_prep),
+                                                 blk8_scales(W_prep, d), (cudaStream_t)stream));
   return cuda_status(launch_prepare_weight(d->dtype, W, W_prep, d->out_dim, d->in_dim,
                                            (cudaStream_t)stream));
 }
 
 size_t lora_dora_norm_workspace_size(const lora_desc* d) {
-  if (check_desc(d, 0, false) != LORA_OK) return 0;
+  if (check_desc(d, 0, false) != LORA_OK || (d->dtype != LORA_F32 && d->dtype != LORA_BF16)) return 0;
   return dora_norm_carve(d, nullptr).bytes;
 }
 
@@ -1288,6 +1332,7 @@ int lora_dora_norm(const lora_desc* d, const void* W, const float* A, const floa
                    float* norm_out, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_desc(d, 0, false);
   if (rc) return rc;
+  if (d->dtype != LORA_F32 && d->dtype != LORA_BF16) return LORA_ERR_UNSUPPORTED;   // no DoRA there
   if (!W || !A || !B || !norm_out || !ws) return LORA_ERR_INVALID;
   if (!al16(W) || !al16(A) || !al16(B) || !al16(norm_out) || !al16(ws)) return LORA_ERR_ALIGN;
   if (ws_bytes < dora_norm_carve(d, nullptr).bytes) return LORA_ERR_WORKSPACE;
@@ -1307,7 +1352,8 @@ int lora_forward(const lora_desc* d, const lora_ctx* c, int64_t T, const void* X
   if (rc) return rc;
   DropParams dp;
   if ((rc = build_drop(d, c, T, dp))) return rc;
-  if (!X || !W || !W_prep || !A || !B || !Y || !H_save || !ws) return LORA_ERR_INVALID;
+  if (!X || (!W && d->dtype != LORA_BF16_BLK8) || !W_prep || !A || !B || !Y || !H_save || !ws)
+    return LORA_ERR_INVALID;
   if (d->dora && (!dora_m || !dora_n)) return LORA_ERR_INVALID;
   if (!al16(X) || !al16(W) || !al16(W_prep) || !al16(A) || !al16(B) || !al16(Y) ||
       !al16(H_save) || !al16(ws))

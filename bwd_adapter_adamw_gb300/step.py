@@ -20,7 +20,8 @@ import torch
 
 from . import binding as L
 
-_DT = {"f32": L.LORA_F32, "bf16": L.LORA_BF16, "bf16fp8": L.LORA_BF16_FP8}
+_DT = {"f32": L.LORA_F32, "bf16": L.LORA_BF16, "bf16fp8": L.LORA_BF16_FP8,
+       "bf16blk8": L.LORA_BF16_BLK8}
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:
@@ -223,6 +224,93 @@ class LoraStep:
         passes step 0 again."""
         L.lora_restore(self.arena.params, snap, self.arena.grads, self.arena.m, self.arena.v,
                        self.groups(0.0, 0), zero_grads)
+
+
+class SublayerStep(LoraStep):
+    """One optimizer step of a pre-norm sublayer: a layer norm (or RMS norm) in front of adapted
+    projections that read its output,
+        H = norm(X),  Y_k = projection_k(H),  dX = dX_res + norm'(sum_k dX_k),
+    with the norm's weight (and shift) trained beside the adapters. They live in the arena's
+    magnitude range, so one group holds the global clip of everything; A and B take the
+    orthogonalised update, the norm's parameters AdamW (no decay, plain learning rate)."""
+
+    def __init__(self, X: torch.Tensor, linears: Sequence[Linear], *, kind: str = "layer",
+                 eps: float = 1e-5, muon: Optional[L.lora_muon_hp] = None, **kw):
+        self.X_in = X                                  # [T, dim], the sublayer's input
+        self.H_norm = torch.empty_like(X)
+        for l in linears:
+            l.X = self.H_norm
+        self.norm = L.make_norm_desc(X.shape[1], L.LORA_NORM_RMS if kind == "rms" else L.LORA_NORM_LAYER,
+                                     L.LORA_F32 if X.dtype == torch.float32 else L.LORA_BF16, eps)
+        super().__init__(linears, **kw)
+        if self.dora:
+            raise ValueError("the sublayer's magnitude range holds the norm's parameters")
+        dim, shift = X.shape[1], kind != "rms"
+        old, self.n_mag = self.arena, dim * (2 if shift else 1)
+        base = self.n_a + self.n_b
+        self.arena = Arena(base + self.n_mag, self.device)
+        del old
+        oa, ob = 0, self.n_a
+        for l in self.linears:
+            l.A, l.gA = (self.arena.view(w, oa, (self.rank, l.in_dim)) for w in ("params", "grads"))
+            l.B, l.gB = (self.arena.view(w, ob, (l.out_dim, self.rank)) for w in ("params", "grads"))
+            oa += self.rank * l.in_dim
+            ob += l.out_dim * self.rank
+        self.gamma, self.dgamma = (self.arena.view(w, base, (dim,)) for w in ("params", "grads"))
+        self.beta = self.dbeta = None
+        if shift:
+            self.beta, self.dbeta = (self.arena.view(w, base + dim, (dim,)) for w in ("params", "grads"))
+        self.gamma.fill_(1.0)
+        self.stats = torch.empty((self.T, 2), dtype=torch.float32, device=self.device)
+        self.dX = torch.empty_like(X)
+        self.norm_ws = _ws(L.lora_norm_backward_workspace_size(self.norm, self.T), self.device)
+        self.muon = muon if muon is not None else L.make_muon_hp()
+        mats, oa, ob = [], 0, self.n_a
+        for l in self.linears:
+            mats.append(dict(offset=oa, rows=self.rank, cols=l.in_dim, kind=L.LORA_KIND_A))
+            oa += self.rank * l.in_dim
+        for l in self.linears:
+            mats.append(dict(offset=ob, rows=l.out_dim, cols=self.rank, kind=L.LORA_KIND_B))
+            ob += l.out_dim * self.rank
+        self.mats = L.make_mats(mats)
+        self.muon_ws = _ws(L.lora_muon_workspace_size(self.mats), self.device)
+
+    def forward(self, opt_step: int = 0):
+        """The norm and every projection (the serving call, and the first half of a step)."""
+        L.lora_norm_forward(self.norm, self.T, self.X_in, self.gamma, self.beta, self.H_norm, self.stats)
+        for l in self.linears:
+            ctx = L.make_ctx(opt_step, 0, self.T // self.chunks)
+            L.lora_forward(self.desc(l), ctx, self.T, l.X, l.W, l.Wp, l.A, l.B, None, None, l.Y, l.H,
+                           self.ws[0])
+
+    def forward_backward(self, opt_step: int, dX_res: Optional[torch.Tensor] = None):
+        """Forward, then every projection's backward; the norm's backward runs once per projection
+        (it is linear in its upstream gradient), adding up into dX."""
+        self.forward(opt_step)
+        add = dX_res
+        for l in self.linears:
+            ctx = L.make_ctx(opt_step, 0, self.T // self.chunks)
+            L.lora_backward(self.desc(l), ctx, self.T, l.X, l.Wp, l.A, l.B, l.dY, l.H, None, None,
+                            None, l.dX, l.gA, l.gB, None, self.ws[0])
+            L.lora_norm_backward(self.norm, self.T, self.X_in, self.gamma, l.dX, self.stats, add,
+                                 self.dX, self.dgamma, self.dbeta, self.norm_ws)
+            add = self.dX
+
+    def optimizer_step(self, lr: float, step: int, zero_grads: bool = True):
+        g = self.groups(lr, step)
+        L.lora_grad_prepare(self.arena.grads, g, self.scale_norm, self.status, self.prepare_ws())
+        a = self.arena
+        L.lora_muon_step(a.params, a.grads, a.m, g, self.mats, self.muon, self.scale_norm, self.status,
+                         zero_grads, self.muon_ws)
+        norm = L.make_groups([dict(offset=self.n_a + self.n_b, n_mag=self.n_mag,
+                                   grad_scale=1.0 / self.T, max_norm=self.max_norm, lr=lr, step=step)])
+        L.lora_adamw_step(a.params, a.grads, a.m, a.v, norm, self.hp, self.scale_norm, self.status,
+                          zero_grads)
+
+    def run(self, opt_step: int, lr: float, dX_res: Optional[torch.Tensor] = None,
+            zero_grads: bool = True):
+        self.forward_backward(opt_step, dX_res)
+        self.optimizer_step(lr, opt_step, zero_grads)
 
 
 @dataclass

@@ -28,7 +28,8 @@
  *     the matching *_workspace_size call gives; a smaller workspace returns LORA_ERR_WORKSPACE.
  *   - Calls are not thread-safe on one workspace; two calls in flight need two workspaces.
  *   - Activations X, dY, Y, dX and the frozen W share one dtype (LORA_F32 or LORA_BF16;
- *     LORA_BF16_FP8 is bf16 with an E4M3 frozen product, see its definition).
+ *     LORA_BF16_FP8 and LORA_BF16_BLK8 are bf16 with an E4M3 frozen product, see their
+ *     definitions).
  *     A, B, their gradients, the Adam moments, H and the DoRA vectors are always fp32.
  *   - Shapes: 1 <= rank <= LORA_MAX_RANK and rank % 4 == 0; in and out multiples of 8;
  *     all pointers 16-byte aligned (LORA_ERR_ALIGN otherwise).
@@ -73,6 +74,14 @@ extern "C" {
  * Quantized rollout: an FP8 base under a bf16-trained adapter). Single-adapter calls without
  * DoRA; in_dim and out_dim multiples of 16 and at most 16384 (LORA_ERR_UNSUPPORTED otherwise). */
 #define LORA_BF16_FP8 2
+/* bf16 activations over a frozen weight kept as E4M3 codes with one scale per 128 x 128 block (see
+ * lora_block_product): W_prep = [W8 (out x in codes) | sw], from lora_prepare_weight (which
+ * quantises a bf16 W) or filled by the caller with a checkpoint's codes and scales (the sections of
+ * lora_prepared_weight_size); lora_forward does not read W, which may be NULL. X and dY' are
+ * quantised per 1 x 128 block inside each call; both products read the same codes. The adapter
+ * branch reads the bf16 tensors unchanged. Single-adapter calls without DoRA (LORA_ERR_UNSUPPORTED
+ * otherwise); in_dim and out_dim multiples of 16 (LORA_ERR_ALIGN). */
+#define LORA_BF16_BLK8 3
 
 #define LORA_SCHED_CONSTANT 0
 #define LORA_SCHED_WARMUP_COSINE 1
@@ -88,7 +97,7 @@ typedef struct lora_desc {
   int64_t out_dim;
   int32_t rank;        /* r; for multi-LoRA calls: the largest slot rank (H row stride) */
   float scale;         /* s = lora_scale(alpha, rank, rslora); ignored by multi-LoRA calls */
-  int32_t dtype;       /* LORA_F32 | LORA_BF16 | LORA_BF16_FP8 for X, W, dY, Y, dX */
+  int32_t dtype;       /* LORA_F32 | LORA_BF16 | LORA_BF16_FP8 | LORA_BF16_BLK8 for X, W, dY, Y, dX */
   float dropout_p;     /* 0 <= p < 1; applies to the adapter branch input only */
   uint64_t seed;       /* dropout seed */
   uint32_t layer_id;   /* dropout key fields */
@@ -169,7 +178,9 @@ size_t lora_workspace_size(const lora_desc* d, int64_t T);
  *         (nearest even) and x_lo = (x - x_hi) rounded to bf16 (8 * in_dim * out_dim bytes);
  *   bf16 with the E4M3 frozen product: [W8 (out x in codes) | sw (out fp32 row scales) |
  *         WT8 (in x out codes of W's columns) | swT (in fp32)], each section starting on a
- *         16-byte boundary (about 2 * in_dim * out_dim bytes).
+ *         16-byte boundary (about 2 * in_dim * out_dim bytes);
+ *   LORA_BF16_BLK8: [W8 (out x in codes, row-major) | sw (ceil(out / 128) x ceil(in / 128) fp32)],
+ *         the second section from byte in_dim * out_dim (a multiple of 256).
  * Returns 0 for an invalid descriptor. */
 size_t lora_prepared_weight_size(const lora_desc* d);
 

@@ -47,7 +47,8 @@ class LoraConfig:
     rank: int
     alpha: float
     rslora: bool
-    dtype: str                 # "f32", "bf16", or "bf16fp8" (bf16 with an E4M3 frozen product)
+    dtype: str                 # "f32", "bf16", or bf16 with an E4M3 frozen product: "bf16fp8" (a scale
+                               # per row), "bf16blk8" (a scale per block of 128)
     tokens: int                # tokens per optimizer step
     chunks: int                # accumulation chunks per step
     x_var: float = 1.0
@@ -123,6 +124,9 @@ CONFIGS: Dict[str, LoraConfig] = {
     # c4's workload (same seeded inputs) with the frozen products on E4M3 tensor cores.
     "c4fp8": LoraConfig("c4fp8", 4, LLAMA_PROJS, 32, rank=64, alpha=128, rslora=True,
                         dtype="bf16fp8", tokens=8192, chunks=8, dy_var=1e-2),
+    # The same over codes with a scale per 128 x 128 block.
+    "c4blk8": LoraConfig("c4blk8", 4, LLAMA_PROJS, 32, rank=64, alpha=128, rslora=True,
+                         dtype="bf16blk8", tokens=8192, chunks=8, dy_var=1e-2),
     # Slot-keyed multi-LoRA on one Qwen3-4B-shaped layer, 8 slots.
     "c5": LoraConfig("c5", 5, QWEN3_4B_PROJS, 1, rank=64, alpha=128, rslora=False, dtype="bf16",
                      tokens=16384, chunks=1, dy_var=1e-2,
