@@ -966,14 +966,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
           fence_before();
           __syncthreads();
           fence_after();
-          const float step = ok ? mt.step : 0.f, dec = ok ? mt.lr * mt.decay : 0.f;
+          const float step = mt.step, dec = mt.lr * mt.decay;
           float pc[16];
 #pragma unroll
           for (int v = 0; v < 16; ++v) pc[v] = pn[v];
           load_p(next);
           float* pp = p0 + (int64_t)t * 128 * sj;
           if (mt.tall) {
-            if (pcol) {
+            if (pcol && ok) {
 #pragma unroll
               for (int v = 0; v < 4; ++v) {
                 const int j = prow + v * 32;
@@ -986,7 +986,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
               }
             }
           } else {
-            const int k = t * 128 + prow < left0 ? s - pq : 0;
+            const int k = ok && t * 128 + prow < left0 ? s - pq : 0;
             const uint8_t* xrow = tile + prow * 256 + pq * 4;
 #pragma unroll
             for (int v = 0; v < 16; ++v, pp += 4 * si) {

@@ -180,8 +180,10 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
   const int group = RPB * dim * (int)sizeof(E);
   const int64_t step = (int64_t)gridDim.x * RPB;
   const int64_t t_first = (int64_t)blockIdx.x * RPB;
+  int filled = 0, waited = 0;            // thread 0: groups asked for, groups that have arrived
   auto fill = [&](int s, int64_t t0) {   // thread 0: rows t0 .. of the group, as far as they exist
     if (t0 >= T) return;
+    ++filled;
     const int64_t rows = T - t0 < RPB ? T - t0 : RPB;
     const uint32_t bytes = (uint32_t)(rows * dim * (int64_t)sizeof(E));
     tc::mbar_expect_tx(&full[s], 2 * bytes);
@@ -230,6 +232,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
     const bool live = t < T;
     const float2 sc = live ? __ldg(stats + t) : make_float2(0.f, 0.f);
     ok = ok && tc::mbar_wait(&full[s], phase, 1u, err);
+    waited += ok;
     const uint4* px = reinterpret_cast<const uint4*>(bufs + (size_t)(2 * s) * group) + row * nvec;
     const uint4* py = reinterpret_cast<const uint4*>(bufs + (size_t)(2 * s + 1) * group) + row * nvec;
     uint4 xc[NV], yc[NV];
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
       if ((threadIdx.x & 31) == 0) sh[buf][warp] = make_float2(s1, s2);
     }
     __syncthreads();   // the sums are in place, and every thread has read the buffer
-    if (threadIdx.x == 0) fill(s, t0 + ring * step);
+    if (threadIdx.x == 0 && ok) fill(s, t0 + ring * step);
     if (++s == ring) {
       s = 0;
       phase ^= 1u;
@@ -311,6 +314,10 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
       __stcs(reinterpret_cast<uint4*>(dX + t * dim) + i, Pack<E>::put(x));
     }
   }
+  // after a wait that ran out: the copies still under way land before the CTA exits
+  if (threadIdx.x == 0)
+    for (; waited < filled; ++waited)
+      if (!tc::mbar_wait(&full[waited % ring], (uint32_t)(waited / ring) & 1u, 1u, err)) break;
   if (!(want & 6)) return;
   float* out = part + (int64_t)blockIdx.x * 2 * dim;
   float* comb = reinterpret_cast<float*>(bufs);   // every copy has landed and been read
