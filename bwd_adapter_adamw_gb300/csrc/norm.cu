@@ -54,25 +54,31 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the WPR warps of a row, the same in every lane. `sh` holds one float per warp; the
-// caller alternates two buffers so that one barrier per sum suffices.
-template <int WPR>
-__device__ __forceinline__ float row_sum(float v, float* sh) {
-  v = warp_sum(v);
+// Sums over the WPR warps of a row for R rows, the same in every lane. `sh` holds R floats per warp;
+// the caller alternates two buffers so that one barrier per sum suffices.
+template <int WPR, int R>
+__device__ __forceinline__ void row_sums(float (&v)[R], float (*sh)[kNormThreads / 32]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) v[r] = warp_sum(v[r]);
   if constexpr (WPR > 1) {
     const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) sh[warp] = v;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) sh[r][warp] = v[r];
+    }
     __syncthreads();
     const int w0 = warp / WPR * WPR;
-    v = 0.f;
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) v += sh[w0 + w];
+    for (int r = 0; r < R; ++r) {
+      v[r] = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) v[r] += sh[r][w0 + w];
+    }
   }
-  return v;
 }
 
-// WPR warps per row, NV 16-byte vectors per lane, 8 / WPR rows per CTA.
-template <typename E, int WPR, int NV>
+// WPR warps per row, NV 16-byte vectors per lane and row, R rows per warp, 8 R / WPR rows per CTA.
+template <typename E, int WPR, int NV, int R>
 __global__ void __launch_bounds__(kNormThreads) k_norm_fwd(const E* __restrict__ X,
                                                            const float* __restrict__ gamma,
                                                            const float* __restrict__ beta,
@@ -82,64 +88,81 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_fwd(const E* __restrict__
                                                            int rms) {
   grid_dep_sync();
   constexpr int N = Pack<E>::N;
-  __shared__ float sh[2][kNormThreads / 32];
+  __shared__ float sh[2][R][kNormThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * (kNormThreads / 32 / WPR) + warp / WPR;
-  const bool live = t < T;
+  const int64_t t0 = ((int64_t)blockIdx.x * (kNormThreads / 32 / WPR) + warp / WPR) * R;
   const int nvec = dim / N;
   const int first = (warp % WPR) * 32 + lane;
-  const uint4* src = reinterpret_cast<const uint4*>(X + t * dim);
-  uint4 v[NV];
-  float s = 0.f;
+  uint4 v[R][NV];
+  float s[R], mean[R];
 #pragma unroll
-  for (int u = 0; u < NV; ++u) {
-    const int i = first + u * 32 * WPR;
-    v[u] = live && i < nvec ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-  }
-  float mean = 0.f;
-  if (!rms) {
+  for (int r = 0; r < R; ++r) {
+    const uint4* src = reinterpret_cast<const uint4*>(X + (t0 + r) * dim);
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-      float f[N];
-      Pack<E>::get(v[u], f);
-#pragma unroll
-      for (int j = 0; j < N; ++j) s += f[j];
+      const int i = first + u * 32 * WPR;
+      v[r][u] = t0 + r < T && i < nvec ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
     }
-    mean = row_sum<WPR>(s, sh[0]) * inv_dim;
+    mean[r] = 0.f;
   }
-  s = 0.f;
+  if (!rms) {
 #pragma unroll
-  for (int u = 0; u < NV; ++u) {
-    const int i = first + u * 32 * WPR;
-    if (i < nvec) {
-      float f[N];
-      Pack<E>::get(v[u], f);
+    for (int r = 0; r < R; ++r) {
+      s[r] = 0.f;
 #pragma unroll
-      for (int j = 0; j < N; ++j) s = fmaf(f[j] - mean, f[j] - mean, s);
+      for (int u = 0; u < NV; ++u) {
+        float f[N];
+        Pack<E>::get(v[r][u], f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) s[r] += f[j];
+      }
+    }
+    row_sums<WPR, R>(s, sh[0]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) mean[r] = s[r] * inv_dim;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    s[r] = 0.f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int i = first + u * 32 * WPR;
+      if (i < nvec) {
+        float f[N];
+        Pack<E>::get(v[r][u], f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) s[r] = fmaf(f[j] - mean[r], f[j] - mean[r], s[r]);
+      }
     }
   }
-  const float var = row_sum<WPR>(s, sh[1]) * inv_dim;
-  const float rstd = 1.f / sqrtf(var + eps);
-  if (!live) return;
-  if (first == 0) stats[t] = make_float2(mean, rstd);
-  uint4* dst = reinterpret_cast<uint4*>(Y + t * dim);
+  row_sums<WPR, R>(s, sh[1]);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    s[r] = 1.f / sqrtf(s[r] * inv_dim + eps);
+    if (first == 0 && t0 + r < T) stats[t0 + r] = make_float2(mean[r], s[r]);
+  }
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     const int i = first + u * 32 * WPR;
     if (i >= nvec) continue;
-    float f[N], ga[N], be[N];
-    Pack<E>::get(v[u], f);
+    float ga[N], be[N];
 #pragma unroll
     for (int j = 0; j < N; j += 4) {
       load16(gamma + i * N + j, ga + j);
       if (beta) load16(beta + i * N + j, be + j);
     }
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const float h = (f[j] - mean) * rstd;
-      f[j] = beta ? fmaf(h, ga[j], be[j]) : h * ga[j];
+    for (int r = 0; r < R; ++r) {
+      if (t0 + r >= T) break;
+      float f[N];
+      Pack<E>::get(v[r][u], f);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float h = (f[j] - mean[r]) * s[r];
+        f[j] = beta ? fmaf(h, ga[j], be[j]) : h * ga[j];
+      }
+      reinterpret_cast<uint4*>(Y + (t0 + r) * dim)[i] = Pack<E>::put(f);
     }
-    dst[i] = Pack<E>::put(f);
   }
 }
 
@@ -378,11 +401,11 @@ __global__ void __launch_bounds__(32 * kRedRuns) k_norm_reduce(const float* __re
   if (tx == 0 && cc < dim) dst[cc] += s;
 }
 
-template <typename E, int WPR, int NV>
+template <typename E, int WPR, int NV, int R = 1>
 cudaError_t fwd_launch(const NormArgs& a, cudaStream_t st) {
-  constexpr int rows = kNormThreads / 32 / WPR;
+  constexpr int rows = kNormThreads / 32 / WPR * R;
   prof_begin(0, st);
-  return launch_kernel(k_norm_fwd<E, WPR, NV>, (unsigned)((a.T + rows - 1) / rows), kNormThreads,
+  return launch_kernel(k_norm_fwd<E, WPR, NV, R>, (unsigned)((a.T + rows - 1) / rows), kNormThreads,
                        0, st, static_cast<const E*>(a.X), a.gamma, a.beta, static_cast<E*>(a.Y),
                        reinterpret_cast<float2*>(a.stats), a.T, (int)a.dim, 1.f / (float)a.dim,
                        a.eps, a.rms);
@@ -394,9 +417,15 @@ cudaError_t fwd_type(const NormArgs& a, cudaStream_t st) {
   if (nvec <= 32) return fwd_launch<E, 1, 1>(a, st);
   if (nvec <= 64) return fwd_launch<E, 1, 2>(a, st);
   if (a.T > 2048) {
-    if (nvec <= 128) return fwd_launch<E, 1, 4>(a, st);
-    if (nvec <= 256) return fwd_launch<E, 2, 4>(a, st);
-    if (nvec <= 512) return fwd_launch<E, 4, 4>(a, st);
+    // Enough rows to fill the SMs: few warps per row. In bf16 two rows share the fp32 weight and
+    // shift, which otherwise are four times a row's own bytes through L1 (8192 x 4096: 24.1 us with
+    // two rows, 29.0 with one, 28.3 with four, whose registers cost residency; 4096 x 2560: 11.2
+    // against 13.1; fp32 8192 x 2048: 22.1 against 21.3).
+    constexpr int R = sizeof(E) == 2 ? 2 : 1;
+    if (nvec <= 128) return fwd_launch<E, 1, 4, R>(a, st);
+    if (nvec <= 256) return fwd_launch<E, 2, 4, R>(a, st);
+    if (nvec <= 384) return fwd_launch<E, 4, 3, R>(a, st);
+    if (nvec <= 512) return fwd_launch<E, 4, 4, R>(a, st);
   }
   if (nvec <= 256) return fwd_launch<E, 8, 1>(a, st);
   if (nvec <= 512) return fwd_launch<E, 8, 2>(a, st);
