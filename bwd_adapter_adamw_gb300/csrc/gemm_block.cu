@@ -132,13 +132,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
   using C = TileCfg<BN>;
   constexpr int kStages = C::kStages;
   constexpr int kSlots = C::kSlots;
+  // An odd number of stages and two MMA warps: a stage has a barrier for either, since a warp that
+  // has not seen a barrier's last phase (the other warp's load) cannot tell it from its own.
+  constexpr int kFull = 2 * kStages;
+  static_assert(kStages % 2 == 1 && kSlots % 2 == 0, "a barrier belongs to one MMA warp");
   constexpr int HC = BN / 2;   // columns of an epilogue warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* boxes = base + kStages * C::kStageBytes;
   float* scales = reinterpret_cast<float*>(boxes + C::kEpiBytes);   // [2 kSlots][2][128]
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(boxes + C::kEpiBytes + C::kScaleBytes);
-  uint64_t* empty_bar = full_bar + kStages;
+  uint64_t* empty_bar = full_bar + kFull;
   uint64_t* acc_full = empty_bar + kStages;   // [kSlots]
   uint64_t* acc_empty = acc_full + kSlots;    // [kSlots]
   uint64_t* mma_done = acc_empty + kSlots;    // [2]
@@ -150,6 +154,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
     *failed = 0;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full_bar[s], 1);
+      mbar_init(&full_bar[s + kStages], 1);
       mbar_init(&empty_bar[s], 1);
     }
     for (int b = 0; b < kSlots; ++b) {
@@ -190,25 +195,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
             }
             uint8_t* sa = base + s * C::kStageBytes;
             uint8_t* sb = sa + kTileBytes;
-            mbar_expect_tx(&full_bar[s], C::kStageBytes);
+            uint64_t* full = &full_bar[g % kFull];
+            mbar_expect_tx(full, C::kStageBytes);
             if (kb < p.nk) {
-              tma_load_2d(sa, &p.ta, &full_bar[s], kb * kBlk, m0);
+              tma_load_2d(sa, &p.ta, full, kb * kBlk, m0);
               if constexpr (TR) {
 #pragma unroll
                 for (int c = 0; c < BN / 128; ++c)
-                  tma_load_2d(sb + c * kTileBytes, &p.tb, &full_bar[s], n0 + c * 128, kb * kBlk);
+                  tma_load_2d(sb + c * kTileBytes, &p.tb, full, n0 + c * 128, kb * kBlk);
               } else {
-                tma_load_2d(sb, &p.tb, &full_bar[s], kb * kBlk, n0);
+                tma_load_2d(sb, &p.tb, full, kb * kBlk, n0);
               }
             } else {
-              tma_load_2d(sa, &p.tp, &full_bar[s], (kb - p.nk) * 32, m0);
-              tma_load_2d(sb, &p.tq, &full_bar[s], (kb - p.nk) * 32, n0);
+              tma_load_2d(sa, &p.tp, full, (kb - p.nk) * 32, m0);
+              tma_load_2d(sb, &p.tq, full, (kb - p.nk) * 32, n0);
             }
           }
         }
         // every issued load has landed before the CTA may exit
         for (int gg = (g > kStages ? g - kStages : 0); gg < g; ++gg)
-          if (!mbar_wait(&full_bar[gg % kStages], (uint32_t)(gg / kStages) & 1u, 1u, p.err)) break;
+          if (!mbar_wait(&full_bar[gg % kFull], (uint32_t)(gg / kFull) & 1u, 1u, p.err)) break;
       }
     } else if (warp <= 2) {
       if (lane == 0) {
@@ -220,13 +226,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
           for (int kb = 0; kb < nblk; ++kb, ++j) {
             if ((j & 1) != warp - 1) continue;   // the other MMA warp's block
             const int b = j % kSlots, use = j / kSlots, s = j % kStages;
-            // The accumulator first: once block j - kSlots has been read out, every load up to it
-            // has landed, the stage's last one (j - kStages) among them. Only then does the parity
-            // name this block's phase and not the one before it, which the other warp waited for.
-            static_assert(kStages >= kSlots && kSlots % 2 == 0, "phases of the stages");
-            if ((use >= 1 &&
-                 !mbar_wait_for(&acc_empty[b], (uint32_t)(use - 1) & 1u, 2u, p.err, p.wait_limit)) ||
-                !mbar_wait_for(&full_bar[s], (uint32_t)(j / kStages) & 1u, 2u, p.err, p.wait_limit)) {
+            if (!mbar_wait_for(&full_bar[j % kFull], (uint32_t)(j / kFull) & 1u, 2u, p.err, p.wait_limit) ||
+                (use >= 1 &&
+                 !mbar_wait_for(&acc_empty[b], (uint32_t)(use - 1) & 1u, 2u, p.err, p.wait_limit))) {
               ok = false;
               break;
             }
