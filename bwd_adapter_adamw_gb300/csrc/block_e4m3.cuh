@@ -35,14 +35,14 @@ __device__ __forceinline__ uint2 encode8(const uint4& v, float rcp) {
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
+// max |x| of 8 bf16 values, two at a time (a maximum of bf16 values is one of them; NaNs are passed
+// over, and reach their row through their codes)
 __device__ __forceinline__ float amax8(const uint4& v) {
-  const uint32_t h[4] = {v.x, v.y, v.z, v.w};
-  float m = 0.f;
+  const uint32_t h[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
+  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&h[0]);
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(h[e] << 16)),
-                       fabsf(__uint_as_float(h[e] & 0xFFFF0000u))));
-  return m;
+  for (int e = 1; e < 4; ++e) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&h[e]));
+  return fmaxf(__low2float(m), __high2float(m));
 }
 
 }  // namespace lora
