@@ -106,6 +106,8 @@ struct TileParams {
   int64_t T, N;
   int32_t nk, n_lora;           // K-blocks; 32-wide LoRA blocks (0: none)
   int32_t n_tiles, m_tiles, group_m, total;
+  int32_t splits;               // CTAs (of a cluster) that share a tile's blocks
+  __nv_bfloat16* Y;
   uint32_t* err;
   unsigned long long wait_limit;
   DropParams drop;
@@ -127,7 +129,7 @@ __device__ __forceinline__ void tile_at(const TileParams& p, int t, int32_t& m0,
 
 // MASK: the LoRA blocks are masked by dropout at (t, n); otherwise they are added like any other
 // block, with scale one.
-template <int BN, bool TR, bool MASK>
+template <int BN, bool TR, bool MASK, bool SPLIT>
 __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_constant__ TileParams p) {
   using C = TileCfg<BN>;
   constexpr int kStages = C::kStages;
@@ -173,7 +175,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
   const uint32_t tmem = *tmem_slot;
   grid_dep_sync();
 
-  const int nblk = p.nk + p.n_lora;   // blocks of a tile
+  // this CTA's blocks of its tiles: all, or a share of them
+  const int nblk = p.nk + p.n_lora, splits = SPLIT ? p.splits : 1;
+  const int split = SPLIT ? (int)blockIdx.x % splits : 0;
+  const int kb0 = SPLIT ? nblk * split / splits : 0, kb1 = SPLIT ? nblk * (split + 1) / splits : nblk;
   if (warp < 4) {
     // 384 threads start with 168 registers each; the epilogue takes what the other four warps leave:
     // 72 + 2 x 216 = 3 x 168
@@ -182,11 +187,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
       if (lane == 0) {
         int g = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < p.total && ok; t += gridDim.x) {
+        for (int t = (int)blockIdx.x / splits; t < p.total && ok; t += (int)gridDim.x / splits) {
           int32_t m0, nt;
           tile_at(p, t, m0, nt);
           const int n0 = nt * BN;
-          for (int kb = 0; kb < nblk; ++kb, ++g) {
+          for (int kb = kb0; kb < kb1; ++kb, ++g) {
             const int s = g % kStages;
             const uint32_t ph = (uint32_t)(g / kStages) & 1u;
             if (g >= kStages && !mbar_wait_for(&empty_bar[s], ph ^ 1u, 1u, p.err, p.wait_limit)) {
@@ -222,8 +227,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
         constexpr uint32_t id32 = idesc(kFmtTF32, 128, BN);
         int j = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < p.total && ok; t += gridDim.x) {
-          for (int kb = 0; kb < nblk; ++kb, ++j) {
+        for (int t = (int)blockIdx.x / splits; t < p.total && ok; t += (int)gridDim.x / splits) {
+          for (int kb = kb0; kb < kb1; ++kb, ++j) {
             if ((j & 1) != warp - 1) continue;   // the other MMA warp's block
             const int b = j % kSlots, use = j / kSlots, s = j % kStages;
             if (!mbar_wait_for(&full_bar[j % kFull], (uint32_t)(j / kFull) & 1u, 2u, p.err, p.wait_limit) ||
@@ -262,14 +267,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
       // had released its accumulator before block j - kSlots, already passed on, was begun.
       int j = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < p.total; t += gridDim.x) {
+      for (int t = (int)blockIdx.x / splits; t < p.total; t += (int)gridDim.x / splits) {
         int32_t m0, nt;
         tile_at(p, t, m0, nt);
         const float4* sx = reinterpret_cast<const float4*>(p.sx + m0) + lane;   // 4 rows per lane
         const int64_t nb0 = (int64_t)nt * BN / kBlk, nb1 = nb0 * kBlk + HC < p.N ? ((int64_t)nt * BN + HC) / kBlk : nb0;
-        float4 x = __ldg(sx);
-        float w0 = __ldg(p.sw + nb0 * p.sw_n), w1 = __ldg(p.sw + nb1 * p.sw_n);
-        for (int kb = 0; kb < nblk; ++kb, ++j) {
+        const int kf = kb0 < p.nk ? kb0 : 0;
+        float4 x = __ldg(sx + kf * (p.ld_sx / 4));
+        float w0 = __ldg(p.sw + nb0 * p.sw_n + kf * p.sw_k), w1 = __ldg(p.sw + nb1 * p.sw_n + kf * p.sw_k);
+        for (int kb = kb0; kb < kb1; ++kb, ++j) {
           float4* dst = reinterpret_cast<float4*>(scales + (j % (2 * kSlots)) * 256) + lane;
           if (kb < p.nk) {
             dst[0] = make_float4(x.x * w0, x.y * w0, x.z * w0, x.w * w0);
@@ -301,7 +307,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
     const int q = warp & 3, h = (warp - 4) >> 2;
     uint8_t* box0 = boxes + (warp - 4) * (BN / 64) * kBox;
     int j = 0;
-    for (int t = blockIdx.x; t < p.total; t += gridDim.x) {
+    for (int t = (int)blockIdx.x / splits; t < p.total; t += (int)gridDim.x / splits) {
       int32_t m0, nt;
       tile_at(p, t, m0, nt);
       const int64_t n0 = (int64_t)nt * BN + h * HC;
@@ -324,8 +330,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
 #pragma unroll
       for (int c = 0; c < HC / 2; ++c) acc[c] = 0;
       const uint32_t tcol = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * HC);
-      const int plain = MASK ? p.nk : nblk;
-      for (int kb = 0; kb < plain; ++kb, ++j) {
+      const int plain = MASK && kb1 > p.nk ? p.nk : kb1;
+      for (int kb = kb0; kb < plain; ++kb, ++j) {
         epi_barrier();
         fence_after();
         const float sf = scales[(j % (2 * kSlots)) * 256 + h * 128 + q * 32 + lane];
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
         }
       }
       if constexpr (MASK) {
-        for (int l = 0; l < p.n_lora; ++l, ++j) {
+        for (int kb = kb0 > p.nk ? kb0 : p.nk; kb < kb1; ++kb, ++j) {
           epi_barrier();
           fence_after();
           const uint32_t d = tcol + (uint32_t)(BN * (j % kSlots));
@@ -371,6 +377,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(&acc_empty[j % kSlots]);
         }
+      }
+      if constexpr (SPLIT) {   // the partial tile [BN][128], over the stages that every MMA has read
+        float* part = reinterpret_cast<float*>(base) + h * HC * 128 + q * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < HC / 2; ++c) {
+          float a, b;
+          unpack2(acc[c], a, b);
+          part[2 * c * 128] = a;
+          part[(2 * c + 1) * 128] = b;
+        }
+        break;
       }
       // rows past T and columns past N are clipped by the bulk store
       const int32_t wrow = m0 + q * 32;
@@ -402,6 +419,46 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
     __syncwarp();
     fence_before();
   }
+  if constexpr (SPLIT) {
+    __syncwarp();
+    // The partial tiles meet in distributed shared memory: this CTA adds an S-th of the tile, 4 rows
+    // x 8 columns per thread, in split order, so that reruns are bitwise equal.
+    cluster_sync_all();
+    if (warp >= 4 && *reinterpret_cast<volatile uint32_t*>(failed) == 0u) {
+      int32_t m0, nt;
+      tile_at(p, (int)blockIdx.x / splits, m0, nt);
+      const float* part = reinterpret_cast<const float*>(base);
+      for (int e = split * (kEpiWarps * 32) + (int)threadIdx.x - 128; e < 32 * (BN / 8);
+           e += p.splits * (kEpiWarps * 32)) {
+        // 8 lanes along the rows, so that their loads cover the banks once; 4 along the columns
+        const int r = (e >> 5) % 4 * 32 + (e & 7) * 4, c = ((e >> 5) / 4 * 4 + (e >> 3 & 3)) * 8;
+        const int64_t n = (int64_t)nt * BN + c;
+        if (m0 + r >= p.T || n >= p.N) continue;
+        float4 f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = dsmem_ld4(part + (c + i) * 128 + r, 0);
+        for (int k = 1; k < p.splits; ++k) {
+          float4 o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = dsmem_ld4(part + (c + i) * 128 + r, (uint32_t)k);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            f[i].x += o[i].x; f[i].y += o[i].y; f[i].z += o[i].z; f[i].w += o[i].w;
+          }
+        }
+        float v[4][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[0][i] = f[i].x; v[1][i] = f[i].y; v[2][i] = f[i].z; v[3][i] = f[i].w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (m0 + r + i < p.T) store8(p.Y + (int64_t)(m0 + r + i) * p.N + n, v[i]);
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();   // the peers have read this CTA's shared memory
+  }
   __syncthreads();
   if (warp == 1) {
     fence_after();
@@ -409,18 +466,61 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
   }
 }
 
-template <int BN, bool TR, bool MASK>
+constexpr int kMaxSplits = 8;   // portable cluster size
+
+template <int BN, bool TR, bool MASK, bool SPLIT>
 cudaError_t launch_tile(const TileParams& prm, cudaStream_t st) {
   static bool attr = false;
   if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(k_block_tile<BN, TR, MASK>,
+    cudaError_t e = cudaFuncSetAttribute(k_block_tile<BN, TR, MASK, SPLIT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<BN>::kSmem);
     if (e != cudaSuccess) return e;
     attr = true;
   }
   const int sms = sm_count();
-  return launch_kernel(k_block_tile<BN, TR, MASK>, (unsigned)(prm.total < sms ? prm.total : sms),
-                       kTileThreads, TileCfg<BN>::kSmem, st, prm);
+  if constexpr (!SPLIT)
+    return launch_kernel(k_block_tile<BN, TR, MASK, SPLIT>, (unsigned)(prm.total < sms ? prm.total : sms),
+                         kTileThreads, TileCfg<BN>::kSmem, st, prm);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(prm.total * prm.splits));
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = TileCfg<BN>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)prm.splits;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = add_pdl_attr(at, 1);
+  return cudaLaunchKernelEx(&cfg, k_block_tile<BN, TR, MASK, SPLIT>, prm);
+}
+
+// Clusters of `splits` CTAs (one per SM) that the device holds at once, per size (0: not known).
+int resident_clusters(int splits) {
+  static int known[kMaxSplits + 1];   // n + 1
+  if (known[splits] == 0) {
+    auto kernel = k_block_tile<128, false, false, true>;
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)splits);
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = TileCfg<128>::kSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)splits;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<128>::kSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    known[splits] = n + 1;
+  }
+  return known[splits] - 1;
 }
 
 cudaError_t run_tile(const BlockProductArgs& a, cudaStream_t st, int prof_kind) {
@@ -434,9 +534,28 @@ cudaError_t run_tile(const BlockProductArgs& a, cudaStream_t st, int prof_kind) 
   const int64_t mt = (a.T + 127) / 128;
   // rounds of tiles times a K-block's time: 0.48 us for 128 x 256, 0.37 us for 128 x 128 (the
   // smaller tile reads as many bytes of shared memory per output, and hands over twice as often)
+  const int64_t t128 = mt * ((N + 127) / 128);
   const int64_t r256 = (mt * ((N + 255) / 256) + sms - 1) / sms;
-  const int64_t r128 = (mt * ((N + 127) / 128) + sms - 1) / sms;
+  const int64_t r128 = (t128 + sms - 1) / sms;
   const int bn = 37 * r128 < 48 * r256 ? 128 : 256;
+  // Few tiles: a cluster shares each one's blocks. A round of 128 x 128 tiles takes 0.31 us per block
+  // then, S shares cost 1.6 + 0.7 S us for meeting (us with S = 1 / 2 / 3 / 4 / 6 / 8: 300 tokens 14336 ->
+  // 512 44.0 / 27.0 / 22.2 / 19.9 / 18.1 / 17.8; 129 tokens 9728 -> 2560 30.9 / 20.8 / 18.8; 129 tokens
+  // 2560 -> 2560 11.9 / 11.3 / 10.7; 512 tokens 1024 -> 1024 7.3 / 8.7). Only as long as every cluster
+  // is resident at once (300 tokens 2560 -> 1024, 24 clusters: 10.9 with 4, 17.0 with 6). Halves of
+  // a 128 x 256 tile never paid: its partial sums are twice as large.
+  int splits = 1;
+  if (bn == 128 && r128 == 1) {
+    const int64_t n = (K + kBlk - 1) / kBlk + (a.p ? (a.rank + 31) / 32 : 0);
+    int64_t best = 31 * n;
+    for (int s = 2; s <= kMaxSplits && s <= n && t128 * s <= sms; ++s) {
+      const int64_t us = 31 * ((n + s - 1) / s) + 160 + 70 * s;
+      if (us < best && t128 <= resident_clusters(s)) {
+        best = us;
+        splits = s;
+      }
+    }
+  }
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (!make_map_2d(&prm.ta, a.codes, u8, 1, K, a.T, K, 128, 128) ||
       !make_map_2d(&prm.tb, a.W8, u8, 1, a.in_dim, a.out_dim, a.in_dim, 128, a.transposed ? 128 : bn) ||
@@ -462,6 +581,8 @@ cudaError_t run_tile(const BlockProductArgs& a, cudaStream_t st, int prof_kind) 
   prm.group_m = prm.n_tiles > 16 ? 32 : 1;
   if ((int64_t)prm.n_tiles * mt > INT32_MAX) return cudaErrorInvalidValue;
   prm.total = (int32_t)(prm.n_tiles * mt);
+  prm.splits = splits;
+  prm.Y = static_cast<__nv_bfloat16*>(a.Y);
   prm.err = error_word();
   if (!prm.err) return cudaErrorInvalidDevice;
   prm.wait_limit = tc_wait_limit();
@@ -469,12 +590,15 @@ cudaError_t run_tile(const BlockProductArgs& a, cudaStream_t st, int prof_kind) 
   cudaError_t e;
   const bool mask = prm.n_lora > 0 && prm.drop.enabled;
   if (mask && !a.transposed) return cudaErrorInvalidValue;   // only the input gradient is masked
-  if (bn == 256)
-    e = mask ? launch_tile<256, true, true>(prm, st)
-             : a.transposed ? launch_tile<256, true, false>(prm, st) : launch_tile<256, false, false>(prm, st);
+  if (splits > 1)
+    e = mask ? launch_tile<128, true, true, true>(prm, st)
+             : a.transposed ? launch_tile<128, true, false, true>(prm, st) : launch_tile<128, false, false, true>(prm, st);
+  else if (bn == 256)
+    e = mask ? launch_tile<256, true, true, false>(prm, st)
+             : a.transposed ? launch_tile<256, true, false, false>(prm, st) : launch_tile<256, false, false, false>(prm, st);
   else
-    e = mask ? launch_tile<128, true, true>(prm, st)
-             : a.transposed ? launch_tile<128, true, false>(prm, st) : launch_tile<128, false, false>(prm, st);
+    e = mask ? launch_tile<128, true, true, false>(prm, st)
+             : a.transposed ? launch_tile<128, true, false, false>(prm, st) : launch_tile<128, false, false, false>(prm, st);
   if (e != cudaSuccess) return e;
   prof_end(prof_kind, st);
   return cudaGetLastError();

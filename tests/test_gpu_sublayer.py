@@ -40,7 +40,8 @@ def _problem(T, in_d, out_d, r, seed):
 @pytest.mark.parametrize("T,in_d,out_d,r,p", [(384, 256, 384, 16, 0.0), (512, 528, 256, 8, 0.1),
                                               (257, 1024, 528, 64, 0.0), (5, 272, 400, 36, 0.3),
                                               (130, 144, 1040, 4, 0.0),
-                                              (2048, 640, 2816, 64, 0.0), (2816, 2560, 384, 64, 0.2)])
+                                              (2048, 640, 2816, 64, 0.0), (2816, 2560, 384, 64, 0.2),
+                                              (200, 2064, 400, 64, 0.2), (140, 400, 4112, 36, 0.1)])
 def test_blk8_forward_backward(L, T, in_d, out_d, r, p):
     from bwd_adapter_adamw_gb300.step import Linear, LoraStep
     X, W, dY, A, B = _problem(T, in_d, out_d, r, T + in_d)
@@ -91,6 +92,25 @@ def test_blk8_from_checkpoint_codes_without_a_bf16_weight(L):
     assert rel_err(Y, S.block_product(X.float().numpy(), c, sc, False)[0] + f0.Y) <= TOL_BF16
 
 
+@pytest.mark.parametrize("T,in_d,out_d,dx", [(300, 14336, 512, False), (129, 2560, 1008, False),
+                                             (260, 528, 4112, True), (131, 1040, 272, False),
+                                             (140, 144, 2064, True), (640, 1936, 400, False)])
+def test_product_of_few_tiles_and_long_contractions(L, T, in_d, out_d, dx):
+    """Sizes whose tiles are shared by a cluster: against the oracle, and reruns bitwise equal."""
+    rng = np.random.default_rng(T + in_d)
+    X = _bf16(rng.standard_normal((T, out_d if dx else in_d)))
+    W = _bf16(rng.standard_normal((out_d, in_d)) / np.sqrt(in_d))
+    c, sc = S.quantize_blocks(W.float().numpy(), 128, 128)
+    cd, sd, Xd = torch.from_numpy(c).cuda(), torch.from_numpy(sc).cuda(), X.cuda()
+    ws = torch.empty(L.lora_block_product_workspace_size(T, out_d, in_d, dx), dtype=torch.uint8, device="cuda")
+    Y = [torch.full((T, in_d if dx else out_d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for y in Y:
+        L.lora_block_product(T, out_d, in_d, Xd, cd, sd, y, dx, ws)
+    assert L.lora_device_check() == L.LORA_OK
+    assert torch.equal(Y[0], Y[1])
+    assert rel_err(Y[0], S.block_product(X.float().numpy(), c, sc, dx)[0]) <= TOL_BF16
+
+
 def test_blk8_refusals(L):
     bad = lambda *a, **k: L.lora_prepared_weight_size(L.make_desc(*a, **k))   # noqa: E731
     assert bad(64, 64, 8, 1.0, L.LORA_BF16_BLK8) > 0
@@ -109,7 +129,7 @@ def test_blk8_refusals(L):
     assert e.value.status == L.LORA_ERR_UNSUPPORTED
 
 
-@pytest.mark.parametrize("T", [4, 40, 300])
+@pytest.mark.parametrize("T", [4, 40, 200, 300, 1000])
 def test_product_short_wait_bound_reports_timeout_and_recovers(L, T):
     """Waits shortened to one cycle run out on an ordinary launch: the status says so, and with the
     default bound the same call is right again."""
