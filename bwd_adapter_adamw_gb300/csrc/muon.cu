@@ -16,6 +16,11 @@
 //
 // s <= 16: CUDA cores, u in fp32 (k_muon_simt). Larger s: the two long products on tensor cores
 // (k_muon_tc), u as a two-term bf16 split, all four products of the terms kept.
+//
+// Measured: 22 layers of rank 8 (2048 + 256 columns) 15 us, a chain of passes and cluster barriers;
+// 32 layers of rank 64 (4096 + 14336 columns) 375 us, 755 MB at the least, 0.98 GB moved (the tiles
+// beyond the four that a CTA holds go through L2): bound by the latency of a tile's steps (load,
+// split, MMA, drain), one after the other, and by the small products, during which no tile moves.
 #include <algorithm>
 #include <atomic>
 
