@@ -78,11 +78,15 @@ __device__ __forceinline__ void fma2(uint64_t& a, uint64_t s, uint32_t d0, uint3
 //
 // Bound by the epilogue's reads of tensor memory: a block takes about 950 cycles against the
 // MMAs' 512, and the epilogue warps wait 14 of them for their next block and read for 790, beside
-// MMAs that themselves read and write the other accumulator. Wider reads (32 columns), scalar FMAs
-// and a fourth stage of operands measured the same or slower. 8192 x 4096 -> 14336 400 us (2400
+// MMAs that themselves read and write the other accumulator. Wider reads (32 columns), scalar FMAs,
+// sixteen epilogue warps of 64 columns (436 us) and a fourth stage of operands measured the same or
+// slower. 8192 x 4096 -> 14336 400 us (2400
 // TF/s; the per-row-scaled product, which reads its accumulator once per tile, runs at 2690).
 constexpr int kTileThreads = 384;
 constexpr int kEpiWarps = 8;
+constexpr int kLaunchRegs = 168, kIssueRegs = 72, kEpiRegs = 216;   // per thread
+static_assert(128 * kIssueRegs + 32 * kEpiWarps * kEpiRegs <= kTileThreads * kLaunchRegs,
+              "setmaxnreg draws on the block's own registers");
 constexpr int kBox = 32 * 64;   // 32 rows x 32 bf16 columns, 64-byte swizzle
 
 template <int BN>
@@ -186,9 +190,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
   const int split = SPLIT ? (int)blockIdx.x % splits : 0;
   const int kb0 = SPLIT ? nblk * split / splits : 0, kb1 = SPLIT ? nblk * (split + 1) / splits : nblk;
   if (warp < 4) {
-    // 384 threads start with 168 registers each; the epilogue takes what the other four warps leave:
-    // 72 + 2 x 216 = 3 x 168
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // the epilogue takes the registers that these four warps leave
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 0) {
       if (lane == 0) {
         int g = 0;
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int q = warp & 3, h = (warp - 4) >> 2;
     uint8_t* box0 = boxes + (warp - 4) * (BN / 64) * kBox;
     int j = 0;
@@ -480,7 +483,11 @@ cudaError_t launch_tile(const TileParams& prm, cudaStream_t st) {
   if (!attr) {
     cudaError_t e = cudaFuncSetAttribute(k_block_tile<BN, TR, MASK, SPLIT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<BN>::kSmem);
+    // a build that launches with fewer registers would wait for them forever
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, k_block_tile<BN, TR, MASK, SPLIT>);
     if (e != cudaSuccess) return e;
+    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
     attr = true;
   }
   const int sms = sm_count();
