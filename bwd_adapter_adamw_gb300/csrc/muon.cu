@@ -360,11 +360,28 @@ __global__ void __launch_bounds__(kMuonThreads) k_muon_simt(float* __restrict__ 
 //   Q X    rows are K-major A operands, B = [Q_hi; Q_lo] (N = 128): hi and lo into one
 //          accumulator, the two halves of its columns added in the epilogue
 constexpr int kTcThreads = 512;
-constexpr int kTcTiles = 4;                    // tiles held per CTA; others go through `spill`
+// A CTA has room for six tiles. Up to five are held (the sixth's room serves the small matrices). Of
+// more, three are held and the others go through `spill` and the three rooms left, two of them on
+// their way while one is in use.
+constexpr int kTcSlots = 6;
+constexpr int kTcHeld = 3;
+constexpr int kTcScr = kTcSlots - kTcHeld;
 constexpr int kTcTileBytes = 32 * 1024;
 constexpr int kTcAhead = 4;                    // tiles prefetched to L2 ahead of the one in use
-constexpr int kTcSmem = (kTcTiles + 2) * kTcTileBytes + 2 * 16 * 1024 + 256 + 1024;
+constexpr int kTcSmem = kTcSlots * kTcTileBytes + 2 * 16 * 1024 + 256 + 1024;
 static_assert(kTcSmem <= 227 * 1024, "shared memory per CTA");
+
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -405,6 +422,7 @@ struct TcArgs {
   const int32_t* status;
   uint8_t* spill;        // [CTA][spill_tiles][kTcTileBytes]
   int32_t spill_tiles;
+  int32_t held;          // tiles held per CTA: kTcSlots - 1, or kTcHeld where there are more
   int32_t zero_grads, C;
   uint32_t* err;
 };
@@ -478,19 +496,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
                                                              const MuonK hp, const TcArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* scratch = tiles + kTcTiles * kTcTileBytes;   // two spilled tiles; the first also two
-                                                        //   small matrices
-  uint8_t* qop = scratch + 2 * kTcTileBytes;            // [Q_hi; Q_lo] operand, or Q in fp32
+  uint8_t* scratch = tiles + kTcHeld * kTcTileBytes;    // kTcScr spilled tiles
+  uint8_t* small = tiles + (kTcSlots - 1) * kTcTileBytes;   // two small matrices, over the last room
+  uint8_t* qop = tiles + kTcSlots * kTcTileBytes;       // [Q_hi; Q_lo] operand, or Q in fp32
   float* g0 = reinterpret_cast<float*>(qop + 16 * 1024);   // Gram matrix
   float* sh = g0 + 64 * 64;                         // [20]
   uint64_t* bar_apply = reinterpret_cast<uint64_t*>(sh + 20);   // [2]
   uint64_t* bar_gram = bar_apply + 2;
-  uint64_t* bar_load = bar_gram + 1;   // [2]: a spilled tile is back
-  uint64_t* bar_used = bar_load + 2;   // [2]: a spilled tile's Gram products are done
-  uint64_t* bar_done = bar_used + 2;   // every MMA of this CTA is done
+  uint64_t* bar_load = bar_gram + 1;        // [kTcScr]: a spilled tile is back
+  uint64_t* bar_used = bar_load + kTcScr;   // [kTcScr]: a spilled tile's Gram products are done
+  uint64_t* bar_done = bar_used + kTcScr;   // every MMA of this CTA is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_done + 1);
   volatile uint32_t* failed = tmem_slot + 1;
-  float* t1 = reinterpret_cast<float*>(scratch);
+  float* t1 = reinterpret_cast<float*>(small);
   float* t2 = t1 + 64 * 64;
   float* qf = reinterpret_cast<float*>(qop);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -502,7 +520,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
     *failed = 0u;
     mbar_init(bar_gram, 1);
     mbar_init(bar_done, 1);
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kTcScr; ++b) {
       mbar_init(&bar_load[b], 1);
       mbar_init(&bar_used[b], 1);
     }
@@ -524,7 +542,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
   constexpr uint32_t id_gram = idesc(kFmtBF16, 128, 128, true, true);
   constexpr uint32_t id_apply = idesc(kFmtBF16, 128, 128);
   uint32_t ph_apply[2] = {0, 0}, ph_gram = 0;   // the same in every thread
-  uint32_t ph_load[2] = {0, 0}, ph_used[2] = {0, 0};   // of thread 0, which alone waits on them
+  uint32_t ph_load = 0, ph_used = 0;   // a bit per room, of thread 0, which alone waits on them
+  const int held = a.held;
   bool ok = true;                                      // no wait has run out of its bound
   // One warp polls, the others wait at the barrier: polling by all of them took most of the issue
   // slots. A wait that runs out of its bound marks the launch as failed: its parameters are not
@@ -558,29 +577,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
     float* m = a.M + mt.offset;
     const bool nesterov = hp.nesterov;
     const float mu_u = nesterov ? mu : 1.f, c_u = nesterov ? c : 0.f;   // u = c_u g + mu_u m
-    // Tile t of this CTA: held, or, while it is in use, in one of the two scratch tiles. Spilled tiles
-    // move by bulk copies of thread 0.
-    auto place = [&](int t) {
-      return t < kTcTiles ? tiles + t * kTcTileBytes : scratch + ((t - kTcTiles) & 1) * kTcTileBytes;
-    };
-    auto wait0 = [&](uint64_t* bar, uint32_t& ph) {   // thread 0
-      if (!mbar_wait_for(bar, ph, 2u, a.err, bound())) *failed = 1u;
-      ph ^= 1u;
+    // Tile t of this CTA: held, or, while it is in use, in room (t - held) % kTcScr of the scratch.
+    // Spilled tiles move by bulk copies of thread 0.
+    auto room = [&](int t) { return (t - held) % kTcScr; };
+    auto place = [&](int t) { return t < held ? tiles + t * kTcTileBytes : scratch + room(t) * kTcTileBytes; };
+    auto wait0 = [&](uint64_t* bars, uint32_t& ph, int b) {   // thread 0
+      if (!mbar_wait_for(&bars[b], (ph >> b) & 1u, 2u, a.err, bound())) *failed = 1u;
+      ph ^= 1u << b;
       fence_after();
     };
     auto begin_fetch = [&](int t) {
-      uint64_t* bar = &bar_load[(t - kTcTiles) & 1];
+      uint64_t* bar = &bar_load[room(t)];
       mbar_expect_tx(bar, kTcTileBytes);
       asm volatile(
           "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
               smem_u32(place(t))),
-          "l"(spill + (size_t)(t - kTcTiles) * kTcTileBytes), "r"(kTcTileBytes), "r"(smem_u32(bar)), "l"(keep)
+          "l"(spill + (size_t)(t - held) * kTcTileBytes), "r"(kTcTileBytes), "r"(smem_u32(bar)), "l"(keep)
           : "memory");
     };
-    auto end_fetch = [&](int t) { wait0(&bar_load[(t - kTcTiles) & 1], ph_load[(t - kTcTiles) & 1]); };
+    auto end_fetch = [&](int t) { wait0(bar_load, ph_load, room(t)); };
     auto begin_flush = [&](int t) {   // after publish
       asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;" ::"l"(
-                       spill + (size_t)(t - kTcTiles) * kTcTileBytes),
+                       spill + (size_t)(t - held) * kTcTileBytes),
                    "r"(smem_u32(place(t))), "r"(kTcTileBytes), "l"(keep)
                    : "memory");
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -589,16 +607,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       asm volatile("fence.proxy.async;" ::: "memory");
     };
-    // The scratch tile of a pass's spilled tile is free: its user two spilled tiles earlier in the pass
-    // has been copied out and its Gram products are done (the one between has not begun its copy).
-    auto scratch_free = [&](int t) {
-      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      wait0(&bar_used[(t - kTcTiles) & 1], ph_used[(t - kTcTiles) & 1]);
+    // The room of a pass's spilled tile is free: its user kTcScr spilled tiles earlier in the pass has
+    // been copied out and its Gram products are done. In the first pass one later copy has begun by
+    // then, in the others none.
+    auto room_free = [&](int t, bool first_pass) {
+      if (first_pass) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      wait0(bar_used, ph_used, room(t));
     };
-    // the last one or two uses of the scratch tiles, at the end of a pass
+    // the last uses of the rooms, at the end of a pass
     auto drain_used = [&]() {
-      const int n = nt - kTcTiles;   // spilled tiles
-      for (int k = 0; k < min(n, 2); ++k) wait0(&bar_used[k], ph_used[k]);
+      for (int k = 0; k < min(nt - held, kTcScr); ++k) wait0(bar_used, ph_used, k);
     };
     auto gram_mma = [&](const uint8_t* tile, bool begin) {   // thread 0
       const uint64_t d = smem_desc_sw128_mn(smem_u32(tile), 16 * 1024);
@@ -716,12 +735,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
         for (int un = 0; un < 2; ++un) put_split8(hi, lo, row[un], ch[un], w + 8 * un);
       }
       // the next tile's room, checked while this tile is finished; publish tells the other threads
-      if (tid == 0 && t + 1 < nt && t + 1 >= kTcTiles + 2) scratch_free(t + 1);
+      if (tid == 0 && t + 1 < nt && t + 1 >= held + kTcScr) room_free(t + 1, true);
       publish();
       if (tid == 0) {
         gram_mma(hi, t == 0);
-        if (t >= kTcTiles) {
-          umma_commit(&bar_used[(t - kTcTiles) & 1]);
+        if (t >= held) {
+          umma_commit(&bar_used[room(t)]);
           begin_flush(t);
         }
         if (t + 1 == nt) {
@@ -816,7 +835,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
             publish();
             for (int t = 0; t < nt; ++t) {
               uint32_t* w = reinterpret_cast<uint32_t*>(place(t));
-              if (tid == 0 && t >= kTcTiles) {
+              if (tid == 0 && t >= held) {
                 begin_fetch(t);
                 end_fetch(t);
               }
@@ -832,11 +851,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
               publish();
               if (tid == 0) {
                 gram_mma(place(t), t == 0);
-                if (t >= kTcTiles) {
-                  umma_commit(&bar_used[(t - kTcTiles) & 1]);
+                if (t >= held) {
+                  umma_commit(&bar_used[room(t)]);
                   begin_flush(t);
                   end_flushes();
-                  wait0(&bar_used[(t - kTcTiles) & 1], ph_used[(t - kTcTiles) & 1]);
+                  wait0(bar_used, ph_used, room(t));
                 }
                 if (t + 1 == nt) umma_commit(bar_gram);
               }
@@ -892,8 +911,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       backwards = !backwards;
       auto order = [&](int i) { return backwards ? nt - 1 - i : i; };
       if (tid == 0 && nt > 0) {
-        if (nt > kTcTiles) begin_fetch(backwards ? nt - 1 : kTcTiles);
-        if (order(0) < kTcTiles) apply_mma(place(order(0)), 0);
+        for (int k = 0; k < min(nt - held, kTcScr - 1); ++k) begin_fetch(backwards ? nt - 1 - k : held + k);
+        if (order(0) < held) apply_mma(place(order(0)), 0);
       }
       // The parameters of a tile are on their way while the tile before it is updated. A thread's are
       // four 16-byte vectors, 512 threads apart (tall), or 16 rows of a column, four apart (wide).
@@ -920,21 +939,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
         if (tid >= 256)
           for (int i = 1; i < min(kTcAhead, nt); ++i) prefetch(p, order(i), tid & 255);
       }
+      bool early = false;   // thread 0: a spilled tile's products have begun
       for (int i = 0; i < nt; ++i) {
         const int t = order(i), next = i + 1 < nt ? order(i + 1) : INT32_MAX;   // the latter: none
         if (last && tid >= 256 && i + kTcAhead < nt) prefetch(p, order(i + kTcAhead), tid & 255);
         const int buf = i & 1;
         uint8_t* tile = place(t);
         if (tid == 0) {
-          if (t >= kTcTiles) {
-            end_fetch(t);
-            apply_mma(tile, buf);
-            if (next < nt && next >= kTcTiles) {   // over the spilled tile before this one
-              if (!last && (backwards ? nt - 1 - t : t - kTcTiles) >= 1) scratch_free(next);
-              begin_fetch(next);
+          if (t >= held) {
+            if (!early) {
+              end_fetch(t);
+              apply_mma(tile, buf);
+            }
+            // the tile kTcScr - 1 ahead, into the room of the spilled tile before this one
+            const int k = backwards ? nt - 1 - t : t - held, f = order(i + kTcScr - 1);
+            if (k + kTcScr - 1 < nt - held) {
+              if (!last && k >= 1) room_free(f, false);
+              begin_fetch(f);
             }
           }
-          if (next < kTcTiles) apply_mma(place(next), buf ^ 1);
+          // the next tile's products run while this one is read, if it is there
+          early = false;
+          if (next < held) {
+            apply_mma(place(next), buf ^ 1);
+          } else if (next < nt && mbar_test(&bar_load[room(next)], (ph_load >> room(next)) & 1u)) {
+            end_fetch(next);
+            apply_mma(place(next), buf ^ 1);
+            early = true;
+          }
         }
         wait(&bar_apply[buf], ph_apply[buf]);
         ph_apply[buf] ^= 1u;
@@ -953,8 +985,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
           publish();
           if (tid == 0) {
             gram_mma(tile, i == 0);
-            if (t >= kTcTiles) {
-              umma_commit(&bar_used[(t - kTcTiles) & 1]);
+            if (t >= held) {
+              umma_commit(&bar_used[room(t)]);
               begin_flush(t);
             }
             if (i + 1 == nt) {
@@ -1087,9 +1119,9 @@ int muon_cluster(const MuonMat& m, int n_mats) {
 size_t muon_spill_bytes(const MuonMat& m, int C, int n) {
   if (m.s <= 16) return 0;
   const int64_t tiles = ((m.n + 127) / 128 + C - 1) / C;
-  if (tiles <= kTcTiles) return 0;
+  if (tiles < kTcSlots) return 0;
   const int64_t ctas = (int64_t)std::max(1, std::min(n, kMuonMaxCtas / C)) * C;
-  return (size_t)ctas * (tiles - kTcTiles) * kTcTileBytes;
+  return (size_t)ctas * (tiles - kTcHeld) * kTcTileBytes;
 }
 
 cudaError_t launch_muon(float* p, float* g, float* m, const MuonTab& tab, const MuonK& hp,
@@ -1113,7 +1145,8 @@ cudaError_t launch_muon(float* p, float* g, float* m, const MuonTab& tab, const 
   a.scale_norm = scale_norm; a.status = status;
   a.spill = static_cast<uint8_t*>(spill);
   const int64_t tiles = ((n + 127) / 128 + C - 1) / C;
-  a.spill_tiles = (int32_t)std::max<int64_t>(0, tiles - kTcTiles);
+  a.held = tiles < kTcSlots ? kTcSlots - 1 : kTcHeld;
+  a.spill_tiles = (int32_t)std::max<int64_t>(0, tiles - a.held);
   a.zero_grads = zero_grads; a.C = C;
   a.err = error_word();
   if (!a.err) return cudaErrorInvalidDevice;
