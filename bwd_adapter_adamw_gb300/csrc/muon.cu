@@ -18,8 +18,8 @@
 // (k_muon_tc), u as a two-term bf16 split, all four products of the terms kept.
 //
 // Measured: 22 layers of rank 8 (2048 + 256 columns) 15 us, a chain of passes and cluster barriers;
-// 32 layers of rank 64 (4096 + 14336 columns) 375 us, 755 MB at the least, 0.98 GB moved (the tiles
-// beyond the four that a CTA holds go through L2): bound by the latency of a tile's steps (load,
+// 32 layers of rank 64 (4096 + 14336 columns) 370 us, 755 MB at the least, 0.98 GB moved (the tiles
+// beyond those that a CTA holds go through L2): bound by the latency of a tile's steps (load,
 // split, MMA, drain), one after the other, and by the small products, during which no tile moves.
 #include <algorithm>
 #include <atomic>
@@ -443,9 +443,11 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const float (&a)[4], flo
 // D = gamma A B + beta E + alpha I (alpha on the first s of the diagonal) for commuting symmetric
 // matrices, D one of them or another, 16 warps: warp w the rows 16 (w % 4) .. and columns
 // 16 (w / 4) .., three tf32 products of a two-term split (about 2^-21). Thread-level tensor-core
-// instructions fit here: the operands are fp32 in shared memory already, and the product is bound
-// by latency (tcgen05 would need split operands written out and a trip through tensor memory each
-// time). Not inlined: one copy of its code serves the fourteen products of an update.
+// instructions fit here: the operands are fp32 in shared memory already (tcgen05 would need split
+// operands written out and a trip through tensor memory each time). Bound by their latency: 4700
+// cycles a product at s = 64; the upper triangle alone (two blocks in turn for some warps) took
+// 5600, fp32 FMAs 6000, three chains of accumulators instead of one 5000. Not inlined: one copy of
+// its code serves the fourteen products of an update.
 __device__ __noinline__ void small_product(float* D, const float* A, const float* B, const float* E, int s,
                                            float alpha, float beta, float gamma) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -821,9 +823,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       float inv = 1.f;
       if (done == 0) {   // X = u / ||u||, ||u||^2 = trace G
         auto trace = [&]() {
-          float tr = 0.f;
-          for (int i = 0; i < s; ++i) tr += g0[mat_at(i, i)];
-          return tr;
+          float tr = g0[mat_at(lane, lane)] + g0[mat_at(lane + 32, lane + 32)];   // zeros past s
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) tr += __shfl_xor_sync(0xffffffffu, tr, o);
+          return tr;   // the same in every lane
         };
         float tr = trace();
         if (!(tr > 1e-18f && tr < 1e30f)) {
