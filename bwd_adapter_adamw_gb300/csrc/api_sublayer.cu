@@ -75,8 +75,8 @@ int check_mats(int32_t n_mats, const lora_mat* mats, const GroupTab* groups) {
 }
 
 // The matrices in the order of their launches: by kernel (smaller side at most 16, each of its own,
-// or above) and falling length. A launch takes a run of equal keys; the cluster size is the largest
-// that one of the kernel's matrices asks for, so that the matrices of a call share one launch.
+// or above) and falling length. A launch takes a run of equal keys; a kernel's matrices have one
+// cluster size, so that those of a call share one launch.
 struct MuonOrder {
   int32_t at;      // index into the caller's table
   int32_t key;     // cluster size and smaller side (0: above 16)
@@ -97,12 +97,15 @@ std::vector<MuonOrder> muon_order(int32_t n_mats, const lora_mat* mats) {
     t.group = e.group;
     v[i].at = i;
     v[i].key = t.s <= 16 ? t.s : 0;
-    cluster[v[i].key] = std::max(cluster[v[i].key], muon_cluster(t, n_mats));
+    if (v[i].key) cluster[v[i].key] = std::max(cluster[v[i].key], muon_cluster_simt(t, n_mats));
   }
-  for (MuonOrder& e : v) e.key += 32 * cluster[e.key];
   std::stable_sort(v.begin(), v.end(), [](const MuonOrder& a, const MuonOrder& b) {
     return a.key != b.key ? a.key < b.key : a.m.n > b.m.n;
   });
+  std::vector<int64_t> n;   // of the tensor cores' matrices, which come first
+  for (int32_t i = 0; i < n_mats && v[i].key == 0; ++i) n.push_back(v[i].m.n);
+  if (!n.empty()) cluster[0] = muon_cluster_tc(n.data(), (int)n.size());
+  for (MuonOrder& e : v) e.key += 32 * cluster[e.key];
   return v;
 }
 

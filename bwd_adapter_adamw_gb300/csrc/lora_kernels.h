@@ -460,7 +460,8 @@ struct MuonK {
 };
 constexpr int kMuonMaxCtas = 152;      // CTAs of a persistent launch of the tensor-core form
 // CTAs of the cluster that takes a matrix, with n_mats matrices in the call
-int muon_cluster(const MuonMat& m, int n_mats);
+int muon_cluster_simt(const MuonMat& m, int n_mats);
+int muon_cluster_tc(const int64_t* n, int count);
 // workspace of a launch over n such matrices (tiles that do not fit on chip)
 size_t muon_spill_bytes(const MuonMat& m, int C, int n);
 // One launch: the table's matrices share the cluster size C, and their smaller sides are all

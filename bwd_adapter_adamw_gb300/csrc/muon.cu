@@ -1105,18 +1105,33 @@ cudaError_t run_simt(float* p, float* g, float* m, const MuonTab& tab, const Muo
 
 }  // namespace
 
-// CTAs of a matrix's cluster. CUDA cores: 512 columns a CTA. Tensor cores: small clusters, since
-// every CTA repeats the products of the small matrices and clusters of 16 leave SMs without a
-// place (32 matrices 64 x 14336: 571 us with 16 CTAs each, five or six clusters at a time); as
-// many as the call needs to use every SM, and at least a tile per CTA.
-int muon_cluster(const MuonMat& m, int n_mats) {
+// CTAs of a matrix's cluster on CUDA cores: 512 columns a CTA, fewer while there are SMs left.
+int muon_cluster_simt(const MuonMat& m, int n_mats) {
   int C = 1;
-  if (m.s <= 16) {
-    while (C < 16 && (m.n > 512 * (int64_t)C || (n_mats * C * 2 <= 152 && m.n > 128 * C))) C *= 2;
-  } else {
-    while (C < 16 && n_mats * C < 152 && m.n > 128 * (int64_t)C) C *= 2;
-  }
+  while (C < 16 && (m.n > 512 * (int64_t)C || (n_mats * C * 2 <= 152 && m.n > 128 * C))) C *= 2;
   return C;
+}
+
+// On tensor cores, for the `count` matrices of a call with long axes n in falling order: the size
+// whose first cluster, which takes every R-th matrix (R: clusters resident at once), is done first. A
+// matrix costs a tile's time for each tile of a CTA and about six more, the chain of its small
+// products and cluster barriers, which every CTA repeats (us with the next power of two that filled
+// the SMs / with this rule: 24 matrices of 2560 and 1024 112 / 78, 44 of 2048 116 / 90, 64 of 4096 219 / 180, 4
+// layers of 4096 and 14336 161 / 147; 32 such layers 370 either way).
+int muon_cluster_tc(const int64_t* n, int count) {
+  constexpr int kResident[5] = {152, 76, 37, 17, 5};   // of 1, 2, 4, 8, 16 CTAs
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int k = 0; k < 5; ++k) {
+    const int C = 1 << k;
+    int64_t cost = 0;
+    for (int i = 0; i < count; i += kResident[k]) cost += 6 + ((n[i] + 127) / 128 + C - 1) / C;
+    if (cost < least) {
+      least = cost;
+      best = C;
+    }
+  }
+  return best;
 }
 
 size_t muon_spill_bytes(const MuonMat& m, int C, int n) {
