@@ -829,6 +829,9 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<NT, FUSED>::kPerSm)
         }
       }
       fence_before();
+      // the scales' reads come before the copy that overwrites them (another proxy: the arrive alone
+      // does not order them, and late reads found the scales of block i + kStages)
+      if constexpr (!FUSED) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&acc_empty[b]);

@@ -352,7 +352,10 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
         if ((threadIdx.x & 31) == 0) sh[buf][r][warp] = make_float2(s1[r], s2[r]);
       }
     }
-    __syncthreads();   // the sums are in place, and every thread has read the buffer
+    // the sums are in place, and every thread has read the buffer (its reads come before the next
+    // copy, which is of another proxy)
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
     if (threadIdx.x == 0 && ok) fill(s, t0 + ring * step);
     if (++s == ring) {
       s = 0;

@@ -111,6 +111,54 @@ def test_product_of_few_tiles_and_long_contractions(L, T, in_d, out_d, dx):
     assert rel_err(Y[0], S.block_product(X.float().numpy(), c, sc, dx)[0]) <= TOL_BF16
 
 
+@pytest.mark.parametrize("T,in_d,out_d,dx", [(29, 3456, 10816, False), (100, 3456, 10816, False),
+                                             (29, 3456, 10816, True), (500, 2560, 4096, False),
+                                             (8, 2560, 4096, False)])
+def test_product_reruns_are_bitwise_equal(L, T, in_d, out_d, dx):
+    """Many reruns, alone and on three streams at once: a stage that is overwritten before its last
+    reader is done shows as a few different elements."""
+    g = torch.Generator(device="cuda").manual_seed(T + in_d)
+    X = torch.randn(T, out_d if dx else in_d, generator=g, device="cuda").to(torch.bfloat16)
+    X[:, ::64] *= 20
+    W = (torch.randn(out_d, in_d, generator=g, device="cuda") / in_d ** 0.5).to(torch.bfloat16)
+    c = torch.empty(out_d, in_d, dtype=torch.uint8, device="cuda")
+    sc = torch.empty(-(-out_d // 128), -(-in_d // 128), device="cuda")
+    L.lora_block_quantize_weight(W, out_d, in_d, c, sc)
+    n, streams = L.lora_block_product_workspace_size(T, out_d, in_d, dx), [torch.cuda.Stream() for _ in range(3)]
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in streams]
+    Y = [torch.empty(T, in_d if dx else out_d, dtype=torch.bfloat16, device="cuda") for _ in streams]
+    L.lora_block_product(T, out_d, in_d, X, c, sc, Y[0], dx, ws[0])
+    want = Y[0].clone()
+    torch.cuda.synchronize()
+    for k in range(150):
+        for st, w, y in list(zip(streams, ws, Y))[:1 if k < 75 else 3]:
+            with torch.cuda.stream(st):
+                for _ in range(3):
+                    L.lora_block_product(T, out_d, in_d, X, c, sc, y, dx, w)
+        torch.cuda.synchronize()
+        for y in Y[:1 if k < 75 else 3]:
+            assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T,dim,dt", [(2100, 4096, torch.bfloat16), (2100, 2048, torch.float32), (700, 8192, torch.bfloat16)])
+def test_norm_backward_reruns_are_bitwise_equal(L, T, dim, dt):
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    x, dy = (torch.randn(T, dim, generator=g, device="cuda").to(dt) for _ in range(2))
+    gamma, st = torch.rand(dim, generator=g, device="cuda"), torch.empty(T, 2, device="cuda")
+    d = L.make_norm_desc(dim, L.LORA_NORM_LAYER, L.LORA_BF16 if dt == torch.bfloat16 else L.LORA_F32)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    ws = torch.empty(L.lora_norm_backward_workspace_size(d, T), dtype=torch.uint8, device="cuda")
+    L.lora_norm_forward(d, T, x, gamma, None, y, st)
+    want = None
+    for _ in range(100):
+        dg, db = torch.zeros(dim, device="cuda"), torch.zeros(dim, device="cuda")
+        for a, b, out in ((dg, db, dx), (dg, db, None)):   # the second: the token sums alone
+            L.lora_norm_backward(d, T, x, gamma, dy, st, None, out, a, b, ws)
+        got = (dx.clone(), dg, db)
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_blk8_refusals(L):
     bad = lambda *a, **k: L.lora_prepared_weight_size(L.make_desc(*a, **k))   # noqa: E731
     assert bad(64, 64, 8, 1.0, L.LORA_BF16_BLK8) > 0
