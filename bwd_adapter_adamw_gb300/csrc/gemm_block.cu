@@ -350,11 +350,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
         tmem_ldc(d, r0);
 #pragma unroll
         for (int c = 0; c < HC / 16; c += 2) {
-          tmem_wait_ld();
+          tmem_wait_ld(r0);
           tmem_ldc(d + (uint32_t)((c + 1) * 16), r1);
 #pragma unroll
           for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], s, r0[2 * i], r0[2 * i + 1]);
-          tmem_wait_ld();
+          tmem_wait_ld(r1);
           if (c + 2 < HC / 16) {
             tmem_ldc(d + (uint32_t)((c + 2) * 16), r0);
           } else {   // this warp has read its part of the buffer
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
           for (int c = 0; c < HC / 16; ++c) {
             uint32_t r[16];
             tmem_ldc(d + (uint32_t)(c * 16), r);
-            tmem_wait_ld();
+            tmem_wait_ld(r);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               if (!(keep[c / 2] >> (16 * (c & 1) + i) & 1u)) r[i] = 0u;
@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<NT, FUSED>::kPerSm)
         uint32_t r[CH];
         const uint32_t d = tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(b * NT + c * CH);
         tmem_ldc(d, r);
-        tmem_wait_ld();
+        tmem_wait_ld(r);
 #pragma unroll
         for (int v = 0; v < CH; v += 4) {
           const float4 f = sc[(c * CH + v) / 4];

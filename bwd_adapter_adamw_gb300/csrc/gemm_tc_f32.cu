@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_gemm_f32(const __grid_consta
         uint32_t big[16], small[16];
         tmem_ld16_nw(reg + (uint32_t)(h * 16), big);
         tmem_ld16_nw(reg + 128u + (uint32_t)(h * 16), small);
-        tmem_wait_ld();
+        tmem_wait_ld(big);
+        tmem_hold(small);
         if (masked) {
           // dropout-masked LoRA term: keep bits first (a rolled loop: the hash is register-heavy)
           uint32_t keep = 0u;
