@@ -167,3 +167,22 @@ def test_oracle_newton_schulz():
     # the cubic-quintic (2, -1.5, 0.5) converges to the orthogonal factor
     y, _ = S.newton_schulz(u, (2.0, -1.5, 0.5), 40)
     assert np.allclose(y, U @ V, atol=1e-9) and gain > 1.0
+
+
+def test_block_scaled_base_sizes_and_refusals(L):
+    """dtype LORA_BF16_BLK8: one copy of codes with a scale per block; no DoRA, no slots, no fused group."""
+    d = L.make_desc(272, 400, 8, 1.0, L.LORA_BF16_BLK8)
+    assert L.lora_prepared_weight_size(d) == 400 * 272 + 4 * 4 * 3
+    assert L.lora_workspace_size(d, 100) > 0
+    for bad in (L.make_desc(24, 64, 8, 1.0, L.LORA_BF16_BLK8), L.make_desc(64, 40, 8, 1.0, L.LORA_BF16_BLK8),
+                L.make_desc(64, 64, 8, 1.0, L.LORA_BF16_BLK8, dora=True),
+                L.make_desc(64, (1 << 20) + 16, 8, 1.0, L.LORA_BF16_BLK8)):
+        assert L.lora_prepared_weight_size(bad) == 0 and L.lora_workspace_size(bad, 16) == 0
+    assert L.lora_dora_norm_workspace_size(d) == 0
+    F = 1 << 20   # never touched: every call is refused on the host
+    for args, status in (((d, None, 4, F, None, None, F, F, None, None, F, F, F, 1 << 30), L.LORA_ERR_INVALID),
+                         ((d, None, 4, F, None, F, F, F, None, None, F, F, F, 16), L.LORA_ERR_WORKSPACE),
+                         ((d, None, 4, F + 2, None, F, F, F, None, None, F, F, F, 1 << 30), L.LORA_ERR_ALIGN)):
+        with pytest.raises(L.LoraError) as e:
+            L.lora_forward(*args, stream=0)
+        assert e.value.status == status
