@@ -448,34 +448,41 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
   }
 }
 
-// dst[c] += sum over the CTAs of part[CTA][k][c]: 32 interleaved runs in CTA order, then the runs in
-// a fixed tree. A thread's whole run is in flight at once.
-constexpr int kRedRuns = 32;
+// dst[c] += sum over the CTAs of part[CTA][k][c]: interleaved runs in CTA order, then the runs in a
+// fixed tree. A thread's whole run, at most ten partials, is in flight at once; few partials take few
+// runs (256 x 4096 bf16, dX and both sums: 9.9 us with 32 runs, 7.6 with 8).
+constexpr int kRedRun = 10;
 constexpr int kRedMost = 2 * 152;   // most CTAs of k_norm_bwd
-__global__ void __launch_bounds__(32 * kRedRuns) k_norm_reduce(const float* __restrict__ part, int n, int dim,
-                                                               float* dgamma, float* dbeta) {
+template <int RUNS>
+__global__ void __launch_bounds__(32 * RUNS) k_norm_reduce(const float* __restrict__ part, int n, int dim,
+                                                           float* dgamma, float* dbeta) {
+  static_assert(RUNS == 8 || RUNS == 32, "a warp adds the runs of 32 / RUNS columns");
   grid_dep_sync();
-  __shared__ float sh[kRedRuns][33];
+  __shared__ float sh[RUNS][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;
   float* dst = blockIdx.y ? dbeta : dgamma;
   if (!dst) return;
   const float* p = part + (int64_t)blockIdx.y * dim + c;
-  float v[(kRedMost + kRedRuns - 1) / kRedRuns];
+  float v[kRedRun];
 #pragma unroll
-  for (int k = 0; k < (kRedMost + kRedRuns - 1) / kRedRuns; ++k) {
-    const int i = ty + k * kRedRuns;
+  for (int k = 0; k < kRedRun; ++k) {
+    const int i = ty + k * RUNS;
     v[k] = c < dim && i < n ? __ldcg(p + (int64_t)i * 2 * dim) : 0.f;
   }
   float s = 0.f;
 #pragma unroll
-  for (int k = 0; k < (kRedMost + kRedRuns - 1) / kRedRuns; ++k) s += v[k];
+  for (int k = 0; k < kRedRun; ++k) s += v[k];
   sh[ty][tx] = s;
   __syncthreads();
-  s = warp_sum(sh[tx][ty]);   // warp ty: column ty of the block
-  const int cc = blockIdx.x * 32 + ty;
-  if (tx == 0 && cc < dim) dst[cc] += s;
+  // warp ty: columns ty 32 / RUNS .., RUNS lanes each
+  const int col = ty * (32 / RUNS) + tx / RUNS, cc = blockIdx.x * 32 + col;
+  s = sh[tx % RUNS][col];
+#pragma unroll
+  for (int o = RUNS / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (tx % RUNS == 0 && cc < dim) dst[cc] += s;
 }
+static_assert(32 * kRedRun >= kRedMost, "the partials fit the runs");
 
 template <typename E, int WPR, int NV, int R = 1>
 cudaError_t fwd_launch(const NormArgs& a, cudaStream_t st) {
@@ -537,15 +544,28 @@ cudaError_t bwd_launch(const NormArgs& a, int grid, cudaStream_t st) {
       1.f / (float)a.dim, a.rms, want, ring, err);
   if (e != cudaSuccess || !(want & 6)) return e;
   prof_begin(0, st);
-  return launch_kernel(k_norm_reduce, dim3((unsigned)((a.dim + 31) / 32), 2), 32 * kRedRuns, 0, st, a.part,
-                       grid, (int)a.dim, a.dgamma, a.dbeta);
+  const dim3 blocks((unsigned)((a.dim + 31) / 32), 2);
+  return grid <= 8 * kRedRun
+             ? launch_kernel(k_norm_reduce<8>, blocks, 256, 0, st, a.part, grid, (int)a.dim, a.dgamma, a.dbeta)
+             : launch_kernel(k_norm_reduce<32>, blocks, 1024, 0, st, a.part, grid, (int)a.dim, a.dgamma, a.dbeta);
+}
+
+// Threads of a CTA and of a row of a backward pass.
+void norm_bwd_shape(int64_t dim, int dtype, int64_t& th, int64_t& tpr) {
+  const int64_t nvec = dim / (dtype == LORA_BF16 ? 8 : 4);
+  th = nvec <= 512 ? 256 : 512;
+  tpr = 32;
+  while (2 * tpr < nvec && tpr < th) tpr *= 2;
 }
 
 // Rows per thread of a backward pass: two where a CTA has many groups of them, so that a wait and a
-// barrier serve both (8192 x 4096 bf16 38.9 -> 35.3 us, 8192 x 2048 fp32 37.9 -> 31.8).
+// barrier serve both (8192 x 4096 bf16 38.9 -> 35.3 us, 8192 x 2048 fp32 37.9 -> 31.8, 2048 x 4096
+// 17.9 -> 17.3; 1023 x 4096 11.8 -> 14.2, 2048 x 1024 7.5 -> 9.3).
 int norm_bwd_rows(int64_t dim, int dtype, int64_t T) {
   const int64_t nvec = dim / (dtype == LORA_BF16 ? 8 : 4);
-  return nvec > 32 && nvec <= 512 && T >= 2048 ? 2 : 1;
+  int64_t th, tpr;
+  norm_bwd_shape(dim, dtype, th, tpr);
+  return nvec > 32 && nvec <= 512 && T * tpr / th >= 6 * kRedMost ? 2 : 1;
 }
 
 template <typename E>
@@ -570,13 +590,11 @@ cudaError_t bwd_type(const NormArgs& a, cudaStream_t st) {
 // threads, and few enough that a CTA has four groups of rows (the partials are 8 bytes per column
 // and CTA, a row 6 or 12).
 int norm_bwd_parts(int64_t dim, int dtype, int64_t T) {
-  const int64_t nvec = dim / (dtype == LORA_BF16 ? 8 : 4);
-  const int64_t th = nvec <= 512 ? 256 : 512;
-  int64_t tpr = 32;
-  while (2 * tpr < nvec && tpr < th) tpr *= 2;
+  int64_t th, tpr;
+  norm_bwd_shape(dim, dtype, th, tpr);
   const int64_t per = th / tpr * norm_bwd_rows(dim, dtype, T);
   const int64_t groups = (T + per - 1) / per;
-  const int64_t most = nvec <= 512 ? kRedMost : kRedMost / 2;
+  const int64_t most = th == 256 ? kRedMost : kRedMost / 2;
   const int64_t want = (groups + 3) / 4;
   return (int)(want < most ? want : most);
 }
