@@ -173,6 +173,25 @@ def test_update_does_not_depend_on_the_gradients_size(L, rows, cols, size):
     pr.check()
 
 
+@pytest.mark.parametrize("size", [1e-30, 1.0, 1e30])
+@pytest.mark.parametrize("rows,cols", [(64, 10240), (12288, 64), (40, 14336), (64, 30000)])
+def test_tiles_past_the_chips_room(L, rows, cols, size):
+    """One matrix whose CTAs hold all their tiles, or move some through memory, also where u is
+    rescaled on its way."""
+    pr = Problem(L, [(rows, cols, "A", 0)], seed=11, momentum=False,
+                 grad=lambda rng, r, c: _grad(rng, r, c) * size)
+    pr.run()
+    pr.check()
+
+
+def test_long_chains_of_matrices(L):
+    """More matrices than clusters, of unequal lengths: the CTAs go from one to the next."""
+    mats = [(64, 2048 + 128 * (i % 5), "A", 0) for i in range(90)] + [(700 + 60 * i, 48, "B", 1) for i in range(70)]
+    pr = Problem(L, mats, seed=12)
+    pr.run(zero=True)
+    pr.check(zero=True)
+
+
 @pytest.mark.parametrize("kw", [dict(steps=1), dict(steps=2), dict(steps=3), dict(steps=4),
                                 dict(steps=8), dict(nesterov=False), dict(adjust=1),
                                 dict(coef=(2.0, -1.5, 0.5), steps=6)])
