@@ -597,12 +597,12 @@ def lora_device_check(stream=None) -> int:
 
 
 def lora_set_wait_limit(cycles: int) -> None:
-    """Test hook: bound of the frozen products' pipeline waits (0 = the default)."""
+    """Test hook: bound of the tensor-core kernels' pipeline waits (0 = the default)."""
     _check(_lib.lora_set_wait_limit(int(cycles)), "lora_set_wait_limit")
 
 
 def lora_device_error(reset: bool = False) -> int:
-    """Device error bits of the tensor-core products (0 = none); synchronous."""
+    """Device error bits of the tensor-core kernels (0 = none); synchronous."""
     v = C.c_uint32(0)
     _check(_lib.lora_device_error(C.byref(v), 1 if reset else 0), "lora_device_error")
     return v.value

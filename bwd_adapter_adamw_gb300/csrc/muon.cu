@@ -425,6 +425,7 @@ struct TcArgs {
   int32_t held;          // tiles held per CTA: kTcSlots - 1, or kTcHeld where there are more
   int32_t zero_grads, C;
   uint32_t* err;
+  unsigned long long wait_limit;   // bound of the pipeline waits (cycles); the drains keep kWaitCycles
 };
 
 // The small matrices are [64][64] fp32 with the 16-byte chunks of a row spread by the row (no bank
@@ -545,17 +546,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
   constexpr uint32_t id_apply = idesc(kFmtBF16, 128, 128);
   uint32_t ph_apply[2] = {0, 0}, ph_gram = 0;   // the same in every thread
   uint32_t ph_load = 0, ph_used = 0;   // a bit per room, of thread 0, which alone waits on them
+  uint32_t fetching = 0;               // thread 0: rooms with a copy on its way
   const int held = a.held;
-  bool ok = true;                                      // no wait has run out of its bound
-  // One warp polls, the others wait at the barrier: polling by all of them took most of the issue
-  // slots. A wait that runs out of its bound marks the launch as failed: its parameters are not
-  // written, and the waits that follow are short.
-  auto bound = [&]() { return ok ? kWaitCycles : 1ull << 22; };
+  // A wait that runs out of its bound marks its CTA: once a thread knows of it (`ok`), it begins no copy and
+  // no product, waits no more and writes no parameters, but keeps up with the cluster's barriers. With the
+  // next Gram matrix the whole cluster learns of it and leaves (`gone`), so that an invalid matrix is never
+  // used: each element of the parameters holds its update or is as it was.
+  bool ok = true, gone = false;
+  // One warp polls, the others wait at the barrier: polling by all of them took most of the issue slots.
   auto wait = [&](uint64_t* bar, uint32_t ph) {
-    if (warp == 0 && !mbar_wait_for(bar, ph, 2u, a.err, bound())) *failed = 1u;
+    if (warp == 0 && !(ok && mbar_wait_strict(bar, ph, 2u, a.err, a.wait_limit))) *failed = 1u;
     __syncthreads();
     ok = *failed == 0u;
     fence_after();
+  };
+  // whether a CTA of the cluster is marked; after a barrier of the cluster, and none waits before the next
+  auto marked = [&]() {
+    const float* f = reinterpret_cast<const float*>(const_cast<const uint32_t*>(failed));
+    return __any_sync(0xffffffffu, lane < C && __float_as_uint(dsmem_ld(f, (uint32_t)lane)) != 0u);
   };
   // every thread's writes to shared memory become visible to the tensor cores and bulk copies
   auto publish = [&]() {
@@ -584,11 +592,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
     auto room = [&](int t) { return (t - held) % kTcScr; };
     auto place = [&](int t) { return t < held ? tiles + t * kTcTileBytes : scratch + room(t) * kTcTileBytes; };
     auto wait0 = [&](uint64_t* bars, uint32_t& ph, int b) {   // thread 0
-      if (!mbar_wait_for(&bars[b], (ph >> b) & 1u, 2u, a.err, bound())) *failed = 1u;
-      ph ^= 1u << b;
+      const bool done = mbar_wait_strict(&bars[b], (ph >> b) & 1u, 2u, a.err, a.wait_limit);
+      if (done) {
+        ph ^= 1u << b;
+      } else {
+        *failed = 1u;
+        ok = false;
+      }
       fence_after();
+      return done;
     };
     auto begin_fetch = [&](int t) {
+      fetching |= 1u << room(t);
       uint64_t* bar = &bar_load[room(t)];
       mbar_expect_tx(bar, kTcTileBytes);
       asm volatile(
@@ -597,7 +612,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
           "l"(spill + (size_t)(t - held) * kTcTileBytes), "r"(kTcTileBytes), "r"(smem_u32(bar)), "l"(keep)
           : "memory");
     };
-    auto end_fetch = [&](int t) { wait0(bar_load, ph_load, room(t)); };
+    auto end_fetch = [&](int t) {
+      if (wait0(bar_load, ph_load, room(t))) fetching &= ~(1u << room(t));
+    };
     auto begin_flush = [&](int t) {   // after publish
       asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;" ::"l"(
                        spill + (size_t)(t - held) * kTcTileBytes),
@@ -737,9 +754,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
         for (int un = 0; un < 2; ++un) put_split8(hi, lo, row[un], ch[un], w + 8 * un);
       }
       // the next tile's room, checked while this tile is finished; publish tells the other threads
-      if (tid == 0 && t + 1 < nt && t + 1 >= held + kTcScr) room_free(t + 1, true);
+      if (tid == 0 && ok && t + 1 < nt && t + 1 >= held + kTcScr) room_free(t + 1, true);
       publish();
-      if (tid == 0) {
+      if (tid == 0 && ok) {
         gram_mma(hi, t == 0);
         if (t >= held) {
           umma_commit(&bar_used[room(t)]);
@@ -753,7 +770,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       }
     }
 
-    // G of the tiles (the Gram products in D_gram), summed over the cluster, in g0
+    // G of the tiles (the Gram products in D_gram), summed over the cluster, in g0; invalid once `gone`
     auto gram_all = [&]() {
       if (nt > 0) {
         wait(bar_gram, ph_gram);
@@ -793,10 +810,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
         fence_before();
       }
       __syncthreads();
-      if (C > 1) {
+      if (C == 1) {
+        gone = *failed != 0u;
+      } else {
         // CTA r adds an r-th of the matrix over the ranks, then every CTA gathers the parts
         const int per = 1024 / C;
         cluster_sync();
+        gone = marked();
         for (int e = tid; e < per; e += kTcThreads) {
           const int at = rank * per + e;
           float4 v = dsmem_ld4(g0 + at * 4, 0);
@@ -820,6 +840,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       const int left = hp.steps - done;
       const int now = left % kStageSteps ? left % kStageSteps : kStageSteps;
       gram_all();
+      if (gone) break;
       float inv = 1.f;
       if (done == 0) {   // X = u / ||u||, ||u||^2 = trace G
         auto trace = [&]() {
@@ -838,7 +859,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
             publish();
             for (int t = 0; t < nt; ++t) {
               uint32_t* w = reinterpret_cast<uint32_t*>(place(t));
-              if (tid == 0 && t >= held) {
+              if (tid == 0 && ok && t >= held) {
                 begin_fetch(t);
                 end_fetch(t);
               }
@@ -852,7 +873,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
               for (int e = tid; e < kTcTileBytes / 4; e += kTcThreads)
                 w[e] = pack_bf16(__uint_as_float(w[e] << 16) * pre, __uint_as_float(w[e] & 0xFFFF0000u) * pre);
               publish();
-              if (tid == 0) {
+              if (tid == 0 && ok) {
                 gram_mma(place(t), t == 0);
                 if (t >= held) {
                   umma_commit(&bar_used[room(t)]);
@@ -864,12 +885,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
               }
               __syncthreads();
             }
-            if (pass == 0) pre = range_scale<kTcThreads>(mx, sh, C);
+            if (pass == 0) {
+              pre = range_scale<kTcThreads>(mx, sh, C);
+              if (C > 1) cluster_sync();
+              gone = marked();
+              if (C > 1) cluster_sync();
+              else __syncthreads();
+              if (gone) break;
+            }
           }
-          if (pre != 1.f) {
+          if (!gone && pre != 1.f) {
             gram_all();
             tr = trace();
           }
+          if (gone) break;
         }
         inv = tr > 0.f ? 1.f / sqrtf(tr) : 0.f;
         __syncthreads();
@@ -913,7 +942,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       // a pass begins with the spilled tiles that were written last.
       backwards = !backwards;
       auto order = [&](int i) { return backwards ? nt - 1 - i : i; };
-      if (tid == 0 && nt > 0) {
+      if (tid == 0 && ok && nt > 0) {
         for (int k = 0; k < min(nt - held, kTcScr - 1); ++k) begin_fetch(backwards ? nt - 1 - k : held + k);
         if (order(0) < held) apply_mma(place(order(0)), 0);
       }
@@ -948,7 +977,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
         if (last && tid >= 256 && i + kTcAhead < nt) prefetch(p, order(i + kTcAhead), tid & 255);
         const int buf = i & 1;
         uint8_t* tile = place(t);
-        if (tid == 0) {
+        if (tid == 0 && ok) {
           if (t >= held) {
             if (!early) {
               end_fetch(t);
@@ -986,7 +1015,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
 #pragma unroll
           for (int q = 0; q < 2; ++q) put_split8(tile, tile + 16 * 1024, jrow, ih * 2 + q, x + q * 8);
           publish();
-          if (tid == 0) {
+          if (tid == 0 && ok) {
             gram_mma(tile, i == 0);
             if (t >= held) {
               umma_commit(&bar_used[room(t)]);
@@ -1040,10 +1069,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_muon_tc(const __grid_constant
       }
     }
     __syncthreads();
+    if (gone) break;
   }
-  // every MMA is done before the tensor memory is freed (after a failed wait nothing else says so);
-  // the peers are done with this CTA's memory
+  // every copy and every MMA is done before the tensor memory is freed (after a failed wait nothing else
+  // says so); the peers are done with this CTA's memory
   if (tid == 0) {
+    for (int b = 0; b < kTcScr; ++b)
+      if (fetching >> b & 1u) mbar_wait(&bar_load[b], (ph_load >> b) & 1u, 2u, a.err);
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     umma_commit(bar_done);
     mbar_wait(bar_done, 0u, 2u, a.err);
   }
@@ -1168,6 +1201,7 @@ cudaError_t launch_muon(float* p, float* g, float* m, const MuonTab& tab, const 
   a.zero_grads = zero_grads; a.C = C;
   a.err = error_word();
   if (!a.err) return cudaErrorInvalidDevice;
+  a.wait_limit = tc_wait_limit();
   return launch_clusters(k_muon_tc, kTcThreads, kTcSmem, tab.n, C, kMuonMaxCtas, st, tab, hp, a);
 }
 

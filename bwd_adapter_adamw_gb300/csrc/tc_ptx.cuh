@@ -62,6 +62,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   return mbar_wait_for(bar, parity, err_bit, err, kWaitCycles);
 }
 
+// The same for short waits: under a bound below the default (a test's) an attempt that succeeds too late
+// counts as failed, since one attempt takes microseconds, within which most waits end.
+__device__ __forceinline__ bool mbar_wait_strict(uint64_t* bar, uint32_t parity, uint32_t err_bit, uint32_t* err,
+                                                 unsigned long long limit) {
+  const bool strict = limit < kWaitCycles;
+  unsigned long long t0 = strict ? clock64() : 0ull;
+  if (mbar_try_wait(bar, parity) && !strict) return true;
+  if (!strict) t0 = clock64();
+  do {
+    if (clock64() - t0 > limit) {
+      atomicOr(err, err_bit);
+      return false;
+    }
+  } while (!mbar_try_wait(bar, parity));
+  return true;
+}
+
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int32_t c0, int32_t c1) {
   asm volatile(

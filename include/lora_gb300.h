@@ -362,7 +362,9 @@ typedef struct lora_muon_hp {
  *   A: p -= lr s X + lr wd p      B: p -= lr plus_ratio s X       (p before the update in the decay)
  * lr is the group's; zero_grads != 0 clears the matrices' gradients after reading them. Elements
  * of the arenas outside the matrices (DoRA magnitudes, norm weights) are not touched: give them
- * to lora_adamw_step in a group of their own. Matrices must not overlap; any number of them. */
+ * to lora_adamw_step in a group of their own. Matrices must not overlap; any number of them.
+ * When lora_device_check reports LORA_ERR_TIMEOUT after it, every element of the parameters holds its
+ * update or is as it was; m (and the gradients, where they are cleared) may be those of either. */
 size_t lora_muon_workspace_size(int32_t n_mats, const lora_mat* mats);
 int lora_muon_step(float* params, float* grads, float* m, int32_t n_groups,
                    const lora_group* groups, int32_t n_mats, const lora_mat* mats,
@@ -518,7 +520,7 @@ uint64_t lora_launch_counter(void);
 /* Text of the last CUDA error an entry point of this library reported as LORA_ERR_CUDA in the
  * calling thread ("no error" if none). */
 const char* lora_last_cuda_error(void);
-/* Error bits raised on the device by the tensor-core products when a pipeline wait ran out of
+/* Error bits raised on the device by the tensor-core kernels when a pipeline wait ran out of
  * its bound (bit 0 loads, bit 1 MMA, bit 2 epilogue): the kernel then skipped its remaining
  * work, released its tensor memory and returned, so the output is invalid. Synchronous (reads
  * a device word of the current device); reset != 0 clears it. */
@@ -532,7 +534,8 @@ int lora_device_error(uint32_t* flags, int32_t reset);
  * state changes; here the same rule for a stalled kernel). */
 int lora_device_check(void* stream);
 /* Test hook: bound, in SM clock cycles, of the pipeline waits of the frozen-product kernels
- * (bf16 and E4M3) launched after this call; 0 restores the default (2^33 cycles, seconds).
+ * (bf16 and E4M3) and of the orthogonalised update launched after this call; 0 restores the default
+ * (2^33 cycles, seconds).
  * Process-wide, not thread-safe with concurrent launches. A small bound makes a correct launch
  * give up: its error bits are set and its outputs are invalid. Waits that drain work already
  * issued (copies in flight, MMAs before the tensor memory is freed) keep the default bound, so
