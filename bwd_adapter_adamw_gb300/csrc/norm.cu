@@ -239,7 +239,8 @@ template <typename E, int TH, int TPR, int NV, int R>
 __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
     k_norm_bwd(const E* __restrict__ X, const float* __restrict__ gamma, const E* __restrict__ dY,
                const float2* __restrict__ stats, const E* dX_add, E* dX, float* __restrict__ part,
-               int64_t T, int dim, float inv_dim, int rms, int want, int ring, uint32_t* err) {
+               int64_t T, int dim, float inv_dim, int rms, int want, int ring, uint32_t* err,
+               unsigned long long wait_limit) {
   grid_dep_sync();
   constexpr int N = Pack<E>::N;
   constexpr int RPB = TH / TPR * R;   // rows of a group; a thread's R rows are row, row + TH / TPR, ..
@@ -247,6 +248,8 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
   extern __shared__ __align__(16) uint8_t bufs[];   // [ring][X | dY][RPB][dim]; then the column sums
   __shared__ float2 sh[2][R][TH / 32];
   __shared__ uint64_t full[kBwdRing];
+  __shared__ uint32_t mark;              // a wait of this CTA has run out
+  volatile uint32_t* failed = &mark;
   const int row = threadIdx.x / TPR, col = threadIdx.x % TPR;
   const int warp = threadIdx.x >> 5;
   const int nvec = dim / N;
@@ -268,6 +271,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
           : "memory");
   };
   if (threadIdx.x == 0) {
+    *failed = 0u;
     for (int s = 0; s < ring; ++s) tc::mbar_init(&full[s], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
   __syncthreads();   // the barriers are set up
   int buf = 0, s = 0;
   uint32_t phase = 0;
-  bool ok = true;
+  bool ok = true;   // from the barrier of a group on, the same in every thread: no wait has run out
   for (int64_t t0 = t_first; t0 < T; t0 += step, buf ^= 1) {
     float2 sc[R];
 #pragma unroll
@@ -305,7 +309,10 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
       const int64_t t = t0 + row + r * (TH / TPR);
       sc[r] = t < T ? __ldg(stats + t) : make_float2(0.f, 0.f);
     }
-    ok = ok && tc::mbar_wait(&full[s], phase, 1u, err);
+    if (ok && !tc::mbar_wait_strict(&full[s], phase, 1u, err, wait_limit)) {
+      *failed = 1u;
+      ok = false;
+    }
     waited += ok;
     uint4 xc[R][NV], yc[R][NV];
     f2 hk[R][kHold ? NV * P : 1], gk[R][kHold ? NV * P : 1];
@@ -356,6 +363,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
     // copy, which is of another proxy)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
+    ok = *failed == 0u;
     if (threadIdx.x == 0 && ok) fill(s, t0 + ring * step);
     if (++s == ring) {
       s = 0;
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int64_t t = t0 + row + r * (TH / TPR);
-      if (t >= T) continue;
+      if (t >= T || !ok) continue;
       const float c1 = rms ? 0.f : s1[r] * inv_dim * sc[r].y, c2 = s2[r] * inv_dim * sc[r].y;
       const f2 m = mk2(-sc[r].x, -sc[r].x), q = mk2(sc[r].y, sc[r].y);
       const f2 n1 = mk2(-c1, -c1), n2 = mk2(-c2, -c2);
@@ -415,6 +423,11 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1)
     for (; waited < filled; ++waited)
       if (!tc::mbar_wait(&full[waited % ring], (uint32_t)(waited / ring) & 1u, 1u, err)) break;
   if (!(want & 6)) return;
+  // sums that lack rows are not passed on: a NaN, which the gradients' preparation rejects
+  if (!ok) {
+#pragma unroll
+    for (int j = 0; j < NV * P; ++j) dg[j] = db[j] = mk2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
+  }
   float* out = part + (int64_t)blockIdx.x * 2 * dim;
   float* comb = reinterpret_cast<float*>(bufs);   // every copy has landed and been read
 #pragma unroll
@@ -541,7 +554,7 @@ cudaError_t bwd_launch(const NormArgs& a, int grid, cudaStream_t st) {
       k_norm_bwd<E, TH, TPR, NV, R>, (unsigned)grid, TH, (size_t)smem, st, static_cast<const E*>(a.X),
       a.gamma, static_cast<const E*>(a.dY), reinterpret_cast<const float2*>(a.stats),
       static_cast<const E*>(a.dX_add), static_cast<E*>(a.dX), a.part, a.T, (int)a.dim,
-      1.f / (float)a.dim, a.rms, want, ring, err);
+      1.f / (float)a.dim, a.rms, want, ring, err, tc_wait_limit());
   if (e != cudaSuccess || !(want & 6)) return e;
   prof_begin(0, st);
   const dim3 blocks((unsigned)((a.dim + 31) / 32), 2);

@@ -312,7 +312,9 @@ int lora_block_quantize(const void* src, int64_t rows, int64_t K, uint8_t* codes
  * once. beta may be NULL (no shift); dX_add [T, dim] (the residual branch's gradient) may be NULL
  * and may be dX itself; dgamma, dbeta and dX may be NULL each (not all). The token sums are
  * reduced in a fixed order: reruns are bitwise equal. dim a multiple of 8 (LORA_ERR_ALIGN) and at
- * most LORA_NORM_MAX_DIM, T below 2^31 - 256 (LORA_ERR_UNSUPPORTED); T = 0 is a no-op. */
+ * most LORA_NORM_MAX_DIM, T below 2^31 - 256 (LORA_ERR_UNSUPPORTED); T = 0 is a no-op.
+ * When lora_device_check reports LORA_ERR_TIMEOUT after a backward pass, rows of dX may be as they were
+ * and dgamma and dbeta are NaN (which lora_grad_prepare rejects), never sums that lack rows. */
 #define LORA_NORM_LAYER 0
 #define LORA_NORM_RMS 1
 #define LORA_NORM_MAX_DIM 16384
@@ -534,8 +536,8 @@ int lora_device_error(uint32_t* flags, int32_t reset);
  * state changes; here the same rule for a stalled kernel). */
 int lora_device_check(void* stream);
 /* Test hook: bound, in SM clock cycles, of the pipeline waits of the frozen-product kernels
- * (bf16 and E4M3) and of the orthogonalised update launched after this call; 0 restores the default
- * (2^33 cycles, seconds).
+ * (bf16 and E4M3), the norms' backward pass and the orthogonalised update launched after this call;
+ * 0 restores the default (2^33 cycles, seconds).
  * Process-wide, not thread-safe with concurrent launches. A small bound makes a correct launch
  * give up: its error bits are set and its outputs are invalid. Waits that drain work already
  * issued (copies in flight, MMAs before the tensor memory is freed) keep the default bound, so

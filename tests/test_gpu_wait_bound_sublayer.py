@@ -65,3 +65,41 @@ def test_update_writes_right_parameters_or_none(L, mats, size):
     again.run(zero=True)
     assert L.lora_device_check() == L.LORA_OK
     assert torch.equal(again.p, new.p) and torch.equal(again.m, new.m)
+
+
+@pytest.mark.parametrize("T,dim,dtype", [(2100, 4096, "bf16"), (1023, 2048, "f32"), (700, 8192, "bf16"),
+                                         (3000, 256, "bf16"), (40, 16384, "f32")])
+def test_norm_backward_writes_right_rows_and_no_partial_sums(L, T, dim, dtype):
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    x, dy = (torch.randn(T, dim, generator=g, device="cuda").to(dt) for _ in range(2))
+    gamma, st = torch.rand(dim, generator=g, device="cuda"), torch.empty(T, 2, device="cuda")
+    d = L.make_norm_desc(dim, L.LORA_NORM_LAYER, L.LORA_BF16 if dtype == "bf16" else L.LORA_F32)
+    L.lora_norm_forward(d, T, x, gamma, None, torch.empty_like(x), st)
+    ws = torch.empty(L.lora_norm_backward_workspace_size(d, T), dtype=torch.uint8, device="cuda")
+    dx, grads = torch.empty_like(x), torch.empty(2 * dim, device="cuda")
+
+    def call():
+        dx.fill_(77.0)
+        grads.fill_(1.0)
+        L.lora_norm_backward(d, T, x, gamma, dy, st, None, dx, grads[:dim], grads[dim:], ws)
+
+    call()
+    want, sums = dx.clone(), grads.clone()
+    seen = []
+    for limit in LIMITS:
+        seen.append(_short(L, limit, call))
+        assert bool(((dx == 77.0) | (dx == want)).all())
+        if seen[-1] == L.LORA_OK:
+            assert torch.equal(dx, want) and torch.equal(grads, sums)
+        else:
+            assert bool(torch.isnan(grads).all())
+            groups = L.make_groups([dict(offset=0, n_mag=2 * dim, grad_scale=1.0, max_norm=1.0, lr=1e-3, step=0)])
+            sn, status = torch.zeros(2, dtype=torch.float64, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+            pw = torch.empty(L.lora_grad_prepare_workspace_size(groups), dtype=torch.uint8, device="cuda")
+            L.lora_grad_prepare(grads, groups, sn, status, pw)
+            assert status.item() == L.LORA_ERR_NONFINITE
+    assert seen[0] == L.LORA_ERR_TIMEOUT
+    call()
+    assert L.lora_device_check() == L.LORA_OK
+    assert torch.equal(dx, want) and torch.equal(grads, sums)
