@@ -46,6 +46,8 @@ __device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t (&r)[32]) 
       : "r"(taddr));
 }
 
+constexpr uint64_t kNan2 = 0x7FFFFFFF7FFFFFFFull;   // a pair of NaNs
+
 __device__ __forceinline__ void tmem_ldc(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32_nw(taddr, r); }
 __device__ __forceinline__ void tmem_ldc(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16_nw(taddr, r); }
 
@@ -389,10 +391,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_block_tile(const __grid_con
       }
       if constexpr (SPLIT) {   // the partial tile [BN][128], over the stages that every MMA has read
         float* part = reinterpret_cast<float*>(base) + h * HC * 128 + q * 32 + lane;
+        // after a wait that ran out a NaN, which no sum with it hides
+        const bool lost = *reinterpret_cast<volatile uint32_t*>(failed) != 0u;
 #pragma unroll
         for (int c = 0; c < HC / 2; ++c) {
           float a, b;
-          unpack2(acc[c], a, b);
+          unpack2(lost ? kNan2 : acc[c], a, b);
           part[2 * c * 128] = a;
           part[(2 * c + 1) * 128] = b;
         }
@@ -706,6 +710,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<NT, FUSED>::kPerSm)
   if constexpr (FUSED) grid_dep_sync();   // X and the weight may come from the kernel before this one
 
   uint64_t acc[NT / 2];
+  bool lost = false;   // epilogue: a wait has run out
   if (warp == 4) {
     if (lane == 0) {
       // Not fused: the weight does not depend on the kernel before this one (the quantisation of X,
@@ -812,7 +817,10 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<NT, FUSED>::kPerSm)
         ready = mbar_wait_for(&full_bar[s], (uint32_t)(i / kStages) & 1u, 4u, p.err, p.wait_limit);
       }
       ready = ready && mbar_wait_for(&acc_full[b], (uint32_t)(i >> 1) & 1u, 4u, p.err, p.wait_limit);
-      if (!__all_sync(0xffffffffu, ready)) break;
+      if (!__all_sync(0xffffffffu, ready)) {
+        lost = true;
+        break;
+      }
       fence_after();
       const float4* sc = reinterpret_cast<const float4*>(scales + (FUSED ? i : s) * NT);
 #pragma unroll
@@ -846,7 +854,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<NT, FUSED>::kPerSm)
 #pragma unroll
     for (int c = 0; c < NT / 2; ++c) {
       float a, b;
-      unpack2(acc[c], a, b);
+      unpack2(lost ? kNan2 : acc[c], a, b);   // (no sum with a NaN hides it)
       part[2 * c * 128 + warp * 32 + lane] = a;
       part[(2 * c + 1) * 128 + warp * 32 + lane] = b;
     }

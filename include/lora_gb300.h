@@ -283,7 +283,9 @@ int lora_adamw_step(float* params, float* grads, float* m, float* v, int32_t n_g
  * Both directions read the same codes, so the gradient is that of the forward's weight, and one
  * copy of the weight serves both. A row of X holding a NaN or an infinity gives a NaN row of Y
  * and touches no other row. T from 1 (one decoded token) up; in_dim and out_dim multiples of 16
- * (LORA_ERR_ALIGN), T below 2^31 - 256 and dimensions at most 2^20 (LORA_ERR_UNSUPPORTED). */
+ * (LORA_ERR_ALIGN), T below 2^31 - 256 and dimensions at most 2^20 (LORA_ERR_UNSUPPORTED).
+ * When lora_device_check reports LORA_ERR_TIMEOUT after it, an element of Y holds its value, is NaN or is
+ * as it was. */
 #define LORA_SCALE_BLOCK 128
 size_t lora_block_product_workspace_size(int64_t T, int64_t out_dim, int64_t in_dim,
                                          int32_t transposed);

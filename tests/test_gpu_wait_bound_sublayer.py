@@ -103,3 +103,36 @@ def test_norm_backward_writes_right_rows_and_no_partial_sums(L, T, dim, dtype):
     call()
     assert L.lora_device_check() == L.LORA_OK
     assert torch.equal(dx, want) and torch.equal(grads, sums)
+
+
+# the fused and the streaming form, tiles shared by a cluster, tiles of 128 and of 256 outputs
+@pytest.mark.parametrize("dx", [False, True])
+@pytest.mark.parametrize("T,out_d,in_d", [(1, 2560, 4096), (8, 2560, 4096), (12, 2560, 4096), (37, 2560, 9728),
+                                          (100, 4096, 2560), (129, 2560, 2560), (300, 512, 7168), (1000, 2560, 4096)])
+def test_product_writes_right_values_or_none(L, T, out_d, in_d, dx):
+    g = torch.Generator(device="cuda").manual_seed(T + in_d)
+    X = torch.randn(T, out_d if dx else in_d, generator=g, device="cuda").to(torch.bfloat16)
+    W = (torch.randn(out_d, in_d, generator=g, device="cuda") / in_d ** 0.5).to(torch.bfloat16)
+    c = torch.empty(out_d, in_d, dtype=torch.uint8, device="cuda")
+    sc = torch.empty(-(-out_d // 128), -(-in_d // 128), device="cuda")
+    L.lora_block_quantize_weight(W, out_d, in_d, c, sc)
+    ws = torch.empty(L.lora_block_product_workspace_size(T, out_d, in_d, dx), dtype=torch.uint8, device="cuda")
+    Y = torch.empty(T, in_d if dx else out_d, dtype=torch.bfloat16, device="cuda")
+
+    def call():
+        Y.fill_(1e30)
+        L.lora_block_product(T, out_d, in_d, X, c, sc, Y, dx, ws)
+
+    old = torch.full_like(Y, 1e30)
+    call()
+    want = Y.clone()
+    seen = []
+    for limit in LIMITS * 3:
+        seen.append(_short(L, limit, call))
+        assert bool(((Y == want) | (Y == old) | torch.isnan(Y)).all())
+        if seen[-1] == L.LORA_OK:
+            assert torch.equal(Y, want)
+    assert seen[0] == L.LORA_ERR_TIMEOUT
+    call()
+    assert L.lora_device_check() == L.LORA_OK
+    assert torch.equal(Y, want)
