@@ -59,7 +59,7 @@ int check_mats(int32_t n_mats, const lora_mat* mats, const GroupTab* groups) {
     if (groups) {
       if (e.group >= groups->n) return LORA_ERR_INVALID;
       const int64_t lo = groups->offset[e.group], hi = lo + groups->count[e.group];
-      if (e.offset < lo || e.offset + s * n > hi) return LORA_ERR_INVALID;
+      if (e.offset < lo || e.offset > hi || s * n > hi - e.offset) return LORA_ERR_INVALID;   // (no overflow)
     }
     if (i && e.offset < mats[i - 1].offset + mats[i - 1].rows * mats[i - 1].cols) sorted = false;
   }
