@@ -2,6 +2,7 @@
 // the orthogonalised update. Everything is checked on the host before anything is enqueued.
 #include <algorithm>
 #include <cmath>
+#include <new>
 #include <vector>
 
 #include "api_util.h"
@@ -115,6 +116,77 @@ int32_t muon_run(const std::vector<MuonOrder>& v, int32_t at) {   // matrices of
   return n;
 }
 
+// f(), or `bad` where the host's memory runs out: no exception leaves a C entry point.
+template <typename R, typename F>
+R no_throw(R bad, F f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc&) {
+    return bad;
+  }
+}
+
+size_t muon_workspace(int32_t n_mats, const lora_mat* mats) {
+  if (check_mats(n_mats, mats, nullptr) != LORA_OK) return 0;
+  // the launches run one after the other and share the room for tiles that do not fit on chip
+  const std::vector<MuonOrder> v = muon_order(n_mats, mats);
+  size_t most = 0;
+  for (int32_t at = 0; at < n_mats;) {
+    const int32_t n = muon_run(v, at);
+    most = std::max(most, muon_spill_bytes(v[at].m, v[at].key / 32, n));
+    at += n;
+  }
+  return most + kWsAlign;
+}
+
+int muon_step(float* params, float* grads, float* m, int32_t n_groups, const lora_group* groups,
+              int32_t n_mats, const lora_mat* mats, const lora_muon_hp* hp, const double* d_scale_norm,
+              const int32_t* d_status, int32_t zero_grads, void* ws, size_t ws_bytes, void* stream) {
+  if (!hp) return LORA_ERR_INVALID;
+  if (!(hp->momentum >= 0.0 && hp->momentum < 1.0) || !std::isfinite(hp->weight_decay) ||
+      !std::isfinite(hp->plus_ratio) || !std::isfinite(hp->coef[0]) ||
+      !std::isfinite(hp->coef[1]) || !std::isfinite(hp->coef[2]) || hp->steps < 1 ||
+      hp->steps > 8 || (hp->nesterov != 0 && hp->nesterov != 1) ||
+      (hp->adjust != LORA_MUON_ADJUST_ASPECT && hp->adjust != LORA_MUON_ADJUST_RMS))
+    return LORA_ERR_INVALID;
+  GroupTab g;
+  int rc = build_groups(n_groups, groups, g, nullptr);
+  if (rc) return rc;
+  if ((rc = check_mats(n_mats, mats, &g))) return rc;
+  if (!params || !grads || !m || !d_scale_norm || !d_status || !ws) return LORA_ERR_INVALID;
+  if (!al16(params) || !al16(grads) || !al16(m) || !al16(ws) ||
+      (reinterpret_cast<uintptr_t>(d_scale_norm) & 7u) ||
+      (reinterpret_cast<uintptr_t>(d_status) & 3u))
+    return LORA_ERR_ALIGN;
+  if (ws_bytes < muon_workspace(n_mats, mats)) return LORA_ERR_WORKSPACE;
+  clear_stale();
+  MuonK k;
+  k.mu = (float)hp->momentum;
+  k.a = (float)hp->coef[0]; k.b = (float)hp->coef[1]; k.c = (float)hp->coef[2];
+  k.steps = hp->steps; k.nesterov = hp->nesterov;
+  MuonTab tab;
+  const std::vector<MuonOrder> v = muon_order(n_mats, mats);
+  for (int32_t at = 0; at < n_mats;) {
+    tab.n = muon_run(v, at);
+    for (int32_t i = 0; i < tab.n; ++i) {
+      const lora_mat& e = mats[v[at + i].at];
+      MuonMat& t = tab.m[i];
+      t = v[at + i].m;
+      const double lr = g.lr[e.group];
+      const double adj = hp->adjust == LORA_MUON_ADJUST_RMS
+                             ? 0.2 * std::sqrt((double)t.n)
+                             : std::sqrt(std::max(1.0, (double)e.rows / (double)e.cols));
+      t.lr = (float)lr;
+      t.decay = e.kind == LORA_KIND_A ? (float)hp->weight_decay : 0.f;
+      t.step = (float)(lr * adj * (e.kind == LORA_KIND_B ? hp->plus_ratio : 1.0));
+    }
+    LORA_TRY(launch_muon(params, grads, m, tab, k, d_scale_norm, d_status, zero_grads != 0,
+                         v[at].key / 32, Carve(ws).take<char>(1), (cudaStream_t)stream));
+    at += tab.n;
+  }
+  return LORA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -207,65 +279,18 @@ int lora_norm_backward(const lora_norm_desc* d, int64_t T, const void* X, const 
 }
 
 size_t lora_muon_workspace_size(int32_t n_mats, const lora_mat* mats) {
-  if (check_mats(n_mats, mats, nullptr) != LORA_OK) return 0;
-  // the launches run one after the other and share the room for tiles that do not fit on chip
-  const std::vector<MuonOrder> v = muon_order(n_mats, mats);
-  size_t most = 0;
-  for (int32_t at = 0; at < n_mats;) {
-    const int32_t n = muon_run(v, at);
-    most = std::max(most, muon_spill_bytes(v[at].m, v[at].key / 32, n));
-    at += n;
-  }
-  return most + kWsAlign;
+  return no_throw(size_t(0), [&] { return muon_workspace(n_mats, mats); });
 }
 
 int lora_muon_step(float* params, float* grads, float* m, int32_t n_groups,
                    const lora_group* groups, int32_t n_mats, const lora_mat* mats,
                    const lora_muon_hp* hp, const double* d_scale_norm, const int32_t* d_status,
                    int32_t zero_grads, void* ws, size_t ws_bytes, void* stream) {
-  if (!hp) return LORA_ERR_INVALID;
-  if (!(hp->momentum >= 0.0 && hp->momentum < 1.0) || !std::isfinite(hp->weight_decay) ||
-      !std::isfinite(hp->plus_ratio) || !std::isfinite(hp->coef[0]) ||
-      !std::isfinite(hp->coef[1]) || !std::isfinite(hp->coef[2]) || hp->steps < 1 ||
-      hp->steps > 8 || (hp->nesterov != 0 && hp->nesterov != 1) ||
-      (hp->adjust != LORA_MUON_ADJUST_ASPECT && hp->adjust != LORA_MUON_ADJUST_RMS))
-    return LORA_ERR_INVALID;
-  GroupTab g;
-  int rc = build_groups(n_groups, groups, g, nullptr);
-  if (rc) return rc;
-  if ((rc = check_mats(n_mats, mats, &g))) return rc;
-  if (!params || !grads || !m || !d_scale_norm || !d_status || !ws) return LORA_ERR_INVALID;
-  if (!al16(params) || !al16(grads) || !al16(m) || !al16(ws) ||
-      (reinterpret_cast<uintptr_t>(d_scale_norm) & 7u) ||
-      (reinterpret_cast<uintptr_t>(d_status) & 3u))
-    return LORA_ERR_ALIGN;
-  if (ws_bytes < lora_muon_workspace_size(n_mats, mats)) return LORA_ERR_WORKSPACE;
-  clear_stale();
-  MuonK k;
-  k.mu = (float)hp->momentum;
-  k.a = (float)hp->coef[0]; k.b = (float)hp->coef[1]; k.c = (float)hp->coef[2];
-  k.steps = hp->steps; k.nesterov = hp->nesterov;
-  MuonTab tab;
-  const std::vector<MuonOrder> v = muon_order(n_mats, mats);
-  for (int32_t at = 0; at < n_mats;) {
-    tab.n = muon_run(v, at);
-    for (int32_t i = 0; i < tab.n; ++i) {
-      const lora_mat& e = mats[v[at + i].at];
-      MuonMat& t = tab.m[i];
-      t = v[at + i].m;
-      const double lr = g.lr[e.group];
-      const double adj = hp->adjust == LORA_MUON_ADJUST_RMS
-                             ? 0.2 * std::sqrt((double)t.n)
-                             : std::sqrt(std::max(1.0, (double)e.rows / (double)e.cols));
-      t.lr = (float)lr;
-      t.decay = e.kind == LORA_KIND_A ? (float)hp->weight_decay : 0.f;
-      t.step = (float)(lr * adj * (e.kind == LORA_KIND_B ? hp->plus_ratio : 1.0));
-    }
-    LORA_TRY(launch_muon(params, grads, m, tab, k, d_scale_norm, d_status, zero_grads != 0,
-                         v[at].key / 32, Carve(ws).take<char>(1), (cudaStream_t)stream));
-    at += tab.n;
-  }
-  return LORA_OK;
+  // the host's tables are made before anything is enqueued
+  return no_throw<int>(LORA_ERR_UNSUPPORTED, [&] {
+    return muon_step(params, grads, m, n_groups, groups, n_mats, mats, hp, d_scale_norm, d_status,
+                     zero_grads, ws, ws_bytes, stream);
+  });
 }
 
 }  // extern "C"
