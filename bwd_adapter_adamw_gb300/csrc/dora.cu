@@ -297,9 +297,12 @@ cudaError_t launch_dora_dm(int dtype, const void* dY, const void* Y, const float
   const int64_t blocks = (out_dim + cols - 1) / cols;
   // 16 token groups when 8 would leave most SMs idle (narrow outputs), if the device hosts such
   // clusters (the size above 8 needs the non-portable attribute)
-  static int wide_ok[2] = {-1, -1};
-  const int ti = dtype == LORA_F32 ? 0 : 1;
-  if (wide_ok[ti] < 0) {
+  static DeviceValues<2> wide_ok;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    sms = 152;
+  const int wide = wide_ok.get(dev, dtype == LORA_F32 ? 0 : 1, [&] {
     cudaError_t ea = dtype == LORA_F32
         ? cudaFuncSetAttribute(k_dora_dm<float>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)
         : cudaFuncSetAttribute(k_dora_dm<__nv_bfloat16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -321,13 +324,9 @@ cudaError_t launch_dora_dm(int dtype, const void* dY, const void* Y, const float
         n = 0;
     }
     cudaGetLastError();
-    wide_ok[ti] = n > 0 ? 1 : 0;
-  }
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    sms = 152;
-  const int groups = (wide_ok[ti] == 1 && blocks * kDmGroups < sms) ? 16 : kDmGroups;
+    return n > 0 ? 1 : 0;
+  });
+  const int groups = (wide == 1 && blocks * kDmGroups < sms) ? 16 : kDmGroups;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)blocks, (unsigned)groups);
   cfg.blockDim = dim3(256);

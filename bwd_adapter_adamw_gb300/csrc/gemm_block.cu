@@ -483,17 +483,17 @@ constexpr int kMaxSplits = 8;   // portable cluster size
 
 template <int BN, bool TR, bool MASK, bool SPLIT>
 cudaError_t launch_tile(const TileParams& prm, cudaStream_t st) {
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(k_block_tile<BN, TR, MASK, SPLIT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<BN>::kSmem);
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t e = once_on_device(set, [] {
+    cudaError_t err = cudaFuncSetAttribute(k_block_tile<BN, TR, MASK, SPLIT>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<BN>::kSmem);
     // a build that launches with fewer registers would wait for them forever
     cudaFuncAttributes fa;
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, k_block_tile<BN, TR, MASK, SPLIT>);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-    attr = true;
-  }
+    if (err == cudaSuccess) err = cudaFuncGetAttributes(&fa, k_block_tile<BN, TR, MASK, SPLIT>);
+    if (err == cudaSuccess && fa.numRegs != kLaunchRegs) err = cudaErrorInvalidConfiguration;
+    return err;
+  });
+  if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if constexpr (!SPLIT)
     return launch_kernel(k_block_tile<BN, TR, MASK, SPLIT>, (unsigned)(prm.total < sms ? prm.total : sms),
@@ -513,10 +513,10 @@ cudaError_t launch_tile(const TileParams& prm, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k_block_tile<BN, TR, MASK, SPLIT>, prm);
 }
 
-// Clusters of `splits` CTAs (one per SM) that the device holds at once, per size (0: not known).
+// Clusters of `splits` CTAs (one per SM) that the device holds at once (0: not known).
 int resident_clusters(int splits) {
-  static int known[kMaxSplits + 1];   // n + 1
-  if (known[splits] == 0) {
+  static DeviceValues<kMaxSplits + 1> known;
+  const int found = known.get(current_device(), splits, [&] {
     auto kernel = k_block_tile<128, false, false, true>;
     int n = 0;
     cudaLaunchConfig_t cfg = {};
@@ -533,11 +533,11 @@ int resident_clusters(int splits) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<128>::kSmem) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      n = 0;
+      return -1;
     }
-    known[splits] = n + 1;
-  }
-  return known[splits] - 1;
+    return n;
+  });
+  return found < 0 ? 0 : found;
 }
 
 cudaError_t run_tile(const BlockProductArgs& a, cudaStream_t st, int prof_kind) {
@@ -903,15 +903,14 @@ int stream_splits(int64_t tiles, int64_t nk, int per_sm) {
 template <int NT, bool TR, bool FUSED>
 cudaError_t launch_stream(const BlockProductArgs& a, StreamParams& prm, cudaStream_t st) {
   using C = StreamCfg<NT, FUSED>;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(k_block_stream<NT, TR, FUSED>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_block_stream<NT, TR, FUSED>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t e = once_on_device(set, [] {
+    const cudaError_t err = cudaFuncSetAttribute(k_block_stream<NT, TR, FUSED>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return err != cudaSuccess ? err : cudaFuncSetAttribute(k_block_stream<NT, TR, FUSED>,
+                                                           cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  if (e != cudaSuccess) return e;
   if (!FUSED && !make_map_2d(&prm.tx, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, prm.K, a.T, prm.K, 128, NT))
     return cudaErrorInvalidValue;
   const int64_t nt = (prm.N + 127) / 128, tt = (a.T + NT - 1) / NT;

@@ -511,14 +511,12 @@ bool make_map_2d(CUtensorMap* map, const void* ptr, CUtensorMapDataType dt, int 
 namespace {
 template <int BN, bool F8>
 cudaError_t launch_gemm_bn(unsigned grid, cudaStream_t st, const TcParams& prm) {
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(k_tc_gemm<BN, F8>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         GemmCfg<BN>::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t e = once_on_device(set, [] {
+    return cudaFuncSetAttribute(k_tc_gemm<BN, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                GemmCfg<BN>::kSmemBytes);
+  });
+  if (e != cudaSuccess) return e;
   return launch_kernel(k_tc_gemm<BN, F8>, grid, kThreads, GemmCfg<BN>::kSmemBytes, st, prm);
 }
 

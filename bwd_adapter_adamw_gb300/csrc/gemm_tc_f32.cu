@@ -448,17 +448,14 @@ cudaError_t launch_tc_gemm_f32(const TcGemmArgs& a, cudaStream_t st, int prof_ki
   prm.ldo = a.ldo;
   prm.n_out = a.n_rows;
   prm.drop = a.drop;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(k_tc_gemm_f32, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSmemBytes);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  static std::atomic<uint64_t> set{0};
+  cudaError_t e = once_on_device(set, [] {
+    return cudaFuncSetAttribute(k_tc_gemm_f32, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  });
+  if (e != cudaSuccess) return e;
   if (a.max_items <= 0) return cudaSuccess;
   dim3 grid((unsigned)((a.n_rows + kBN - 1) / kBN), (unsigned)a.max_items, (unsigned)prm.splits);
   prof_begin(prof_kind, st);
-  cudaError_t e = cudaSuccess;
   if (prm.splits > 1) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;

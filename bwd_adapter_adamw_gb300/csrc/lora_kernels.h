@@ -2,6 +2,7 @@
 #pragma once
 
 #include "lora_common.cuh"
+#include "per_device.h"
 
 namespace lora {
 
@@ -15,6 +16,16 @@ inline unsigned add_pdl_attr(cudaLaunchAttribute* attr, unsigned n) {
   attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[n].val.programmaticStreamSerializationAllowed = 1;
   return n + 1;
+}
+
+inline int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+// A kernel's attributes, set by f() once on the current device.
+template <typename F>
+cudaError_t once_on_device(std::atomic<uint64_t>& done, F f) {
+  return once_on_device(done, current_device(), cudaSuccess, f);
 }
 
 // Kernel launch on a stream with programmatic dependent launch. Errors are also left for

@@ -1010,12 +1010,9 @@ cudaError_t launch_tc_rows(const TcRowsArgs& a, cudaStream_t st, int prof_kind) 
   switch (NP) {
 #define LORA_ROWS_CASE(NPV)                                                             \
   case NPV: {                                                                           \
-    static bool attr = false;                                                           \
-    if (!attr) {                                                                        \
-      e = set_smem(k_tc_rows<NPV>, RowsCfg<NPV>::kSmem);                                \
-      if (e != cudaSuccess) return e;                                                   \
-      attr = true;                                                                      \
-    }                                                                                   \
+    static std::atomic<uint64_t> set{0};                                                \
+    e = once_on_device(set, [] { return set_smem(k_tc_rows<NPV>, RowsCfg<NPV>::kSmem); }); \
+    if (e != cudaSuccess) return e;                                                     \
     e = launch_cluster_y(k_tc_rows<NPV>, grid, a.splits, RowsCfg<NPV>::kSmem, st, prm); \
     break;                                                                              \
   }
@@ -1083,15 +1080,15 @@ int red_resident(int size) {
 
 template <int BN>
 cudaError_t launch_red_bn(dim3 grid, int splits, cudaStream_t st, const RedParams& prm) {
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = set_smem(k_tc_red<BN>, RedCfg<BN>::kSmem);
-    if (e != cudaSuccess) return e;
-    if (cudaFuncSetAttribute(k_tc_red<BN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-        cudaSuccess)
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t e = once_on_device(set, [] {
+    const cudaError_t err = set_smem(k_tc_red<BN>, RedCfg<BN>::kSmem);
+    if (err == cudaSuccess && cudaFuncSetAttribute(k_tc_red<BN>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                                   1) != cudaSuccess)
       cudaGetLastError();
-    attr = true;
-  }
+    return err;
+  });
+  if (e != cudaSuccess) return e;
   return launch_cluster_y(k_tc_red<BN>, grid, splits, RedCfg<BN>::kSmem, st, prm);
 }
 
@@ -1264,18 +1261,18 @@ cudaError_t launch_red_multi_na(const TcRedMultiArgs& a, cudaStream_t st, int pr
   prm.r = a.r;
   prm.N = a.N;
   prm.T = a.T;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = set_smem(k_tc_red_multi<NA>, RedMultiCfg<NA>::kSmem);
-    if (e != cudaSuccess) return e;
-    if (cudaFuncSetAttribute(k_tc_red_multi<NA>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-        cudaSuccess)
+  static std::atomic<uint64_t> set{0};
+  cudaError_t e = once_on_device(set, [] {
+    const cudaError_t err = set_smem(k_tc_red_multi<NA>, RedMultiCfg<NA>::kSmem);
+    if (err == cudaSuccess && cudaFuncSetAttribute(k_tc_red_multi<NA>,
+                                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
       cudaGetLastError();
-    attr = true;
-  }
+    return err;
+  });
+  if (e != cudaSuccess) return e;
   dim3 grid((unsigned)tiles, (unsigned)splits, 1);
   prof_begin(prof_kind, st);
-  cudaError_t e = launch_cluster_y(k_tc_red_multi<NA>, grid, splits, RedMultiCfg<NA>::kSmem, st, prm);
+  e = launch_cluster_y(k_tc_red_multi<NA>, grid, splits, RedMultiCfg<NA>::kSmem, st, prm);
   if (e != cudaSuccess) return e;
   prof_end(prof_kind, st);
   return cudaGetLastError();

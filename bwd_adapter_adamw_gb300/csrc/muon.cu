@@ -1102,14 +1102,14 @@ cudaError_t launch_clusters(K kernel, int threads, int smem, int n, int C, int m
   cfg.numAttrs = add_pdl_attr(at, 1);
   cfg.gridDim = dim3((unsigned)C);
   if (most < (1 << 20)) {   // persistent: as many clusters as are resident at a time
-    static std::atomic<int> fits[17];   // by cluster size
-    int fit = fits[C].load();
-    if (fit == 0) {
-      cudaError_t e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
-      if (e != cudaSuccess) return e;
-      fit = std::max(fit, 1);
-      fits[C].store(fit);
-    }
+    static DeviceValues<17> fits;   // by cluster size
+    cudaError_t e = cudaSuccess;
+    const int fit = fits.get(current_device(), C, [&] {
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      return e == cudaSuccess ? std::max(n, 1) : -1;
+    });
+    if (e != cudaSuccess) return e;
     most = std::min(most / C, fit);
   }
   cfg.gridDim = dim3((unsigned)(std::max(1, std::min(n, most)) * C));
@@ -1129,8 +1129,10 @@ cudaError_t run_simt(float* p, float* g, float* m, const MuonTab& tab, const Muo
                      const double* scale_norm, const int32_t* status, int zero_grads, int C,
                      int held, cudaStream_t st) {
   using F = SimtCfg<S4>;
-  static cudaError_t set = set_attrs(k_muon_simt<S4>, (F::kSmallFloats + F::kCap * F::SP) * 4);
-  if (set != cudaSuccess) return set;
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t e =
+      once_on_device(set, [] { return set_attrs(k_muon_simt<S4>, (F::kSmallFloats + F::kCap * F::SP) * 4); });
+  if (e != cudaSuccess) return e;
   const int smem = (F::kSmallFloats + std::min(held, F::kCap) * F::SP) * 4;
   return launch_clusters(k_muon_simt<S4>, kMuonThreads, smem, tab.n, C, 1 << 20, st, p, g, m, tab, hp, scale_norm,
                          status, zero_grads, C);
@@ -1189,8 +1191,9 @@ cudaError_t launch_muon(float* p, float* g, float* m, const MuonTab& tab, const 
       default: return run_simt<4>(p, g, m, tab, hp, scale_norm, status, zero_grads, C, held, st);
     }
   }
-  static cudaError_t set = set_attrs(k_muon_tc, kTcSmem);
-  if (set != cudaSuccess) return set;
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t e = once_on_device(set, [] { return set_attrs(k_muon_tc, kTcSmem); });
+  if (e != cudaSuccess) return e;
   TcArgs a{};
   a.P = p; a.G = g; a.M = m;
   a.scale_norm = scale_norm; a.status = status;

@@ -534,13 +534,12 @@ cudaError_t fwd_type(const NormArgs& a, cudaStream_t st) {
 template <typename E, int TH, int TPR, int NV, int R>
 cudaError_t bwd_launch(const NormArgs& a, int grid, cudaStream_t st) {
   constexpr int RPB = TH / TPR * R;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(k_norm_bwd<E, TH, TPR, NV, R>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  static std::atomic<uint64_t> set{0};
+  cudaError_t e = once_on_device(set, [] {
+    return cudaFuncSetAttribute(k_norm_bwd<E, TH, TPR, NV, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                200 * 1024);
+  });
+  if (e != cudaSuccess) return e;
   const int64_t group = RPB * a.dim * (int64_t)sizeof(E);
   const int ring = bwd_ring(group, TH);
   int64_t smem = 2 * ring * group;
@@ -550,7 +549,7 @@ cudaError_t bwd_launch(const NormArgs& a, int grid, cudaStream_t st) {
   if (!err) return cudaErrorInvalidDevice;
   prof_begin(0, st);
   const int want = (a.dX ? 1 : 0) | (a.dgamma ? 2 : 0) | (a.dbeta ? 4 : 0);
-  cudaError_t e = launch_kernel(
+  e = launch_kernel(
       k_norm_bwd<E, TH, TPR, NV, R>, (unsigned)grid, TH, (size_t)smem, st, static_cast<const E*>(a.X),
       a.gamma, static_cast<const E*>(a.dY), reinterpret_cast<const float2*>(a.stats),
       static_cast<const E*>(a.dX_add), static_cast<E*>(a.dX), a.part, a.T, (int)a.dim,

@@ -52,3 +52,49 @@ print("ok")
 """ % ROOT
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", (r.returncode, r.stderr[-500:])
+
+
+CSRC = os.path.join(ROOT, "bwd_adapter_adamw_gb300", "csrc")
+
+
+def test_what_is_found_per_device_is_kept_per_device(tmp_path):
+    """Attributes are set once on each device and again after a failure; values are found per device."""
+    src = tmp_path / "t.cpp"
+    src.write_text("""
+#include "per_device.h"
+#include <cassert>
+#include <initializer_list>
+int main() {
+  std::atomic<uint64_t> done{0};
+  int calls = 0, status = 0;
+  auto set = [&] { ++calls; return status; };
+  for (int dev : {0, 1, 0, 1, 63, 63, 0}) assert(lora::once_on_device(done, dev, 0, set) == 0);
+  assert(calls == 3);
+  status = 7;                                       // a device that fails is asked again
+  assert(lora::once_on_device(done, 5, 0, set) == 7 && lora::once_on_device(done, 5, 0, set) == 7 && calls == 5);
+  status = 0;
+  assert(lora::once_on_device(done, 5, 0, set) == 0 && lora::once_on_device(done, 5, 0, set) == 0 && calls == 6);
+  for (int dev : {-1, 64, 64}) assert(lora::once_on_device(done, dev, 0, set) == 0);
+  assert(calls == 9);
+  static lora::DeviceValues<4> v;
+  int found = 0;
+  for (int dev = 0; dev < 3; ++dev)
+    for (int k = 0; k < 2; ++k) assert(v.get(dev, 3, [&] { ++found; return 10 * dev; }) == 10 * dev);
+  assert(found == 3);
+  assert(v.get(0, 2, [] { return -1; }) == -1 && v.get(0, 2, [] { return 4; }) == 4);
+  return 0;
+}
+""")
+    exe = str(tmp_path / "t")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", CSRC, str(src), "-o", exe], check=True)
+    assert subprocess.run([exe]).returncode == 0
+
+
+def test_no_launcher_keeps_a_devices_state_for_the_process():
+    """Every place that sets a kernel's attribute or asks how many clusters are resident does so through
+    the helpers that keep it per device, or through a table by device."""
+    import re
+    for f in sorted(os.listdir(CSRC)):
+        text = open(os.path.join(CSRC, f)).read()
+        plain = re.findall(r"static (?:bool|int|cudaError_t|std::atomic<int>) \w+(?:\[[^\]]*\])*\s*(?:=[^;(]*|=[^;]*\([^;]*)?;", text)
+        assert all("[64]" in p for p in plain), (f, plain)
