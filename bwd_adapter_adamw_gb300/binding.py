@@ -30,6 +30,7 @@ LORA_BF16_BLK8 = 3
 LORA_NORM_LAYER = 0
 LORA_NORM_RMS = 1
 LORA_NORM_MAX_DIM = 16384
+LORA_SUM_MAX = 16
 LORA_KIND_A = 0
 LORA_KIND_B = 1
 LORA_MUON_ADJUST_ASPECT = 0
@@ -148,6 +149,7 @@ def _load() -> C.CDLL:
         "lora_norm_backward_workspace_size": (SZ, [C.POINTER(lora_norm_desc), I64]),
         "lora_norm_backward": (C.c_int, [C.POINTER(lora_norm_desc), I64, P, P, P, P, P, P, P, P,
                                          P, SZ, P]),
+        "lora_sum": (C.c_int, [I32, C.POINTER(P), I64, I32, P, P]),
         "lora_muon_workspace_size": (SZ, [I32, C.POINTER(lora_mat)]),
         "lora_muon_step": (C.c_int, [P, P, P, I32, C.POINTER(lora_group), I32,
                                      C.POINTER(lora_mat), C.POINTER(lora_muon_hp), P, P, I32, P,
@@ -183,7 +185,7 @@ EXPORTED = ("lora_status_string", "lora_scale", "lora_lr_at", "lora_workspace_si
             "lora_block_product_workspace_size", "lora_block_product",
             "lora_block_quantize_weight", "lora_block_quantize", "lora_norm_forward",
             "lora_norm_backward_workspace_size", "lora_norm_backward",
-            "lora_muon_workspace_size", "lora_muon_step",
+            "lora_sum", "lora_muon_workspace_size", "lora_muon_step",
             "lora_dropout_mask", "lora_quantize_e4m3", "multi_lora_token_slots", "lora_profile_arm",
             "lora_profile_used", "lora_launch_counter", "lora_last_cuda_error",
             "lora_device_error", "lora_device_check", "lora_set_wait_limit")
@@ -527,6 +529,13 @@ def lora_norm_backward(d: lora_norm_desc, T: int, X, gamma, dY, stats, dX_add, d
                                  _ptr(dX_add), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws),
                                  _nbytes(ws, ws_bytes), _stream(stream))
     return _check(st, "lora_norm_backward") if check else st
+
+
+def lora_sum(srcs: Sequence, count: int, dtype: int, dst, stream=None, check=True):
+    """dst = the sum of tensors of `count` elements, in fp32 and rounded once."""
+    src = (C.c_void_p * max(1, len(srcs)))(*[_ptr(s) for s in srcs])
+    st = _lib.lora_sum(len(srcs), src, count, dtype, _ptr(dst), _stream(stream))
+    return _check(st, "lora_sum") if check else st
 
 
 def make_mats(mats: Sequence[dict]):

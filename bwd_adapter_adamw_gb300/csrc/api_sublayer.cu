@@ -13,6 +13,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 256;
 constexpr int64_t kMaxDim = int64_t(1) << 20;
+constexpr int64_t kMaxElements = int64_t(1) << 40;   // 2^30 blocks of 256 vectors at the least
 
 int check_product(int64_t T, int64_t out_dim, int64_t in_dim) {
   if (T < 0 || out_dim <= 0 || in_dim <= 0) return LORA_ERR_INVALID;
@@ -276,6 +277,22 @@ int lora_norm_backward(const lora_norm_desc* d, int64_t T, const void* X, const 
   a.dX_add = dX_add; a.dX = dX; a.dgamma = dgamma; a.dbeta = dbeta;
   a.part = Carve(ws).take<float>(1);
   return cuda_status(launch_norm_backward(a, (cudaStream_t)stream));
+}
+
+int lora_sum(int32_t n, const void* const* src, int64_t count, int32_t dtype, void* dst, void* stream) {
+  if (n < 1 || !src || count < 0 || !dst || (dtype != LORA_F32 && dtype != LORA_BF16)) return LORA_ERR_INVALID;
+  if (n > LORA_SUM_MAX || count >= kMaxElements) return LORA_ERR_UNSUPPORTED;
+  SumArgs a{};
+  for (int32_t k = 0; k < n; ++k) {
+    if (!src[k]) return LORA_ERR_INVALID;
+    if (!al16(src[k])) return LORA_ERR_ALIGN;
+    a.src[k] = src[k];
+  }
+  if (!al16(dst) || count % 8) return LORA_ERR_ALIGN;
+  if (count == 0) return LORA_OK;
+  clear_stale();
+  a.n = n; a.count = count; a.dtype = dtype; a.dst = dst;
+  return cuda_status(launch_sum(a, (cudaStream_t)stream));
 }
 
 size_t lora_muon_workspace_size(int32_t n_mats, const lora_mat* mats) {

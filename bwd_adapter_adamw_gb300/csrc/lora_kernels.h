@@ -448,6 +448,14 @@ struct NormArgs {
 int norm_bwd_parts(int64_t dim, int dtype, int64_t T);
 cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t st);
+struct SumArgs {
+  const void* src[LORA_SUM_MAX];
+  int32_t n;
+  int64_t count;             // a multiple of 8
+  int dtype;
+  void* dst;                 // may be one of src
+};
+cudaError_t launch_sum(const SumArgs& a, cudaStream_t st);
 
 // ---- muon.cu ----
 struct MuonMat {             // s x n over the smaller and the longer side

@@ -263,6 +263,7 @@ class SublayerStep(LoraStep):
         self.gamma.fill_(1.0)
         self.stats = torch.empty((self.T, 2), dtype=torch.float32, device=self.device)
         self.dX = torch.empty_like(X)
+        self.dH_norm = torch.empty_like(X) if len(self.linears) > 1 else None   # the norm output's gradient
         self.norm_ws = _ws(L.lora_norm_backward_workspace_size(self.norm, self.T), self.device)
         self.muon = muon if muon is not None else L.make_muon_hp()
         mats, oa, ob = [], 0, self.n_a
@@ -284,17 +285,19 @@ class SublayerStep(LoraStep):
                            self.ws[0])
 
     def forward_backward(self, opt_step: int, dX_res: Optional[torch.Tensor] = None):
-        """Forward, then every projection's backward; the norm's backward runs once per projection
-        (it is linear in its upstream gradient), adding up into dX."""
+        """Forward, every projection's backward, and the norm's backward on the sum of their input
+        gradients (added in fp32: rounded once, and dX once more with the residual's gradient)."""
         self.forward(opt_step)
-        add = dX_res
         for l in self.linears:
             ctx = L.make_ctx(opt_step, 0, self.T // self.chunks)
             L.lora_backward(self.desc(l), ctx, self.T, l.X, l.Wp, l.A, l.B, l.dY, l.H, None, None,
                             None, l.dX, l.gA, l.gB, None, self.ws[0])
-            L.lora_norm_backward(self.norm, self.T, self.X_in, self.gamma, l.dX, self.stats, add,
-                                 self.dX, self.dgamma, self.dbeta, self.norm_ws)
-            add = self.dX
+        dH = self.linears[0].dX
+        if len(self.linears) > 1:
+            dH = self.dH_norm
+            L.lora_sum([l.dX for l in self.linears], dH.numel(), self.norm.dtype, dH)
+        L.lora_norm_backward(self.norm, self.T, self.X_in, self.gamma, dH, self.stats, dX_res, self.dX,
+                             self.dgamma, self.dbeta, self.norm_ws)
 
     def optimizer_step(self, lr: float, step: int, zero_grads: bool = True):
         g = self.groups(lr, step)

@@ -333,6 +333,14 @@ int lora_norm_backward(const lora_norm_desc* d, int64_t T, const void* X, const 
                        const void* dY, const float* stats, const void* dX_add, void* dX,
                        float* dgamma, float* dbeta, void* ws, size_t ws_bytes, void* stream);
 
+/* The gradients of several projections that read the norm's output, for its backward pass:
+ *   dst[i] = sum_k src[k][i], k = 0 .. n - 1 in order, in fp32, rounded once to dtype
+ * (LORA_F32 or LORA_BF16). src is a host array of n device pointers, 1 <= n <= LORA_SUM_MAX
+ * (LORA_ERR_UNSUPPORTED above); count elements each, a multiple of 8 (LORA_ERR_ALIGN); dst may be one
+ * of them; count = 0 is a no-op. */
+#define LORA_SUM_MAX 16
+int lora_sum(int32_t n, const void* const* src, int64_t count, int32_t dtype, void* dst, void* stream);
+
 /* ---- orthogonalised update (in place of lora_adamw_step for the adapter matrices) -------------*/
 /* One matrix of the flat arenas, [rows, cols] row-major from element `offset` (a multiple of 4).
  * The smaller side is at most LORA_MAX_RANK and a multiple of 4. `group` indexes the call's groups

@@ -98,3 +98,20 @@ def test_no_launcher_keeps_a_devices_state_for_the_process():
         text = open(os.path.join(CSRC, f)).read()
         plain = re.findall(r"static (?:bool|int|cudaError_t|std::atomic<int>) \w+(?:\[[^\]]*\])*\s*(?:=[^;(]*|=[^;]*\([^;]*)?;", text)
         assert all("[64]" in p for p in plain), (f, plain)
+
+
+def test_sum_refusals(L):
+    def call(n=2, src=None, count=64, dtype=None, dst=FAKE):
+        return L.lora_sum([FAKE] * n if src is None else src, count, L.LORA_BF16 if dtype is None else dtype, dst,
+                          stream=0, check=False)
+    assert call(n=0) == L.LORA_ERR_INVALID
+    assert call(n=L.LORA_SUM_MAX + 1) == L.LORA_ERR_UNSUPPORTED
+    assert call(src=[FAKE, None]) == L.LORA_ERR_INVALID
+    assert call(src=[FAKE, FAKE + 8]) == L.LORA_ERR_ALIGN
+    assert call(dst=None) == L.LORA_ERR_INVALID
+    assert call(dst=FAKE + 2) == L.LORA_ERR_ALIGN
+    assert call(count=-8) == L.LORA_ERR_INVALID
+    assert call(count=12) == L.LORA_ERR_ALIGN
+    assert call(count=1 << 41) == L.LORA_ERR_UNSUPPORTED
+    assert call(dtype=L.LORA_BF16_FP8) == L.LORA_ERR_INVALID
+    assert call(count=0) == L.LORA_OK
