@@ -236,6 +236,18 @@ class SublayerStep(LoraStep):
 
     def __init__(self, X: torch.Tensor, linears: Sequence[Linear], *, kind: str = "layer",
                  eps: float = 1e-5, muon: Optional[L.lora_muon_hp] = None, **kw):
+        if kind not in ("layer", "rms"):
+            raise ValueError(f"kind {kind!r}: 'layer' or 'rms'")
+        if not 1 <= len(linears) <= L.LORA_SUM_MAX:
+            raise ValueError(f"{len(linears)} projections: 1 to {L.LORA_SUM_MAX}")
+        if X.dim() != 2 or not X.is_contiguous() or X.shape[0] != kw.get("tokens"):
+            raise ValueError(f"X {tuple(X.shape)}: a contiguous [tokens, dim], tokens {kw.get('tokens')}")
+        if (X.dtype == torch.float32) != (kw.get("dtype") == "f32"):
+            raise ValueError(f"X is {X.dtype} in a step of dtype {kw.get('dtype')}")
+        for l in linears:
+            if l.in_dim != X.shape[1] or tuple(l.dY.shape) != (X.shape[0], l.out_dim):
+                raise ValueError(f"projection {l.proj_id}: W {tuple(l.W.shape)} and dY {tuple(l.dY.shape)} "
+                                 f"do not fit X {tuple(X.shape)}")
         self.X_in = X                                  # [T, dim], the sublayer's input
         self.H_norm = torch.empty_like(X)
         for l in linears:
@@ -287,6 +299,9 @@ class SublayerStep(LoraStep):
     def forward_backward(self, opt_step: int, dX_res: Optional[torch.Tensor] = None):
         """Forward, every projection's backward, and the norm's backward on the sum of their input
         gradients (added in fp32: rounded once, and dX once more with the residual's gradient)."""
+        if dX_res is not None and not (torch.is_tensor(dX_res) and dX_res.shape == self.X_in.shape and
+                                       dX_res.dtype == self.X_in.dtype and dX_res.is_contiguous()):
+            raise ValueError("dX_res: a contiguous tensor of X's shape and type")
         self.forward(opt_step)
         for l in self.linears:
             ctx = L.make_ctx(opt_step, 0, self.T // self.chunks)

@@ -115,3 +115,30 @@ def test_sum_refusals(L):
     assert call(count=1 << 41) == L.LORA_ERR_UNSUPPORTED
     assert call(dtype=L.LORA_BF16_FP8) == L.LORA_ERR_INVALID
     assert call(count=0) == L.LORA_OK
+
+
+def _sublayer(L, T=16, dim=64, outs=(32, 48), in_dims=None, dt=None, **kw):
+    import torch
+
+    from bwd_adapter_adamw_gb300.step import Linear, SublayerStep
+    dt = torch.bfloat16 if dt is None else dt
+    lins = [Linear(0, i, None, torch.zeros(o, d, dtype=dt), torch.zeros(T, o, dtype=dt))
+            for i, (o, d) in enumerate(zip(outs, in_dims or [dim] * len(outs)))]
+    kw = dict(dict(rank=8, scale=1.0, dtype="bf16", tokens=T, chunks=1, device="cpu"), **kw)
+    return SublayerStep(kw.pop("X", torch.zeros(T, dim, dtype=dt)), lins, **kw)
+
+
+def test_sublayer_step_refuses_shapes_that_do_not_fit(L):
+    """The library takes pointers: a projection of another width would read past the norm's output."""
+    import torch
+    assert _sublayer(L).n_mag == 2 * 64 and _sublayer(L, kind="rms").n_mag == 64
+    for kw in (dict(in_dims=[64, 72]), dict(X=torch.zeros(8, 64, dtype=torch.bfloat16)), dict(tokens=32),
+               dict(X=torch.zeros(16, 72, dtype=torch.bfloat16)), dict(X=torch.zeros(16, 128, dtype=torch.bfloat16)[:, ::2]),
+               dict(X=torch.zeros(16, 64)), dict(dtype="f32"), dict(outs=()), dict(outs=(8,) * (L.LORA_SUM_MAX + 1)),
+               dict(kind="batch")):
+        with pytest.raises(ValueError):
+            _sublayer(L, **kw)
+    st = _sublayer(L)
+    for res in (torch.zeros(16, 72, dtype=torch.bfloat16), torch.zeros(16, 64), True):
+        with pytest.raises(ValueError):
+            st.forward_backward(0, res)
