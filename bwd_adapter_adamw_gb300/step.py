@@ -232,7 +232,8 @@ class SublayerStep(LoraStep):
         H = norm(X),  Y_k = projection_k(H),  dX = dX_res + norm'(sum_k dX_k),
     with the norm's weight (and shift) trained beside the adapters. They live in the arena's
     magnitude range, so one group holds the global clip of everything; A and B take the
-    orthogonalised update, the norm's parameters AdamW (no decay, plain learning rate)."""
+    orthogonalised update (with `hp`'s decay and LoRA+ ratio unless `muon` is given), the norm's
+    parameters AdamW (no decay, plain learning rate)."""
 
     def __init__(self, X: torch.Tensor, linears: Sequence[Linear], *, kind: str = "layer",
                  eps: float = 1e-5, muon: Optional[L.lora_muon_hp] = None, **kw):
@@ -277,7 +278,8 @@ class SublayerStep(LoraStep):
         self.dX = torch.empty_like(X)
         self.dH_norm = torch.empty_like(X) if len(self.linears) > 1 else None   # the norm output's gradient
         self.norm_ws = _ws(L.lora_norm_backward_workspace_size(self.norm, self.T), self.device)
-        self.muon = muon if muon is not None else L.make_muon_hp()
+        self.muon = muon if muon is not None else L.make_muon_hp(weight_decay=self.hp.weight_decay,
+                                                                 plus_ratio=self.hp.plus_ratio)
         mats, oa, ob = [], 0, self.n_a
         for l in self.linears:
             mats.append(dict(offset=oa, rows=self.rank, cols=l.in_dim, kind=L.LORA_KIND_A))

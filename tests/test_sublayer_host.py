@@ -142,3 +142,12 @@ def test_sublayer_step_refuses_shapes_that_do_not_fit(L):
     for res in (torch.zeros(16, 72, dtype=torch.bfloat16), torch.zeros(16, 64), True):
         with pytest.raises(ValueError):
             st.forward_backward(0, res)
+
+
+def test_sublayer_step_takes_decay_and_ratio_from_its_adamw_settings(L):
+    """A and B take the orthogonalised update: with no settings of its own, the decay and the LoRA+ ratio
+    of the step's `hp`, which LoraStep gives to AdamW."""
+    st = _sublayer(L, hp=L.make_hp(plus_ratio=4.0, weight_decay=0.25))
+    assert (st.muon.plus_ratio, st.muon.weight_decay) == (4.0, 0.25)
+    st = _sublayer(L, hp=L.make_hp(plus_ratio=4.0), muon=L.make_muon_hp(plus_ratio=2.0))
+    assert st.muon.plus_ratio == 2.0
