@@ -103,7 +103,7 @@ class LoraStep:
     def __init__(self, linears: Sequence[Linear], *, rank: int, scale: float, dtype: str,
                  tokens: int, chunks: int, dropout_p: float = 0.0, seed: int = 0,
                  dora: bool = False, max_norm: float = 1.0, hp: Optional[L.lora_adamw_hp] = None,
-                 n_streams: int = 1, device="cuda"):
+                 n_streams: int = 1, device="cuda", n_extra: int = 0):
         self.linears = list(linears)
         self.rank, self.scale, self.dtype = rank, scale, _DT[dtype]
         self.T, self.chunks = tokens, chunks
@@ -111,10 +111,10 @@ class LoraStep:
         self.max_norm = max_norm
         self.hp = hp if hp is not None else L.make_hp()
         self.device = torch.device(device)
-        # arena: [A ... | B ... | MAG ...]
+        # arena: [A ... | B ... | MAG ...], n_extra further parameters at the magnitudes' end
         na = sum(rank * l.in_dim for l in self.linears)
         nb = sum(l.out_dim * rank for l in self.linears)
-        nm = sum(l.out_dim for l in self.linears) if dora else 0
+        nm = (sum(l.out_dim for l in self.linears) if dora else 0) + n_extra
         self.n_a, self.n_b, self.n_mag = na, nb, nm
         self.arena = Arena(na + nb + nm, self.device)
         oa, ob, om = 0, na, na + nb
@@ -176,8 +176,7 @@ class LoraStep:
         return self._prep_ws
 
     # ------------------------------------------------------------------------------------------
-    def forward_backward(self, opt_step: int, per_chunk_calls: bool = False):
-        """Enqueue forward + backward of every linear over all chunks (gradients accumulate)."""
+    def _enqueue(self, opt_step: int, per_chunk_calls: bool, backward: bool):
         main = torch.cuda.current_stream(self.device)
         k, use = _streams_in_use(self)
         _fork(main, use)
@@ -197,9 +196,14 @@ class LoraStep:
                 sl = slice(t0, t0 + n)
                 X, dY, Y, dX, H = l.X[sl], l.dY[sl], l.Y[sl], l.dX[sl], l.H[sl]
                 L.lora_forward(d, ctx, n, X, l.W, l.Wp, l.A, l.B, l.mag, l.norm, Y, H, ws, stream=st)
-                L.lora_backward(d, ctx, n, X, l.Wp, l.A, l.B, dY, H, l.mag, l.norm, Y, dX, l.gA,
-                                l.gB, l.gmag, ws, stream=st)
+                if backward:
+                    L.lora_backward(d, ctx, n, X, l.Wp, l.A, l.B, dY, H, l.mag, l.norm, Y, dX, l.gA,
+                                    l.gB, l.gmag, ws, stream=st)
         _join(main, use)
+
+    def forward_backward(self, opt_step: int, per_chunk_calls: bool = False):
+        """Enqueue forward + backward of every linear over all chunks (gradients accumulate)."""
+        self._enqueue(opt_step, per_chunk_calls, True)
 
     def optimizer_step(self, lr: float, step: int, zero_grads: bool = True):
         g = self.groups(lr, step)
@@ -241,6 +245,8 @@ class SublayerStep(LoraStep):
             raise ValueError(f"kind {kind!r}: 'layer' or 'rms'")
         if not 1 <= len(linears) <= L.LORA_SUM_MAX:
             raise ValueError(f"{len(linears)} projections: 1 to {L.LORA_SUM_MAX}")
+        if kw.get("dora"):
+            raise ValueError("the sublayer's magnitude range holds the norm's parameters")
         if X.dim() != 2 or not X.is_contiguous() or X.shape[0] != kw.get("tokens"):
             raise ValueError(f"X {tuple(X.shape)}: a contiguous [tokens, dim], tokens {kw.get('tokens')}")
         if (X.dtype == torch.float32) != (kw.get("dtype") == "f32"):
@@ -255,20 +261,9 @@ class SublayerStep(LoraStep):
             l.X = self.H_norm
         self.norm = L.make_norm_desc(X.shape[1], L.LORA_NORM_RMS if kind == "rms" else L.LORA_NORM_LAYER,
                                      L.LORA_F32 if X.dtype == torch.float32 else L.LORA_BF16, eps)
-        super().__init__(linears, **kw)
-        if self.dora:
-            raise ValueError("the sublayer's magnitude range holds the norm's parameters")
         dim, shift = X.shape[1], kind != "rms"
-        old, self.n_mag = self.arena, dim * (2 if shift else 1)
+        super().__init__(linears, n_extra=dim * (2 if shift else 1), **kw)
         base = self.n_a + self.n_b
-        self.arena = Arena(base + self.n_mag, self.device)
-        del old
-        oa, ob = 0, self.n_a
-        for l in self.linears:
-            l.A, l.gA = (self.arena.view(w, oa, (self.rank, l.in_dim)) for w in ("params", "grads"))
-            l.B, l.gB = (self.arena.view(w, ob, (l.out_dim, self.rank)) for w in ("params", "grads"))
-            oa += self.rank * l.in_dim
-            ob += l.out_dim * self.rank
         self.gamma, self.dgamma = (self.arena.view(w, base, (dim,)) for w in ("params", "grads"))
         self.beta = self.dbeta = None
         if shift:
@@ -291,24 +286,22 @@ class SublayerStep(LoraStep):
         self.muon_ws = _ws(L.lora_muon_workspace_size(self.mats), self.device)
 
     def forward(self, opt_step: int = 0):
-        """The norm and every projection (the serving call, and the first half of a step)."""
-        L.lora_norm_forward(self.norm, self.T, self.X_in, self.gamma, self.beta, self.H_norm, self.stats)
-        for l in self.linears:
-            ctx = L.make_ctx(opt_step, 0, self.T // self.chunks)
-            L.lora_forward(self.desc(l), ctx, self.T, l.X, l.W, l.Wp, l.A, l.B, None, None, l.Y, l.H,
-                           self.ws[0])
+        """The norm and every projection (the serving call)."""
+        self._norm_forward()
+        self._enqueue(opt_step, False, False)
 
-    def forward_backward(self, opt_step: int, dX_res: Optional[torch.Tensor] = None):
+    def _norm_forward(self):
+        L.lora_norm_forward(self.norm, self.T, self.X_in, self.gamma, self.beta, self.H_norm, self.stats)
+
+    def forward_backward(self, opt_step: int, dX_res: Optional[torch.Tensor] = None,
+                         per_chunk_calls: bool = False):
         """Forward, every projection's backward, and the norm's backward on the sum of their input
         gradients (added in fp32: rounded once, and dX once more with the residual's gradient)."""
         if dX_res is not None and not (torch.is_tensor(dX_res) and dX_res.shape == self.X_in.shape and
                                        dX_res.dtype == self.X_in.dtype and dX_res.is_contiguous()):
             raise ValueError("dX_res: a contiguous tensor of X's shape and type")
-        self.forward(opt_step)
-        for l in self.linears:
-            ctx = L.make_ctx(opt_step, 0, self.T // self.chunks)
-            L.lora_backward(self.desc(l), ctx, self.T, l.X, l.Wp, l.A, l.B, l.dY, l.H, None, None,
-                            None, l.dX, l.gA, l.gB, None, self.ws[0])
+        self._norm_forward()
+        self._enqueue(opt_step, per_chunk_calls, True)
         dH = self.linears[0].dX
         if len(self.linears) > 1:
             dH = self.dH_norm
@@ -328,8 +321,8 @@ class SublayerStep(LoraStep):
                           zero_grads)
 
     def run(self, opt_step: int, lr: float, dX_res: Optional[torch.Tensor] = None,
-            zero_grads: bool = True):
-        self.forward_backward(opt_step, dX_res)
+            zero_grads: bool = True, per_chunk_calls: bool = False):
+        self.forward_backward(opt_step, dX_res, per_chunk_calls)
         self.optimizer_step(lr, opt_step, zero_grads)
 
 

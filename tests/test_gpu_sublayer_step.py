@@ -17,9 +17,9 @@ def L():
     return binding
 
 
-def _step(L, T, dim, outs, seed=0, dtype="bf16", cls=None, **kw):
+def _step(L, T, dim, outs, dtype="bf16", **kw):
     from bwd_adapter_adamw_gb300.step import Linear, SublayerStep
-    g = torch.Generator(device="cuda").manual_seed(seed)
+    g = torch.Generator(device="cuda").manual_seed(4)
     dt = torch.float32 if dtype == "f32" else torch.bfloat16
     rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")   # noqa: E731
     X = rnd(T, dim).to(dt)
@@ -79,3 +79,40 @@ def test_sum_of_tensors(L, n, count, dtype):
     again = src[0].clone()
     L.lora_sum([again] + src[1:], count, L.LORA_F32 if dtype == "f32" else L.LORA_BF16, again)   # in place
     assert torch.equal(again, dst[:count])
+
+
+@pytest.mark.parametrize("per_chunk", [False, True])
+def test_streams_and_chunks_mean_what_they_mean_in_lora_step(L, per_chunk, monkeypatch):
+    """The same projections as a LoraStep over the norm's output, with dropout keyed by chunk: outputs and
+    gradients bitwise equal, calls spread over the streams, chunk by chunk where asked."""
+    from bwd_adapter_adamw_gb300.step import Linear, LoraStep
+    kw = dict(n_streams=3, chunks=3, dropout_p=0.2, seed=11)
+    st = _step(L, 384, 272, (400, 144, 256, 64), **kw)
+    st.beta.normal_()
+    calls, forward = [], L.lora_forward
+
+    def counted(d, c, n, *a, **k):
+        calls.append((n, k["stream"].cuda_stream))
+        return forward(d, c, n, *a, **k)
+    monkeypatch.setattr(L, "lora_forward", counted)
+    st.forward_backward(5, per_chunk_calls=per_chunk)
+    torch.cuda.synchronize()
+    assert len({s for _, s in calls}) == 3
+    assert [n for n, _ in calls] == ([128] * 12 if per_chunk else [384] * 4)
+    one = LoraStep([Linear(l.layer, l.proj_id, st.H_norm, l.W, l.dY, l.Wp) for l in st.linears], rank=8, scale=2.0,
+                   dtype="bf16", tokens=384, max_norm=0.5, **kw)
+    for a, b in zip(one.linears, st.linears):
+        a.A.copy_(b.A)
+        a.B.copy_(b.B)
+    one.forward_backward(5, per_chunk)
+    torch.cuda.synchronize()
+    for a, b in zip(one.linears, st.linears):
+        for x, y in ((a.Y, b.Y), (a.dX, b.dX), (a.gA, b.gA), (a.gB, b.gB)):
+            assert torch.equal(x, y)
+    Y = [l.Y.clone() for l in st.linears]
+    calls.clear()
+    st.forward(5)
+    torch.cuda.synchronize()
+    assert len({s for _, s in calls}) == 3
+    if not per_chunk:
+        assert all(torch.equal(a, l.Y) for a, l in zip(Y, st.linears))

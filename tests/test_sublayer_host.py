@@ -151,3 +151,22 @@ def test_sublayer_step_takes_decay_and_ratio_from_its_adamw_settings(L):
     assert (st.muon.plus_ratio, st.muon.weight_decay) == (4.0, 0.25)
     st = _sublayer(L, hp=L.make_hp(plus_ratio=4.0), muon=L.make_muon_hp(plus_ratio=2.0))
     assert st.muon.plus_ratio == 2.0
+
+
+def test_sublayer_step_allocates_one_arena(L, monkeypatch):
+    from bwd_adapter_adamw_gb300 import step as S
+    made = []
+
+    class Counted(S.Arena):
+        def __init__(self, n, device):
+            made.append(n)
+            super().__init__(n, device)
+    monkeypatch.setattr(S, "Arena", Counted)
+    st = _sublayer(L)
+    assert made == [8 * 64 * 2 + 8 * (32 + 48) + 2 * 64]
+    base = st.n_a + st.n_b
+    assert st.gamma.data_ptr() == st.arena.params.data_ptr() + 4 * base
+    assert st.dbeta.data_ptr() == st.arena.grads.data_ptr() + 4 * (base + 64)
+    assert st.linears[1].B.data_ptr() == st.arena.params.data_ptr() + 4 * (st.n_a + 8 * 32)
+    with pytest.raises(ValueError):
+        _sublayer(L, dora=True)
