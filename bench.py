@@ -146,13 +146,13 @@ def memory_counts(cfg: LI.LoraConfig, layers: int, groups=None):
 # value. Captured with `ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum` on
 # `python bench.py --layers 1 --steps 2 --warmup 3 --no-cpu-baseline --streams 1`.
 NCU_TRAFFIC = {
-    ("c4", 1): {"source": "gemm_tc.cu", "sha256_16": "4819c92179bf6c02",
-                "bytes": 384.9e6,
+    ("c4", 1): {"source": "gemm_tc.cu", "sha256_16": "b57b2d843154d045",
+                "bytes": 385.2e6,
                 "note": "one-layer capture (profiles/launch_list_c4_llama_bf16.md): the seven "
-                        "forward launches move 152.9, 78.3, 78.3, 153.9, 546.1, 548.6 and "
-                        "1136.2 MB (read + write); the wide and long shapes re-read operands "
+                        "forward launches move 155.6, 78.4, 78.2, 153.7, 546.0, 548.8 and "
+                        "1136.0 MB (read + write); the wide and long shapes re-read operands "
                         "while compute-bound"},
-    ("c2", 1): {"source": "gemm_tc_f32.cu", "sha256_16": "0cfe552134b8e004",
+    ("c2", 1): {"source": "gemm_tc_f32.cu", "sha256_16": "f10ba457a60970b9",
                 "bytes": (25.32e6 + 10.58e6) / 2,
                 "note": "wq fwd 25.32 MB, wv fwd (4-way split K) 10.58 MB read (the bf16 hi / lo "
                         "splits of X and W, once), ~0 written (outputs stay in L2)"},
