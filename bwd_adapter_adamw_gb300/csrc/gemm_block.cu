@@ -82,8 +82,9 @@ __device__ __forceinline__ void fma2(uint64_t& a, uint64_t s, uint32_t d0, uint3
 // MMAs' 512, and the epilogue warps wait 14 of them for their next block and read for 790, beside
 // MMAs that themselves read and write the other accumulator. Wider reads (32 columns), scalar FMAs,
 // sixteen epilogue warps of 64 columns (436 us) and a fourth stage of operands measured the same or
-// slower. 8192 x 4096 -> 14336 400 us (2400
-// TF/s; the per-row-scaled product, which reads its accumulator once per tile, runs at 2690).
+// slower. 8192 x 4096 -> 14336 403 us a
+// call, the quantisation's 16 included, in a series of tens (2390 TF/s), 430 to 441 in series of hundreds, at
+// the power limit (the per-row-scaled product, which reads its accumulator once per tile, runs at 2690).
 constexpr int kTileThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kLaunchRegs = 168, kIssueRegs = 72, kEpiRegs = 216;   // per thread

@@ -18,7 +18,7 @@
 // (k_muon_tc), u as a two-term bf16 split, all four products of the terms kept.
 //
 // Measured: 22 layers of rank 8 (2048 + 256 columns) 15 us, a chain of passes and cluster barriers;
-// 32 layers of rank 64 (4096 + 14336 columns) 370 us, 755 MB at the least, 0.98 GB moved (the tiles
+// 32 layers of rank 64 (4096 + 14336 columns) 365 us, 755 MB at the least, 1.00 GB moved (the tiles
 // beyond those that a CTA holds go through L2): bound by the latency of a tile's steps (load,
 // split, MMA, drain), one after the other, and by the small products, during which no tile moves.
 #include <algorithm>
