@@ -58,10 +58,11 @@ int check_mats(int32_t n_mats, const lora_mat* mats, const GroupTab* groups) {
     const int64_t s = std::min(e.rows, e.cols), n = std::max(e.rows, e.cols);
     if (s > LORA_MAX_RANK || s % 4 || n > kMaxDim) return LORA_ERR_UNSUPPORTED;
     if (e.offset % 4 || n % 4) return LORA_ERR_ALIGN;
+    if (e.offset > INT64_MAX - s * n) return LORA_ERR_INVALID;
     if (groups) {
       if (e.group >= groups->n) return LORA_ERR_INVALID;
       const int64_t lo = groups->offset[e.group], hi = lo + groups->count[e.group];
-      if (e.offset < lo || e.offset > hi || s * n > hi - e.offset) return LORA_ERR_INVALID;   // (no overflow)
+      if (e.offset < lo || e.offset + s * n > hi) return LORA_ERR_INVALID;
     }
     if (i && e.offset < mats[i - 1].offset + mats[i - 1].rows * mats[i - 1].cols) sorted = false;
   }

@@ -377,10 +377,10 @@ typedef struct lora_muon_hp {
  * to lora_adamw_step in a group of their own. Matrices must not overlap; any number of them.
  * Precision: momentum, norms and sums in fp32. Up to a smaller side of 16 everything is fp32. Above, the
  * long products run on tensor cores: u, X between stages of at most three steps and a stage's polynomial
- * are held as two bf16 terms (16 significant bits), the small matrices are multiplied as two-term tf32
- * splits (about 2^-21). X is then within (2 stages + 1) 2^-16 of the sequence's largest gain, in the
- * Frobenius norm; the parameters of a rank-64 update came out 2.4e-7 off in relative 2-norm, those of fp32
- * torch operations 6e-8.
+ * are held as two bf16 terms (16 significant bits where max |u| is at least 2^-116), the small matrices
+ * are multiplied as two-term tf32 splits (about 2^-21). X is then within (2 stages + 1) 2^-16 of the
+ * sequence's largest gain, in the Frobenius norm; the parameters of a rank-64 update came out 2.4e-7 off
+ * in relative 2-norm, those of fp32 torch operations 6e-8.
  * When lora_device_check reports LORA_ERR_TIMEOUT after it, every element of the parameters holds its
  * update or is as it was; m (and the gradients, where they are cleared) may be those of either. */
 size_t lora_muon_workspace_size(int32_t n_mats, const lora_mat* mats);

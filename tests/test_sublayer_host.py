@@ -24,6 +24,8 @@ def test_update_refuses_matrices_whose_end_overflows(L, offset):
     mats = L.make_mats([dict(offset=offset, rows=8, cols=64, kind=L.LORA_KIND_A)])
     assert L.lora_muon_step(FAKE, FAKE, FAKE, groups, mats, L.make_muon_hp(), FAKE, FAKE, False, FAKE, 1 << 30,
                             stream=0, check=False) == L.LORA_ERR_INVALID
+    if offset > (1 << 63) - 512:
+        assert L.lora_muon_workspace_size(mats) == 0
 
 
 def test_memory_that_runs_out_is_a_status(L):
