@@ -249,12 +249,12 @@ class SublayerStep(LoraStep):
             raise ValueError("the sublayer's magnitude range holds the norm's parameters")
         if X.dim() != 2 or not X.is_contiguous() or X.shape[0] != kw.get("tokens"):
             raise ValueError(f"X {tuple(X.shape)}: a contiguous [tokens, dim], tokens {kw.get('tokens')}")
-        if (X.dtype == torch.float32) != (kw.get("dtype") == "f32"):
+        if X.dtype != (torch.float32 if kw.get("dtype") == "f32" else torch.bfloat16):
             raise ValueError(f"X is {X.dtype} in a step of dtype {kw.get('dtype')}")
         for l in linears:
-            if l.in_dim != X.shape[1] or tuple(l.dY.shape) != (X.shape[0], l.out_dim):
+            if l.in_dim != X.shape[1] or tuple(l.dY.shape) != (X.shape[0], l.out_dim) or l.dY.dtype != X.dtype:
                 raise ValueError(f"projection {l.proj_id}: W {tuple(l.W.shape)} and dY {tuple(l.dY.shape)} "
-                                 f"do not fit X {tuple(X.shape)}")
+                                 f"{l.dY.dtype} do not fit X {tuple(X.shape)} {X.dtype}")
         self.X_in = X                                  # [T, dim], the sublayer's input
         self.H_norm = torch.empty_like(X)
         for l in linears:

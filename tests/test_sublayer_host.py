@@ -136,7 +136,8 @@ def test_sublayer_step_refuses_shapes_that_do_not_fit(L):
     assert _sublayer(L).n_mag == 2 * 64 and _sublayer(L, kind="rms").n_mag == 64
     for kw in (dict(in_dims=[64, 72]), dict(X=torch.zeros(8, 64, dtype=torch.bfloat16)), dict(tokens=32),
                dict(X=torch.zeros(16, 72, dtype=torch.bfloat16)), dict(X=torch.zeros(16, 128, dtype=torch.bfloat16)[:, ::2]),
-               dict(X=torch.zeros(16, 64)), dict(dtype="f32"), dict(outs=()), dict(outs=(8,) * (L.LORA_SUM_MAX + 1)),
+               dict(X=torch.zeros(16, 64)), dict(dtype="f32"), dict(dt=torch.float16),
+               dict(X=torch.zeros(16, 64, dtype=torch.bfloat16), dt=torch.float32), dict(outs=()), dict(outs=(8,) * (L.LORA_SUM_MAX + 1)),
                dict(kind="batch")):
         with pytest.raises(ValueError):
             _sublayer(L, **kw)
