@@ -31,6 +31,8 @@ LORA_NORM_LAYER = 0
 LORA_NORM_RMS = 1
 LORA_NORM_MAX_DIM = 16384
 LORA_SUM_MAX = 16
+LORA_ROPE_HALVES = 0
+LORA_ROPE_PAIRS = 1
 LORA_KIND_A = 0
 LORA_KIND_B = 1
 LORA_MUON_ADJUST_ASPECT = 0
@@ -85,6 +87,19 @@ class lora_adamw_hp(C.Structure):
 class lora_norm_desc(C.Structure):
     _fields_ = [("dim", C.c_int64), ("kind", C.c_int32), ("dtype", C.c_int32),
                 ("eps", C.c_float)]
+
+
+class lora_rope_desc(C.Structure):
+    _fields_ = [("q_heads", C.c_int32), ("k_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("dtype", C.c_int32), ("layout", C.c_int32), ("eps", C.c_float),
+                ("ld_q", C.c_int64), ("ld_k", C.c_int64), ("ld_yq", C.c_int64),
+                ("ld_yk", C.c_int64)]
+
+
+class lora_attn_desc(C.Structure):
+    _fields_ = [("q_heads", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("dtype", C.c_int32), ("scale", C.c_float), ("ld_q", C.c_int64),
+                ("ld_k", C.c_int64), ("ld_v", C.c_int64), ("ld_o", C.c_int64)]
 
 
 class lora_mat(C.Structure):
@@ -150,6 +165,18 @@ def _load() -> C.CDLL:
         "lora_norm_backward": (C.c_int, [C.POINTER(lora_norm_desc), I64, P, P, P, P, P, P, P, P,
                                          P, SZ, P]),
         "lora_sum": (C.c_int, [I32, C.POINTER(P), I64, I32, P, P]),
+        "lora_rope_table": (C.c_int, [I64, I32, P, P, P]),
+        "lora_rope_forward": (C.c_int, [C.POINTER(lora_rope_desc), I64, P, P, P, P, P, P, I64, P, P,
+                                        P]),
+        "lora_rope_backward_workspace_size": (SZ, [C.POINTER(lora_rope_desc), I64]),
+        "lora_rope_backward": (C.c_int, [C.POINTER(lora_rope_desc), I64, P, P, P, P, P, P, I64, P, P,
+                                         P, P, P, P, P, SZ, P]),
+        "lora_attn_plan_size": (SZ, [I64, I32]),
+        "lora_attn_plan_build": (C.c_int, [I64, I32, P, P, SZ, P]),
+        "lora_attn_forward": (C.c_int, [C.POINTER(lora_attn_desc), I64, I32, P, P, P, P, P, P, P]),
+        "lora_attn_backward_workspace_size": (SZ, [C.POINTER(lora_attn_desc), I64]),
+        "lora_attn_backward": (C.c_int, [C.POINTER(lora_attn_desc), I64, I32, P, P, P, P, P, P, P, P,
+                                         P, P, P, SZ, P]),
         "lora_muon_workspace_size": (SZ, [I32, C.POINTER(lora_mat)]),
         "lora_muon_step": (C.c_int, [P, P, P, I32, C.POINTER(lora_group), I32,
                                      C.POINTER(lora_mat), C.POINTER(lora_muon_hp), P, P, I32, P,
@@ -185,7 +212,10 @@ EXPORTED = ("lora_status_string", "lora_scale", "lora_lr_at", "lora_workspace_si
             "lora_block_product_workspace_size", "lora_block_product",
             "lora_block_quantize_weight", "lora_block_quantize", "lora_norm_forward",
             "lora_norm_backward_workspace_size", "lora_norm_backward",
-            "lora_sum", "lora_muon_workspace_size", "lora_muon_step",
+            "lora_sum", "lora_rope_table", "lora_rope_forward", "lora_rope_backward_workspace_size",
+            "lora_rope_backward", "lora_attn_plan_size", "lora_attn_plan_build",
+            "lora_attn_forward", "lora_attn_backward_workspace_size", "lora_attn_backward",
+            "lora_muon_workspace_size", "lora_muon_step",
             "lora_dropout_mask", "lora_quantize_e4m3", "multi_lora_token_slots", "lora_profile_arm",
             "lora_profile_used", "lora_launch_counter", "lora_last_cuda_error",
             "lora_device_error", "lora_device_check", "lora_set_wait_limit")
@@ -536,6 +566,81 @@ def lora_sum(srcs: Sequence, count: int, dtype: int, dst, stream=None, check=Tru
     src = (C.c_void_p * max(1, len(srcs)))(*[_ptr(s) for s in srcs])
     st = _lib.lora_sum(len(srcs), src, count, dtype, _ptr(dst), _stream(stream))
     return _check(st, "lora_sum") if check else st
+
+
+def make_rope_desc(q_heads, k_heads, head_dim, dtype=LORA_BF16, layout=LORA_ROPE_HALVES, eps=1e-6,
+                   ld_q=0, ld_k=0, ld_yq=0, ld_yk=0) -> lora_rope_desc:
+    return lora_rope_desc(q_heads, k_heads, head_dim, dtype, layout, eps, ld_q, ld_k, ld_yq, ld_yk)
+
+
+def lora_rope_table(n_pos: int, head_dim: int, inv_freq, table, stream=None, check=True):
+    """Cosines and sines of n_pos positions for head_dim / 2 frequencies (doubles)."""
+    st = _lib.lora_rope_table(n_pos, head_dim, _ptr(inv_freq), _ptr(table), _stream(stream))
+    return _check(st, "lora_rope_table") if check else st
+
+
+def lora_rope_forward(d: lora_rope_desc, T: int, Q, K, gamma_q, gamma_k, pos, table, n_pos: int, YQ,
+                      YK, stream=None, check=True):
+    """Norm of each query and key head (with weights) and rotation by position."""
+    st = _lib.lora_rope_forward(C.byref(d), T, _ptr(Q), _ptr(K), _ptr(gamma_q), _ptr(gamma_k),
+                                _ptr(pos), _ptr(table), n_pos, _ptr(YQ), _ptr(YK), _stream(stream))
+    return _check(st, "lora_rope_forward") if check else st
+
+
+def lora_rope_backward_workspace_size(d: lora_rope_desc, T: int) -> int:
+    return _lib.lora_rope_backward_workspace_size(C.byref(d), T)
+
+
+def lora_rope_backward(d: lora_rope_desc, T: int, Q, K, gamma_q, gamma_k, pos, table, n_pos: int,
+                       dYQ, dYK, dQ, dK, dgamma_q, dgamma_k, ws, ws_bytes: Optional[int] = None,
+                       stream=None, check=True):
+    """dQ, dK, dgamma_q += and dgamma_k += from the forward's inputs."""
+    st = _lib.lora_rope_backward(C.byref(d), T, _ptr(Q), _ptr(K), _ptr(gamma_q), _ptr(gamma_k),
+                                 _ptr(pos), _ptr(table), n_pos, _ptr(dYQ), _ptr(dYK), _ptr(dQ),
+                                 _ptr(dK), _ptr(dgamma_q), _ptr(dgamma_k), _ptr(ws),
+                                 _nbytes(ws, ws_bytes), _stream(stream))
+    return _check(st, "lora_rope_backward") if check else st
+
+
+def make_attn_desc(q_heads, kv_heads, head_dim, dtype=LORA_BF16, scale=None, ld_q=0, ld_k=0, ld_v=0,
+                   ld_o=0) -> lora_attn_desc:
+    """scale None: 1 / sqrt(head_dim). Strides in elements, 0: heads * head_dim."""
+    if scale is None:
+        scale = head_dim ** -0.5 if head_dim > 0 else 0.0
+    return lora_attn_desc(q_heads, kv_heads, head_dim, dtype, scale, ld_q, ld_k, ld_v, ld_o)
+
+
+def lora_attn_plan_size(T: int, n_seq: int) -> int:
+    return _lib.lora_attn_plan_size(T, n_seq)
+
+
+def lora_attn_plan_build(T: int, n_seq: int, seq_start, plan, plan_bytes: Optional[int] = None,
+                         stream=None, check=True):
+    """The tiles of a packed batch, shared by every call over it."""
+    st = _lib.lora_attn_plan_build(T, n_seq, _ptr(seq_start), _ptr(plan), _nbytes(plan, plan_bytes),
+                                   _stream(stream))
+    return _check(st, "lora_attn_plan_build") if check else st
+
+
+def lora_attn_forward(d: lora_attn_desc, T: int, n_seq: int, plan, Q, K, V, O, lse, stream=None,
+                      check=True):
+    """Causal attention over packed sequences, and the scores' log sums."""
+    st = _lib.lora_attn_forward(C.byref(d), T, n_seq, _ptr(plan), _ptr(Q), _ptr(K), _ptr(V), _ptr(O),
+                                _ptr(lse), _stream(stream))
+    return _check(st, "lora_attn_forward") if check else st
+
+
+def lora_attn_backward_workspace_size(d: lora_attn_desc, T: int) -> int:
+    return _lib.lora_attn_backward_workspace_size(C.byref(d), T)
+
+
+def lora_attn_backward(d: lora_attn_desc, T: int, n_seq: int, plan, Q, K, V, O, lse, dO, dQ, dK, dV,
+                       ws, ws_bytes: Optional[int] = None, stream=None, check=True):
+    """dQ, dK and dV from the forward's inputs, its output and log sums."""
+    st = _lib.lora_attn_backward(C.byref(d), T, n_seq, _ptr(plan), _ptr(Q), _ptr(K), _ptr(V),
+                                 _ptr(O), _ptr(lse), _ptr(dO), _ptr(dQ), _ptr(dK), _ptr(dV),
+                                 _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream))
+    return _check(st, "lora_attn_backward") if check else st
 
 
 def make_mats(mats: Sequence[dict]):

@@ -1,0 +1,464 @@
+// Causal attention over packed sequences: the plan of a batch's tiles and the forward pass.
+//
+//   S = Q K^T (tcgen05, tiles of 128 x 128),  P = exp2(c S - m),  l = sum P,  O = (P V) / l
+//   with c = scale log2(e) and a running reference m for each row
+//
+// One CTA takes two tiles of 128 query rows that read the same keys: two heads of a group, or, where a
+// group's heads do not pair up, two neighbouring tiles of one head. The tensor cores work on one tile
+// while the softmax of the other runs: per 128 keys they take S and P V of both tiles, 4 x 512 cycles at
+// head_dim 128, and each tile's 128 threads (one row each) have the other tile's 1024 to turn S into P.
+// P goes back to tensor memory over S, so that P V takes it from there.
+//
+// The reference m follows the running maximum only where that has grown by more than 8 (a factor 256 in P,
+// which bf16 and the fp32 sums hold as well): most rows rescale O once or twice, not with every tile.
+//
+// CTA layout (384 threads): warps 0-3 and 4-7 softmax, rescale and epilogue of tile 0 and 1; warp 8 loads
+// (TMA); warp 9 issues the products (10 and 11 fill their warpgroup, which hands its registers to the softmax).
+// Every wait is bounded; a warp whose wait ran out stops, and no later
+// warp sees its part arrive, so that outputs are stored from complete products only.
+#include <new>
+
+#include "attn_common.cuh"
+#include "api_util.h"
+
+namespace lora {
+
+namespace {
+
+using namespace attn;
+
+// ---- the plan ------------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+
+struct PlanK {
+  const int32_t* start;
+  int32_t n_seq;
+  int64_t T;
+  AttnPlan p;
+};
+
+// Inclusive scan over the block; `sh` holds kPlanThreads values.
+template <typename Op>
+__device__ int64_t block_scan(int64_t v, int64_t* sh, Op op) {
+  const int t = threadIdx.x;
+  sh[t] = v;
+  __syncthreads();
+  for (int o = 1; o < kPlanThreads; o <<= 1) {
+    const int64_t u = t >= o ? op(sh[t - o], sh[t]) : sh[t];
+    __syncthreads();
+    sh[t] = u;
+    __syncthreads();
+  }
+  return sh[t];
+}
+
+// One CTA. Sequences (clamped, in order), then for tiles of 128 and of 256 rows: how many sequences have
+// an i-th tile, the place of the tiles of each index in falling order (a causal tile's work grows with its
+// index), and the tiles in their places. The order among tiles of one index is not fixed; it decides when
+// a tile runs, not what it computes.
+__global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constant__ PlanK a) {
+  grid_dep_sync();
+  __shared__ int64_t sh[kPlanThreads];
+  __shared__ int64_t carry;
+  const int t = threadIdx.x;
+  if (t == 0) carry = 0;
+  __syncthreads();
+  for (int64_t k0 = 0; k0 < a.n_seq; k0 += kPlanThreads) {
+    const int64_t k = k0 + t;
+    int64_t lo = 0, hi = 0;
+    if (k < a.n_seq) {
+      lo = a.start[k];
+      hi = a.start[k + 1];
+      lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
+      hi = hi < 0 ? 0 : hi > a.T ? a.T : hi;
+    }
+    const int64_t before = carry;   // the furthest end of the sequences ahead
+    const int64_t incl = block_scan(hi, sh, [](int64_t x, int64_t y) { return x > y ? x : y; });
+    const int64_t prev = t ? sh[t - 1] : 0;
+    const int64_t last = sh[kPlanThreads - 1];
+    __syncthreads();
+    const int64_t end = prev > before ? prev : before;
+    const int64_t from = lo > end ? lo : end;
+    if (k < a.n_seq) a.p.seq[k] = make_int2((int)from, (int)(hi > from ? hi - from : 0));
+    if (t == 0) carry = before > last ? before : last;
+    (void)incl;
+    __syncthreads();
+  }
+  for (int w = 0; w < 2; ++w) {
+    const int rows = kAttnTile << w;
+    const int64_t buckets = (a.T + rows - 1) / rows;
+    for (int64_t i = t; i < buckets; i += kPlanThreads) a.p.hist[i] = 0;
+    __syncthreads();
+    for (int64_t k = t; k < a.n_seq; k += kPlanThreads) {
+      const int n = a.p.seq[k].y;
+      if (n > 0) atomicAdd(a.p.hist + (n - 1) / rows, 1);
+    }
+    __syncthreads();
+    // from the highest index down: sequences that reach it, and tiles placed ahead of it
+    int64_t reach = 0, placed = 0;
+    for (int64_t i0 = 0; i0 < buckets; i0 += kPlanThreads) {
+      const int64_t i = buckets - 1 - (i0 + t);
+      const int64_t here = i >= 0 ? a.p.hist[i] : 0;
+      const auto add = [](int64_t x, int64_t y) { return x + y; };
+      const int64_t n = reach + block_scan(here, sh, add);     // sequences with a tile i
+      const int64_t all = sh[kPlanThreads - 1];
+      __syncthreads();
+      const int64_t upto = placed + block_scan(i >= 0 ? n : 0, sh, add);
+      const int64_t tiles = sh[kPlanThreads - 1];
+      __syncthreads();
+      if (i >= 0) a.p.hist[i] = (int)(upto - n);
+      reach += all;
+      placed += tiles;
+      __syncthreads();
+    }
+    if (t == 0) a.p.count[w] = (int)placed;
+    __syncthreads();
+    // a warp per sequence, a lane per tile
+    for (int64_t k = t / 32; k < a.n_seq; k += kPlanThreads / 32) {
+      const int2 s = a.p.seq[k];
+      const int n = (s.y + rows - 1) / rows;
+      for (int i = t % 32; i < n; i += 32) {
+        const int64_t at = atomicAdd(a.p.hist + i, 1);
+        if (at < a.p.most[w]) a.p.tiles[w][at] = AttnTile{s.x, s.y, i, 0};
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---- forward -------------------------------------------------------------------------------
+constexpr float kRescale = 8.f;   // growth of a row's maximum, in powers of two, that rescales O
+
+template <int D>
+struct FwdCfg {
+  static constexpr int kTile = Tile<D>::kBytes;
+  static constexpr int kStages = D == 128 ? 5 : 8;   // K and V tiles in flight or in use
+  static constexpr int kSmem = (2 + kStages) * kTile + 1024 /*barriers*/ + 1024 /*alignment*/;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static constexpr uint32_t kIdS = idesc(kFmtBF16, 128, 128);
+  static constexpr uint32_t kIdO = idesc(kFmtBF16, 128, D, false, true);
+  // tensor memory: S (and P over it) of both tiles, O of both
+  static constexpr uint32_t kS = 0, kO = 256;
+};
+
+struct FwdK {
+  CUtensorMap tq, tk, tv;
+  const int32_t* count;
+  const AttnTile* tiles;
+  int32_t groups;        // CTAs of a tile of the list
+  int32_t by_heads;      // two heads of a 128-row tile, or two 128-row tiles of a head
+  int32_t per;           // query heads of a key / value head
+  float c;               // scale log2(e)
+  int64_t T, ld_o;
+  __nv_bfloat16* O;
+  float* lse;
+  uint32_t* err;
+  unsigned long long limit;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant__ FwdK p) {
+  using C = FwdCfg<D>;
+  using Tl = Tile<D>;
+  constexpr int ST = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sq = base;
+  uint8_t* ring = base + 2 * C::kTile;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + ST * C::kTile);
+  uint64_t* empty = full + ST;
+  uint64_t* q_full = empty + ST;     // [2]
+  uint64_t* s_full = q_full + 2;     // [2] S of a tile is complete
+  uint64_t* p_full = s_full + 2;     // [2] P is in place, O rescaled
+  uint64_t* o_full = p_full + 2;     // [2] P V is complete
+  uint64_t* fixed = o_full + 2;      // a tile whose rows are zeroed behind a sequence has landed
+  uint64_t* done = fixed + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  grid_dep_sync();
+  const int li = blockIdx.x / p.groups, gi = blockIdx.x - li * p.groups;
+  if (li >= __ldg(p.count)) return;
+  const AttnTile t = p.tiles[li];
+  // tile s: query rows row0 + 128 qi[s] .., head h[s], keys of n[s] tiles
+  const int h0 = p.by_heads ? 2 * gi : gi, h1 = p.by_heads ? h0 + 1 : h0;
+  const int i0 = p.by_heads ? t.index : 2 * t.index, i1 = p.by_heads ? i0 : i0 + 1;
+  const int n0 = i0 + 1, n1 = (int64_t)i1 * kRows < t.len ? i1 + 1 : 0;
+  const int n = n1 > n0 ? n1 : n0;
+  const int kv_col = h0 / p.per * D;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 4);
+      mbar_init(&o_full[s], 1);
+    }
+    mbar_init(fixed, 1);
+    mbar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async();
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 8) issue_regs();
+  if (warp == 8) {
+    // ---- loads: Q of both tiles, then K and V tile by tile ----
+    if (lane == 0) {
+      mbar_expect_tx(&q_full[0], C::kTile);
+      Tl::load(sq, &p.tq, &q_full[0], h0 * D, t.row0 + i0 * kRows);
+      if (n1) {
+        mbar_expect_tx(&q_full[1], C::kTile);
+        Tl::load(sq + C::kTile, &p.tq, &q_full[1], h1 * D, t.row0 + i1 * kRows);
+      }
+    }
+    int g = 0;
+    for (; g < 2 * n; ++g) {
+      const int s = g % ST, j = g >> 1;
+      if (g >= ST && !warp_wait(&empty[s], (uint32_t)(g / ST - 1) & 1u, 1u, p.err, p.limit)) break;
+      uint8_t* dst = ring + s * C::kTile;
+      const CUtensorMap* map = (g & 1) ? &p.tv : &p.tk;
+      const int rows = t.len - j * kRows;   // of the sequence from here on
+      // The rows behind the sequence are another's or padding: P is zero there, but zero times a NaN or an
+      // infinity is not, so V's are zeroed before the product sees the tile.
+      const bool fix = (g & 1) && rows < kRows;
+      if (lane == 0) {
+        uint64_t* bar = fix ? fixed : &full[s];
+        mbar_expect_tx(bar, C::kTile);
+        Tl::load(dst, map, bar, kv_col, t.row0 + j * kRows);
+      }
+      if (fix) {   // the sequence's last tile: at most once
+        if (!__all_sync(0xffffffffu, mbar_wait(fixed, 0u, 1u, p.err))) break;
+        Tl::zero_rows(dst, rows, lane);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+      }
+    }
+    // every copy has landed before the CTA ends
+    if (lane == 0) {
+      mbar_wait(&q_full[0], 0u, 1u, p.err);
+      if (n1) mbar_wait(&q_full[1], 0u, 1u, p.err);
+      for (int k = g > ST ? g - ST : 0; k < g; ++k)
+        if (!mbar_wait(&full[k % ST], (uint32_t)(k / ST) & 1u, 1u, p.err)) break;
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ---- products ----
+    if (lane == 0) {
+      const uint32_t q0 = smem_u32(sq), rg = smem_u32(ring);
+      auto wait = [&](uint64_t* b, uint32_t par) {
+        const bool ok = mbar_wait_strict(b, par, 2u, p.err, p.limit);
+        fence_after();
+        return ok;
+      };
+      auto stage_full = [&](int g) { return wait(&full[g % ST], (uint32_t)(g / ST) & 1u); };
+      auto tile_at = [&](int g) { return rg + (uint32_t)(g % ST) * C::kTile; };
+      bool ok = stage_full(0);
+      for (int s = 0; s < 2 && ok; ++s) {
+        if (s && !n1) break;
+        ok = wait(&q_full[s], 0u);
+        if (!ok) break;
+        Tl::mma_nt(tmem + C::kS + 128 * s, q0 + s * C::kTile, tile_at(0), C::kIdS);
+        umma_commit(&s_full[s]);
+      }
+      if (ok) umma_commit(&empty[0]);
+      for (int j = 0; j < n && ok; ++j) {
+        const int gv = 2 * j + 1, gk = 2 * j + 2;
+        ok = stage_full(gv);
+        bool have_k = false;
+        for (int s = 0; s < 2 && ok; ++s) {
+          const int ns = s ? n1 : n0;
+          if (j >= ns) continue;
+          ok = wait(&p_full[s], (uint32_t)j & 1u);
+          if (!ok) break;
+          const uint32_t ps = tmem + C::kS + 128 * s;
+          Tl::mma_tn(tmem + C::kO + 128 * s, ps, ps + 32, tile_at(gv), C::kIdO, j > 0);
+          umma_commit(&o_full[s]);
+          if (j + 1 < ns) {
+            if (!have_k) ok = stage_full(gk);
+            have_k = true;
+            if (!ok) break;
+            Tl::mma_nt(ps, q0 + s * C::kTile, tile_at(gk), C::kIdS);
+            umma_commit(&s_full[s]);
+          }
+        }
+        if (!ok) break;
+        umma_commit(&empty[gv % ST]);
+        if (have_k) umma_commit(&empty[gk % ST]);
+      }
+      // every product has completed before the tensor memory is freed
+      umma_commit(done);
+      mbar_wait(done, 0u, 2u, p.err);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    compute_regs();
+    // ---- softmax and epilogue: thread = row of tile s ----
+    const int s = warp >> 2, r = threadIdx.x & 127;
+    const int ns = s ? n1 : n0, qi = s ? i1 : i0, h = s ? h1 : h0;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = lanes + C::kS + 128 * s, to = lanes + C::kO + 128 * s;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < ns; ++j) {
+      if (!(ok = warp_wait(&s_full[s], (uint32_t)j & 1u, 4u, p.err, p.limit))) break;
+      fence_after();
+      uint32_t x[128];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_ld32_nw(ts + 32 * k, x + 32 * k);
+      tmem_wait_ld_n<128>(x);
+      if (j == ns - 1) {   // the tile on the diagonal: keys up to the row's own
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if (k > r) x[k] = 0xff800000u;
+      }
+      float mx[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(x[k]);
+#pragma unroll
+      for (int k = 4; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(x[k]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+      if (j == 0) {
+        m = top;
+      } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
+        const bool grow = top > m + kRescale;
+        const float f = grow ? exp2_(m - top) : 1.f;
+        if (!(ok = warp_wait(&o_full[s], (uint32_t)(j - 1) & 1u, 4u, p.err, p.limit))) break;
+        fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t o[32];
+          tmem_ld32_nw(to + 32 * k, o);
+          tmem_wait_ld_n<32>(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          tmem_st32(to + 32 * k, o);
+        }
+        if (grow) m = top;
+        l *= f;
+      }
+      // (a row whose scores are all -inf so far has no reference yet: P is 0)
+      const float ref = m == -INFINITY ? 0.f : m;
+      const f2 c2 = mk2(p.c, p.c), m2 = mk2(-ref, -ref);
+      f2 sum0 = mk2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 e = un2(fma2(mk2(__uint_as_float(x[32 * k + 2 * i]), __uint_as_float(x[32 * k + 2 * i + 1])), c2, m2));
+          const float a = exp2_(e.x), b = exp2_(e.y);
+          if (i & 1) sum1 = add2(sum1, mk2(a, b));
+          else sum0 = add2(sum0, mk2(a, b));
+          w[i] = pack_bf16(a, b);
+        }
+        tmem_st16(ts + 16 * k, w);
+      }
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[s]);
+      const float2 z = un2(add2(sum0, sum1));
+      l += z.x + z.y;
+    }
+    const int row = qi * kRows + r;
+    if (ok && ns > 0 && warp_wait(&o_full[s], (uint32_t)(ns - 1) & 1u, 4u, p.err, p.limit)) {
+      fence_after();
+      const float inv = 1.f / l;
+      const int64_t at = (int64_t)t.row0 + row;
+      __nv_bfloat16* out = p.O + at * p.ld_o + (int64_t)h * D;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        float v[32];
+        tmem_ld32(to + 32 * k, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= inv;
+        if (row < t.len) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) store8(out + 32 * k + 8 * i, v + 8 * i);
+        }
+      }
+      if (row < t.len) p.lse[(int64_t)h * p.T + at] = (m + log2f(l)) * kLn2;
+    }
+    fence_before();
+  }
+  __syncthreads();
+  if (warp == 9) {
+    fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t fwd_launch(const AttnArgs& a, cudaStream_t st) {
+  static std::atomic<uint64_t> set{0};
+  cudaError_t e = once_on_device(set, [] {
+    return set_up(k_attn_fwd<D>, FwdCfg<D>::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  FwdK k{};
+  if (!attn_map(&k.tq, a.Q, a.q_heads * D, a.T, a.ld_q) || !attn_map(&k.tk, a.K, a.kv_heads * D, a.T, a.ld_k) ||
+      !attn_map(&k.tv, a.V, a.kv_heads * D, a.T, a.ld_v))
+    return cudaErrorInvalidValue;
+  k.per = a.q_heads / a.kv_heads;
+  k.by_heads = k.per % 2 == 0;
+  const int w = k.by_heads ? 0 : 1;
+  k.count = a.plan.count + w;
+  k.tiles = a.plan.tiles[w];
+  k.groups = k.by_heads ? a.q_heads / 2 : a.q_heads;
+  k.c = a.scale * kLog2e;
+  k.T = a.T;
+  k.ld_o = a.ld_o;
+  k.O = static_cast<__nv_bfloat16*>(a.O);
+  k.lse = a.lse;
+  k.err = error_word();
+  if (!k.err) return cudaErrorInvalidDevice;
+  k.limit = tc_wait_limit();
+  const int64_t grid = a.plan.most[w] * k.groups;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  prof_begin(0, st);
+  return launch_kernel(k_attn_fwd<D>, (unsigned)grid, kThreads, FwdCfg<D>::kSmem, st, k);
+}
+
+}  // namespace
+
+bool attn_map(CUtensorMap* map, const void* ptr, int64_t cols, int64_t rows, int64_t ld) {
+  return make_map_2d(map, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)cols, (uint64_t)rows, (uint64_t)ld, 64,
+                     kRows);
+}
+
+AttnPlan attn_plan(int64_t T, int32_t n_seq, void* buf) {
+  AttnPlan p{};
+  Carve c(buf);
+  const int64_t some = n_seq < T ? n_seq : T;   // sequences that are not empty
+  p.count = c.take<int32_t>(2);
+  for (int w = 0; w < 2; ++w) {
+    p.most[w] = T / (kAttnTile << w) + some;
+    p.tiles[w] = c.take<AttnTile>((size_t)p.most[w]);
+  }
+  p.seq = c.take<int2>((size_t)n_seq);
+  p.hist = c.take<int32_t>((size_t)((T + kAttnTile - 1) / kAttnTile));
+  p.bytes = c.off;
+  return p;
+}
+
+cudaError_t launch_attn_plan(int64_t T, int32_t n_seq, const int32_t* seq_start, const AttnPlan& plan, cudaStream_t st) {
+  PlanK k{seq_start, n_seq, T, plan};
+  prof_begin(0, st);
+  return launch_kernel(k_attn_plan, 1, kPlanThreads, 0, st, k);
+}
+
+cudaError_t launch_attn_forward(const AttnArgs& a, cudaStream_t st) {
+  return a.dim == 128 ? fwd_launch<128>(a, st) : fwd_launch<64>(a, st);
+}
+
+}  // namespace lora

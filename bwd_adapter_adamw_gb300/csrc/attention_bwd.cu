@@ -1,0 +1,658 @@
+// Causal attention over packed sequences, backward: delta = sum do o, then two kernels that recompute the
+// scores, one for dV and dK and one for dQ.
+//
+//   P = exp2(c S - lse log2(e)),  dP = dO V^T,  dS = P (dP - delta)
+//   dV = P^T dO,  dK = scale dS^T Q   (key tile fixed, over query tiles and the heads of its group)
+//   dQ = scale dS K                   (query tile fixed, over key tiles)
+//
+// Five products are needed; recomputing S and dP for dQ makes seven. The alternative, dQ added up in
+// global memory by the key tiles' CTAs, takes fp32 atomics whose order changes results, 64 KB of them per
+// five products (25 bytes per cycle and SM into L2, as much as all SMs together can add), and a pass that
+// clears and rounds them.
+//
+// dV and dK (k_attn_dkv): the scores are computed turned, S^T = K Q^T and dP^T = V dO^T, keys along the
+// tensor memory's lanes, so that P^T and dS^T, written back over them in bf16, are first operands of
+// P^T dO and dS^T Q as they are; a thread has one key and half the tile's queries. The products of one
+// query tile run while the other half of its elementwise work does: S^T of the next tile under dS^T of
+// this one, dP^T of the next under P^T of the next. At head_dim 128 a pair of tiles takes four products of
+// 512 cycles.
+//
+// dQ (k_attn_dq): S = Q K^T and dP = dO V^T with queries along the lanes; dS, in bf16 over dP, is the first
+// operand of dS K. S alternates between two buffers, so that the next tile's S runs before this one's dS.
+//
+// CTA layout (384 threads): warps 0-7 elementwise (two warpgroups, 64 columns each) and epilogue, warp 8
+// loads, warp 9 issues the products, warp 10 brings the queries' statistics (k_attn_dkv). Waits are bounded
+// as in the forward pass.
+#include "attn_common.cuh"
+
+namespace lora {
+
+namespace {
+
+using namespace attn;
+
+// ---- delta ---------------------------------------------------------------------------------
+// delta[h, t] = sum do o, D / 8 lanes per head of a token. Bound by memory.
+template <int D>
+__global__ void __launch_bounds__(256) k_attn_delta(const __nv_bfloat16* __restrict__ O,
+                                                    const __nv_bfloat16* __restrict__ dO, int64_t ld, int heads,
+                                                    int64_t T, float* __restrict__ delta) {
+  grid_dep_sync();
+  constexpr int G = D / 8;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / G;   // token, then head
+  const int l = threadIdx.x % G;
+  const int64_t t = i / heads;
+  const int h = (int)(i - t * heads);
+  float a[8], b[8], s = 0.f;
+  if (t < T) {
+    load16(O + t * ld + (int64_t)h * D + l * 8, a);
+    load16(dO + t * ld + (int64_t)h * D + l * 8, b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s = fmaf(a[k], b[k], s);
+  }
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (t < T && l == 0) delta[(int64_t)h * T + t] = s;
+}
+
+struct BwdK {
+  CUtensorMap tq, tk, tv, tdo;
+  const int32_t* count;
+  const AttnTile* tiles;
+  int32_t heads;         // CTAs of a tile: key / value heads (dK, dV) or query heads (dQ)
+  int32_t per;
+  float c, scale;
+  int64_t T, ld_q, ld_k, ld_v;
+  const float *lse, *delta;
+  __nv_bfloat16 *dQ, *dK, *dV;
+  uint32_t* err;
+  unsigned long long limit;
+};
+
+// A row of `N` columns of tensor memory from `col`, scaled, to bf16 at `out`.
+template <int N>
+__device__ __forceinline__ void store_row(uint32_t col, float f, __nv_bfloat16* out, bool live) {
+#pragma unroll
+  for (int k = 0; k < N / 32; ++k) {
+    float v[32];
+    tmem_ld32(col + 32 * k, v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= f;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store8(out + 32 * k + 8 * i, v + 8 * i);
+    }
+  }
+}
+
+// ---- dV and dK -----------------------------------------------------------------------------
+template <int D>
+struct DkvCfg {
+  static constexpr int kTile = Tile<D>::kBytes;
+  static constexpr int kQ = 3, kDo = 2;   // tiles of Q and dO in flight or in use: dO's are free earlier
+  static constexpr int kBarriers = 512;
+  static constexpr int kSmem = (2 + kQ + kDo) * kTile + 2 * kRows * 4 + kBarriers + 1024 /*alignment*/;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static constexpr uint32_t kIdS = idesc(kFmtBF16, 128, 128);
+  static constexpr uint32_t kIdD = idesc(kFmtBF16, 128, D, false, true);
+  static constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 384;   // tensor memory
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant__ BwdK p) {
+  using C = DkvCfg<D>;
+  using Tl = Tile<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sk = base;
+  uint8_t* sv = sk + C::kTile;
+  uint8_t* sq = sv + C::kTile;
+  uint8_t* sdo = sq + C::kQ * C::kTile;
+  float* s_lse = reinterpret_cast<float*>(sdo + C::kDo * C::kTile);   // of the query tile, times log2(e)
+  float* s_delta = s_lse + kRows;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(s_delta + kRows);
+  uint64_t* q_empty = q_full + C::kQ;
+  uint64_t* do_full = q_empty + C::kQ;
+  uint64_t* do_empty = do_full + C::kDo;
+  uint64_t* k_full = do_empty + C::kDo;
+  uint64_t* v_full = k_full + 1;
+  uint64_t* s_full = v_full + 1;
+  uint64_t* p_full = s_full + 1;     // P^T is in place
+  uint64_t* dp_full = p_full + 1;
+  uint64_t* ds_full = dp_full + 1;   // dS^T is in place
+  uint64_t* lse_full = ds_full + 1;
+  uint64_t* lse_empty = lse_full + 1;
+  uint64_t* delta_full = lse_empty + 1;
+  uint64_t* delta_empty = delta_full + 1;
+  uint64_t* fix_q = delta_empty + 1;
+  uint64_t* fix_do = fix_q + 1;
+  uint64_t* all = fix_do + 1;        // both sums are complete
+  uint64_t* done = all + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  static_assert((2 * (C::kQ + C::kDo) + 14) * 8 + 4 <= C::kBarriers, "barriers");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  grid_dep_sync();
+  const int li = blockIdx.x / p.heads, hk = blockIdx.x - li * p.heads;
+  if (li >= __ldg(p.count)) return;
+  const AttnTile t = p.tiles[li];
+  const int nb = (t.len + kRows - 1) / kRows;
+  const int j = nb - 1 - t.index;     // the key tile with t.index + 1 query tiles
+  const int nq = t.index + 1, n = nq * p.per;   // iteration it: head it / nq of the group, query tile j + it % nq
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kQ; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+    }
+    for (int s = 0; s < C::kDo; ++s) {
+      mbar_init(&do_full[s], 1);
+      mbar_init(&do_empty[s], 1);
+    }
+    mbar_init(k_full, 1);
+    mbar_init(v_full, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 8);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, 8);
+    mbar_init(lse_full, 1);
+    mbar_init(lse_empty, 8);
+    mbar_init(delta_full, 1);
+    mbar_init(delta_empty, 8);
+    mbar_init(fix_q, 1);
+    mbar_init(fix_do, 1);
+    mbar_init(all, 1);
+    mbar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async();
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 8) issue_regs();
+  if (warp == 8) {
+    // ---- loads ----
+    int fixes = 0;   // of Q and of dO alike
+    // Rows behind the sequence are zeroed: P^T and dS^T are zero there, but zero times a NaN is not.
+    auto fetch = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* fix, int col, int qi) {
+      const int rows = t.len - qi * kRows;
+      if (lane == 0) {
+        uint64_t* bar = rows < kRows ? fix : full;
+        mbar_expect_tx(bar, C::kTile);
+        Tl::load(dst, map, bar, col, t.row0 + qi * kRows);
+      }
+      if (rows >= kRows) return true;
+      if (!__all_sync(0xffffffffu, mbar_wait(fix, (uint32_t)fixes & 1u, 1u, p.err))) return false;
+      Tl::zero_rows(dst, rows, lane);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full);
+      return true;
+    };
+    if (lane == 0) {
+      mbar_expect_tx(k_full, C::kTile);
+      Tl::load(sk, &p.tk, k_full, hk * D, t.row0 + j * kRows);
+      mbar_expect_tx(v_full, C::kTile);
+      Tl::load(sv, &p.tv, v_full, hk * D, t.row0 + j * kRows);
+    }
+    int it = 0, nqs = 0, ndo = 0;   // tiles of Q and dO asked for
+    for (; it < n; ++it) {
+      const int g = it / nq, qi = j + it - g * nq, col = (hk * p.per + g) * D;
+      const int a = it % C::kQ, b = it % C::kDo;
+      if (it >= C::kQ && !warp_wait(&q_empty[a], (uint32_t)(it / C::kQ - 1) & 1u, 1u, p.err, p.limit)) break;
+      ++nqs;
+      if (!fetch(sq + a * C::kTile, &p.tq, &q_full[a], fix_q, col, qi)) break;
+      if (it >= C::kDo && !warp_wait(&do_empty[b], (uint32_t)(it / C::kDo - 1) & 1u, 1u, p.err, p.limit)) break;
+      ++ndo;
+      if (!fetch(sdo + b * C::kTile, &p.tdo, &do_full[b], fix_do, col, qi)) break;
+      if (t.len - qi * kRows < kRows) ++fixes;
+    }
+    if (lane == 0) {   // every copy has landed before the CTA ends
+      mbar_wait(k_full, 0u, 1u, p.err);
+      mbar_wait(v_full, 0u, 1u, p.err);
+      for (int k = nqs > C::kQ ? nqs - C::kQ : 0; k < nqs; ++k)
+        if (!mbar_wait(&q_full[k % C::kQ], (uint32_t)(k / C::kQ) & 1u, 1u, p.err)) break;
+      for (int k = ndo > C::kDo ? ndo - C::kDo : 0; k < ndo; ++k)
+        if (!mbar_wait(&do_full[k % C::kDo], (uint32_t)(k / C::kDo) & 1u, 1u, p.err)) break;
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ---- products ----
+    if (lane == 0) {
+      const uint32_t ak = smem_u32(sk), av = smem_u32(sv), aq = smem_u32(sq), ado = smem_u32(sdo);
+      auto wait = [&](uint64_t* b, uint32_t par) {
+        const bool ok = mbar_wait_strict(b, par, 2u, p.err, p.limit);
+        fence_after();
+        return ok;
+      };
+      auto q_in = [&](int it) { return wait(&q_full[it % C::kQ], (uint32_t)(it / C::kQ) & 1u); };
+      auto do_in = [&](int it) { return wait(&do_full[it % C::kDo], (uint32_t)(it / C::kDo) & 1u); };
+      auto q_at = [&](int it) { return aq + (uint32_t)(it % C::kQ) * C::kTile; };
+      auto do_at = [&](int it) { return ado + (uint32_t)(it % C::kDo) * C::kTile; };
+      const uint32_t ts = tmem + C::kS, tp = tmem + C::kDp;
+      bool ok = wait(k_full, 0u) && q_in(0);
+      if (ok) {
+        Tl::mma_nt(ts, ak, q_at(0), C::kIdS);
+        umma_commit(s_full);
+        ok = wait(v_full, 0u) && do_in(0);
+      }
+      if (ok) {
+        Tl::mma_nt(tp, av, do_at(0), C::kIdS);
+        umma_commit(dp_full);
+      }
+      for (int it = 0; it < n && ok; ++it) {
+        const uint32_t par = (uint32_t)it & 1u;
+        if (!(ok = wait(p_full, par))) break;
+        Tl::mma_tn(tmem + C::kDv, ts, ts + 64, do_at(it), C::kIdD, it > 0);
+        umma_commit(&do_empty[it % C::kDo]);
+        if (it + 1 < n) {
+          if (!(ok = q_in(it + 1))) break;
+          Tl::mma_nt(ts, ak, q_at(it + 1), C::kIdS);
+          umma_commit(s_full);
+        }
+        if (!(ok = wait(ds_full, par))) break;
+        Tl::mma_tn(tmem + C::kDk, tp, tp + 64, q_at(it), C::kIdD, it > 0);
+        umma_commit(&q_empty[it % C::kQ]);
+        if (it + 1 < n) {
+          if (!(ok = do_in(it + 1))) break;
+          Tl::mma_nt(tp, av, do_at(it + 1), C::kIdS);
+          umma_commit(dp_full);
+        }
+      }
+      if (ok) umma_commit(all);
+      umma_commit(done);   // every product has completed before the tensor memory is freed
+      mbar_wait(done, 0u, 2u, p.err);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ---- statistics of the query tile, four queries per lane, read one tile ahead ----
+    float vl[4], vd[4];
+    auto read = [&](int it) {
+      const int g = it / nq, qi = j + it - g * nq;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = qi * kRows + lane + 32 * k;
+        const bool in = it < n && r < t.len;
+        const int64_t at = (int64_t)(hk * p.per + g) * p.T + t.row0 + r;
+        vl[k] = in ? __ldg(p.lse + at) * kLog2e : INFINITY;   // a query behind the sequence: P = 0
+        vd[k] = in ? __ldg(p.delta + at) : 0.f;
+      }
+    };
+    read(0);
+    for (int it = 0; it < n; ++it) {
+      if (it && !warp_wait(lse_empty, (uint32_t)(it - 1) & 1u, 1u, p.err, p.limit)) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s_lse[lane + 32 * k] = vl[k];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(lse_full);
+      if (it && !warp_wait(delta_empty, (uint32_t)(it - 1) & 1u, 1u, p.err, p.limit)) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s_delta[lane + 32 * k] = vd[k];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(delta_full);
+      read(it + 1);
+    }
+  } else if (warp < 8) {
+    compute_regs();
+    // ---- elementwise: thread = key r, queries 64 w .. 64 w + 63 ----
+    const int w = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = lanes + C::kS + 64 * w, tp = lanes + C::kDp + 64 * w;
+    const f2 c2 = mk2(p.c, p.c);
+    bool ok = true;
+    for (int it = 0; it < n; ++it) {
+      const uint32_t par = (uint32_t)it & 1u;
+      const int qi = j + it % nq;
+      if (!(ok = warp_wait(lse_full, par, 4u, p.err, p.limit) && warp_wait(s_full, par, 4u, p.err, p.limit))) break;
+      fence_after();
+      uint32_t x[64], u[32];
+      tmem_ld32_nw(ts, x);
+      tmem_ld32_nw(ts + 32, x + 32);
+      tmem_wait_ld_n<64>(x);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float4 z = *reinterpret_cast<const float4*>(s_lse + 64 * w + 4 * k);
+        const float2 a = un2(fma2(mk2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])), c2, mk2(-z.x, -z.y)));
+        const float2 b = un2(fma2(mk2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])), c2, mk2(-z.z, -z.w)));
+        x[4 * k] = __float_as_uint(exp2_(a.x));
+        x[4 * k + 1] = __float_as_uint(exp2_(a.y));
+        x[4 * k + 2] = __float_as_uint(exp2_(b.x));
+        x[4 * k + 3] = __float_as_uint(exp2_(b.y));
+      }
+      const bool diagonal = qi == j;   // queries from the key's own on
+      if (diagonal) {
+#pragma unroll
+        for (int k = 0; k < 64; ++k)
+          if (64 * w + k < r) x[k] = 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < 32; ++k) u[k] = pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+      tmem_st32(ts, u);
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(p_full);
+        mbar_arrive(lse_empty);
+      }
+      if (!(ok = warp_wait(delta_full, par, 4u, p.err, p.limit) && warp_wait(dp_full, par, 4u, p.err, p.limit))) break;
+      fence_after();
+      uint32_t y[64];
+      tmem_ld32_nw(tp, y);
+      tmem_ld32_nw(tp + 32, y + 32);
+      tmem_wait_ld_n<64>(y);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float4 z = *reinterpret_cast<const float4*>(s_delta + 64 * w + 4 * k);
+        const float2 a = un2(mul2(mk2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])),
+                                  add2(mk2(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1])), mk2(-z.x, -z.y))));
+        const float2 b = un2(mul2(mk2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])),
+                                  add2(mk2(__uint_as_float(y[4 * k + 2]), __uint_as_float(y[4 * k + 3])), mk2(-z.z, -z.w))));
+        u[2 * k] = pack_bf16(a.x, a.y);
+        u[2 * k + 1] = pack_bf16(b.x, b.y);
+      }
+      tmem_st32(tp, u);
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(ds_full);
+        mbar_arrive(delta_empty);
+      }
+    }
+    if (ok && warp_wait(all, 0u, 4u, p.err, p.limit)) {
+      fence_after();
+      const int row = j * kRows + r;
+      const int64_t at = (int64_t)t.row0 + row;
+      if (w == 0)
+        store_row<D>(lanes + C::kDv, 1.f, p.dV + at * p.ld_v + (int64_t)hk * D, row < t.len);
+      else
+        store_row<D>(lanes + C::kDk, p.scale, p.dK + at * p.ld_k + (int64_t)hk * D, row < t.len);
+    }
+    fence_before();
+  }
+  __syncthreads();
+  if (warp == 9) {
+    fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- dQ ------------------------------------------------------------------------------------
+template <int D>
+struct DqCfg {
+  static constexpr int kTile = Tile<D>::kBytes;
+  static constexpr int kK = 3, kV = 2;   // tiles of K and V in flight or in use: V's are free earlier
+  static constexpr int kBarriers = 512;
+  static constexpr int kSmem = (2 + kK + kV) * kTile + kBarriers + 1024 /*alignment*/;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static constexpr uint32_t kIdS = idesc(kFmtBF16, 128, 128);
+  static constexpr uint32_t kIdD = idesc(kFmtBF16, 128, D, false, true);
+  static constexpr uint32_t kS = 0, kDp = 256, kDq = 384;   // tensor memory; S has two buffers
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__ BwdK p) {
+  using C = DqCfg<D>;
+  using Tl = Tile<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sq = base;
+  uint8_t* sdo = sq + C::kTile;
+  uint8_t* sk = sdo + C::kTile;
+  uint8_t* sv = sk + C::kK * C::kTile;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sv + C::kV * C::kTile);
+  uint64_t* k_empty = k_full + C::kK;
+  uint64_t* v_full = k_empty + C::kK;
+  uint64_t* v_empty = v_full + C::kV;
+  uint64_t* q_full = v_empty + C::kV;
+  uint64_t* do_full = q_full + 1;
+  uint64_t* s_full = do_full + 1;    // [2]
+  uint64_t* dp_full = s_full + 2;
+  uint64_t* ds_full = dp_full + 1;   // dS is in place, S and dP have been read
+  uint64_t* fixed = ds_full + 1;
+  uint64_t* all = fixed + 1;
+  uint64_t* done = all + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  static_assert((2 * (C::kK + C::kV) + 9) * 8 + 4 <= C::kBarriers, "barriers");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  grid_dep_sync();
+  const int li = blockIdx.x / p.heads, h = blockIdx.x - li * p.heads;
+  if (li >= __ldg(p.count)) return;
+  const AttnTile t = p.tiles[li];
+  const int qi = t.index, n = t.index + 1;   // key tiles
+  const int q_col = h * D, k_col = h / p.per * D;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kK; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < C::kV; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(do_full, 1);
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, 8);
+    mbar_init(fixed, 1);
+    mbar_init(all, 1);
+    mbar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async();
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 8) issue_regs();
+  if (warp == 8) {
+    // ---- loads ----
+    if (lane == 0) {
+      mbar_expect_tx(q_full, C::kTile);
+      Tl::load(sq, &p.tq, q_full, q_col, t.row0 + qi * kRows);
+      mbar_expect_tx(do_full, C::kTile);
+      Tl::load(sdo, &p.tdo, do_full, q_col, t.row0 + qi * kRows);
+    }
+    int jk = 0, jv = 0;   // tiles of K and V asked for
+    for (int j = 0; j < n; ++j) {
+      const int a = j % C::kK, b = j % C::kV, rows = t.len - j * kRows;
+      if (j >= C::kK && !warp_wait(&k_empty[a], (uint32_t)(j / C::kK - 1) & 1u, 1u, p.err, p.limit)) break;
+      // K's rows behind the sequence are zeroed: dS is zero there, but zero times a NaN is not
+      const bool fix = rows < kRows;
+      uint8_t* dst = sk + a * C::kTile;
+      if (lane == 0) {
+        uint64_t* bar = fix ? fixed : &k_full[a];
+        mbar_expect_tx(bar, C::kTile);
+        Tl::load(dst, &p.tk, bar, k_col, t.row0 + j * kRows);
+      }
+      ++jk;
+      if (fix) {   // the sequence's last tile: at most once
+        if (!__all_sync(0xffffffffu, mbar_wait(fixed, 0u, 1u, p.err))) break;
+        Tl::zero_rows(dst, rows, lane);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[a]);
+      }
+      if (j >= C::kV && !warp_wait(&v_empty[b], (uint32_t)(j / C::kV - 1) & 1u, 1u, p.err, p.limit)) break;
+      if (lane == 0) {
+        mbar_expect_tx(&v_full[b], C::kTile);
+        Tl::load(sv + b * C::kTile, &p.tv, &v_full[b], k_col, t.row0 + j * kRows);
+      }
+      ++jv;
+    }
+    if (lane == 0) {   // every copy has landed before the CTA ends
+      mbar_wait(q_full, 0u, 1u, p.err);
+      mbar_wait(do_full, 0u, 1u, p.err);
+      for (int k = jk > C::kK ? jk - C::kK : 0; k < jk; ++k)
+        if (!mbar_wait(&k_full[k % C::kK], (uint32_t)(k / C::kK) & 1u, 1u, p.err)) break;
+      for (int k = jv > C::kV ? jv - C::kV : 0; k < jv; ++k)
+        if (!mbar_wait(&v_full[k % C::kV], (uint32_t)(k / C::kV) & 1u, 1u, p.err)) break;
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ---- products ----
+    if (lane == 0) {
+      const uint32_t aq = smem_u32(sq), ado = smem_u32(sdo), ak = smem_u32(sk), av = smem_u32(sv);
+      auto wait = [&](uint64_t* b, uint32_t par) {
+        const bool ok = mbar_wait_strict(b, par, 2u, p.err, p.limit);
+        fence_after();
+        return ok;
+      };
+      auto k_in = [&](int j) { return wait(&k_full[j % C::kK], (uint32_t)(j / C::kK) & 1u); };
+      auto v_in = [&](int j) { return wait(&v_full[j % C::kV], (uint32_t)(j / C::kV) & 1u); };
+      auto score = [&](int j) {
+        Tl::mma_nt(tmem + C::kS + 128 * (j & 1), aq, ak + (uint32_t)(j % C::kK) * C::kTile, C::kIdS);
+        umma_commit(&s_full[j & 1]);
+      };
+      auto grad = [&](int j) {
+        Tl::mma_nt(tmem + C::kDp, ado, av + (uint32_t)(j % C::kV) * C::kTile, C::kIdS);
+        umma_commit(dp_full);
+        umma_commit(&v_empty[j % C::kV]);
+      };
+      bool ok = wait(q_full, 0u) && k_in(0);
+      if (ok) {
+        score(0);
+        ok = wait(do_full, 0u) && v_in(0);
+      }
+      if (ok) grad(0);
+      for (int j = 0; j < n && ok; ++j) {
+        if (j + 1 < n) {   // (its buffer of S was read before dS of tile j - 1 was in place)
+          if (!(ok = k_in(j + 1))) break;
+          score(j + 1);
+        }
+        if (!(ok = wait(ds_full, (uint32_t)j & 1u))) break;
+        const uint32_t td = tmem + C::kDp;
+        Tl::mma_tn(tmem + C::kDq, td, td + 64, ak + (uint32_t)(j % C::kK) * C::kTile, C::kIdD, j > 0);
+        umma_commit(&k_empty[j % C::kK]);
+        if (j + 1 < n) {
+          if (!(ok = v_in(j + 1))) break;
+          grad(j + 1);
+        }
+      }
+      if (ok) umma_commit(all);
+      umma_commit(done);   // every product has completed before the tensor memory is freed
+      mbar_wait(done, 0u, 2u, p.err);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    compute_regs();
+    // ---- elementwise: thread = query r, keys 64 w .. 64 w + 63 ----
+    const int w = warp >> 2, r = threadIdx.x & 127, row = qi * kRows + r;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = lanes + C::kS + 64 * w, tp = lanes + C::kDp + 64 * w;
+    const int64_t at = (int64_t)t.row0 + row;
+    const bool live = row < t.len;
+    const float lse = live ? __ldg(p.lse + (int64_t)h * p.T + at) * kLog2e : 0.f;
+    const float delta = live ? __ldg(p.delta + (int64_t)h * p.T + at) : 0.f;
+    const f2 c2 = mk2(p.c, p.c), l2 = mk2(-lse, -lse), d2 = mk2(-delta, -delta);
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      if (!(ok = warp_wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u, 4u, p.err, p.limit))) break;
+      fence_after();
+      uint32_t x[64], y[64], u[32];
+      tmem_ld32_nw(ts + 128 * (j & 1), x);
+      tmem_ld32_nw(ts + 128 * (j & 1) + 32, x + 32);
+      tmem_wait_ld_n<64>(x);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const float2 a = un2(fma2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, l2));
+        x[2 * k] = __float_as_uint(exp2_(a.x));
+        x[2 * k + 1] = __float_as_uint(exp2_(a.y));
+      }
+      if (!(ok = warp_wait(dp_full, (uint32_t)j & 1u, 4u, p.err, p.limit))) break;
+      fence_after();
+      tmem_ld32_nw(tp, y);
+      tmem_ld32_nw(tp + 32, y + 32);
+      tmem_wait_ld_n<64>(y);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const f2 d = mul2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])),
+                          add2(mk2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), d2));
+        const float2 a = un2(d);
+        x[2 * k] = __float_as_uint(a.x);
+        x[2 * k + 1] = __float_as_uint(a.y);
+      }
+      if (j == n - 1) {   // the tile on the diagonal: keys up to the query's own
+#pragma unroll
+        for (int k = 0; k < 64; ++k)
+          if (64 * w + k > r) x[k] = 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < 32; ++k) u[k] = pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+      tmem_st32(tp, u);
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    if (ok && warp_wait(all, 0u, 4u, p.err, p.limit)) {
+      fence_after();
+      store_row<D / 2>(lanes + C::kDq + w * (D / 2), p.scale,
+                       p.dQ + at * p.ld_q + (int64_t)h * D + w * (D / 2), live);
+    }
+    fence_before();
+  }
+  __syncthreads();
+  if (warp == 9) {
+    fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t st) {
+  static std::atomic<uint64_t> set{0};
+  cudaError_t e = once_on_device(set, [] {
+    const cudaError_t r = set_up(k_attn_dkv<D>, DkvCfg<D>::kSmem);
+    return r != cudaSuccess ? r : set_up(k_attn_dq<D>, DqCfg<D>::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  BwdK k{};
+  if (!attn_map(&k.tq, a.Q, a.q_heads * D, a.T, a.ld_q) || !attn_map(&k.tk, a.K, a.kv_heads * D, a.T, a.ld_k) ||
+      !attn_map(&k.tv, a.V, a.kv_heads * D, a.T, a.ld_v) || !attn_map(&k.tdo, a.dO, a.q_heads * D, a.T, a.ld_o))
+    return cudaErrorInvalidValue;
+  k.count = a.plan.count;
+  k.tiles = a.plan.tiles[0];
+  k.per = a.q_heads / a.kv_heads;
+  k.c = a.scale * kLog2e;
+  k.scale = a.scale;
+  k.T = a.T; k.ld_q = a.ld_q; k.ld_k = a.ld_k; k.ld_v = a.ld_v;
+  k.lse = a.lse; k.delta = a.delta;
+  k.dQ = static_cast<__nv_bfloat16*>(a.dQ);
+  k.dK = static_cast<__nv_bfloat16*>(a.dK);
+  k.dV = static_cast<__nv_bfloat16*>(a.dV);
+  k.err = error_word();
+  if (!k.err) return cudaErrorInvalidDevice;
+  k.limit = tc_wait_limit();
+  const int64_t pre = (a.T * a.q_heads * (D / 8) + 255) / 256, grid = a.plan.most[0] * a.q_heads;
+  if (grid > INT32_MAX || pre > INT32_MAX) return cudaErrorInvalidValue;
+  prof_begin(0, st);
+  e = launch_kernel(k_attn_delta<D>, (unsigned)pre, 256, 0, st, static_cast<const __nv_bfloat16*>(a.O),
+                    static_cast<const __nv_bfloat16*>(a.dO), a.ld_o, (int)a.q_heads, a.T, a.delta);
+  if (e != cudaSuccess) return e;
+  k.heads = a.kv_heads;
+  prof_begin(0, st);
+  e = launch_kernel(k_attn_dkv<D>, (unsigned)(a.plan.most[0] * a.kv_heads), kThreads, DkvCfg<D>::kSmem, st, k);
+  if (e != cudaSuccess) return e;
+  k.heads = a.q_heads;
+  prof_begin(0, st);
+  return launch_kernel(k_attn_dq<D>, (unsigned)grid, kThreads, DqCfg<D>::kSmem, st, k);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_backward(const AttnArgs& a, cudaStream_t st) {
+  return a.dim == 128 ? bwd_launch<128>(a, st) : bwd_launch<64>(a, st);
+}
+
+}  // namespace lora

@@ -1,0 +1,173 @@
+// What the attention kernels share: tensor-memory moves of 32 columns, products whose first operand lies
+// in tensor memory, packed fp32 arithmetic, loads of a tile and the zeroing of rows past a sequence.
+#pragma once
+
+#include "tc_ptx.cuh"
+
+namespace lora {
+
+// Tensor map of a [rows, cols] bf16 matrix with ld elements from row to row, in boxes of 128 x 64 (attention.cu).
+bool attn_map(CUtensorMap* map, const void* ptr, int64_t cols, int64_t rows, int64_t ld);
+
+namespace attn {
+
+using namespace tc;
+
+constexpr int kRows = kAttnTile;
+// 384 threads: eight warps that compute, then a warpgroup that loads and issues and leaves them its registers.
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168, kIssueRegs = 72, kComputeRegs = 216;   // per thread
+static_assert(128 * kIssueRegs + 256 * kComputeRegs <= kThreads * kLaunchRegs,
+              "setmaxnreg draws on the block's own registers");
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ---- packed fp32 pairs ----
+using f2 = uint64_t;
+__device__ __forceinline__ f2 mk2(float a, float b) {
+  f2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ float2 un2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float exp2_(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ---- tensor memory, 32 columns of this thread's lane ----
+__device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t* r) {   // valid after ld_wait and hold
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The same as tmem_wait_ld for a run of registers.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld_n(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i])::"memory");
+}
+
+// D += A B with A [128, 16] in tensor memory: lane = row, two bf16 of k per 32-bit column.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc));
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// A tile: 128 rows of D bf16, as D / 64 boxes of 128 rows of 128 swizzled bytes.
+template <int D>
+struct Tile {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kBoxBytes = kRows * 128;
+  static constexpr int kBytes = kBoxes * kBoxBytes;
+  // rows x columns as they lie (k along the columns) and turned (k along the rows)
+  __device__ static void load(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int col, int row) {
+#pragma unroll
+    for (int b = 0; b < kBoxes; ++b) tma_load_2d(dst + b * kBoxBytes, map, bar, col + 64 * b, row);
+  }
+  // D[128, 128] = A B^T over the tiles' D columns
+  __device__ static void mma_nt(uint32_t d, uint32_t sa, uint32_t sb, uint32_t id) {
+#pragma unroll
+    for (int b = 0; b < kBoxes; ++b) {
+      const uint64_t da = smem_desc_sw128(sa + b * kBoxBytes), db = smem_desc_sw128(sb + b * kBoxBytes);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) umma_f16(d, da + 2 * k, db + 2 * k, id, (b || k) ? 1u : 0u);
+    }
+  }
+  // D[128, D] += A B over the tile's 128 rows, A in tensor memory: its columns of 64 rows each start at a0 and a1
+  __device__ static void mma_tn(uint32_t d, uint32_t a0, uint32_t a1, uint32_t sb, uint32_t id, bool acc) {
+    const uint64_t db = smem_desc_sw128_mn(sb, kBoxBytes);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      umma_f16_ts(d, (k < 4 ? a0 + 8 * k : a1 + 8 * (k - 4)), db + 128 * k, id, (acc || k) ? 1u : 0u);
+  }
+  // Zeros in the rows from `rows` on, by a whole warp (the swizzle moves 16-byte pieces within a row only).
+  __device__ static void zero_rows(uint8_t* tile, int rows, int lane) {
+    const int n = (kRows - rows) * 8;
+#pragma unroll
+    for (int b = 0; b < kBoxes; ++b)
+      for (int i = lane; i < n; i += 32)
+        *reinterpret_cast<uint4*>(tile + b * kBoxBytes + rows * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+  }
+};
+
+__device__ __forceinline__ void issue_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs)); }
+__device__ __forceinline__ void compute_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs)); }
+
+// A kernel's attributes. A build that launches with fewer registers would wait for them forever.
+template <typename F>
+cudaError_t set_up(F* kernel, int smem) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaFuncAttributes fa;
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
+  if (e == cudaSuccess && fa.numRegs != kLaunchRegs) e = cudaErrorInvalidConfiguration;
+  return e;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t bit, uint32_t* err,
+                                          unsigned long long limit) {
+  return __all_sync(0xffffffffu, mbar_wait_strict(bar, parity, bit, err, limit));
+}
+
+}  // namespace attn
+}  // namespace lora

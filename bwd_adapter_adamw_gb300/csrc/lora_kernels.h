@@ -457,6 +457,59 @@ struct SumArgs {
 };
 cudaError_t launch_sum(const SumArgs& a, cudaStream_t st);
 
+// ---- head_rope.cu ----
+struct RopeArgs {
+  int64_t T, n_pos;
+  int32_t dim;
+  int32_t dtype;             // LORA_F32 | LORA_BF16
+  bool pairs;
+  float eps;
+  const void* x[2];          // q, k
+  void* y[2];                // y or dx
+  const void* dy[2];         // backward
+  const float* gamma[2];     // both or none
+  float* dgamma[2];
+  int64_t ld_x[2], ld_y[2];  // x and dx, y and dy
+  int32_t heads[2];
+  const int32_t* pos;
+  const float* table;
+  float* part;               // backward: [kRopeMostCtas][2][dim]
+};
+constexpr int kRopeMostCtas = 2 * 152;
+cudaError_t launch_rope(const RopeArgs& a, bool bwd, cudaStream_t st);
+cudaError_t launch_rope_table(int64_t n_pos, int dim, const double* inv_freq, float* table, cudaStream_t st);
+
+// ---- attention.cu, attention_bwd.cu ----
+constexpr int kAttnTile = 128;   // rows of a tile
+struct AttnTile {                // of a sequence of `len` rows from row `row0`
+  int32_t row0, len, index, pad;
+};
+// The plan's parts within its buffer.
+struct AttnPlan {
+  int32_t* count;      // [2] tiles of 128 rows, of 256 rows
+  AttnTile* tiles[2];
+  int64_t most[2];     // room for them
+  int2* seq;           // [n_seq] first row, rows
+  int32_t* hist;       // [buckets of 128 rows]
+  size_t bytes;
+};
+AttnPlan attn_plan(int64_t T, int32_t n_seq, void* buf);
+cudaError_t launch_attn_plan(int64_t T, int32_t n_seq, const int32_t* seq_start, const AttnPlan& plan, cudaStream_t st);
+struct AttnArgs {
+  int64_t T;
+  int32_t q_heads, kv_heads, dim;
+  float scale;
+  int64_t ld_q, ld_k, ld_v, ld_o;
+  AttnPlan plan;
+  const void *Q, *K, *V, *dO;
+  void* O;
+  float* lse;
+  void *dQ, *dK, *dV;
+  float* delta;        // backward: [q_heads, T]
+};
+cudaError_t launch_attn_forward(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_attn_backward(const AttnArgs& a, cudaStream_t st);
+
 // ---- muon.cu ----
 struct MuonMat {             // s x n over the smaller and the longer side
   int64_t offset;

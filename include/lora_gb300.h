@@ -341,6 +341,96 @@ int lora_norm_backward(const lora_norm_desc* d, int64_t T, const void* X, const 
 #define LORA_SUM_MAX 16
 int lora_sum(int32_t n, const void* const* src, int64_t count, int32_t dtype, void* dst, void* stream);
 
+/* ---- between an attention block's projections --------------------------------------------------*/
+/* Norm of each query and key head and rotation by position, in one pass. For the head vector x of a
+ * token at position n (pairs (a, b) of elements: LORA_ROPE_HALVES element i with i + head_dim / 2,
+ * LORA_ROPE_PAIRS element 2 i with 2 i + 1; c, s = table[n, i]):
+ *   r = 1 / sqrt(sum x^2 / head_dim + eps),  xhat = x r,  h = gamma xhat      (gamma NULL: h = x)
+ *   forward   y: (a, b) -> (a c - b s, a s + b c) of h
+ *   backward  h' = dy turned back (s -> -s);  dgamma += sum over tokens and heads of h' xhat
+ *             g = gamma h';  dx = r (g - xhat (sum g xhat) / head_dim)       (gamma NULL: dx = h')
+ * Q [T, q_heads, head_dim] and K [T, k_heads, head_dim] (k_heads may be 0: K and its outputs are not
+ * read) with ld_q, ld_k elements from token to token, so that both may be columns of a fused
+ * projection's output; dQ and dK have the same strides, YQ, YK, dYQ, dYK have ld_yq, ld_yk. A stride of
+ * 0 stands for heads * head_dim. gamma_q, gamma_k and their gradients fp32 [head_dim]; gamma_q and
+ * gamma_k are both given or both NULL, and without them the backward pass does not read Q and K (which
+ * may be NULL) and takes no gradients of them. dgamma_q and dgamma_k may be NULL each. pos int32 [T] on
+ * the device: a token with a negative position is padding, its rows are left as they were and it adds
+ * nothing to the gradients; a position from n_pos on gives NaN. table fp32 [n_pos, head_dim / 2, 2]
+ * (cosine, sine), 16-byte aligned. An output may be an input of the same strides (one decoded token in
+ * place). Sums in fp32, outputs rounded once, the gradients' sums in a fixed order: reruns are bitwise
+ * equal. head_dim 64, 128 or 256, at most 2^13 heads in all, T below 2^31 - 256 and n_pos at most 2^24
+ * (LORA_ERR_UNSUPPORTED); strides multiples of 16 bytes (LORA_ERR_ALIGN); T = 0 is a no-op. */
+#define LORA_ROPE_HALVES 0
+#define LORA_ROPE_PAIRS 1
+typedef struct lora_rope_desc {
+  int32_t q_heads;
+  int32_t k_heads;
+  int32_t head_dim;
+  int32_t dtype;       /* LORA_F32 | LORA_BF16 */
+  int32_t layout;      /* LORA_ROPE_HALVES | LORA_ROPE_PAIRS */
+  float eps;           /* >= 0 */
+  int64_t ld_q, ld_k, ld_yq, ld_yk;
+} lora_rope_desc;
+/* table[n, i] = (cos, sin)(n inv_freq[i]) for n < n_pos, the angles in double (inv_freq: device
+ * doubles [head_dim / 2], 16-byte aligned), rounded to fp32 once. */
+int lora_rope_table(int64_t n_pos, int32_t head_dim, const double* inv_freq, float* table, void* stream);
+int lora_rope_forward(const lora_rope_desc* d, int64_t T, const void* Q, const void* K,
+                      const float* gamma_q, const float* gamma_k, const int32_t* pos,
+                      const float* table, int64_t n_pos, void* YQ, void* YK, void* stream);
+size_t lora_rope_backward_workspace_size(const lora_rope_desc* d, int64_t T);
+int lora_rope_backward(const lora_rope_desc* d, int64_t T, const void* Q, const void* K,
+                       const float* gamma_q, const float* gamma_k, const int32_t* pos,
+                       const float* table, int64_t n_pos, const void* dYQ, const void* dYK, void* dQ,
+                       void* dK, float* dgamma_q, float* dgamma_k, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/* Causal attention over packed sequences with grouped heads. Sequence k covers tokens
+ * [seq_start[k], seq_start[k + 1]); query head h reads key / value head h / (q_heads / kv_heads):
+ *   S[i, j] = scale q_i . k_j for j <= i of the same sequence,  lse_i = log sum_j exp S[i, j]
+ *   forward   P = exp(S - lse),  o_i = sum_j P[i, j] v_j
+ *   backward  (from q, k, v, o, lse and do)  delta_i = do_i . o_i,
+ *             dS[i, j] = P[i, j] (do_i . v_j - delta_i),
+ *             dv_j = sum_i P[i, j] do_i,  dk_j = scale sum_i dS[i, j] q_i,  dq_i = scale sum_j dS[i, j] k_j
+ *             (dk and dv summed over the query heads of their group)
+ * Q, O, dO, dQ [T, q_heads, head_dim] and K, V, dK, dV [T, kv_heads, head_dim], bf16, with ld_q (Q and
+ * dQ), ld_k, ld_v, ld_o (O and dO) elements from token to token (0: heads * head_dim), so that all may be
+ * columns of wider buffers; lse fp32 [q_heads, T]. Tokens behind the last sequence (and between two) are
+ * padding: their rows of the outputs are left as they were and no other row depends on theirs, whatever
+ * they hold. A NaN or infinity within a sequence may reach any row of that sequence.
+ * Products on tensor cores with fp32 sums; scores, statistics and the softmax in fp32; P and dS are
+ * rounded to bf16 (2^-8 of each) as operands of the second products, everything else once at the end. No
+ * atomics: reruns are bitwise equal.
+ * head_dim 64 or 128, q_heads a multiple of kv_heads, dtype LORA_BF16, heads * head_dim at most 2^20 and T
+ * below 2^31 - 256 (LORA_ERR_UNSUPPORTED); strides multiples of 8 elements and at least heads * head_dim
+ * (LORA_ERR_ALIGN, LORA_ERR_INVALID); T = 0 is a no-op. Outputs do not overlap inputs.
+ * When lora_device_check reports LORA_ERR_TIMEOUT after it, an element of an output holds its value or
+ * is as it was. */
+typedef struct lora_attn_desc {
+  int32_t q_heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t dtype;       /* LORA_BF16 */
+  float scale;         /* > 0, usually 1 / sqrt(head_dim) */
+  int64_t ld_q, ld_k, ld_v, ld_o;
+} lora_attn_desc;
+/* The tiles of a batch, longest first, from the sequences' table (device int32 [n_seq + 1],
+ * non-decreasing, within [0, T]; offsets outside are clamped, and a sequence that would begin before the
+ * end of an earlier one begins there). One plan, in a caller-owned device buffer of
+ * lora_attn_plan_size(T, n_seq) bytes, 16-byte aligned, serves every layer's forward and backward calls
+ * over the same batch, on any streams ordered after the build; these pass the same T and n_seq. n_seq from
+ * 1 to 2^24. One launch. */
+size_t lora_attn_plan_size(int64_t T, int32_t n_seq);
+int lora_attn_plan_build(int64_t T, int32_t n_seq, const int32_t* d_seq_start, void* plan,
+                         size_t plan_bytes, void* stream);
+int lora_attn_forward(const lora_attn_desc* d, int64_t T, int32_t n_seq, const void* plan,
+                      const void* Q, const void* K, const void* V, void* O, float* lse, void* stream);
+size_t lora_attn_backward_workspace_size(const lora_attn_desc* d, int64_t T);
+int lora_attn_backward(const lora_attn_desc* d, int64_t T, int32_t n_seq, const void* plan,
+                       const void* Q, const void* K, const void* V, const void* O, const float* lse,
+                       const void* dO, void* dQ, void* dK, void* dV, void* ws, size_t ws_bytes,
+                       void* stream);
+
 /* ---- orthogonalised update (in place of lora_adamw_step for the adapter matrices) -------------*/
 /* One matrix of the flat arenas, [rows, cols] row-major from element `offset` (a multiple of 4).
  * The smaller side is at most LORA_MAX_RANK and a multiple of 4. `group` indexes the call's groups
