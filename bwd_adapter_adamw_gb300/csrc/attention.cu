@@ -157,7 +157,7 @@ struct FwdK {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant__ FwdK p) {
+__global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid_constant__ FwdK p) {
   using C = FwdCfg<D>;
   using Tl = Tile<D>;
   constexpr int ST = C::kStages;
@@ -174,12 +174,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
   uint64_t* fixed = o_full + 2;      // a tile whose rows are zeroed behind a sequence has landed
   uint64_t* done = fixed + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   grid_dep_sync();
   const int li = blockIdx.x / p.groups, gi = blockIdx.x - li * p.groups;
   if (li >= __ldg(p.count)) return;
-  const AttnTile t = p.tiles[li];
+  const AttnTile t = tile_at(p.tiles + li);
   // tile s: query rows row0 + 128 qi[s] .., head h[s], keys of n[s] tiles
   const int h0 = p.by_heads ? 2 * gi : gi, h1 = p.by_heads ? h0 + 1 : h0;
   const int i0 = p.by_heads ? t.index : 2 * t.index, i1 = p.by_heads ? i0 : i0 + 1;
@@ -207,9 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
-  if (warp >= 8) issue_regs();
+  if (warp >= 8) SplitFwd::issue();
   if (warp == 8) {
     // ---- loads: Q of both tiles, then K and V tile by tile ----
     if (lane == 0) {
@@ -253,24 +253,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     __syncwarp();
   } else if (warp == 9) {
     // ---- products ----
-    if (lane == 0) {
+    {
+      const uint32_t one = elect_one();
       const uint32_t q0 = smem_u32(sq), rg = smem_u32(ring);
       auto wait = [&](uint64_t* b, uint32_t par) {
-        const bool ok = mbar_wait_strict(b, par, 2u, p.err, p.limit);
+        const bool ok = warp_wait(b, par, 2u, p.err, p.limit);
         fence_after();
         return ok;
       };
       auto stage_full = [&](int g) { return wait(&full[g % ST], (uint32_t)(g / ST) & 1u); };
-      auto tile_at = [&](int g) { return rg + (uint32_t)(g % ST) * C::kTile; };
+      auto stage_at = [&](int g) { return rg + (uint32_t)(g % ST) * C::kTile; };
       bool ok = stage_full(0);
       for (int s = 0; s < 2 && ok; ++s) {
         if (s && !n1) break;
         ok = wait(&q_full[s], 0u);
         if (!ok) break;
-        Tl::mma_nt(tmem + C::kS + 128 * s, q0 + s * C::kTile, tile_at(0), C::kIdS);
-        umma_commit(&s_full[s]);
+        Tl::mma_nt(tmem + C::kS + 128 * s, q0 + s * C::kTile, stage_at(0), C::kIdS, one);
+        commit(&s_full[s], one);
       }
-      if (ok) umma_commit(&empty[0]);
+      if (ok) commit(&empty[0], one);
       for (int j = 0; j < n && ok; ++j) {
         const int gv = 2 * j + 1, gk = 2 * j + 2;
         ok = stage_full(gv);
@@ -281,27 +282,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           ok = wait(&p_full[s], (uint32_t)j & 1u);
           if (!ok) break;
           const uint32_t ps = tmem + C::kS + 128 * s;
-          Tl::mma_tn(tmem + C::kO + 128 * s, ps, ps + 32, tile_at(gv), C::kIdO, j > 0);
-          umma_commit(&o_full[s]);
+          Tl::template mma_tn<128>(tmem + C::kO + 128 * s, ps, stage_at(gv), C::kIdO, j > 0, one);
+          commit(&o_full[s], one);
           if (j + 1 < ns) {
             if (!have_k) ok = stage_full(gk);
             have_k = true;
             if (!ok) break;
-            Tl::mma_nt(ps, q0 + s * C::kTile, tile_at(gk), C::kIdS);
-            umma_commit(&s_full[s]);
+            Tl::mma_nt(ps, q0 + s * C::kTile, stage_at(gk), C::kIdS, one);
+            commit(&s_full[s], one);
           }
         }
         if (!ok) break;
-        umma_commit(&empty[gv % ST]);
-        if (have_k) umma_commit(&empty[gk % ST]);
+        commit(&empty[gv % ST], one);
+        if (have_k) commit(&empty[gk % ST], one);
       }
       // every product has completed before the tensor memory is freed
-      umma_commit(done);
+      commit(done, one);
       mbar_wait(done, 0u, 2u, p.err);
     }
     __syncwarp();
   } else if (warp < 8) {
-    compute_regs();
+    SplitFwd::compute();
     // ---- softmax and epilogue: thread = row of tile s ----
     const int s = warp >> 2, r = threadIdx.x & 127;
     const int ns = s ? n1 : n0, qi = s ? i1 : i0, h = s ? h1 : h0;
@@ -402,7 +403,7 @@ template <int D>
 cudaError_t fwd_launch(const AttnArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> set{0};
   cudaError_t e = once_on_device(set, [] {
-    return set_up(k_attn_fwd<D>, FwdCfg<D>::kSmem);
+    return set_up<SplitFwd>(k_attn_fwd<D>, FwdCfg<D>::kSmem);
   });
   if (e != cudaSuccess) return e;
   FwdK k{};
@@ -426,7 +427,7 @@ cudaError_t fwd_launch(const AttnArgs& a, cudaStream_t st) {
   const int64_t grid = a.plan.most[w] * k.groups;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   prof_begin(0, st);
-  return launch_kernel(k_attn_fwd<D>, (unsigned)grid, kThreads, FwdCfg<D>::kSmem, st, k);
+  return launch_kernel(k_attn_fwd<D>, (unsigned)grid, SplitFwd::kThreads, FwdCfg<D>::kSmem, st, k);
 }
 
 }  // namespace

@@ -12,7 +12,7 @@
 //
 // dV and dK (k_attn_dkv): the scores are computed turned, S^T = K Q^T and dP^T = V dO^T, keys along the
 // tensor memory's lanes, so that P^T and dS^T, written back over them in bf16, are first operands of
-// P^T dO and dS^T Q as they are; a thread has one key and half the tile's queries. The products of one
+// P^T dO and dS^T Q as they are; a thread has one key and 32 of the tile's queries. The products of one
 // query tile run while the other half of its elementwise work does: S^T of the next tile under dS^T of
 // this one, dP^T of the next under P^T of the next. At head_dim 128 a pair of tiles takes four products of
 // 512 cycles.
@@ -20,8 +20,8 @@
 // dQ (k_attn_dq): S = Q K^T and dP = dO V^T with queries along the lanes; dS, in bf16 over dP, is the first
 // operand of dS K. S alternates between two buffers, so that the next tile's S runs before this one's dS.
 //
-// CTA layout (384 threads): warps 0-7 elementwise (two warpgroups, 64 columns each) and epilogue, warp 8
-// loads, warp 9 issues the products, warp 10 brings the queries' statistics (k_attn_dkv). Waits are bounded
+// CTA layout (640 threads): warps 0-15 elementwise (four warpgroups, 32 columns each) and epilogue, warp 16
+// loads, warp 17 issues the products, warp 18 brings the queries' statistics (k_attn_dkv). Waits are bounded
 // as in the forward pass.
 #include "attn_common.cuh"
 
@@ -30,6 +30,11 @@ namespace lora {
 namespace {
 
 using namespace attn;
+
+using Sp = SplitBwd;
+constexpr int kGroups = (Sp::kThreads - 128) / 128;   // warpgroups that share a tile's columns
+constexpr int kCols = 128 / kGroups;                  // columns of a thread
+constexpr int kComputeWarps = 4 * kGroups, kLoadWarp = kComputeWarps, kIssueWarp = kLoadWarp + 1, kStatWarp = kLoadWarp + 2;
 
 // ---- delta ---------------------------------------------------------------------------------
 // delta[h, t] = sum do o, D / 8 lanes per head of a token. Bound by memory.
@@ -99,7 +104,7 @@ struct DkvCfg {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant__ BwdK p) {
+__global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_constant__ BwdK p) {
   using C = DkvCfg<D>;
   using Tl = Tile<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -130,12 +135,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
   uint64_t* done = all + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   static_assert((2 * (C::kQ + C::kDo) + 14) * 8 + 4 <= C::kBarriers, "barriers");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   grid_dep_sync();
   const int li = blockIdx.x / p.heads, hk = blockIdx.x - li * p.heads;
   if (li >= __ldg(p.count)) return;
-  const AttnTile t = p.tiles[li];
+  const AttnTile t = tile_at(p.tiles + li);
   const int nb = (t.len + kRows - 1) / kRows;
   const int j = nb - 1 - t.index;     // the key tile with t.index + 1 query tiles
   const int nq = t.index + 1, n = nq * p.per;   // iteration it: head it / nq of the group, query tile j + it % nq
@@ -152,13 +157,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     mbar_init(k_full, 1);
     mbar_init(v_full, 1);
     mbar_init(s_full, 1);
-    mbar_init(p_full, 8);
+    mbar_init(p_full, kComputeWarps);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8);
+    mbar_init(ds_full, kComputeWarps);
     mbar_init(lse_full, 1);
-    mbar_init(lse_empty, 8);
+    mbar_init(lse_empty, kComputeWarps);
     mbar_init(delta_full, 1);
-    mbar_init(delta_empty, 8);
+    mbar_init(delta_empty, kComputeWarps);
     mbar_init(fix_q, 1);
     mbar_init(fix_do, 1);
     mbar_init(all, 1);
@@ -166,14 +171,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
   }
-  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  if (warp == kIssueWarp) tmem_alloc(tmem_slot, 512);
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
-  if (warp >= 8) issue_regs();
-  if (warp == 8) {
+  if (warp >= kComputeWarps) Sp::issue();
+  if (warp == kLoadWarp) {
     // ---- loads ----
     int fixes = 0;   // of Q and of dO alike
     // Rows behind the sequence are zeroed: P^T and dS^T are zero there, but zero times a NaN is not.
@@ -219,12 +224,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         if (!mbar_wait(&do_full[k % C::kDo], (uint32_t)(k / C::kDo) & 1u, 1u, p.err)) break;
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kIssueWarp) {
     // ---- products ----
-    if (lane == 0) {
+    {
+      const uint32_t one = elect_one();
       const uint32_t ak = smem_u32(sk), av = smem_u32(sv), aq = smem_u32(sq), ado = smem_u32(sdo);
       auto wait = [&](uint64_t* b, uint32_t par) {
-        const bool ok = mbar_wait_strict(b, par, 2u, p.err, p.limit);
+        const bool ok = warp_wait(b, par, 2u, p.err, p.limit);
         fence_after();
         return ok;
       };
@@ -235,39 +241,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       const uint32_t ts = tmem + C::kS, tp = tmem + C::kDp;
       bool ok = wait(k_full, 0u) && q_in(0);
       if (ok) {
-        Tl::mma_nt(ts, ak, q_at(0), C::kIdS);
-        umma_commit(s_full);
+        Tl::mma_nt(ts, ak, q_at(0), C::kIdS, one);
+        commit(s_full, one);
         ok = wait(v_full, 0u) && do_in(0);
       }
       if (ok) {
-        Tl::mma_nt(tp, av, do_at(0), C::kIdS);
-        umma_commit(dp_full);
+        Tl::mma_nt(tp, av, do_at(0), C::kIdS, one);
+        commit(dp_full, one);
       }
       for (int it = 0; it < n && ok; ++it) {
         const uint32_t par = (uint32_t)it & 1u;
         if (!(ok = wait(p_full, par))) break;
-        Tl::mma_tn(tmem + C::kDv, ts, ts + 64, do_at(it), C::kIdD, it > 0);
-        umma_commit(&do_empty[it % C::kDo]);
+        Tl::template mma_tn<kCols>(tmem + C::kDv, ts, do_at(it), C::kIdD, it > 0, one);
+        commit(&do_empty[it % C::kDo], one);
         if (it + 1 < n) {
           if (!(ok = q_in(it + 1))) break;
-          Tl::mma_nt(ts, ak, q_at(it + 1), C::kIdS);
-          umma_commit(s_full);
+          Tl::mma_nt(ts, ak, q_at(it + 1), C::kIdS, one);
+          commit(s_full, one);
         }
         if (!(ok = wait(ds_full, par))) break;
-        Tl::mma_tn(tmem + C::kDk, tp, tp + 64, q_at(it), C::kIdD, it > 0);
-        umma_commit(&q_empty[it % C::kQ]);
+        Tl::template mma_tn<kCols>(tmem + C::kDk, tp, q_at(it), C::kIdD, it > 0, one);
+        commit(&q_empty[it % C::kQ], one);
         if (it + 1 < n) {
           if (!(ok = do_in(it + 1))) break;
-          Tl::mma_nt(tp, av, do_at(it + 1), C::kIdS);
-          umma_commit(dp_full);
+          Tl::mma_nt(tp, av, do_at(it + 1), C::kIdS, one);
+          commit(dp_full, one);
         }
       }
-      if (ok) umma_commit(all);
-      umma_commit(done);   // every product has completed before the tensor memory is freed
+      if (ok) commit(all, one);
+      commit(done, one);   // every product has completed before the tensor memory is freed
       mbar_wait(done, 0u, 2u, p.err);
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == kStatWarp) {
     // ---- statistics of the query tile, four queries per lane, read one tile ahead ----
     float vl[4], vd[4];
     auto read = [&](int it) {
@@ -295,12 +301,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       if (lane == 0) mbar_arrive(delta_full);
       read(it + 1);
     }
-  } else if (warp < 8) {
-    compute_regs();
-    // ---- elementwise: thread = key r, queries 64 w .. 64 w + 63 ----
+  } else if (warp < kComputeWarps) {
+    Sp::compute();
+    // ---- elementwise: thread = key r, queries kCols w .. ----
     const int w = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = lanes + C::kS + 64 * w, tp = lanes + C::kDp + 64 * w;
+    const uint32_t ts = lanes + C::kS + kCols * w, tp = lanes + C::kDp + kCols * w;
     const f2 c2 = mk2(p.c, p.c);
     bool ok = true;
     for (int it = 0; it < n; ++it) {
@@ -308,13 +314,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       const int qi = j + it % nq;
       if (!(ok = warp_wait(lse_full, par, 4u, p.err, p.limit) && warp_wait(s_full, par, 4u, p.err, p.limit))) break;
       fence_after();
-      uint32_t x[64], u[32];
+      uint32_t x[kCols], u[kCols / 2];
       tmem_ld32_nw(ts, x);
-      tmem_ld32_nw(ts + 32, x + 32);
-      tmem_wait_ld_n<64>(x);
+      tmem_wait_ld_n<kCols>(x);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float4 z = *reinterpret_cast<const float4*>(s_lse + 64 * w + 4 * k);
+      for (int k = 0; k < kCols / 4; ++k) {
+        const float4 z = *reinterpret_cast<const float4*>(s_lse + kCols * w + 4 * k);
         const float2 a = un2(fma2(mk2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])), c2, mk2(-z.x, -z.y)));
         const float2 b = un2(fma2(mk2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])), c2, mk2(-z.z, -z.w)));
         x[4 * k] = __float_as_uint(exp2_(a.x));
@@ -325,12 +330,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       const bool diagonal = qi == j;   // queries from the key's own on
       if (diagonal) {
 #pragma unroll
-        for (int k = 0; k < 64; ++k)
-          if (64 * w + k < r) x[k] = 0u;
+        for (int k = 0; k < kCols; ++k)
+          if (kCols * w + k < r) x[k] = 0u;
       }
 #pragma unroll
-      for (int k = 0; k < 32; ++k) u[k] = pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
-      tmem_st32(ts, u);
+      for (int k = 0; k < kCols / 2; ++k) u[k] = pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+      tmem_st16(ts, u);
       tmem_wait_st();
       fence_before();
       __syncwarp();
@@ -340,13 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       }
       if (!(ok = warp_wait(delta_full, par, 4u, p.err, p.limit) && warp_wait(dp_full, par, 4u, p.err, p.limit))) break;
       fence_after();
-      uint32_t y[64];
+      uint32_t y[kCols];
       tmem_ld32_nw(tp, y);
-      tmem_ld32_nw(tp + 32, y + 32);
-      tmem_wait_ld_n<64>(y);
+      tmem_wait_ld_n<kCols>(y);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float4 z = *reinterpret_cast<const float4*>(s_delta + 64 * w + 4 * k);
+      for (int k = 0; k < kCols / 4; ++k) {
+        const float4 z = *reinterpret_cast<const float4*>(s_delta + kCols * w + 4 * k);
         const float2 a = un2(mul2(mk2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])),
                                   add2(mk2(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1])), mk2(-z.x, -z.y))));
         const float2 b = un2(mul2(mk2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])),
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         u[2 * k] = pack_bf16(a.x, a.y);
         u[2 * k + 1] = pack_bf16(b.x, b.y);
       }
-      tmem_st32(tp, u);
+      tmem_st16(tp, u);
       tmem_wait_st();
       fence_before();
       __syncwarp();
@@ -367,15 +371,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       fence_after();
       const int row = j * kRows + r;
       const int64_t at = (int64_t)t.row0 + row;
-      if (w == 0)
-        store_row<D>(lanes + C::kDv, 1.f, p.dV + at * p.ld_v + (int64_t)hk * D, row < t.len);
+      const int half = w & 1, c0 = half * (D / 2);
+      if (w < 2)
+        store_row<D / 2>(lanes + C::kDv + c0, 1.f, p.dV + at * p.ld_v + (int64_t)hk * D + c0, row < t.len);
       else
-        store_row<D>(lanes + C::kDk, p.scale, p.dK + at * p.ld_k + (int64_t)hk * D, row < t.len);
+        store_row<D / 2>(lanes + C::kDk + c0, p.scale, p.dK + at * p.ld_k + (int64_t)hk * D + c0, row < t.len);
     }
     fence_before();
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kIssueWarp) {
     fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -395,7 +400,7 @@ struct DqCfg {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__ BwdK p) {
+__global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dq(const __grid_constant__ BwdK p) {
   using C = DqCfg<D>;
   using Tl = Tile<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -418,12 +423,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
   uint64_t* done = all + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   static_assert((2 * (C::kK + C::kV) + 9) * 8 + 4 <= C::kBarriers, "barriers");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   grid_dep_sync();
   const int li = blockIdx.x / p.heads, h = blockIdx.x - li * p.heads;
   if (li >= __ldg(p.count)) return;
-  const AttnTile t = p.tiles[li];
+  const AttnTile t = tile_at(p.tiles + li);
   const int qi = t.index, n = t.index + 1;   // key tiles
   const int q_col = h * D, k_col = h / p.per * D;
 
@@ -441,21 +446,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8);
+    mbar_init(ds_full, kComputeWarps);
     mbar_init(fixed, 1);
     mbar_init(all, 1);
     mbar_init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
   }
-  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  if (warp == kIssueWarp) tmem_alloc(tmem_slot, 512);
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
-  if (warp >= 8) issue_regs();
-  if (warp == 8) {
+  if (warp >= kComputeWarps) Sp::issue();
+  if (warp == kLoadWarp) {
     // ---- loads ----
     if (lane == 0) {
       mbar_expect_tx(q_full, C::kTile);
@@ -499,25 +504,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         if (!mbar_wait(&v_full[k % C::kV], (uint32_t)(k / C::kV) & 1u, 1u, p.err)) break;
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kIssueWarp) {
     // ---- products ----
-    if (lane == 0) {
+    {
+      const uint32_t one = elect_one();
       const uint32_t aq = smem_u32(sq), ado = smem_u32(sdo), ak = smem_u32(sk), av = smem_u32(sv);
       auto wait = [&](uint64_t* b, uint32_t par) {
-        const bool ok = mbar_wait_strict(b, par, 2u, p.err, p.limit);
+        const bool ok = warp_wait(b, par, 2u, p.err, p.limit);
         fence_after();
         return ok;
       };
       auto k_in = [&](int j) { return wait(&k_full[j % C::kK], (uint32_t)(j / C::kK) & 1u); };
       auto v_in = [&](int j) { return wait(&v_full[j % C::kV], (uint32_t)(j / C::kV) & 1u); };
       auto score = [&](int j) {
-        Tl::mma_nt(tmem + C::kS + 128 * (j & 1), aq, ak + (uint32_t)(j % C::kK) * C::kTile, C::kIdS);
-        umma_commit(&s_full[j & 1]);
+        Tl::mma_nt(tmem + C::kS + 128 * (j & 1), aq, ak + (uint32_t)(j % C::kK) * C::kTile, C::kIdS, one);
+        commit(&s_full[j & 1], one);
       };
       auto grad = [&](int j) {
-        Tl::mma_nt(tmem + C::kDp, ado, av + (uint32_t)(j % C::kV) * C::kTile, C::kIdS);
-        umma_commit(dp_full);
-        umma_commit(&v_empty[j % C::kV]);
+        Tl::mma_nt(tmem + C::kDp, ado, av + (uint32_t)(j % C::kV) * C::kTile, C::kIdS, one);
+        commit(dp_full, one);
+        commit(&v_empty[j % C::kV], one);
       };
       bool ok = wait(q_full, 0u) && k_in(0);
       if (ok) {
@@ -532,24 +538,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         }
         if (!(ok = wait(ds_full, (uint32_t)j & 1u))) break;
         const uint32_t td = tmem + C::kDp;
-        Tl::mma_tn(tmem + C::kDq, td, td + 64, ak + (uint32_t)(j % C::kK) * C::kTile, C::kIdD, j > 0);
-        umma_commit(&k_empty[j % C::kK]);
+        Tl::template mma_tn<kCols>(tmem + C::kDq, td, ak + (uint32_t)(j % C::kK) * C::kTile, C::kIdD, j > 0, one);
+        commit(&k_empty[j % C::kK], one);
         if (j + 1 < n) {
           if (!(ok = v_in(j + 1))) break;
           grad(j + 1);
         }
       }
-      if (ok) umma_commit(all);
-      umma_commit(done);   // every product has completed before the tensor memory is freed
+      if (ok) commit(all, one);
+      commit(done, one);   // every product has completed before the tensor memory is freed
       mbar_wait(done, 0u, 2u, p.err);
     }
     __syncwarp();
-  } else if (warp < 8) {
-    compute_regs();
-    // ---- elementwise: thread = query r, keys 64 w .. 64 w + 63 ----
+  } else if (warp < kComputeWarps) {
+    Sp::compute();
+    // ---- elementwise: thread = query r, keys kCols w .. ----
     const int w = warp >> 2, r = threadIdx.x & 127, row = qi * kRows + r;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = lanes + C::kS + 64 * w, tp = lanes + C::kDp + 64 * w;
+    const uint32_t ts = lanes + C::kS + kCols * w, tp = lanes + C::kDp + kCols * w;
     const int64_t at = (int64_t)t.row0 + row;
     const bool live = row < t.len;
     const float lse = live ? __ldg(p.lse + (int64_t)h * p.T + at) * kLog2e : 0.f;
@@ -559,12 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     for (int j = 0; j < n; ++j) {
       if (!(ok = warp_wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u, 4u, p.err, p.limit))) break;
       fence_after();
-      uint32_t x[64], y[64], u[32];
+      uint32_t x[kCols], y[kCols], u[kCols / 2];
       tmem_ld32_nw(ts + 128 * (j & 1), x);
-      tmem_ld32_nw(ts + 128 * (j & 1) + 32, x + 32);
-      tmem_wait_ld_n<64>(x);
+      tmem_wait_ld_n<kCols>(x);
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
+      for (int k = 0; k < kCols / 2; ++k) {
         const float2 a = un2(fma2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, l2));
         x[2 * k] = __float_as_uint(exp2_(a.x));
         x[2 * k + 1] = __float_as_uint(exp2_(a.y));
@@ -572,10 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
       if (!(ok = warp_wait(dp_full, (uint32_t)j & 1u, 4u, p.err, p.limit))) break;
       fence_after();
       tmem_ld32_nw(tp, y);
-      tmem_ld32_nw(tp + 32, y + 32);
-      tmem_wait_ld_n<64>(y);
+      tmem_wait_ld_n<kCols>(y);
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
+      for (int k = 0; k < kCols / 2; ++k) {
         const f2 d = mul2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])),
                           add2(mk2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), d2));
         const float2 a = un2(d);
@@ -584,12 +588,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
       }
       if (j == n - 1) {   // the tile on the diagonal: keys up to the query's own
 #pragma unroll
-        for (int k = 0; k < 64; ++k)
-          if (64 * w + k > r) x[k] = 0u;
+        for (int k = 0; k < kCols; ++k)
+          if (kCols * w + k > r) x[k] = 0u;
       }
 #pragma unroll
-      for (int k = 0; k < 32; ++k) u[k] = pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
-      tmem_st32(tp, u);
+      for (int k = 0; k < kCols / 2; ++k) u[k] = pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+      tmem_st16(tp, u);
       tmem_wait_st();
       fence_before();
       __syncwarp();
@@ -597,13 +601,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     }
     if (ok && warp_wait(all, 0u, 4u, p.err, p.limit)) {
       fence_after();
-      store_row<D / 2>(lanes + C::kDq + w * (D / 2), p.scale,
-                       p.dQ + at * p.ld_q + (int64_t)h * D + w * (D / 2), live);
+      if (w < D / 32)
+        store_row<32>(lanes + C::kDq + 32 * w, p.scale, p.dQ + at * p.ld_q + (int64_t)h * D + 32 * w, live);
     }
     fence_before();
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kIssueWarp) {
     fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -613,8 +617,8 @@ template <int D>
 cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> set{0};
   cudaError_t e = once_on_device(set, [] {
-    const cudaError_t r = set_up(k_attn_dkv<D>, DkvCfg<D>::kSmem);
-    return r != cudaSuccess ? r : set_up(k_attn_dq<D>, DqCfg<D>::kSmem);
+    const cudaError_t r = set_up<Sp>(k_attn_dkv<D>, DkvCfg<D>::kSmem);
+    return r != cudaSuccess ? r : set_up<Sp>(k_attn_dq<D>, DqCfg<D>::kSmem);
   });
   if (e != cudaSuccess) return e;
   BwdK k{};
@@ -642,11 +646,11 @@ cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   k.heads = a.kv_heads;
   prof_begin(0, st);
-  e = launch_kernel(k_attn_dkv<D>, (unsigned)(a.plan.most[0] * a.kv_heads), kThreads, DkvCfg<D>::kSmem, st, k);
+  e = launch_kernel(k_attn_dkv<D>, (unsigned)(a.plan.most[0] * a.kv_heads), Sp::kThreads, DkvCfg<D>::kSmem, st, k);
   if (e != cudaSuccess) return e;
   k.heads = a.q_heads;
   prof_begin(0, st);
-  return launch_kernel(k_attn_dq<D>, (unsigned)grid, kThreads, DqCfg<D>::kSmem, st, k);
+  return launch_kernel(k_attn_dq<D>, (unsigned)grid, Sp::kThreads, DqCfg<D>::kSmem, st, k);
 }
 
 }  // namespace

@@ -14,11 +14,17 @@ namespace attn {
 using namespace tc;
 
 constexpr int kRows = kAttnTile;
-// 384 threads: eight warps that compute, then a warpgroup that loads and issues and leaves them its registers.
-constexpr int kThreads = 384;
-constexpr int kLaunchRegs = 168, kIssueRegs = 72, kComputeRegs = 216;   // per thread
-static_assert(128 * kIssueRegs + 256 * kComputeRegs <= kThreads * kLaunchRegs,
-              "setmaxnreg draws on the block's own registers");
+// The forward pass has 384 threads: eight warps that compute, then a warpgroup that loads and issues and
+// leaves them its registers; the backward pass 640, sixteen of them.
+template <int THREADS, int LAUNCH, int ISSUE, int COMPUTE>
+struct Split {
+  static constexpr int kThreads = THREADS, kLaunch = LAUNCH, kIssue = ISSUE, kCompute = COMPUTE;   // registers per thread
+  static_assert(128 * ISSUE + (THREADS - 128) * COMPUTE <= THREADS * LAUNCH, "setmaxnreg draws on the block's own registers");
+  __device__ static void issue() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ISSUE)); }
+  __device__ static void compute() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(COMPUTE)); }
+};
+using SplitFwd = Split<384, 168, 72, 216>;
+using SplitBwd = Split<640, 96, 64, 104>;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -101,13 +107,37 @@ __device__ __forceinline__ void tmem_wait_ld_n(uint32_t* r) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i])::"memory");
 }
 
-// D += A B with A [128, 16] in tensor memory: lane = row, two bf16 of k per 32-bit column.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc));
+// ---- products. The whole warp runs the issuing loop, so that operands stay in uniform registers, and its
+// elected lane (`one` nonzero) issues: a single lane's branch moves every operand there first, and then eight
+// instructions of 64 cycles take 720 to 1040 to issue.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(one));
+  return one;
 }
+// D (+)= A B^T, both in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(one));
+}
+// with A [128, 16] in tensor memory: lane = row, two bf16 of k per 32-bit column
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc), "r"(one));
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+      "r"(one)
+      : "memory");
+}
+// A value that is the same in all lanes, known as such to the compiler.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -126,20 +156,22 @@ struct Tile {
     for (int b = 0; b < kBoxes; ++b) tma_load_2d(dst + b * kBoxBytes, map, bar, col + 64 * b, row);
   }
   // D[128, 128] = A B^T over the tiles' D columns
-  __device__ static void mma_nt(uint32_t d, uint32_t sa, uint32_t sb, uint32_t id) {
+  __device__ static void mma_nt(uint32_t d, uint32_t sa, uint32_t sb, uint32_t id, uint32_t one) {
 #pragma unroll
     for (int b = 0; b < kBoxes; ++b) {
       const uint64_t da = smem_desc_sw128(sa + b * kBoxBytes), db = smem_desc_sw128(sb + b * kBoxBytes);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) umma_f16(d, da + 2 * k, db + 2 * k, id, (b || k) ? 1u : 0u);
+      for (int k = 0; k < 4; ++k) mma_ss(d, da + 2 * k, db + 2 * k, id, (b || k) ? 1u : 0u, one);
     }
   }
-  // D[128, D] += A B over the tile's 128 rows, A in tensor memory: its columns of 64 rows each start at a0 and a1
-  __device__ static void mma_tn(uint32_t d, uint32_t a0, uint32_t a1, uint32_t sb, uint32_t id, bool acc) {
+  // D[128, D] += A B over the tile's 128 rows, A in tensor memory in runs of RUN rows' columns, which start RUN
+  // columns apart (a thread's fp32 values and over them its bf16 ones)
+  template <int RUN>
+  __device__ static void mma_tn(uint32_t d, uint32_t a, uint32_t sb, uint32_t id, bool acc, uint32_t one) {
     const uint64_t db = smem_desc_sw128_mn(sb, kBoxBytes);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      umma_f16_ts(d, (k < 4 ? a0 + 8 * k : a1 + 8 * (k - 4)), db + 128 * k, id, (acc || k) ? 1u : 0u);
+      mma_ts(d, a + 16 * k / RUN * RUN + 16 * k % RUN / 2, db + 128 * k, id, (acc || k) ? 1u : 0u, one);
   }
   // Zeros in the rows from `rows` on, by a whole warp (the swizzle moves 16-byte pieces within a row only).
   __device__ static void zero_rows(uint8_t* tile, int rows, int lane) {
@@ -151,17 +183,19 @@ struct Tile {
   }
 };
 
-__device__ __forceinline__ void issue_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs)); }
-__device__ __forceinline__ void compute_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs)); }
-
 // A kernel's attributes. A build that launches with fewer registers would wait for them forever.
-template <typename F>
+template <typename Split, typename F>
 cudaError_t set_up(F* kernel, int smem) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   cudaFuncAttributes fa;
   if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
-  if (e == cudaSuccess && fa.numRegs != kLaunchRegs) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess && fa.numRegs != Split::kLaunch) e = cudaErrorInvalidConfiguration;
   return e;
+}
+
+__device__ __forceinline__ AttnTile tile_at(const AttnTile* t) {
+  const int4 v = __ldg(reinterpret_cast<const int4*>(t));
+  return AttnTile{uniform(v.x), uniform(v.y), uniform(v.z), 0};
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t bit, uint32_t* err,
