@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
   uint64_t* empty = full + ST;
   uint64_t* q_full = empty + ST;     // [2]
   uint64_t* s_full = q_full + 2;     // [2] S of a tile is complete
-  uint64_t* p_full = s_full + 2;     // [2] P is in place, O rescaled
-  uint64_t* o_full = p_full + 2;     // [2] P V is complete
+  uint64_t* p_full = s_full + 2;     // [2][2] half of a tile's P is in place, O rescaled
+  uint64_t* o_full = p_full + 4;     // [2] P V is complete
   uint64_t* fixed = o_full + 2;      // a tile whose rows are zeroed behind a sequence has landed
   uint64_t* done = fixed + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 4);
+      mbar_init(&p_full[2 * s], 4);
+      mbar_init(&p_full[2 * s + 1], 4);
       mbar_init(&o_full[s], 1);
     }
     mbar_init(fixed, 1);
@@ -279,10 +280,11 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
         for (int s = 0; s < 2 && ok; ++s) {
           const int ns = s ? n1 : n0;
           if (j >= ns) continue;
-          ok = wait(&p_full[s], (uint32_t)j & 1u);
-          if (!ok) break;
           const uint32_t ps = tmem + C::kS + 128 * s;
-          Tl::template mma_tn<128>(tmem + C::kO + 128 * s, ps, stage_at(gv), C::kIdO, j > 0, one);
+          if (!(ok = wait(&p_full[2 * s], (uint32_t)j & 1u))) break;
+          Tl::template mma_tn<128, 0, 4>(tmem + C::kO + 128 * s, ps, stage_at(gv), C::kIdO, j > 0, one);
+          if (!(ok = wait(&p_full[2 * s + 1], (uint32_t)j & 1u))) break;
+          Tl::template mma_tn<128, 4, 8>(tmem + C::kO + 128 * s, ps, stage_at(gv), C::kIdO, true, one);
           commit(&o_full[s], one);
           if (j + 1 < ns) {
             if (!have_k) ok = stage_full(gk);
@@ -326,8 +328,12 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
 #pragma unroll
       for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(x[k]);
 #pragma unroll
-      for (int k = 4; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(x[k]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+      for (int k = 4; k < 124; k += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mx[i] = max3(mx[i], __uint_as_float(x[k + 2 * i]), __uint_as_float(x[k + 2 * i + 1]));
+      const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], __uint_as_float(x[124]), __uint_as_float(x[125])),
+                             fmaxf(__uint_as_float(x[126]), __uint_as_float(x[127]))) * p.c;
       if (j == 0) {
         m = top;
       } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
@@ -363,11 +369,13 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
           w[i] = pack_bf16(a, b);
         }
         tmem_st16(ts + 16 * k, w);
+        if (k & 1) {   // the product of half the keys begins while the other half is turned into P
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * s + (k >> 1)]);
+        }
       }
-      tmem_wait_st();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[s]);
       const float2 z = un2(add2(sum0, sum1));
       l += z.x + z.y;
     }

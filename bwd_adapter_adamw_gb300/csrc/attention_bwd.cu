@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
   uint8_t* sv = sk + C::kTile;
   uint8_t* sq = sv + C::kTile;
   uint8_t* sdo = sq + C::kQ * C::kTile;
-  float* s_lse = reinterpret_cast<float*>(sdo + C::kDo * C::kTile);   // of the query tile, times log2(e)
+  float* s_lse = reinterpret_cast<float*>(sdo + C::kDo * C::kTile);   // of the query tile: -lse log2(e), -delta
   float* s_delta = s_lse + kRows;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(s_delta + kRows);
   uint64_t* q_empty = q_full + C::kQ;
@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
         const int r = qi * kRows + lane + 32 * k;
         const bool in = it < n && r < t.len;
         const int64_t at = (int64_t)(hk * p.per + g) * p.T + t.row0 + r;
-        vl[k] = in ? __ldg(p.lse + at) * kLog2e : INFINITY;   // a query behind the sequence: P = 0
-        vd[k] = in ? __ldg(p.delta + at) : 0.f;
+        vl[k] = in ? -__ldg(p.lse + at) * kLog2e : -INFINITY;   // a query behind the sequence: P = 0
+        vd[k] = in ? -__ldg(p.delta + at) : 0.f;
       }
     };
     read(0);
@@ -303,39 +303,43 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
     }
   } else if (warp < kComputeWarps) {
     Sp::compute();
-    // ---- elementwise: thread = key r, queries kCols w .. ----
-    const int w = warp >> 2, r = threadIdx.x & 127;
+    // ---- elementwise: warpgroup w has queries 32 w .. 32 w + 31. A thread has four keys and eight queries of
+    // each warp's 32 x 32: a whole key's 32 queries would want all their statistics, 16 reads of shared memory
+    // per tile, which the products keep as busy as themselves.
+    const int w = warp >> 2, r = threadIdx.x & 127, q = lane & 3, key = (warp & 3) * 32 + (lane >> 2);
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = lanes + C::kS + kCols * w, tp = lanes + C::kDp + kCols * w;
     const f2 c2 = mk2(p.c, p.c);
+    const uint64_t* z_lse = reinterpret_cast<const uint64_t*>(s_lse + kCols * w + 2 * q);
+    const uint64_t* z_delta = reinterpret_cast<const uint64_t*>(s_delta + kCols * w + 2 * q);
     bool ok = true;
+    int qi = j;
     for (int it = 0; it < n; ++it) {
       const uint32_t par = (uint32_t)it & 1u;
-      const int qi = j + it % nq;
       if (!(ok = warp_wait(lse_full, par, 4u, p.err, p.limit) && warp_wait(s_full, par, 4u, p.err, p.limit))) break;
       fence_after();
-      uint32_t x[kCols], u[kCols / 2];
-      tmem_ld32_nw(ts, x);
+      uint32_t x[kCols], u[kCols / 2];   // x: keys +0 and +8, then +16 and +24
+      tmem_ld16x32_nw(ts, x);
+      tmem_ld16x32_nw(ts + (16u << 16), x + 16);
+      f2 z[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) z[b] = z_lse[4 * b];
       tmem_wait_ld_n<kCols>(x);
 #pragma unroll
-      for (int k = 0; k < kCols / 4; ++k) {
-        const float4 z = *reinterpret_cast<const float4*>(s_lse + kCols * w + 4 * k);
-        const float2 a = un2(fma2(mk2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])), c2, mk2(-z.x, -z.y)));
-        const float2 b = un2(fma2(mk2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])), c2, mk2(-z.z, -z.w)));
-        x[4 * k] = __float_as_uint(exp2_(a.x));
-        x[4 * k + 1] = __float_as_uint(exp2_(a.y));
-        x[4 * k + 2] = __float_as_uint(exp2_(b.x));
-        x[4 * k + 3] = __float_as_uint(exp2_(b.y));
+      for (int k = 0; k < kCols / 2; ++k) {
+        const float2 a = un2(fma2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, z[k / 2 % 4]));
+        x[2 * k] = __float_as_uint(exp2_(a.x));
+        x[2 * k + 1] = __float_as_uint(exp2_(a.y));
       }
-      const bool diagonal = qi == j;   // queries from the key's own on
-      if (diagonal) {
+      if (qi == j) {   // the tile on the diagonal: queries from the key's own on
 #pragma unroll
         for (int k = 0; k < kCols; ++k)
-          if (kCols * w + k < r) x[k] = 0u;
+          if (kCols * w + 8 * (k / 4 % 4) + 2 * q + (k & 1) < key + 8 * (k / 2 % 2) + 16 * (k / 16)) x[k] = 0u;
       }
 #pragma unroll
       for (int k = 0; k < kCols / 2; ++k) u[k] = pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
-      tmem_st16(ts, u);
+      tmem_st16x16(ts, u);
+      tmem_st16x16(ts + (16u << 16), u + 8);
       tmem_wait_st();
       fence_before();
       __syncwarp();
@@ -346,19 +350,19 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
       if (!(ok = warp_wait(delta_full, par, 4u, p.err, p.limit) && warp_wait(dp_full, par, 4u, p.err, p.limit))) break;
       fence_after();
       uint32_t y[kCols];
-      tmem_ld32_nw(tp, y);
+      tmem_ld16x32_nw(tp, y);
+      tmem_ld16x32_nw(tp + (16u << 16), y + 16);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) z[b] = z_delta[4 * b];
       tmem_wait_ld_n<kCols>(y);
 #pragma unroll
-      for (int k = 0; k < kCols / 4; ++k) {
-        const float4 z = *reinterpret_cast<const float4*>(s_delta + kCols * w + 4 * k);
-        const float2 a = un2(mul2(mk2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])),
-                                  add2(mk2(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1])), mk2(-z.x, -z.y))));
-        const float2 b = un2(mul2(mk2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])),
-                                  add2(mk2(__uint_as_float(y[4 * k + 2]), __uint_as_float(y[4 * k + 3])), mk2(-z.z, -z.w))));
-        u[2 * k] = pack_bf16(a.x, a.y);
-        u[2 * k + 1] = pack_bf16(b.x, b.y);
+      for (int k = 0; k < kCols / 2; ++k) {
+        const float2 a = un2(mul2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])),
+                                  add2(mk2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), z[k / 2 % 4])));
+        u[k] = pack_bf16(a.x, a.y);
       }
-      tmem_st16(tp, u);
+      tmem_st16x16(tp, u);
+      tmem_st16x16(tp + (16u << 16), u + 8);
       tmem_wait_st();
       fence_before();
       __syncwarp();
@@ -366,6 +370,7 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
         mbar_arrive(ds_full);
         mbar_arrive(delta_empty);
       }
+      if (++qi == nb) qi = j;
     }
     if (ok && warp_wait(all, 0u, 4u, p.err, p.limit)) {
       fence_after();

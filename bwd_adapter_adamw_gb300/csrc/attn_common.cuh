@@ -60,6 +60,11 @@ __device__ __forceinline__ float exp2_(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -95,6 +100,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "%12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// 32 columns of 16 lanes, spread over the warp: register 4 b + 2 i + j is lane (thread / 4) + 8 i, column
+// 8 b + 2 (thread % 4) + j.
+__device__ __forceinline__ void tmem_ld16x32_nw(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// 16 columns of 16 lanes: register 2 b + i is lane (thread / 4) + 8 i, column 4 b + thread % 4.
+__device__ __forceinline__ void tmem_st16x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -166,11 +189,12 @@ struct Tile {
   }
   // D[128, D] += A B over the tile's 128 rows, A in tensor memory in runs of RUN rows' columns, which start RUN
   // columns apart (a thread's fp32 values and over them its bf16 ones)
-  template <int RUN>
+  // (rows 16 K0 .. 16 K1 - 1 of them)
+  template <int RUN, int K0 = 0, int K1 = 8>
   __device__ static void mma_tn(uint32_t d, uint32_t a, uint32_t sb, uint32_t id, bool acc, uint32_t one) {
     const uint64_t db = smem_desc_sw128_mn(sb, kBoxBytes);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = K0; k < K1; ++k)
       mma_ts(d, a + 16 * k / RUN * RUN + 16 * k % RUN / 2, db + 128 * k, id, (acc || k) ? 1u : 0u, one);
   }
   // Zeros in the rows from `rows` on, by a whole warp (the swizzle moves 16-byte pieces within a row only).
