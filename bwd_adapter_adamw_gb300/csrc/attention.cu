@@ -3,7 +3,7 @@
 //   S = Q K^T (tcgen05, tiles of 128 x 128),  P = exp2(c S - m),  l = sum P,  O = (P V) / l
 //   with c = scale log2(e) and a running reference m for each row
 //
-// One CTA takes two tiles of 128 query rows that read the same keys: two heads of a group, or, where a
+// A work item is two tiles of 128 query rows that read the same keys: two heads of a group, or, where a
 // group's heads do not pair up, two neighbouring tiles of one head. The tensor cores work on one tile
 // while the softmax of the other runs: per 128 keys they take S and P V of both tiles, 4 x 512 cycles at
 // head_dim 128, and each tile's 128 threads (one row each) have the other tile's 1024 to turn S into P.
@@ -168,24 +168,14 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + ST * C::kTile);
   uint64_t* empty = full + ST;
   uint64_t* q_full = empty + ST;     // [2]
-  uint64_t* s_full = q_full + 2;     // [2] S of a tile is complete
+  uint64_t* q_empty = q_full + 2;    // [2] the last S of a tile is complete
+  uint64_t* s_full = q_empty + 2;    // [2] S of a tile is complete
   uint64_t* p_full = s_full + 2;     // [2][2] half of a tile's P is in place, O rescaled
   uint64_t* o_full = p_full + 4;     // [2] P V is complete
   uint64_t* fixed = o_full + 2;      // a tile whose rows are zeroed behind a sequence has landed
   uint64_t* done = fixed + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-
-  grid_dep_sync();
-  const int li = blockIdx.x / p.groups, gi = blockIdx.x - li * p.groups;
-  if (li >= __ldg(p.count)) return;
-  const AttnTile t = tile_at(p.tiles + li);
-  // tile s: query rows row0 + 128 qi[s] .., head h[s], keys of n[s] tiles
-  const int h0 = p.by_heads ? 2 * gi : gi, h1 = p.by_heads ? h0 + 1 : h0;
-  const int i0 = p.by_heads ? t.index : 2 * t.index, i1 = p.by_heads ? i0 : i0 + 1;
-  const int n0 = i0 + 1, n1 = (int64_t)i1 * kRows < t.len ? i1 + 1 : 0;
-  const int n = n1 > n0 ? n1 : n0;
-  const int kv_col = h0 / p.per * D;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
@@ -194,6 +184,7 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[2 * s], 4);
       mbar_init(&p_full[2 * s + 1], 4);
@@ -209,182 +200,212 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
   __syncthreads();
   fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+  grid_dep_sync();   // from here on, the earlier kernels' outputs are visible
 
   if (warp >= 8) SplitFwd::issue();
+  AttnTile t;
+  int group;
+  Items items(p.tiles, p.groups, p.count);
   if (warp == 8) {
     // ---- loads: Q of both tiles, then K and V tile by tile ----
-    if (lane == 0) {
-      mbar_expect_tx(&q_full[0], C::kTile);
-      Tl::load(sq, &p.tq, &q_full[0], h0 * D, t.row0 + i0 * kRows);
-      if (n1) {
-        mbar_expect_tx(&q_full[1], C::kTile);
-        Tl::load(sq + C::kTile, &p.tq, &q_full[1], h1 * D, t.row0 + i1 * kRows);
-      }
-    }
-    int g = 0;
-    for (; g < 2 * n; ++g) {
-      const int s = g % ST, j = g >> 1;
-      if (g >= ST && !warp_wait(&empty[s], (uint32_t)(g / ST - 1) & 1u, 1u, p.err, p.limit)) break;
-      uint8_t* dst = ring + s * C::kTile;
-      const CUtensorMap* map = (g & 1) ? &p.tv : &p.tk;
-      const int rows = t.len - j * kRows;   // of the sequence from here on
-      // The rows behind the sequence are another's or padding: P is zero there, but zero times a NaN or an
-      // infinity is not, so V's are zeroed before the product sees the tile.
-      const bool fix = (g & 1) && rows < kRows;
-      if (lane == 0) {
-        uint64_t* bar = fix ? fixed : &full[s];
-        mbar_expect_tx(bar, C::kTile);
-        Tl::load(dst, map, bar, kv_col, t.row0 + j * kRows);
-      }
-      if (fix) {   // the sequence's last tile: at most once
-        if (!__all_sync(0xffffffffu, mbar_wait(fixed, 0u, 1u, p.err))) break;
-        Tl::zero_rows(dst, rows, lane);
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
+    int g = 0, fixes = 0, nq0 = 0, nq1 = 0;   // tiles of the ring, zeroed ones, of Q
+    bool ok = true;
+    while (ok && items.take(t, group)) {
+      const Pair pr(t, group, p.by_heads);
+      const int kv_col = pr.h0 / p.per * D;
+      for (int j = 0; j < 2 * pr.most && ok; ++j, ++g) {
+        if (j < 2 && pr.n(j)) {   // Q of tile 0 ahead of the first K, of tile 1 behind it
+          const int before = j ? nq1++ : nq0++;
+          if (before && !(ok = warp_wait(&q_empty[j], (uint32_t)(before - 1) & 1u, 1u, p.err, p.limit))) {
+            (j ? nq1 : nq0) = before;
+            break;
+          }
+          if (lane == 0) {
+            mbar_expect_tx(&q_full[j], C::kTile);
+            Tl::load(sq + j * C::kTile, &p.tq, &q_full[j], pr.h(j) * D, t.row0 + pr.qi(j) * kRows);
+          }
+        }
+        const int s = g % ST, kt = j >> 1;
+        if (g >= ST && !(ok = warp_wait(&empty[s], (uint32_t)(g / ST - 1) & 1u, 1u, p.err, p.limit))) break;
+        uint8_t* dst = ring + s * C::kTile;
+        const int rows = t.len - kt * kRows;   // of the sequence from here on
+        // The rows behind the sequence are another's or padding: P is zero there, but zero times a NaN or an
+        // infinity is not, so V's are zeroed before the product sees the tile.
+        const bool fix = (j & 1) && rows < kRows;
+        if (lane == 0) {
+          uint64_t* bar = fix ? fixed : &full[s];
+          mbar_expect_tx(bar, C::kTile);
+          Tl::load(dst, (j & 1) ? &p.tv : &p.tk, bar, kv_col, t.row0 + kt * kRows);
+        }
+        if (fix) {
+          ok = __all_sync(0xffffffffu, mbar_wait(fixed, (uint32_t)fixes & 1u, 1u, p.err));
+          ++fixes;
+          if (!ok) {
+            ++g;
+            break;
+          }
+          Tl::zero_rows(dst, rows, lane);
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+        }
       }
     }
     // every copy has landed before the CTA ends
     if (lane == 0) {
-      mbar_wait(&q_full[0], 0u, 1u, p.err);
-      if (n1) mbar_wait(&q_full[1], 0u, 1u, p.err);
+      if (nq0) mbar_wait(&q_full[0], (uint32_t)(nq0 - 1) & 1u, 1u, p.err);
+      if (nq1) mbar_wait(&q_full[1], (uint32_t)(nq1 - 1) & 1u, 1u, p.err);
       for (int k = g > ST ? g - ST : 0; k < g; ++k)
         if (!mbar_wait(&full[k % ST], (uint32_t)(k / ST) & 1u, 1u, p.err)) break;
     }
     __syncwarp();
   } else if (warp == 9) {
     // ---- products ----
-    {
-      const uint32_t one = elect_one();
-      const uint32_t q0 = smem_u32(sq), rg = smem_u32(ring);
-      auto wait = [&](uint64_t* b, uint32_t par) {
-        const bool ok = warp_wait(b, par, 2u, p.err, p.limit);
-        fence_after();
-        return ok;
-      };
-      auto stage_full = [&](int g) { return wait(&full[g % ST], (uint32_t)(g / ST) & 1u); };
-      auto stage_at = [&](int g) { return rg + (uint32_t)(g % ST) * C::kTile; };
-      bool ok = stage_full(0);
-      for (int s = 0; s < 2 && ok; ++s) {
-        if (s && !n1) break;
-        ok = wait(&q_full[s], 0u);
-        if (!ok) break;
-        Tl::mma_nt(tmem + C::kS + 128 * s, q0 + s * C::kTile, stage_at(0), C::kIdS, one);
+    const uint32_t one = elect_one();
+    const uint32_t q0 = smem_u32(sq), rg = smem_u32(ring);
+    auto wait = [&](uint64_t* b, uint32_t par) {
+      const bool r = warp_wait(b, par & 1u, 2u, p.err, p.limit);
+      fence_after();
+      return r;
+    };
+    auto stage_full = [&](int g) { return wait(&full[g % ST], (uint32_t)(g / ST)); };
+    auto stage_at = [&](int g) { return rg + (uint32_t)(g % ST) * C::kTile; };
+    int g0 = 0;                          // ring tiles before this item
+    uint32_t nq[2] = {0, 0}, np[2] = {0, 0};   // of each tile: items, P's waited for
+    bool ok = true;
+    while (ok && items.take(t, group)) {
+      const Pair pr(t, group, p.by_heads);
+      auto score = [&](int s, int j) {   // S of key tile j, over the P before it
+        Tl::mma_nt(tmem + C::kS + 128 * s, q0 + s * C::kTile, stage_at(g0 + 2 * j), C::kIdS, one);
         commit(&s_full[s], one);
+        if (j + 1 == pr.n(s)) commit(&q_empty[s], one);
+      };
+      ok = stage_full(g0);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!ok || !pr.n(s)) break;
+        if (!(ok = wait(&q_full[s], nq[s]++))) break;
+        score(s, 0);
       }
-      if (ok) commit(&empty[0], one);
-      for (int j = 0; j < n && ok; ++j) {
-        const int gv = 2 * j + 1, gk = 2 * j + 2;
+      if (ok) commit(&empty[g0 % ST], one);
+      for (int j = 0; j < pr.most && ok; ++j) {
+        const int gv = g0 + 2 * j + 1, gk = gv + 1;
         ok = stage_full(gv);
         bool have_k = false;
-        for (int s = 0; s < 2 && ok; ++s) {
-          const int ns = s ? n1 : n0;
-          if (j >= ns) continue;
-          const uint32_t ps = tmem + C::kS + 128 * s;
-          if (!(ok = wait(&p_full[2 * s], (uint32_t)j & 1u))) break;
-          Tl::template mma_tn<128, 0, 4>(tmem + C::kO + 128 * s, ps, stage_at(gv), C::kIdO, j > 0, one);
-          if (!(ok = wait(&p_full[2 * s + 1], (uint32_t)j & 1u))) break;
-          Tl::template mma_tn<128, 4, 8>(tmem + C::kO + 128 * s, ps, stage_at(gv), C::kIdO, true, one);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (!ok || j >= pr.n(s)) continue;
+          const uint32_t ps = tmem + C::kS + 128 * s, os = tmem + C::kO + 128 * s;
+          if (!(ok = wait(&p_full[2 * s], np[s]))) break;
+          Tl::template mma_tn<128, 0, 4>(os, ps, stage_at(gv), C::kIdO, j > 0, one);
+          if (!(ok = wait(&p_full[2 * s + 1], np[s]))) break;
+          Tl::template mma_tn<128, 4, 8>(os, ps, stage_at(gv), C::kIdO, true, one);
           commit(&o_full[s], one);
-          if (j + 1 < ns) {
+          ++np[s];
+          if (j + 1 < pr.n(s)) {
             if (!have_k) ok = stage_full(gk);
             have_k = true;
             if (!ok) break;
-            Tl::mma_nt(ps, q0 + s * C::kTile, stage_at(gk), C::kIdS, one);
-            commit(&s_full[s], one);
+            score(s, j + 1);
           }
         }
         if (!ok) break;
         commit(&empty[gv % ST], one);
         if (have_k) commit(&empty[gk % ST], one);
       }
-      // every product has completed before the tensor memory is freed
-      commit(done, one);
-      mbar_wait(done, 0u, 2u, p.err);
+      g0 += 2 * pr.most;
     }
+    // every product has completed before the tensor memory is freed
+    commit(done, one);
+    mbar_wait(done, 0u, 2u, p.err);
     __syncwarp();
   } else if (warp < 8) {
     SplitFwd::compute();
     // ---- softmax and epilogue: thread = row of tile s ----
     const int s = warp >> 2, r = threadIdx.x & 127;
-    const int ns = s ? n1 : n0, qi = s ? i1 : i0, h = s ? h1 : h0;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = lanes + C::kS + 128 * s, to = lanes + C::kO + 128 * s;
-    float m = -INFINITY, l = 0.f;
+    uint32_t ns = 0, no = 0;   // S's waited for, P V's before this item
     bool ok = true;
-    for (int j = 0; j < ns; ++j) {
-      if (!(ok = warp_wait(&s_full[s], (uint32_t)j & 1u, 4u, p.err, p.limit))) break;
-      fence_after();
-      uint32_t x[128];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_ld32_nw(ts + 32 * k, x + 32 * k);
-      tmem_wait_ld_n<128>(x);
-      if (j == ns - 1) {   // the tile on the diagonal: keys up to the row's own
-#pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if (k > r) x[k] = 0xff800000u;
-      }
-      float mx[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(x[k]);
-#pragma unroll
-      for (int k = 4; k < 124; k += 8)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mx[i] = max3(mx[i], __uint_as_float(x[k + 2 * i]), __uint_as_float(x[k + 2 * i + 1]));
-      const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], __uint_as_float(x[124]), __uint_as_float(x[125])),
-                             fmaxf(__uint_as_float(x[126]), __uint_as_float(x[127]))) * p.c;
-      if (j == 0) {
-        m = top;
-      } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
-        const bool grow = top > m + kRescale;
-        const float f = grow ? exp2_(m - top) : 1.f;
-        if (!(ok = warp_wait(&o_full[s], (uint32_t)(j - 1) & 1u, 4u, p.err, p.limit))) break;
+    while (ok && items.take(t, group)) {
+      const Pair pr(t, group, p.by_heads);
+      const int n = pr.n(s);
+      if (!n) continue;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        if (!(ok = warp_wait(&s_full[s], ns++ & 1u, 4u, p.err, p.limit))) break;
         fence_after();
+        uint32_t x[128];
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t o[32];
-          tmem_ld32_nw(to + 32 * k, o);
-          tmem_wait_ld_n<32>(o);
+        for (int k = 0; k < 4; ++k) tmem_ld32_nw(ts + 32 * k, x + 32 * k);
+        tmem_wait_ld_n<128>(x);
+        if (j == n - 1) {   // the tile on the diagonal: keys up to the row's own
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st32(to + 32 * k, o);
+          for (int k = 0; k < 128; ++k)
+            if (k > r) x[k] = 0xff800000u;
         }
-        if (grow) m = top;
-        l *= f;
+        float mx[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(x[k]);
+#pragma unroll
+        for (int k = 4; k < 124; k += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx[i] = max3(mx[i], __uint_as_float(x[k + 2 * i]), __uint_as_float(x[k + 2 * i + 1]));
+        const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], __uint_as_float(x[124]), __uint_as_float(x[125])),
+                               fmaxf(__uint_as_float(x[126]), __uint_as_float(x[127]))) * p.c;
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
+          const bool grow = top > m + kRescale;
+          const float f = grow ? exp2_(m - top) : 1.f;
+          if (!(ok = warp_wait(&o_full[s], (no + j - 1) & 1u, 4u, p.err, p.limit))) break;
+          fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t o[32];
+            tmem_ld32_nw(to + 32 * k, o);
+            tmem_wait_ld_n<32>(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(to + 32 * k, o);
+          }
+          if (grow) m = top;
+          l *= f;
+        }
+        // (a row whose scores are all -inf so far has no reference yet: P is 0)
+        const float ref = m == -INFINITY ? 0.f : m;
+        const f2 c2 = mk2(p.c, p.c), m2 = mk2(-ref, -ref);
+        f2 sum0 = mk2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = un2(fma2(mk2(__uint_as_float(x[32 * k + 2 * i]), __uint_as_float(x[32 * k + 2 * i + 1])), c2, m2));
+            const float a = exp2_(e.x), b = exp2_(e.y);
+            if (i & 1) sum1 = add2(sum1, mk2(a, b));
+            else sum0 = add2(sum0, mk2(a, b));
+            w[i] = pack_bf16(a, b);
+          }
+          tmem_st16(ts + 16 * k, w);
+          if (k & 1) {   // the product of half the keys begins while the other half is turned into P
+            tmem_wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * s + (k >> 1)]);
+          }
+        }
+        const float2 z = un2(add2(sum0, sum1));
+        l += z.x + z.y;
       }
-      // (a row whose scores are all -inf so far has no reference yet: P is 0)
-      const float ref = m == -INFINITY ? 0.f : m;
-      const f2 c2 = mk2(p.c, p.c), m2 = mk2(-ref, -ref);
-      f2 sum0 = mk2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 e = un2(fma2(mk2(__uint_as_float(x[32 * k + 2 * i]), __uint_as_float(x[32 * k + 2 * i + 1])), c2, m2));
-          const float a = exp2_(e.x), b = exp2_(e.y);
-          if (i & 1) sum1 = add2(sum1, mk2(a, b));
-          else sum0 = add2(sum0, mk2(a, b));
-          w[i] = pack_bf16(a, b);
-        }
-        tmem_st16(ts + 16 * k, w);
-        if (k & 1) {   // the product of half the keys begins while the other half is turned into P
-          tmem_wait_st();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * s + (k >> 1)]);
-        }
-      }
-      const float2 z = un2(add2(sum0, sum1));
-      l += z.x + z.y;
-    }
-    const int row = qi * kRows + r;
-    if (ok && ns > 0 && warp_wait(&o_full[s], (uint32_t)(ns - 1) & 1u, 4u, p.err, p.limit)) {
+      no += n;
+      if (!ok || !(ok = warp_wait(&o_full[s], (no - 1) & 1u, 4u, p.err, p.limit))) break;
       fence_after();
+      const int row = pr.qi(s) * kRows + r;
       const float inv = 1.f / l;
       const int64_t at = (int64_t)t.row0 + row;
-      __nv_bfloat16* out = p.O + at * p.ld_o + (int64_t)h * D;
+      __nv_bfloat16* out = p.O + at * p.ld_o + (int64_t)pr.h(s) * D;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
         float v[32];
@@ -396,7 +417,8 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
           for (int i = 0; i < 4; ++i) store8(out + 32 * k + 8 * i, v + 8 * i);
         }
       }
-      if (row < t.len) p.lse[(int64_t)h * p.T + at] = (m + log2f(l)) * kLn2;
+      if (row < t.len) p.lse[(int64_t)pr.h(s) * p.T + at] = (m + log2f(l)) * kLn2;
+      fence_before();   // (O has been read before the next item's first P arrives)
     }
     fence_before();
   }
@@ -432,10 +454,12 @@ cudaError_t fwd_launch(const AttnArgs& a, cudaStream_t st) {
   k.err = error_word();
   if (!k.err) return cudaErrorInvalidDevice;
   k.limit = tc_wait_limit();
-  const int64_t grid = a.plan.most[w] * k.groups;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  const int64_t most = a.plan.most[w] * k.groups;
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  if (most > INT32_MAX) return cudaErrorInvalidValue;
   prof_begin(0, st);
-  return launch_kernel(k_attn_fwd<D>, (unsigned)grid, SplitFwd::kThreads, FwdCfg<D>::kSmem, st, k);
+  return launch_kernel(k_attn_fwd<D>, (unsigned)(most < sms ? most : sms), SplitFwd::kThreads, FwdCfg<D>::kSmem, st, k);
 }
 
 }  // namespace

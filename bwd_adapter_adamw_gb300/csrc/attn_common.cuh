@@ -23,7 +23,7 @@ struct Split {
   __device__ static void issue() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ISSUE)); }
   __device__ static void compute() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(COMPUTE)); }
 };
-using SplitFwd = Split<384, 168, 72, 216>;
+using SplitFwd = Split<384, 168, 56, 224>;
 using SplitBwd = Split<640, 96, 64, 104>;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -221,6 +221,46 @@ __device__ __forceinline__ AttnTile tile_at(const AttnTile* t) {
   const int4 v = __ldg(reinterpret_cast<const int4*>(t));
   return AttnTile{uniform(v.x), uniform(v.y), uniform(v.z), 0};
 }
+
+// The work of a persistent CTA: items of the plan's list (a tile and one of its `groups` groups of heads), the
+// longest first, dealt out to and fro so that every CTA's sum comes out alike. Every role of a CTA walks the
+// same items; the loading warp comes to each first, so that the others find its tile in L1.
+struct Items {
+  const AttnTile* tiles;
+  int groups, n, round;
+  __device__ Items(const AttnTile* t, int g, const int32_t* count) : tiles(t), groups(g), n(uniform(__ldg(count) * g)), round(0) {}
+  // the next item, false if there is none
+  __device__ bool take(AttnTile& t, int& group) {
+    const int b = (int)blockIdx.x, grid = (int)gridDim.x;
+    const int64_t i = (int64_t)round * grid + ((round & 1) ? grid - 1 - b : b);
+    ++round;
+    if (i >= n) return false;
+    const int li = (int)i / groups;
+    group = (int)i - li * groups;
+    const int4 v = __ldg(reinterpret_cast<const int4*>(tiles + li));
+    t = AttnTile{uniform(v.x), uniform(v.y), uniform(v.z), 0};
+    return true;
+  }
+};
+
+// Two tiles of 128 queries that read the same keys: two heads of a group, or, where a group's heads do not pair
+// up, two neighbouring tiles of one head. Tile s: head h(s), queries from qi(s) * 128, n(s) key tiles (0: there
+// is no such tile).
+struct Pair {
+  int h0, h1, q0, q1, n0, n1, most;
+  __device__ Pair(const AttnTile& t, int group, bool by_heads) {
+    h0 = by_heads ? 2 * group : group;
+    h1 = by_heads ? h0 + 1 : h0;
+    q0 = by_heads ? t.index : 2 * t.index;
+    q1 = by_heads ? q0 : q0 + 1;
+    n0 = q0 + 1;
+    n1 = (int64_t)q1 * kRows < t.len ? q1 + 1 : 0;
+    most = n1 > n0 ? n1 : n0;
+  }
+  __device__ int h(int s) const { return s ? h1 : h0; }
+  __device__ int qi(int s) const { return s ? q1 : q0; }
+  __device__ int n(int s) const { return s ? n1 : n0; }
+};
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t bit, uint32_t* err,
                                           unsigned long long limit) {
