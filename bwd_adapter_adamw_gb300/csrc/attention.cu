@@ -270,50 +270,48 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
     };
     auto stage_full = [&](int g) { return wait(&full[g % ST], (uint32_t)(g / ST)); };
     auto stage_at = [&](int g) { return rg + (uint32_t)(g % ST) * C::kTile; };
-    int g0 = 0;                          // ring tiles before this item
-    uint32_t nq[2] = {0, 0}, np[2] = {0, 0};   // of each tile: items, P's waited for
+    int g = 0;                                // ring tiles before key tile j's
+    uint32_t i0 = 0, i1 = 0, c0 = 0, c1 = 0;  // of each tile: items and key tiles so far
     bool ok = true;
     while (ok && items.take(t, group)) {
       const Pair pr(t, group, p.by_heads);
-      auto score = [&](int s, int j) {   // S of key tile j, over the P before it
-        Tl::mma_nt(tmem + C::kS + 128 * s, q0 + s * C::kTile, stage_at(g0 + 2 * j), C::kIdS, one);
+      const int tiles = pr.n1 ? 2 : 1;
+      auto score = [&](int s, int at, bool last) {   // S over the P before it
+        Tl::mma_nt(tmem + C::kS + 128 * s, q0 + s * C::kTile, stage_at(at), C::kIdS, one);
         commit(&s_full[s], one);
-        if (j + 1 == pr.n(s)) commit(&q_empty[s], one);
+        if (last) commit(&q_empty[s], one);
       };
-      ok = stage_full(g0);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (!ok || !pr.n(s)) break;
-        if (!(ok = wait(&q_full[s], nq[s]++))) break;
-        score(s, 0);
+      ok = stage_full(g);
+#pragma unroll 1
+      for (int s = 0; s < tiles && ok; ++s) {
+        if (!(ok = wait(&q_full[s], s ? i1 : i0))) break;
+        score(s, g, pr.n(s) == 1);
       }
-      if (ok) commit(&empty[g0 % ST], one);
-      for (int j = 0; j < pr.most && ok; ++j) {
-        const int gv = g0 + 2 * j + 1, gk = gv + 1;
-        ok = stage_full(gv);
+      if (ok) commit(&empty[g % ST], one);
+#pragma unroll 1
+      for (int j = 0; j < pr.most && ok; ++j, g += 2) {
+        if (!(ok = stage_full(g + 1))) break;
         bool have_k = false;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (!ok || j >= pr.n(s)) continue;
-          const uint32_t ps = tmem + C::kS + 128 * s, os = tmem + C::kO + 128 * s;
-          if (!(ok = wait(&p_full[2 * s], np[s]))) break;
-          Tl::template mma_tn<128, 0, 4>(os, ps, stage_at(gv), C::kIdO, j > 0, one);
-          if (!(ok = wait(&p_full[2 * s + 1], np[s]))) break;
-          Tl::template mma_tn<128, 4, 8>(os, ps, stage_at(gv), C::kIdO, true, one);
+#pragma unroll 1
+        for (int s = j < pr.n0 ? 0 : 1; s < tiles; ++s) {
+          const uint32_t ps = tmem + C::kS + 128 * s, os = tmem + C::kO + 128 * s, c = s ? c1 : c0;
+          if (!(ok = wait(&p_full[2 * s], c))) break;
+          Tl::template mma_tn<128, 0, 4>(os, ps, stage_at(g + 1), C::kIdO, j > 0, one);
+          if (!(ok = wait(&p_full[2 * s + 1], c))) break;
+          Tl::template mma_tn<128, 4, 8>(os, ps, stage_at(g + 1), C::kIdO, true, one);
           commit(&o_full[s], one);
-          ++np[s];
+          if (s + 1 == tiles) commit(&empty[(g + 1) % ST], one);
+          if (s) ++c1; else ++c0;
           if (j + 1 < pr.n(s)) {
-            if (!have_k) ok = stage_full(gk);
+            if (!have_k && !(ok = stage_full(g + 2))) break;
             have_k = true;
-            if (!ok) break;
-            score(s, j + 1);
+            score(s, g + 2, j + 2 == pr.n(s));
           }
         }
-        if (!ok) break;
-        commit(&empty[gv % ST], one);
-        if (have_k) commit(&empty[gk % ST], one);
+        if (ok && have_k) commit(&empty[(g + 2) % ST], one);
       }
-      g0 += 2 * pr.most;
+      ++i0;
+      if (pr.n1) ++i1;
     }
     // every product has completed before the tensor memory is freed
     commit(done, one);

@@ -21,8 +21,8 @@
 // operand of dS K. S alternates between two buffers, so that the next tile's S runs before this one's dS.
 //
 // CTA layout (640 threads): warps 0-15 elementwise (four warpgroups, 32 columns each) and epilogue, warp 16
-// loads, warp 17 issues the products, warp 18 brings the queries' statistics (k_attn_dkv). Waits are bounded
-// as in the forward pass.
+// loads, warp 17 issues the products, warp 18 brings the queries' statistics (k_attn_dkv); as in the forward
+// pass (k_attn_dq). Waits are bounded as there.
 #include "attn_common.cuh"
 
 namespace lora {
@@ -64,7 +64,9 @@ struct BwdK {
   CUtensorMap tq, tk, tv, tdo;
   const int32_t* count;
   const AttnTile* tiles;
-  int32_t heads;         // CTAs of a tile: key / value heads (dK, dV) or query heads (dQ)
+  int32_t heads;         // dK, dV: CTAs of a tile
+  int32_t groups;        // dQ: work items of a tile of the list
+  int32_t by_heads;      // dQ: two heads of a 128-row tile, or two 128-row tiles of a head
   int32_t per;
   float c, scale;
   int64_t T, ld_q, ld_k, ld_v;
@@ -226,52 +228,46 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
     __syncwarp();
   } else if (warp == kIssueWarp) {
     // ---- products ----
-    {
-      const uint32_t one = elect_one();
-      const uint32_t ak = smem_u32(sk), av = smem_u32(sv), aq = smem_u32(sq), ado = smem_u32(sdo);
-      auto wait = [&](uint64_t* b, uint32_t par) {
-        const bool ok = warp_wait(b, par, 2u, p.err, p.limit);
-        fence_after();
-        return ok;
-      };
-      auto q_in = [&](int it) { return wait(&q_full[it % C::kQ], (uint32_t)(it / C::kQ) & 1u); };
-      auto do_in = [&](int it) { return wait(&do_full[it % C::kDo], (uint32_t)(it / C::kDo) & 1u); };
-      auto q_at = [&](int it) { return aq + (uint32_t)(it % C::kQ) * C::kTile; };
-      auto do_at = [&](int it) { return ado + (uint32_t)(it % C::kDo) * C::kTile; };
-      const uint32_t ts = tmem + C::kS, tp = tmem + C::kDp;
-      bool ok = wait(k_full, 0u) && q_in(0);
-      if (ok) {
-        Tl::mma_nt(ts, ak, q_at(0), C::kIdS, one);
-        commit(s_full, one);
-        ok = wait(v_full, 0u) && do_in(0);
+    const uint32_t one = elect_one();
+    const uint32_t ak = smem_u32(sk), av = smem_u32(sv), aq = smem_u32(sq), ado = smem_u32(sdo);
+    auto wait = [&](uint64_t* b, uint32_t par) {
+      const bool r = warp_wait(b, par & 1u, 2u, p.err, p.limit);
+      fence_after();
+      return r;
+    };
+    auto q_in = [&](int it) { return wait(&q_full[it % C::kQ], (uint32_t)(it / C::kQ)); };
+    auto do_in = [&](int it) { return wait(&do_full[it % C::kDo], (uint32_t)(it / C::kDo)); };
+    auto q_at = [&](int it) { return aq + (uint32_t)(it % C::kQ) * C::kTile; };
+    auto do_at = [&](int it) { return ado + (uint32_t)(it % C::kDo) * C::kTile; };
+    const uint32_t ts = tmem + C::kS, tp = tmem + C::kDp;
+    bool ok = wait(k_full, 0u) && wait(v_full, 0u);
+    // S and dP of tile it over the P and dS of the one before, whose products come first
+#pragma unroll 1
+    for (int it = 0; it <= n && ok; ++it) {
+      if (it > 0) {
+        if (!(ok = wait(p_full, (uint32_t)(it - 1)))) break;
+        Tl::template mma_tn<kCols>(tmem + C::kDv, ts, do_at(it - 1), C::kIdD, it > 1, one);
+        commit(&do_empty[(it - 1) % C::kDo], one);
       }
-      if (ok) {
-        Tl::mma_nt(tp, av, do_at(0), C::kIdS, one);
+      if (it < n) {
+        if (!(ok = q_in(it))) break;
+        Tl::mma_nt(ts, ak, q_at(it), C::kIdS, one);
+        commit(s_full, one);
+      }
+      if (it > 0) {
+        if (!(ok = wait(ds_full, (uint32_t)(it - 1)))) break;
+        Tl::template mma_tn<kCols>(tmem + C::kDk, tp, q_at(it - 1), C::kIdD, it > 1, one);
+        commit(&q_empty[(it - 1) % C::kQ], one);
+      }
+      if (it < n) {
+        if (!(ok = do_in(it))) break;
+        Tl::mma_nt(tp, av, do_at(it), C::kIdS, one);
         commit(dp_full, one);
       }
-      for (int it = 0; it < n && ok; ++it) {
-        const uint32_t par = (uint32_t)it & 1u;
-        if (!(ok = wait(p_full, par))) break;
-        Tl::template mma_tn<kCols>(tmem + C::kDv, ts, do_at(it), C::kIdD, it > 0, one);
-        commit(&do_empty[it % C::kDo], one);
-        if (it + 1 < n) {
-          if (!(ok = q_in(it + 1))) break;
-          Tl::mma_nt(ts, ak, q_at(it + 1), C::kIdS, one);
-          commit(s_full, one);
-        }
-        if (!(ok = wait(ds_full, par))) break;
-        Tl::template mma_tn<kCols>(tmem + C::kDk, tp, q_at(it), C::kIdD, it > 0, one);
-        commit(&q_empty[it % C::kQ], one);
-        if (it + 1 < n) {
-          if (!(ok = do_in(it + 1))) break;
-          Tl::mma_nt(tp, av, do_at(it + 1), C::kIdS, one);
-          commit(dp_full, one);
-        }
-      }
-      if (ok) commit(all, one);
-      commit(done, one);   // every product has completed before the tensor memory is freed
-      mbar_wait(done, 0u, 2u, p.err);
     }
+    if (ok) commit(all, one);
+    commit(done, one);   // every product has completed before the tensor memory is freed
+    mbar_wait(done, 0u, 2u, p.err);
     __syncwarp();
   } else if (warp == kStatWarp) {
     // ---- statistics of the query tile, four queries per lane, read one tile ahead ----
@@ -395,47 +391,44 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
 template <int D>
 struct DqCfg {
   static constexpr int kTile = Tile<D>::kBytes;
-  static constexpr int kK = 3, kV = 2;   // tiles of K and V in flight or in use: V's are free earlier
+  static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 1 : 3;   // tiles of K and V in flight or in use
   static constexpr int kBarriers = 512;
-  static constexpr int kSmem = (2 + kK + kV) * kTile + kBarriers + 1024 /*alignment*/;
+  static constexpr int kSmem = (4 + kK + kV) * kTile + kBarriers + 1024 /*alignment*/;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t kIdS = idesc(kFmtBF16, 128, 128);
   static constexpr uint32_t kIdD = idesc(kFmtBF16, 128, D, false, true);
-  static constexpr uint32_t kS = 0, kDp = 256, kDq = 384;   // tensor memory; S has two buffers
+  static constexpr uint32_t kX = 0, kDq = 256;   // tensor memory: S, then dP, then dS of both tiles; dQ of both
 };
 
 template <int D>
-__global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dq(const __grid_constant__ BwdK p) {
+__global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_constant__ BwdK p) {
   using C = DqCfg<D>;
   using Tl = Tile<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sq = base;
-  uint8_t* sdo = sq + C::kTile;
-  uint8_t* sk = sdo + C::kTile;
+  uint8_t* sdo = sq + 2 * C::kTile;
+  uint8_t* sk = sdo + 2 * C::kTile;
   uint8_t* sv = sk + C::kK * C::kTile;
   uint64_t* k_full = reinterpret_cast<uint64_t*>(sv + C::kV * C::kTile);
   uint64_t* k_empty = k_full + C::kK;
   uint64_t* v_full = k_empty + C::kK;
   uint64_t* v_empty = v_full + C::kV;
-  uint64_t* q_full = v_empty + C::kV;
-  uint64_t* do_full = q_full + 1;
-  uint64_t* s_full = do_full + 1;    // [2]
-  uint64_t* dp_full = s_full + 2;
-  uint64_t* ds_full = dp_full + 1;   // dS is in place, S and dP have been read
-  uint64_t* fixed = ds_full + 1;
-  uint64_t* all = fixed + 1;
-  uint64_t* done = all + 1;
+  uint64_t* q_full = v_empty + C::kV;   // [2]
+  uint64_t* q_empty = q_full + 2;       // [2] the last S of a tile is complete
+  uint64_t* do_full = q_empty + 2;      // [2]
+  uint64_t* do_empty = do_full + 2;     // [2] the last dP of a tile is complete
+  uint64_t* s_full = do_empty + 2;      // [2]
+  uint64_t* s_read = s_full + 2;        // [2] S is in registers
+  uint64_t* dp_full = s_read + 2;       // [2]
+  uint64_t* ds_full = dp_full + 2;      // [2][2] half of a tile's dS is in place
+  uint64_t* dq_full = ds_full + 4;      // [2]
+  uint64_t* fixed = dq_full + 2;
+  uint64_t* done = fixed + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  static_assert((2 * (C::kK + C::kV) + 9) * 8 + 4 <= C::kBarriers, "barriers");
+  float* s_c = reinterpret_cast<float*>(tmem_slot + 1);
+  static_assert((2 * (C::kK + C::kV) + 22) * 8 + 8 <= C::kBarriers, "barriers");
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-
-  grid_dep_sync();
-  const int li = blockIdx.x / p.heads, h = blockIdx.x - li * p.heads;
-  if (li >= __ldg(p.count)) return;
-  const AttnTile t = tile_at(p.tiles + li);
-  const int qi = t.index, n = t.index + 1;   // key tiles
-  const int q_col = h * D, k_col = h / p.per * D;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kK; ++s) {
@@ -446,173 +439,245 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dq(const __grid_consta
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
-    mbar_init(q_full, 1);
-    mbar_init(do_full, 1);
-    mbar_init(&s_full[0], 1);
-    mbar_init(&s_full[1], 1);
-    mbar_init(dp_full, 1);
-    mbar_init(ds_full, kComputeWarps);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+      mbar_init(&do_full[s], 1);
+      mbar_init(&do_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_read[s], 4);
+      mbar_init(&dp_full[s], 1);
+      mbar_init(&ds_full[2 * s], 4);
+      mbar_init(&ds_full[2 * s + 1], 4);
+      mbar_init(&dq_full[s], 1);
+    }
     mbar_init(fixed, 1);
-    mbar_init(all, 1);
     mbar_init(done, 1);
+    *s_c = p.c;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
   }
-  if (warp == kIssueWarp) tmem_alloc(tmem_slot, 512);
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+  grid_dep_sync();   // from here on, the earlier kernels' outputs are visible
 
-  if (warp >= kComputeWarps) Sp::issue();
-  if (warp == kLoadWarp) {
-    // ---- loads ----
-    if (lane == 0) {
-      mbar_expect_tx(q_full, C::kTile);
-      Tl::load(sq, &p.tq, q_full, q_col, t.row0 + qi * kRows);
-      mbar_expect_tx(do_full, C::kTile);
-      Tl::load(sdo, &p.tdo, do_full, q_col, t.row0 + qi * kRows);
-    }
-    int jk = 0, jv = 0;   // tiles of K and V asked for
-    for (int j = 0; j < n; ++j) {
-      const int a = j % C::kK, b = j % C::kV, rows = t.len - j * kRows;
-      if (j >= C::kK && !warp_wait(&k_empty[a], (uint32_t)(j / C::kK - 1) & 1u, 1u, p.err, p.limit)) break;
-      // K's rows behind the sequence are zeroed: dS is zero there, but zero times a NaN is not
-      const bool fix = rows < kRows;
-      uint8_t* dst = sk + a * C::kTile;
+  if (warp >= 8) SplitFwd::issue();
+  AttnTile t;
+  int group;
+  Items items(p.tiles, p.groups, p.count);
+  if (warp == 8) {
+    // ---- loads, in the order in which the products free their places ----
+    int gk = 0, gv = 0, fixes = 0, nq0 = 0, nq1 = 0, nd0 = 0, nd1 = 0;   // tiles asked for
+    bool ok = true;
+    auto own = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* empty, int& n, int col, int row) {
+      if (n && !warp_wait(empty, (uint32_t)(n - 1) & 1u, 1u, p.err, p.limit)) return false;
+      ++n;
       if (lane == 0) {
-        uint64_t* bar = fix ? fixed : &k_full[a];
-        mbar_expect_tx(bar, C::kTile);
-        Tl::load(dst, &p.tk, bar, k_col, t.row0 + j * kRows);
+        mbar_expect_tx(full, C::kTile);
+        Tl::load(dst, map, full, col, row);
       }
-      ++jk;
-      if (fix) {   // the sequence's last tile: at most once
-        if (!__all_sync(0xffffffffu, mbar_wait(fixed, 0u, 1u, p.err))) break;
-        Tl::zero_rows(dst, rows, lane);
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&k_full[a]);
+      return true;
+    };
+    while (ok && items.take(t, group)) {
+      const Pair pr(t, group, p.by_heads);
+      const int col = pr.h0 / p.per * D;
+      ok = own(sq, &p.tq, &q_full[0], &q_empty[0], nq0, pr.h0 * D, t.row0 + pr.q0 * kRows);
+      for (int j = 0; j < pr.most && ok; ++j) {
+        const int a = gk % C::kK, b = gv % C::kV, rows = t.len - j * kRows;
+        if (gk >= C::kK && !(ok = warp_wait(&k_empty[a], (uint32_t)(gk / C::kK - 1) & 1u, 1u, p.err, p.limit))) break;
+        // K's rows behind the sequence are zeroed: dS is zero there, but zero times a NaN is not
+        const bool fix = rows < kRows;
+        uint8_t* dst = sk + a * C::kTile;
+        if (lane == 0) {
+          uint64_t* bar = fix ? fixed : &k_full[a];
+          mbar_expect_tx(bar, C::kTile);
+          Tl::load(dst, &p.tk, bar, col, t.row0 + j * kRows);
+        }
+        ++gk;
+        if (fix) {
+          ok = __all_sync(0xffffffffu, mbar_wait(fixed, (uint32_t)fixes & 1u, 1u, p.err));
+          ++fixes;
+          if (!ok) break;
+          Tl::zero_rows(dst, rows, lane);
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&k_full[a]);
+        }
+        if (j == 0) {
+          if (pr.n1 && !(ok = own(sq + C::kTile, &p.tq, &q_full[1], &q_empty[1], nq1, pr.h1 * D, t.row0 + pr.q1 * kRows))) break;
+          if (!(ok = own(sdo, &p.tdo, &do_full[0], &do_empty[0], nd0, pr.h0 * D, t.row0 + pr.q0 * kRows))) break;
+        }
+        if (gv >= C::kV && !(ok = warp_wait(&v_empty[b], (uint32_t)(gv / C::kV - 1) & 1u, 1u, p.err, p.limit))) break;
+        if (lane == 0) {
+          mbar_expect_tx(&v_full[b], C::kTile);
+          Tl::load(sv + b * C::kTile, &p.tv, &v_full[b], col, t.row0 + j * kRows);
+        }
+        ++gv;
+        if (j == 0 && pr.n1)
+          ok = own(sdo + C::kTile, &p.tdo, &do_full[1], &do_empty[1], nd1, pr.h1 * D, t.row0 + pr.q1 * kRows);
       }
-      if (j >= C::kV && !warp_wait(&v_empty[b], (uint32_t)(j / C::kV - 1) & 1u, 1u, p.err, p.limit)) break;
-      if (lane == 0) {
-        mbar_expect_tx(&v_full[b], C::kTile);
-        Tl::load(sv + b * C::kTile, &p.tv, &v_full[b], k_col, t.row0 + j * kRows);
-      }
-      ++jv;
     }
     if (lane == 0) {   // every copy has landed before the CTA ends
-      mbar_wait(q_full, 0u, 1u, p.err);
-      mbar_wait(do_full, 0u, 1u, p.err);
-      for (int k = jk > C::kK ? jk - C::kK : 0; k < jk; ++k)
+      if (nq0) mbar_wait(&q_full[0], (uint32_t)(nq0 - 1) & 1u, 1u, p.err);
+      if (nq1) mbar_wait(&q_full[1], (uint32_t)(nq1 - 1) & 1u, 1u, p.err);
+      if (nd0) mbar_wait(&do_full[0], (uint32_t)(nd0 - 1) & 1u, 1u, p.err);
+      if (nd1) mbar_wait(&do_full[1], (uint32_t)(nd1 - 1) & 1u, 1u, p.err);
+      for (int k = gk > C::kK ? gk - C::kK : 0; k < gk; ++k)
         if (!mbar_wait(&k_full[k % C::kK], (uint32_t)(k / C::kK) & 1u, 1u, p.err)) break;
-      for (int k = jv > C::kV ? jv - C::kV : 0; k < jv; ++k)
+      for (int k = gv > C::kV ? gv - C::kV : 0; k < gv; ++k)
         if (!mbar_wait(&v_full[k % C::kV], (uint32_t)(k / C::kV) & 1u, 1u, p.err)) break;
     }
     __syncwarp();
-  } else if (warp == kIssueWarp) {
+  } else if (warp == 9) {
     // ---- products ----
-    {
-      const uint32_t one = elect_one();
-      const uint32_t aq = smem_u32(sq), ado = smem_u32(sdo), ak = smem_u32(sk), av = smem_u32(sv);
-      auto wait = [&](uint64_t* b, uint32_t par) {
-        const bool ok = warp_wait(b, par, 2u, p.err, p.limit);
-        fence_after();
-        return ok;
-      };
-      auto k_in = [&](int j) { return wait(&k_full[j % C::kK], (uint32_t)(j / C::kK) & 1u); };
-      auto v_in = [&](int j) { return wait(&v_full[j % C::kV], (uint32_t)(j / C::kV) & 1u); };
-      auto score = [&](int j) {
-        Tl::mma_nt(tmem + C::kS + 128 * (j & 1), aq, ak + (uint32_t)(j % C::kK) * C::kTile, C::kIdS, one);
-        commit(&s_full[j & 1], one);
-      };
-      auto grad = [&](int j) {
-        Tl::mma_nt(tmem + C::kDp, ado, av + (uint32_t)(j % C::kV) * C::kTile, C::kIdS, one);
-        commit(dp_full, one);
-        commit(&v_empty[j % C::kV], one);
-      };
-      bool ok = wait(q_full, 0u) && k_in(0);
-      if (ok) {
-        score(0);
-        ok = wait(do_full, 0u) && v_in(0);
-      }
-      if (ok) grad(0);
-      for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n) {   // (its buffer of S was read before dS of tile j - 1 was in place)
-          if (!(ok = k_in(j + 1))) break;
-          score(j + 1);
-        }
-        if (!(ok = wait(ds_full, (uint32_t)j & 1u))) break;
-        const uint32_t td = tmem + C::kDp;
-        Tl::template mma_tn<kCols>(tmem + C::kDq, td, ak + (uint32_t)(j % C::kK) * C::kTile, C::kIdD, j > 0, one);
-        commit(&k_empty[j % C::kK], one);
-        if (j + 1 < n) {
-          if (!(ok = v_in(j + 1))) break;
-          grad(j + 1);
-        }
-      }
-      if (ok) commit(all, one);
-      commit(done, one);   // every product has completed before the tensor memory is freed
-      mbar_wait(done, 0u, 2u, p.err);
-    }
-    __syncwarp();
-  } else if (warp < kComputeWarps) {
-    Sp::compute();
-    // ---- elementwise: thread = query r, keys kCols w .. ----
-    const int w = warp >> 2, r = threadIdx.x & 127, row = qi * kRows + r;
-    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = lanes + C::kS + kCols * w, tp = lanes + C::kDp + kCols * w;
-    const int64_t at = (int64_t)t.row0 + row;
-    const bool live = row < t.len;
-    const float lse = live ? __ldg(p.lse + (int64_t)h * p.T + at) * kLog2e : 0.f;
-    const float delta = live ? __ldg(p.delta + (int64_t)h * p.T + at) : 0.f;
-    const f2 c2 = mk2(p.c, p.c), l2 = mk2(-lse, -lse), d2 = mk2(-delta, -delta);
+    const uint32_t one = elect_one();
+    const uint32_t aq = smem_u32(sq), ado = smem_u32(sdo), ak = smem_u32(sk), av = smem_u32(sv);
+    auto wait = [&](uint64_t* b, uint32_t n) {
+      const bool r = warp_wait(b, n & 1u, 2u, p.err, p.limit);
+      fence_after();
+      return r;
+    };
+    auto k_in = [&](int g) { return wait(&k_full[g % C::kK], (uint32_t)(g / C::kK)); };
+    auto v_in = [&](int g) { return wait(&v_full[g % C::kV], (uint32_t)(g / C::kV)); };
+    int g = 0;                                // key tiles so far
+    uint32_t i0 = 0, i1 = 0, c0 = 0, c1 = 0;  // of each tile: items and key tiles so far
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      if (!(ok = warp_wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u, 4u, p.err, p.limit))) break;
-      fence_after();
-      uint32_t x[kCols], y[kCols], u[kCols / 2];
-      tmem_ld32_nw(ts + 128 * (j & 1), x);
-      tmem_wait_ld_n<kCols>(x);
-#pragma unroll
-      for (int k = 0; k < kCols / 2; ++k) {
-        const float2 a = un2(fma2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, l2));
-        x[2 * k] = __float_as_uint(exp2_(a.x));
-        x[2 * k + 1] = __float_as_uint(exp2_(a.y));
+    while (ok && items.take(t, group)) {
+      const Pair pr(t, group, p.by_heads);
+      const int tiles = pr.n1 ? 2 : 1;
+      auto score = [&](int s, int at, bool last) {   // S over the dS before it
+        Tl::mma_nt(tmem + C::kX + 128 * s, aq + s * C::kTile, ak + (uint32_t)(at % C::kK) * C::kTile, C::kIdS, one);
+        commit(&s_full[s], one);
+        if (last) commit(&q_empty[s], one);
+      };
+      ok = k_in(g);
+#pragma unroll 1
+      for (int s = 0; s < tiles && ok; ++s) {
+        if (!(ok = wait(&q_full[s], s ? i1 : i0))) break;
+        score(s, g, pr.n(s) == 1);
       }
-      if (!(ok = warp_wait(dp_full, (uint32_t)j & 1u, 4u, p.err, p.limit))) break;
-      fence_after();
-      tmem_ld32_nw(tp, y);
-      tmem_wait_ld_n<kCols>(y);
-#pragma unroll
-      for (int k = 0; k < kCols / 2; ++k) {
-        const f2 d = mul2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])),
-                          add2(mk2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), d2));
-        const float2 a = un2(d);
-        x[2 * k] = __float_as_uint(a.x);
-        x[2 * k + 1] = __float_as_uint(a.y);
+#pragma unroll 1
+      for (int j = 0; j < pr.most && ok; ++j, ++g) {
+        if (!(ok = v_in(g))) break;
+#pragma unroll 1
+        for (int s = j < pr.n0 ? 0 : 1; s < tiles; ++s) {
+          if (j == 0 && !(ok = wait(&do_full[s], s ? i1 : i0))) break;
+          if (!(ok = wait(&s_read[s], s ? c1 : c0))) break;
+          Tl::mma_nt(tmem + C::kX + 128 * s, ado + s * C::kTile, av + (uint32_t)(g % C::kV) * C::kTile, C::kIdS, one);
+          commit(&dp_full[s], one);
+          if (j + 1 == pr.n(s)) commit(&do_empty[s], one);
+        }
+        if (!ok) break;
+        commit(&v_empty[g % C::kV], one);
+        const uint32_t kt = ak + (uint32_t)(g % C::kK) * C::kTile;
+        bool have_k = false;
+#pragma unroll 1
+        for (int s = j < pr.n0 ? 0 : 1; s < tiles; ++s) {
+          const uint32_t td = tmem + C::kX + 128 * s, tq = tmem + C::kDq + 128 * s, c = s ? c1 : c0;
+          if (!(ok = wait(&ds_full[2 * s], c))) break;
+          Tl::template mma_tn<128, 0, 4>(tq, td, kt, C::kIdD, j > 0, one);
+          if (!(ok = wait(&ds_full[2 * s + 1], c))) break;
+          Tl::template mma_tn<128, 4, 8>(tq, td, kt, C::kIdD, true, one);
+          if (s + 1 == tiles) commit(&k_empty[g % C::kK], one);
+          if (s) ++c1; else ++c0;
+          if (j + 1 < pr.n(s)) {
+            if (!have_k && !(ok = k_in(g + 1))) break;
+            have_k = true;
+            score(s, g + 1, j + 2 == pr.n(s));
+          } else {
+            commit(&dq_full[s], one);
+          }
+        }
       }
-      if (j == n - 1) {   // the tile on the diagonal: keys up to the query's own
-#pragma unroll
-        for (int k = 0; k < kCols; ++k)
-          if (kCols * w + k > r) x[k] = 0u;
-      }
-#pragma unroll
-      for (int k = 0; k < kCols / 2; ++k) u[k] = pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
-      tmem_st16(tp, u);
-      tmem_wait_st();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      ++i0;
+      if (pr.n1) ++i1;
     }
-    if (ok && warp_wait(all, 0u, 4u, p.err, p.limit)) {
+    commit(done, one);   // every product has completed before the tensor memory is freed
+    mbar_wait(done, 0u, 2u, p.err);
+    __syncwarp();
+  } else if (warp < 8) {
+    SplitFwd::compute();
+    // ---- elementwise and epilogue: thread = query r of tile s ----
+    const int s = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tx = lanes + C::kX + 128 * s, tq = lanes + C::kDq + 128 * s;
+    uint32_t c = 0, i = 0;   // key tiles and items so far
+    bool ok = true;
+    while (ok && items.take(t, group)) {
+      const Pair pr(t, group, p.by_heads);
+      const int n = pr.n(s);
+      if (!n) continue;
+      const int row = pr.qi(s) * kRows + r, h = pr.h(s);
+      const int64_t at = (int64_t)t.row0 + row;
+      const bool live = row < t.len;
+      const float lse = live ? __ldg(p.lse + (int64_t)h * p.T + at) * kLog2e : 0.f;
+      const float delta = live ? __ldg(p.delta + (int64_t)h * p.T + at) : 0.f;
+      for (int j = 0; j < n; ++j, ++c) {
+        if (!(ok = warp_wait(&s_full[s], c & 1u, 4u, p.err, p.limit))) break;
+        fence_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld32_nw(tx + 32 * k, x + 32 * k);
+        tmem_wait_ld_n<128>(x);
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_read[s]);   // dP may go over it, while P is computed
+        const float c1 = read_here(s_c);
+        const f2 c2 = mk2(c1, c1), l2 = mk2(-lse, -lse), d2 = mk2(-delta, -delta);
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          const float2 a = un2(fma2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, l2));
+          x[2 * k] = __float_as_uint(exp2_(a.x));
+          x[2 * k + 1] = __float_as_uint(exp2_(a.y));
+        }
+        if (!(ok = warp_wait(&dp_full[s], c & 1u, 4u, p.err, p.limit))) break;
+        fence_after();
+        uint32_t y[2][32];   // dP, 32 columns worked on and 32 on their way
+        tmem_ld32_nw(tx, y[0]);
+        tmem_ld32_nw(tx + 32, y[1]);
+        tmem_wait_ld_n<32>(y[0]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t* yk = y[k & 1];
+          uint32_t u[16];
+          if (k) tmem_wait_ld_n<32>(yk);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int at2 = 32 * k + 2 * e;
+            const float2 a = un2(mul2(mk2(__uint_as_float(x[at2]), __uint_as_float(x[at2 + 1])),
+                                      add2(mk2(__uint_as_float(yk[2 * e]), __uint_as_float(yk[2 * e + 1])), d2)));
+            u[e] = pack_bf16(a.x, a.y);
+          }
+          if (j == n - 1) {   // the tile on the diagonal: keys up to the query's own
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int at2 = 32 * k + 2 * e;
+              if (at2 > r) u[e] = 0u;
+              else if (at2 + 1 > r) u[e] &= 0xffffu;
+            }
+          }
+          tmem_st16(tx + 16 * k, u);
+          if (k & 1) {   // the product of half the keys begins while the other half is turned into dS
+            tmem_wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ds_full[2 * s + (k >> 1)]);
+          }
+          if (k < 2) tmem_ld32_nw(tx + 32 * (k + 2), yk);
+        }
+      }
+      if (!ok || !(ok = warp_wait(&dq_full[s], i++ & 1u, 4u, p.err, p.limit))) break;
       fence_after();
-      if (w < D / 32)
-        store_row<32>(lanes + C::kDq + 32 * w, p.scale, p.dQ + at * p.ld_q + (int64_t)h * D + 32 * w, live);
+      store_row<D>(tq, p.scale, p.dQ + at * p.ld_q + (int64_t)h * D, live);
+      fence_before();   // (dQ has been read before the next item's first dS arrives)
     }
     fence_before();
   }
   __syncthreads();
-  if (warp == kIssueWarp) {
+  if (warp == 9) {
     fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -623,15 +688,13 @@ cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> set{0};
   cudaError_t e = once_on_device(set, [] {
     const cudaError_t r = set_up<Sp>(k_attn_dkv<D>, DkvCfg<D>::kSmem);
-    return r != cudaSuccess ? r : set_up<Sp>(k_attn_dq<D>, DqCfg<D>::kSmem);
+    return r != cudaSuccess ? r : set_up<SplitFwd>(k_attn_dq<D>, DqCfg<D>::kSmem);
   });
   if (e != cudaSuccess) return e;
   BwdK k{};
   if (!attn_map(&k.tq, a.Q, a.q_heads * D, a.T, a.ld_q) || !attn_map(&k.tk, a.K, a.kv_heads * D, a.T, a.ld_k) ||
       !attn_map(&k.tv, a.V, a.kv_heads * D, a.T, a.ld_v) || !attn_map(&k.tdo, a.dO, a.q_heads * D, a.T, a.ld_o))
     return cudaErrorInvalidValue;
-  k.count = a.plan.count;
-  k.tiles = a.plan.tiles[0];
   k.per = a.q_heads / a.kv_heads;
   k.c = a.scale * kLog2e;
   k.scale = a.scale;
@@ -643,19 +706,28 @@ cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t st) {
   k.err = error_word();
   if (!k.err) return cudaErrorInvalidDevice;
   k.limit = tc_wait_limit();
-  const int64_t pre = (a.T * a.q_heads * (D / 8) + 255) / 256, grid = a.plan.most[0] * a.q_heads;
-  if (grid > INT32_MAX || pre > INT32_MAX) return cudaErrorInvalidValue;
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  k.by_heads = k.per % 2 == 0;
+  const int w = k.by_heads ? 0 : 1;
+  k.groups = k.by_heads ? a.q_heads / 2 : a.q_heads;
+  const int64_t pre = (a.T * a.q_heads * (D / 8) + 255) / 256, most = a.plan.most[w] * k.groups;
+  const int64_t grid = a.plan.most[0] * a.kv_heads;
+  if (pre > INT32_MAX || most > INT32_MAX || grid > INT32_MAX) return cudaErrorInvalidValue;
   prof_begin(0, st);
   e = launch_kernel(k_attn_delta<D>, (unsigned)pre, 256, 0, st, static_cast<const __nv_bfloat16*>(a.O),
                     static_cast<const __nv_bfloat16*>(a.dO), a.ld_o, (int)a.q_heads, a.T, a.delta);
   if (e != cudaSuccess) return e;
+  k.count = a.plan.count;
+  k.tiles = a.plan.tiles[0];
   k.heads = a.kv_heads;
   prof_begin(0, st);
-  e = launch_kernel(k_attn_dkv<D>, (unsigned)(a.plan.most[0] * a.kv_heads), Sp::kThreads, DkvCfg<D>::kSmem, st, k);
+  e = launch_kernel(k_attn_dkv<D>, (unsigned)grid, Sp::kThreads, DkvCfg<D>::kSmem, st, k);
   if (e != cudaSuccess) return e;
-  k.heads = a.q_heads;
+  k.count = a.plan.count + w;
+  k.tiles = a.plan.tiles[w];
   prof_begin(0, st);
-  return launch_kernel(k_attn_dq<D>, (unsigned)grid, Sp::kThreads, DqCfg<D>::kSmem, st, k);
+  return launch_kernel(k_attn_dq<D>, (unsigned)(most < sms ? most : sms), SplitFwd::kThreads, DqCfg<D>::kSmem, st, k);
 }
 
 }  // namespace

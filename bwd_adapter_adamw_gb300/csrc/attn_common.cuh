@@ -70,6 +70,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A value of shared memory, read where this stands: what is computed from it is not moved ahead of the
+// arrivals before it.
+__device__ __forceinline__ float read_here(const float* p) {
+  float v;
+  asm volatile("ld.volatile.shared.f32 %0, [%1];" : "=f"(v) : "r"(smem_u32(p)) : "memory");
+  return v;
+}
+
 // ---- tensor memory, 32 columns of this thread's lane ----
 __device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t* r) {   // valid after ld_wait and hold
   asm volatile(
@@ -262,9 +270,20 @@ struct Pair {
   __device__ int n(int s) const { return s ? n1 : n0; }
 };
 
+// Bounded wait of a whole warp: the same answer in every lane. Under a bound below the default (a test's) an
+// attempt that succeeds too late counts as failed. Short, since the issuing warp's loop runs through it several
+// times for each tile.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t bit, uint32_t* err,
                                           unsigned long long limit) {
-  return __all_sync(0xffffffffu, mbar_wait_strict(bar, parity, bit, err, limit));
+  if (limit >= kWaitCycles && __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = clock64();
+  do {
+    if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
+      atomicOr(err, bit);
+      return false;
+    }
+  } while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)));
+  return true;
 }
 
 }  // namespace attn
