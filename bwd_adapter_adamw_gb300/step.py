@@ -176,12 +176,13 @@ class LoraStep:
         return self._prep_ws
 
     # ------------------------------------------------------------------------------------------
-    def _enqueue(self, opt_step: int, per_chunk_calls: bool, backward: bool):
+    def _enqueue(self, opt_step: int, per_chunk_calls: bool, backward: bool, forward: bool = True,
+                 linears: Optional[Sequence[Linear]] = None):
         main = torch.cuda.current_stream(self.device)
         k, use = _streams_in_use(self)
         _fork(main, use)
         ct = self.T // self.chunks
-        for i, l in enumerate(self.linears):
+        for i, l in enumerate(self.linears if linears is None else linears):
             st = use[i % k] if use else main
             ws = self.ws[i % k]
             d = self.desc(l)
@@ -195,7 +196,8 @@ class LoraStep:
                 ctx = L.make_ctx(opt_step, ordinal, ct)
                 sl = slice(t0, t0 + n)
                 X, dY, Y, dX, H = l.X[sl], l.dY[sl], l.Y[sl], l.dX[sl], l.H[sl]
-                L.lora_forward(d, ctx, n, X, l.W, l.Wp, l.A, l.B, l.mag, l.norm, Y, H, ws, stream=st)
+                if forward:
+                    L.lora_forward(d, ctx, n, X, l.W, l.Wp, l.A, l.B, l.mag, l.norm, Y, H, ws, stream=st)
                 if backward:
                     L.lora_backward(d, ctx, n, X, l.Wp, l.A, l.B, dY, H, l.mag, l.norm, Y, dX, l.gA,
                                     l.gB, l.gmag, ws, stream=st)
@@ -240,7 +242,10 @@ class SublayerStep(LoraStep):
     parameters AdamW (no decay, plain learning rate)."""
 
     def __init__(self, X: torch.Tensor, linears: Sequence[Linear], *, kind: str = "layer",
-                 eps: float = 1e-5, muon: Optional[L.lora_muon_hp] = None, **kw):
+                 eps: float = 1e-5, muon: Optional[L.lora_muon_hp] = None, inner: Sequence[Linear] = (),
+                 n_inner: int = 0, **kw):
+        """`inner`: further projections of the sublayer, which read something else; n_inner: further
+        parameters at the magnitudes' end."""
         if kind not in ("layer", "rms"):
             raise ValueError(f"kind {kind!r}: 'layer' or 'rms'")
         if not 1 <= len(linears) <= L.LORA_SUM_MAX:
@@ -255,6 +260,7 @@ class SublayerStep(LoraStep):
             if l.in_dim != X.shape[1] or tuple(l.dY.shape) != (X.shape[0], l.out_dim) or l.dY.dtype != X.dtype:
                 raise ValueError(f"projection {l.proj_id}: W {tuple(l.W.shape)} and dY {tuple(l.dY.shape)} "
                                  f"{l.dY.dtype} do not fit X {tuple(X.shape)} {X.dtype}")
+        self.readers = list(linears)                   # the projections that read the norm's output
         self.X_in = X                                  # [T, dim], the sublayer's input
         self.H_norm = torch.empty_like(X)
         for l in linears:
@@ -262,7 +268,7 @@ class SublayerStep(LoraStep):
         self.norm = L.make_norm_desc(X.shape[1], L.LORA_NORM_RMS if kind == "rms" else L.LORA_NORM_LAYER,
                                      L.LORA_F32 if X.dtype == torch.float32 else L.LORA_BF16, eps)
         dim, shift = X.shape[1], kind != "rms"
-        super().__init__(linears, n_extra=dim * (2 if shift else 1), **kw)
+        super().__init__(self.readers + list(inner), n_extra=dim * (2 if shift else 1) + n_inner, **kw)
         base = self.n_a + self.n_b
         self.gamma, self.dgamma = (self.arena.view(w, base, (dim,)) for w in ("params", "grads"))
         self.beta = self.dbeta = None
@@ -271,7 +277,7 @@ class SublayerStep(LoraStep):
         self.gamma.fill_(1.0)
         self.stats = torch.empty((self.T, 2), dtype=torch.float32, device=self.device)
         self.dX = torch.empty_like(X)
-        self.dH_norm = torch.empty_like(X) if len(self.linears) > 1 else None   # the norm output's gradient
+        self.dH_norm = torch.empty_like(X) if len(self.readers) > 1 else None   # the norm output's gradient
         self.norm_ws = _ws(L.lora_norm_backward_workspace_size(self.norm, self.T), self.device)
         self.muon = muon if muon is not None else L.make_muon_hp(weight_decay=self.hp.weight_decay,
                                                                  plus_ratio=self.hp.plus_ratio)
@@ -297,15 +303,21 @@ class SublayerStep(LoraStep):
                          per_chunk_calls: bool = False):
         """Forward, every projection's backward, and the norm's backward on the sum of their input
         gradients (added in fp32: rounded once, and dX once more with the residual's gradient)."""
+        self._check_residual(dX_res)
+        self._norm_forward()
+        self._enqueue(opt_step, per_chunk_calls, True)
+        self._norm_backward(dX_res)
+
+    def _check_residual(self, dX_res: Optional[torch.Tensor]):
         if dX_res is not None and not (torch.is_tensor(dX_res) and dX_res.shape == self.X_in.shape and
                                        dX_res.dtype == self.X_in.dtype and dX_res.is_contiguous()):
             raise ValueError("dX_res: a contiguous tensor of X's shape and type")
-        self._norm_forward()
-        self._enqueue(opt_step, per_chunk_calls, True)
-        dH = self.linears[0].dX
-        if len(self.linears) > 1:
+
+    def _norm_backward(self, dX_res: Optional[torch.Tensor]):
+        dH = self.readers[0].dX
+        if len(self.readers) > 1:
             dH = self.dH_norm
-            L.lora_sum([l.dX for l in self.linears], dH.numel(), self.norm.dtype, dH)
+            L.lora_sum([l.dX for l in self.readers], dH.numel(), self.norm.dtype, dH)
         L.lora_norm_backward(self.norm, self.T, self.X_in, self.gamma, dH, self.stats, dX_res, self.dX,
                              self.dgamma, self.dbeta, self.norm_ws)
 
@@ -324,6 +336,99 @@ class SublayerStep(LoraStep):
             zero_grads: bool = True, per_chunk_calls: bool = False):
         self.forward_backward(opt_step, dX_res, per_chunk_calls)
         self.optimizer_step(lr, opt_step, zero_grads)
+
+
+class AttentionStep(SublayerStep):
+    """One optimizer step of an attention sublayer: a norm, adapted query, key and value projections,
+    the norm of each query and key head with the rotation by position, causal attention over packed
+    sequences, and the adapted output projection,
+        Q, K, V = projections(norm(X)),  Y = projection_o(attention(rope(Q), rope(K), V)),
+    with the norms' weights trained beside the adapters (as in SublayerStep; without the heads' norms
+    with head_norm=False). q, k, v and o are the Linears of the four projections; o.dY is the
+    sublayer's output gradient, the other three gradients are the step's own. seq_start: int32 [n + 1]
+    on the device, the sequences' first tokens and the last one's end; tokens of no sequence are padding
+    (their output gradients have to be zero). pos: int32 [tokens], from 0 in each sequence unless given
+    (negative: padding); inv_freq: the rotation's frequencies, rope_base^(-2 i / head_dim) unless given."""
+
+    def __init__(self, X: torch.Tensor, q: Linear, k: Linear, v: Linear, o: Linear, *, q_heads: int,
+                 kv_heads: int, head_dim: int, seq_start: torch.Tensor, pos: Optional[torch.Tensor] = None,
+                 n_pos: Optional[int] = None, rope_base: float = 10000.0,
+                 inv_freq: Optional[torch.Tensor] = None, pairs: bool = False, head_norm: bool = True,
+                 head_eps: float = 1e-6, **kw):
+        if X.dtype != torch.bfloat16:
+            raise ValueError("the attention step takes bf16 activations")
+        T, dev, wq, wk = X.shape[0], X.device, q_heads * head_dim, kv_heads * head_dim
+        for name, l, width in (("q", q, wq), ("k", k, wk), ("v", v, wk)):
+            if l.out_dim != width:
+                raise ValueError(f"projection {name}: {l.out_dim} outputs for {width // max(head_dim, 1)} heads of {head_dim}")
+        if o.in_dim != wq or tuple(o.dY.shape) != (T, o.out_dim) or o.dY.dtype != X.dtype:
+            raise ValueError(f"projection o: W {tuple(o.W.shape)} and dY {tuple(o.dY.shape)} {o.dY.dtype}")
+        if seq_start.dtype != torch.int32 or seq_start.dim() != 1 or seq_start.numel() < 2:
+            raise ValueError("seq_start: int32 [sequences + 1]")
+        new = lambda n: torch.zeros((T, n), dtype=X.dtype, device=dev)   # noqa: E731  (padding rows stay zero)
+        for l in (q, k, v):
+            l.dY = new(l.out_dim)
+        self.q, self.k, self.v, self.o = q, k, v, o
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
+        o.X = new(wq)                                      # the attention's output
+        super().__init__(X, [q, k, v], inner=[o], n_inner=2 * head_dim if head_norm else 0, **kw)
+        self.gamma_q = self.gamma_k = self.dgamma_q = self.dgamma_k = None
+        if head_norm:
+            at = self.n_a + self.n_b + self.n_mag - 2 * head_dim
+            self.gamma_q, self.dgamma_q = (self.arena.view(w, at, (head_dim,)) for w in ("params", "grads"))
+            self.gamma_k, self.dgamma_k = (self.arena.view(w, at + head_dim, (head_dim,)) for w in ("params", "grads"))
+            self.gamma_q.fill_(1.0)
+            self.gamma_k.fill_(1.0)
+        self.seq_start, self.n_seq = seq_start, seq_start.numel() - 1
+        if pos is None:
+            at = seq_start.long().clamp(0, T)
+            seq = torch.searchsorted(at, torch.arange(T, device=dev), right=True) - 1
+            pos = torch.arange(T, device=dev) - at[seq.clamp(min=0)]
+            pos = torch.where((seq >= 0) & (seq < self.n_seq), pos, -1).int()
+        if pos.dtype != torch.int32 or tuple(pos.shape) != (T,):
+            raise ValueError("pos: int32 [tokens]")
+        self.pos, self.n_pos = pos.contiguous(), T if n_pos is None else n_pos
+        if inv_freq is None:
+            inv_freq = rope_base ** (-torch.arange(0, head_dim, 2, dtype=torch.float64) / head_dim)
+        self.table = torch.empty((self.n_pos, head_dim // 2, 2), dtype=torch.float32, device=dev)
+        L.lora_rope_table(self.n_pos, head_dim, inv_freq.to(device=dev, dtype=torch.float64).contiguous(), self.table)
+        self.rope = L.make_rope_desc(q_heads, kv_heads, head_dim, L.LORA_BF16,
+                                     L.LORA_ROPE_PAIRS if pairs else L.LORA_ROPE_HALVES, head_eps)
+        self.attn = L.make_attn_desc(q_heads, kv_heads, head_dim)
+        self.plan = _ws(L.lora_attn_plan_size(T, self.n_seq), dev)
+        self.Qr, self.Kr, self.dQr, self.dKr = new(wq), new(wk), new(wq), new(wk)   # turned
+        self.lse = torch.zeros((q_heads, T), dtype=torch.float32, device=dev)
+        self.attn_ws = _ws(max(L.lora_attn_backward_workspace_size(self.attn, T),
+                               L.lora_rope_backward_workspace_size(self.rope, T)), dev)
+
+    def _forward(self, opt_step: int, per_chunk_calls: bool):
+        """Everything up to the output projection."""
+        self._norm_forward()
+        self._enqueue(opt_step, per_chunk_calls, False, linears=self.readers)
+        T = self.T
+        L.lora_attn_plan_build(T, self.n_seq, self.seq_start, self.plan)
+        L.lora_rope_forward(self.rope, T, self.q.Y, self.k.Y, self.gamma_q, self.gamma_k, self.pos, self.table,
+                            self.n_pos, self.Qr, self.Kr)
+        L.lora_attn_forward(self.attn, T, self.n_seq, self.plan, self.Qr, self.Kr, self.v.Y, self.o.X, self.lse)
+
+    def forward(self, opt_step: int = 0):
+        self._forward(opt_step, False)
+        self._enqueue(opt_step, False, False, linears=[self.o])
+
+    def forward_backward(self, opt_step: int, dX_res: Optional[torch.Tensor] = None,
+                         per_chunk_calls: bool = False):
+        """Forward and backward of the whole sublayer; gradients accumulate into the arena."""
+        self._check_residual(dX_res)
+        self._forward(opt_step, per_chunk_calls)
+        self._enqueue(opt_step, per_chunk_calls, True, linears=[self.o])
+        T = self.T
+        L.lora_attn_backward(self.attn, T, self.n_seq, self.plan, self.Qr, self.Kr, self.v.Y, self.o.X, self.lse,
+                             self.o.dX, self.dQr, self.dKr, self.v.dY, self.attn_ws)
+        L.lora_rope_backward(self.rope, T, self.q.Y, self.k.Y, self.gamma_q, self.gamma_k, self.pos, self.table,
+                             self.n_pos, self.dQr, self.dKr, self.q.dY, self.k.dY, self.dgamma_q, self.dgamma_k,
+                             self.attn_ws)
+        self._enqueue(opt_step, per_chunk_calls, True, forward=False, linears=self.readers)
+        self._norm_backward(dX_res)
 
 
 @dataclass
