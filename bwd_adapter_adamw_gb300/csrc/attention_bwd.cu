@@ -64,7 +64,8 @@ struct BwdK {
   CUtensorMap tq, tk, tv, tdo;
   const int32_t* count;
   const AttnTile* tiles;
-  int32_t heads;         // dK, dV: CTAs of a tile
+  int32_t heads;         // dK, dV: work items of a tile
+  int32_t split;         // dK, dV: CTAs of a cluster, which share a group's query heads
   int32_t groups;        // dQ: work items of a tile of the list
   int32_t by_heads;      // dQ: two heads of a 128-row tile, or two 128-row tiles of a head
   int32_t per;
@@ -100,12 +101,22 @@ struct DkvCfg {
   static constexpr int kBarriers = 512;
   static constexpr int kSmem = (2 + kQ + kDo) * kTile + 2 * kRows * 4 + kBarriers + 1024 /*alignment*/;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static_assert((kQ + kDo) * kTile >= 2 * kRows * D * 4, "both sums fit where Q and dO were");
   static constexpr uint32_t kIdS = idesc(kFmtBF16, 128, 128);
   static constexpr uint32_t kIdD = idesc(kFmtBF16, 128, D, false, true);
   static constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 384;   // tensor memory
 };
 
+// Element (row, 4 c ..) of a [128, D] fp32 tile in shared memory, in 16-byte pieces, turned within each row so that
+// 32 rows' pieces lie in different banks.
 template <int D>
+__device__ __forceinline__ float* sum_at(float* tile, int row, int c) {
+  return tile + row * D + ((c ^ (row & (D / 4 - 1))) << 2);
+}
+
+// CL: the query heads of a group are dealt out to the `split` CTAs of a cluster, one item each, and their sums added
+// up over the cluster; otherwise the CTAs are persistent over the items and take all heads of a group.
+template <int D, bool CL>
 __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_constant__ BwdK p) {
   using C = DkvCfg<D>;
   using Tl = Tile<D>;
@@ -122,8 +133,10 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
   uint64_t* do_full = q_empty + C::kQ;
   uint64_t* do_empty = do_full + C::kDo;
   uint64_t* k_full = do_empty + C::kDo;
-  uint64_t* v_full = k_full + 1;
-  uint64_t* s_full = v_full + 1;
+  uint64_t* k_empty = k_full + 1;    // the item's last S is complete
+  uint64_t* v_full = k_empty + 1;
+  uint64_t* v_empty = v_full + 1;    // the item's last dP is complete
+  uint64_t* s_full = v_empty + 1;
   uint64_t* p_full = s_full + 1;     // P^T is in place
   uint64_t* dp_full = p_full + 1;
   uint64_t* ds_full = dp_full + 1;   // dS^T is in place
@@ -133,19 +146,17 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
   uint64_t* delta_empty = delta_full + 1;
   uint64_t* fix_q = delta_empty + 1;
   uint64_t* fix_do = fix_q + 1;
-  uint64_t* all = fix_do + 1;        // both sums are complete
+  uint64_t* all = fix_do + 1;        // both sums of an item are complete
   uint64_t* done = all + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  static_assert((2 * (C::kQ + C::kDo) + 14) * 8 + 4 <= C::kBarriers, "barriers");
+  uint32_t* complete = tmem_slot + 1;   // CL: this CTA's sums are in shared memory
+  static_assert((2 * (C::kQ + C::kDo) + 16) * 8 + 8 <= C::kBarriers, "barriers");
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-
-  grid_dep_sync();
-  const int li = blockIdx.x / p.heads, hk = blockIdx.x - li * p.heads;
-  if (li >= __ldg(p.count)) return;
-  const AttnTile t = tile_at(p.tiles + li);
-  const int nb = (t.len + kRows - 1) / kRows;
-  const int j = nb - 1 - t.index;     // the key tile with t.index + 1 query tiles
-  const int nq = t.index + 1, n = nq * p.per;   // iteration it: head it / nq of the group, query tile j + it % nq
+  const int rank = CL ? (int)cluster_ctarank() : 0;
+  if constexpr (CL) {   // clusters behind the last item leave before they take tensor memory
+    grid_dep_sync();
+    if ((int)blockIdx.x / p.split >= __ldg(p.count) * p.heads) return;
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kQ; ++s) {
@@ -157,7 +168,9 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
       mbar_init(&do_empty[s], 1);
     }
     mbar_init(k_full, 1);
+    mbar_init(k_empty, 1);
     mbar_init(v_full, 1);
+    mbar_init(v_empty, 1);
     mbar_init(s_full, 1);
     mbar_init(p_full, kComputeWarps);
     mbar_init(dp_full, 1);
@@ -170,6 +183,7 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
     mbar_init(fix_do, 1);
     mbar_init(all, 1);
     mbar_init(done, 1);
+    *complete = 1u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
   }
@@ -178,11 +192,24 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
   __syncthreads();
   fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+  if constexpr (!CL) grid_dep_sync();   // from here on, the earlier kernels' outputs are visible
 
   if (warp >= kComputeWarps) Sp::issue();
+  AttnTile t{};
+  int hk = 0;
+  Items items(p.tiles, p.heads, p.count, CL ? p.split : 1);
+  const int mine = p.per / (CL ? p.split : 1);   // query heads of an item in this CTA
+  // An item: key tile j of nb, its query tiles j .. nb - 1 under each of its query heads, head by head.
+  struct Span {
+    int nb, j, nq, n, h0;
+    __device__ Span(const AttnTile& t, int hk, int per, int mine, int rank)
+        : nb((t.len + kRows - 1) / kRows), j(nb - 1 - t.index), nq(t.index + 1), n(nq * mine), h0(hk * per + rank * mine) {}
+  };
   if (warp == kLoadWarp) {
     // ---- loads ----
-    int fixes = 0;   // of Q and of dO alike
+    int fixes = 0;                  // of Q and of dO alike
+    int nk = 0, nv = 0, nqs = 0, ndo = 0;   // tiles asked for
+    bool ok = true;
     // Rows behind the sequence are zeroed: P^T and dS^T are zero there, but zero times a NaN is not.
     auto fetch = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* fix, int col, int qi) {
       const int rows = t.len - qi * kRows;
@@ -199,27 +226,38 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
       if (lane == 0) mbar_arrive(full);
       return true;
     };
-    if (lane == 0) {
-      mbar_expect_tx(k_full, C::kTile);
-      Tl::load(sk, &p.tk, k_full, hk * D, t.row0 + j * kRows);
-      mbar_expect_tx(v_full, C::kTile);
-      Tl::load(sv, &p.tv, v_full, hk * D, t.row0 + j * kRows);
-    }
-    int it = 0, nqs = 0, ndo = 0;   // tiles of Q and dO asked for
-    for (; it < n; ++it) {
-      const int g = it / nq, qi = j + it - g * nq, col = (hk * p.per + g) * D;
-      const int a = it % C::kQ, b = it % C::kDo;
-      if (it >= C::kQ && !warp_wait(&q_empty[a], (uint32_t)(it / C::kQ - 1) & 1u, 1u, p.err, p.limit)) break;
-      ++nqs;
-      if (!fetch(sq + a * C::kTile, &p.tq, &q_full[a], fix_q, col, qi)) break;
-      if (it >= C::kDo && !warp_wait(&do_empty[b], (uint32_t)(it / C::kDo - 1) & 1u, 1u, p.err, p.limit)) break;
-      ++ndo;
-      if (!fetch(sdo + b * C::kTile, &p.tdo, &do_full[b], fix_do, col, qi)) break;
-      if (t.len - qi * kRows < kRows) ++fixes;
+    auto keys = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* empty, int& n, int j) {
+      if (n && !warp_wait(empty, (uint32_t)(n - 1) & 1u, 1u, p.err, p.limit)) return false;
+      ++n;
+      if (lane == 0) {
+        mbar_expect_tx(full, C::kTile);
+        Tl::load(dst, map, full, hk * D, t.row0 + j * kRows);
+      }
+      return true;
+    };
+    while (ok && items.take(t, hk)) {
+      const Span sp(t, hk, p.per, mine, rank);
+      if (!(ok = keys(sk, &p.tk, k_full, k_empty, nk, sp.j))) break;
+      int qi = sp.j, h = sp.h0;
+      for (int it = 0; it < sp.n; ++it) {
+        const int a = nqs % C::kQ, b = ndo % C::kDo, col = h * D;
+        if (nqs >= C::kQ && !(ok = warp_wait(&q_empty[a], (uint32_t)(nqs / C::kQ - 1) & 1u, 1u, p.err, p.limit))) break;
+        ++nqs;
+        if (!(ok = fetch(sq + a * C::kTile, &p.tq, &q_full[a], fix_q, col, qi))) break;
+        if (it == 0 && !(ok = keys(sv, &p.tv, v_full, v_empty, nv, sp.j))) break;
+        if (ndo >= C::kDo && !(ok = warp_wait(&do_empty[b], (uint32_t)(ndo / C::kDo - 1) & 1u, 1u, p.err, p.limit))) break;
+        ++ndo;
+        if (!(ok = fetch(sdo + b * C::kTile, &p.tdo, &do_full[b], fix_do, col, qi))) break;
+        if (t.len - qi * kRows < kRows) ++fixes;
+        if (++qi == sp.nb) {
+          qi = sp.j;
+          ++h;
+        }
+      }
     }
     if (lane == 0) {   // every copy has landed before the CTA ends
-      mbar_wait(k_full, 0u, 1u, p.err);
-      mbar_wait(v_full, 0u, 1u, p.err);
+      if (nk) mbar_wait(k_full, (uint32_t)(nk - 1) & 1u, 1u, p.err);
+      if (nv) mbar_wait(v_full, (uint32_t)(nv - 1) & 1u, 1u, p.err);
       for (int k = nqs > C::kQ ? nqs - C::kQ : 0; k < nqs; ++k)
         if (!mbar_wait(&q_full[k % C::kQ], (uint32_t)(k / C::kQ) & 1u, 1u, p.err)) break;
       for (int k = ndo > C::kDo ? ndo - C::kDo : 0; k < ndo; ++k)
@@ -235,67 +273,86 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
       fence_after();
       return r;
     };
-    auto q_in = [&](int it) { return wait(&q_full[it % C::kQ], (uint32_t)(it / C::kQ)); };
-    auto do_in = [&](int it) { return wait(&do_full[it % C::kDo], (uint32_t)(it / C::kDo)); };
-    auto q_at = [&](int it) { return aq + (uint32_t)(it % C::kQ) * C::kTile; };
-    auto do_at = [&](int it) { return ado + (uint32_t)(it % C::kDo) * C::kTile; };
+    auto q_in = [&](int g) { return wait(&q_full[g % C::kQ], (uint32_t)(g / C::kQ)); };
+    auto do_in = [&](int g) { return wait(&do_full[g % C::kDo], (uint32_t)(g / C::kDo)); };
+    auto q_at = [&](int g) { return aq + (uint32_t)(g % C::kQ) * C::kTile; };
+    auto do_at = [&](int g) { return ado + (uint32_t)(g % C::kDo) * C::kTile; };
     const uint32_t ts = tmem + C::kS, tp = tmem + C::kDp;
-    bool ok = wait(k_full, 0u) && wait(v_full, 0u);
-    // S and dP of tile it over the P and dS of the one before, whose products come first
+    int g = 0;          // query tiles so far
+    uint32_t i = 0;     // items so far
+    bool ok = true;
+    while (ok && items.take(t, hk)) {
+      const Span sp(t, hk, p.per, mine, rank);
+      if (!(ok = wait(k_full, i))) break;
+      // S and dP of tile it over the P and dS of the one before, whose products come first
 #pragma unroll 1
-    for (int it = 0; it <= n && ok; ++it) {
-      if (it > 0) {
-        if (!(ok = wait(p_full, (uint32_t)(it - 1)))) break;
-        Tl::template mma_tn<kCols>(tmem + C::kDv, ts, do_at(it - 1), C::kIdD, it > 1, one);
-        commit(&do_empty[(it - 1) % C::kDo], one);
+      for (int it = 0; it <= sp.n; ++it, ++g) {
+        if (it > 0) {
+          if (!(ok = wait(p_full, (uint32_t)(g - 1)))) break;
+          Tl::template mma_tn<kCols>(tmem + C::kDv, ts, do_at(g - 1), C::kIdD, it > 1, one);
+          commit(&do_empty[(g - 1) % C::kDo], one);
+        }
+        if (it < sp.n) {
+          if (!(ok = q_in(g))) break;
+          Tl::mma_nt(ts, ak, q_at(g), C::kIdS, one);
+          commit(s_full, one);
+          if (it + 1 == sp.n) commit(k_empty, one);
+        }
+        if (it > 0) {
+          if (!(ok = wait(ds_full, (uint32_t)(g - 1)))) break;
+          Tl::template mma_tn<kCols>(tmem + C::kDk, tp, q_at(g - 1), C::kIdD, it > 1, one);
+          commit(&q_empty[(g - 1) % C::kQ], one);
+        }
+        if (it < sp.n) {
+          if (!(ok = (it > 0 || wait(v_full, i)) && do_in(g))) break;
+          Tl::mma_nt(tp, av, do_at(g), C::kIdS, one);
+          commit(dp_full, one);
+          if (it + 1 == sp.n) commit(v_empty, one);
+        }
       }
-      if (it < n) {
-        if (!(ok = q_in(it))) break;
-        Tl::mma_nt(ts, ak, q_at(it), C::kIdS, one);
-        commit(s_full, one);
-      }
-      if (it > 0) {
-        if (!(ok = wait(ds_full, (uint32_t)(it - 1)))) break;
-        Tl::template mma_tn<kCols>(tmem + C::kDk, tp, q_at(it - 1), C::kIdD, it > 1, one);
-        commit(&q_empty[(it - 1) % C::kQ], one);
-      }
-      if (it < n) {
-        if (!(ok = do_in(it))) break;
-        Tl::mma_nt(tp, av, do_at(it), C::kIdS, one);
-        commit(dp_full, one);
-      }
+      --g;   // (n + 1 rounds)
+      ++i;
+      if (ok) commit(all, one);
     }
-    if (ok) commit(all, one);
     commit(done, one);   // every product has completed before the tensor memory is freed
     mbar_wait(done, 0u, 2u, p.err);
     __syncwarp();
   } else if (warp == kStatWarp) {
     // ---- statistics of the query tile, four queries per lane, read one tile ahead ----
-    float vl[4], vd[4];
-    auto read = [&](int it) {
-      const int g = it / nq, qi = j + it - g * nq;
+    uint32_t g = 0;
+    bool ok = true;
+    while (ok && items.take(t, hk)) {
+      const Span sp(t, hk, p.per, mine, rank);
+      float vl[4], vd[4];
+      int qi = sp.j, h = sp.h0;
+      auto read = [&](bool more) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = qi * kRows + lane + 32 * k;
-        const bool in = it < n && r < t.len;
-        const int64_t at = (int64_t)(hk * p.per + g) * p.T + t.row0 + r;
-        vl[k] = in ? -__ldg(p.lse + at) * kLog2e : -INFINITY;   // a query behind the sequence: P = 0
-        vd[k] = in ? -__ldg(p.delta + at) : 0.f;
+        for (int k = 0; k < 4; ++k) {
+          const int r = qi * kRows + lane + 32 * k;
+          const bool in = more && r < t.len;
+          const int64_t at = (int64_t)h * p.T + t.row0 + r;
+          vl[k] = in ? -__ldg(p.lse + at) * kLog2e : -INFINITY;   // a query behind the sequence: P = 0
+          vd[k] = in ? -__ldg(p.delta + at) : 0.f;
+        }
+      };
+      read(true);
+      for (int it = 0; it < sp.n; ++it, ++g) {
+        if (g && !(ok = warp_wait(lse_empty, (g - 1) & 1u, 1u, p.err, p.limit))) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s_lse[lane + 32 * k] = vl[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(lse_full);
+        if (g && !(ok = warp_wait(delta_empty, (g - 1) & 1u, 1u, p.err, p.limit))) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s_delta[lane + 32 * k] = vd[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(delta_full);
+        if (++qi == sp.nb) {
+          qi = sp.j;
+          ++h;
+        }
+        read(it + 1 < sp.n);
       }
-    };
-    read(0);
-    for (int it = 0; it < n; ++it) {
-      if (it && !warp_wait(lse_empty, (uint32_t)(it - 1) & 1u, 1u, p.err, p.limit)) break;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s_lse[lane + 32 * k] = vl[k];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(lse_full);
-      if (it && !warp_wait(delta_empty, (uint32_t)(it - 1) & 1u, 1u, p.err, p.limit)) break;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s_delta[lane + 32 * k] = vd[k];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(delta_full);
-      read(it + 1);
     }
   } else if (warp < kComputeWarps) {
     Sp::compute();
@@ -308,77 +365,127 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
     const f2 c2 = mk2(p.c, p.c);
     const uint64_t* z_lse = reinterpret_cast<const uint64_t*>(s_lse + kCols * w + 2 * q);
     const uint64_t* z_delta = reinterpret_cast<const uint64_t*>(s_delta + kCols * w + 2 * q);
+    uint32_t g = 0, item = 0;
     bool ok = true;
-    int qi = j;
-    for (int it = 0; it < n; ++it) {
-      const uint32_t par = (uint32_t)it & 1u;
-      if (!(ok = warp_wait(lse_full, par, 4u, p.err, p.limit) && warp_wait(s_full, par, 4u, p.err, p.limit))) break;
+    while (ok && items.take(t, hk)) {
+      const Span sp(t, hk, p.per, mine, rank);
+      int qi = sp.j;
+      for (int it = 0; it < sp.n; ++it, ++g) {
+        const uint32_t par = g & 1u;
+        if (!(ok = warp_wait(lse_full, par, 4u, p.err, p.limit) && warp_wait(s_full, par, 4u, p.err, p.limit))) break;
+        fence_after();
+        uint32_t x[kCols], u[kCols / 2];   // x: keys +0 and +8, then +16 and +24
+        tmem_ld16x32_nw(ts, x);
+        tmem_ld16x32_nw(ts + (16u << 16), x + 16);
+        f2 z[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) z[b] = z_lse[4 * b];
+        tmem_wait_ld_n<kCols>(x);
+#pragma unroll
+        for (int k = 0; k < kCols / 2; ++k) {
+          const float2 a = un2(fma2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, z[k / 2 % 4]));
+          x[2 * k] = __float_as_uint(exp2_(a.x));
+          x[2 * k + 1] = __float_as_uint(exp2_(a.y));
+        }
+        if (qi == sp.j) {   // the tile on the diagonal: queries from the key's own on
+#pragma unroll
+          for (int k = 0; k < kCols; ++k)
+            if (kCols * w + 8 * (k / 4 % 4) + 2 * q + (k & 1) < key + 8 * (k / 2 % 2) + 16 * (k / 16)) x[k] = 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < kCols / 2; ++k) u[k] = pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+        tmem_st16x16(ts, u);
+        tmem_st16x16(ts + (16u << 16), u + 8);
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(p_full);
+          mbar_arrive(lse_empty);
+        }
+        if (!(ok = warp_wait(delta_full, par, 4u, p.err, p.limit) && warp_wait(dp_full, par, 4u, p.err, p.limit))) break;
+        fence_after();
+        uint32_t y[kCols];
+        tmem_ld16x32_nw(tp, y);
+        tmem_ld16x32_nw(tp + (16u << 16), y + 16);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) z[b] = z_delta[4 * b];
+        tmem_wait_ld_n<kCols>(y);
+#pragma unroll
+        for (int k = 0; k < kCols / 2; ++k) {
+          const float2 a = un2(mul2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])),
+                                    add2(mk2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), z[k / 2 % 4])));
+          u[k] = pack_bf16(a.x, a.y);
+        }
+        tmem_st16x16(tp, u);
+        tmem_st16x16(tp + (16u << 16), u + 8);
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(ds_full);
+          mbar_arrive(delta_empty);
+        }
+        if (++qi == sp.nb) qi = sp.j;
+      }
+      if (!ok || !(ok = warp_wait(all, item++ & 1u, 4u, p.err, p.limit))) break;
       fence_after();
-      uint32_t x[kCols], u[kCols / 2];   // x: keys +0 and +8, then +16 and +24
-      tmem_ld16x32_nw(ts, x);
-      tmem_ld16x32_nw(ts + (16u << 16), x + 16);
-      f2 z[4];
+      const int row = sp.j * kRows + r, half = w & 1, c0 = half * (D / 2);
+      if constexpr (CL) {
+        // the item's only one: no copy is under way into Q's and dO's places, and every product has read them
+        float* tile = reinterpret_cast<float*>(sq) + (w >> 1) * kRows * D;
+        const uint32_t col = lanes + (w < 2 ? C::kDv : C::kDk) + c0;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) z[b] = z_lse[4 * b];
-      tmem_wait_ld_n<kCols>(x);
+        for (int k = 0; k < D / 64; ++k) {
+          float v[32];
+          tmem_ld32(col + 32 * k, v);
 #pragma unroll
-      for (int k = 0; k < kCols / 2; ++k) {
-        const float2 a = un2(fma2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, z[k / 2 % 4]));
-        x[2 * k] = __float_as_uint(exp2_(a.x));
-        x[2 * k + 1] = __float_as_uint(exp2_(a.y));
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float4*>(sum_at<D>(tile, r, c0 / 4 + 8 * k + c)) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        }
+      } else {
+        const int64_t at = (int64_t)t.row0 + row;
+        if (w < 2)
+          store_row<D / 2>(lanes + C::kDv + c0, 1.f, p.dV + at * p.ld_v + (int64_t)hk * D + c0, row < t.len);
+        else
+          store_row<D / 2>(lanes + C::kDk + c0, p.scale, p.dK + at * p.ld_k + (int64_t)hk * D + c0, row < t.len);
       }
-      if (qi == j) {   // the tile on the diagonal: queries from the key's own on
-#pragma unroll
-        for (int k = 0; k < kCols; ++k)
-          if (kCols * w + 8 * (k / 4 % 4) + 2 * q + (k & 1) < key + 8 * (k / 2 % 2) + 16 * (k / 16)) x[k] = 0u;
-      }
-#pragma unroll
-      for (int k = 0; k < kCols / 2; ++k) u[k] = pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
-      tmem_st16x16(ts, u);
-      tmem_st16x16(ts + (16u << 16), u + 8);
-      tmem_wait_st();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(p_full);
-        mbar_arrive(lse_empty);
-      }
-      if (!(ok = warp_wait(delta_full, par, 4u, p.err, p.limit) && warp_wait(dp_full, par, 4u, p.err, p.limit))) break;
-      fence_after();
-      uint32_t y[kCols];
-      tmem_ld16x32_nw(tp, y);
-      tmem_ld16x32_nw(tp + (16u << 16), y + 16);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) z[b] = z_delta[4 * b];
-      tmem_wait_ld_n<kCols>(y);
-#pragma unroll
-      for (int k = 0; k < kCols / 2; ++k) {
-        const float2 a = un2(mul2(mk2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])),
-                                  add2(mk2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), z[k / 2 % 4])));
-        u[k] = pack_bf16(a.x, a.y);
-      }
-      tmem_st16x16(tp, u);
-      tmem_st16x16(tp + (16u << 16), u + 8);
-      tmem_wait_st();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(ds_full);
-        mbar_arrive(delta_empty);
-      }
-      if (++qi == nb) qi = j;
+      fence_before();   // (the sums have been read before the next item's first P arrives)
     }
-    if (ok && warp_wait(all, 0u, 4u, p.err, p.limit)) {
-      fence_after();
-      const int row = j * kRows + r;
-      const int64_t at = (int64_t)t.row0 + row;
-      const int half = w & 1, c0 = half * (D / 2);
-      if (w < 2)
-        store_row<D / 2>(lanes + C::kDv + c0, 1.f, p.dV + at * p.ld_v + (int64_t)hk * D + c0, row < t.len);
-      else
-        store_row<D / 2>(lanes + C::kDk + c0, p.scale, p.dK + at * p.ld_k + (int64_t)hk * D + c0, row < t.len);
-    }
+    if (CL && !ok) *complete = 0u;
     fence_before();
+  }
+  if constexpr (CL) {
+    cluster_sync_all();
+    Items again(p.tiles, p.heads, p.count, p.split);
+    // (the compute warps alone: the others have few registers left)
+    if (warp < kComputeWarps && again.take(t, hk)) {   // the same for every CTA of the cluster
+      const int split = p.split, j = (t.len + kRows - 1) / kRows - 1 - t.index;
+      bool whole = true;   // sums that lack a CTA's part are not stored
+      for (int k = 0; k < split; ++k) {
+        uint32_t at, v;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(complete)), "r"(k));
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+        whole = whole && v != 0u;
+      }
+      // this CTA's share of the rows, the CTAs' parts added in order
+      const int rows = kRows / split, total = 2 * rows * (D / 4);
+      for (int e = threadIdx.x; whole && e < total; e += 32 * kComputeWarps) {
+        const int c = e % (D / 4), rr = e / (D / 4), which = rr / rows, r = rank * rows + rr % rows;
+        const int64_t row = (int64_t)j * kRows + r;
+        if (row >= t.len) continue;
+        const float* src = sum_at<D>(reinterpret_cast<float*>(sq) + which * kRows * D, r, c);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < split; ++k) {
+          const float4 u = dsmem_ld4(src, k);
+          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
+        const float f = which ? p.scale : 1.f;
+        const float out[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
+        store4((which ? p.dK + (t.row0 + row) * p.ld_k : p.dV + (t.row0 + row) * p.ld_v) + (int64_t)hk * D + 4 * c, out);
+      }
+    }
+    cluster_sync_all();   // the peers have read this CTA's shared memory
   }
   __syncthreads();
   if (warp == kIssueWarp) {
@@ -683,11 +790,38 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
   }
 }
 
+// CTAs that share a key tile's query heads: as many as the SMs hold at once, so that few key heads over few tokens
+// still use them.
+int dkv_split(const AttnArgs& a, int sms) {
+  const int64_t items = (a.T + kRows - 1) / kRows * a.kv_heads;
+  int n = 1;
+  while (n < 8 && a.q_heads / a.kv_heads % (2 * n) == 0 && items * 2 * n <= sms) n *= 2;
+  return n;
+}
+
+cudaError_t launch_clusters(void (*kernel)(const BwdK), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                            const BwdK& k, int cluster) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = add_pdl_attr(at, 1);
+  return cudaLaunchKernelEx(&cfg, kernel, k);
+}
+
 template <int D>
 cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> set{0};
   cudaError_t e = once_on_device(set, [] {
-    const cudaError_t r = set_up<Sp>(k_attn_dkv<D>, DkvCfg<D>::kSmem);
+    cudaError_t r = set_up<Sp>(k_attn_dkv<D, false>, DkvCfg<D>::kSmem);
+    if (r == cudaSuccess) r = set_up<Sp>(k_attn_dkv<D, true>, DkvCfg<D>::kSmem);
     return r != cudaSuccess ? r : set_up<SplitFwd>(k_attn_dq<D>, DqCfg<D>::kSmem);
   });
   if (e != cudaSuccess) return e;
@@ -721,8 +855,11 @@ cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t st) {
   k.count = a.plan.count;
   k.tiles = a.plan.tiles[0];
   k.heads = a.kv_heads;
+  k.split = dkv_split(a, sms);
+  if (grid * k.split > INT32_MAX) return cudaErrorInvalidValue;
   prof_begin(0, st);
-  e = launch_kernel(k_attn_dkv<D>, (unsigned)grid, Sp::kThreads, DkvCfg<D>::kSmem, st, k);
+  e = k.split > 1 ? launch_clusters(k_attn_dkv<D, true>, (unsigned)(grid * k.split), Sp::kThreads, DkvCfg<D>::kSmem, st, k, k.split)
+                  : launch_kernel(k_attn_dkv<D, false>, (unsigned)(grid < sms ? grid : sms), Sp::kThreads, DkvCfg<D>::kSmem, st, k);
   if (e != cudaSuccess) return e;
   k.count = a.plan.count + w;
   k.tiles = a.plan.tiles[w];

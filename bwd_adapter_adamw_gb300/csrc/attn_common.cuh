@@ -235,11 +235,11 @@ __device__ __forceinline__ AttnTile tile_at(const AttnTile* t) {
 // same items; the loading warp comes to each first, so that the others find its tile in L1.
 struct Items {
   const AttnTile* tiles;
-  int groups, n, round;
-  __device__ Items(const AttnTile* t, int g, const int32_t* count) : tiles(t), groups(g), n(uniform(__ldg(count) * g)), round(0) {}
+  int groups, n, round, b, grid;
+  __device__ Items(const AttnTile* t, int g, const int32_t* count, int cluster = 1)
+      : tiles(t), groups(g), n(uniform(__ldg(count) * g)), round(0), b((int)blockIdx.x / cluster), grid((int)gridDim.x / cluster) {}
   // the next item, false if there is none
   __device__ bool take(AttnTile& t, int& group) {
-    const int b = (int)blockIdx.x, grid = (int)gridDim.x;
     const int64_t i = (int64_t)round * grid + ((round & 1) ? grid - 1 - b : b);
     ++round;
     if (i >= n) return false;

@@ -119,7 +119,10 @@ BATCHES = [([1], 2, 1, 64, 0, False), ([1], 1, 1, 128, 5, True), ([17], 4, 2, 12
            ([257], 8, 1, 64, 3, False), ([383, 1, 0, 130], 4, 4, 128, 7, True), ([1] * 9, 6, 2, 128, 0, False),
            ([0, 0, 5, 0], 2, 1, 64, 2, False), ([300, 0, 64, 513], 4, 2, 64, 100, True),
            ([640, 200], 5, 1, 128, 0, False), ([1100], 2, 1, 128, 0, True), ([900, 31, 128], 6, 3, 64, 9, False),
-           ([64, 65, 66, 67, 68] * 3, 8, 2, 128, 30, True)]
+           ([64, 65, 66, 67, 68] * 3, 8, 2, 128, 30, True),
+           # more items than SMs: several for each CTA, in both forms of a pair
+           ([700, 1, 900, 0, 333, 566], 16, 8, 64, 11, False), ([900, 410, 640], 9, 9, 128, 0, True),
+           ([600] * 4, 8, 8, 128, 60, False), ([1300, 129, 700], 16, 16, 64, 0, True)]
 
 
 @pytest.mark.parametrize("batch", range(len(BATCHES)))
