@@ -93,7 +93,10 @@ def attention_bounds(q, k, v, o, lse, do, starts, scale: float, backward: bool):
     exponent's argument (2^-22 of |S| and |lse|) and of the exponential (2^-21): e_p in all; as an operand it
     is rounded to bf16, 2^-8. Sums of n such terms in fp32 add n 2^-23, at most 2^-10 here (n <= 8192).
     dS = P (dP - delta) carries P's factor, the roundings of dP and delta (dim 2^-23 of their terms' sizes)
-    and its own to bf16."""
+    and its own to bf16. The exponential gives 0 below the smallest normal number, 2^-126: P may be off by
+    that much besides, and dS by that times |dP - delta|; with the subnormal roundings of the two operands
+    (2^-134) and products with at least as small a term, `tiny` = 2^-125 of the other factors holds it."""
+    tiny = 2.0 ** -125
     q, k, v, o, do = (np.asarray(a, np.float64) for a in (q, k, v, o, do))
     H, per, dim = q.shape[1], q.shape[1] // k.shape[1], q.shape[2]
     u = dim * 2.0 ** -23
@@ -115,14 +118,15 @@ def attention_bounds(q, k, v, o, lse, do, starts, scale: float, backward: bool):
             if not backward:
                 # the sum of P is off by the mean of e_p at most; the running reference rescales both alike
                 mean = (p * e_p).sum(1, keepdims=True)
-                outs[0][a:b, h] = (p * (e_p + mean + 2.0 ** -8 + 2 * n)) @ np.abs(v[a:b, g])
+                outs[0][a:b, h] = (p * (e_p + mean + 2.0 ** -8 + 2 * n) + tiny) @ np.abs(v[a:b, g])
                 outs[1][h, a:b] = mean[:, 0] + n + 2.0 ** -21 * (1 + np.abs(lse[h, a:b]))
                 continue
-            outs[2][a:b, g] += (p * (e_p + 2.0 ** -8 + n)).T @ np.abs(do[a:b, h])
+            outs[2][a:b, g] += (p * (e_p + 2.0 ** -8 + n) + tiny).T @ np.abs(do[a:b, h])
             ad, av = np.abs(do[a:b, h]), np.abs(v[a:b, g])
             delta = (do[a:b, h] * o[a:b, h]).sum(1, keepdims=True)
-            ds = np.abs(p * (do[a:b, h] @ v[a:b, g].T - delta))
-            e_ds = ds * (e_p + 2.0 ** -8 + n) + p * u * (ad @ av.T + (ad * np.abs(o[a:b, h])).sum(1, keepdims=True)) * 1.01
+            dp = np.abs(do[a:b, h] @ v[a:b, g].T - delta)
+            e_ds = p * dp * (e_p + 2.0 ** -8 + n) + tiny * (1 + dp)
+            e_ds += p * u * (ad @ av.T + (ad * np.abs(o[a:b, h])).sum(1, keepdims=True)) * 1.01
             outs[0][a:b, h] = scale * e_ds @ np.abs(k[a:b, g])
             outs[1][a:b, g] += scale * e_ds.T @ np.abs(q[a:b, h])
     return outs
