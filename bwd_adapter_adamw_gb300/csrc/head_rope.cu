@@ -8,7 +8,7 @@
 // Bound by memory: a head's vector is read once, held in registers by a group of lanes between its sum
 // and its outputs, and written once. The statistics are recomputed in the backward pass, which reads x
 // anyway, so that the forward pass writes no more than y.
-#include "tc_ptx.cuh"
+#include "attn_common.cuh"
 
 namespace lora {
 
@@ -32,36 +32,41 @@ struct RopeK {
   float* part;             // backward: [CTA][q | k][head_dim] sums of the weights' gradients
 };
 
-// A lane's 2 V elements of a head: V from `lane V` of each half.
+using attn::f2;
+using attn::add2;
+using attn::fma2;
+using attn::mk2;
+using attn::mul2;
+using attn::un2;
+
+// A lane's 2 V elements of a head: V = 4 from `lane V` of each half, as packed pairs of neighbours (one instruction
+// for two elements). In bf16 that is 8 bytes of each half: with 16 a lane's vectors, angles, weights and sums took
+// 128 registers in the backward pass, and two CTAs of 256 threads per SM left the memory waiting.
 template <typename E> struct Half;
 template <> struct Half<float> {
   static constexpr int V = 4;
-  __device__ static void get(const uint4& v, float* f) {
-    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+  using raw = uint4;
+  __device__ static raw none() { return make_uint4(0, 0, 0, 0); }
+  __device__ static void get(const raw& v, f2* f) {
+    f[0] = mk2(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = mk2(__uint_as_float(v.z), __uint_as_float(v.w));
   }
-  __device__ static uint4 put(const float* f) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  __device__ static raw put(const f2* f) {
+    const float2 a = un2(f[0]), b = un2(f[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
   }
 };
 template <> struct Half<__nv_bfloat16> {
-  static constexpr int V = 8;
-  __device__ static void get(const uint4& v, float* f) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(w[j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
+  static constexpr int V = 4;
+  using raw = uint2;
+  __device__ static raw none() { return make_uint2(0, 0); }
+  __device__ static void get(const raw& v, f2* f) {
+    f[0] = mk2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+    f[1] = mk2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
   }
-  __device__ static uint4 put(const float* f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-      w[j] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+  __device__ static raw put(const f2* f) {
+    const float2 a = un2(f[0]), b = un2(f[1]);
+    return make_uint2(attn::pack_bf16(a.x, a.y), attn::pack_bf16(b.x, b.y));
   }
 };
 
@@ -79,53 +84,73 @@ __device__ __forceinline__ float head_sum(float v) {
   for (int o = LPH / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+__device__ __forceinline__ float sum2(f2 v) {
+  const float2 a = un2(v);
+  return a.x + a.y;
+}
 
-// Cosines and sines of a lane's pairs: HALVES, pair i is element i of both vectors; PAIRS, pair i <
-// V / 2 is elements 2 i, 2 i + 1 of the first vector, the others of the second. A position outside the
-// table gives NaN.
+// Cosines and sines of a lane's pairs. HALVES: pair i is element i of both vectors; c and s hold the cosines and
+// the sines of two neighbouring pairs. PAIRS: pair i < V / 2 is elements 2 i, 2 i + 1 of the
+// first vector, the others of the second; c holds a pair's cosine and sine. A position outside the table gives NaN.
 template <typename E, int D, bool PAIRS>
-__device__ __forceinline__ void load_turn(const RopeK& p, int64_t n, int l, float2 (&cs)[Half<E>::V]) {
-  constexpr int V = Half<E>::V;
-  if (n >= p.n_pos) {
+struct Turn {
+  static constexpr int V = Half<E>::V;
+  f2 c[PAIRS ? V : V / 2], s[PAIRS ? 1 : V / 2];
+  __device__ void load(const RopeK& p, int64_t pos, int l) {
+    const float2* row = p.table + pos * (D / 2);
+    const bool in = pos < p.n_pos;
+    const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
-    for (int i = 0; i < V; ++i) cs[i] = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
-    return;
+    for (int i = 0; i < V; i += 2) {
+      const int at = PAIRS ? (i < V / 2 ? l * (V / 2) + i : D / 4 + l * (V / 2) + i - V / 2) : l * V + i;
+      const float4 t = in ? __ldg(reinterpret_cast<const float4*>(row + at)) : make_float4(nan, nan, nan, nan);
+      if constexpr (PAIRS) {
+        c[i] = mk2(t.x, t.y);
+        c[i + 1] = mk2(t.z, t.w);
+      } else {
+        c[i / 2] = mk2(t.x, t.z);
+        s[i / 2] = mk2(t.y, t.w);
+      }
+    }
   }
-  const float2* row = p.table + n * (D / 2);
+  // the pairs of f turned by the angle (BACK: by its negative)
+  template <bool BACK>
+  __device__ void apply(f2 (&f)[V]) const {
+    if constexpr (PAIRS) {
 #pragma unroll
-  for (int i = 0; i < V; i += 2) {
-    const int at = PAIRS ? (i < V / 2 ? l * (V / 2) + i : D / 4 + l * (V / 2) + i - V / 2) : l * V + i;
-    const float4 t = __ldg(reinterpret_cast<const float4*>(row + at));
-    cs[i] = make_float2(t.x, t.y);
-    cs[i + 1] = make_float2(t.z, t.w);
-  }
-}
-
-// The pairs of (a | b) turned by the angle (SIGN 1) or back (SIGN -1).
-template <int V, bool PAIRS, int SIGN>
-__device__ __forceinline__ void turn(float (&f)[2 * V], const float2 (&cs)[V]) {
+      for (int i = 0; i < V; ++i) {
+        const float2 x = un2(f[i]), t = un2(c[i]);
+        const float z = BACK ? -t.y : t.y;
+        f[i] = mk2(x.x * t.x - x.y * z, x.x * z + x.y * t.x);
+      }
+    } else {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float& a = f[PAIRS ? 2 * i : i];
-    float& b = f[PAIRS ? 2 * i + 1 : V + i];
-    const float c = cs[i].x, s = SIGN * cs[i].y, u = a;
-    a = u * c - b * s;
-    b = u * s + b * c;
+      for (int i = 0; i < V / 2; ++i) {
+        const f2 a = f[i], b = f[V / 2 + i], n = s[i] ^ 0x8000000080000000ull;   // - the sines
+        f[i] = fma2(b, BACK ? s[i] : n, mul2(a, c[i]));
+        f[V / 2 + i] = fma2(a, BACK ? n : s[i], mul2(b, c[i]));
+      }
+    }
   }
-}
+};
 
 template <int V>
-__device__ __forceinline__ void load_gamma(const float* g, int l, int half, float (&w)[2 * V]) {
+__device__ __forceinline__ void load_gamma(const float* g, int l, int half, f2 (&w)[V]) {
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int i = 0; i < V; i += 4) load16(g + k * half + l * V + i, w + k * V + i);
+    for (int i = 0; i < V; i += 4) {
+      const float4 t = __ldg(reinterpret_cast<const float4*>(g + k * half + l * V + i));
+      w[(k * V + i) / 2] = mk2(t.x, t.y);
+      w[(k * V + i) / 2 + 1] = mk2(t.z, t.w);
+    }
 }
 
 // A warp takes a share of one token's heads, HPW at a time and R such steps in flight: the token's
-// angles and the weights stay in registers over them (they are as many bytes as a head's).
+// angles and the weights stay in registers over them (they are as many bytes as a head's). 8192 tokens of 40 heads of
+// 128 in bf16: 30.1 us, 5.7 TB/s; with two steps in flight and three CTAs per SM 39.8, with 16 bytes a lane 34.2.
 template <typename E, int D, bool PAIRS, bool NORM, int R>
-__global__ void __launch_bounds__(kRopeThreads) k_rope_fwd(const __grid_constant__ RopeK p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) k_rope_fwd(const __grid_constant__ RopeK p) {
   grid_dep_sync();
   using S = RopeShape<E, D>;
   constexpr int V = S::V;
@@ -136,56 +161,63 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_fwd(const __grid_constant
   const int part = (int)(item - t * p.parts);
   const int64_t n = __ldg(p.pos + t);
   if (n < 0) return;
-  float2 cs[V];
-  load_turn<E, D, PAIRS>(p, n, l, cs);
+  Turn<E, D, PAIRS> turn;
+  turn.load(p, n, l);
 #pragma unroll 1
   for (int s = 0; s < 2; ++s) {
     const int steps = (p.heads[s] + S::HPW - 1) / S::HPW;
-    float w[2 * V];
+    f2 w[V];
     if (NORM && part < steps) load_gamma<V>(p.gamma[s], l, D / 2, w);
     const E* x = static_cast<const E*>(p.x[s]) + t * p.ld_x[s] + l * V;
     E* y = static_cast<E*>(p.y[s]) + t * p.ld_y[s] + l * V;
 #pragma unroll 1
     for (int k = part; k < steps; k += R * p.parts) {
-      uint4 v[R][2];
+      typename Half<E>::raw v[R][2];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int h = (k + r * p.parts) * S::HPW + sub;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          v[r][j] = h < p.heads[s] ? *reinterpret_cast<const uint4*>(x + h * D + j * (D / 2)) : make_uint4(0, 0, 0, 0);
+          v[r][j] = h < p.heads[s] ? *reinterpret_cast<const typename Half<E>::raw*>(x + h * D + j * (D / 2)) : Half<E>::none();
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int h = (k + r * p.parts) * S::HPW + sub;
-        float f[2 * V];
+        f2 f[V];
         Half<E>::get(v[r][0], f);
-        Half<E>::get(v[r][1], f + V);
+        Half<E>::get(v[r][1], f + V / 2);
         if constexpr (NORM) {
-          float q = 0.f;
+          f2 q = mul2(f[0], f[0]);
 #pragma unroll
-          for (int i = 0; i < 2 * V; ++i) q = fmaf(f[i], f[i], q);
-          const float rstd = 1.f / sqrtf(head_sum<S::LPH>(q) * (1.f / D) + p.eps);
+          for (int i = 1; i < V; ++i) q = fma2(f[i], f[i], q);
+          const float rstd = rsqrtf(head_sum<S::LPH>(sum2(q)) * (1.f / D) + p.eps);
+          const f2 r2 = mk2(rstd, rstd);
 #pragma unroll
-          for (int i = 0; i < 2 * V; ++i) f[i] = f[i] * rstd * w[i];
+          for (int i = 0; i < V; ++i) f[i] = mul2(mul2(f[i], r2), w[i]);
         }
-        turn<V, PAIRS, 1>(f, cs);
+        turn.template apply<false>(f);
         if (h < p.heads[s]) {
-          *reinterpret_cast<uint4*>(y + h * D) = Half<E>::put(f);
-          *reinterpret_cast<uint4*>(y + h * D + D / 2) = Half<E>::put(f + V);
+          *reinterpret_cast<typename Half<E>::raw*>(y + h * D) = Half<E>::put(f);
+          *reinterpret_cast<typename Half<E>::raw*>(y + h * D + D / 2) = Half<E>::put(f + V / 2);
         }
       }
     }
   }
 }
 
-// Persistent over tokens, the query heads of all of them before the key heads, so that a lane keeps one
-// weight vector and one vector of its gradient's sums. The CTA's sums go to part[CTA][q | k], added up in
-// order by k_rope_reduce.
+// Persistent over tokens, the query heads of all of them before the key heads, so that a lane keeps one weight
+// vector and one vector of its gradient's sums. Both sums of a head, x^2 and (gamma h') x, are taken before rstd is
+// known, so that their shuffles run together. The CTA's sums go to part[CTA][q | k], added up in order by
+// k_rope_reduce.
+//
+// 8192 tokens of 40 heads of 128 in bf16: 53 us, 4.8 TB/s, half of it the kernel's own instructions (140 per warp and
+// two heads). Two steps in flight instead of four: 61 us; three CTAs per SM: 69. Rows brought by bulk copies to
+// per-warp rings in shared memory: 66.
 template <typename E, int D, bool PAIRS, bool NORM, int R>
 __global__ void __launch_bounds__(kRopeThreads, 2) k_rope_bwd(const __grid_constant__ RopeK p) {
   grid_dep_sync();
   using S = RopeShape<E, D>;
+  using raw = typename Half<E>::raw;
   constexpr int V = S::V;
   __shared__ float sums[NORM ? kRopeWarps * S::HPW : 1][D];
   const int lane = threadIdx.x & 31, l = lane % S::LPH, sub = lane / S::LPH, warp = threadIdx.x >> 5;
@@ -193,9 +225,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) k_rope_bwd(const __grid_const
 #pragma unroll 1
   for (int s = 0; s < 2; ++s) {
     const int steps = (p.heads[s] + S::HPW - 1) / S::HPW;
-    float w[2 * V], dg[2 * V];
+    f2 w[V], dg[V];
 #pragma unroll
-    for (int i = 0; i < 2 * V; ++i) dg[i] = 0.f;
+    for (int i = 0; i < V; ++i) dg[i] = mk2(0.f, 0.f);
     if (NORM && steps > 0) load_gamma<V>(p.gamma[s], l, D / 2, w);
 #pragma unroll 1
     for (int64_t item = (int64_t)blockIdx.x * kRopeWarps + warp; item < items; item += step) {
@@ -203,54 +235,56 @@ __global__ void __launch_bounds__(kRopeThreads, 2) k_rope_bwd(const __grid_const
       const int part = (int)(item - t * p.parts);
       const int64_t n = __ldg(p.pos + t);
       if (n < 0 || part >= steps) continue;
-      float2 cs[V];
-      load_turn<E, D, PAIRS>(p, n, l, cs);
+      Turn<E, D, PAIRS> turn;
+      turn.load(p, n, l);
       const E* x = static_cast<const E*>(p.x[s]) + t * p.ld_x[s] + l * V;
       E* dx = static_cast<E*>(p.y[s]) + t * p.ld_x[s] + l * V;
       const E* dy = static_cast<const E*>(p.dy[s]) + t * p.ld_y[s] + l * V;
 #pragma unroll 1
       for (int k = part; k < steps; k += R * p.parts) {
-        uint4 a[R][2], b[R][2];
+        raw a[R][2], b[R][2];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const int h = (k + r * p.parts) * S::HPW + sub;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const bool in = h < p.heads[s];
-            b[r][j] = in ? *reinterpret_cast<const uint4*>(dy + h * D + j * (D / 2)) : make_uint4(0, 0, 0, 0);
-            if (NORM) a[r][j] = in ? *reinterpret_cast<const uint4*>(x + h * D + j * (D / 2)) : make_uint4(0, 0, 0, 0);
+            b[r][j] = in ? *reinterpret_cast<const raw*>(dy + h * D + j * (D / 2)) : Half<E>::none();
+            if (NORM) a[r][j] = in ? *reinterpret_cast<const raw*>(x + h * D + j * (D / 2)) : Half<E>::none();
           }
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const int h = (k + r * p.parts) * S::HPW + sub;
-          float g[2 * V];
+          const bool in = h < p.heads[s];
+          f2 g[V];
           Half<E>::get(b[r][0], g);
-          Half<E>::get(b[r][1], g + V);
-          turn<V, PAIRS, -1>(g, cs);
+          Half<E>::get(b[r][1], g + V / 2);
+          turn.template apply<true>(g);
           if constexpr (NORM) {
-            float f[2 * V];
+            f2 f[V];
             Half<E>::get(a[r][0], f);
-            Half<E>::get(a[r][1], f + V);
-            float q = 0.f, z = 0.f;
+            Half<E>::get(a[r][1], f + V / 2);
+            f2 q = mul2(f[0], f[0]), z = mul2(mul2(g[0], w[0]), f[0]);
 #pragma unroll
-            for (int i = 0; i < 2 * V; ++i) q = fmaf(f[i], f[i], q);
-            const float rstd = 1.f / sqrtf(head_sum<S::LPH>(q) * (1.f / D) + p.eps);
-            const bool in = h < p.heads[s];   // (a NaN angle times a missing head's zeros is none of a sum's)
-#pragma unroll
-            for (int i = 0; i < 2 * V; ++i) {
-              f[i] *= rstd;
-              if (in) dg[i] = fmaf(g[i], f[i], dg[i]);
-              g[i] *= w[i];
-              z = fmaf(g[i], f[i], z);
+            for (int i = 1; i < V; ++i) {
+              q = fma2(f[i], f[i], q);
+              z = fma2(mul2(g[i], w[i]), f[i], z);
             }
-            z = head_sum<S::LPH>(z) * (1.f / D);
+            const float qs = head_sum<S::LPH>(sum2(q)), zs = head_sum<S::LPH>(sum2(z));
+            const float rstd = rsqrtf(qs * (1.f / D) + p.eps);
+            const float m = -rstd * zs * (1.f / D);   // - (sum gamma h' xhat) / dim
+            const f2 r2 = mk2(rstd, rstd), m2 = mk2(m, m);
 #pragma unroll
-            for (int i = 0; i < 2 * V; ++i) g[i] = (g[i] - f[i] * z) * rstd;
+            for (int i = 0; i < V; ++i) {
+              f[i] = mul2(f[i], r2);
+              if (in) dg[i] = fma2(g[i], f[i], dg[i]);   // (a NaN angle times a missing head's zeros is none of a sum's)
+              g[i] = mul2(fma2(f[i], m2, mul2(g[i], w[i])), r2);
+            }
           }
-          if (h < p.heads[s]) {
-            *reinterpret_cast<uint4*>(dx + h * D) = Half<E>::put(g);
-            *reinterpret_cast<uint4*>(dx + h * D + D / 2) = Half<E>::put(g + V);
+          if (in) {
+            *reinterpret_cast<raw*>(dx + h * D) = Half<E>::put(g);
+            *reinterpret_cast<raw*>(dx + h * D + D / 2) = Half<E>::put(g + V / 2);
           }
         }
       }
@@ -258,9 +292,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) k_rope_bwd(const __grid_const
     if constexpr (NORM) {
       __syncthreads();   // the sums of the query heads have been read
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i) sums[warp * S::HPW + sub][k * (D / 2) + l * V + i] = dg[k * V + i];
+      for (int i = 0; i < V; ++i)
+        *reinterpret_cast<float2*>(&sums[warp * S::HPW + sub][2 * i / V * (D / 2) + l * V + 2 * i % V]) = un2(dg[i]);
       __syncthreads();
       for (int c = threadIdx.x; c < D; c += kRopeThreads) {
         float v = 0.f;
@@ -272,19 +305,26 @@ __global__ void __launch_bounds__(kRopeThreads, 2) k_rope_bwd(const __grid_const
   }
 }
 
-// dgamma[c] += sum over the CTAs, interleaved runs of CTAs in order, then the runs in a fixed tree.
+// dgamma[c] += sum over the CTAs: interleaved runs of CTAs in order, a run's partials all under way at once, then
+// the runs in a fixed tree.
 constexpr int kRopeRuns = 32;
 __global__ void __launch_bounds__(32 * kRopeRuns) k_rope_reduce(const float* __restrict__ part, int n, int D,
                                                                 float* dgq, float* dgk) {
   grid_dep_sync();
+  constexpr int kRun = (kRopeMostCtas + kRopeRuns - 1) / kRopeRuns;
   __shared__ float sh[kRopeRuns][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   float* dst = blockIdx.y ? dgk : dgq;
   if (!dst) return;
   const float* src = part + (int64_t)blockIdx.y * D + blockIdx.x * 32;
-  float v = 0.f;
-#pragma unroll 4
-  for (int i = ty; i < n; i += kRopeRuns) v += __ldcg(src + (int64_t)i * 2 * D + tx);
+  float a[kRun], v = 0.f;
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) {
+    const int i = ty + k * kRopeRuns;
+    a[k] = i < n ? __ldcg(src + (int64_t)i * 2 * D + tx) : 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) v += a[k];
   sh[ty][tx] = v;
   __syncthreads();
   v = sh[tx][ty];   // warp ty: the runs of column ty
@@ -302,6 +342,10 @@ __global__ void k_rope_table(int64_t n_pos, int half, const double* __restrict__
   sincos((double)n * inv_freq[i - n * half], &s, &c);
   table[i] = make_float2((float)c, (float)s);
 }
+
+// Steps of a warp in flight: 64 bytes of each tensor a lane.
+template <typename E>
+constexpr int kFlight = sizeof(E) == 2 ? 4 : 2;
 
 // Warps that share a token: one per token where the tokens fill the SMs with warps, as many as the
 // token has steps where there are few (one decoded token is bound by latency).
@@ -332,9 +376,9 @@ cudaError_t rope_launch(const RopeArgs& a, bool bwd, cudaStream_t st) {
   const RopeK k = rope_args(a, rope_parts(a, S::HPW, sms));
   const int64_t blocks = (a.T * k.parts + kRopeWarps - 1) / kRopeWarps;
   prof_begin(0, st);
-  if (!bwd) return launch_kernel(k_rope_fwd<E, D, PAIRS, NORM, 2>, (unsigned)blocks, kRopeThreads, 0, st, k);
+  if (!bwd) return launch_kernel(k_rope_fwd<E, D, PAIRS, NORM, kFlight<E>>, (unsigned)blocks, kRopeThreads, 0, st, k);
   const unsigned grid = (unsigned)(blocks < kRopeMostCtas ? blocks : kRopeMostCtas);
-  cudaError_t e = launch_kernel(k_rope_bwd<E, D, PAIRS, NORM, 2>, grid, kRopeThreads, 0, st, k);
+  cudaError_t e = launch_kernel(k_rope_bwd<E, D, PAIRS, NORM, kFlight<E>>, grid, kRopeThreads, 0, st, k);
   if (e != cudaSuccess || !NORM || (!a.dgamma[0] && !a.dgamma[1])) return e;
   prof_begin(0, st);
   return launch_kernel(k_rope_reduce, dim3(D / 32, 2), 32 * kRopeRuns, 0, st, (const float*)a.part, (int)grid, D,

@@ -119,7 +119,7 @@ class Heads:
 
 
 SHAPES = [(1, 1, 1, 64), (1, 32, 8, 128), (3, 5, 3, 64), (7, 4, 0, 128), (33, 3, 1, 256), (130, 32, 4, 64), (257, 9, 9, 128),
-          (2600, 6, 2, 128), (3001, 2, 1, 64)]
+          (2600, 6, 2, 128), (3001, 2, 1, 64), (1500, 33, 5, 64), (5000, 1, 0, 256), (700, 40, 40, 128)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -139,11 +139,11 @@ def test_forward_and_backward(L, shape, dtype, pairs, norm, fused):
     assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
-@pytest.mark.parametrize("norm", [False, True])
-def test_padding_and_positions_past_the_table(L, norm):
+@pytest.mark.parametrize("norm,times", [(False, 40), (True, 40), (False, 900), (True, 900)])
+def test_padding_and_positions_past_the_table(L, norm, times):
     """Padding rows, which may hold anything, are left as they were and add to no gradient; a position past
     the table gives NaN there."""
-    pos = [4, -1, 499, 0, -7, 499, 20] * 40
+    pos = [4, -1, 499, 0, -7, 499, 20] * times
     h = Heads(L, len(pos), 6, 2, 128, norm=norm, seed=2, pos=pos)
     pad = h.pos < 0
     for x in (h.q, h.k, h.dyq, h.dyk):
@@ -165,10 +165,11 @@ def test_padding_and_positions_past_the_table(L, norm):
         assert bool(torch.isnan(h.dgq).all()) and bool(torch.isnan(h.dgk).all())
 
 
+@pytest.mark.parametrize("T", [77, 3000])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_in_place(L, dtype):
+def test_in_place(L, dtype, T):
     """Outputs over inputs of the same strides: y over x, dx over dy."""
-    h = Heads(L, 77, 8, 2, 128, dtype=dtype, seed=5)
+    h = Heads(L, T, 8, 2, 128, dtype=dtype, seed=5)
     h.forward()
     h.backward()
     q, k, dyq, dyk = h.q.clone(), h.k.clone(), h.dyq.clone(), h.dyk.clone()
