@@ -582,7 +582,7 @@ def lora_rope_table(n_pos: int, head_dim: int, inv_freq, table, stream=None, che
 def lora_rope_forward(d: lora_rope_desc, T: int, Q, K, gamma_q, gamma_k, pos, table, n_pos: int, YQ,
                       YK, stream=None, check=True):
     """Norm of each query and key head (with weights) and rotation by position."""
-    st = _lib.lora_rope_forward(C.byref(d), T, _ptr(Q), _ptr(K), _ptr(gamma_q), _ptr(gamma_k),
+    st = _lib.lora_rope_forward(d, T, _ptr(Q), _ptr(K), _ptr(gamma_q), _ptr(gamma_k),
                                 _ptr(pos), _ptr(table), n_pos, _ptr(YQ), _ptr(YK), _stream(stream))
     return _check(st, "lora_rope_forward") if check else st
 
@@ -595,7 +595,7 @@ def lora_rope_backward(d: lora_rope_desc, T: int, Q, K, gamma_q, gamma_k, pos, t
                        dYQ, dYK, dQ, dK, dgamma_q, dgamma_k, ws, ws_bytes: Optional[int] = None,
                        stream=None, check=True):
     """dQ, dK, dgamma_q += and dgamma_k += from the forward's inputs."""
-    st = _lib.lora_rope_backward(C.byref(d), T, _ptr(Q), _ptr(K), _ptr(gamma_q), _ptr(gamma_k),
+    st = _lib.lora_rope_backward(d, T, _ptr(Q), _ptr(K), _ptr(gamma_q), _ptr(gamma_k),
                                  _ptr(pos), _ptr(table), n_pos, _ptr(dYQ), _ptr(dYK), _ptr(dQ),
                                  _ptr(dK), _ptr(dgamma_q), _ptr(dgamma_k), _ptr(ws),
                                  _nbytes(ws, ws_bytes), _stream(stream))
@@ -625,7 +625,7 @@ def lora_attn_plan_build(T: int, n_seq: int, seq_start, plan, plan_bytes: Option
 def lora_attn_forward(d: lora_attn_desc, T: int, n_seq: int, plan, Q, K, V, O, lse, stream=None,
                       check=True):
     """Causal attention over packed sequences, and the scores' log sums."""
-    st = _lib.lora_attn_forward(C.byref(d), T, n_seq, _ptr(plan), _ptr(Q), _ptr(K), _ptr(V), _ptr(O),
+    st = _lib.lora_attn_forward(d, T, n_seq, _ptr(plan), _ptr(Q), _ptr(K), _ptr(V), _ptr(O),
                                 _ptr(lse), _stream(stream))
     return _check(st, "lora_attn_forward") if check else st
 
@@ -637,7 +637,7 @@ def lora_attn_backward_workspace_size(d: lora_attn_desc, T: int) -> int:
 def lora_attn_backward(d: lora_attn_desc, T: int, n_seq: int, plan, Q, K, V, O, lse, dO, dQ, dK, dV,
                        ws, ws_bytes: Optional[int] = None, stream=None, check=True):
     """dQ, dK and dV from the forward's inputs, its output and log sums."""
-    st = _lib.lora_attn_backward(C.byref(d), T, n_seq, _ptr(plan), _ptr(Q), _ptr(K), _ptr(V),
+    st = _lib.lora_attn_backward(d, T, n_seq, _ptr(plan), _ptr(Q), _ptr(K), _ptr(V),
                                  _ptr(O), _ptr(lse), _ptr(dO), _ptr(dQ), _ptr(dK), _ptr(dV),
                                  _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream))
     return _check(st, "lora_attn_backward") if check else st
