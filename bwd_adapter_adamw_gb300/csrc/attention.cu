@@ -132,8 +132,9 @@ constexpr float kRescale = 8.f;   // growth of a row's maximum, in powers of two
 template <int D>
 struct FwdCfg {
   static constexpr int kTile = Tile<D>::kBytes;
-  static constexpr int kStages = D == 128 ? 5 : 8;   // K and V tiles in flight or in use
-  static constexpr int kSmem = (2 + kStages) * kTile + 1024 /*barriers*/ + 1024 /*alignment*/;
+  static constexpr int kStages = D == 128 ? 4 : 8;   // K and V tiles in flight or in use
+  static constexpr int kStage = 32 * 64 * 2;         // a warp's rows on their way out, 64 columns at a time
+  static constexpr int kSmem = (2 + kStages) * kTile + 8 * kStage + 1024 /*barriers*/ + 1024 /*alignment*/;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t kIdS = idesc(kFmtBF16, 128, 128);
   static constexpr uint32_t kIdO = idesc(kFmtBF16, 128, D, false, true);
@@ -165,7 +166,8 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sq = base;
   uint8_t* ring = base + 2 * C::kTile;
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + ST * C::kTile);
+  uint8_t* stages = ring + ST * C::kTile;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stages + 8 * C::kStage);
   uint64_t* empty = full + ST;
   uint64_t* q_full = empty + ST;     // [2]
   uint64_t* q_empty = q_full + 2;    // [2] the last S of a tile is complete
@@ -400,22 +402,13 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
       no += n;
       if (!ok || !(ok = warp_wait(&o_full[s], (no - 1) & 1u, 4u, p.err, p.limit))) break;
       fence_after();
-      const int row = pr.qi(s) * kRows + r;
-      const float inv = 1.f / l;
-      const int64_t at = (int64_t)t.row0 + row;
+      const int row = pr.qi(s) * kRows + r, row0 = row - lane;
+      const int64_t at = (int64_t)t.row0 + row0;
       __nv_bfloat16* out = p.O + at * p.ld_o + (int64_t)pr.h(s) * D;
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        float v[32];
-        tmem_ld32(to + 32 * k, v);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= inv;
-        if (row < t.len) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) store8(out + 32 * k + 8 * i, v + 8 * i);
-        }
-      }
-      if (row < t.len) p.lse[(int64_t)pr.h(s) * p.T + at] = (m + log2f(l)) * kLn2;
+      for (int k = 0; k < D / 64; ++k)
+        store_rows<64>(stages + warp * C::kStage, to + 64 * k, 1.f / l, out + 64 * k, p.ld_o, t.len - row0, lane);
+      if (row < t.len) p.lse[(int64_t)pr.h(s) * p.T + at + lane] = (m + log2f(l)) * kLn2;
       fence_before();   // (O has been read before the next item's first P arrives)
     }
     fence_before();

@@ -77,22 +77,6 @@ struct BwdK {
   unsigned long long limit;
 };
 
-// A row of `N` columns of tensor memory from `col`, scaled, to bf16 at `out`.
-template <int N>
-__device__ __forceinline__ void store_row(uint32_t col, float f, __nv_bfloat16* out, bool live) {
-#pragma unroll
-  for (int k = 0; k < N / 32; ++k) {
-    float v[32];
-    tmem_ld32(col + 32 * k, v);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= f;
-    if (live) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) store8(out + 32 * k + 8 * i, v + 8 * i);
-    }
-  }
-}
-
 // ---- dV and dK -----------------------------------------------------------------------------
 template <int D>
 struct DkvCfg {
@@ -135,7 +119,7 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
   uint64_t* k_full = do_empty + C::kDo;
   uint64_t* k_empty = k_full + 1;    // the item's last S is complete
   uint64_t* v_full = k_empty + 1;
-  uint64_t* v_empty = v_full + 1;    // the item's last dP is complete
+  uint64_t* v_empty = v_full + 1;    // the item's sums have left through V's place
   uint64_t* s_full = v_empty + 1;
   uint64_t* p_full = s_full + 1;     // P^T is in place
   uint64_t* dp_full = p_full + 1;
@@ -170,7 +154,7 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
     mbar_init(k_full, 1);
     mbar_init(k_empty, 1);
     mbar_init(v_full, 1);
-    mbar_init(v_empty, 1);
+    mbar_init(v_empty, kComputeWarps);
     mbar_init(s_full, 1);
     mbar_init(p_full, kComputeWarps);
     mbar_init(dp_full, 1);
@@ -307,7 +291,6 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
           if (!(ok = (it > 0 || wait(v_full, i)) && do_in(g))) break;
           Tl::mma_nt(tp, av, do_at(g), C::kIdS, one);
           commit(dp_full, one);
-          if (it + 1 == sp.n) commit(v_empty, one);
         }
       }
       --g;   // (n + 1 rounds)
@@ -444,11 +427,18 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
             *reinterpret_cast<float4*>(sum_at<D>(tile, r, c0 / 4 + 8 * k + c)) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
         }
       } else {
-        const int64_t at = (int64_t)t.row0 + row;
-        if (w < 2)
-          store_row<D / 2>(lanes + C::kDv + c0, 1.f, p.dV + at * p.ld_v + (int64_t)hk * D + c0, row < t.len);
-        else
-          store_row<D / 2>(lanes + C::kDk + c0, p.scale, p.dK + at * p.ld_k + (int64_t)hk * D + c0, row < t.len);
+        // through V's place, whose products are complete
+        const int row0 = row - lane;
+        const int64_t at = (int64_t)t.row0 + row0, ld = w < 2 ? p.ld_v : p.ld_k;
+        __nv_bfloat16* out = (w < 2 ? p.dV : p.dK) + at * ld + (int64_t)hk * D + c0;
+        const uint32_t col = lanes + (w < 2 ? C::kDv : C::kDk) + c0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          store_rows<D / 4>(sv + warp * (C::kTile / kComputeWarps), col + k * (D / 4), w < 2 ? 1.f : p.scale, out + k * (D / 4), ld,
+                            t.len - row0, lane);
+        fence_async();   // (the reads come before the next copy, which is of another proxy)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_empty);
       }
       fence_before();   // (the sums have been read before the next item's first P arrives)
     }
@@ -524,7 +514,7 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
   uint64_t* q_full = v_empty + C::kV;   // [2]
   uint64_t* q_empty = q_full + 2;       // [2] the last S of a tile is complete
   uint64_t* do_full = q_empty + 2;      // [2]
-  uint64_t* do_empty = do_full + 2;     // [2] the last dP of a tile is complete
+  uint64_t* do_empty = do_full + 2;     // [2] dQ of a tile has left through dO's place
   uint64_t* s_full = do_empty + 2;      // [2]
   uint64_t* s_read = s_full + 2;        // [2] S is in registers
   uint64_t* dp_full = s_read + 2;       // [2]
@@ -550,7 +540,7 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
       mbar_init(&do_full[s], 1);
-      mbar_init(&do_empty[s], 1);
+      mbar_init(&do_empty[s], 4);
       mbar_init(&s_full[s], 1);
       mbar_init(&s_read[s], 4);
       mbar_init(&dp_full[s], 1);
@@ -675,7 +665,6 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
           if (!(ok = wait(&s_read[s], s ? c1 : c0))) break;
           Tl::mma_nt(tmem + C::kX + 128 * s, ado + s * C::kTile, av + (uint32_t)(g % C::kV) * C::kTile, C::kIdS, one);
           commit(&dp_full[s], one);
-          if (j + 1 == pr.n(s)) commit(&do_empty[s], one);
         }
         if (!ok) break;
         commit(&v_empty[g % C::kV], one);
@@ -778,7 +767,14 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
       }
       if (!ok || !(ok = warp_wait(&dq_full[s], i++ & 1u, 4u, p.err, p.limit))) break;
       fence_after();
-      store_row<D>(tq, p.scale, p.dQ + at * p.ld_q + (int64_t)h * D, live);
+      // through dO's place, whose products are complete
+      __nv_bfloat16* out = p.dQ + (at - lane) * p.ld_q + (int64_t)h * D;
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k)
+        store_rows<64>(sdo + s * C::kTile + (warp & 3) * 4096, tq + 64 * k, p.scale, out + 64 * k, p.ld_q, t.len - (row - lane), lane);
+      fence_async();   // (the reads come before the next copy, which is of another proxy)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&do_empty[s]);
       fence_before();   // (dQ has been read before the next item's first dS arrives)
     }
     fence_before();

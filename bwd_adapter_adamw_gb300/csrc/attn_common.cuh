@@ -270,6 +270,39 @@ struct Pair {
   __device__ int n(int s) const { return s ? n1 : n0; }
 };
 
+// 32 lanes' COLS columns of tensor memory, scaled by each lane's f, as bf16 rows of `out` (row 0, first column; ld
+// elements apart, `live` rows of them): turned in `stage`, the warp's own 32 x COLS bf16 of shared memory, so that a
+// store covers whole runs of a row. A lane's row written piece by piece, 32 rows to a store, filled the load and
+// store queue for 3500 cycles per tile and held up the next item's first loads and waits for 2300 more.
+template <int COLS>
+__device__ __forceinline__ void store_rows(uint8_t* stage, uint32_t taddr, float f, __nv_bfloat16* out, int64_t ld,
+                                           int live, int lane) {
+  constexpr int NC = COLS / 8, RPI = 32 / NC;   // 16-byte pieces of a row, rows of a store
+  static_assert(COLS % 16 == 0 && 32 % NC == 0, "columns");
+#pragma unroll
+  for (int k = 0; k < COLS / 16; ++k) {
+    float v[16];
+    tmem_ld16(taddr + 16 * k, v);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint4 u;
+      u.x = pack_bf16(v[8 * c] * f, v[8 * c + 1] * f);
+      u.y = pack_bf16(v[8 * c + 2] * f, v[8 * c + 3] * f);
+      u.z = pack_bf16(v[8 * c + 4] * f, v[8 * c + 5] * f);
+      u.w = pack_bf16(v[8 * c + 6] * f, v[8 * c + 7] * f);
+      *reinterpret_cast<uint4*>(stage + lane * (COLS * 2) + (((2 * k + c) ^ (lane & (NC - 1))) << 4)) = u;
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int row = i * RPI + lane / NC, c = lane % NC;
+    const uint4 u = *reinterpret_cast<const uint4*>(stage + row * (COLS * 2) + ((c ^ (row & (NC - 1))) << 4));
+    if (row < live) *reinterpret_cast<uint4*>(out + row * ld + 8 * c) = u;
+  }
+  __syncwarp();
+}
+
 // Bounded wait of a whole warp: the same answer in every lane. Under a bound below the default (a test's) an
 // attempt that succeeds too late counts as failed. Short, since the issuing warp's loop runs through it several
 // times for each tile.
