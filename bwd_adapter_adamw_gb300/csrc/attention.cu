@@ -339,10 +339,20 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
 #pragma unroll
         for (int k = 0; k < 4; ++k) tmem_ld32_nw(ts + 32 * k, x + 32 * k);
         tmem_wait_ld_n<128>(x);
-        if (j == n - 1) {   // the tile on the diagonal: keys up to the row's own
+        if (j == n - 1) {   // the tile on the diagonal: keys up to the row's own, 32 at a time beside the warp's rows
 #pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k > r) x[k] = 0xff800000u;
+          for (int b = 0; b < 4; ++b) {
+            int ahead = b - (warp & 3);   // (hidden from the compiler, which would index x by the warp)
+            asm volatile("" : "+r"(ahead));
+            if (ahead == 0) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (k > lane) x[32 * b + k] = 0xff800000u;
+            } else if (ahead > 0) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[32 * b + k] = 0xff800000u;
+            }
+          }
         }
         float mx[4];
 #pragma unroll
@@ -405,7 +415,7 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
       const int row = pr.qi(s) * kRows + r, row0 = row - lane;
       const int64_t at = (int64_t)t.row0 + row0;
       __nv_bfloat16* out = p.O + at * p.ld_o + (int64_t)pr.h(s) * D;
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < D / 64; ++k)
         store_rows<64>(stages + warp * C::kStage, to + 64 * k, 1.f / l, out + 64 * k, p.ld_o, t.len - row0, lane);
       if (row < t.len) p.lse[(int64_t)pr.h(s) * p.T + at + lane] = (m + log2f(l)) * kLn2;

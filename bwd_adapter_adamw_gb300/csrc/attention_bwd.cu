@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
     // ---- elementwise: warpgroup w has queries 32 w .. 32 w + 31. A thread has four keys and eight queries of
     // each warp's 32 x 32: a whole key's 32 queries would want all their statistics, 16 reads of shared memory
     // per tile, which the products keep as busy as themselves.
-    const int w = warp >> 2, r = threadIdx.x & 127, q = lane & 3, key = (warp & 3) * 32 + (lane >> 2);
+    const int w = warp >> 2, r = threadIdx.x & 127, q = lane & 3;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = lanes + C::kS + kCols * w, tp = lanes + C::kDp + kCols * w;
     const f2 c2 = mk2(p.c, p.c);
@@ -370,10 +370,11 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
           x[2 * k] = __float_as_uint(exp2_(a.x));
           x[2 * k + 1] = __float_as_uint(exp2_(a.y));
         }
-        if (qi == sp.j) {   // the tile on the diagonal: queries from the key's own on
+        if (qi == sp.j && w <= (warp & 3)) {   // the tile on the diagonal: queries from the key's own on
+          const int key = w == (warp & 3) ? lane >> 2 : 32;   // (none beside keys behind all of the warpgroup's queries)
 #pragma unroll
           for (int k = 0; k < kCols; ++k)
-            if (kCols * w + 8 * (k / 4 % 4) + 2 * q + (k & 1) < key + 8 * (k / 2 % 2) + 16 * (k / 16)) x[k] = 0u;
+            if (8 * (k / 4 % 4) + 2 * q + (k & 1) < key + 8 * (k / 2 % 2) + 16 * (k / 16)) x[k] = 0u;
         }
 #pragma unroll
         for (int k = 0; k < kCols / 2; ++k) u[k] = pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
@@ -747,12 +748,16 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
                                       add2(mk2(__uint_as_float(yk[2 * e]), __uint_as_float(yk[2 * e + 1])), d2)));
             u[e] = pack_bf16(a.x, a.y);
           }
-          if (j == n - 1) {   // the tile on the diagonal: keys up to the query's own
+          if (j == n - 1) {   // the tile on the diagonal: keys up to the query's own, 32 at a time beside the warp's rows
+            if (k == (warp & 3)) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int at2 = 32 * k + 2 * e;
-              if (at2 > r) u[e] = 0u;
-              else if (at2 + 1 > r) u[e] &= 0xffffu;
+              for (int e = 0; e < 16; ++e) {
+                if (2 * e > lane) u[e] = 0u;
+                else if (2 * e + 1 > lane) u[e] &= 0xffffu;
+              }
+            } else if (k > (warp & 3)) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) u[e] = 0u;
             }
           }
           tmem_st16(tx + 16 * k, u);
@@ -769,7 +774,7 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
       fence_after();
       // through dO's place, whose products are complete
       __nv_bfloat16* out = p.dQ + (at - lane) * p.ld_q + (int64_t)h * D;
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < D / 64; ++k)
         store_rows<64>(sdo + s * C::kTile + (warp & 3) * 4096, tq + 64 * k, p.scale, out + 64 * k, p.ld_q, t.len - (row - lane), lane);
       fence_async();   // (the reads come before the next copy, which is of another proxy)

@@ -279,19 +279,24 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, uint32_t taddr, float
                                            int live, int lane) {
   constexpr int NC = COLS / 8, RPI = 32 / NC;   // 16-byte pieces of a row, rows of a store
   static_assert(COLS % 16 == 0 && 32 % NC == 0, "columns");
+  uint32_t v[COLS];
+  if constexpr (COLS >= 32) {
 #pragma unroll
-  for (int k = 0; k < COLS / 16; ++k) {
-    float v[16];
-    tmem_ld16(taddr + 16 * k, v);
+    for (int k = 0; k < COLS / 32; ++k) tmem_ld32_nw(taddr + 32 * k, v + 32 * k);
+  } else {
+    tmem_ld16_nw(taddr, v);
+  }
+  tmem_wait_ld_n<COLS>(v);
+  const f2 f2_ = mk2(f, f);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint4 u;
-      u.x = pack_bf16(v[8 * c] * f, v[8 * c + 1] * f);
-      u.y = pack_bf16(v[8 * c + 2] * f, v[8 * c + 3] * f);
-      u.z = pack_bf16(v[8 * c + 4] * f, v[8 * c + 5] * f);
-      u.w = pack_bf16(v[8 * c + 6] * f, v[8 * c + 7] * f);
-      *reinterpret_cast<uint4*>(stage + lane * (COLS * 2) + (((2 * k + c) ^ (lane & (NC - 1))) << 4)) = u;
+  for (int c = 0; c < NC; ++c) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 e = un2(mul2(mk2(__uint_as_float(v[8 * c + 2 * i]), __uint_as_float(v[8 * c + 2 * i + 1])), f2_));
+      u[i] = pack_bf16(e.x, e.y);
     }
+    *reinterpret_cast<uint4*>(stage + lane * (COLS * 2) + ((c ^ (lane & (NC - 1))) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
   }
   __syncwarp();
 #pragma unroll
