@@ -143,7 +143,7 @@ struct FwdCfg {
 };
 
 struct FwdK {
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   const int32_t* count;
   const AttnTile* tiles;
   int32_t groups;        // CTAs of a tile of the list
@@ -414,13 +414,24 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
       fence_after();
       const int row = pr.qi(s) * kRows + r, row0 = row - lane;
       const int64_t at = (int64_t)t.row0 + row0;
-      __nv_bfloat16* out = p.O + at * p.ld_o + (int64_t)pr.h(s) * D;
+      uint8_t* stage = stages + warp * C::kStage;
 #pragma unroll 1
-      for (int k = 0; k < D / 64; ++k)
-        store_rows<64>(stages + warp * C::kStage, to + 64 * k, 1.f / l, out + 64 * k, p.ld_o, t.len - row0, lane);
+      for (int k = 0; k < D / 64; ++k) {
+        uint32_t u[32];
+        read_rows<64>(to + 64 * k, 1.f / l, u);
+        rows_read(lane);   // (what was sent before)
+        stage_rows<64>(stage, u, lane);
+        const int col = pr.h(s) * D + 64 * k;
+        if (t.len - row0 >= 32)
+          send_rows(&p.to, stage, col, at, lane);
+        else   // the rows behind belong to others
+          write_rows<64>(stage, p.O + at * p.ld_o + col, p.ld_o, t.len - row0, lane);
+      }
       if (row < t.len) p.lse[(int64_t)pr.h(s) * p.T + at + lane] = (m + log2f(l)) * kLn2;
       fence_before();   // (O has been read before the next item's first P arrives)
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // rows sent have been written
+    __syncwarp();
     fence_before();
   }
   __syncthreads();
@@ -439,7 +450,7 @@ cudaError_t fwd_launch(const AttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   FwdK k{};
   if (!attn_map(&k.tq, a.Q, a.q_heads * D, a.T, a.ld_q) || !attn_map(&k.tk, a.K, a.kv_heads * D, a.T, a.ld_k) ||
-      !attn_map(&k.tv, a.V, a.kv_heads * D, a.T, a.ld_v))
+      !attn_map(&k.tv, a.V, a.kv_heads * D, a.T, a.ld_v) || !attn_map(&k.to, a.O, a.q_heads * D, a.T, a.ld_o, 32))
     return cudaErrorInvalidValue;
   k.per = a.q_heads / a.kv_heads;
   k.by_heads = k.per % 2 == 0;
@@ -465,9 +476,9 @@ cudaError_t fwd_launch(const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-bool attn_map(CUtensorMap* map, const void* ptr, int64_t cols, int64_t rows, int64_t ld) {
+bool attn_map(CUtensorMap* map, const void* ptr, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
   return make_map_2d(map, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)cols, (uint64_t)rows, (uint64_t)ld, 64,
-                     kRows);
+                     (uint32_t)box_rows);
 }
 
 AttnPlan attn_plan(int64_t T, int32_t n_seq, void* buf) {

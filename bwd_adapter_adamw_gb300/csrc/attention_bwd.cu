@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(256) k_attn_delta(const __nv_bfloat16* __restr
 }
 
 struct BwdK {
-  CUtensorMap tq, tk, tv, tdo;
+  CUtensorMap tq, tk, tv, tdo, tdq;
   const int32_t* count;
   const AttnTile* tiles;
   int32_t heads;         // dK, dV: work items of a tile
@@ -434,9 +434,13 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
         __nv_bfloat16* out = (w < 2 ? p.dV : p.dK) + at * ld + (int64_t)hk * D + c0;
         const uint32_t col = lanes + (w < 2 ? C::kDv : C::kDk) + c0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          store_rows<D / 4>(sv + warp * (C::kTile / kComputeWarps), col + k * (D / 4), w < 2 ? 1.f : p.scale, out + k * (D / 4), ld,
-                            t.len - row0, lane);
+        for (int k = 0; k < 2; ++k) {
+          uint8_t* stage = sv + warp * (C::kTile / kComputeWarps);
+          uint32_t u[D / 8];
+          read_rows<D / 4>(col + k * (D / 4), w < 2 ? 1.f : p.scale, u);
+          stage_rows<D / 4>(stage, u, lane);
+          write_rows<D / 4>(stage, out + k * (D / 4), ld, t.len - row0, lane);
+        }
         fence_async();   // (the reads come before the next copy, which is of another proxy)
         __syncwarp();
         if (lane == 0) mbar_arrive(v_empty);
@@ -773,15 +777,27 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
       if (!ok || !(ok = warp_wait(&dq_full[s], i++ & 1u, 4u, p.err, p.limit))) break;
       fence_after();
       // through dO's place, whose products are complete
-      __nv_bfloat16* out = p.dQ + (at - lane) * p.ld_q + (int64_t)h * D;
+      const int row0 = row - lane;
+      const bool whole = t.len - row0 >= 32;
 #pragma unroll 1
-      for (int k = 0; k < D / 64; ++k)
-        store_rows<64>(sdo + s * C::kTile + (warp & 3) * 4096, tq + 64 * k, p.scale, out + 64 * k, p.ld_q, t.len - (row - lane), lane);
+      for (int k = 0; k < D / 64; ++k) {
+        uint8_t* stage = sdo + s * C::kTile + ((warp & 3) * (D / 64) + k) * 4096;
+        uint32_t u[32];
+        read_rows<64>(tq + 64 * k, p.scale, u);
+        stage_rows<64>(stage, u, lane);
+        if (whole)
+          send_rows(&p.tdq, stage, h * D + 64 * k, at - lane, lane);
+        else   // the rows behind belong to others
+          write_rows<64>(stage, p.dQ + (at - lane) * p.ld_q + (int64_t)h * D + 64 * k, p.ld_q, t.len - row0, lane);
+      }
+      rows_read(lane);
       fence_async();   // (the reads come before the next copy, which is of another proxy)
       __syncwarp();
       if (lane == 0) mbar_arrive(&do_empty[s]);
       fence_before();   // (dQ has been read before the next item's first dS arrives)
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // rows sent have been written
+    __syncwarp();
     fence_before();
   }
   __syncthreads();
@@ -828,7 +844,8 @@ cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   BwdK k{};
   if (!attn_map(&k.tq, a.Q, a.q_heads * D, a.T, a.ld_q) || !attn_map(&k.tk, a.K, a.kv_heads * D, a.T, a.ld_k) ||
-      !attn_map(&k.tv, a.V, a.kv_heads * D, a.T, a.ld_v) || !attn_map(&k.tdo, a.dO, a.q_heads * D, a.T, a.ld_o))
+      !attn_map(&k.tv, a.V, a.kv_heads * D, a.T, a.ld_v) || !attn_map(&k.tdo, a.dO, a.q_heads * D, a.T, a.ld_o) ||
+      !attn_map(&k.tdq, a.dQ, a.q_heads * D, a.T, a.ld_q, 32))
     return cudaErrorInvalidValue;
   k.per = a.q_heads / a.kv_heads;
   k.c = a.scale * kLog2e;

@@ -6,8 +6,8 @@
 
 namespace lora {
 
-// Tensor map of a [rows, cols] bf16 matrix with ld elements from row to row, in boxes of 128 x 64 (attention.cu).
-bool attn_map(CUtensorMap* map, const void* ptr, int64_t cols, int64_t rows, int64_t ld);
+// Tensor map of a [rows, cols] bf16 matrix with ld elements from row to row, in boxes of box_rows x 64 (attention.cu).
+bool attn_map(CUtensorMap* map, const void* ptr, int64_t cols, int64_t rows, int64_t ld, int box_rows = kAttnTile);
 
 namespace attn {
 
@@ -270,15 +270,15 @@ struct Pair {
   __device__ int n(int s) const { return s ? n1 : n0; }
 };
 
-// 32 lanes' COLS columns of tensor memory, scaled by each lane's f, as bf16 rows of `out` (row 0, first column; ld
-// elements apart, `live` rows of them): turned in `stage`, the warp's own 32 x COLS bf16 of shared memory, so that a
-// store covers whole runs of a row. A lane's row written piece by piece, 32 rows to a store, filled the load and
-// store queue for 3500 cycles per tile and held up the next item's first loads and waits for 2300 more.
+// 32 lanes' COLS columns of tensor memory, scaled by each lane's f, as bf16 rows in `stage`, the warp's own
+// 32 x COLS bf16 of shared memory, in the swizzle of a bulk tensor store of that box.
 template <int COLS>
-__device__ __forceinline__ void store_rows(uint8_t* stage, uint32_t taddr, float f, __nv_bfloat16* out, int64_t ld,
-                                           int live, int lane) {
-  constexpr int NC = COLS / 8, RPI = 32 / NC;   // 16-byte pieces of a row, rows of a store
-  static_assert(COLS % 16 == 0 && 32 % NC == 0, "columns");
+__device__ __forceinline__ uint32_t piece_at(int row, int c) {   // byte of 16-byte piece c of a row
+  constexpr int NC = COLS / 8;
+  return row * (COLS * 2) + ((c ^ ((NC == 8 ? row : row >> 1) & (NC - 1))) << 4);
+}
+template <int COLS>
+__device__ __forceinline__ void read_rows(uint32_t taddr, float f, uint32_t (&u)[COLS / 2]) {
   uint32_t v[COLS];
   if constexpr (COLS >= 32) {
 #pragma unroll
@@ -287,24 +287,47 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, uint32_t taddr, float
     tmem_ld16_nw(taddr, v);
   }
   tmem_wait_ld_n<COLS>(v);
-  const f2 f2_ = mk2(f, f);
+  const f2 ff = mk2(f, f);
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 e = un2(mul2(mk2(__uint_as_float(v[8 * c + 2 * i]), __uint_as_float(v[8 * c + 2 * i + 1])), f2_));
-      u[i] = pack_bf16(e.x, e.y);
-    }
-    *reinterpret_cast<uint4*>(stage + lane * (COLS * 2) + ((c ^ (lane & (NC - 1))) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+  for (int i = 0; i < COLS / 2; ++i) {
+    const float2 e = un2(mul2(mk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ff));
+    u[i] = pack_bf16(e.x, e.y);
   }
+}
+template <int COLS>
+__device__ __forceinline__ void stage_rows(uint8_t* stage, const uint32_t (&u)[COLS / 2], int lane) {
+#pragma unroll
+  for (int c = 0; c < COLS / 8; ++c)
+    *reinterpret_cast<uint4*>(stage + piece_at<COLS>(lane, c)) = make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+}
+// The staged rows, `live` of them, to `out` (row 0, first column; ld elements apart), a store covering whole runs
+// of a row. (A lane's row written piece by piece, 32 rows to a store, filled the load and store queue for 3500 cycles
+// per tile and held up the next item's first loads and waits for 2300 more.)
+template <int COLS>
+__device__ __forceinline__ void write_rows(const uint8_t* stage, __nv_bfloat16* out, int64_t ld, int live, int lane) {
+  constexpr int NC = COLS / 8, RPI = 32 / NC;   // 16-byte pieces of a row, rows of a store
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int row = i * RPI + lane / NC, c = lane % NC;
-    const uint4 u = *reinterpret_cast<const uint4*>(stage + row * (COLS * 2) + ((c ^ (row & (NC - 1))) << 4));
+    const uint4 u = *reinterpret_cast<const uint4*>(stage + piece_at<COLS>(row, c));
     if (row < live) *reinterpret_cast<uint4*>(out + row * ld + 8 * c) = u;
   }
+  __syncwarp();
+}
+// The same as a bulk tensor store of all 32 rows, which the warp need not wait for: 8 pairs of a read and a store
+// take it 700 to 1200 cycles.
+__device__ __forceinline__ void send_rows(const CUtensorMap* map, const uint8_t* stage, int col, int64_t row, int lane) {
+  fence_async();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(map, stage, col, (int32_t)row);
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+// Lane 0's bulk stores have read their stages.
+__device__ __forceinline__ void rows_read(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();
 }
 
