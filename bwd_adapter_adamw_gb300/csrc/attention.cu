@@ -13,7 +13,8 @@
 // which bf16 and the fp32 sums hold as well): most rows rescale O once or twice, not with every tile.
 //
 // CTA layout (384 threads): warps 0-3 and 4-7 softmax, rescale and epilogue of tile 0 and 1; warp 8 loads
-// (TMA); warp 9 issues the products (10 and 11 fill their warpgroup, which hands its registers to the softmax).
+// (TMA); warp 9 issues the products; warp 10 zeroes rows behind a sequence (11 fills their warpgroup, which hands
+// its registers to the softmax).
 // Every wait is bounded; a warp whose wait ran out stops, and no later
 // warp sees its part arrive, so that outputs are stored from complete products only.
 #include <new>
@@ -174,15 +175,17 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
   uint64_t* s_full = q_empty + 2;    // [2] S of a tile is complete
   uint64_t* p_full = s_full + 2;     // [2][2] half of a tile's P is in place, O rescaled
   uint64_t* o_full = p_full + 4;     // [2] P V is complete
-  uint64_t* fixed = o_full + 2;      // a tile whose rows are zeroed behind a sequence has landed
-  uint64_t* done = fixed + 1;
+  uint64_t* landed = o_full + 2;     // [ST] see Partial
+  uint64_t* done = landed + ST;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint32_t* ended = tmem_slot + 1;   // see Partial
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&landed[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1);
@@ -192,8 +195,8 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
       mbar_init(&p_full[2 * s + 1], 4);
       mbar_init(&o_full[s], 1);
     }
-    mbar_init(fixed, 1);
     mbar_init(done, 1);
+    *ended = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
   }
@@ -210,7 +213,8 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
   Items items(p.tiles, p.groups, p.count);
   if (warp == 8) {
     // ---- loads: Q of both tiles, then K and V tile by tile ----
-    int g = 0, fixes = 0, nq0 = 0, nq1 = 0;   // tiles of the ring, zeroed ones, of Q
+    int g = 0, nq0 = 0, nq1 = 0;   // tiles of the ring, of Q
+    Partial part;
     bool ok = true;
     while (ok && items.take(t, group)) {
       const Pair pr(t, group, p.by_heads);
@@ -231,32 +235,21 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
         if (g >= ST && !(ok = warp_wait(&empty[s], (uint32_t)(g / ST - 1) & 1u, 1u, p.err, p.limit))) break;
         uint8_t* dst = ring + s * C::kTile;
         const int rows = t.len - kt * kRows;   // of the sequence from here on
-        // The rows behind the sequence are another's or padding: P is zero there, but zero times a NaN or an
-        // infinity is not, so V's are zeroed before the product sees the tile.
-        const bool fix = (j & 1) && rows < kRows;
+        const bool some = (j & 1) && rows < kRows;   // V of the sequence's last rows
         if (lane == 0) {
-          uint64_t* bar = fix ? fixed : &full[s];
+          uint64_t* bar = some ? &landed[s] : &full[s];
           mbar_expect_tx(bar, C::kTile);
           Tl::load(dst, (j & 1) ? &p.tv : &p.tk, bar, kv_col, t.row0 + kt * kRows);
         }
-        if (fix) {
-          ok = __all_sync(0xffffffffu, mbar_wait(fixed, (uint32_t)fixes & 1u, 1u, p.err));
-          ++fixes;
-          if (!ok) {
-            ++g;
-            break;
-          }
-          Tl::zero_rows(dst, rows, lane);
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[s]);
-        }
+        if (some) part.next(s);
       }
     }
     // every copy has landed before the CTA ends
     if (lane == 0) {
+      *static_cast<volatile uint32_t*>(ended) = 1u + part.n;
       if (nq0) mbar_wait(&q_full[0], (uint32_t)(nq0 - 1) & 1u, 1u, p.err);
       if (nq1) mbar_wait(&q_full[1], (uint32_t)(nq1 - 1) & 1u, 1u, p.err);
+      part.drain(landed, ST, p.err);
       for (int k = g > ST ? g - ST : 0; k < g; ++k)
         if (!mbar_wait(&full[k % ST], (uint32_t)(k / ST) & 1u, 1u, p.err)) break;
     }
@@ -319,6 +312,16 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
     commit(done, one);
     mbar_wait(done, 0u, 2u, p.err);
     __syncwarp();
+  } else if (warp == 10) {
+    // ---- zeros behind the sequences, in V ----
+    Partial part;
+    int g = 0;   // tiles of the ring
+    while (items.take(t, group)) {
+      const Pair pr(t, group, p.by_heads);
+      g += 2 * pr.most;
+      const int rows = t.len - (pr.most - 1) * kRows, s = (g - 1) % ST;
+      if (rows < kRows && !part.pass<D>(ring + s * C::kTile, s, rows, landed, full, lane, p.err, ended, part.n)) break;
+    }
   } else if (warp < 8) {
     SplitFwd::compute();
     // ---- softmax and epilogue: thread = row of tile s ----

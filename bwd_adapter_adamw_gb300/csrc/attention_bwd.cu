@@ -21,8 +21,8 @@
 // operand of dS K. S alternates between two buffers, so that the next tile's S runs before this one's dS.
 //
 // CTA layout (640 threads): warps 0-15 elementwise (four warpgroups, 32 columns each) and epilogue, warp 16
-// loads, warp 17 issues the products, warp 18 brings the queries' statistics (k_attn_dkv); as in the forward
-// pass (k_attn_dq). Waits are bounded as there.
+// loads, warp 17 issues the products, warp 18 brings the queries' statistics, warp 19 zeroes rows behind a sequence
+// (k_attn_dkv); as in the forward pass (k_attn_dq). Waits are bounded as there.
 #include "attn_common.cuh"
 
 namespace lora {
@@ -34,7 +34,7 @@ using namespace attn;
 using Sp = SplitBwd;
 constexpr int kGroups = (Sp::kThreads - 128) / 128;   // warpgroups that share a tile's columns
 constexpr int kCols = 128 / kGroups;                  // columns of a thread
-constexpr int kComputeWarps = 4 * kGroups, kLoadWarp = kComputeWarps, kIssueWarp = kLoadWarp + 1, kStatWarp = kLoadWarp + 2;
+constexpr int kComputeWarps = 4 * kGroups, kLoadWarp = kComputeWarps, kIssueWarp = kLoadWarp + 1, kStatWarp = kLoadWarp + 2, kZeroWarp = kLoadWarp + 3;
 
 // ---- delta ---------------------------------------------------------------------------------
 // delta[h, t] = sum do o, D / 8 lanes per head of a token. Bound by memory.
@@ -128,13 +128,14 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
   uint64_t* lse_empty = lse_full + 1;
   uint64_t* delta_full = lse_empty + 1;
   uint64_t* delta_empty = delta_full + 1;
-  uint64_t* fix_q = delta_empty + 1;
-  uint64_t* fix_do = fix_q + 1;
-  uint64_t* all = fix_do + 1;        // both sums of an item are complete
+  uint64_t* landed_q = delta_empty + 1;       // [kQ], [kDo] see Partial
+  uint64_t* landed_do = landed_q + C::kQ;
+  uint64_t* all = landed_do + C::kDo;        // both sums of an item are complete
   uint64_t* done = all + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   uint32_t* complete = tmem_slot + 1;   // CL: this CTA's sums are in shared memory
-  static_assert((2 * (C::kQ + C::kDo) + 16) * 8 + 8 <= C::kBarriers, "barriers");
+  uint32_t* ended = tmem_slot + 2;      // see Partial
+  static_assert((3 * (C::kQ + C::kDo) + 14) * 8 + 12 <= C::kBarriers, "barriers");
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rank = CL ? (int)cluster_ctarank() : 0;
   if constexpr (CL) {   // clusters behind the last item leave before they take tensor memory
@@ -146,10 +147,12 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
     for (int s = 0; s < C::kQ; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
+      mbar_init(&landed_q[s], 1);
     }
     for (int s = 0; s < C::kDo; ++s) {
       mbar_init(&do_full[s], 1);
       mbar_init(&do_empty[s], 1);
+      mbar_init(&landed_do[s], 1);
     }
     mbar_init(k_full, 1);
     mbar_init(k_empty, 1);
@@ -163,11 +166,10 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
     mbar_init(lse_empty, kComputeWarps);
     mbar_init(delta_full, 1);
     mbar_init(delta_empty, kComputeWarps);
-    mbar_init(fix_q, 1);
-    mbar_init(fix_do, 1);
     mbar_init(all, 1);
     mbar_init(done, 1);
     *complete = 1u;
+    *ended = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
   }
@@ -191,24 +193,17 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
   };
   if (warp == kLoadWarp) {
     // ---- loads ----
-    int fixes = 0;                  // of Q and of dO alike
     int nk = 0, nv = 0, nqs = 0, ndo = 0;   // tiles asked for
+    Partial part_q, part_do;
     bool ok = true;
-    // Rows behind the sequence are zeroed: P^T and dS^T are zero there, but zero times a NaN is not.
-    auto fetch = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* fix, int col, int qi) {
-      const int rows = t.len - qi * kRows;
+    auto fetch = [&](uint8_t* tiles, int s, const CUtensorMap* map, uint64_t* full, uint64_t* landed, Partial& part, int col, int qi) {
+      const bool some = t.len - qi * kRows < kRows;   // the sequence's last rows
       if (lane == 0) {
-        uint64_t* bar = rows < kRows ? fix : full;
+        uint64_t* bar = some ? &landed[s] : &full[s];
         mbar_expect_tx(bar, C::kTile);
-        Tl::load(dst, map, bar, col, t.row0 + qi * kRows);
+        Tl::load(tiles + s * C::kTile, map, bar, col, t.row0 + qi * kRows);
       }
-      if (rows >= kRows) return true;
-      if (!__all_sync(0xffffffffu, mbar_wait(fix, (uint32_t)fixes & 1u, 1u, p.err))) return false;
-      Tl::zero_rows(dst, rows, lane);
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full);
-      return true;
+      if (some) part.next(s);
     };
     auto keys = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* empty, int& n, int j) {
       if (n && !warp_wait(empty, (uint32_t)(n - 1) & 1u, 1u, p.err, p.limit)) return false;
@@ -227,12 +222,11 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
         const int a = nqs % C::kQ, b = ndo % C::kDo, col = h * D;
         if (nqs >= C::kQ && !(ok = warp_wait(&q_empty[a], (uint32_t)(nqs / C::kQ - 1) & 1u, 1u, p.err, p.limit))) break;
         ++nqs;
-        if (!(ok = fetch(sq + a * C::kTile, &p.tq, &q_full[a], fix_q, col, qi))) break;
+        fetch(sq, a, &p.tq, q_full, landed_q, part_q, col, qi);
         if (it == 0 && !(ok = keys(sv, &p.tv, v_full, v_empty, nv, sp.j))) break;
         if (ndo >= C::kDo && !(ok = warp_wait(&do_empty[b], (uint32_t)(ndo / C::kDo - 1) & 1u, 1u, p.err, p.limit))) break;
         ++ndo;
-        if (!(ok = fetch(sdo + b * C::kTile, &p.tdo, &do_full[b], fix_do, col, qi))) break;
-        if (t.len - qi * kRows < kRows) ++fixes;
+        fetch(sdo, b, &p.tdo, do_full, landed_do, part_do, col, qi);
         if (++qi == sp.nb) {
           qi = sp.j;
           ++h;
@@ -240,8 +234,11 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
       }
     }
     if (lane == 0) {   // every copy has landed before the CTA ends
+      *static_cast<volatile uint32_t*>(ended) = 1u + part_q.n + part_do.n;
       if (nk) mbar_wait(k_full, (uint32_t)(nk - 1) & 1u, 1u, p.err);
       if (nv) mbar_wait(v_full, (uint32_t)(nv - 1) & 1u, 1u, p.err);
+      part_q.drain(landed_q, C::kQ, p.err);
+      part_do.drain(landed_do, C::kDo, p.err);
       for (int k = nqs > C::kQ ? nqs - C::kQ : 0; k < nqs; ++k)
         if (!mbar_wait(&q_full[k % C::kQ], (uint32_t)(k / C::kQ) & 1u, 1u, p.err)) break;
       for (int k = ndo > C::kDo ? ndo - C::kDo : 0; k < ndo; ++k)
@@ -336,6 +333,22 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
         }
         read(it + 1 < sp.n);
       }
+    }
+  } else if (warp == kZeroWarp) {
+    // ---- zeros behind the sequences, in Q and dO ----
+    Partial part_q, part_do;
+    int g = 0;   // query tiles so far
+    bool ok = true;
+    while (ok && items.take(t, hk)) {
+      const Span sp(t, hk, p.per, mine, rank);
+      const int rows = t.len - (sp.nb - 1) * kRows;
+      if (rows < kRows)
+        for (int it = sp.nq - 1; it < sp.n && ok; it += sp.nq) {   // the last query tile of each head
+          const int a = (g + it) % C::kQ, b = (g + it) % C::kDo;
+          ok = part_q.pass<D>(sq + a * C::kTile, a, rows, landed_q, q_full, lane, p.err, ended, part_q.n + part_do.n) &&
+               part_do.pass<D>(sdo + b * C::kTile, b, rows, landed_do, do_full, lane, p.err, ended, part_q.n + part_do.n);
+        }
+      g += sp.n;
     }
   } else if (warp < kComputeWarps) {
     Sp::compute();
@@ -525,17 +538,19 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
   uint64_t* dp_full = s_read + 2;       // [2]
   uint64_t* ds_full = dp_full + 2;      // [2][2] half of a tile's dS is in place
   uint64_t* dq_full = ds_full + 4;      // [2]
-  uint64_t* fixed = dq_full + 2;
-  uint64_t* done = fixed + 1;
+  uint64_t* landed = dq_full + 2;       // [kK] see Partial
+  uint64_t* done = landed + C::kK;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  float* s_c = reinterpret_cast<float*>(tmem_slot + 1);
-  static_assert((2 * (C::kK + C::kV) + 22) * 8 + 8 <= C::kBarriers, "barriers");
+  uint32_t* ended = tmem_slot + 1;      // see Partial
+  float* s_c = reinterpret_cast<float*>(tmem_slot + 2);
+  static_assert((3 * C::kK + 2 * C::kV + 21) * 8 + 12 <= C::kBarriers, "barriers");
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kK; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
+      mbar_init(&landed[s], 1);
     }
     for (int s = 0; s < C::kV; ++s) {
       mbar_init(&v_full[s], 1);
@@ -553,9 +568,9 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
       mbar_init(&ds_full[2 * s + 1], 4);
       mbar_init(&dq_full[s], 1);
     }
-    mbar_init(fixed, 1);
     mbar_init(done, 1);
     *s_c = p.c;
+    *ended = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
   }
@@ -572,7 +587,8 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
   Items items(p.tiles, p.groups, p.count);
   if (warp == 8) {
     // ---- loads, in the order in which the products free their places ----
-    int gk = 0, gv = 0, fixes = 0, nq0 = 0, nq1 = 0, nd0 = 0, nd1 = 0;   // tiles asked for
+    int gk = 0, gv = 0, nq0 = 0, nq1 = 0, nd0 = 0, nd1 = 0;   // tiles asked for
+    Partial part;
     bool ok = true;
     auto own = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* empty, int& n, int col, int row) {
       if (n && !warp_wait(empty, (uint32_t)(n - 1) & 1u, 1u, p.err, p.limit)) return false;
@@ -590,24 +606,14 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
       for (int j = 0; j < pr.most && ok; ++j) {
         const int a = gk % C::kK, b = gv % C::kV, rows = t.len - j * kRows;
         if (gk >= C::kK && !(ok = warp_wait(&k_empty[a], (uint32_t)(gk / C::kK - 1) & 1u, 1u, p.err, p.limit))) break;
-        // K's rows behind the sequence are zeroed: dS is zero there, but zero times a NaN is not
-        const bool fix = rows < kRows;
-        uint8_t* dst = sk + a * C::kTile;
+        const bool some = rows < kRows;   // the sequence's last rows
         if (lane == 0) {
-          uint64_t* bar = fix ? fixed : &k_full[a];
+          uint64_t* bar = some ? &landed[a] : &k_full[a];
           mbar_expect_tx(bar, C::kTile);
-          Tl::load(dst, &p.tk, bar, col, t.row0 + j * kRows);
+          Tl::load(sk + a * C::kTile, &p.tk, bar, col, t.row0 + j * kRows);
         }
+        if (some) part.next(a);
         ++gk;
-        if (fix) {
-          ok = __all_sync(0xffffffffu, mbar_wait(fixed, (uint32_t)fixes & 1u, 1u, p.err));
-          ++fixes;
-          if (!ok) break;
-          Tl::zero_rows(dst, rows, lane);
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&k_full[a]);
-        }
         if (j == 0) {
           if (pr.n1 && !(ok = own(sq + C::kTile, &p.tq, &q_full[1], &q_empty[1], nq1, pr.h1 * D, t.row0 + pr.q1 * kRows))) break;
           if (!(ok = own(sdo, &p.tdo, &do_full[0], &do_empty[0], nd0, pr.h0 * D, t.row0 + pr.q0 * kRows))) break;
@@ -623,10 +629,12 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
       }
     }
     if (lane == 0) {   // every copy has landed before the CTA ends
+      *static_cast<volatile uint32_t*>(ended) = 1u + part.n;
       if (nq0) mbar_wait(&q_full[0], (uint32_t)(nq0 - 1) & 1u, 1u, p.err);
       if (nq1) mbar_wait(&q_full[1], (uint32_t)(nq1 - 1) & 1u, 1u, p.err);
       if (nd0) mbar_wait(&do_full[0], (uint32_t)(nd0 - 1) & 1u, 1u, p.err);
       if (nd1) mbar_wait(&do_full[1], (uint32_t)(nd1 - 1) & 1u, 1u, p.err);
+      part.drain(landed, C::kK, p.err);
       for (int k = gk > C::kK ? gk - C::kK : 0; k < gk; ++k)
         if (!mbar_wait(&k_full[k % C::kK], (uint32_t)(k / C::kK) & 1u, 1u, p.err)) break;
       for (int k = gv > C::kV ? gv - C::kV : 0; k < gv; ++k)
@@ -699,6 +707,16 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
     commit(done, one);   // every product has completed before the tensor memory is freed
     mbar_wait(done, 0u, 2u, p.err);
     __syncwarp();
+  } else if (warp == 10) {
+    // ---- zeros behind the sequences, in K ----
+    Partial part;
+    int g = 0;   // key tiles so far
+    while (items.take(t, group)) {
+      const Pair pr(t, group, p.by_heads);
+      g += pr.most;
+      const int rows = t.len - (pr.most - 1) * kRows, a = (g - 1) % C::kK;
+      if (rows < kRows && !part.pass<D>(sk + a * C::kTile, a, rows, landed, k_full, lane, p.err, ended, part.n)) break;
+    }
   } else if (warp < 8) {
     SplitFwd::compute();
     // ---- elementwise and epilogue: thread = query r of tile s ----

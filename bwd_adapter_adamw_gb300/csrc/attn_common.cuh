@@ -347,5 +347,47 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
   return true;
 }
 
+// Tiles whose rows behind the sequence are zeroed before the products see them: P and dS are zero there, but zero
+// times another sequence's or padding's NaN is not. The copy lands on the buffer's `landed` barrier, and a warp of its
+// own zeroes the rows and passes the tile on (`full`), so that the loading warp need not wait (1500 cycles a tile;
+// dK and dV meet one for every query head). Both warps walk the same tiles and count each buffer's uses.
+struct Partial {
+  static constexpr unsigned long long kLongest = 1ull << 40;   // cycles: minutes
+  uint32_t parity = 0, used = 0;   // by buffer: the next use's parity, whether there was one
+  uint32_t n = 0;                  // tiles so far
+  __device__ void next(int s) {
+    parity ^= 1u << s;
+    used |= 1u << s;
+    ++n;
+  }
+  // the zeroing warp, which has passed `before` tiles: false where the copy does not land. Its next tile may be many
+  // items away, so that its wait has no short bound of its own: the loading warp, whose waits have one, leaves 1 + the
+  // tiles it asked for in `ended`, and what was asked for lands.
+  template <int D>
+  __device__ bool pass(uint8_t* tile, int s, int rows, uint64_t* landed, uint64_t* full, int lane, uint32_t* err,
+                       const uint32_t* ended, uint32_t before) {
+    const uint32_t par = parity >> s & 1u;
+    const unsigned long long t0 = clock64();
+    while (!__all_sync(0xffffffffu, mbar_try_wait(&landed[s], par))) {
+      const uint32_t v = __shfl_sync(0xffffffffu, *static_cast<const volatile uint32_t*>(ended), 0);
+      if (v != 0u || __any_sync(0xffffffffu, clock64() - t0 > kLongest)) {
+        if ((v != 0u && before + 1u >= v) || !warp_wait(&landed[s], par, 1u, err, kWaitCycles)) return false;
+        break;
+      }
+    }
+    next(s);
+    Tile<D>::zero_rows(tile, rows, lane);
+    fence_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[s]);
+    return true;
+  }
+  // the loading warp's lane 0, at its end: every copy has landed
+  __device__ void drain(uint64_t* landed, int n, uint32_t* err) const {
+    for (int s = 0; s < n; ++s)
+      if (used >> s & 1u) mbar_wait(&landed[s], (parity >> s & 1u) ^ 1u, 1u, err);
+  }
+};
+
 }  // namespace attn
 }  // namespace lora
