@@ -62,7 +62,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constan
   __shared__ int64_t sh[kPlanThreads];
   __shared__ int64_t carry;
   const int t = threadIdx.x;
-  if (t == 0) carry = 0;
+  if (t == 0) {
+    carry = 0;
+    a.p.count[2] = (int)a.T;
+    a.p.count[3] = a.n_seq;
+  }
   __syncthreads();
   for (int64_t k0 = 0; k0 < a.n_seq; k0 += kPlanThreads) {
     const int64_t k = k0 + t;
@@ -145,9 +149,8 @@ struct FwdCfg {
 
 struct FwdK {
   CUtensorMap tq, tk, tv, to;
-  const int32_t* count;
-  const AttnTile* tiles;
-  int32_t groups;        // CTAs of a tile of the list
+  PlanRef plan;
+  int32_t groups;        // items of a tile of the list
   int32_t by_heads;      // two heads of a 128-row tile, or two 128-row tiles of a head
   int32_t per;           // query heads of a key / value head
   float c;               // scale log2(e)
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
   if (warp >= 8) SplitFwd::issue();
   AttnTile t;
   int group;
-  Items items(p.tiles, p.groups, p.count);
+  Items items(p.plan, p.groups);
   if (warp == 8) {
     // ---- loads: Q of both tiles, then K and V tile by tile ----
     int g = 0, nq0 = 0, nq1 = 0;   // tiles of the ring, of Q
@@ -458,8 +461,7 @@ cudaError_t fwd_launch(const AttnArgs& a, cudaStream_t st) {
   k.per = a.q_heads / a.kv_heads;
   k.by_heads = k.per % 2 == 0;
   const int w = k.by_heads ? 0 : 1;
-  k.count = a.plan.count + w;
-  k.tiles = a.plan.tiles[w];
+  k.plan = plan_ref(a, w);
   k.groups = k.by_heads ? a.q_heads / 2 : a.q_heads;
   k.c = a.scale * kLog2e;
   k.T = a.T;
@@ -488,7 +490,8 @@ AttnPlan attn_plan(int64_t T, int32_t n_seq, void* buf) {
   AttnPlan p{};
   Carve c(buf);
   const int64_t some = n_seq < T ? n_seq : T;   // sequences that are not empty
-  p.count = c.take<int32_t>(2);
+  p.count = c.take<int32_t>(4);
+  p.n_seq = n_seq;
   for (int w = 0; w < 2; ++w) {
     p.most[w] = T / (kAttnTile << w) + some;
     p.tiles[w] = c.take<AttnTile>((size_t)p.most[w]);

@@ -62,8 +62,7 @@ __global__ void __launch_bounds__(256) k_attn_delta(const __nv_bfloat16* __restr
 
 struct BwdK {
   CUtensorMap tq, tk, tv, tdo, tdq;
-  const int32_t* count;
-  const AttnTile* tiles;
+  PlanRef plan;
   int32_t heads;         // dK, dV: work items of a tile
   int32_t split;         // dK, dV: CTAs of a cluster, which share a group's query heads
   int32_t groups;        // dQ: work items of a tile of the list
@@ -140,7 +139,7 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
   const int rank = CL ? (int)cluster_ctarank() : 0;
   if constexpr (CL) {   // clusters behind the last item leave before they take tensor memory
     grid_dep_sync();
-    if ((int)blockIdx.x / p.split >= __ldg(p.count) * p.heads) return;
+    if ((int)blockIdx.x / p.split >= p.plan.items(p.heads)) return;
   }
 
   if (threadIdx.x == 0) {
@@ -183,7 +182,7 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
   if (warp >= kComputeWarps) Sp::issue();
   AttnTile t{};
   int hk = 0;
-  Items items(p.tiles, p.heads, p.count, CL ? p.split : 1);
+  Items items(p.plan, p.heads, CL ? p.split : 1);
   const int mine = p.per / (CL ? p.split : 1);   // query heads of an item in this CTA
   // An item: key tile j of nb, its query tiles j .. nb - 1 under each of its query heads, head by head.
   struct Span {
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
   }
   if constexpr (CL) {
     cluster_sync_all();
-    Items again(p.tiles, p.heads, p.count, p.split);
+    Items again(p.plan, p.heads, p.split);
     // (the compute warps alone: the others have few registers left)
     if (warp < kComputeWarps && again.take(t, hk)) {   // the same for every CTA of the cluster
       const int split = p.split, j = (t.len + kRows - 1) / kRows - 1 - t.index;
@@ -584,7 +583,7 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
   if (warp >= 8) SplitFwd::issue();
   AttnTile t;
   int group;
-  Items items(p.tiles, p.groups, p.count);
+  Items items(p.plan, p.groups);
   if (warp == 8) {
     // ---- loads, in the order in which the products free their places ----
     int gk = 0, gv = 0, nq0 = 0, nq1 = 0, nd0 = 0, nd1 = 0;   // tiles asked for
@@ -888,8 +887,7 @@ cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t st) {
   e = launch_kernel(k_attn_delta<D>, (unsigned)pre, 256, 0, st, static_cast<const __nv_bfloat16*>(a.O),
                     static_cast<const __nv_bfloat16*>(a.dO), a.ld_o, (int)a.q_heads, a.T, a.delta);
   if (e != cudaSuccess) return e;
-  k.count = a.plan.count;
-  k.tiles = a.plan.tiles[0];
+  k.plan = plan_ref(a, 0);
   k.heads = a.kv_heads;
   k.split = dkv_split(a, sms);
   if (grid * k.split > INT32_MAX) return cudaErrorInvalidValue;
@@ -897,8 +895,7 @@ cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t st) {
   e = k.split > 1 ? launch_clusters(k_attn_dkv<D, true>, (unsigned)(grid * k.split), Sp::kThreads, DkvCfg<D>::kSmem, st, k, k.split)
                   : launch_kernel(k_attn_dkv<D, false>, (unsigned)(grid < sms ? grid : sms), Sp::kThreads, DkvCfg<D>::kSmem, st, k);
   if (e != cudaSuccess) return e;
-  k.count = a.plan.count + w;
-  k.tiles = a.plan.tiles[w];
+  k.plan = plan_ref(a, w);
   prof_begin(0, st);
   return launch_kernel(k_attn_dq<D>, (unsigned)(most < sms ? most : sms), SplitFwd::kThreads, DqCfg<D>::kSmem, st, k);
 }

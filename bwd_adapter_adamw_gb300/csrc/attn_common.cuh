@@ -230,14 +230,29 @@ __device__ __forceinline__ AttnTile tile_at(const AttnTile* t) {
   return AttnTile{uniform(v.x), uniform(v.y), uniform(v.z), 0};
 }
 
+// One of a plan's lists. A plan of other tokens or sequences than the call's has none of its items: nothing is
+// computed, and nothing outside the call's tensors is touched.
+struct PlanRef {
+  const int32_t* head;     // tiles of 128 rows, of 256 rows, tokens, sequences
+  const AttnTile* tiles;
+  int32_t list, tokens, n_seq;
+  __device__ int items(int groups) const {
+    const int4 v = __ldg(reinterpret_cast<const int4*>(head));
+    return uniform(v.z == tokens && v.w == n_seq ? (list ? v.y : v.x) * groups : 0);
+  }
+};
+inline PlanRef plan_ref(const AttnArgs& a, int list) {
+  return PlanRef{a.plan.count, a.plan.tiles[list], list, (int32_t)a.T, a.plan.n_seq};
+}
+
 // The work of a persistent CTA: items of the plan's list (a tile and one of its `groups` groups of heads), the
 // longest first, dealt out to and fro so that every CTA's sum comes out alike. Every role of a CTA walks the
 // same items; the loading warp comes to each first, so that the others find its tile in L1.
 struct Items {
   const AttnTile* tiles;
   int groups, n, round, b, grid;
-  __device__ Items(const AttnTile* t, int g, const int32_t* count, int cluster = 1)
-      : tiles(t), groups(g), n(uniform(__ldg(count) * g)), round(0), b((int)blockIdx.x / cluster), grid((int)gridDim.x / cluster) {}
+  __device__ Items(const PlanRef& p, int g, int cluster = 1)
+      : tiles(p.tiles), groups(g), n(p.items(g)), round(0), b((int)blockIdx.x / cluster), grid((int)gridDim.x / cluster) {}
   // the next item, false if there is none
   __device__ bool take(AttnTile& t, int& group) {
     const int64_t i = (int64_t)round * grid + ((round & 1) ? grid - 1 - b : b);

@@ -351,7 +351,7 @@ constexpr int kFlight = sizeof(E) == 2 ? 4 : 2;
 // token has steps where there are few (one decoded token is bound by latency).
 int rope_parts(const RopeArgs& a, int hpw, int sms) {
   const int64_t want = (int64_t)sms * 16;
-  int64_t n = a.T >= want ? 1 : (want + a.T - 1) / a.T;
+  int64_t n = want / (a.T < want ? a.T : want);   // (one round of them)
   const int most = (a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1]) + hpw - 1;
   if (n > most / hpw) n = most / hpw;
   return (int)(n < 1 ? 1 : n);

@@ -486,11 +486,12 @@ struct AttnTile {                // of a sequence of `len` rows from row `row0`
 };
 // The plan's parts within its buffer.
 struct AttnPlan {
-  int32_t* count;      // [2] tiles of 128 rows, of 256 rows
+  int32_t* count;      // [4] tiles of 128 rows, of 256 rows, tokens, sequences
   AttnTile* tiles[2];
   int64_t most[2];     // room for them
   int2* seq;           // [n_seq] first row, rows
   int32_t* hist;       // [buckets of 128 rows]
+  int32_t n_seq;
   size_t bytes;
 };
 AttnPlan attn_plan(int64_t T, int32_t n_seq, void* buf);

@@ -363,8 +363,9 @@ class AttentionStep(SublayerStep):
                 raise ValueError(f"projection {name}: {l.out_dim} outputs for {width // max(head_dim, 1)} heads of {head_dim}")
         if o.in_dim != wq or tuple(o.dY.shape) != (T, o.out_dim) or o.dY.dtype != X.dtype:
             raise ValueError(f"projection o: W {tuple(o.W.shape)} and dY {tuple(o.dY.shape)} {o.dY.dtype}")
-        if seq_start.dtype != torch.int32 or seq_start.dim() != 1 or seq_start.numel() < 2:
-            raise ValueError("seq_start: int32 [sequences + 1]")
+        if seq_start.dtype != torch.int32 or seq_start.dim() != 1 or seq_start.numel() < 2 or \
+                seq_start.device != dev or not seq_start.is_contiguous():
+            raise ValueError("seq_start: int32 [sequences + 1] on the activations' device")
         new = lambda n: torch.zeros((T, n), dtype=X.dtype, device=dev)   # noqa: E731  (padding rows stay zero)
         for l in (q, k, v):
             l.dY = new(l.out_dim)
@@ -385,8 +386,10 @@ class AttentionStep(SublayerStep):
             seq = torch.searchsorted(at, torch.arange(T, device=dev), right=True) - 1
             pos = torch.arange(T, device=dev) - at[seq.clamp(min=0)]
             pos = torch.where((seq >= 0) & (seq < self.n_seq), pos, -1).int()
-        if pos.dtype != torch.int32 or tuple(pos.shape) != (T,):
-            raise ValueError("pos: int32 [tokens]")
+        if pos.dtype != torch.int32 or tuple(pos.shape) != (T,) or pos.device != dev:
+            raise ValueError("pos: int32 [tokens] on the activations' device")
+        if inv_freq is not None and tuple(inv_freq.shape) != (head_dim // 2,):
+            raise ValueError("inv_freq: [head_dim / 2]")
         self.pos, self.n_pos = pos.contiguous(), T if n_pos is None else n_pos
         if inv_freq is None:
             inv_freq = rope_base ** (-torch.arange(0, head_dim, 2, dtype=torch.float64) / head_dim)

@@ -401,9 +401,9 @@ int lora_rope_backward(const lora_rope_desc* d, int64_t T, const void* Q, const 
  * Products on tensor cores with fp32 sums; scores, statistics and the softmax in fp32; P and dS are
  * rounded to bf16 (2^-8 of each) as operands of the second products, everything else once at the end. No
  * atomics: reruns are bitwise equal.
- * head_dim 64 or 128, q_heads a multiple of kv_heads, dtype LORA_BF16, heads * head_dim at most 2^20 and T
- * below 2^31 - 256 (LORA_ERR_UNSUPPORTED); strides multiples of 8 elements and at least heads * head_dim
- * (LORA_ERR_ALIGN, LORA_ERR_INVALID); T = 0 is a no-op. Outputs do not overlap inputs.
+ * q_heads a multiple of kv_heads, strides at least heads * head_dim (LORA_ERR_INVALID) and multiples of 8
+ * elements (LORA_ERR_ALIGN); head_dim 64 or 128, dtype LORA_BF16, heads * head_dim at most 2^20 and T below
+ * 2^31 - 256 (LORA_ERR_UNSUPPORTED); T = 0 is a no-op. Outputs do not overlap inputs.
  * When lora_device_check reports LORA_ERR_TIMEOUT after it, an element of an output holds its value or
  * is as it was. */
 typedef struct lora_attn_desc {
@@ -418,8 +418,8 @@ typedef struct lora_attn_desc {
  * non-decreasing, within [0, T]; offsets outside are clamped, and a sequence that would begin before the
  * end of an earlier one begins there). One plan, in a caller-owned device buffer of
  * lora_attn_plan_size(T, n_seq) bytes, 16-byte aligned, serves every layer's forward and backward calls
- * over the same batch, on any streams ordered after the build; these pass the same T and n_seq. n_seq from
- * 1 to 2^24. One launch. */
+ * over the same batch, on any streams ordered after the build; these pass the same T and n_seq (with others
+ * they find no tiles and write nothing). n_seq from 1 to 2^24. One launch. */
 size_t lora_attn_plan_size(int64_t T, int32_t n_seq);
 int lora_attn_plan_build(int64_t T, int32_t n_seq, const int32_t* d_seq_start, void* plan,
                          size_t plan_bytes, void* stream);
@@ -642,7 +642,7 @@ int lora_device_error(uint32_t* flags, int32_t reset);
  * state changes; here the same rule for a stalled kernel). */
 int lora_device_check(void* stream);
 /* Test hook: bound, in SM clock cycles, of the pipeline waits of the frozen-product kernels
- * (bf16 and E4M3), the norms' backward pass and the orthogonalised update launched after this call;
+ * (bf16 and E4M3), the norms' backward pass, the attention and the orthogonalised update launched after this call;
  * 0 restores the default (2^33 cycles, seconds).
  * Process-wide, not thread-safe with concurrent launches. A small bound makes a correct launch
  * give up: its error bits are set and its outputs are invalid. Waits that drain work already

@@ -248,6 +248,25 @@ def test_tables_out_of_order_or_range(L, starts, rows):
     assert np.all(got[~inside] == 77.0) and np.all(gl[:, ~inside] == 77.0)
 
 
+def test_plan_of_other_tokens_or_sequences(L):
+    """A plan built for another T or n_seq, or never built: nothing is written."""
+    b, other = Batch(L, [200, 100], 4, 2, 64, seed=1), Batch(L, [200, 100, 50], 4, 2, 64, seed=2)
+    b.exact_statistics()
+    keep = b.o.clone(), b.lse.clone()
+    for plan in (other.plan, Batch(L, [100, 100, 100], 4, 2, 64).plan, Batch(L, [290, 9], 4, 2, 64).plan,
+                 torch.zeros_like(other.plan)):
+        b.plan = plan
+        b.o.fill_(77.0)
+        b.lse.fill_(77.0)
+        b.forward()
+        assert bool((b.o == 77.0).all()) and bool((b.lse == 77.0).all())
+        b.o.copy_(keep[0])
+        b.lse.copy_(keep[1])
+        b.backward()
+        assert all(bool((x == 77.0).all()) for x in (b.dq, b.dk, b.dv))
+    assert L.lora_device_check() == L.LORA_OK
+
+
 def torch_reference(b, h):
     """(o, lse, dq of head h, and dk, dv of its key head's group) in float64 on the GPU."""
     per = b.hq // b.hk

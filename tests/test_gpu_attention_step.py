@@ -166,6 +166,7 @@ def test_refusals(L):
                              head_dim=64, seq_start=start, **kw)
     build()
     for kw in (dict(X=X.float(), dtype="f32"), dict(kq=64), dict(o_in=64), dict(start=s.long()), dict(start=s[:1]),
-               dict(dY=X[:4]), dict(pos=s.long()), dict(pos=s), dict(tokens=9)):
+               dict(dY=X[:4]), dict(pos=s.long()), dict(pos=s), dict(tokens=9),
+               dict(start=s.cpu()), dict(pos=torch.zeros(8, dtype=torch.int32)), dict(inv_freq=torch.ones(3))):
         with pytest.raises(ValueError):
             build(**kw)
