@@ -225,11 +225,6 @@ cudaError_t set_up(F* kernel, int smem) {
   return e;
 }
 
-__device__ __forceinline__ AttnTile tile_at(const AttnTile* t) {
-  const int4 v = __ldg(reinterpret_cast<const int4*>(t));
-  return AttnTile{uniform(v.x), uniform(v.y), uniform(v.z), 0};
-}
-
 // One of a plan's lists. A plan of other tokens or sequences than the call's has none of its items: nothing is
 // computed, and nothing outside the call's tensors is touched.
 struct PlanRef {

@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) k_rope_fwd(const __grid_const
 // known, so that their shuffles run together. The CTA's sums go to part[CTA][q | k], added up in order by
 // k_rope_reduce.
 //
-// 8192 tokens of 40 heads of 128 in bf16: 53 us, 4.8 TB/s, half of it the kernel's own instructions (140 per warp and
-// two heads). Two steps in flight instead of four: 61 us; three CTAs per SM: 69. Rows brought by bulk copies to
-// per-warp rings in shared memory: 66.
+// 8192 tokens of 40 heads of 128 in bf16: 51 us, 4.9 TB/s, half of it the kernel's own instructions (140 per warp and
+// two heads); 59 with the reduction and two copies of the weights' gradients. So measured, two steps in flight instead
+// of four take 68 us, three CTAs per SM 75, rows brought by bulk copies to per-warp rings in shared memory 72.
 template <typename E, int D, bool PAIRS, bool NORM, int R>
 __global__ void __launch_bounds__(kRopeThreads, 2) k_rope_bwd(const __grid_constant__ RopeK p) {
   grid_dep_sync();
