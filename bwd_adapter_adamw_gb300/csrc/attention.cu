@@ -344,10 +344,15 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
       const Pair pr(t, group, p.by_heads);
       const int n = pr.n(s);
       if (!n) continue;
+      const bool dead = pr.qi(s) * kRows + (warp & 3) * 32 >= t.len;   // all of the warp's rows lie behind the sequence
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
         if (!(ok = warp_wait(&s_full[s], ns++ & 1u, 4u, p.err, p.limit))) break;
         fence_after();
+        if (dead) {   // (whatever stands there as P makes O's rows of these queries alone)
+          if (lane < 2) mbar_arrive(&p_full[2 * s + lane]);
+          continue;
+        }
         uint32_t x[128];
 #pragma unroll
         for (int k = 0; k < 4; ++k) tmem_ld32_nw(ts + 32 * k, x + 32 * k);
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_fwd(const __grid
       const int64_t at = (int64_t)t.row0 + row0;
       uint8_t* stage = stages + warp * C::kStage;
 #pragma unroll 1
-      for (int k = 0; k < D / 64; ++k) {
+      for (int k = 0; k < (dead ? 0 : D / 64); ++k) {
         uint32_t u[32];
         read_rows<64>(to + 64 * k, 1.f / l, u);
         rows_read(lane);   // (what was sent before)
