@@ -18,10 +18,10 @@
 // Every wait is bounded; a warp whose wait ran out stops, and no later
 // warp sees its part arrive, so that outputs are stored from complete products only.
 //
-// Bound by the tensor cores at the power limit's clock: one sequence of 8192 tokens, 32 / 8 heads of 128, 358-373 us
-// (1470 to 1540 TFLOP/s of the 1763 that a library product sustains; 330 us and the tensor cores busy for 74% of
-// them where the clock holds), 32768 tokens 5.5 ms (1610). 16384 tokens in sequences of 64 to 1024 take 118 us, 650
-// TFLOP/s of useful and 1080 of tiles' operations: there an item's 2.9 key tiles stand between its first load and
+// Bound by the tensor cores at the power limit's clock: one sequence of 8192 tokens, 32 / 8 heads of 128, 355-373 us
+// (1470 to 1550 TFLOP/s of the 1763 that a library product sustains; 330 us and the tensor cores busy for 74% of
+// them where the clock holds), 32768 tokens 5.5 ms (1610). 16384 tokens in sequences of 64 to 1024 take 117 us, 840
+// TFLOP/s of useful and 1390 of tiles' operations: there an item's 2.9 key tiles stand between its first load and
 // its last store. Steps at 8192 tokens: products issued by a
 // single lane's branch 481, by a whole warp 380; P in halves and three-operand maxima 369; persistent CTAs 364. Not
 // kept: two issuing warps 421, half of P against the reference of the tile before 384.

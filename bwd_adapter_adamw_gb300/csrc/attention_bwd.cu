@@ -24,9 +24,9 @@
 // loads, warp 17 issues the products, warp 18 brings the queries' statistics, warp 19 zeroes rows behind a sequence
 // (k_attn_dkv); as in the forward pass (k_attn_dq). Waits are bounded as there.
 //
-// One sequence of 8192 tokens, 32 / 8 heads of 128: 1178 to 1191 us (seven products: 1620 TFLOP/s, near the 1763 that
+// One sequence of 8192 tokens, 32 / 8 heads of 128: 1166 to 1187 us (seven products: 1620 to 1650 TFLOP/s, near the 1763 that
 // the power limit leaves a library product); alone delta takes 25 us, dV and dK 599 (1840 TFLOP/s, tensor cores 88%
-// busy), dQ 468 (1760, 77%). 16384 tokens in sequences of 64 to 1024: 410 us, where delta is 40, dV and dK 183,
+// busy), dQ 468 (1760, 77%). 16384 tokens in sequences of 64 to 1024: 404 us; one by one delta takes 40, dV and dK 183,
 // dQ 156.
 #include "attn_common.cuh"
 
@@ -583,7 +583,12 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
   __syncthreads();
   fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
-  grid_dep_sync();   // from here on, the earlier kernels' outputs are visible
+  // The kernel ahead, k_attn_dkv, reads what this one reads and writes none of it: a CTA begins where that leaves an SM,
+  // and waits for it at its end only, so that whatever follows finds both complete. It lets this kernel in after its
+  // own wait for delta's and all earlier kernels; the fence drops what this SM's L1 holds from before those. (Packed
+  // batch 411 -> 404 us.)
+  __threadfence();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp >= 8) SplitFwd::issue();
   AttnTile t;
@@ -827,12 +832,13 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
     fence_after();
     tmem_dealloc(tmem, 512);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // CTAs that share a key tile's query heads: as many as the SMs hold at once, so that few key heads over few tokens
 // still use them. 8 sequences of 128 tokens, 32 / 4 heads of 64: 32 items, a cluster of 4 each; all of the backward
-// pass 19.4 us, 22.6 when every item took a CTA per query head pair. Where items fill the SMs, persistent CTAs
-// overlap them: 448 us against 457 on the packed batch above.
+// pass 19.3 us, 21.2 with one CTA or a cluster of two for each. Where items fill the SMs, persistent CTAs overlap them:
+// 448 us against 457 on the packed batch above.
 int dkv_split(const AttnArgs& a, int sms) {
   const int64_t items = (a.T + kRows - 1) / kRows * a.kv_heads;
   int n = 1;

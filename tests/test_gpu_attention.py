@@ -382,6 +382,37 @@ def test_one_plan_on_two_streams_and_in_graphs(L):
     assert all(torch.equal(t, u) for x, w in zip((a, b), want) for t, u in zip(outs(x), w))
 
 
+@pytest.mark.parametrize("lens,hq,hk,dim", [([640], 8, 1, 128), ([2048], 32, 8, 128), ([300, 17, 900], 16, 4, 64)])
+def test_calls_in_a_row_wait_for_one_another(L, lens, hq, hk, dim):
+    """The backward pass's last kernel begins beside the one ahead of it: what follows in the stream, here a second
+    batch with the same workspace and a kernel that overwrites the queries, still finds both complete."""
+    a, b = Batch(L, lens, hq, hk, dim, seed=1), Batch(L, lens, hq, hk, dim, seed=2)
+    b.ws = a.ws
+    want = []
+    for x in (a, b):
+        x.forward()
+        x.backward()
+        torch.cuda.synchronize()
+        want.append([y.clone() for y in (x.dq, x.dk, x.dv)])
+    kept, other = a.q.clone(), torch.full_like(a.q, 3.0)
+    desc = L.make_rope_desc(hq, 0, dim)
+    pos = torch.zeros(a.T, dtype=torch.int32, device="cuda")
+    table = torch.tensor([[1.0, 0.0]], device="cuda").repeat(1, dim // 2, 1)   # no rotation: a copy
+    copy = lambda src, dst: L.lora_rope_forward(desc, a.T, src, None, None, None, pos, table, 1, dst, None)   # noqa: E731
+    for x in (a, b):
+        for y in (x.dq, x.dk, x.dv):
+            y.fill_(77.0)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        a.backward()
+        copy(other, a.q)
+        copy(kept, a.q)
+        b.backward()
+    torch.cuda.synchronize()
+    for x, w in zip((a, b), want):
+        assert all(torch.equal(g, y) for g, y in zip((x.dq, x.dk, x.dv), w))
+
+
 def test_many_sequences(L):
     """More sequences than the plan's threads, most of them of one token or none."""
     g = torch.Generator().manual_seed(0)
