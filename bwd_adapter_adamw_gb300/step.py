@@ -347,8 +347,10 @@ class AttentionStep(SublayerStep):
     with head_norm=False). q, k, v and o are the Linears of the four projections; o.dY is the
     sublayer's output gradient, the other three gradients are the step's own. seq_start: int32 [n + 1]
     on the device, the sequences' first tokens and the last one's end; tokens of no sequence are padding
-    (their output gradients have to be zero). pos: int32 [tokens], from 0 in each sequence unless given
-    (negative: padding); inv_freq: the rotation's frequencies, rope_base^(-2 i / head_dim) unless given."""
+    (their rows of X have to be finite, their output gradients zero). pos: int32 [tokens], from 0 in each
+    sequence unless given (negative: padding). Both are copied; set_sequences gives the step another batch's.
+    inv_freq: the rotation's frequencies, rope_base^(-2 i / head_dim) unless given, for n_pos positions
+    (the batch's tokens unless given)."""
 
     def __init__(self, X: torch.Tensor, q: Linear, k: Linear, v: Linear, o: Linear, *, q_heads: int,
                  kv_heads: int, head_dim: int, seq_start: torch.Tensor, pos: Optional[torch.Tensor] = None,
@@ -363,9 +365,7 @@ class AttentionStep(SublayerStep):
                 raise ValueError(f"projection {name}: {l.out_dim} outputs for {width // max(head_dim, 1)} heads of {head_dim}")
         if o.in_dim != wq or tuple(o.dY.shape) != (T, o.out_dim) or o.dY.dtype != X.dtype:
             raise ValueError(f"projection o: W {tuple(o.W.shape)} and dY {tuple(o.dY.shape)} {o.dY.dtype}")
-        if seq_start.dtype != torch.int32 or seq_start.dim() != 1 or seq_start.numel() < 2 or \
-                seq_start.device != dev or not seq_start.is_contiguous():
-            raise ValueError("seq_start: int32 [sequences + 1] on the activations' device")
+        self._check_sequences(seq_start, pos, T, dev)
         new = lambda n: torch.zeros((T, n), dtype=X.dtype, device=dev)   # noqa: E731  (padding rows stay zero)
         for l in (q, k, v):
             l.dY = new(l.out_dim)
@@ -380,17 +380,9 @@ class AttentionStep(SublayerStep):
             self.gamma_k, self.dgamma_k = (self.arena.view(w, at + head_dim, (head_dim,)) for w in ("params", "grads"))
             self.gamma_q.fill_(1.0)
             self.gamma_k.fill_(1.0)
-        self.seq_start, self.n_seq = seq_start, seq_start.numel() - 1
-        if pos is None:
-            at = seq_start.long().clamp(0, T)
-            seq = torch.searchsorted(at, torch.arange(T, device=dev), right=True) - 1
-            pos = torch.arange(T, device=dev) - at[seq.clamp(min=0)]
-            pos = torch.where((seq >= 0) & (seq < self.n_seq), pos, -1).int()
-        if pos.dtype != torch.int32 or tuple(pos.shape) != (T,) or pos.device != dev:
-            raise ValueError("pos: int32 [tokens] on the activations' device")
         if inv_freq is not None and tuple(inv_freq.shape) != (head_dim // 2,):
             raise ValueError("inv_freq: [head_dim / 2]")
-        self.pos, self.n_pos = pos.contiguous(), T if n_pos is None else n_pos
+        self.n_seq, self.n_pos = seq_start.numel() - 1, T if n_pos is None else n_pos
         if inv_freq is None:
             inv_freq = rope_base ** (-torch.arange(0, head_dim, 2, dtype=torch.float64) / head_dim)
         self.table = torch.empty((self.n_pos, head_dim // 2, 2), dtype=torch.float32, device=dev)
@@ -403,13 +395,43 @@ class AttentionStep(SublayerStep):
         self.lse = torch.zeros((q_heads, T), dtype=torch.float32, device=dev)
         self.attn_ws = _ws(max(L.lora_attn_backward_workspace_size(self.attn, T),
                                L.lora_rope_backward_workspace_size(self.rope, T)), dev)
+        self.seq_start = torch.empty_like(seq_start)
+        self.pos = torch.empty(T, dtype=torch.int32, device=dev)
+        self.set_sequences(seq_start, pos)
+
+    @staticmethod
+    def _check_sequences(seq_start: torch.Tensor, pos: Optional[torch.Tensor], T: int, dev: torch.device):
+        if seq_start.dtype != torch.int32 or seq_start.dim() != 1 or seq_start.numel() < 2 or \
+                seq_start.device != dev or not seq_start.is_contiguous():
+            raise ValueError("seq_start: int32 [sequences + 1] on the activations' device")
+        if pos is not None and (pos.dtype != torch.int32 or tuple(pos.shape) != (T,) or pos.device != dev):
+            raise ValueError("pos: int32 [tokens] on the activations' device")
+
+    def set_sequences(self, seq_start: torch.Tensor, pos: Optional[torch.Tensor] = None):
+        """The sequences (as many as before, empty ones among them) and positions of the steps from here on, on
+        the current stream; captured steps take them, too. Rows that were in a sequence and are padding now are
+        cleared."""
+        T = self.T
+        dev = self.X_in.device
+        self._check_sequences(seq_start, pos, T, dev)
+        if seq_start.numel() != self.n_seq + 1:
+            raise ValueError(f"{seq_start.numel() - 1} sequences for a step of {self.n_seq}")
+        if pos is None:
+            at = seq_start.long().clamp(0, T).cummax(0).values
+            seq = torch.searchsorted(at, torch.arange(T, device=dev), right=True) - 1
+            pos = torch.arange(T, device=dev) - at[seq.clamp(min=0)]
+            pos = torch.where((seq >= 0) & (seq < self.n_seq), pos, -1)
+        self.seq_start.copy_(seq_start)
+        self.pos.copy_(pos)
+        for t in (self.o.X, self.lse, self.Qr, self.Kr, self.dQr, self.dKr, self.q.dY, self.k.dY, self.v.dY):
+            t.zero_()
+        L.lora_attn_plan_build(T, self.n_seq, self.seq_start, self.plan)
 
     def _forward(self, opt_step: int, per_chunk_calls: bool):
         """Everything up to the output projection."""
         self._norm_forward()
         self._enqueue(opt_step, per_chunk_calls, False, linears=self.readers)
         T = self.T
-        L.lora_attn_plan_build(T, self.n_seq, self.seq_start, self.plan)
         L.lora_rope_forward(self.rope, T, self.q.Y, self.k.Y, self.gamma_q, self.gamma_k, self.pos, self.table,
                             self.n_pos, self.Qr, self.Kr)
         L.lora_attn_forward(self.attn, T, self.n_seq, self.plan, self.Qr, self.Kr, self.v.Y, self.o.X, self.lse)

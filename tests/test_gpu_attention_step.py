@@ -170,3 +170,45 @@ def test_refusals(L):
                dict(start=s.cpu()), dict(pos=torch.zeros(8, dtype=torch.int32)), dict(inv_freq=torch.ones(3))):
         with pytest.raises(ValueError):
             build(**kw)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_another_batch_of_the_same_step(L, captured):
+    """set_sequences gives a step another batch: rows that are padding in it, after they were in a sequence, add
+    nothing to any gradient, in eager and in captured steps. The caller's own table is not read again."""
+    first, second = [0, 100, 333], [0, 31, 260]
+    st, rnd = make(first, 0)
+    dY = st.o.dY.clone()
+    graph = torch.cuda.CUDAGraph()
+    if captured:
+        st.forward_backward(0)
+        torch.cuda.synchronize()
+        st.arena.grads.zero_()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            st.arena.grads.zero_()
+            st.forward_backward(0)
+
+    def step():
+        if captured:
+            graph.replay()
+        else:
+            st.arena.grads.zero_()
+            st.forward_backward(0)
+        torch.cuda.synchronize()
+
+    step()
+    check(st, first)
+    table = torch.tensor(second, dtype=torch.int32, device="cuda")
+    st.o.dY[second[-1]:] = 0
+    st.set_sequences(table)
+    table.zero_()
+    step()
+    check(st, second)
+    st.o.dY.copy_(dY)
+    st.set_sequences(torch.tensor(first, dtype=torch.int32, device="cuda"))
+    step()
+    check(st, first)
+    with pytest.raises(ValueError):
+        st.set_sequences(torch.tensor([0, 333], dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        st.set_sequences(torch.tensor(first, device="cuda"))
