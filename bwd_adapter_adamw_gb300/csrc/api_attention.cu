@@ -185,7 +185,9 @@ int lora_attn_backward(const lora_attn_desc* d, int64_t T, int32_t n_seq, const 
   a.plan = attn_plan(T, n_seq, const_cast<void*>(plan));
   a.Q = Q; a.K = K; a.V = V; a.O = const_cast<void*>(O); a.lse = const_cast<float*>(lse); a.dO = dO;
   a.dQ = dQ; a.dK = dK; a.dV = dV;
-  a.delta = Carve(ws).take<float>(1);
+  Carve c(ws);
+  a.ready = c.take<int32_t>(1);
+  a.delta = c.take<float>(1);
   return cuda_status(launch_attn_backward(a, (cudaStream_t)stream));
 }
 

@@ -46,8 +46,9 @@ constexpr int kComputeWarps = 4 * kGroups, kLoadWarp = kComputeWarps, kIssueWarp
 template <int D>
 __global__ void __launch_bounds__(256) k_attn_delta(const __nv_bfloat16* __restrict__ O,
                                                     const __nv_bfloat16* __restrict__ dO, int64_t ld, int heads,
-                                                    int64_t T, float* __restrict__ delta) {
+                                                    int64_t T, float* __restrict__ delta, int32_t* ready) {
   grid_dep_sync();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ready = 0;   // (the last call's readers are done)
   constexpr int G = D / 8;
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / G;   // token, then head
   const int l = threadIdx.x % G;
@@ -76,6 +77,7 @@ struct BwdK {
   float c, scale;
   int64_t T, ld_q, ld_k, ld_v;
   const float *lse, *delta;
+  int32_t* ready;        // set by k_attn_dkv once it may read delta, for k_attn_dq
   __nv_bfloat16 *dQ, *dK, *dV;
   uint32_t* err;
   unsigned long long limit;
@@ -100,6 +102,16 @@ struct DkvCfg {
 template <int D>
 __device__ __forceinline__ float* sum_at(float* tile, int row, int c) {
   return tile + row * D + ((c ^ (row & (D / 4 - 1))) << 2);
+}
+
+// k_attn_dkv's wait for the kernels ahead of it. Behind it their outputs are visible, and the first CTA passes that on to
+// k_attn_dq before it lets that begin (a CTA's first thread to issue the instruction counts).
+__device__ __forceinline__ void dkv_dep_sync(int32_t* ready) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x == 0) {
+    if (blockIdx.x == 0) flag_set(ready);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
 }
 
 // CL: the query heads of a group are dealt out to the `split` CTAs of a cluster, one item each, and their sums added
@@ -143,7 +155,7 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rank = CL ? (int)cluster_ctarank() : 0;
   if constexpr (CL) {   // clusters behind the last item leave before they take tensor memory
-    grid_dep_sync();
+    dkv_dep_sync(p.ready);
     if ((int)blockIdx.x / p.split >= p.plan.items(p.heads)) return;
   }
 
@@ -182,7 +194,7 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
   __syncthreads();
   fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
-  if constexpr (!CL) grid_dep_sync();   // from here on, the earlier kernels' outputs are visible
+  if constexpr (!CL) dkv_dep_sync(p.ready);   // from here on, the earlier kernels' outputs are visible
 
   if (warp >= kComputeWarps) Sp::issue();
   AttnTile t{};
@@ -315,8 +327,8 @@ __global__ void __launch_bounds__(Sp::kThreads, 1) k_attn_dkv(const __grid_const
           const int r = qi * kRows + lane + 32 * k;
           const bool in = more && r < t.len;
           const int64_t at = (int64_t)h * p.T + t.row0 + r;
-          vl[k] = in ? -__ldg(p.lse + at) * kLog2e : -INFINITY;   // a query behind the sequence: P = 0
-          vd[k] = in ? -__ldg(p.delta + at) : 0.f;
+          vl[k] = in ? -p.lse[at] * kLog2e : -INFINITY;   // a query behind the sequence: P = 0
+          vd[k] = in ? -p.delta[at] : 0.f;
         }
       };
       read(true);
@@ -547,7 +559,8 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   uint32_t* ended = tmem_slot + 1;      // see Partial
   float* s_c = reinterpret_cast<float*>(tmem_slot + 2);
-  static_assert((3 * C::kK + 2 * C::kV + 21) * 8 + 12 <= C::kBarriers, "barriers");
+  uint32_t* go = tmem_slot + 3;         // the inputs are there
+  static_assert((3 * C::kK + 2 * C::kV + 21) * 8 + 16 <= C::kBarriers, "barriers");
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -579,21 +592,24 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
     fence_async();
   }
   if (warp == 9) tmem_alloc(tmem_slot, 512);
+  // The kernel ahead, k_attn_dkv, reads what this one reads and writes none of it: a CTA begins where that leaves an SM,
+  // and waits for it at its end only, so that whatever follows finds both complete. That it was let in says nothing of
+  // what it can see. The outputs of delta's and all earlier kernels are seen through `ready`, which k_attn_dkv
+  // releases behind its own wait for them, and before it lets this kernel in, so that the flag is there at the first
+  // look; the barrier hands it to all threads, the fence to the bulk copies. (Packed batch 411 -> 404 us.)
+  if (warp == 11 && lane == 0) *go = flag_wait(p.ready, 1u, p.err, p.limit) ? 1u : 0u;
   fence_before();
   __syncthreads();
   fence_after();
+  asm volatile("fence.proxy.async;" ::: "memory");
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
-  // The kernel ahead, k_attn_dkv, reads what this one reads and writes none of it: a CTA begins where that leaves an SM,
-  // and waits for it at its end only, so that whatever follows finds both complete. It lets this kernel in after its
-  // own wait for delta's and all earlier kernels; the fence drops what this SM's L1 holds from before those. (Packed
-  // batch 411 -> 404 us.)
-  __threadfence();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp >= 8) SplitFwd::issue();
   AttnTile t;
   int group;
   Items items(p.plan, p.groups);
+  if (!uniform((int)*go)) items.n = 0;
   if (warp == 8) {
     // ---- loads, in the order in which the products free their places ----
     int gk = 0, gv = 0, nq0 = 0, nq1 = 0, nd0 = 0, nd1 = 0;   // tiles asked for
@@ -741,8 +757,8 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
       const int row = pr.qi(s) * kRows + r, h = pr.h(s);
       const int64_t at = (int64_t)t.row0 + row;
       const bool live = row < t.len;
-      const float lse = live ? __ldg(p.lse + (int64_t)h * p.T + at) * kLog2e : 0.f;
-      const float delta = live ? __ldg(p.delta + (int64_t)h * p.T + at) : 0.f;
+      const float lse = live ? p.lse[(int64_t)h * p.T + at] * kLog2e : 0.f;
+      const float delta = live ? p.delta[(int64_t)h * p.T + at] : 0.f;
       for (int j = 0; j < n; ++j, ++c) {
         if (!(ok = warp_wait(&s_full[s], c & 1u, 4u, p.err, p.limit))) break;
         fence_after();
@@ -881,7 +897,7 @@ cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t st) {
   k.c = a.scale * kLog2e;
   k.scale = a.scale;
   k.T = a.T; k.ld_q = a.ld_q; k.ld_k = a.ld_k; k.ld_v = a.ld_v;
-  k.lse = a.lse; k.delta = a.delta;
+  k.lse = a.lse; k.delta = a.delta; k.ready = a.ready;
   k.dQ = static_cast<__nv_bfloat16*>(a.dQ);
   k.dK = static_cast<__nv_bfloat16*>(a.dK);
   k.dV = static_cast<__nv_bfloat16*>(a.dV);
@@ -898,7 +914,7 @@ cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t st) {
   if (pre > INT32_MAX || most > INT32_MAX || grid > INT32_MAX) return cudaErrorInvalidValue;
   prof_begin(0, st);
   e = launch_kernel(k_attn_delta<D>, (unsigned)pre, 256, 0, st, static_cast<const __nv_bfloat16*>(a.O),
-                    static_cast<const __nv_bfloat16*>(a.dO), a.ld_o, (int)a.q_heads, a.T, a.delta);
+                    static_cast<const __nv_bfloat16*>(a.dO), a.ld_o, (int)a.q_heads, a.T, a.delta, a.ready);
   if (e != cudaSuccess) return e;
   k.plan = plan_ref(a, 0);
   k.heads = a.kv_heads;

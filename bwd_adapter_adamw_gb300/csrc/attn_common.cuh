@@ -173,6 +173,24 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// A flag between two kernels that run side by side: what the setting thread has seen is seen by a thread that has
+// found the flag set.
+__device__ __forceinline__ void flag_set(int32_t* flag) {
+  asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(flag), "r"(1) : "memory");
+}
+// false (and an error bit) if the flag is not set within `limit` cycles
+__device__ __forceinline__ bool flag_wait(const int32_t* flag, uint32_t bit, uint32_t* err, unsigned long long limit) {
+  const unsigned long long t0 = clock64();
+  for (;;) {
+    int32_t v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+    if (v) return true;
+    if (clock64() - t0 > limit) {
+      atomicOr(err, bit);
+      return false;
+    }
+  }
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // A tile: 128 rows of D bf16, as D / 64 boxes of 128 rows of 128 swizzled bytes.
@@ -225,6 +243,15 @@ cudaError_t set_up(F* kernel, int smem) {
   return e;
 }
 
+// What other kernels wrote, the plan's lists and the rows' statistics, is read by plain loads: the non-coherent path is
+// for data that nothing writes while the kernel lives, and with programmatic launch a CTA may be there before its
+// producer is done. (As the language's own load these 16 bytes cost k_attn_dq at head_dim 128 36 bytes of spills more.)
+__device__ __forceinline__ int4 load_plain(const void* p) {
+  int4 v;
+  asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 // One of a plan's lists. A plan of other tokens or sequences than the call's has none of its items: nothing is
 // computed, and nothing outside the call's tensors is touched.
 struct PlanRef {
@@ -232,7 +259,7 @@ struct PlanRef {
   const AttnTile* tiles;
   int32_t list, tokens, n_seq;
   __device__ int items(int groups) const {
-    const int4 v = __ldg(reinterpret_cast<const int4*>(head));
+    const int4 v = load_plain(head);
     return uniform(v.z == tokens && v.w == n_seq ? (list ? v.y : v.x) * groups : 0);
   }
 };
@@ -255,7 +282,7 @@ struct Items {
     if (i >= n) return false;
     const int li = (int)i / groups;
     group = (int)i - li * groups;
-    const int4 v = __ldg(reinterpret_cast<const int4*>(tiles + li));
+    const int4 v = load_plain(tiles + li);
     t = AttnTile{uniform(v.x), uniform(v.y), uniform(v.z), 0};
     return true;
   }

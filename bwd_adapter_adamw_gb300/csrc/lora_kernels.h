@@ -506,6 +506,7 @@ struct AttnArgs {
   void* O;
   float* lse;
   void *dQ, *dK, *dV;
+  int32_t* ready;      // backward: delta may be read
   float* delta;        // backward: [q_heads, T]
 };
 cudaError_t launch_attn_forward(const AttnArgs& a, cudaStream_t st);
