@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) k_rope_bwd(const __grid_const
 }
 
 // dgamma[c] += sum over the CTAs: interleaved runs of CTAs in order, a run's partials all under way at once, then
-// the runs in a fixed tree.
+// the runs in a fixed tree. A CTA takes 32 columns of one weight, or, where both weights' gradients are one array, of
+// both, one after the other.
 constexpr int kRopeRuns = 32;
 __global__ void __launch_bounds__(32 * kRopeRuns) k_rope_reduce(const float* __restrict__ part, int n, int D,
                                                                 float* dgq, float* dgk) {
@@ -314,23 +315,27 @@ __global__ void __launch_bounds__(32 * kRopeRuns) k_rope_reduce(const float* __r
   constexpr int kRun = (kRopeMostCtas + kRopeRuns - 1) / kRopeRuns;
   __shared__ float sh[kRopeRuns][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  float* dst = blockIdx.y ? dgk : dgq;
-  if (!dst) return;
-  const float* src = part + (int64_t)blockIdx.y * D + blockIdx.x * 32;
-  float a[kRun], v = 0.f;
+#pragma unroll 1
+  for (int s = blockIdx.y; s < 2; s += gridDim.y) {
+    float* dst = s ? dgk : dgq;
+    if (!dst) return;   // (one array is given for both or for none)
+    const float* src = part + (int64_t)s * D + blockIdx.x * 32;
+    float a[kRun], v = 0.f;
 #pragma unroll
-  for (int k = 0; k < kRun; ++k) {
-    const int i = ty + k * kRopeRuns;
-    a[k] = i < n ? __ldcg(src + (int64_t)i * 2 * D + tx) : 0.f;
+    for (int k = 0; k < kRun; ++k) {
+      const int i = ty + k * kRopeRuns;
+      a[k] = i < n ? __ldcg(src + (int64_t)i * 2 * D + tx) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) v += a[k];
+    if (s != (int)blockIdx.y) __syncthreads();   // the runs before have been read
+    sh[ty][tx] = v;
+    __syncthreads();
+    v = sh[tx][ty];   // warp ty: the runs of column ty
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (tx == 0) dst[blockIdx.x * 32 + ty] += v;
   }
-#pragma unroll
-  for (int k = 0; k < kRun; ++k) v += a[k];
-  sh[ty][tx] = v;
-  __syncthreads();
-  v = sh[tx][ty];   // warp ty: the runs of column ty
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (tx == 0) dst[blockIdx.x * 32 + ty] += v;
 }
 
 __global__ void k_rope_table(int64_t n_pos, int half, const double* __restrict__ inv_freq, float2* __restrict__ table) {
@@ -381,8 +386,9 @@ cudaError_t rope_launch(const RopeArgs& a, bool bwd, cudaStream_t st) {
   cudaError_t e = launch_kernel(k_rope_bwd<E, D, PAIRS, NORM, kFlight<E>>, grid, kRopeThreads, 0, st, k);
   if (e != cudaSuccess || !NORM || (!a.dgamma[0] && !a.dgamma[1])) return e;
   prof_begin(0, st);
-  return launch_kernel(k_rope_reduce, dim3(D / 32, 2), 32 * kRopeRuns, 0, st, (const float*)a.part, (int)grid, D,
-                       a.dgamma[0], a.heads[1] ? a.dgamma[1] : (float*)nullptr);
+  float* dgk = a.heads[1] ? a.dgamma[1] : nullptr;
+  return launch_kernel(k_rope_reduce, dim3(D / 32, dgk && dgk == a.dgamma[0] ? 1 : 2), 32 * kRopeRuns, 0, st,
+                       (const float*)a.part, (int)grid, D, a.dgamma[0], dgk);
 }
 
 template <typename E, int D>

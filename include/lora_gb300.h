@@ -354,7 +354,8 @@ int lora_sum(int32_t n, const void* const* src, int64_t count, int32_t dtype, vo
  * projection's output; dQ and dK have the same strides, YQ, YK, dYQ, dYK have ld_yq, ld_yk. A stride of
  * 0 stands for heads * head_dim. gamma_q, gamma_k and their gradients fp32 [head_dim]; gamma_q and
  * gamma_k are both given or both NULL, and without them the backward pass does not read Q and K (which
- * may be NULL) and takes no gradients of them. dgamma_q and dgamma_k may be NULL each. pos int32 [T] on
+ * may be NULL) and takes no gradients of them. dgamma_q and dgamma_k may be NULL each, and the same array where
+ * both norms share a weight (the queries' sum is added first). pos int32 [T] on
  * the device: a token with a negative position is padding, its rows are left as they were and it adds
  * nothing to the gradients; a position from n_pos on gives NaN. table fp32 [n_pos, head_dim / 2, 2]
  * (cosine, sine), 16-byte aligned. An output may be an input of the same strides (one decoded token in
