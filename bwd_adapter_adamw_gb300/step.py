@@ -350,7 +350,8 @@ class AttentionStep(SublayerStep):
     (their rows of X have to be finite, their output gradients zero). pos: int32 [tokens], from 0 in each
     sequence unless given (negative: padding). Both are copied; set_sequences gives the step another batch's.
     inv_freq: the rotation's frequencies, rope_base^(-2 i / head_dim) unless given, for n_pos positions
-    (the batch's tokens unless given)."""
+    (the batch's tokens unless given; a position from n_pos on, as in a longer sequence, makes its sequence
+    and the gradients NaN)."""
 
     def __init__(self, X: torch.Tensor, q: Linear, k: Linear, v: Linear, o: Linear, *, q_heads: int,
                  kv_heads: int, head_dim: int, seq_start: torch.Tensor, pos: Optional[torch.Tensor] = None,
@@ -366,6 +367,16 @@ class AttentionStep(SublayerStep):
         if o.in_dim != wq or tuple(o.dY.shape) != (T, o.out_dim) or o.dY.dtype != X.dtype:
             raise ValueError(f"projection o: W {tuple(o.W.shape)} and dY {tuple(o.dY.shape)} {o.dY.dtype}")
         self._check_sequences(seq_start, pos, T, dev)
+        n_pos = T if n_pos is None else n_pos
+        if inv_freq is not None and tuple(inv_freq.shape) != (head_dim // 2,):
+            raise ValueError("inv_freq: [head_dim / 2]")
+        attn = L.make_attn_desc(q_heads, kv_heads, head_dim)
+        rope = L.make_rope_desc(q_heads, kv_heads, head_dim, L.LORA_BF16,
+                                L.LORA_ROPE_PAIRS if pairs else L.LORA_ROPE_HALVES, head_eps)
+        sizes = [L.lora_attn_backward_workspace_size(attn, T), L.lora_rope_backward_workspace_size(rope, T)]
+        if 0 in sizes or not 1 <= n_pos <= 1 << 24:
+            raise ValueError(f"{q_heads} / {kv_heads} heads of {head_dim}, eps {head_eps}, {n_pos} positions: query heads a "
+                             "multiple of the key heads, head_dim 64 or 128, 1 to 2^24 positions")
         new = lambda n: torch.zeros((T, n), dtype=X.dtype, device=dev)   # noqa: E731  (padding rows stay zero)
         for l in (q, k, v):
             l.dY = new(l.out_dim)
@@ -380,21 +391,16 @@ class AttentionStep(SublayerStep):
             self.gamma_k, self.dgamma_k = (self.arena.view(w, at + head_dim, (head_dim,)) for w in ("params", "grads"))
             self.gamma_q.fill_(1.0)
             self.gamma_k.fill_(1.0)
-        if inv_freq is not None and tuple(inv_freq.shape) != (head_dim // 2,):
-            raise ValueError("inv_freq: [head_dim / 2]")
-        self.n_seq, self.n_pos = seq_start.numel() - 1, T if n_pos is None else n_pos
+        self.n_seq, self.n_pos = seq_start.numel() - 1, n_pos
         if inv_freq is None:
             inv_freq = rope_base ** (-torch.arange(0, head_dim, 2, dtype=torch.float64) / head_dim)
         self.table = torch.empty((self.n_pos, head_dim // 2, 2), dtype=torch.float32, device=dev)
         L.lora_rope_table(self.n_pos, head_dim, inv_freq.to(device=dev, dtype=torch.float64).contiguous(), self.table)
-        self.rope = L.make_rope_desc(q_heads, kv_heads, head_dim, L.LORA_BF16,
-                                     L.LORA_ROPE_PAIRS if pairs else L.LORA_ROPE_HALVES, head_eps)
-        self.attn = L.make_attn_desc(q_heads, kv_heads, head_dim)
+        self.rope, self.attn = rope, attn
         self.plan = _ws(L.lora_attn_plan_size(T, self.n_seq), dev)
         self.Qr, self.Kr, self.dQr, self.dKr = new(wq), new(wk), new(wq), new(wk)   # turned
         self.lse = torch.zeros((q_heads, T), dtype=torch.float32, device=dev)
-        self.attn_ws = _ws(max(L.lora_attn_backward_workspace_size(self.attn, T),
-                               L.lora_rope_backward_workspace_size(self.rope, T)), dev)
+        self.attn_ws = _ws(max(sizes), dev)
         self.seq_start = torch.empty_like(seq_start)
         self.pos = torch.empty(T, dtype=torch.int32, device=dev)
         self.set_sequences(seq_start, pos)
