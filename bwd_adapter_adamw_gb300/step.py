@@ -413,6 +413,16 @@ class AttentionStep(SublayerStep):
         if pos is not None and (pos.dtype != torch.int32 or tuple(pos.shape) != (T,) or pos.device != dev):
             raise ValueError("pos: int32 [tokens] on the activations' device")
 
+    @staticmethod
+    def _positions(seq_start: torch.Tensor, T: int) -> torch.Tensor:
+        """Each token's place in its sequence, -1 in none, of the sequences that the attention's plan makes of a table:
+        clamped to the tokens, and each begins no earlier than those before it end."""
+        s, at = seq_start.long().clamp(0, T), torch.arange(T, device=seq_start.device)
+        end = s[1:].cummax(0).values
+        seq = torch.searchsorted(end, at, right=True)      # sequences that end at or before the token
+        pos = at - torch.cat((s[:1], end))[seq]
+        return torch.where((seq < end.numel()) & (pos >= 0), pos, -1)
+
     def set_sequences(self, seq_start: torch.Tensor, pos: Optional[torch.Tensor] = None):
         """The sequences (as many as before, empty ones among them) and positions of the steps from here on, on
         the current stream; captured steps take them, too. Rows that were in a sequence and are padding now are
@@ -423,10 +433,7 @@ class AttentionStep(SublayerStep):
         if seq_start.numel() != self.n_seq + 1:
             raise ValueError(f"{seq_start.numel() - 1} sequences for a step of {self.n_seq}")
         if pos is None:
-            at = seq_start.long().clamp(0, T).cummax(0).values
-            seq = torch.searchsorted(at, torch.arange(T, device=dev), right=True) - 1
-            pos = torch.arange(T, device=dev) - at[seq.clamp(min=0)]
-            pos = torch.where((seq >= 0) & (seq < self.n_seq), pos, -1)
+            pos = self._positions(seq_start, T)
         self.seq_start.copy_(seq_start)
         self.pos.copy_(pos)
         for t in (self.o.X, self.lse, self.Qr, self.Kr, self.dQr, self.dKr, self.q.dY, self.k.dY, self.v.dY):
