@@ -348,7 +348,8 @@ class AttentionStep(SublayerStep):
     sublayer's output gradient, the other three gradients are the step's own. seq_start: int32 [n + 1]
     on the device, the sequences' first tokens and the last one's end; tokens of no sequence are padding
     (their rows of X have to be finite, their output gradients zero). pos: int32 [tokens], from 0 in each
-    sequence unless given (negative: padding). Both are copied; set_sequences gives the step another batch's.
+    sequence unless given (padding's are not read; a negative one in a sequence leaves that token's turned query
+    and key zero, which take no gradient). Both are copied; set_sequences gives the step another batch's.
     inv_freq: the rotation's frequencies, rope_base^(-2 i / head_dim) unless given, for n_pos positions
     (the batch's tokens unless given; a position from n_pos on, as in a longer sequence, makes its sequence
     and the gradients NaN)."""
@@ -432,8 +433,8 @@ class AttentionStep(SublayerStep):
         self._check_sequences(seq_start, pos, T, dev)
         if seq_start.numel() != self.n_seq + 1:
             raise ValueError(f"{seq_start.numel() - 1} sequences for a step of {self.n_seq}")
-        if pos is None:
-            pos = self._positions(seq_start, T)
+        place = self._positions(seq_start, T)
+        pos = place if pos is None else torch.where(place >= 0, pos, -1)   # (whatever is given for padding)
         self.seq_start.copy_(seq_start)
         self.pos.copy_(pos)
         for t in (self.o.X, self.lse, self.Qr, self.Kr, self.dQr, self.dKr, self.q.dY, self.k.dY, self.v.dY):

@@ -51,3 +51,21 @@ def test_statistics_of_every_call_are_its_own(L, lens, hq, hk, dim, captured):
     assert L.lora_device_error() == 0
     for i, out in enumerate(outs):
         assert all(torch.equal(x, y) for x, y in zip(out, want[i % 2])), i
+
+
+def test_positions_of_padding_are_not_read(L):
+    """Positions that a caller gives for tokens of no sequence, past the table or before it, change nothing: padding's
+    turned rows stay zero and no gradient takes a NaN from them."""
+    from tests.test_gpu_attention_step import make
+    starts, pad = [0, 70, 200], 30
+    outs = []
+    for junk in (-1, 3, 1 << 20):
+        st, _ = make(starts, pad)
+        pos = torch.cat([torch.arange(70), torch.arange(130), torch.full((pad,), junk)]).int().cuda()
+        st.set_sequences(st.seq_start.clone(), pos)
+        st.forward_backward(0)
+        torch.cuda.synchronize()
+        outs.append([t.clone() for t in (st.Qr, st.Kr, st.o.Y, st.dX, st.arena.grads)])
+    assert bool(torch.isfinite(outs[0][-1]).all())
+    for other in outs[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(outs[0], other))
