@@ -69,3 +69,21 @@ def test_positions_of_padding_are_not_read(L):
     assert bool(torch.isfinite(outs[0][-1]).all())
     for other in outs[1:]:
         assert all(torch.equal(x, y) for x, y in zip(outs[0], other))
+
+
+@pytest.mark.parametrize("lens,hq,hk,dim", [([8] * 128, 32, 4, 64), ([8] * 128, 32, 8, 128), ([1] * 700, 8, 1, 64)])
+def test_many_short_sequences_take_persistent_ctas(L, lens, hq, hk, dim):
+    """Every sequence has a key tile of its own, however short: few tokens in many sequences are many items. They take the
+    form that a large batch takes, bit for bit (clusters that share a group's heads add their sums in another order)."""
+    from tests.test_gpu_attention import Batch
+    a = Batch(L, lens, hq, hk, dim, seed=6)
+    b = Batch(L, lens, hq, hk, dim, seed=6, pad=60 * 128)
+    for x, y in ((b.q, a.q), (b.k, a.k), (b.v, a.v), (b.do, a.do)):
+        x[:a.T] = y
+    for x in (a, b):
+        x.forward()
+        x.backward()
+    torch.cuda.synchronize()
+    assert L.lora_device_error() == 0
+    for x, y in ((a.o, b.o), (a.dq, b.dq), (a.dk, b.dk), (a.dv, b.dv)):
+        assert torch.equal(x, y[:a.T])
