@@ -20,9 +20,10 @@
 //
 // Bound by the tensor cores at the power limit's clock: one sequence of 8192 tokens, 32 / 8 heads of 128, 355-373 us
 // (1470 to 1550 TFLOP/s of the 1763 that a library product sustains; 330 us and the tensor cores busy for 74% of
-// them where the clock holds), 32768 tokens 5.5 ms (1610). 16384 tokens in sequences of 64 to 1024 take 117 us, 840
-// TFLOP/s of useful and 1390 of tiles' operations: there an item's 2.9 key tiles stand between its first load and
-// its last store. Steps at 8192 tokens: products issued by a
+// them where the clock holds), 32768 tokens 5.4 to 5.5 ms (1590 to 1620). 16384 tokens in 28 sequences of 66 to 1008
+// take 115 to 117 us, 840 TFLOP/s of useful and 1150 to 1160 of tiles' operations: whole tiles are 1.37 times the
+// useful operations, and a query tile has 3.5 key tiles between its first load and its last store, where both tiles of
+// a CTA end together and leave the tensor cores the next item's first scores alone. Steps at 8192 tokens: products issued by a
 // single lane's branch 481, by a whole warp 380; P in halves and three-operand maxima 369; persistent CTAs 364. Not
 // kept: two issuing warps 421, half of P against the reference of the tile before 384.
 #include <new>
@@ -64,7 +65,8 @@ __device__ int64_t block_scan(int64_t v, int64_t* sh, Op op) {
 // One CTA. Sequences (clamped, in order), then for tiles of 128 and of 256 rows: how many sequences have
 // an i-th tile, the place of the tiles of each index in falling order (a causal tile's work grows with its
 // index), and the tiles in their places. The order among tiles of one index is not fixed; it decides when
-// a tile runs, not what it computes.
+// a tile runs, not what it computes. 11 us for up to 8 sequences of 1024 tokens, 12 for 28 of 16380 tokens in all, 12 to
+// 14 for one of 8192, 100 to 135 for 3000 of 5 tokens: once for all layers of a batch.
 __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constant__ PlanK a) {
   grid_dep_sync();
   __shared__ int64_t sh[kPlanThreads];

@@ -6,28 +6,32 @@
 //   dQ = scale dS K                   (query tile fixed, over key tiles)
 //
 // Five products are needed; recomputing S and dP for dQ makes seven. The alternative, dQ added up in
-// global memory by the key tiles' CTAs, takes fp32 atomics whose order changes results, 64 KB of them per
-// five products (25 bytes per cycle and SM into L2, as much as all SMs together can add), and a pass that
-// clears and rounds them.
+// global memory by the key tiles' CTAs, takes fp32 additions in a fixed order if reruns are to be equal, 64 KB of
+// them per five products (25 bytes per cycle and SM into L2, whose rate for additions was not measured), and a pass
+// that clears and rounds them. It was not built.
 //
 // dV and dK (k_attn_dkv): the scores are computed turned, S^T = K Q^T and dP^T = V dO^T, keys along the
 // tensor memory's lanes, so that P^T and dS^T, written back over them in bf16, are first operands of
-// P^T dO and dS^T Q as they are; a thread has one key and 32 of the tile's queries. The products of one
+// P^T dO and dS^T Q as they are; a warp has 32 keys and 32 of the tile's queries. The products of one
 // query tile run while the other half of its elementwise work does: S^T of the next tile under dS^T of
 // this one, dP^T of the next under P^T of the next. At head_dim 128 a pair of tiles takes four products of
 // 512 cycles.
 //
-// dQ (k_attn_dq): S = Q K^T and dP = dO V^T with queries along the lanes; dS, in bf16 over dP, is the first
-// operand of dS K. S alternates between two buffers, so that the next tile's S runs before this one's dS.
+// dQ (k_attn_dq): two query tiles over shared keys, as in the forward pass; S = Q K^T and dP = dO V^T with queries
+// along the lanes. A tile's S, dP and dS share one place in tensor memory: dP goes over S once that is in registers,
+// dS, in bf16, over dP, as the first operand of dS K, and the next S over dS behind that product. The elementwise work
+// of one tile runs beside the products of the other.
 //
-// CTA layout (640 threads): warps 0-15 elementwise (four warpgroups, 32 columns each) and epilogue, warp 16
-// loads, warp 17 issues the products, warp 18 brings the queries' statistics, warp 19 zeroes rows behind a sequence
-// (k_attn_dkv); as in the forward pass (k_attn_dq). Waits are bounded as there.
+// CTA layout, k_attn_dkv (640 threads): warps 0-15 elementwise (four warpgroups, 32 columns each) and epilogue, warp 16
+// loads, warp 17 issues the products, warp 18 brings the queries' statistics, warp 19 zeroes rows behind a sequence.
+// k_attn_dq (384 threads): as in the forward pass. Waits are bounded as there. The cluster form of k_attn_dkv reloads
+// 108 (head_dim 128) and 136 bytes of spilled registers a thread, k_attn_dq at head_dim 128 20, the others none.
 //
-// One sequence of 8192 tokens, 32 / 8 heads of 128: 1166 to 1187 us (seven products: 1620 to 1650 TFLOP/s, near the 1763 that
-// the power limit leaves a library product); alone delta takes 25 us, dV and dK 599 (1840 TFLOP/s, tensor cores 88%
-// busy), dQ 468 (1760, 77%). 16384 tokens in sequences of 64 to 1024: 404 us; one by one delta takes 40, dV and dK 183,
-// dQ 156.
+// One sequence of 8192 tokens, 32 / 8 heads of 128: 1166 to 1194 us by the clock that the power limit leaves (seven
+// products: 1610 to 1650 TFLOP/s; a library product sustains 1763); alone delta takes 24 us, dV and dK 589 (1870
+// TFLOP/s, tensor cores 90% busy), dQ 473 (1745, 77%). 16384 tokens in sequences of 64 to 1024: 393 to 406 us; one by
+// one delta takes 40, dV and dK 183, dQ 156. The tiles' seven products are 470 GFLOP there (tiles are 1.37 times the
+// useful operations), 267 us at the sustained rate.
 #include "attn_common.cuh"
 
 namespace lora {
@@ -596,7 +600,8 @@ __global__ void __launch_bounds__(SplitFwd::kThreads, 1) k_attn_dq(const __grid_
   // and waits for it at its end only, so that whatever follows finds both complete. That it was let in says nothing of
   // what it can see. The outputs of delta's and all earlier kernels are seen through `ready`, which k_attn_dkv
   // releases behind its own wait for them, and before it lets this kernel in, so that the flag is there at the first
-  // look; the barrier hands it to all threads, the fence to the bulk copies. (Packed batch 411 -> 404 us.)
+  // look; the barrier hands it to all threads, the fence to the bulk copies. (Packed batch, when the early start came in:
+  // 411 -> 404 us.)
   if (warp == 11 && lane == 0) *go = flag_wait(p.ready, 1u, p.err, p.limit) ? 1u : 0u;
   fence_before();
   __syncthreads();

@@ -14,8 +14,8 @@ namespace attn {
 using namespace tc;
 
 constexpr int kRows = kAttnTile;
-// The forward pass has 384 threads: eight warps that compute, then a warpgroup that loads and issues and
-// leaves them its registers; the backward pass 640, sixteen of them.
+// The forward pass and k_attn_dq have 384 threads: eight warps that compute, then a warpgroup that loads and issues and
+// leaves them its registers; k_attn_dkv 640, sixteen of them.
 template <int THREADS, int LAUNCH, int ISSUE, int COMPUTE>
 struct Split {
   static constexpr int kThreads = THREADS, kLaunch = LAUNCH, kIssue = ISSUE, kCompute = COMPUTE;   // registers per thread
@@ -79,7 +79,7 @@ __device__ __forceinline__ float read_here(const float* p) {
 }
 
 // ---- tensor memory, 32 columns of this thread's lane ----
-__device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t* r) {   // valid after ld_wait and hold
+__device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t* r) {   // valid after tmem_wait_ld_n
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
       "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "

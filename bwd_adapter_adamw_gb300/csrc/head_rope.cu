@@ -40,8 +40,10 @@ using attn::mul2;
 using attn::un2;
 
 // A lane's 2 V elements of a head: V = 4 from `lane V` of each half, as packed pairs of neighbours (one instruction
-// for two elements). In bf16 that is 8 bytes of each half: with 16 a lane's vectors, angles, weights and sums took
-// 128 registers in the backward pass, and two CTAs of 256 threads per SM left the memory waiting.
+// for two elements). In bf16 that is 8 bytes of each half. With 16 the same bytes in flight (two steps of a warp for
+// four) do not fit the registers that the CTAs per SM leave, 64 forward and 128 backward: a lane's vectors, angles,
+// weights and sums spill 148 and 216 bytes. 8192 tokens of 40 heads of 128: 39.9 and 63.0 us against 29.6 and 49.9; with
+// one step in flight 35.2 and 57.9.
 template <typename E> struct Half;
 template <> struct Half<float> {
   static constexpr int V = 4;
@@ -148,7 +150,8 @@ __device__ __forceinline__ void load_gamma(const float* g, int l, int half, f2 (
 
 // A warp takes a share of one token's heads, HPW at a time and R such steps in flight: the token's
 // angles and the weights stay in registers over them (they are as many bytes as a head's). 8192 tokens of 40 heads of
-// 128 in bf16: 30.1 us, 5.7 TB/s; with two steps in flight and three CTAs per SM 39.8, with 16 bytes a lane 34.2.
+// 128: 29.6 us in bf16, 5.8 TB/s (20 bytes are reloaded at 64 registers), 53.4 in fp32, 6.4 TB/s; bf16 with two steps
+// in flight and three CTAs per SM, so measured earlier, 39.8.
 template <typename E, int D, bool PAIRS, bool NORM, int R>
 __global__ void __launch_bounds__(kRopeThreads, 4) k_rope_fwd(const __grid_constant__ RopeK p) {
   grid_dep_sync();
@@ -210,9 +213,12 @@ __global__ void __launch_bounds__(kRopeThreads, 4) k_rope_fwd(const __grid_const
 // known, so that their shuffles run together. The CTA's sums go to part[CTA][q | k], added up in order by
 // k_rope_reduce.
 //
-// 8192 tokens of 40 heads of 128 in bf16: 51 us, 4.9 TB/s, half of it the kernel's own instructions (140 per warp and
-// two heads); 59 with the reduction and two copies of the weights' gradients. So measured, two steps in flight instead
-// of four take 68 us, three CTAs per SM 75, rows brought by bulk copies to per-warp rings in shared memory 72.
+// 8192 tokens of 40 heads of 128: 49.9 us in bf16, 5.1 TB/s, 80.3 in fp32, 6.4 TB/s; 51.0 and 82.9 with the reduction. In
+// bf16 two CTAs of 256 threads per SM (128 registers) wait for their loads and compute in turn: issue slots are 44% busy,
+// and long_scoreboard is the largest stall. 59.5 for a call with two copies of the weights' gradients ahead of it; so
+// measured, two steps in flight instead of four take 68 us, three CTAs per SM 75, rows brought by bulk copies to per-warp
+// rings in shared memory 72. 1023 tokens of 36 heads of 64 in fp32: 7.7 us and 2.2 for the reduction, the latency of two
+// launches with one round of warps.
 template <typename E, int D, bool PAIRS, bool NORM, int R>
 __global__ void __launch_bounds__(kRopeThreads, 2) k_rope_bwd(const __grid_constant__ RopeK p) {
   grid_dep_sync();

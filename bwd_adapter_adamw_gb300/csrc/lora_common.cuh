@@ -12,9 +12,10 @@ namespace lora {
 // Programmatic dependent launch. Every kernel of the library starts with grid_dep_sync(): it waits
 // until the kernels before it in the stream have completed and their writes are visible
 // (griddepcontrol.wait), then lets the next kernel in the stream begin its launch
-// (griddepcontrol.launch_dependents). (k_attn_dq, behind a kernel it needs nothing of, waits at its
-// end.) Launched with the programmatic stream serialization attribute (launch_kernel), a kernel's launch and CTA dispatch overlap the tail of the kernel
-// before it; launched without it, the wait returns at once.
+// (griddepcontrol.launch_dependents). (k_attn_dq, behind a kernel it needs no output of, waits at its
+// end, and is ordered behind the kernels ahead of that one by a flag.) Launched with the programmatic
+// stream serialization attribute (launch_kernel), a kernel's launch and CTA dispatch overlap the tail
+// of the kernel before it; launched without it, the wait returns at once.
 __device__ __forceinline__ void grid_dep_sync() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

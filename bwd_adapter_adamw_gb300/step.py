@@ -345,7 +345,7 @@ class AttentionStep(SublayerStep):
         Q, K, V = projections(norm(X)),  Y = projection_o(attention(rope(Q), rope(K), V)),
     with the norms' weights trained beside the adapters (as in SublayerStep; without the heads' norms
     with head_norm=False). q, k, v and o are the Linears of the four projections; o.dY is the
-    sublayer's output gradient, the other three gradients are the step's own. seq_start: int32 [n + 1]
+    sublayer's output gradient, the other three gradients and the four inputs are the step's own. seq_start: int32 [n + 1]
     on the device, the sequences' first tokens and the last one's end; tokens of no sequence are padding
     (their rows of X have to be finite, their output gradients zero). pos: int32 [tokens], from 0 in each
     sequence unless given (padding's are not read; a negative one in a sequence leaves that token's turned query
